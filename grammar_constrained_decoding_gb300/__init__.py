@@ -10,6 +10,13 @@ and the current stream) for device data.
     ctx.fill_bitmask(states, bitmask, gid=None, forced=None)
     ctx.mask_and_sample(logits, bitmask, temp, top_p, seed, step, out_tok)
     ctx.accept(states, toks, out_states, out_flags)
+
+On the same masked rows, with settings and random numbers per row, the best
+tokens, and a student's distillation loss (see distill() for autograd):
+
+    ctx.sample_rows(logits, uniform, out_tok, bitmask, temp, top_k, top_p, min_p)
+    ctx.top_logprobs(logits, out_ids, out_logprobs, bitmask)
+    ctx.distill_loss(logits, ids, teacher, out_loss, temp, bitmask)
 """
 
 from __future__ import annotations
@@ -259,6 +266,67 @@ class Ctx:
             int(seed), int(step), _ptr(counts), max_tokens, _ptr(h_out_tok), _ptr(out_tok), _ptr(out_states),
             _ptr(out_flags)))
 
+    def sample_rows(self, logits, uniform, out_tok, bitmask=None, temp=None, top_k=None, top_p=None, min_p=None,
+                    out_logprob=None) -> None:
+        """One token per row: temperature, top-k, top-p and min-p of each row's
+        own ([B] tensors or None), drawn with the given random numbers uniform
+        [B, V] (a [1, V] or expanded tensor shares one row; None for an all-greedy
+        batch); out_logprob receives log p of the token before any cut."""
+        from . import _rows as R
+        call, B, W = "cg_sample_rows", logits.shape[0], self.W
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
+        u, ldu = None, 0
+        if uniform is not None:
+            shared = uniform.shape[0] == 1
+            u, ldu = R.rows_of(call, uniform, "uniform", R.F32, (1 if shared else B, self.V))
+            ldu = 0 if shared else ldu
+        rc = L.lib().cg_sample_rows(
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, W)),
+            R.opt(call, temp, "temp", R.F32, (B,)), R.opt(call, top_k, "top_k", R.U32, (B,)),
+            R.opt(call, top_p, "top_p", R.F32, (B,)), R.opt(call, min_p, "min_p", R.F32, (B,)), u, ldu,
+            R.want(call, out_tok, "out_tok", R.U32, (B,)), R.opt(call, out_logprob, "out_logprob", R.F32, (B,)))
+        L.check(call, rc)
+
+    def top_logprobs(self, logits, out_ids, out_logprobs, bitmask=None, out_lse=None) -> None:
+        """The n best allowed tokens of each row (n = out_ids.shape[1]), best
+        first, with their log-probabilities."""
+        from . import _rows as R
+        call, B, n = "cg_top_logprobs", logits.shape[0], out_ids.shape[1]
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
+        rc = L.lib().cg_top_logprobs(
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)), n,
+            R.want(call, out_ids, "out_ids", R.U32, (B, n)), R.want(call, out_logprobs, "out_logprobs", R.F32, (B, n)),
+            R.opt(call, out_lse, "out_lse", R.F32, (B,)))
+        L.check(call, rc)
+
+    def distill_loss(self, logits, ids, teacher, out_loss, temp: float = 1.0, bitmask=None, out_lse=None,
+                     out_grad=None, grad_loss=None) -> None:
+        """Loss of each row against the teacher's listed tokens (ids, teacher
+        [B, K]); with out_grad also the gradient by the logits, times grad_loss [B]."""
+        from . import _rows as R
+        call, B, K = "cg_distill_loss", logits.shape[0], ids.shape[1]
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
+        g, ldg = (None, 0) if out_grad is None else R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
+        rc = L.lib().cg_distill_loss(
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)),
+            R.want(call, ids, "ids", R.U32, (B, K)), R.want(call, teacher, "teacher", R.F32, (B, K)), K, temp,
+            R.want(call, out_loss, "out_loss", R.F32, (B,)), R.opt(call, out_lse, "out_lse", R.F32, (B,)),
+            R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
+        L.check(call, rc)
+
+    def distill_grad(self, logits, ids, teacher, lse, out_grad, temp: float = 1.0, bitmask=None,
+                     grad_loss=None) -> None:
+        """The gradient alone, from the normaliser distill_loss left in out_lse."""
+        from . import _rows as R
+        call, B, K = "cg_distill_grad", logits.shape[0], ids.shape[1]
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
+        g, ldg = R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
+        rc = L.lib().cg_distill_grad(
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)),
+            R.want(call, ids, "ids", R.U32, (B, K)), R.want(call, teacher, "teacher", R.F32, (B, K)), K, temp,
+            R.want(call, lse, "lse", R.F32, (B,)), R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
+        L.check(call, rc)
+
     def self_test_wait_timeout(self) -> None:
         """Make one bounded device wait run out (the status then reads CG_DEV_TIMEOUT)."""
         L.check("cg_self_test_wait_timeout", L.lib().cg_self_test_wait_timeout(self._h))
@@ -387,3 +455,11 @@ class Driver:
                                                               forced_used.ctypes.data, forced_next.ctypes.data,
                                                               C.byref(n)))
         return n.value
+
+
+def distill(ctx: Ctx, logits, ids, teacher, temp: float = 1.0, bitmask=None):
+    """Distillation loss of each row, f32 [B], differentiable by logits (and by
+    nothing else): Ctx.distill_loss forward, Ctx.distill_grad backward.  Runs on
+    the context's stream, ordered after and before torch's current one."""
+    from .autograd import DistillLoss
+    return DistillLoss.apply(logits, ctx, ids, teacher, float(temp), bitmask)

@@ -22,6 +22,8 @@ CG_SAMPLE_INPLACE = 1
 CG_NOALLOC_MAX_ROWS = 64
 CG_RESULT_CALC_TAG, CG_RESULT_JSON_ANSWER, CG_RESULT_STROP_TAG = 0, 1, 2
 CG_PDA_MAX_DEPTH = 64
+CG_TOP_MAX = 1024
+CG_DEV_BAD_TOKEN, CG_DEV_BAD_PARAM = 2, 10
 
 ERROR_NAMES = {CG_E_ARG: "CG_E_ARG", CG_E_SYNTAX: "CG_E_SYNTAX", CG_E_UNSUPPORTED: "CG_E_UNSUPPORTED",
                CG_E_EMPTY: "CG_E_EMPTY", CG_E_UNDEFINED_RULE: "CG_E_UNDEFINED_RULE", CG_E_LIMIT: "CG_E_LIMIT",
@@ -82,6 +84,17 @@ SIGNATURES = {
                           C.c_void_p, C.c_void_p]),
     "cg_accept": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint32, C.c_void_p,
                             C.c_uint32, C.c_void_p, C.c_void_p]),
+    "cg_sample_rows": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_uint32, C.c_uint32, C.c_uint64, C.c_void_p,
+                                 C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64, C.c_void_p,
+                                 C.c_void_p]),
+    "cg_top_logprobs": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_uint32, C.c_uint32, C.c_uint64, C.c_void_p,
+                                  C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "cg_distill_loss": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_uint32, C.c_uint32, C.c_uint64, C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_uint32, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p,
+                                  C.c_void_p, C.c_uint64]),
+    "cg_distill_grad": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_uint32, C.c_uint32, C.c_uint64, C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_uint32, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p,
+                                  C.c_uint64]),
     "cg_eval_strop": (C.c_int, [C.c_char_p, C.c_size_t, C.c_void_p, C.c_size_t, C.POINTER(C.c_size_t),
                                 C.POINTER(C.c_int)]),
     "cg_eval_arith": (C.c_int, [C.c_char_p, C.c_size_t, C.c_int, C.c_void_p, C.c_size_t, C.POINTER(C.c_size_t),

@@ -100,6 +100,8 @@ extern "C" {
 #define CG_DEV_TIMEOUT         8  /* sample: a bounded wait for an asynchronous copy ran out;
                                      the row gets CG_NO_TOKEN */
 #define CG_DEV_BAD_LENGTH      9  /* accept_many: a draft length > K (clamped to K) */
+#define CG_DEV_BAD_PARAM      10  /* sample_rows: a row's temperature is negative, infinite or NaN, or its
+                                     top_p or min_p is NaN; the row gets CG_NO_TOKEN */
 
 /* mask_and_sample flags */
 #define CG_SAMPLE_INPLACE 1u     /* also write -inf into masked logits (the "&mut [f32]" form) */
@@ -409,6 +411,102 @@ int cg_accept_many(cg_ctx* c, const uint32_t* d_states, const uint16_t* d_gid, c
  * Asynchronous on the context stream; the wait polls for well under a second.
  * Errors: CG_E_ARG, CG_E_CUDA. */
 int cg_self_test_wait_timeout(cg_ctx* c);
+
+/* ---- per-row sampling, best tokens, distillation -------------------------------- */
+
+/* What a server and a trainer do with the masked rows beyond step 2: sampling
+ * with settings and random numbers of each row's own, the best tokens of a row
+ * with their log-probabilities, and the loss of a student against a teacher's
+ * recorded best tokens, with its gradient.  The pages state the constraint
+ * ("The guarantee", usetacet.com/docs/grammar: the mask applies whatever the
+ * sampling strategy) and give no form for these; the definitions are here.
+ *
+ * Common to the four calls
+ *  d_logits  : [B][ld] CG_F32 or CG_BF16, row b starts at element b * ld
+ *              (ld >= V: rows of a wider or padded buffer); any alignment that
+ *              the element type has (16-byte aligned rows load fastest)
+ *  d_bitmask : u32 [B][W] as cg_fill_bitmask writes it, or NULL: every token
+ *              is allowed
+ *  A logit that is -inf or NaN counts as not allowed; +inf counts as the
+ *  largest finite value of the type.  A_b is the set of row b's allowed tokens.
+ *  Sums, maxima and normalisers are held in 32 bits or more, and no result
+ *  depends on the order in which the device runs its blocks.
+ *  The calls allocate nothing and may be captured; they run on the context's
+ *  stream like the step calls, so inputs made on another stream need an event
+ *  between the two.  Errors: CG_E_ARG for a NULL required pointer, an unknown
+ *  dtype, V other than the vocabulary's, ld < V, a misaligned pointer or a size
+ *  out of range; CG_E_LIMIT as noted; CG_E_CUDA. */
+
+/* Sampling with settings per row from given random numbers.  For row b with
+ * T = d_temp[b], x_t its logits, m = max x over A_b, z_t = (x_t - m) / T and
+ * p_t = exp(z_t) / sum exp(z):
+ *   top-k  keeps the tokens with x_t >= the k-th largest x (k = d_top_k[b];
+ *          0, or k >= the number of allowed tokens, keeps all);
+ *   top-p  renormalises over those and keeps x_t >= tau, tau the largest value
+ *          whose upper set carries at least top_p of their mass (top_p >= 1
+ *          keeps all, top_p <= 0 only the maximum);
+ *   min-p  keeps p_t >= min_p * max p, i.e. z_t >= log(min_p) (0 keeps all);
+ *   token = argmax over the kept set of z_t - log(-log u_t), ties to the lowest
+ *          id, u_t = d_uniform[b * ld_uniform + t] clamped into
+ *          [2^-32, 1 - 2^-24] (a NaN counts as 2^-32).
+ * Tokens that tie with a threshold stay.  T = 0 takes the maximum (lowest id)
+ * and reads neither the other settings nor d_uniform.
+ *  d_temp, d_top_k, d_top_p, d_min_p : f32/u32/f32/f32 [B]; NULL means 1, 0, 1, 0
+ *  d_uniform  : f32, row b at element b * ld_uniform; ld_uniform >= V, or 0 for
+ *               one row of numbers shared by every row (coupled draws: a draft
+ *               and its verification see the same numbers).  Only the kept
+ *               tokens' numbers are read.  NULL is allowed when d_temp is given
+ *               and every temperature is 0 (a row with T > 0 then records
+ *               CG_DEV_BAD_PARAM).
+ *  d_out_tok  : u32 [B]; CG_NO_TOKEN for a row without allowed tokens
+ *  d_out_logprob : f32 [B] or NULL: log p of the token in the softmax over A_b at
+ *               temperature T (1 where T = 0), before any cut; -inf without a token
+ * Device errors: CG_DEV_BAD_PARAM. */
+int cg_sample_rows(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                   const uint32_t* d_bitmask, const float* d_temp, const uint32_t* d_top_k, const float* d_top_p,
+                   const float* d_min_p, const float* d_uniform, uint64_t ld_uniform, uint32_t* d_out_tok,
+                   float* d_out_logprob);
+
+/* The n best allowed tokens of each row, in order (larger logit first, equal
+ * logits by lower id), with their log-probabilities in the softmax over A_b.
+ *  n            : 1..CG_TOP_MAX (CG_E_LIMIT above)
+ *  d_out_ids    : u32 [B][n]; CG_NO_TOKEN past the number of allowed tokens
+ *  d_out_logprobs : f32 [B][n]; -inf there
+ *  d_out_lse    : f32 [B] or NULL: log sum over A_b of exp x (-inf for an empty row) */
+#define CG_TOP_MAX 1024u
+int cg_top_logprobs(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                    const uint32_t* d_bitmask, uint32_t n, uint32_t* d_out_ids, float* d_out_logprobs,
+                    float* d_out_lse);
+
+/* Distillation from a teacher's top logits.  For row b, with T = temp and the
+ * teacher's list of K token ids and logits (or log-probabilities: a constant
+ * added to a row changes nothing):
+ *   S_b = the entries whose id is not CG_NO_TOKEN, is in A_b and whose teacher
+ *         logit is not -inf or NaN (+inf counts as the largest finite value);
+ *   q   = softmax over S_b of teacher / T,   p = softmax over A_b of x / T;
+ *   loss[b] = T^2 * sum over S_b of q_k (log q_k - log p[id_k]);
+ *   dloss[b]/dx_v = T * (p_v - sum over the entries of S_b with id v of q_k)
+ *         for v in A_b, 0 for the others.
+ * An empty S_b gives loss 0 and gradient 0.  An id may be listed twice (its
+ * weights add up).  An id >= V other than CG_NO_TOKEN records CG_DEV_BAD_TOKEN
+ * and counts as not listed.
+ *  d_ids, d_teacher : u32, f32 [B][K], 1 <= K <= CG_TOP_MAX (CG_E_LIMIT above)
+ *  temp      : T > 0, finite
+ *  d_out_loss: f32 [B]; d_out_lse: f32 [B] or NULL: log sum over A_b of exp(x / T)
+ *  d_out_grad: [B][ld_grad] of the logits' dtype or NULL: the gradient times
+ *              d_grad_loss[b] (f32 [B], NULL for 1), written in the same pass;
+ *              rounded once from 32 bits to the dtype.  May be d_logits itself
+ *              (with ld_grad == ld); must not overlap it otherwise.
+ * cg_distill_grad is the backward pass alone: d_lse as cg_distill_loss wrote it
+ * for the same logits, mask and temperature.
+ * Device errors: CG_DEV_BAD_TOKEN. */
+int cg_distill_loss(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                    const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
+                    float temp, float* d_out_loss, float* d_out_lse, const float* d_grad_loss, void* d_out_grad,
+                    uint64_t ld_grad);
+int cg_distill_grad(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                    const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
+                    float temp, const float* d_lse, const float* d_grad_loss, void* d_out_grad, uint64_t ld_grad);
 
 /* ---- pushdown automaton for recursive grammars ---------------------------------- */
 
