@@ -5,9 +5,12 @@
 //   dloss/dx_v = T (p_v - sum_{k: id_k = v} q_k),
 // q the softmax of the teacher's listed logits / T, S = sum exp((x - m) / T).
 //
-// One block per row; each pass reads the row again.  The gradient is written
-// for every token as T w p_v first; the listed ones are written over after a
-// block barrier (same block, so in order).
+// The row is held on chip by a cluster (logit_row.cuh): the logits are read from
+// memory once and the gradient is written once from the registers.  Every
+// gradient is written as T w p_v first; the block that wrote a listed token's
+// writes it over after a block barrier.  All reads of the row's logits, the
+// listed ones by every block included, come before the cluster meets, all
+// writes after it, so the gradient may take the logits' place.
 #include "logit_row.cuh"
 
 namespace cgk {
@@ -15,7 +18,20 @@ namespace {
 
 using namespace row;
 
-constexpr uint32_t kSlotsMax = 2 * CG_TOP_MAX;
+constexpr uint32_t kHash = 2 * CG_TOP_MAX;  // slots of the repeated-id check
+
+// The teacher's list in shared memory
+struct List {
+  uint32_t id[CG_TOP_MAX];   // listed ids that count, CG_NO_TOKEN for the others
+  float t[CG_TOP_MAX];       // teacher logits, then weights q
+  float x[CG_TOP_MAX];       // the student's logits there
+  uint32_t hash[kHash];
+  uint32_t repeated;
+};
+struct DistillShared {
+  List list;
+  Common s;
+};
 
 struct DistillArgs {
   const void* logits;
@@ -36,82 +52,160 @@ struct DistillArgs {
 };
 
 template <bool BF16>
-__device__ __forceinline__ void store_grad(void* row, uint32_t t, float g) {
-  if (BF16) static_cast<__nv_bfloat16*>(row)[t] = __float2bfloat16_rn(g);
-  else static_cast<float*>(row)[t] = g;
+__device__ __forceinline__ void store_grad(char* row, uint32_t t, float g) {
+  if (BF16) reinterpret_cast<__nv_bfloat16*>(row)[t] = __float2bfloat16_rn(g);
+  else reinterpret_cast<float*>(row)[t] = g;
+}
+__device__ __forceinline__ uint32_t bf16_pack(float2 g) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(g.x, g.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// one group's gradients: 16 bytes at once inside the row when the gradient's
+// rows lie on the 16-byte grid like the logits', else one by one
+template <bool BF16>
+__device__ __forceinline__ void store_group(char* row, int t0, uint32_t V, bool wide, const float2* g) {
+  constexpr uint32_t E = Fmt<BF16>::E;
+  if (wide && t0 >= 0 && uint32_t(t0) + E <= V) {
+    uint4 v;
+    if (BF16) v = make_uint4(bf16_pack(g[0]), bf16_pack(g[1]), bf16_pack(g[2]), bf16_pack(g[3]));
+    else v = make_uint4(__float_as_uint(g[0].x), __float_as_uint(g[0].y), __float_as_uint(g[1].x),
+                        __float_as_uint(g[1].y));
+    *reinterpret_cast<uint4*>(row + ptrdiff_t(t0) * ptrdiff_t(Fmt<BF16>::kSize)) = v;
+    return;
+  }
+#pragma unroll
+  for (uint32_t e = 0; e < E; ++e) {
+    const int t = t0 + int(e);
+    if (t >= 0 && t < int(V)) store_grad<BF16>(row, uint32_t(t), (e & 1u) ? g[e / 2].y : g[e / 2].x);
+  }
 }
 
-template <bool BF16, bool LOSS>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) {
-  __shared__ uint32_t s_id[CG_TOP_MAX];   // listed ids that count, CG_NO_TOKEN for the others
-  __shared__ float s_t[CG_TOP_MAX];       // teacher logits, then weights q
-  __shared__ float s_x[CG_TOP_MAX];       // the student's logits there
-  __shared__ float red[33];
+template <bool BF16, int NV, bool LOSS>
+__global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) distill_kernel(const DistillArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  List& l = reinterpret_cast<DistillShared*>(smem)->list;
+  Common& s = reinterpret_cast<DistillShared*>(smem)->s;
   griddep_launch_dependents();
+  const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x, K = a.K;
+  if (LOSS && n > 1) cluster_arrive();  // this block's shared memory is ready for the others
   griddep_wait();
-  const uint32_t b = blockIdx.x, tid = threadIdx.x, K = a.K;
   const float T = a.temp, c = exp_scale(T);
-  const Row<BF16> r{static_cast<const char*>(a.logits) + size_t(b) * a.ld * (BF16 ? 2 : 4),
-                    a.bitmask ? a.bitmask + size_t(b) * a.W : nullptr, a.V};
+  Held<BF16, NV> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b));
+  h.load();
+
   // the teacher's list
+  uint32_t slots = 2;
+  while (slots < 2 * K) slots <<= 1;
+  for (uint32_t i = tid; i < slots; i += kThreads) l.hash[i] = CG_NO_TOKEN;
+  if (tid == 0) l.repeated = 0;
   float tm = -INFINITY;
   for (uint32_t k = tid; k < K; k += kThreads) {
     uint32_t id = a.ids[size_t(b) * K + k];
-    const float t = fminf(a.teacher[size_t(b) * K + k], FLT_MAX);
-    const bool nan = a.teacher[size_t(b) * K + k] != a.teacher[size_t(b) * K + k];
+    const float raw = a.teacher[size_t(b) * K + k];
+    const float t = raw != raw ? -INFINITY : fminf(raw, FLT_MAX);
     float x = -INFINITY;
-    if (id < a.V) x = r.at(id);
-    else if (id != CG_NO_TOKEN) record_error(a.status, CG_DEV_BAD_TOKEN);
-    if (!(x > -INFINITY) || nan || !(t > -INFINITY)) id = CG_NO_TOKEN;
-    s_id[k] = id;
-    s_x[k] = x;
-    s_t[k] = t;
+    if (id < a.V) x = h.r.at(id);
+    else if (id != CG_NO_TOKEN && rank == 0) record_error(a.status, CG_DEV_BAD_TOKEN);
+    if (!(x > -INFINITY) || !(t > -INFINITY)) id = CG_NO_TOKEN;
+    l.id[k] = id;
+    l.x[k] = x;
+    l.t[k] = t;
     if (id != CG_NO_TOKEN) tm = fmaxf(tm, t);
   }
-  tm = block_reduce(tm, MaxOp(), -INFINITY, red);
-  float ts = 0.f;
-  for (uint32_t k = tid; k < K; k += kThreads)
-    if (s_id[k] != CG_NO_TOKEN) ts += ex2((s_t[k] - tm) * c);
-  ts = block_reduce(ts, SumOp(), 0.f, red);
+  tm = block_max(tm, s.red_f);
   const bool listed = tm > -INFINITY;
+  float ts = 0.f;
+  for (uint32_t k = tid; k < K; k += kThreads) {
+    const uint32_t id = l.id[k];
+    if (id == CG_NO_TOKEN) continue;
+    ts += ex2((l.t[k] - tm) * c);
+    // repeated ids: every id claims a slot (more slots than ids), the second
+    // of equal ones finds it taken by itself
+    for (uint32_t at = (id * 0x9E3779B1u) & (slots - 1);; at = (at + 1) & (slots - 1)) {
+      const uint32_t old = atomicCAS(l.hash + at, CG_NO_TOKEN, id);
+      if (old == CG_NO_TOKEN) break;
+      if (old == id) {
+        l.repeated = 1;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  ts = block_sum(ts, s.red_f);
+  __syncthreads();
 
   float M = 0.f, S = 1.f;  // p = exp2((x - M) c) / S
   if (LOSS) {
-    max_and_sum(r, c, M, S);
-    float l = 0.f;
-    const float log_ts = logf(ts), log_s = logf(S);
-    for (uint32_t k = tid; k < K; k += kThreads)
-      if (s_id[k] != CG_NO_TOKEN) {
-        const float lt = __fdiv_rn(s_t[k] - tm, T);
-        const float q = __fdiv_rn(ex2((s_t[k] - tm) * c), ts);
-        if (q > 0.f) l += q * ((lt - log_ts) - (__fdiv_rn(s_x[k] - M, T) - log_s));
+    if (n > 1) cluster_wait();
+    uint32_t low, none = 0;
+    h.find_max(s, low);
+    const float sum = h.sum_exps(s, c);
+    exchange(s, n, rank, h.m, sum, 0u);
+    merge(s, n, c, M, S, none);
+    if (rank == 0) {
+      float part = 0.f;
+      const float log_ts = logf(ts), log_s = logf(S);
+      for (uint32_t k = tid; k < K; k += kThreads)
+        if (l.id[k] != CG_NO_TOKEN) {
+          const float q = __fdiv_rn(ex2((l.t[k] - tm) * c), ts);
+          if (q > 0.f) part += q * ((__fdiv_rn(l.t[k] - tm, T) - log_ts) - (__fdiv_rn(l.x[k] - M, T) - log_s));
+        }
+      __syncthreads();
+      part = block_sum(part, s.red_f);
+      if (tid == 0) {
+        a.loss[b] = listed ? T * T * part : 0.f;
+        if (a.lse_out) a.lse_out[b] = M > -INFINITY ? __fdiv_rn(M, T) + log_s : -INFINITY;
       }
-    l = block_reduce(l, SumOp(), 0.f, red);
-    if (tid == 0) {
-      a.loss[b] = listed ? T * T * l : 0.f;
-      if (a.lse_out) a.lse_out[b] = M > -INFINITY ? __fdiv_rn(M, T) + log_s : -INFINITY;
     }
+    if (!a.grad) return;
+  } else {
+    M = a.lse_in[b] * T;  // p = exp((x - lse T) / T)
+    h.clean_own();
+    if (a.grad == a.logits) cluster_sync(n);
   }
-  if (!a.grad) return;
-  const float up = a.up ? a.up[b] : 1.f;
-  const float scale = listed ? T * up : 0.f;
-  char* grow = static_cast<char*>(a.grad) + size_t(b) * a.ld_grad * (BF16 ? 2 : 4);
-  const float lse = LOSS ? 0.f : a.lse_in[b];
-  auto prob = [&](float x) { return LOSS ? __fdiv_rn(ex2((x - M) * c), S) : ex2((__fdiv_rn(x, T) - lse) * kLog2e); };
-  for (uint32_t k = tid; k < K; k += kThreads) s_t[k] = __fdiv_rn(ex2((s_t[k] - tm) * c), ts);
-  for (uint32_t t = tid; t < a.V; t += kThreads) {
-    const float x = r.at(t);
-    store_grad<BF16>(grow, t, x > -INFINITY && listed ? scale * prob(x) : 0.f);
+
+  const float scale = listed ? T * (a.up ? a.up[b] : 1.f) : 0.f;
+  const float r = __fdiv_rn(scale, S);
+  char* row = static_cast<char*>(a.grad) + size_t(b) * a.ld_grad * Fmt<BF16>::kSize;
+  const bool wide = ((reinterpret_cast<uintptr_t>(row) / Fmt<BF16>::kSize - h.r.a) & (Fmt<BF16>::E - 1)) == 0;
+  const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c), r2 = make_float2(r, r);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (!h.r.in_row(h.group(j))) continue;
+    float2 g[Fmt<BF16>::E / 2];
+#pragma unroll
+    for (uint32_t q = 0; q < Fmt<BF16>::E / 2; ++q) {
+      g[q] = make_float2(0.f, 0.f);
+      if (listed) g[q] = __fmul2_rn(ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(h.v[j], q), nm), c2)), r2);
+    }
+    store_group<BF16>(row, h.first_token(j), a.V, wide, g);
   }
+  if (!listed) return;
   __syncthreads();
+  const bool repeated = l.repeated != 0;
   for (uint32_t k = tid; k < K; k += kThreads) {
-    const uint32_t id = s_id[k];
+    const uint32_t id = l.id[k];
     if (id == CG_NO_TOKEN) continue;
-    float q = 0.f;  // an id listed twice: every one of its entries writes the same sum
-    for (uint32_t j = 0; j < K; ++j)
-      if (s_id[j] == id) q += s_t[j];
-    store_grad<BF16>(grow, id, scale * (prob(s_x[k]) - q));
+    const uint32_t g = (id + h.r.a) / Fmt<BF16>::E;
+    if ((g / kThreads) % n != rank) continue;
+    float q = ex2((l.t[k] - tm) * c);
+    if (repeated) {  // every entry of the id writes the same sum
+      q = 0.f;
+      for (uint32_t j = 0; j < K; ++j)
+        if (l.id[j] == id) q += ex2((l.t[j] - tm) * c);
+    }
+    store_grad<BF16>(row, id, scale * (__fdiv_rn(ex2((l.x[k] - M) * c), S) - __fdiv_rn(q, ts)));
   }
+}
+
+template <bool BF16>
+cudaError_t launch_distill(int device, uint32_t B, const DistillArgs& a, bool loss, cudaStream_t stream) {
+  const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld));
+  return with_nv<BF16>(plan.nv, [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    return loss ? launch_clusters<distill_kernel<BF16, NV, true>>(device, B, plan.n, sizeof(DistillShared), stream, a)
+                : launch_clusters<distill_kernel<BF16, NV, false>>(device, B, plan.n, sizeof(DistillShared), stream, a);
+  });
 }
 
 int distill(cg_ctx* c, const char* call, const DistillArgs& base, int dtype, uint32_t B, bool loss) {
@@ -122,9 +216,10 @@ int distill(cg_ctx* c, const char* call, const DistillArgs& base, int dtype, uin
   DistillArgs a = base;
   a.W = v.t.W;
   a.status = v.t.status;
-  auto* kernel = dtype == CG_BF16 ? (loss ? distill_kernel<true, true> : distill_kernel<true, false>)
-                                  : (loss ? distill_kernel<false, true> : distill_kernel<false, false>);
-  return launch_dependent(kernel, B, row::kThreads, 0, v.stream, a) == cudaSuccess ? CG_OK : CG_E_CUDA;
+  const int dev = ctx_device(c);
+  const cudaError_t e = dtype == CG_BF16 ? launch_distill<true>(dev, B, a, loss, v.stream)
+                                         : launch_distill<false>(dev, B, a, loss, v.stream);
+  return e == cudaSuccess ? CG_OK : CG_E_CUDA;
 }
 
 // Whether the gradient overlaps the logits other than as the same rows: their

@@ -1,8 +1,20 @@
-// A row of logits as the per-row operators see it (sample_rows, top_logprobs,
-// distill): a logit that is -inf or NaN, or whose bitmask bit is clear, is not
-// allowed and reads as -inf; +inf reads as the largest finite value.
+// Rows of logits held on chip, the frame of the per-row operators
+// (sample_rows, top_logprobs, distill).
+//
+// A row belongs to a cluster of n <= 8 blocks of 512 threads.  Every thread
+// loads NV 16-byte groups of it (8 bf16 or 4 floats each) once and keeps them in
+// registers, so the row is read from memory once whatever the operator does
+// with it; the blocks exchange what they must (maxima, sums, bounds,
+// histograms) through one another's shared memory.  Groups lie on the 16-byte
+// grid of the memory, not of the row: a row that starts off the grid has a
+// first group with some elements before the row, loaded one by one, and every
+// other load stays 16 bytes wide.
+//
+// A logit that is -inf or NaN, or whose bitmask bit is clear, is not allowed
+// and reads as -inf; +inf reads as the largest finite value.
 #pragma once
 
+#include <atomic>
 #include <cfloat>
 
 #include "bf16_ops.cuh"
@@ -11,110 +23,526 @@ namespace cgk {
 namespace row {
 
 constexpr uint32_t kThreads = 512;
+constexpr uint32_t kWarps = kThreads / 32;
+constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kBins = 1024;       // bins of one selection level
-constexpr uint32_t kSortCap = 2048;    // entries of the sorted list
+constexpr uint32_t kListCap = 2048;    // entries of a block's list and of the gathered list
+constexpr uint32_t kPairCap = 256;     // lists ranked by comparing all pairs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxBf16 = 3.38953138925e38f;  // largest finite bf16
+constexpr uint32_t kKeyInf = 0xFF800000u;      // fkey(+inf); NaN keys lie above
+constexpr uint32_t kKeyLowest = 0x00800000u;   // fkey(-FLT_MAX); fkey(-inf) lies below
 
 template <bool BF16>
-struct Row {
-  const void* x;         // the row's first logit
-  const uint32_t* mask;  // its bitmask or null
-  uint32_t V;
-  __device__ __forceinline__ bool bit(uint32_t t) const { return !mask || ((mask[t >> 5] >> (t & 31)) & 1u); }
-  __device__ __forceinline__ float value(uint32_t t) const {
-    const float v = BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(x)[t]) : static_cast<const float*>(x)[t];
-    return v != v ? -INFINITY : fminf(v, BF16 ? kMaxBf16 : FLT_MAX);
-  }
-  __device__ __forceinline__ float at(uint32_t t) const { return bit(t) ? value(t) : -INFINITY; }
-  // f(token, logit) for every allowed token, spread over the block
-  template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-    for (uint32_t t = threadIdx.x; t < V; t += blockDim.x) {
-      const float v = at(t);
-      if (v > -INFINITY) f(t, v);
-    }
-  }
+struct Fmt {
+  static constexpr uint32_t E = BF16 ? 8 : 4;         // elements per group
+  static constexpr uint32_t kSize = BF16 ? 2 : 4;     // bytes per element
+  static constexpr uint32_t kNegInf = BF16 ? 0xFF80FF80u : 0xFF800000u;
+  // selection keys: the bits that tell two logits of the type apart
+  static __device__ __forceinline__ uint32_t key(float x) { return BF16 ? fkey(x) >> 16 : fkey(x); }
 };
+
+// ---- clusters ---------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// address of the same shared variable in the block of rank r
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t r) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(r));
+  return a;
+}
+__device__ __forceinline__ void st_remote(uint32_t a, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t a, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_remote(uint32_t a, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ uint32_t ld_remote(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void ld_remote2(uint32_t a, unsigned long long& x, unsigned long long& y) {
+  asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a) : "memory");
+}
+// all blocks of the cluster (a cluster of one: the block)
+__device__ __forceinline__ void cluster_sync(uint32_t n) {
+  if (n == 1) {
+    __syncthreads();
+  } else {
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// What a block tells the others about its part of the row.
+struct __align__(16) Record {
+  float m, s;      // its maximum, its sum of exp2((x - m) c)
+  uint32_t cut;    // key: at least its share of the tokens lie at or above
+  uint32_t pad;
+};
+
+// Reductions and exchange
+struct Common {
+  Record rec[kMaxCluster];             // one per block, written by it
+  unsigned long long best[kMaxCluster];
+  unsigned long long sums[kMaxCluster];
+  unsigned long long red64[kWarps];
+  unsigned long long base;
+  uint32_t red_max[kWarps], red_min[kWarps];
+  float red_f[kWarps];
+  uint32_t n_list, n_local, bin, total;
+};
+// ... with lists and histograms
+struct Shared : Common {
+  __align__(16) unsigned long long list[kListCap];   // gathered entries (rank 0) as pack_best packs them
+  __align__(16) unsigned long long local[kListCap];  // this block's entries at or above the cut
+  __align__(16) unsigned long long hist[2][kBins];   // selection levels, alternating
+};
+
+// ---- block reductions that cost one barrier each --------------------------------------
+// (the caller keeps a barrier between two uses of the same array)
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_reduce(v, SumOp());
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_reduce(red[threadIdx.x & (kWarps - 1)], SumOp()) * 0.5f;  // every value twice in the warp
+}
+__device__ __forceinline__ float block_max(float v, float* red) {
+  v = warp_reduce(v, MaxOp());
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_reduce(red[threadIdx.x & (kWarps - 1)], MaxOp());
+}
+__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long* red) {
+  v = warp_reduce(v, SumOp());
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_reduce(red[threadIdx.x & (kWarps - 1)], SumOp()) >> 1;
+}
+__device__ __forceinline__ unsigned long long block_max(unsigned long long v, unsigned long long* red) {
+  v = warp_reduce(v, MaxOp());
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_reduce(red[threadIdx.x & (kWarps - 1)], MaxOp());
+}
+static_assert(kWarps == 16, "the reductions above read 16 warp results twice per warp");
 
 // scale of the exponent of exp((x - m) / T) as a power of two, finite for every T > 0
 __device__ __forceinline__ float exp_scale(float T) { return fminf(__fdiv_rn(kLog2e, T), FLT_MAX); }
 
-// m = max and s = sum exp2((x - m) c) over the row, to every thread
-template <bool BF16>
-__device__ void max_and_sum(const Row<BF16>& r, float c, float& m, float& s) {
-  __shared__ float red[33];
-  float a = -INFINITY;
-  r.each([&](uint32_t, float x) { a = fmaxf(a, x); });
-  m = block_reduce(a, MaxOp(), -INFINITY, red);
-  const float mm = m;
-  float b = 0.f;
-  r.each([&](uint32_t, float x) { b += ex2((x - mm) * c); });
-  s = block_reduce(b, SumOp(), 0.f, red);
+// ---- the row ----------------------------------------------------------------------------
+
+__device__ __forceinline__ uint4 ld_group(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
-// Largest key k in [lo, hi] whose upper set {key >= k} carries at least
-// `target` of the weights that each(f) reports through f(key, weight); lo when
-// none does.  Radix selection: up to 1024 equal bins of the key interval per
-// level, then the bin that the target falls into.  Integer weights: the result
-// does not depend on the order of the atomics.  hist: kBins words of shared
-// memory.  All threads take part and get the result.
+// Where a row's groups lie.  Group g holds tokens g * E - a + (0 .. E-1).
+template <bool BF16>
+struct Row {
+  using F = Fmt<BF16>;
+  const char* base;      // the row's start rounded down to 16 bytes
+  uint32_t a;            // elements between base and the row's start
+  uint32_t V;
+  const uint8_t* mask;   // the row's bitmask or null
+
+  __device__ __forceinline__ Row(const void* logits, uint64_t ld, const uint32_t* bitmask, uint32_t W, uint32_t V_,
+                                 uint32_t b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(logits) + size_t(b) * ld * F::kSize;
+    base = reinterpret_cast<const char*>(p & ~uintptr_t(15));
+    a = uint32_t(p & 15u) / F::kSize;
+    V = V_;
+    mask = bitmask ? reinterpret_cast<const uint8_t*>(bitmask + size_t(b) * W) : nullptr;
+  }
+  // Bit e: element e of group g is allowed by the bitmask.  t0 is the group's
+  // first token; some token of the group is in the row.
+  __device__ __forceinline__ uint32_t mask_bits(int t0) const {
+    if (t0 < 0) return uint32_t(mask[0]) << -t0;
+    const uint32_t sh = uint32_t(t0) & 7u;
+    uint32_t w = mask[t0 >> 3];
+    // the second byte exists: the last token of the group that is in the row lies in it or before
+    if (sh + F::E > 8u && uint32_t(t0 | 7) + 1u < V) w |= uint32_t(mask[(t0 >> 3) + 1]) << 8;
+    return w >> sh;
+  }
+  // group g's bits, -inf outside the row (the mask not applied)
+  __device__ __forceinline__ uint4 load(uint32_t g) const {
+    const int t0 = int(g * F::E) - int(a);
+    if (t0 >= 0 && uint32_t(t0) + F::E <= V) return ld_group(base + size_t(g) * 16);
+    uint4 v = make_uint4(F::kNegInf, F::kNegInf, F::kNegInf, F::kNegInf);
+    if (t0 >= int(V)) return v;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (uint32_t e = 0; e < F::E; ++e) {
+      const int t = t0 + int(e);
+      if (t < 0 || t >= int(V)) continue;
+      const char* p = base + size_t(g) * 16 + e * F::kSize;
+      if (BF16) {
+        const uint32_t h = *reinterpret_cast<const volatile uint16_t*>(p);
+        w[e >> 1] = (e & 1u) ? (w[e >> 1] & 0xFFFFu) | (h << 16) : (w[e >> 1] & 0xFFFF0000u) | h;
+      } else {
+        w[e] = *reinterpret_cast<const volatile uint32_t*>(p);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint4 masked(uint4 v, uint32_t bits) const {
+    if (BF16) return apply_mask(v, pair_mask_of(bits & 0xFFu));
+    if (!(bits & 1u)) v.x = F::kNegInf;
+    if (!(bits & 2u)) v.y = F::kNegInf;
+    if (!(bits & 4u)) v.z = F::kNegInf;
+    if (!(bits & 8u)) v.w = F::kNegInf;
+    return v;
+  }
+  __device__ __forceinline__ bool in_row(uint32_t g) const { return int(g * F::E) - int(a) < int(V); }
+  // the logit of one token with every convention applied (a plain load)
+  __device__ __forceinline__ float at(uint32_t t) const {
+    if (mask && !((mask[t >> 3] >> (t & 7u)) & 1u)) return -INFINITY;
+    return value(t);
+  }
+  __device__ __forceinline__ float value(uint32_t t) const {
+    const char* p = base + (size_t(t) + a) * F::kSize;
+    const float x = BF16 ? bf16_bits_to_float(*reinterpret_cast<const volatile uint16_t*>(p))
+                         : *reinterpret_cast<const volatile float*>(p);
+    return x != x ? -INFINITY : fminf(x, BF16 ? kMaxBf16 : FLT_MAX);
+  }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float elem(const uint4& v, uint32_t e) {
+  if (BF16) return group_at(v, e);
+  return __uint_as_float(e < 2 ? (e == 0 ? v.x : v.y) : (e == 2 ? v.z : v.w));
+}
+template <bool BF16>
+__device__ __forceinline__ float2 pair(const uint4& v, uint32_t q) {  // elements 2q and 2q + 1
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (BF16) return make_float2(lo_f(w[q]), hi_f(w[q]));
+  return make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// maximum of a group, a (positive) NaN when it holds one
+template <bool BF16>
+__device__ __forceinline__ float group_max_nan(const uint4& v) {
+  if (BF16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+    const __nv_bfloat162 r = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&r);
+    return max_nan(lo_f(u), hi_f(u));
+  }
+  return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                 max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+// NaN -> -inf, +inf -> the largest finite value
+template <bool BF16>
+__device__ __forceinline__ uint32_t clean_word(uint32_t w) {
+  if (!BF16) {
+    const float x = __uint_as_float(w);
+    return x != x ? 0xFF800000u : __float_as_uint(fminf(x, FLT_MAX));
+  }
+  uint32_t r = 0;
+#pragma unroll
+  for (uint32_t s = 0; s < 32; s += 16) {
+    uint32_t h = (w >> s) & 0xFFFFu;
+    if ((h & 0x7FFFu) > 0x7F80u) h = 0xFF80u;
+    else if (h == 0x7F80u) h = 0x7F7Fu;
+    r |= h << s;
+  }
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 clean_group(uint4 v) {
+  return make_uint4(clean_word<BF16>(v.x), clean_word<BF16>(v.y), clean_word<BF16>(v.z), clean_word<BF16>(v.w));
+}
+
+// bit e: element e >= cut (cut finite; for bf16 the least bf16 not below it in both halves of cut2)
+template <bool BF16>
+__device__ __forceinline__ uint32_t ge_bits(const uint4& v, float cut, uint32_t cut2) {
+  if (BF16) return group_ge_bits(v, cut2);
+  return (__uint_as_float(v.x) >= cut ? 1u : 0u) | (__uint_as_float(v.y) >= cut ? 2u : 0u) |
+         (__uint_as_float(v.z) >= cut ? 4u : 0u) | (__uint_as_float(v.w) >= cut ? 8u : 0u);
+}
+__device__ __forceinline__ uint32_t bf16_pair_up(float cut) {
+  const __nv_bfloat162 t = __bfloat162bfloat162(__float2bfloat16_ru(cut));
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// The part of a row that a block holds, and what the cluster knows of the row.
+template <bool BF16, int NV>
+struct Held {
+  using F = Fmt<BF16>;
+  Row<BF16> r;
+  uint32_t n, rank;   // cluster size, this block
+  uint4 v[NV];
+  uint32_t tkey;      // fkey of this thread's maximum
+  float m;            // block maximum
+
+  __device__ __forceinline__ Held(const Row<BF16>& row) : r(row), n(cluster_size()), rank(cluster_rank()) {}
+  // group j of this thread: consecutive threads hold consecutive groups, the
+  // blocks take turns at runs of 512
+  __device__ __forceinline__ uint32_t group(uint32_t j) const { return (j * n + rank) * kThreads + threadIdx.x; }
+  __device__ __forceinline__ int first_token(uint32_t j) const { return int(group(j) * F::E) - int(r.a); }
+
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = r.load(group(j));
+    if (r.mask) {
+      uint32_t bits[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) bits[j] = r.in_row(group(j)) ? r.mask_bits(first_token(j)) : 0u;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = r.masked(v[j], bits[j]);
+    }
+  }
+  __device__ __forceinline__ float thread_max() const {
+    float t = group_max_nan<BF16>(v[0]);
+#pragma unroll
+    for (int j = 1; j < NV; ++j) t = max_nan(t, group_max_nan<BF16>(v[j]));
+    return t;
+  }
+  // block maximum (NaN and +inf replaced first if there are any); lo receives
+  // the least thread maximum's key
+  __device__ __forceinline__ void find_max(Common& s, uint32_t& lo) {
+    for (int pass = 0;; ++pass) {
+      tkey = fkey(thread_max());
+      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, tkey), low = __reduce_min_sync(0xFFFFFFFFu, tkey);
+      if ((threadIdx.x & 31) == 0) {
+        s.red_max[threadIdx.x >> 5] = hi;
+        s.red_min[threadIdx.x >> 5] = low;
+      }
+      __syncthreads();
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, s.red_max[threadIdx.x & (kWarps - 1)]);
+      lo = __reduce_min_sync(0xFFFFFFFFu, s.red_min[threadIdx.x & (kWarps - 1)]);
+      m = fkey_inv(top);
+      if (top < kKeyInf || pass) return;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = clean_group<BF16>(v[j]);
+      __syncthreads();
+    }
+  }
+  // the same replacement without the block
+  __device__ __forceinline__ void clean_own() {
+    if (fkey(thread_max()) < kKeyInf) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = clean_group<BF16>(v[j]);
+  }
+  // block sum of exp2((x - m) c)
+  __device__ __forceinline__ float sum_exps(Common& s, float c) const {
+    float t = 0.f;
+    if (m > -INFINITY) {
+      const float2 nm = make_float2(-m, -m), c2 = make_float2(c, c);
+      float2 acc[4] = {};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (uint32_t q = 0; q < F::E / 2; ++q)
+          acc[q] = __fadd2_rn(acc[q], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[j], q), nm), c2)));
+#pragma unroll
+      for (uint32_t q = 0; q < 4; ++q) t += acc[q].x + acc[q].y;
+    }
+    return block_sum(t, s.red_f);
+  }
+  // A key such that at least `share` threads of the block hold a token at or
+  // above it (0 when fewer threads hold any): bisection over the thread maxima.
+  __device__ __forceinline__ uint32_t share_cut(uint32_t share, uint32_t lo) const {
+    if (share > kThreads) return 0u;
+    uint32_t hi = fkey(m);
+    if (__syncthreads_count(tkey >= hi) >= int(share)) return hi;
+#pragma unroll 1
+    for (int i = 0; i < 16 && hi - lo > 0x2000u; ++i) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      if (__syncthreads_count(tkey >= mid) >= int(share)) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+  // f(token, logit) for every element of this block's part that is >= cut,
+  // from memory again (for parts too large for the lists)
+  template <typename Fn>
+  __device__ __forceinline__ void each_slow(float cut, Fn f) const {
+#pragma unroll 1
+    for (uint32_t j = 0; j < NV; ++j) {
+      const uint32_t g = group(j);
+      if (!r.in_row(g)) break;
+      uint4 x = clean_group<BF16>(r.load(g));
+      if (r.mask) x = r.masked(x, r.mask_bits(first_token(j)));
+#pragma unroll 1
+      for (uint32_t e = 0; e < F::E; ++e) {
+        const float y = elem<BF16>(x, e);
+        if (y >= cut) f(uint32_t(first_token(j)) + e, y);
+      }
+    }
+  }
+  // Appends (logit, token) of every element >= cut to a list of kListCap
+  // entries: this block's own (to_rank0 false) or rank 0's gathered one.  The
+  // count goes on past the capacity, the entries do not.  Order is arbitrary.
+  __device__ __forceinline__ void collect(Shared& s, float cut, bool to_rank0) const {
+    const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u, lane = threadIdx.x & 31;
+    uint32_t hits[(NV + 3) / 4] = {};
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint32_t h = ge_bits<BF16>(v[j], cut, cut2);
+      hits[j / 4] |= h << (8 * (j % 4));
+    }
+#pragma unroll
+    for (int i = 0; i < (NV + 3) / 4; ++i) mine += __popc(hits[i]);
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= uint32_t(o)) inc += y;
+    }
+    uint32_t at = 0;
+    if (lane == 31 && inc)
+      at = to_rank0 ? add_remote(at_rank(&s.n_list, 0), inc) : atomicAdd(&s.n_local, inc);
+    at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - mine;
+    const uint32_t list = at_rank(to_rank0 ? s.list : s.local, to_rank0 ? 0u : rank);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      uint32_t h = (hits[j / 4] >> (8 * (j % 4))) & 0xFFu;
+      while (h) {
+        const uint32_t e = __ffs(h) - 1;
+        h &= h - 1;
+        if (at < kListCap) st_remote(list + at * 8, pack_best(elem<BF16>(v[j], e), uint32_t(first_token(j)) + e));
+        ++at;
+      }
+    }
+  }
+  // f(token, logit) for every element >= cut, after collect() into the block's
+  // own list with that cut and a barrier: from the list when it holds them all
+  template <typename Fn>
+  __device__ __forceinline__ void each(const Shared& s, float cut, Fn f) const {
+    if (s.n_local <= kListCap) {
+      for (uint32_t i = threadIdx.x; i < s.n_local; i += kThreads) {
+        const unsigned long long e = s.local[i];
+        f(best_id(e), fkey_inv(uint32_t(e >> 32)));
+      }
+    } else {
+      each_slow(cut, f);
+    }
+  }
+};
+
+// Publishes this block's record to every block of the cluster and waits for all
+// of theirs.  The blocks must have met once before (their shared memory exists).
+__device__ __forceinline__ void exchange(Common& s, uint32_t n, uint32_t rank, float m, float sum, uint32_t cut) {
+  if (threadIdx.x < n) {
+    const uint4 rec = make_uint4(__float_as_uint(m), __float_as_uint(sum), cut, 0u);
+    st_remote(at_rank(&s.rec[rank], threadIdx.x), rec);
+  }
+  cluster_sync(n);
+}
+// The row's maximum, sum of exp2((x - M) c) and the least of the cuts
+__device__ __forceinline__ void merge(const Common& s, uint32_t n, float c, float& M, float& S, uint32_t& cut) {
+  M = -INFINITY;
+  cut = 0xFFFFFFFFu;
+  for (uint32_t i = 0; i < n; ++i) {
+    M = fmaxf(M, s.rec[i].m);
+    cut = min(cut, s.rec[i].cut);
+  }
+  S = 0.f;
+  for (uint32_t i = 0; i < n; ++i)
+    if (s.rec[i].m > -INFINITY) S += s.rec[i].s * ex2((s.rec[i].m - M) * c);
+}
+
+// Largest key k in [lo, hi] whose upper set {key >= k}, over the whole row,
+// carries at least `target` of the weights that each(f) reports for this block's
+// part through f(key, weight); lo when none does.  Radix selection: up to 1024
+// equal bins of the key interval per level, the blocks' bins added up by every
+// block, then the bin that the target falls into.  Integer weights: the result
+// does not depend on the order of the atomics.  `above` receives the weight of
+// the keys above the result's bin.  `level` counts the uses of the two
+// histograms (start with 0, keep it).
 template <typename Each>
-__device__ uint32_t select_key(Each each, uint32_t lo, uint32_t hi, unsigned long long target,
-                               unsigned long long* hist) {
-  __shared__ unsigned long long s_part[33];
-  __shared__ uint32_t s_bin;
-  __shared__ unsigned long long s_base;
+__device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, uint32_t hi, unsigned long long target,
+                               uint32_t& level, unsigned long long& above) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned long long base = 0;  // weight above hi
+  above = 0;
   for (;;) {
     const uint32_t range = hi - lo;
     const uint32_t shift = range < kBins ? 0u : 22u - __clz(range);
-    __syncthreads();
-    for (uint32_t i = tid; i < kBins; i += kThreads) hist[i] = 0ull;
-    if (tid == 0) s_bin = kBins;
+    unsigned long long* hist = s.hist[level++ & 1u];
+    // the level two before, which used this histogram, was read by every block
+    // before the cluster met in the level between
+    hist[tid] = 0ull;
+    hist[tid + kThreads] = 0ull;
+    if (tid == 0) s.bin = kBins;
     __syncthreads();
     each([&](uint32_t key, unsigned long long w) {
       if (key >= lo && key <= hi) atomicAdd(hist + ((hi - key) >> shift), w);
     });
-    __syncthreads();
+    cluster_sync(n);
     // two bins a thread, bins in order
-    const unsigned long long h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
+    unsigned long long h0 = 0, h1 = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+      unsigned long long x, y;
+      ld_remote2(at_rank(hist + 2 * tid, i), x, y);
+      h0 += x;
+      h1 += y;
+    }
     unsigned long long inc = h0 + h1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= uint32_t(o)) inc += y;
     }
-    if (lane == 31) s_part[warp] = inc;
+    if (lane == 31) s.red64[warp] = inc;
     __syncthreads();
-    unsigned long long before = base;
-    for (uint32_t i = 0; i < warp; ++i) before += s_part[i];
+    unsigned long long before = above;
+    for (uint32_t i = 0; i < warp; ++i) before += s.red64[i];
     before += inc - h0 - h1;
-    if (before + h0 + h1 >= target) atomicMin(&s_bin, before + h0 >= target ? 2 * tid : 2 * tid + 1);
+    if (before + h0 + h1 >= target) atomicMin(&s.bin, before + h0 >= target ? 2 * tid : 2 * tid + 1);
     __syncthreads();
-    const uint32_t bin = s_bin;
+    const uint32_t bin = s.bin;
+    if (bin >> 1 == tid) s.base = before + ((bin & 1u) ? h0 : 0ull);
+    __syncthreads();
     if (bin == kBins) return lo;
-    if (bin >> 1 == tid) s_base = before + ((bin & 1u) ? h0 : 0ull);
-    __syncthreads();
-    base = s_base;
+    above = s.base;
     hi -= bin << shift;
     const uint32_t width = (1u << shift) - 1u;
     lo = hi - lo > width ? hi - width : lo;
     if (shift == 0) return hi;
+    __syncthreads();  // s.bin is set again above
   }
 }
+static_assert(kBins == 2 * kThreads, "two bins a thread");
 
 // Descending sort of list[0 .. n) (bitonic network over the next power of two,
-// padded with zeros, which sort last).  list: kSortCap words of shared memory.
+// padded with zeros, which sort last).  list: kListCap words of shared memory.
 __device__ inline void sort_desc(unsigned long long* list, uint32_t n) {
   uint32_t N = 2;
   while (N < n) N <<= 1;
-  for (uint32_t i = n + threadIdx.x; i < N; i += blockDim.x) list[i] = 0ull;
+  for (uint32_t i = n + threadIdx.x; i < N; i += kThreads) list[i] = 0ull;
   __syncthreads();
   for (uint32_t k = 2; k <= N; k <<= 1)
     for (uint32_t j = k >> 1; j > 0; j >>= 1) {
-      for (uint32_t i = threadIdx.x; i < N / 2; i += blockDim.x) {
+      for (uint32_t i = threadIdx.x; i < N / 2; i += kThreads) {
         const uint32_t a = 2 * i - (i & (j - 1)), b = a + j;
         const unsigned long long x = list[a], y = list[b];
         if ((x < y) == ((a & k) == 0)) {
@@ -126,6 +554,69 @@ __device__ inline void sort_desc(unsigned long long* list, uint32_t n) {
     }
 }
 
+// ---- launching -----------------------------------------------------------------------
+
+// NV and the cluster size of a launch.  Few rows take the smallest NV (the
+// widest cluster): the row is split over more SMs while all blocks are resident
+// together; many rows take NV = 8, two blocks an SM.
+struct Plan {
+  uint32_t nv, n;
+};
+inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned) {
+  const uint32_t E = bf16 ? 8 : 4;
+  const uint32_t groups = (V + (aligned ? 0 : E - 1) + E - 1) / E;
+  Plan best{0, 0};
+  for (uint32_t nv : {1u, 2u, 4u, 8u, 16u, 24u}) {
+    const uint32_t n = (groups + kThreads * nv - 1) / (kThreads * nv);
+    if (n > kMaxCluster || (best.nv && nv > 8)) continue;
+    best = {nv, n};
+    if (n == 1 || uint64_t(B) * n <= 2 * 152) break;
+  }
+  return best;
+}
+
+// Launches Kernel on clusters of n blocks, `rows` of them.  The dynamic shared
+// memory limit is raised on the first launch on a device.
+template <auto Kernel, typename... Args>
+cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, size_t smem, cudaStream_t stream, Args&&... args) {
+  static std::atomic<uint64_t> raised{0};
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if (smem > 48 * 1024 && !(raised.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows * n);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = n;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, Kernel, std::forward<Args>(args)...);
+}
+
+// f<NV>() for the plan's NV (24 only for floats, whose rows are the longest)
+template <bool BF16, typename Fn>
+cudaError_t with_nv(uint32_t nv, Fn f) {
+  switch (nv) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 8: return f(std::integral_constant<int, 8>());
+    case 16: return f(std::integral_constant<int, 16>());
+    case 24: return f(std::integral_constant<int, BF16 ? 16 : 24>());
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 }  // namespace row
 
 // Host checks shared by the per-row entry points: an aligned pointer of the
@@ -134,10 +625,13 @@ inline bool row_args_ok(const cg_ctx* c, const void* logits, int dtype, uint32_t
                         const uint32_t* bitmask) {
   if (!c || (dtype != CG_F32 && dtype != CG_BF16)) return false;
   if (V != ctx_view(c).t.V || ld < V || ld > (uint64_t(1) << 40)) return false;
-  if (B > 0x07FFFFFFu || (B && !logits)) return false;  // the grid: a few blocks a row
+  if (B > 0x07FFFFFFu || (B && !logits)) return false;  // the grid: up to 8 blocks a row
   const uintptr_t size = dtype == CG_BF16 ? 2 : 4;
   return reinterpret_cast<uintptr_t>(logits) % size == 0 && reinterpret_cast<uintptr_t>(bitmask) % 4 == 0;
 }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool rows_on_grid(const void* logits, int dtype, uint64_t ld) {
+  return ((reinterpret_cast<uintptr_t>(logits) | (ld * (dtype == CG_BF16 ? 2 : 4))) & 15u) == 0;
+}
 
 }  // namespace cgk
