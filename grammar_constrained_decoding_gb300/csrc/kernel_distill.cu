@@ -81,7 +81,7 @@ __device__ __forceinline__ void store_group(char* row, int t0, uint32_t V, bool 
 }
 
 template <bool BF16, int NV, bool LOSS>
-__global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   List& l = reinterpret_cast<DistillShared*>(smem)->list;
   Common& s = reinterpret_cast<DistillShared*>(smem)->s;

@@ -15,11 +15,10 @@
 //          together less than (1 - p) S of the mass S, so the threshold lies
 //          above them;
 //   min-p  is the threshold itself.
-// Only tokens at or above the bound matter from there on.  When they are few
-// they are gathered by rank 0, which settles the cuts by comparing all pairs
-// (the weight strictly above each token decides whether it stays); otherwise
-// every block keeps its own list and the threshold comes from histograms over
-// the cluster.
+// Only tokens at or above the bound matter from there on.  Where they are few by
+// the settings (top-k, min-p) rank 0 gathers and settles them; where they may be
+// many (top-p, a large k) the blocks count them by key, add up the counts, find
+// the threshold and each draw from their own part.
 #include "logit_row.cuh"
 
 namespace cgk {
@@ -46,11 +45,11 @@ struct DrawArgs {
   uint32_t* status;
 };
 
-// top-k rows up to this k, and top-p rows whose nucleus holds at least this
-// mass in units of the best token, are gathered; beyond it the list would
-// overflow its kListCap entries as a rule
+// top-k rows up to this k, and min-p rows whose kept tokens cannot be more than
+// this, are gathered: the list then overflows only by ties
 constexpr uint32_t kGatherK = 1024;
-constexpr float kGatherMass = 256.f;
+constexpr float kGatherCount = 1536.f;
+constexpr float kMassOne = 1099511627776.f;  // mass_q of the maximum
 
 struct RowSettings {
   float T, Ts, p, floor_z;  // Ts: the softmax's temperature (1 for greedy rows)
@@ -58,86 +57,294 @@ struct RowSettings {
   bool greedy;
 };
 
+__device__ __forceinline__ float clamp_u(float u) { return fminf(fmaxf(u, kULo), kUHi); }
 // score of a kept token; false when min-p drops it
-__device__ __forceinline__ bool score_of(const RowSettings& q, float d, const float* u, uint32_t t, float& score) {
-  if (q.greedy) {
-    score = 0.f;
-    return true;
-  }
+__device__ __forceinline__ bool score_of(const RowSettings& q, float d, float u, float& score) {
   const float z = __fdiv_rn(d, q.T);
-  if (!(z >= q.floor_z)) return false;
-  score = z - logf(-logf(fminf(fmaxf(u[t], kULo), kUHi)));
-  return true;
+  score = z - logf(-logf(clamp_u(u)));
+  return z >= q.floor_z;
+}
+__device__ __forceinline__ unsigned long long mass_target(float p, unsigned long long kept) {
+  const unsigned long long t = static_cast<unsigned long long>(double(p) * double(kept));
+  return t ? t : 1ull;
+}
+__device__ __forceinline__ unsigned long long mass_total(float S) {
+  return static_cast<unsigned long long>(double(S) * double(kMassOne));
 }
 
-// Rank 0: the threshold key of list[0 .. c) under top-k and top-p.  kept_mass:
-// the mass top-p is relative to when there is no top-k.
-__device__ uint32_t list_threshold(Shared& s, uint32_t c, const RowSettings& q, float M, float scale, float S) {
-  uint32_t tau = 0;
-  if (c <= kPairCap) {
-    // entry i against all: parts of the block take parts of the list
-    uint32_t C = 32;
-    while (C < c) C <<= 1;
-    const uint32_t i = threadIdx.x & (C - 1), part = threadIdx.x / C, parts = kThreads / C;
-    unsigned long long* above_n = s.hist[0];            // [C]
-    unsigned long long* above_w = s.hist[0] + kPairCap; // [C]
-    if (threadIdx.x < C) above_n[threadIdx.x] = above_w[threadIdx.x] = 0ull;
-    __syncthreads();
-    const uint32_t key = i < c ? uint32_t(s.list[i] >> 32) : 0u;
-    const unsigned long long w = i < c ? mass_q(fkey_inv(key), M, scale) : 0ull;
-    if (i < c) {
-      unsigned long long nn = 0, ww = 0;
-      for (uint32_t j = part; j < c; j += parts) {
-        const uint32_t kj = uint32_t(s.list[j] >> 32);
-        if (kj > key) {
-          ++nn;
-          ww += mass_q(fkey_inv(kj), M, scale);
-        }
-      }
-      if (nn) atomicAdd(above_n + i, nn);
-      if (ww) atomicAdd(above_w + i, ww);
-    }
-    __syncthreads();
-    bool stays = i < c && (q.k == 0 || above_n[i] < q.k);
-    if (q.p < 1.f) {
-      unsigned long long kept = static_cast<unsigned long long>(double(S) * 1099511627776.0);
-      if (q.k) kept = block_sum(stays && part == 0 ? w : 0ull, s.red64);
-      unsigned long long target = static_cast<unsigned long long>(double(q.p) * double(kept));
-      stays = stays && above_w[i] < (target ? target : 1ull);
-    }
-    // the least key that stays
-    const uint32_t low = __reduce_min_sync(0xFFFFFFFFu, stays ? key : 0xFFFFFFFFu);
-    if ((threadIdx.x & 31) == 0) s.red_min[threadIdx.x >> 5] = low;
-    __syncthreads();
-    return __reduce_min_sync(0xFFFFFFFFu, s.red_min[threadIdx.x & (kWarps - 1)]);
-  }
-  uint32_t level = 0;
-  unsigned long long above;
+// The threshold's key (fkey) under top-k and top-p by radix selection over the
+// weights that keys(f) reports through f(key), in one block or over the cluster
+template <typename Keys>
+__device__ uint32_t threshold_by_levels(Shared& s, uint32_t n, uint32_t rank, Keys keys, const RowSettings& q,
+                                        float cut, float M, float scale, float S) {
   const uint32_t top = fkey(M);
-  auto entries = [&](auto f) {
-    for (uint32_t i = threadIdx.x; i < c; i += kThreads) f(uint32_t(s.list[i] >> 32));
-  };
-  if (q.k && q.k < c)
-    tau = select_key(s, 1, [&](auto f) { entries([&](uint32_t key) { f(key, 1ull); }); }, kKeyLowest, top, q.k, level,
-                     above);
-  if (q.p < 1.f) {
-    unsigned long long kept = static_cast<unsigned long long>(double(S) * 1099511627776.0);
-    if (q.k) {
-      unsigned long long w = 0;
-      entries([&](uint32_t key) { w += key >= tau ? mass_q(fkey_inv(key), M, scale) : 0ull; });
-      __syncthreads();
-      kept = block_sum(w, s.red64);
-      __syncthreads();
+  uint32_t tau = fkey(cut), level = 0;
+  unsigned long long above;
+  if (q.k) tau = select_key(s, n, [&](auto f) { keys([&](uint32_t key) { f(key, 1ull); }); }, tau, top, q.k, level, above);
+  if (q.p >= 1.f) return tau;
+  unsigned long long kept = mass_total(S);
+  if (q.k) {  // the mass of what top-k keeps
+    unsigned long long w = 0;
+    keys([&](uint32_t key) { w += key >= tau ? mass_q(fkey_inv(key), M, scale) : 0ull; });
+    __syncthreads();
+    w = block_sum(w, s.red64);
+    kept = w;
+    if (n > 1) {
+      if (threadIdx.x < n) st_remote(at_rank(&s.sums[rank], threadIdx.x), w);
+      cluster_sync(n);
+      kept = 0;
+      for (uint32_t i = 0; i < n; ++i) kept += s.sums[i];
     }
-    const unsigned long long target = static_cast<unsigned long long>(double(q.p) * double(kept));
-    tau = select_key(s, 1, [&](auto f) { entries([&](uint32_t key) { f(key, mass_q(fkey_inv(key), M, scale)); }); },
-                     max(tau, kKeyLowest), top, target ? target : 1ull, level, above);
   }
-  return tau;
+  return select_key(s, n, [&](auto f) { keys([&](uint32_t key) { f(key, mass_q(fkey_inv(key), M, scale)); }); }, tau, top,
+                    mass_target(q.p, kept), level, above);
+}
+
+// ---- counting bf16 keys -----------------------------------------------------------
+// Tokens of one bf16 value have one mass, so counts per value give both the
+// k-th largest and every upper set's mass.  Bins follow the values from M down to
+// the cut: a signed magnitude index, magnitudes up to H0 sharing bin 0 (their
+// tokens' mass is added up apart, should there be several values).  H0 is 0, or
+// M's or the cut's magnitude when both have one sign, or, where the interval
+// reaches over zero, the least that leaves kCounts bins: 2^-14 or so of the
+// largest magnitude.
+struct KeyBins {
+  uint32_t H0;
+  int top;       // signed index of M
+  uint32_t n;    // bins
+  bool one0;     // bin 0 holds a single value
+
+  __device__ __forceinline__ int index(uint32_t h) const {
+    const int q = int(max(h & 0x7FFFu, H0) - H0);
+    return (h & 0x8000u) ? -q : q;
+  }
+  __device__ __forceinline__ KeyBins(float M, float cut) {
+    uint32_t hm = __float_as_uint(M) >> 16, hc = bf16_pair_up(cut) & 0xFFFFu;
+    hm = hm == 0x8000u ? 0u : hm;
+    hc = hc == 0x8000u ? 0u : hc;
+    const uint32_t a = hm & 0x7FFFu, b = hc & 0x7FFFu, big = max(a, b), most = kCounts - 2;
+    const uint32_t low = big > most ? big - most : 0u;
+    if ((hm ^ hc) & 0x8000u) {
+      H0 = max(low, a + b > most ? (a + b - most + 1) / 2 : 0u);
+      one0 = H0 == 0;
+    } else {
+      H0 = max(low, min(a, b));
+      one0 = H0 == min(a, b);
+    }
+    top = index(hm);
+    n = uint32_t(top - index(hc)) + 1u;
+  }
+  __device__ __forceinline__ uint32_t bin(uint32_t h) const { return min(uint32_t(top - index(h)), n - 1u); }
+  __device__ __forceinline__ bool is_odd(uint32_t i) const { return !one0 && int(i) == top; }
+  // the value of bin i (of the odd bin: zero)
+  __device__ __forceinline__ float value(uint32_t i) const {
+    const int q = top - int(i);
+    if (q == 0 && !one0) return 0.f;
+    const uint32_t h = H0 + uint32_t(q < 0 ? -q : q);
+    // bin 0 with a single value other than zero is M or the cut, of the sign of both
+    return bf16_bits_to_float(q < 0 || (q == 0 && negative0) ? h | 0x8000u : h);
+  }
+  bool negative0 = false;
+};
+
+// First bin at which the running sum of weight(i) reaches target, from bin 0 to
+// n - 1; n when it never does.  before: the sum above it.
+template <typename Weight>
+__device__ uint32_t find_bin(Shared& s, uint32_t n, unsigned long long target, Weight weight,
+                             unsigned long long& before) {
+  const uint32_t tid = threadIdx.x;
+  unsigned long long base = 0;
+  for (uint32_t from = 0; from < n; from += 4 * kThreads) {
+    __syncthreads();
+    if (tid == 0) s.bin = n;
+    unsigned long long w[4], mine = 0;
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      const uint32_t i = from + 4 * tid + q;
+      w[q] = i < n ? weight(i) : 0ull;
+      mine += w[q];
+    }
+    const unsigned long long upto = base + block_scan(mine, s.red64);
+    if (tid == kThreads - 1) s.base = upto;
+    if (upto >= target && upto - mine < target) {
+      unsigned long long b = upto - mine;
+      uint32_t i = 0;
+#pragma unroll
+      for (uint32_t q = 0; q < 3; ++q)
+        if (i == q && b + w[q] < target) {
+          b += w[q];
+          ++i;
+        }
+      s.bin = from + 4 * tid + i;
+      s.sums[0] = b;
+    }
+    __syncthreads();
+    if (s.bin < n) {
+      before = s.sums[0];
+      return s.bin;
+    }
+    base = s.base;
+  }
+  before = base;
+  return n;
+}
+
+// The threshold (a value) under top-k and top-p of a bf16 row by counting; false
+// when it falls among the several values of the odd bin.
+template <int NV>
+__device__ bool threshold_by_counts(Shared& s, const Held<true, NV>& h, const RowSettings& q, float cut, float M,
+                                    float scale, float S, float& tau) {
+  const uint32_t tid = threadIdx.x;
+  KeyBins bins(M, cut);
+  bins.negative0 = M < 0.f;
+  const uint32_t words = (bins.n + 3u) & ~3u;
+  for (uint32_t i = tid; i < words; i += kThreads) s.counts[i] = 0u;
+  if (tid == 0) s.odd_mass = 0ull;
+  __syncthreads();
+  const uint32_t cut2 = bf16_pair_up(cut);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const uint32_t hits = group_ge_bits(h.v[j], cut2);
+    if (!hits) continue;
+    const uint32_t w[4] = {h.v[j].x, h.v[j].y, h.v[j].z, h.v[j].w};
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e)
+      if ((hits >> e) & 1u) {
+        const uint32_t i = bins.bin((e & 1u) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
+        atomicAdd(s.counts + i, 1u);
+        if (bins.is_odd(i)) atomicAdd(&s.odd_mass, mass_q(group_at(h.v[j], e), M, scale));
+      }
+  }
+  cluster_sync(h.n);
+  // the whole row's counts, four bins a load
+  for (uint32_t i = 4 * tid; i < words; i += 4 * kThreads) {
+    uint4 t = make_uint4(0u, 0u, 0u, 0u);
+    for (uint32_t r = 0; r < h.n; ++r) {
+      const uint4 x = ld_remote4(at_rank(s.counts + i, r));
+      t.x += x.x;
+      t.y += x.y;
+      t.z += x.z;
+      t.w += x.w;
+    }
+    *reinterpret_cast<uint4*>(s.merged + i) = t;
+  }
+  unsigned long long odd = 0;
+  if (!bins.one0)
+    for (uint32_t r = 0; r < h.n; ++r) odd += ld_remote64(at_rank(&s.odd_mass, r));
+  __syncthreads();
+  auto mass = [&](uint32_t i) {
+    return bins.is_odd(i) ? odd : static_cast<unsigned long long>(s.merged[i]) * mass_q(bins.value(i), M, scale);
+  };
+  uint32_t last = bins.n - 1;
+  unsigned long long before, kept = mass_total(S);
+  if (q.k) {
+    last = min(last, find_bin(s, bins.n, q.k, [&](uint32_t i) { return static_cast<unsigned long long>(s.merged[i]); }, before));
+    if (q.p < 1.f) {
+      unsigned long long w = 0;
+      for (uint32_t i = tid; i <= last; i += kThreads) w += mass(i);
+      kept = block_sum(w, s.red64b);
+    }
+  }
+  if (q.p < 1.f) last = min(last, find_bin(s, last + 1u, mass_target(q.p, kept), mass, before));
+  tau = bins.value(last);
+  return !bins.is_odd(last);
+}
+
+// ---- drawing ------------------------------------------------------------------------
+
+// Rank 0: draws from the gathered list[0 .. c), c <= kPairCap, an entry a thread.
+// In order, with running masses, the cuts are positions; the random numbers are
+// on their way meanwhile.
+__device__ unsigned long long draw_sorted(Shared& s, uint32_t c, const RowSettings& q, float M, float scale, float S,
+                                          const float* u) {
+  const uint32_t tid = threadIdx.x;
+  const unsigned long long e = tid < c ? s.list[tid] : 0ull;
+  const float ut = tid < c ? u[best_id(e)] : 0.5f;
+  uint32_t tau = 0;
+  if (q.k || q.p < 1.f) {
+    place_entries(s, c);
+    if (tid < c) s.sorted[s.place[tid]] = e;
+    __syncthreads();
+    const uint32_t key = tid < c ? uint32_t(s.sorted[tid] >> 32) : 0u;
+    if (q.k && q.k <= c) tau = uint32_t(s.sorted[q.k - 1] >> 32);
+    if (q.p < 1.f) {
+      const unsigned long long upto = block_scan(tid < c ? mass_q(fkey_inv(key), M, scale) : 0ull, s.red64);
+      unsigned long long kept = mass_total(S);
+      if (q.k) kept = block_max(key >= tau && tid < c ? upto : 0ull, s.red64b);
+      // the best place whose running mass reaches the target
+      uint32_t at = upto >= mass_target(q.p, kept) ? key : 0u;
+      at = block_max(at, s.red_max);
+      tau = max(tau, at);
+    }
+  }
+  unsigned long long best = 0ull;
+  float score;
+  if (tid < c && uint32_t(e >> 32) >= tau && score_of(q, fkey_inv(uint32_t(e >> 32)) - M, ut, score))
+    best = pack_best(score, best_id(e));
+  __syncthreads();
+  return block_max(best, s.red64);
+}
+
+// Draws from this block's part, tokens >= tau, when they are too many to list:
+// from -log u >= 1 - u, a score is at most z - log(1 - u), which costs one
+// logarithm in the multi-function unit.  Every thread finds its two best bounds
+// and scores the first exactly; a thread whose second bound reaches the block's
+// best exact score scores its whole part.
+template <bool BF16, int NV>
+__device__ unsigned long long draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSettings& q, float tau, float M,
+                                            float c, const float* u) {
+  constexpr uint32_t E = Fmt<BF16>::E;
+  const bool wide = ((reinterpret_cast<uintptr_t>(u) / 4 - h.r.a) & 3u) == 0;
+  float first = -INFINITY, second = -INFINITY, fx = 0.f;
+  uint32_t ft = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int t0 = h.first_token(j);
+    if (t0 >= int(h.r.V)) continue;
+    float un[E];
+    if (wide && t0 >= 0 && uint32_t(t0) + E <= h.r.V) {
+#pragma unroll
+      for (uint32_t i = 0; i < E / 4; ++i) {
+        const uint4 w = ld_group(u + t0 + 4 * i);
+        un[4 * i] = __uint_as_float(w.x);
+        un[4 * i + 1] = __uint_as_float(w.y);
+        un[4 * i + 2] = __uint_as_float(w.z);
+        un[4 * i + 3] = __uint_as_float(w.w);
+      }
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e) un[e] = t0 + int(e) >= 0 && t0 + int(e) < int(h.r.V) ? u[t0 + int(e)] : 0.5f;
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e) {
+      const float x = elem<BF16>(h.v[j], e);
+      float lg;
+      asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(1.f - clamp_u(un[e])));
+      const float ub = x >= tau ? (x - M) * c - lg : -INFINITY;
+      second = fmaxf(second, fminf(first, ub));
+      if (ub > first) {
+        first = ub;
+        fx = x;
+        ft = uint32_t(t0) + e;
+      }
+    }
+  }
+  unsigned long long best = 0ull;
+  float score;
+  if (first > -INFINITY && score_of(q, fx - M, u[ft], score)) best = pack_best(score, ft);
+  best = block_max(best, s.red64);
+  // 1e-3 covers the roundings of the bound (bounds in bits, scores in nats)
+  if (second > -INFINITY && (best == 0ull || second * 0.6931472f + 1e-3f >= fkey_inv(uint32_t(best >> 32)))) {
+    h.each(tau, [&](uint32_t t, float x) {
+      float sc;
+      if (score_of(q, x - M, u[t], sc)) best = max(best, pack_best(sc, t));
+    });
+  }
+  return block_max(best, s.red64b);
 }
 
 template <bool BF16, int NV>
-__global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) draw_kernel(const DrawArgs a) {
+__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const DrawArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   griddep_launch_dependents();
@@ -155,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) draw_kernel(const D
   q.greedy = q.T == 0.f;
   q.Ts = q.greedy ? 1.f : q.T;
   const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || p != p || mp != mp || (!q.greedy && !a.u);
-  if (q.k >= a.V) q.k = 0;
+  if (q.k >= a.V || q.greedy) q.k = 0;
   q.floor_z = logf(fminf(fmaxf(mp, 0.f), 1.f));  // -inf for min_p = 0
   const float c = exp_scale(q.Ts);
 
   uint32_t low, cut_key = 0;
   h.find_max(s, low);
   const float sum = bad ? 0.f : h.sum_exps(s, c);
-  if (q.k && !q.greedy) cut_key = h.share_cut((q.k + n - 1) / n, low);
+  if (q.k) cut_key = h.share_cut((q.k + n - 1) / n, low);
   if (n > 1) cluster_wait();
   exchange(s, n, rank, h.m, sum, cut_key);
   float M, S;
@@ -178,96 +385,93 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) draw_kernel(const D
     return;  // nobody reads this block's shared memory after the exchange
   }
 
-  // a lower bound of the threshold, and how to settle it
+  // a lower bound of the threshold, and how to settle it.  Without top-k the
+  // mass that top-p refers to is known, so min-p bounds what matters as well.
   float cut = -FLT_MAX;
-  bool gather = false, select = false;
+  bool gather = false;
   if (q.greedy) {
     cut = M;
   } else if (q.k) {
     if (cut_key >= kKeyLowest) cut = fkey_inv(cut_key);
     gather = q.k <= kGatherK;
-    select = !gather;
-  } else if (q.p < 1.f) {
-    // 1e-3 nats more than D, for the roundings
-    const float D = logf(float(a.V) / ((1.f - q.p) * S)) + 1e-3f;
-    cut = fmaxf(M - D * q.T, -FLT_MAX);
-    gather = q.p * S <= kGatherMass;
-    select = !gather;
   } else {
-    // min-p alone: z >= floor_z decides, a little above its rounding
-    cut = fmaxf(M + q.floor_z * q.T * (q.floor_z < 0.f ? 1.000001f : 1.f) - 1e-6f * fabsf(M), -FLT_MAX);
+    // a little below M + T log(min_p), for the roundings
+    if (q.floor_z > -INFINITY) {
+      cut = fmaxf(M + q.floor_z * q.T * 1.000001f - 1e-6f * fabsf(M), -FLT_MAX);
+      gather = S <= kGatherCount * mp;  // every kept token has at least min_p of the maximum's mass
+    }
+    if (q.p < 1.f) cut = fmaxf(cut, M - (logf(float(a.V) / ((1.f - q.p) * S)) + 1e-3f) * q.T);
   }
 
   unsigned long long best = 0ull;
   if (gather) {
     h.collect(s, cut, true);
-    cluster_sync(n);
-    uint32_t total = s.n_list;
-    if (rank != 0) {
-      if (tid == 0) s.total = ld_remote(at_rank(&s.n_list, 0));
-      __syncthreads();
-      total = s.total;
-    }
     if (n > 1) {
-      cluster_arrive();  // rank 0's count has been read
-      if (rank != 0 || total > kListCap) cluster_wait();
+      cluster_arrive();
+      if (rank != 0) return;  // its entries are with rank 0
+      cluster_wait();
+    } else {
+      __syncthreads();
     }
-    if (total <= kListCap) {
-      if (rank != 0) return;  // rank 0 reads nobody else's shared memory
-      const uint32_t tau = list_threshold(s, total, q, M, c, S);
-      for (uint32_t i = tid; i < total; i += kThreads) {
-        const unsigned long long e = s.list[i];
-        const uint32_t key = uint32_t(e >> 32), t = best_id(e);
+    const uint32_t total = s.n_list;
+    if (total <= kPairCap) {
+      best = draw_sorted(s, total, q, M, c, S, u);
+    } else {
+      // many ties: from the list, or from the row when it has overflowed
+      const bool fits = total <= kListCap;
+      auto entries = [&](auto f) {
+        if (fits) {
+          for (uint32_t i = tid; i < total; i += kThreads)
+            f(best_id(s.list[i]), fkey_inv(uint32_t(s.list[i] >> 32)));
+        } else {
+          each_of_row(h.r, f);
+        }
+      };
+      const uint32_t tau = threshold_by_levels(
+          s, 1, 0, [&](auto f) { entries([&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S);
+      entries([&](uint32_t t, float x) {
         float score;
-        if (key >= tau && score_of(q, fkey_inv(key) - M, u, t, score)) best = max(best, pack_best(score, t));
-      }
+        if (fkey(x) >= tau && score_of(q, x - M, u[t], score)) best = max(best, pack_best(score, t));
+      });
       __syncthreads();
       best = block_max(best, s.red64);
-      if (n > 1) cluster_wait();  // before this block's count goes away
+    }
+  } else {
+    float tau = cut;
+    if (!q.greedy && (q.k || q.p < 1.f)) {
+      bool settled = false;
+      if constexpr (BF16) {
+        settled = threshold_by_counts<NV>(s, h, q, cut, M, c, S, tau);
+        if (!settled) cluster_sync(n);  // everybody has read the counts: the histograms take their place
+      }
+      if (!settled)
+        tau = fkey_inv(threshold_by_levels(
+            s, n, rank, [&](auto f) { h.each(cut, [&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S));
+    }
+    bool listed = false;
+    if (q.greedy) {
+      h.each(M, [&](uint32_t t, float) { best = max(best, pack_best(0.f, t)); });
+      best = block_max(best, s.red64);
     } else {
-      select = true;
-    }
-  }
-  if (!gather || select) {
-    h.collect(s, cut, false);
-    __syncthreads();
-    uint32_t tau = 0;
-    if (select) {
-      using F = Fmt<BF16>;
-      const uint32_t lo = F::key(cut), hi = F::key(M);
-      uint32_t level = 0;
-      unsigned long long above, kept = static_cast<unsigned long long>(double(S) * 1099511627776.0);
-      uint32_t tk = 0;
-      if (q.k) {
-        tk = select_key(s, n, [&](auto f) { h.each(s, cut, [&](uint32_t, float x) { f(F::key(x), 1ull); }); }, lo, hi,
-                        q.k, level, above);
-        if (q.p < 1.f) {  // the mass of what top-k keeps
-          unsigned long long w = 0;
-          h.each(s, cut, [&](uint32_t, float x) { w += F::key(x) >= tk ? mass_q(x, M, c) : 0ull; });
-          __syncthreads();
-          w = block_sum(w, s.red64);
-          if (tid < n) st_remote(at_rank(&s.sums[rank], tid), w);
-          cluster_sync(n);
-          kept = 0;
-          for (uint32_t i = 0; i < n; ++i) kept += s.sums[i];
+      if (tau > -FLT_MAX) {
+        __syncthreads();  // s.merged has been read
+        h.collect(s, tau, false);
+        __syncthreads();
+        listed = s.n_local <= kListCap;
+      }
+      if (listed) {
+        for (uint32_t i = tid; i < s.n_local; i += kThreads) {
+          const unsigned long long e = s.local[i];
+          float score;
+          if (score_of(q, fkey_inv(uint32_t(e >> 32)) - M, u[best_id(e)], score)) best = max(best, pack_best(score, best_id(e)));
         }
+        best = block_max(best, s.red64);
+      } else {
+        best = draw_screened<BF16, NV>(s, h, q, tau, M, c, u);
       }
-      uint32_t tp = tk;
-      if (q.p < 1.f) {
-        const unsigned long long target = static_cast<unsigned long long>(double(q.p) * double(kept));
-        tp = select_key(s, n, [&](auto f) { h.each(s, cut, [&](uint32_t, float x) { f(F::key(x), mass_q(x, M, c)); }); },
-                        max(lo, tk), hi, target ? target : 1ull, level, above);
-      }
-      tau = BF16 ? tp << 16 : tp;  // a 16-bit key's tokens have fkey >= it shifted
     }
-    h.each(s, cut, [&](uint32_t t, float x) {
-      float score;
-      if (fkey(x) >= tau && score_of(q, x - M, u, t, score)) best = max(best, pack_best(score, t));
-    });
-    __syncthreads();
-    best = block_max(best, s.red64);
     if (tid == 0) st_remote(at_rank(&s.best[rank], 0), best);
-    cluster_sync(n);
+    cluster_sync(n);  // everybody waits: the others may still be reading this block's counts before it
     if (rank != 0) return;
     for (uint32_t i = 0; i < n; ++i) best = max(best, s.best[i]);
   }

@@ -5,9 +5,9 @@
 // finds a bound that ceil(n / N) of its threads' maxima reach; at least n
 // tokens lie at or above the least of these bounds, and little more (a thread
 // rarely holds two of the best).  Those are gathered by rank 0 and put in order
-// by (logit, lower id).  Where ties or small clusters make the gathered list
-// overflow, the n-th largest logit comes from histograms over the cluster, the
-// last ids among its ties from a second selection, and exactly n are gathered.
+// by (logit, lower id).  Where ties make the gathered list overflow, rank 0 reads
+// the row again by itself: the n-th largest logit and the last ids among its
+// ties by radix selection, then exactly n entries.
 #include "logit_row.cuh"
 
 namespace cgk {
@@ -26,7 +26,7 @@ struct TopArgs {
 };
 
 template <bool BF16, int NV>
-__global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) top_kernel(const TopArgs a) {
+__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const TopArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   using F = Fmt<BF16>;
@@ -46,52 +46,40 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) top_kernel(const To
   float M, S;
   merge(s, n, kLog2e, M, S, cut_key);
   uint32_t found = 0;
-  bool waiting = false;
   if (M > -INFINITY) {
-    const float cut = cut_key >= kKeyLowest ? fkey_inv(cut_key) : -FLT_MAX;
-    h.collect(s, cut, true);
-    cluster_sync(n);
+    h.collect(s, cut_key >= kKeyLowest ? fkey_inv(cut_key) : -FLT_MAX, true);
+    if (n > 1) {
+      cluster_arrive();
+      if (rank != 0) return;  // its entries are with rank 0
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
     found = s.n_list;
-    if (rank != 0) {
-      if (tid == 0) s.total = ld_remote(at_rank(&s.n_list, 0));
-      __syncthreads();
-      found = s.total;
-    }
-    waiting = n > 1;
-    if (waiting) {
-      cluster_arrive();  // rank 0's count has been read
-      if (rank != 0 || found > kListCap) {
-        cluster_wait();
-        waiting = false;
-      }
-    }
     if (found > kListCap) {
-      h.collect(s, cut, false);
-      __syncthreads();
       uint32_t level = 0;
       unsigned long long above;
       // the n-th largest logit: a key whose upper set holds n tokens
-      const uint32_t tau = select_key(s, n, [&](auto f) { h.each(s, cut, [&](uint32_t, float x) { f(F::key(x), 1ull); }); },
-                                      F::key(cut), F::key(M), a.n, level, above);
+      const uint32_t tau = select_key(
+          s, 1, [&](auto f) { each_of_row(h.r, [&](uint32_t, float x) { f(F::key(x), 1ull); }); }, F::key(-FLT_MAX),
+          F::key(M), a.n, level, above);
       // of the tokens with that key, the lowest ids (as many as are missing)
-      const uint32_t first = ~(a.V - 1u);
+      unsigned long long skip;
       const uint32_t last = select_key(
-          s, n, [&](auto f) { h.each(s, cut, [&](uint32_t t, float x) { if (F::key(x) == tau) f(~t, 1ull); }); }, first,
-          ~0u, a.n - above, level, above);
-      if (rank == 0 && tid == 0) s.n_list = 0;
-      cluster_sync(n);
-      const uint32_t count = at_rank(&s.n_list, 0), list = at_rank(s.list, 0);
-      h.each(s, cut, [&](uint32_t t, float x) {
+          s, 1, [&](auto f) { each_of_row(h.r, [&](uint32_t t, float x) { if (F::key(x) == tau) f(~t, 1ull); }); },
+          ~(a.V - 1u), ~0u, a.n - above, level, skip);
+      if (tid == 0) s.n_list = 0;
+      __syncthreads();
+      each_of_row(h.r, [&](uint32_t t, float x) {
         const uint32_t key = F::key(x);
         if (key > tau || (key == tau && ~t >= last)) {
-          const uint32_t at = add_remote(count, 1u);
-          if (at < kListCap) st_remote(list + at * 8, pack_best(x, t));
+          const uint32_t at = atomicAdd(&s.n_list, 1u);
+          if (at < kListCap) s.list[at] = pack_best(x, t);
         }
       });
-      cluster_sync(n);
+      __syncthreads();
       found = s.n_list;
     }
-    if (rank != 0) return;  // rank 0 reads nobody else's shared memory from here on
   } else if (rank != 0) {
     return;
   }
@@ -103,22 +91,8 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) top_kernel(const To
     lps[i] = (fkey_inv(uint32_t(e >> 32)) - M) - log_s;
   };
   if (found <= kPairCap) {
-    // an entry's place is the number of entries above it; parts of the block
-    // compare with parts of the list
-    uint32_t C = 32;
-    while (C < found) C <<= 1;
-    const uint32_t i = tid & (C - 1), part = tid / C, parts = kThreads / C;
-    uint32_t* place = reinterpret_cast<uint32_t*>(s.local);
-    if (tid < C) place[tid] = 0;
-    __syncthreads();
-    const unsigned long long e = i < found ? s.list[i] : 0ull;
-    if (i < found) {
-      uint32_t before = 0;
-      for (uint32_t j = part; j < found; j += parts) before += s.list[j] > e;
-      if (before) atomicAdd(place + i, before);
-    }
-    __syncthreads();
-    if (part == 0 && i < found && place[i] < a.n) write(place[i], e);
+    place_entries(s, found);
+    if (tid < found && s.place[tid] < a.n) write(s.place[tid], s.list[tid]);
   } else {
     sort_desc(s.list, found);
     for (uint32_t i = tid; i < min(found, a.n); i += kThreads) write(i, s.list[i]);
@@ -128,7 +102,6 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) top_kernel(const To
     lps[i] = -INFINITY;
   }
   if (a.out_lse && tid == 0) a.out_lse[b] = M > -INFINITY ? M + log_s : -INFINITY;
-  if (waiting) cluster_wait();  // before this block's count goes away
 }
 
 template <bool BF16>

@@ -1,7 +1,7 @@
 // Rows of logits held on chip, the frame of the per-row operators
 // (sample_rows, top_logprobs, distill).
 //
-// A row belongs to a cluster of n <= 8 blocks of 512 threads.  Every thread
+// A row belongs to a cluster of n <= 16 blocks of 256 threads.  Every thread
 // loads NV 16-byte groups of it (8 bf16 or 4 floats each) once and keeps them in
 // registers, so the row is read from memory once whatever the operator does
 // with it; the blocks exchange what they must (maxima, sums, bounds,
@@ -22,12 +22,13 @@
 namespace cgk {
 namespace row {
 
-constexpr uint32_t kThreads = 512;
+constexpr uint32_t kThreads = 256;
 constexpr uint32_t kWarps = kThreads / 32;
-constexpr uint32_t kMaxCluster = 8;
+constexpr uint32_t kMaxCluster = 16;   // more than 8 is not portable, but the one target has it
 constexpr uint32_t kBins = 1024;       // bins of one selection level
 constexpr uint32_t kListCap = 2048;    // entries of a block's list and of the gathered list
-constexpr uint32_t kPairCap = 256;     // lists ranked by comparing all pairs
+constexpr uint32_t kPairCap = kThreads;  // lists ranked by comparing all pairs, an entry a thread
+constexpr uint32_t kCounts = 4096;     // bins of the bf16 key counts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxBf16 = 3.38953138925e38f;  // largest finite bf16
 constexpr uint32_t kKeyInf = 0xFF800000u;      // fkey(+inf); NaN keys lie above
@@ -74,9 +75,17 @@ __device__ __forceinline__ uint32_t add_remote(uint32_t a, uint32_t v) {
   asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
   return old;
 }
-__device__ __forceinline__ uint32_t ld_remote(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+__device__ __forceinline__ uint4 ld_remote4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long ld_remote64(uint32_t a) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void ld_remote2(uint32_t a, unsigned long long& x, unsigned long long& y) {
@@ -104,47 +113,63 @@ struct Common {
   Record rec[kMaxCluster];             // one per block, written by it
   unsigned long long best[kMaxCluster];
   unsigned long long sums[kMaxCluster];
-  unsigned long long red64[kWarps];
+  unsigned long long red64[kWarps], red64b[kWarps];
   unsigned long long base;
   uint32_t red_max[kWarps], red_min[kWarps];
   float red_f[kWarps];
   uint32_t n_list, n_local, bin, total;
 };
-// ... with lists and histograms
+// ... with lists and histograms.  A row is gathered or counted, not both at once.
 struct Shared : Common {
-  __align__(16) unsigned long long list[kListCap];   // gathered entries (rank 0) as pack_best packs them
-  __align__(16) unsigned long long local[kListCap];  // this block's entries at or above the cut
-  __align__(16) unsigned long long hist[2][kBins];   // selection levels, alternating
+  union {
+    __align__(16) unsigned long long list[kListCap];   // gathered entries (rank 0) as pack_best packs them
+    __align__(16) unsigned long long local[kListCap];  // this block's entries that stay
+    __align__(16) uint32_t merged[kCounts];            // key counts of the whole row
+  };
+  union {
+    __align__(16) unsigned long long hist[2][kBins];   // selection levels, alternating
+    __align__(16) uint32_t counts[kCounts];            // this block's key counts
+    struct {
+      __align__(16) unsigned long long sorted[kPairCap]; // gathered entries in order
+      uint32_t place[kPairCap];                          // their places
+    };
+  };
+  unsigned long long odd_mass;  // mass of the tokens in the bin of the smallest magnitudes
 };
 
 // ---- block reductions that cost one barrier each --------------------------------------
 // (the caller keeps a barrier between two uses of the same array)
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  v = warp_reduce(v, SumOp());
+template <typename T, typename Op>
+__device__ __forceinline__ T block_fold(T v, Op op, T* red) {
+  v = warp_reduce(v, op);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  return warp_reduce(red[threadIdx.x & (kWarps - 1)], SumOp()) * 0.5f;  // every value twice in the warp
+  v = red[threadIdx.x & (kWarps - 1)];  // kWarps is a power of two: a butterfly over as many lanes
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
 }
-__device__ __forceinline__ float block_max(float v, float* red) {
-  v = warp_reduce(v, MaxOp());
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T* red) { return block_fold(v, SumOp(), red); }
+template <typename T>
+__device__ __forceinline__ T block_max(T v, T* red) { return block_fold(v, MaxOp(), red); }
+static_assert((kWarps & (kWarps - 1)) == 0 && kWarps <= 32, "the butterfly above");
+
+// Inclusive sums over the block in thread order
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* red) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= uint32_t(o)) v += y;
+  }
+  if (lane == 31) red[warp] = v;
   __syncthreads();
-  return warp_reduce(red[threadIdx.x & (kWarps - 1)], MaxOp());
+  for (uint32_t i = 0; i < warp; ++i) v += red[i];
+  return v;
 }
-__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long* red) {
-  v = warp_reduce(v, SumOp());
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_reduce(red[threadIdx.x & (kWarps - 1)], SumOp()) >> 1;
-}
-__device__ __forceinline__ unsigned long long block_max(unsigned long long v, unsigned long long* red) {
-  v = warp_reduce(v, MaxOp());
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_reduce(red[threadIdx.x & (kWarps - 1)], MaxOp());
-}
-static_assert(kWarps == 16, "the reductions above read 16 warp results twice per warp");
 
 // scale of the exponent of exp((x - m) / T) as a power of two, finite for every T > 0
 __device__ __forceinline__ float exp_scale(float T) { return fminf(__fdiv_rn(kLog2e, T), FLT_MAX); }
@@ -229,6 +254,17 @@ struct Row {
   }
 };
 
+// f(token, logit) for every allowed token of the row, spread over one block,
+// from memory: for rank 0 on its own, where a gathered list has overflowed
+template <bool BF16, typename Fn>
+__device__ __forceinline__ void each_of_row(const Row<BF16>& r, Fn f) {
+#pragma unroll 1
+  for (uint32_t t = threadIdx.x; t < r.V; t += kThreads) {
+    const float x = r.at(t);
+    if (x > -INFINITY) f(t, x);
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ float elem(const uint4& v, uint32_t e) {
   if (BF16) return group_at(v, e);
@@ -304,7 +340,7 @@ struct Held {
 
   __device__ __forceinline__ Held(const Row<BF16>& row) : r(row), n(cluster_size()), rank(cluster_rank()) {}
   // group j of this thread: consecutive threads hold consecutive groups, the
-  // blocks take turns at runs of 512
+  // blocks take turns at runs of kThreads
   __device__ __forceinline__ uint32_t group(uint32_t j) const { return (j * n + rank) * kThreads + threadIdx.x; }
   __device__ __forceinline__ int first_token(uint32_t j) const { return int(group(j) * F::E) - int(r.a); }
 
@@ -381,20 +417,17 @@ struct Held {
     }
     return lo;
   }
-  // f(token, logit) for every element of this block's part that is >= cut,
-  // from memory again (for parts too large for the lists)
+  // f(token, logit) for every element of this block's part that is >= cut (finite)
   template <typename Fn>
-  __device__ __forceinline__ void each_slow(float cut, Fn f) const {
-#pragma unroll 1
-    for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t g = group(j);
-      if (!r.in_row(g)) break;
-      uint4 x = clean_group<BF16>(r.load(g));
-      if (r.mask) x = r.masked(x, r.mask_bits(first_token(j)));
-#pragma unroll 1
-      for (uint32_t e = 0; e < F::E; ++e) {
-        const float y = elem<BF16>(x, e);
-        if (y >= cut) f(uint32_t(first_token(j)) + e, y);
+  __device__ __forceinline__ void each(float cut, Fn f) const {
+    const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      uint32_t hits = ge_bits<BF16>(v[j], cut, cut2);
+      while (hits) {
+        const uint32_t e = __ffs(hits) - 1;
+        hits &= hits - 1;
+        f(uint32_t(first_token(j)) + e, elem<BF16>(v[j], e));
       }
     }
   }
@@ -434,19 +467,6 @@ struct Held {
       }
     }
   }
-  // f(token, logit) for every element >= cut, after collect() into the block's
-  // own list with that cut and a barrier: from the list when it holds them all
-  template <typename Fn>
-  __device__ __forceinline__ void each(const Shared& s, float cut, Fn f) const {
-    if (s.n_local <= kListCap) {
-      for (uint32_t i = threadIdx.x; i < s.n_local; i += kThreads) {
-        const unsigned long long e = s.local[i];
-        f(best_id(e), fkey_inv(uint32_t(e >> 32)));
-      }
-    } else {
-      each_slow(cut, f);
-    }
-  }
 };
 
 // Publishes this block's record to every block of the cluster and waits for all
@@ -482,7 +502,9 @@ __device__ __forceinline__ void merge(const Common& s, uint32_t n, float c, floa
 template <typename Each>
 __device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, uint32_t hi, unsigned long long target,
                                uint32_t& level, unsigned long long& above) {
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr uint32_t kOwn = kBins / kThreads;
+  static_assert(kOwn % 2 == 0, "two bins a load");
+  const uint32_t tid = threadIdx.x;
   above = 0;
   for (;;) {
     const uint32_t range = hi - lo;
@@ -490,37 +512,49 @@ __device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, ui
     unsigned long long* hist = s.hist[level++ & 1u];
     // the level two before, which used this histogram, was read by every block
     // before the cluster met in the level between
-    hist[tid] = 0ull;
-    hist[tid + kThreads] = 0ull;
+    for (uint32_t i = tid; i < kBins; i += kThreads) hist[i] = 0ull;
     if (tid == 0) s.bin = kBins;
     __syncthreads();
     each([&](uint32_t key, unsigned long long w) {
       if (key >= lo && key <= hi) atomicAdd(hist + ((hi - key) >> shift), w);
     });
     cluster_sync(n);
-    // two bins a thread, bins in order
-    unsigned long long h0 = 0, h1 = 0;
+    // kOwn consecutive bins a thread
+    unsigned long long own[kOwn] = {};
     for (uint32_t i = 0; i < n; ++i) {
-      unsigned long long x, y;
-      ld_remote2(at_rank(hist + 2 * tid, i), x, y);
-      h0 += x;
-      h1 += y;
-    }
-    unsigned long long inc = h0 + h1;
+      const uint32_t at = at_rank(hist + kOwn * tid, i);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= uint32_t(o)) inc += y;
+      for (uint32_t q = 0; q < kOwn; q += 2) {
+        unsigned long long x, y;
+        ld_remote2(at + q * 8, x, y);
+        own[q] += x;
+        own[q + 1] += y;
+      }
     }
-    if (lane == 31) s.red64[warp] = inc;
-    __syncthreads();
-    unsigned long long before = above;
-    for (uint32_t i = 0; i < warp; ++i) before += s.red64[i];
-    before += inc - h0 - h1;
-    if (before + h0 + h1 >= target) atomicMin(&s.bin, before + h0 >= target ? 2 * tid : 2 * tid + 1);
+    unsigned long long mine = 0;
+#pragma unroll
+    for (uint32_t q = 0; q < kOwn; ++q) mine += own[q];
+    unsigned long long before = above + block_scan(mine, s.red64) - mine;
+    if (before + mine >= target) {
+      unsigned long long w = before;
+      uint32_t q = 0;
+#pragma unroll
+      for (uint32_t i = 0; i + 1 < kOwn; ++i)
+        if (q == i && w + own[i] < target) {
+          w += own[i];
+          ++q;
+        }
+      atomicMin(&s.bin, kOwn * tid + q);
+    }
     __syncthreads();
     const uint32_t bin = s.bin;
-    if (bin >> 1 == tid) s.base = before + ((bin & 1u) ? h0 : 0ull);
+    if (bin / kOwn == tid) {
+      unsigned long long w = before;
+#pragma unroll
+      for (uint32_t i = 0; i + 1 < kOwn; ++i)
+        if (i < bin % kOwn) w += own[i];
+      s.base = w;
+    }
     __syncthreads();
     if (bin == kBins) return lo;
     above = s.base;
@@ -531,7 +565,25 @@ __device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, ui
     __syncthreads();  // s.bin is set again above
   }
 }
-static_assert(kBins == 2 * kThreads, "two bins a thread");
+
+// Places of list[0 .. c), c <= kPairCap entries all different, in descending
+// order: the number of entries above each.  The block's threads share the pairs
+// out (parts of it compare with parts of the list).  s.place[i] receives the
+// place of entry i; ends with a barrier.
+__device__ __forceinline__ void place_entries(Shared& s, uint32_t c) {
+  uint32_t C = 32;
+  while (C < c) C <<= 1;
+  const uint32_t i = threadIdx.x & (C - 1), part = threadIdx.x / C, parts = kThreads / C;
+  s.place[threadIdx.x] = 0;
+  __syncthreads();
+  if (i < c) {
+    const unsigned long long e = s.list[i];
+    uint32_t before = 0;
+    for (uint32_t j = part; j < c; j += parts) before += s.list[j] > e;
+    if (before) atomicAdd(s.place + i, before);
+  }
+  __syncthreads();
+}
 
 // Descending sort of list[0 .. n) (bitonic network over the next power of two,
 // padded with zeros, which sort last).  list: kListCap words of shared memory.
@@ -558,10 +610,11 @@ __device__ inline void sort_desc(unsigned long long* list, uint32_t n) {
 
 // NV and the cluster size of a launch.  Few rows take the smallest NV (the
 // widest cluster): the row is split over more SMs while all blocks are resident
-// together; many rows take NV = 8, two blocks an SM.
+// together; many rows take NV = 8, four blocks an SM.
 struct Plan {
   uint32_t nv, n;
 };
+constexpr uint32_t kSlots = 4 * 152;  // blocks resident at NV = 8
 inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned) {
   const uint32_t E = bf16 ? 8 : 4;
   const uint32_t groups = (V + (aligned ? 0 : E - 1) + E - 1) / E;
@@ -570,19 +623,20 @@ inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned) {
     const uint32_t n = (groups + kThreads * nv - 1) / (kThreads * nv);
     if (n > kMaxCluster || (best.nv && nv > 8)) continue;
     best = {nv, n};
-    if (n == 1 || uint64_t(B) * n <= 2 * 152) break;
+    if (n == 1 || uint64_t(B) * n <= kSlots) break;
   }
   return best;
 }
 
-// Launches Kernel on clusters of n blocks, `rows` of them.  The dynamic shared
-// memory limit is raised on the first launch on a device.
+// Launches Kernel on clusters of n blocks, `rows` of them.  The kernel's shared
+// memory and cluster size limits are raised on the first launch on a device.
 template <auto Kernel, typename... Args>
 cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, size_t smem, cudaStream_t stream, Args&&... args) {
   static std::atomic<uint64_t> raised{0};
   const uint64_t bit = uint64_t(1) << (device & 63);
-  if (smem > 48 * 1024 && !(raised.load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -625,7 +679,7 @@ inline bool row_args_ok(const cg_ctx* c, const void* logits, int dtype, uint32_t
                         const uint32_t* bitmask) {
   if (!c || (dtype != CG_F32 && dtype != CG_BF16)) return false;
   if (V != ctx_view(c).t.V || ld < V || ld > (uint64_t(1) << 40)) return false;
-  if (B > 0x07FFFFFFu || (B && !logits)) return false;  // the grid: up to 8 blocks a row
+  if (B > 0x07FFFFFFu || (B && !logits)) return false;  // the grid: up to 16 blocks a row
   const uintptr_t size = dtype == CG_BF16 ? 2 : 4;
   return reinterpret_cast<uintptr_t>(logits) % size == 0 && reinterpret_cast<uintptr_t>(bitmask) % 4 == 0;
 }
