@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
   Common& s = reinterpret_cast<DistillShared*>(smem)->s;
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x, K = a.K;
-  if (LOSS && n > 1) cluster_arrive();  // this block's shared memory is ready for the others
+  if (LOSS) begin(s);
   griddep_wait();
   const float T = a.temp, c = exp_scale(T);
   Held<BF16, NV> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b));
@@ -136,12 +136,23 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
 
   float M = 0.f, S = 1.f;  // p = exp2((x - M) c) / S
   if (LOSS) {
-    if (n > 1) cluster_wait();
-    uint32_t low, none = 0;
-    h.find_max(s, low);
-    const float sum = h.sum_exps(s, c);
-    exchange(s, n, rank, h.m, sum, 0u);
-    merge(s, n, c, M, S, none);
+    h.find_max();
+    h.sum_exps(c);
+    ready_others();
+    h.publish(s, c, 0u);
+    if (tid < 32) {
+      const bool ok = wait_sent(&s.bar_rec);
+      float m, sum;
+      merge(s, n, c, m, sum);
+      if (tid == 0) {
+        s.M = m;
+        s.S = sum;
+        if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
+      }
+    }
+    __syncthreads();
+    M = s.M;
+    S = s.S;
     if (rank == 0) {
       float part = 0.f;
       const float log_ts = logf(ts), log_s = logf(S);
@@ -160,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
     if (!a.grad) return;
   } else {
     M = a.lse_in[b] * T;  // p = exp((x - lse T) / T)
-    h.clean_own();
+    h.find_max();  // for its replacements
     if (a.grad == a.logits) cluster_sync(n);
   }
 

@@ -9,16 +9,18 @@
 //
 // The row is held on chip by a cluster (logit_row.cuh).  A lower bound of the
 // threshold is known after one exchange between the blocks:
-//   top-k  the k-th largest logit is at least the least of the blocks' bounds c,
-//          each block having ceil(k / n) threads whose maximum is >= its c;
+//   top-k  the k-th largest logit is at least the k-th largest of the maxima of
+//          groups of lanes that the warps publish;
 //   top-p  tokens more than D = log(V / ((1 - p) S)) nats below the maximum have
 //          together less than (1 - p) S of the mass S, so the threshold lies
 //          above them;
 //   min-p  is the threshold itself.
-// Only tokens at or above the bound matter from there on.  Where they are few by
-// the settings (top-k, min-p) rank 0 gathers and settles them; where they may be
-// many (top-p, a large k) the blocks count them by key, add up the counts, find
-// the threshold and each draw from their own part.
+// Only tokens at or above the bound matter from there on.  Where they are few rank
+// 0 gathers and settles them alone.  D supposes all V tokens just below the bound,
+// so a top-p row first gathers down to kGuess nats less, with the gathered mass
+// added up: it is settled when that reaches the target, which every block sees.
+// Otherwise, and for a large k, the blocks count the tokens at or above the bound
+// by key, add up the counts, find the threshold and each draw from their own part.
 #include "logit_row.cuh"
 
 namespace cgk {
@@ -45,11 +47,13 @@ struct DrawArgs {
   uint32_t* status;
 };
 
-// top-k rows up to this k, and min-p rows whose kept tokens cannot be more than
-// this, are gathered: the list then overflows only by ties
-constexpr uint32_t kGatherK = 1024;
+// min-p rows whose kept tokens cannot be more than this are gathered: the list
+// then overflows only by ties
 constexpr float kGatherCount = 1536.f;
+constexpr float kGuess = 3.f;
 constexpr float kMassOne = 1099511627776.f;  // mass_q of the maximum
+
+enum Mode : uint32_t { kNothing, kGather, kGuessFirst, kSpread };
 
 struct RowSettings {
   float T, Ts, p, floor_z;  // Ts: the softmax's temperature (1 for greedy rows)
@@ -189,8 +193,29 @@ __device__ uint32_t find_bin(Shared& s, uint32_t n, unsigned long long target, W
   return n;
 }
 
-// The threshold (a value) under top-k and top-p of a bf16 row by counting; false
-// when it falls among the several values of the odd bin.
+// The threshold (a value) under top-k and top-p from the counts of bf16 values;
+// false when it falls among the several values of the odd bin.
+__device__ bool threshold_in_counts(Shared& s, const KeyBins& bins, const uint32_t* counts, unsigned long long odd,
+                                    const RowSettings& q, float M, float scale, float S, float& tau) {
+  auto mass = [&](uint32_t i) {
+    return bins.is_odd(i) ? odd : static_cast<unsigned long long>(counts[i]) * mass_q(bins.value(i), M, scale);
+  };
+  uint32_t last = bins.n - 1;
+  unsigned long long before, kept = mass_total(S);
+  if (q.k) {
+    last = min(last, find_bin(s, bins.n, q.k, [&](uint32_t i) { return static_cast<unsigned long long>(counts[i]); }, before));
+    if (q.p < 1.f) {
+      unsigned long long w = 0;
+      for (uint32_t i = threadIdx.x; i <= last; i += kThreads) w += mass(i);
+      kept = block_sum(w, s.red64b);
+    }
+  }
+  if (q.p < 1.f) last = min(last, find_bin(s, last + 1u, mass_target(q.p, kept), mass, before));
+  tau = bins.value(last);
+  return !bins.is_odd(last);
+}
+
+// ... of a row whose blocks count their parts
 template <int NV>
 __device__ bool threshold_by_counts(Shared& s, const Held<true, NV>& h, const RowSettings& q, float cut, float M,
                                     float scale, float S, float& tau) {
@@ -232,57 +257,72 @@ __device__ bool threshold_by_counts(Shared& s, const Held<true, NV>& h, const Ro
   if (!bins.one0)
     for (uint32_t r = 0; r < h.n; ++r) odd += ld_remote64(at_rank(&s.odd_mass, r));
   __syncthreads();
-  auto mass = [&](uint32_t i) {
-    return bins.is_odd(i) ? odd : static_cast<unsigned long long>(s.merged[i]) * mass_q(bins.value(i), M, scale);
-  };
-  uint32_t last = bins.n - 1;
-  unsigned long long before, kept = mass_total(S);
-  if (q.k) {
-    last = min(last, find_bin(s, bins.n, q.k, [&](uint32_t i) { return static_cast<unsigned long long>(s.merged[i]); }, before));
-    if (q.p < 1.f) {
-      unsigned long long w = 0;
-      for (uint32_t i = tid; i <= last; i += kThreads) w += mass(i);
-      kept = block_sum(w, s.red64b);
-    }
+  return threshold_in_counts(s, bins, s.merged, odd, q, M, scale, S, tau);
+}
+
+// The same from the gathered list[0 .. c)
+__device__ bool threshold_in_list(Shared& s, uint32_t c, const RowSettings& q, float cut, float M, float scale, float S,
+                                  float& tau) {
+  const uint32_t tid = threadIdx.x;
+  KeyBins bins(M, cut);
+  bins.negative0 = M < 0.f;
+  for (uint32_t i = tid; i < bins.n; i += kThreads) s.counts[i] = 0u;
+  if (tid == 0) s.odd_mass = 0ull;
+  __syncthreads();
+  for (uint32_t i = tid; i < c; i += kThreads) {
+    const float x = fkey_inv(uint32_t(s.list[i] >> 32));
+    const uint32_t at = bins.bin(__float_as_uint(x) >> 16);
+    atomicAdd(s.counts + at, 1u);
+    if (bins.is_odd(at)) atomicAdd(&s.odd_mass, mass_q(x, M, scale));
   }
-  if (q.p < 1.f) last = min(last, find_bin(s, last + 1u, mass_target(q.p, kept), mass, before));
-  tau = bins.value(last);
-  return !bins.is_odd(last);
+  __syncthreads();
+  return threshold_in_counts(s, bins, s.counts, s.odd_mass, q, M, scale, S, tau);
 }
 
 // ---- drawing ------------------------------------------------------------------------
 
-// Rank 0: draws from the gathered list[0 .. c), c <= kPairCap, an entry a thread.
-// In order, with running masses, the cuts are positions; the random numbers are
-// on their way meanwhile.
-__device__ unsigned long long draw_sorted(Shared& s, uint32_t c, const RowSettings& q, float M, float scale, float S,
-                                          const float* u) {
-  const uint32_t tid = threadIdx.x;
-  const unsigned long long e = tid < c ? s.list[tid] : 0ull;
-  const float ut = tid < c ? u[best_id(e)] : 0.5f;
-  uint32_t tau = 0;
-  if (q.k || q.p < 1.f) {
-    place_entries(s, c);
-    if (tid < c) s.sorted[s.place[tid]] = e;
-    __syncthreads();
-    const uint32_t key = tid < c ? uint32_t(s.sorted[tid] >> 32) : 0u;
-    if (q.k && q.k <= c) tau = uint32_t(s.sorted[q.k - 1] >> 32);
-    if (q.p < 1.f) {
-      const unsigned long long upto = block_scan(tid < c ? mass_q(fkey_inv(key), M, scale) : 0ull, s.red64);
-      unsigned long long kept = mass_total(S);
-      if (q.k) kept = block_max(key >= tau && tid < c ? upto : 0ull, s.red64b);
-      // the best place whose running mass reaches the target
-      uint32_t at = upto >= mass_target(q.p, kept) ? key : 0u;
-      at = block_max(at, s.red_max);
-      tau = max(tau, at);
+// The best of a list and, carried along, its logit
+struct Drawn {
+  unsigned long long best = 0ull;
+  float x = 0.f;
+  __device__ __forceinline__ void offer(float score, uint32_t t, float logit) {
+    const unsigned long long e = pack_best(score, t);
+    if (e > best) {
+      best = e;
+      x = logit;
     }
   }
-  unsigned long long best = 0ull;
+};
+
+// Rank 0: draws from the gathered list[0 .. c), c <= kPairCap, an entry a thread.
+// With the number of entries above each (its place) and the masses added up by
+// place, an entry stays when fewer than k are above it and less than the target's
+// mass; the random numbers are on their way meanwhile.
+__device__ Drawn draw_pairs(Shared& s, uint32_t c, const RowSettings& q, float M, float scale, float S, const float* u) {
+  const uint32_t tid = threadIdx.x;
+  const unsigned long long e = tid < c ? s.list[tid] : 0ull;
+  const float x = fkey_inv(uint32_t(e >> 32)), ut = tid < c ? u[best_id(e)] : 0.5f;
+  bool stays = tid < c;
+  if (q.k || q.p < 1.f) {
+    s.masses[tid] = 0ull;
+    place_entries<false>(s, c);
+    const uint32_t place = s.place[tid];
+    if (q.k) stays = stays && place < q.k;
+    if (q.p < 1.f) {
+      const unsigned long long w = stays ? mass_q(x, M, scale) : 0ull;
+      if (w) atomicAdd(s.masses + place, w);
+      __syncthreads();
+      const unsigned long long own = s.masses[tid], upto = block_scan(own, s.red64);
+      s.masses[tid] = upto - own;  // mass above place tid
+      if (tid == kThreads - 1) s.base = upto;
+      __syncthreads();
+      stays = stays && s.masses[place] < mass_target(q.p, q.k ? s.base : mass_total(S));
+    }
+  }
+  Drawn d;
   float score;
-  if (tid < c && uint32_t(e >> 32) >= tau && score_of(q, fkey_inv(uint32_t(e >> 32)) - M, ut, score))
-    best = pack_best(score, best_id(e));
-  __syncthreads();
-  return block_max(best, s.red64);
+  if (stays && score_of(q, x - M, ut, score)) d.offer(score, best_id(e), x);
+  return d;
 }
 
 // Draws from this block's part, tokens >= tau, when they are too many to list:
@@ -349,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
   Shared& s = *reinterpret_cast<Shared*>(smem);
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
-  if (tid == 0) s.n_list = s.n_local = 0;
-  if (n > 1) cluster_arrive();  // this block's shared memory is ready for the others
+  begin(s);
   griddep_wait();
   Held<BF16, NV> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b));
   h.load();
@@ -361,63 +400,101 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
   q.p = fmaxf(p, 0.f);
   q.greedy = q.T == 0.f;
   q.Ts = q.greedy ? 1.f : q.T;
-  const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || p != p || mp != mp || (!q.greedy && !a.u);
   if (q.k >= a.V || q.greedy) q.k = 0;
-  q.floor_z = logf(fminf(fmaxf(mp, 0.f), 1.f));  // -inf for min_p = 0
   const float c = exp_scale(q.Ts);
-
-  uint32_t low, cut_key = 0;
-  h.find_max(s, low);
-  const float sum = bad ? 0.f : h.sum_exps(s, c);
-  if (q.k) cut_key = h.share_cut((q.k + n - 1) / n, low);
-  if (n > 1) cluster_wait();
-  exchange(s, n, rank, h.m, sum, cut_key);
-  float M, S;
-  merge(s, n, c, M, S, cut_key);
+  const uint32_t per_warp = q.k ? bounds_per_warp(q.k, n) : 0u;
+  h.find_max();
+  h.sum_exps(c);
+  ready_others();
+  h.publish(s, c, per_warp);
+  if (tid < 32) {
+    const bool ok = wait_sent(&s.bar_rec);
+    float M, S;
+    merge(s, n, c, M, S);
+    // a lower bound of the threshold, and how to settle it.  Without top-k the
+    // mass that top-p refers to is known, so min-p bounds what matters as well.
+    const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || p != p || mp != mp || (!q.greedy && !a.u);
+    const float floor_z = logf(fminf(fmaxf(mp, 0.f), 1.f));  // -inf for min_p = 0
+    float cut = -FLT_MAX, guess = 0.f;
+    Mode mode = kSpread;
+    if (bad || !ok || M == -INFINITY) {
+      mode = kNothing;
+    } else if (q.greedy) {
+      cut = M;
+    } else if (q.k) {
+      const uint32_t key = per_warp ? bound_key(s, n * kWarps * per_warp, q.k) : 0u;
+      if (key >= kKeyLowest) cut = fkey_inv(key);
+      if (per_warp) mode = kGather;
+    } else {
+      // a little below M + T log(min_p), for the roundings
+      if (floor_z > -INFINITY) {
+        cut = fmaxf(M + floor_z * q.T * 1.000001f - 1e-6f * fabsf(M), -FLT_MAX);
+        if (S <= kGatherCount * mp) mode = kGather;  // every kept token has at least min_p of the maximum's mass
+      }
+      if (q.p < 1.f) {
+        const float D = logf(float(a.V) / ((1.f - q.p) * S)) + 1e-3f;
+        cut = fmaxf(cut, M - D * q.T);
+        if (mode != kGather && q.p * S < float(kListCap)) {
+          guess = fmaxf(cut, M - fmaxf(D - kGuess, 0.f) * q.T);
+          mode = kGuessFirst;
+        }
+      }
+    }
+    if (tid == 0) {
+      s.M = M;
+      s.S = S;
+      s.cut = cut;
+      s.guess = guess;
+      s.floor_z = floor_z;
+      s.mode = mode;
+      s.late = !ok;
+      if (rank == 0 && mode == kNothing) {
+        if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
+        else if (bad) record_error(a.status, CG_DEV_BAD_PARAM);
+        a.out_tok[b] = CG_NO_TOKEN;
+        if (a.out_lp) a.out_lp[b] = -INFINITY;
+      }
+    }
+  }
+  __syncthreads();
+  const float M = s.M, S = s.S, cut = s.cut;
+  uint32_t mode = s.mode;
+  if (mode == kNothing) return;
+  q.floor_z = s.floor_z;
   const float* u = a.u + size_t(b) * a.ld_u;
 
-  if (bad || M == -INFINITY) {  // the same in every block
-    if (rank == 0 && tid == 0) {
-      if (bad) record_error(a.status, CG_DEV_BAD_PARAM);
+  Drawn d;
+  float list_cut = cut;
+  uint32_t total = 0;
+  if (mode == kGather) {
+    h.gather(s, cut, false, [](float) { return 0ull; });
+    if (rank != 0) return;  // its entries are with rank 0
+    unsigned long long none;
+    if (!h.tallied(s, total, none)) mode = kNothing;
+  } else if (mode == kGuessFirst) {
+    list_cut = s.guess;
+    h.gather(s, list_cut, true, [&](float x) { return mass_q(x, M, c); });
+    unsigned long long mass;
+    const bool ok = h.tallied(s, total, mass);
+    mode = !ok ? kNothing : total <= kListCap && mass >= mass_target(q.p, mass_total(S)) ? kGather : kSpread;
+    if (rank != 0 && mode != kSpread) return;
+  }
+  // the entries are on their way to rank 0, which settles them or, after a wrong
+  // guess, uses the list's memory again
+  if (s.mode != kSpread && rank == 0 && (mode == kNothing || !h.listed(s, total))) {
+    if (tid == 0) {
+      record_error(a.status, CG_DEV_TIMEOUT);
       a.out_tok[b] = CG_NO_TOKEN;
       if (a.out_lp) a.out_lp[b] = -INFINITY;
     }
-    return;  // nobody reads this block's shared memory after the exchange
+    return;
   }
-
-  // a lower bound of the threshold, and how to settle it.  Without top-k the
-  // mass that top-p refers to is known, so min-p bounds what matters as well.
-  float cut = -FLT_MAX;
-  bool gather = false;
-  if (q.greedy) {
-    cut = M;
-  } else if (q.k) {
-    if (cut_key >= kKeyLowest) cut = fkey_inv(cut_key);
-    gather = q.k <= kGatherK;
-  } else {
-    // a little below M + T log(min_p), for the roundings
-    if (q.floor_z > -INFINITY) {
-      cut = fmaxf(M + q.floor_z * q.T * 1.000001f - 1e-6f * fabsf(M), -FLT_MAX);
-      gather = S <= kGatherCount * mp;  // every kept token has at least min_p of the maximum's mass
-    }
-    if (q.p < 1.f) cut = fmaxf(cut, M - (logf(float(a.V) / ((1.f - q.p) * S)) + 1e-3f) * q.T);
-  }
-
-  unsigned long long best = 0ull;
+  const bool gather = mode == kGather;
   if (gather) {
-    h.collect(s, cut, true);
-    if (n > 1) {
-      cluster_arrive();
-      if (rank != 0) return;  // its entries are with rank 0
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
-    const uint32_t total = s.n_list;
     if (total <= kPairCap) {
-      best = draw_sorted(s, total, q, M, c, S, u);
+      d = draw_pairs(s, total, q, M, c, S, u);
     } else {
-      // many ties: from the list, or from the row when it has overflowed
+      // from the list, or from the row when ties have made it overflow
       const bool fits = total <= kListCap;
       auto entries = [&](auto f) {
         if (fits) {
@@ -427,16 +504,30 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
           each_of_row(h.r, f);
         }
       };
-      const uint32_t tau = threshold_by_levels(
-          s, 1, 0, [&](auto f) { entries([&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S);
+      float tau = list_cut;
+      if (q.k || q.p < 1.f) {
+        if (!(BF16 && fits && threshold_in_list(s, total, q, list_cut, M, c, S, tau))) {
+          __syncthreads();
+          tau = fkey_inv(threshold_by_levels(
+              s, 1, 0, [&](auto f) { entries([&](uint32_t, float x) { f(fkey(x)); }); }, q, list_cut, M, c, S));
+        }
+      }
       entries([&](uint32_t t, float x) {
         float score;
-        if (fkey(x) >= tau && score_of(q, x - M, u[t], score)) best = max(best, pack_best(score, t));
+        if (x >= tau && score_of(q, x - M, u[t], score)) d.offer(score, t, x);
       });
-      __syncthreads();
-      best = block_max(best, s.red64);
     }
-  } else {
+    __syncthreads();
+    const unsigned long long best = block_max(d.best, s.red64);
+    if (d.best == best && (best != 0ull || tid == 0)) {
+      a.out_tok[b] = best_id(best);
+      if (a.out_lp) a.out_lp[b] = __fdiv_rn(d.x - M, q.Ts) - logf(S);
+    }
+    return;
+  }
+
+  unsigned long long best = 0ull;
+  {
     float tau = cut;
     if (!q.greedy && (q.k || q.p < 1.f)) {
       bool settled = false;
@@ -450,12 +541,13 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
     }
     bool listed = false;
     if (q.greedy) {
-      h.each(M, [&](uint32_t t, float) { best = max(best, pack_best(0.f, t)); });
+      if (h.tm == M) h.each(M, [&](uint32_t t, float) { best = max(best, pack_best(0.f, t)); });
       best = block_max(best, s.red64);
     } else {
       if (tau > -FLT_MAX) {
         __syncthreads();  // s.merged has been read
-        h.collect(s, tau, false);
+        unsigned long long none;
+        h.collect(s, tau, false, [](float) { return 0ull; }, none);
         __syncthreads();
         listed = s.n_local <= kListCap;
       }
@@ -470,15 +562,24 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
         best = draw_screened<BF16, NV>(s, h, q, tau, M, c, u);
       }
     }
-    if (tid == 0) st_remote(at_rank(&s.best[rank], 0), best);
-    cluster_sync(n);  // everybody waits: the others may still be reading this block's counts before it
+    if (tid == 0) send(at_rank(&s.best[rank], 0), best, at_rank(&s.bar_best, 0));
+    if (!q.greedy && (q.k || q.p < 1.f)) {  // the others may still be reading this block's counts
+      cluster_arrive_relaxed();
+      cluster_wait();
+    }
     if (rank != 0) return;
-    for (uint32_t i = 0; i < n; ++i) best = max(best, s.best[i]);
+    if (tid == 0) mbar_expect_tx(&s.bar_best, n * 8u);
+    if (!wait_sent(&s.bar_best)) {
+      if (tid == 0) record_error(a.status, CG_DEV_TIMEOUT);
+      best = 0ull;
+    } else {
+      for (uint32_t i = 0; i < n; ++i) best = max(best, s.best[i]);
+    }
   }
   if (tid == 0) {
-    const uint32_t tok = best_id(best);
+    const uint32_t tok = best ? best_id(best) : CG_NO_TOKEN;
     a.out_tok[b] = tok;
-    if (a.out_lp) a.out_lp[b] = __fdiv_rn(h.r.value(tok) - M, q.Ts) - logf(S);
+    if (a.out_lp) a.out_lp[b] = best ? __fdiv_rn(h.r.value(tok) - M, q.Ts) - logf(S) : -INFINITY;
   }
 }
 

@@ -1,10 +1,9 @@
 // The n best allowed tokens of each row with their log-probabilities
 // (cg_top_logprobs).
 //
-// The row is held on chip by a cluster (logit_row.cuh).  With N blocks, each
-// finds a bound that ceil(n / N) of its threads' maxima reach; at least n
-// tokens lie at or above the least of these bounds, and little more (a thread
-// rarely holds two of the best).  Those are gathered by rank 0 and put in order
+// The row is held on chip by a cluster (logit_row.cuh).  The warps publish maxima
+// of groups of their lanes; at least n tokens lie at or above the n-th largest of
+// them, and little more.  Those are gathered by rank 0 and put in order
 // by (logit, lower id).  Where ties make the gathered list overflow, rank 0 reads
 // the row again by itself: the n-th largest logit and the last ids among its
 // ties by radix selection, then exactly n entries.
@@ -23,6 +22,7 @@ struct TopArgs {
   uint32_t* out_ids;
   float* out_lp;
   float* out_lse;
+  uint32_t* status;
 };
 
 template <bool BF16, int NV>
@@ -32,30 +32,37 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const To
   using F = Fmt<BF16>;
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
-  if (tid == 0) s.n_list = s.n_local = 0;
-  if (n > 1) cluster_arrive();  // this block's shared memory is ready for the others
+  begin(s);
   griddep_wait();
   Held<BF16, NV> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b));
   h.load();
-  uint32_t low;
-  h.find_max(s, low);
-  const float sum = h.sum_exps(s, kLog2e);
-  uint32_t cut_key = h.share_cut((a.n + n - 1) / n, low);
-  if (n > 1) cluster_wait();
-  exchange(s, n, rank, h.m, sum, cut_key);
-  float M, S;
-  merge(s, n, kLog2e, M, S, cut_key);
-  uint32_t found = 0;
-  if (M > -INFINITY) {
-    h.collect(s, cut_key >= kKeyLowest ? fkey_inv(cut_key) : -FLT_MAX, true);
-    if (n > 1) {
-      cluster_arrive();
-      if (rank != 0) return;  // its entries are with rank 0
-      cluster_wait();
-    } else {
-      __syncthreads();
+  h.find_max();
+  h.sum_exps(kLog2e);
+  const uint32_t per_warp = bounds_per_warp(a.n, n);
+  ready_others();
+  h.publish(s, kLog2e, per_warp);
+  if (tid < 32) {
+    const bool ok = wait_sent(&s.bar_rec);
+    float m, sum;
+    merge(s, n, kLog2e, m, sum);
+    const uint32_t key = per_warp ? bound_key(s, n * kWarps * per_warp, a.n) : 0u;
+    if (tid == 0) {
+      s.M = m;
+      s.S = sum;
+      s.cut = key >= kKeyLowest ? fkey_inv(key) : -FLT_MAX;
+      s.late = !ok;
     }
-    found = s.n_list;
+  }
+  __syncthreads();
+  const float M = s.M, S = s.S;
+  uint32_t found = 0;
+  bool late = s.late != 0;
+  if (M > -INFINITY && !late) {
+    h.gather(s, s.cut, false, [](float) { return 0ull; });
+    if (rank != 0) return;  // its entries are with rank 0
+    unsigned long long none;
+    late = !h.tallied(s, found, none) || !h.listed(s, found);
+    if (late) found = 0;
     if (found > kListCap) {
       uint32_t level = 0;
       unsigned long long above;
@@ -83,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const To
   } else if (rank != 0) {
     return;
   }
+  if (late && tid == 0) record_error(a.status, CG_DEV_TIMEOUT);
   const float log_s = logf(S);
   uint32_t* ids = a.out_ids + size_t(b) * a.n;
   float* lps = a.out_lp + size_t(b) * a.n;
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const To
     lps[i] = (fkey_inv(uint32_t(e >> 32)) - M) - log_s;
   };
   if (found <= kPairCap) {
-    place_entries(s, found);
+    place_entries<true>(s, found);
     if (tid < found && s.place[tid] < a.n) write(s.place[tid], s.list[tid]);
   } else {
     sort_desc(s.list, found);
@@ -127,7 +135,7 @@ extern "C" int cg_top_logprobs(cg_ctx* c, const void* d_logits, int dtype, uint3
   DeviceGuard dg(ctx_device(c), "cg_top_logprobs");
   if (!dg.ok) return CG_E_CUDA;
   const CtxView v = ctx_view(c);
-  const TopArgs a{d_logits, ld, d_bitmask, V, v.t.W, n, d_out_ids, d_out_logprobs, d_out_lse};
+  const TopArgs a{d_logits, ld, d_bitmask, V, v.t.W, n, d_out_ids, d_out_logprobs, d_out_lse, v.t.status};
   const int dev = ctx_device(c);
   const cudaError_t e =
       dtype == CG_BF16 ? launch_top<true>(dev, B, a, v.stream) : launch_top<false>(dev, B, a, v.stream);

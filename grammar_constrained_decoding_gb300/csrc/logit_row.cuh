@@ -4,8 +4,11 @@
 // A row belongs to a cluster of n <= 16 blocks of 256 threads.  Every thread
 // loads NV 16-byte groups of it (8 bf16 or 4 floats each) once and keeps them in
 // registers, so the row is read from memory once whatever the operator does
-// with it; the blocks exchange what they must (maxima, sums, bounds,
-// histograms) through one another's shared memory.  Groups lie on the 16-byte
+// with it; the blocks exchange what they must (maxima, sums, bounds, entries,
+// counts) through one another's shared memory.  Short messages go as asynchronous
+// stores that complete on the receiver's mbarrier: the sender neither fences nor
+// waits (a cluster barrier with release semantics made every thread wait for its
+// stores, the longest stall of an earlier form).  Groups lie on the 16-byte
 // grid of the memory, not of the row: a row that starts off the grid has a
 // first group with some elements before the row, loaded one by one, and every
 // other load stays 16 bytes wide.
@@ -56,6 +59,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // address of the same shared variable in the block of rank r
 __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t r) {
@@ -63,12 +67,39 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t r) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(r));
   return a;
 }
-__device__ __forceinline__ void st_remote(uint32_t a, uint4 v) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
 __device__ __forceinline__ void st_remote(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+// asynchronous stores that complete 4, 8 or 16 bytes on a barrier of the block
+// that a lies in
+__device__ __forceinline__ void send(uint32_t a, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(a), "r"(v),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void send(uint32_t a, unsigned long long v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(a), "l"(v),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void send(uint32_t a, uint4 v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+               : "memory");
+}
+// bounded wait for what others have sent
+__device__ __forceinline__ bool wait_sent(uint64_t* bar, uint32_t parity = 0) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
 }
 __device__ __forceinline__ uint32_t add_remote(uint32_t a, uint32_t v) {
   uint32_t old;
@@ -101,23 +132,36 @@ __device__ __forceinline__ void cluster_sync(uint32_t n) {
   }
 }
 
-// What a block tells the others about its part of the row.
-struct __align__(16) Record {
-  float m, s;      // its maximum, its sum of exp2((x - m) c)
-  uint32_t cut;    // key: at least its share of the tokens lie at or above
-  uint32_t pad;
+constexpr uint32_t kMaxRecords = kMaxCluster * kWarps;  // warps of a cluster
+constexpr uint32_t kMaxBounds = 1024;                    // group maxima a cluster exchanges
+
+// What a warp tells all blocks about its part of the row: its maximum and its
+// sum of exp2((x - m) c).
+struct __align__(8) Record {
+  float m, s;
+};
+// ... about the entries it has listed
+struct __align__(16) Tally {
+  unsigned long long mass;
+  uint32_t count, pad;
 };
 
 // Reductions and exchange
 struct Common {
-  Record rec[kMaxCluster];             // one per block, written by it
+  uint64_t bar_rec, bar_tally, bar_list, bar_best;  // one phase each
+  float M, S, cut, guess, floor_z;     // what the merging warp found
+  uint32_t mode;
+  uint32_t late;                       // a bounded wait ran out
+  Record rec[kMaxRecords];
+  uint32_t bound[kMaxBounds];          // keys of group maxima
+  Tally tally[kMaxRecords];
   unsigned long long best[kMaxCluster];
   unsigned long long sums[kMaxCluster];
   unsigned long long red64[kWarps], red64b[kWarps];
   unsigned long long base;
-  uint32_t red_max[kWarps], red_min[kWarps];
+  uint32_t red_max[kWarps];
   float red_f[kWarps];
-  uint32_t n_list, n_local, bin, total;
+  uint32_t n_list, n_local, bin;
 };
 // ... with lists and histograms.  A row is gathered or counted, not both at once.
 struct Shared : Common {
@@ -130,8 +174,9 @@ struct Shared : Common {
     __align__(16) unsigned long long hist[2][kBins];   // selection levels, alternating
     __align__(16) uint32_t counts[kCounts];            // this block's key counts
     struct {
-      __align__(16) unsigned long long sorted[kPairCap]; // gathered entries in order
-      uint32_t place[kPairCap];                          // their places
+      __align__(16) uint32_t keys[kPairCap];             // of the gathered entries
+      uint32_t place[kPairCap];                          // entries above each
+      unsigned long long masses[kPairCap];               // by place
     };
   };
   unsigned long long odd_mass;  // mass of the tokens in the bin of the smallest magnitudes
@@ -170,6 +215,22 @@ __device__ __forceinline__ T block_scan(T v, T* red) {
   for (uint32_t i = 0; i < warp; ++i) v += red[i];
   return v;
 }
+
+// The block's barriers and counters, before anything is sent to it.  With
+// ready_others() the blocks of a cluster know that all of them have got here.
+__device__ __forceinline__ void begin(Common& s) {
+  if (threadIdx.x == 0) {
+    mbar_init(&s.bar_rec, 1);
+    mbar_init(&s.bar_tally, 1);
+    mbar_init(&s.bar_list, 1);
+    mbar_init(&s.bar_best, 1);
+    s.n_list = s.n_local = s.late = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
+  cluster_arrive_relaxed();
+}
+__device__ __forceinline__ void ready_others() { cluster_wait(); }
 
 // scale of the exponent of exp((x - m) / T) as a power of two, finite for every T > 0
 __device__ __forceinline__ float exp_scale(float T) { return fminf(__fdiv_rn(kLog2e, T), FLT_MAX); }
@@ -335,8 +396,8 @@ struct Held {
   Row<BF16> r;
   uint32_t n, rank;   // cluster size, this block
   uint4 v[NV];
-  uint32_t tkey;      // fkey of this thread's maximum
-  float m;            // block maximum
+  float tm;           // this thread's maximum
+  float ts;           // its sum of exp2((x - tm) c)
 
   __device__ __forceinline__ Held(const Row<BF16>& row) : r(row), n(cluster_size()), rank(cluster_rank()) {}
   // group j of this thread: consecutive threads hold consecutive groups, the
@@ -361,61 +422,48 @@ struct Held {
     for (int j = 1; j < NV; ++j) t = max_nan(t, group_max_nan<BF16>(v[j]));
     return t;
   }
-  // block maximum (NaN and +inf replaced first if there are any); lo receives
-  // the least thread maximum's key
-  __device__ __forceinline__ void find_max(Common& s, uint32_t& lo) {
-    for (int pass = 0;; ++pass) {
-      tkey = fkey(thread_max());
-      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, tkey), low = __reduce_min_sync(0xFFFFFFFFu, tkey);
-      if ((threadIdx.x & 31) == 0) {
-        s.red_max[threadIdx.x >> 5] = hi;
-        s.red_min[threadIdx.x >> 5] = low;
-      }
-      __syncthreads();
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, s.red_max[threadIdx.x & (kWarps - 1)]);
-      lo = __reduce_min_sync(0xFFFFFFFFu, s.red_min[threadIdx.x & (kWarps - 1)]);
-      m = fkey_inv(top);
-      if (top < kKeyInf || pass) return;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) v[j] = clean_group<BF16>(v[j]);
-      __syncthreads();
-    }
-  }
-  // the same replacement without the block
-  __device__ __forceinline__ void clean_own() {
-    if (fkey(thread_max()) < kKeyInf) return;
+  // this thread's maximum, after NaN and +inf have been replaced
+  __device__ __forceinline__ void find_max() {
+    tm = thread_max();
+    if (fkey(tm) < kKeyInf) return;
 #pragma unroll
     for (int j = 0; j < NV; ++j) v[j] = clean_group<BF16>(v[j]);
+    tm = thread_max();
   }
-  // block sum of exp2((x - m) c)
-  __device__ __forceinline__ float sum_exps(Common& s, float c) const {
-    float t = 0.f;
-    if (m > -INFINITY) {
-      const float2 nm = make_float2(-m, -m), c2 = make_float2(c, c);
-      float2 acc[4] = {};
+  // its sum of exp2((x - tm) c)
+  __device__ __forceinline__ void sum_exps(float c) {
+    ts = 0.f;
+    if (!(tm > -INFINITY)) return;
+    const float2 nm = make_float2(-tm, -tm), c2 = make_float2(c, c);
+    float2 acc[4] = {};
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (uint32_t q = 0; q < F::E / 2; ++q)
-          acc[q] = __fadd2_rn(acc[q], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[j], q), nm), c2)));
+      for (uint32_t q = 0; q < F::E / 2; ++q)
+        acc[q] = __fadd2_rn(acc[q], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[j], q), nm), c2)));
 #pragma unroll
-      for (uint32_t q = 0; q < 4; ++q) t += acc[q].x + acc[q].y;
-    }
-    return block_sum(t, s.red_f);
+    for (uint32_t q = 0; q < 4; ++q) ts += acc[q].x + acc[q].y;
   }
-  // A key such that at least `share` threads of the block hold a token at or
-  // above it (0 when fewer threads hold any): bisection over the thread maxima.
-  __device__ __forceinline__ uint32_t share_cut(uint32_t share, uint32_t lo) const {
-    if (share > kThreads) return 0u;
-    uint32_t hi = fkey(m);
-    if (__syncthreads_count(tkey >= hi) >= int(share)) return hi;
-#pragma unroll 1
-    for (int i = 0; i < 16 && hi - lo > 0x2000u; ++i) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      if (__syncthreads_count(tkey >= mid) >= int(share)) lo = mid;
-      else hi = mid;
-    }
-    return lo;
+  // Tells every block of the cluster this warp's maximum and sum, and, for a
+  // bound on the k-th largest logit, the maxima of `per_warp` groups of its
+  // lanes (a power of two, 0 for none), completing on bar_rec.  After
+  // ready_others().
+  __device__ __forceinline__ void publish(Common& s, float c, uint32_t per_warp) const {
+    const uint32_t lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
+    if (threadIdx.x == 0) mbar_expect_tx(&s.bar_rec, n * kWarps * (8u + 4u * per_warp));
+    const float m = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, fkey(tm)));
+    const float sum = warp_reduce(tm > -INFINITY ? ts * ex2((tm - m) * c) : 0.f, SumOp());
+    if (lane < n)
+      send(at_rank(&s.rec[w], lane),
+           (static_cast<unsigned long long>(__float_as_uint(sum)) << 32) | __float_as_uint(m),
+           at_rank(&s.bar_rec, lane));
+    if (per_warp == 0) return;
+    uint32_t key = fkey(tm);
+    for (uint32_t o = 16; o >= per_warp; o >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
+    // every lane holds the maximum of the lanes equal to it modulo per_warp
+    for (uint32_t i = lane; i < per_warp * n; i += 32)
+      send(at_rank(&s.bound[w * per_warp + (i & (per_warp - 1))], i / per_warp), key,
+           at_rank(&s.bar_rec, i / per_warp));
   }
   // f(token, logit) for every element of this block's part that is >= cut (finite)
   template <typename Fn>
@@ -432,17 +480,20 @@ struct Held {
     }
   }
   // Appends (logit, token) of every element >= cut to a list of kListCap
-  // entries: this block's own (to_rank0 false) or rank 0's gathered one.  The
-  // count goes on past the capacity, the entries do not.  Order is arbitrary.
-  __device__ __forceinline__ void collect(Shared& s, float cut, bool to_rank0) const {
+  // entries: this block's own (to_rank0 false; a block barrier completes it) or
+  // rank 0's gathered one (completing on its bar_list).  The count goes on past
+  // the capacity, the entries do not.  Order is arbitrary.  weigh(x) is added up
+  // over the warp's entries into mass; returns their count.
+  template <typename Weigh>
+  __device__ __forceinline__ uint32_t collect(Shared& s, float cut, bool to_rank0, Weigh weigh,
+                                              unsigned long long& mass) const {
+    mass = 0;
+    if (!__any_sync(0xFFFFFFFFu, tm >= cut)) return 0u;  // most warps, when little is wanted
     const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u, lane = threadIdx.x & 31;
     uint32_t hits[(NV + 3) / 4] = {};
     uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const uint32_t h = ge_bits<BF16>(v[j], cut, cut2);
-      hits[j / 4] |= h << (8 * (j % 4));
-    }
+    for (int j = 0; j < NV; ++j) hits[j / 4] |= ge_bits<BF16>(v[j], cut, cut2) << (8 * (j % 4));
 #pragma unroll
     for (int i = 0; i < (NV + 3) / 4; ++i) mine += __popc(hits[i]);
     uint32_t inc = mine;
@@ -452,43 +503,105 @@ struct Held {
       if (lane >= uint32_t(o)) inc += y;
     }
     uint32_t at = 0;
-    if (lane == 31 && inc)
+    if (lane == 31)
       at = to_rank0 ? add_remote(at_rank(&s.n_list, 0), inc) : atomicAdd(&s.n_local, inc);
     at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - mine;
-    const uint32_t list = at_rank(to_rank0 ? s.list : s.local, to_rank0 ? 0u : rank);
+    const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       uint32_t h = (hits[j / 4] >> (8 * (j % 4))) & 0xFFu;
       while (h) {
         const uint32_t e = __ffs(h) - 1;
         h &= h - 1;
-        if (at < kListCap) st_remote(list + at * 8, pack_best(elem<BF16>(v[j], e), uint32_t(first_token(j)) + e));
+        const float x = elem<BF16>(v[j], e);
+        const unsigned long long entry = pack_best(x, uint32_t(first_token(j)) + e);
+        if (at < kListCap) {
+          if (to_rank0) send(list + at * 8, entry, bar);
+          else s.local[at] = entry;
+        }
+        mass += weigh(x);
         ++at;
       }
     }
+    mass = warp_reduce(mass, SumOp());
+    return __shfl_sync(0xFFFFFFFFu, inc, 31);
+  }
+  // collect() to rank 0 followed by this warp's count and mass, to rank 0 or to
+  // every block (all), completing on bar_tally
+  template <typename Weigh>
+  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, Weigh weigh) const {
+    unsigned long long mass;
+    const uint32_t found = collect(s, cut, true, weigh, mass), lane = threadIdx.x & 31;
+    if (lane < (all ? n : 1u))
+      send(at_rank(&s.tally[rank * kWarps + (threadIdx.x >> 5)], lane),
+           make_uint4(uint32_t(mass), uint32_t(mass >> 32), found, 0u), at_rank(&s.bar_tally, lane));
+  }
+  // The gathered count and mass, to every thread of a block that tallies go to;
+  // false when the wait ran out.  The barrier's expectation is set here: early
+  // tallies wait in its transaction count.
+  __device__ __forceinline__ bool tallied(Shared& s, uint32_t& count, unsigned long long& mass) const {
+    if (threadIdx.x == 0) mbar_expect_tx(&s.bar_tally, n * kWarps * uint32_t(sizeof(Tally)));
+    const bool ok = wait_sent(&s.bar_tally);
+    mass = 0;
+    count = 0;
+    for (uint32_t i = threadIdx.x & 31; i < n * kWarps; i += 32) {
+      mass += s.tally[i].mass;
+      count += s.tally[i].count;
+    }
+    mass = warp_reduce(mass, SumOp());
+    count = warp_reduce(count, SumOp());
+    return ok;
+  }
+  // Rank 0, after tallied(): the list's entries are there
+  __device__ __forceinline__ bool listed(Shared& s, uint32_t count) const {
+    if (threadIdx.x == 0) mbar_expect_tx(&s.bar_list, min(count, kListCap) * 8u);
+    return wait_sent(&s.bar_list);
   }
 };
 
-// Publishes this block's record to every block of the cluster and waits for all
-// of theirs.  The blocks must have met once before (their shared memory exists).
-__device__ __forceinline__ void exchange(Common& s, uint32_t n, uint32_t rank, float m, float sum, uint32_t cut) {
-  if (threadIdx.x < n) {
-    const uint4 rec = make_uint4(__float_as_uint(m), __float_as_uint(sum), cut, 0u);
-    st_remote(at_rank(&s.rec[rank], threadIdx.x), rec);
-  }
-  cluster_sync(n);
+// The row's maximum and sum of exp2((x - M) c) from the warps' records, the same
+// in every warp of the cluster.  For one warp of a block, after its wait.
+__device__ __forceinline__ void merge(const Common& s, uint32_t n, float c, float& M, float& S) {
+  const uint32_t lane = threadIdx.x & 31, count = n * kWarps;
+  uint32_t top = 0;
+  for (uint32_t i = lane; i < count; i += 32) top = max(top, fkey(s.rec[i].m));
+  M = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, top));
+  float t = 0.f;
+  for (uint32_t i = lane; i < count; i += 32)
+    if (s.rec[i].m > -INFINITY) t += s.rec[i].s * ex2((s.rec[i].m - M) * c);
+  S = warp_reduce(t, SumOp());
 }
-// The row's maximum, sum of exp2((x - M) c) and the least of the cuts
-__device__ __forceinline__ void merge(const Common& s, uint32_t n, float c, float& M, float& S, uint32_t& cut) {
-  M = -INFINITY;
-  cut = 0xFFFFFFFFu;
-  for (uint32_t i = 0; i < n; ++i) {
-    M = fmaxf(M, s.rec[i].m);
-    cut = min(cut, s.rec[i].cut);
+
+// Groups of lanes per warp whose maxima bound the k-th largest logit: somewhat
+// more groups than k over the cluster; 0 when k is too large for that.  More
+// groups make the bound tighter (with P groups of random logits about
+// -P log(1 - k / P) tokens lie at or above it) and the exchange longer.
+__device__ __forceinline__ uint32_t bounds_per_warp(uint32_t k, uint32_t n) {
+  const uint32_t warps = n * kWarps;
+  for (uint32_t g = 1; g <= 32u && warps * g <= kMaxBounds; g <<= 1)
+    if (4 * k <= 3 * warps * g) return g;
+  return 0;
+}
+// A key that at least k of the published group maxima reach, by bisection (at
+// least k tokens then lie at or above it).  For one warp.
+__device__ __forceinline__ uint32_t bound_key(const Common& s, uint32_t count, uint32_t k) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  for (uint32_t i = lane; i < count; i += 32) {
+    lo = min(lo, s.bound[i]);
+    hi = max(hi, s.bound[i]);
   }
-  S = 0.f;
-  for (uint32_t i = 0; i < n; ++i)
-    if (s.rec[i].m > -INFINITY) S += s.rec[i].s * ex2((s.rec[i].m - M) * c);
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi) + 1u;  // fewer than k reach hi, all reach lo
+#pragma unroll 1
+  while (hi - lo > 0x4000u) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    uint32_t reach = 0;
+    for (uint32_t i = lane; i < count; i += 32) reach += s.bound[i] >= mid;
+    if (__reduce_add_sync(0xFFFFFFFFu, reach) >= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 // Largest key k in [lo, hi] whose upper set {key >= k}, over the whole row,
@@ -566,21 +679,31 @@ __device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, ui
   }
 }
 
-// Places of list[0 .. c), c <= kPairCap entries all different, in descending
-// order: the number of entries above each.  The block's threads share the pairs
-// out (parts of it compare with parts of the list).  s.place[i] receives the
-// place of entry i; ends with a barrier.
+// s.place[i] = the number of entries of list[0 .. c), c <= kPairCap, above entry i:
+// by key alone, or by key and id.  The block's threads share the pairs out (parts
+// of it compare with parts of the list).  Ends with a barrier.
+template <bool IDS>
 __device__ __forceinline__ void place_entries(Shared& s, uint32_t c) {
   uint32_t C = 32;
   while (C < c) C <<= 1;
-  const uint32_t i = threadIdx.x & (C - 1), part = threadIdx.x / C, parts = kThreads / C;
-  s.place[threadIdx.x] = 0;
+  const uint32_t tid = threadIdx.x, i = tid & (C - 1), part = tid / C, parts = kThreads / C;
+  if (!IDS) s.keys[tid] = tid < c ? uint32_t(s.list[tid] >> 32) : 0u;  // zeros are above nothing
+  s.place[tid] = 0;
   __syncthreads();
   if (i < c) {
-    const unsigned long long e = s.list[i];
-    uint32_t before = 0;
-    for (uint32_t j = part; j < c; j += parts) before += s.list[j] > e;
-    if (before) atomicAdd(s.place + i, before);
+    uint32_t above = 0;
+    if (IDS) {
+      const unsigned long long e = s.list[i];
+      for (uint32_t j = part; j < c; j += parts) above += s.list[j] > e;
+    } else {
+      const uint32_t key = s.keys[i];
+#pragma unroll 4
+      for (uint32_t j = 4 * part; j < c; j += 4 * parts) {
+        const uint4 k = *reinterpret_cast<const uint4*>(s.keys + j);
+        above += (k.x > key) + (k.y > key) + (k.z > key) + (k.w > key);
+      }
+    }
+    if (above) atomicAdd(s.place + i, above);
   }
   __syncthreads();
 }
