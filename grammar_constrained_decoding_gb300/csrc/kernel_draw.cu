@@ -19,8 +19,13 @@
 // 0 gathers and settles them alone.  D supposes all V tokens just below the bound,
 // so a top-p row first gathers down to kGuess nats less, with the gathered mass
 // added up: it is settled when that reaches the target, which every block sees.
-// Otherwise, and for a large k, the blocks count the tokens at or above the bound
-// by key, add up the counts, find the threshold and each draw from their own part.
+//
+// A top-p row with many tokens is drawn without finding its threshold: the best
+// scored token w of those at or above the cut is the answer exactly when the mass
+// strictly above x_w is less than the target (w then belongs to the kept set, and
+// nothing in it scores better).  If it is not, nothing at or below x_w is kept,
+// and the best of the rest is tried.  The first try succeeds with probability
+// top_p; after kTries the threshold is found by radix selection.
 #include "logit_row.cuh"
 
 namespace cgk {
@@ -51,9 +56,12 @@ struct DrawArgs {
 // then overflows only by ties
 constexpr float kGatherCount = 1536.f;
 constexpr float kGuess = 3.f;
+constexpr float kFallOff = 0.35f;
+constexpr float kFlat = 3.f;
+constexpr uint32_t kTries = 16;
 constexpr float kMassOne = 1099511627776.f;  // mass_q of the maximum
 
-enum Mode : uint32_t { kNothing, kGather, kGuessFirst, kSpread };
+enum Mode : uint32_t { kNothing, kGather, kGuessFirst, kSample, kSpread };
 
 struct RowSettings {
   float T, Ts, p, floor_z;  // Ts: the softmax's temperature (1 for greedy rows)
@@ -63,10 +71,12 @@ struct RowSettings {
 
 __device__ __forceinline__ float clamp_u(float u) { return fminf(fmaxf(u, kULo), kUHi); }
 // score of a kept token; false when min-p drops it
+__device__ __forceinline__ float exact_score(float d, float T, float u) {
+  return __fdiv_rn(d, T) - logf(-logf(clamp_u(u)));
+}
 __device__ __forceinline__ bool score_of(const RowSettings& q, float d, float u, float& score) {
-  const float z = __fdiv_rn(d, q.T);
-  score = z - logf(-logf(clamp_u(u)));
-  return z >= q.floor_z;
+  score = exact_score(d, q.T, u);
+  return q.floor_z == -INFINITY || __fdiv_rn(d, q.T) >= q.floor_z;
 }
 __device__ __forceinline__ unsigned long long mass_target(float p, unsigned long long kept) {
   const unsigned long long t = static_cast<unsigned long long>(double(p) * double(kept));
@@ -102,181 +112,6 @@ __device__ uint32_t threshold_by_levels(Shared& s, uint32_t n, uint32_t rank, Ke
   }
   return select_key(s, n, [&](auto f) { keys([&](uint32_t key) { f(key, mass_q(fkey_inv(key), M, scale)); }); }, tau, top,
                     mass_target(q.p, kept), level, above);
-}
-
-// ---- counting bf16 keys -----------------------------------------------------------
-// Tokens of one bf16 value have one mass, so counts per value give both the
-// k-th largest and every upper set's mass.  Bins follow the values from M down to
-// the cut: a signed magnitude index, magnitudes up to H0 sharing bin 0 (their
-// tokens' mass is added up apart, should there be several values).  H0 is 0, or
-// M's or the cut's magnitude when both have one sign, or, where the interval
-// reaches over zero, the least that leaves kCounts bins: 2^-14 or so of the
-// largest magnitude.
-struct KeyBins {
-  uint32_t H0;
-  int top;       // signed index of M
-  uint32_t n;    // bins
-  bool one0;     // bin 0 holds a single value
-
-  __device__ __forceinline__ int index(uint32_t h) const {
-    const int q = int(max(h & 0x7FFFu, H0) - H0);
-    return (h & 0x8000u) ? -q : q;
-  }
-  __device__ __forceinline__ KeyBins(float M, float cut) {
-    uint32_t hm = __float_as_uint(M) >> 16, hc = bf16_pair_up(cut) & 0xFFFFu;
-    hm = hm == 0x8000u ? 0u : hm;
-    hc = hc == 0x8000u ? 0u : hc;
-    const uint32_t a = hm & 0x7FFFu, b = hc & 0x7FFFu, big = max(a, b), most = kCounts - 2;
-    const uint32_t low = big > most ? big - most : 0u;
-    if ((hm ^ hc) & 0x8000u) {
-      H0 = max(low, a + b > most ? (a + b - most + 1) / 2 : 0u);
-      one0 = H0 == 0;
-    } else {
-      H0 = max(low, min(a, b));
-      one0 = H0 == min(a, b);
-    }
-    top = index(hm);
-    n = uint32_t(top - index(hc)) + 1u;
-  }
-  __device__ __forceinline__ uint32_t bin(uint32_t h) const { return min(uint32_t(top - index(h)), n - 1u); }
-  __device__ __forceinline__ bool is_odd(uint32_t i) const { return !one0 && int(i) == top; }
-  // the value of bin i (of the odd bin: zero)
-  __device__ __forceinline__ float value(uint32_t i) const {
-    const int q = top - int(i);
-    if (q == 0 && !one0) return 0.f;
-    const uint32_t h = H0 + uint32_t(q < 0 ? -q : q);
-    // bin 0 with a single value other than zero is M or the cut, of the sign of both
-    return bf16_bits_to_float(q < 0 || (q == 0 && negative0) ? h | 0x8000u : h);
-  }
-  bool negative0 = false;
-};
-
-// First bin at which the running sum of weight(i) reaches target, from bin 0 to
-// n - 1; n when it never does.  before: the sum above it.
-template <typename Weight>
-__device__ uint32_t find_bin(Shared& s, uint32_t n, unsigned long long target, Weight weight,
-                             unsigned long long& before) {
-  const uint32_t tid = threadIdx.x;
-  unsigned long long base = 0;
-  for (uint32_t from = 0; from < n; from += 4 * kThreads) {
-    __syncthreads();
-    if (tid == 0) s.bin = n;
-    unsigned long long w[4], mine = 0;
-#pragma unroll
-    for (uint32_t q = 0; q < 4; ++q) {
-      const uint32_t i = from + 4 * tid + q;
-      w[q] = i < n ? weight(i) : 0ull;
-      mine += w[q];
-    }
-    const unsigned long long upto = base + block_scan(mine, s.red64);
-    if (tid == kThreads - 1) s.base = upto;
-    if (upto >= target && upto - mine < target) {
-      unsigned long long b = upto - mine;
-      uint32_t i = 0;
-#pragma unroll
-      for (uint32_t q = 0; q < 3; ++q)
-        if (i == q && b + w[q] < target) {
-          b += w[q];
-          ++i;
-        }
-      s.bin = from + 4 * tid + i;
-      s.sums[0] = b;
-    }
-    __syncthreads();
-    if (s.bin < n) {
-      before = s.sums[0];
-      return s.bin;
-    }
-    base = s.base;
-  }
-  before = base;
-  return n;
-}
-
-// The threshold (a value) under top-k and top-p from the counts of bf16 values;
-// false when it falls among the several values of the odd bin.
-__device__ bool threshold_in_counts(Shared& s, const KeyBins& bins, const uint32_t* counts, unsigned long long odd,
-                                    const RowSettings& q, float M, float scale, float S, float& tau) {
-  auto mass = [&](uint32_t i) {
-    return bins.is_odd(i) ? odd : static_cast<unsigned long long>(counts[i]) * mass_q(bins.value(i), M, scale);
-  };
-  uint32_t last = bins.n - 1;
-  unsigned long long before, kept = mass_total(S);
-  if (q.k) {
-    last = min(last, find_bin(s, bins.n, q.k, [&](uint32_t i) { return static_cast<unsigned long long>(counts[i]); }, before));
-    if (q.p < 1.f) {
-      unsigned long long w = 0;
-      for (uint32_t i = threadIdx.x; i <= last; i += kThreads) w += mass(i);
-      kept = block_sum(w, s.red64b);
-    }
-  }
-  if (q.p < 1.f) last = min(last, find_bin(s, last + 1u, mass_target(q.p, kept), mass, before));
-  tau = bins.value(last);
-  return !bins.is_odd(last);
-}
-
-// ... of a row whose blocks count their parts
-template <int NV>
-__device__ bool threshold_by_counts(Shared& s, const Held<true, NV>& h, const RowSettings& q, float cut, float M,
-                                    float scale, float S, float& tau) {
-  const uint32_t tid = threadIdx.x;
-  KeyBins bins(M, cut);
-  bins.negative0 = M < 0.f;
-  const uint32_t words = (bins.n + 3u) & ~3u;
-  for (uint32_t i = tid; i < words; i += kThreads) s.counts[i] = 0u;
-  if (tid == 0) s.odd_mass = 0ull;
-  __syncthreads();
-  const uint32_t cut2 = bf16_pair_up(cut);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const uint32_t hits = group_ge_bits(h.v[j], cut2);
-    if (!hits) continue;
-    const uint32_t w[4] = {h.v[j].x, h.v[j].y, h.v[j].z, h.v[j].w};
-#pragma unroll
-    for (uint32_t e = 0; e < 8; ++e)
-      if ((hits >> e) & 1u) {
-        const uint32_t i = bins.bin((e & 1u) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
-        atomicAdd(s.counts + i, 1u);
-        if (bins.is_odd(i)) atomicAdd(&s.odd_mass, mass_q(group_at(h.v[j], e), M, scale));
-      }
-  }
-  cluster_sync(h.n);
-  // the whole row's counts, four bins a load
-  for (uint32_t i = 4 * tid; i < words; i += 4 * kThreads) {
-    uint4 t = make_uint4(0u, 0u, 0u, 0u);
-    for (uint32_t r = 0; r < h.n; ++r) {
-      const uint4 x = ld_remote4(at_rank(s.counts + i, r));
-      t.x += x.x;
-      t.y += x.y;
-      t.z += x.z;
-      t.w += x.w;
-    }
-    *reinterpret_cast<uint4*>(s.merged + i) = t;
-  }
-  unsigned long long odd = 0;
-  if (!bins.one0)
-    for (uint32_t r = 0; r < h.n; ++r) odd += ld_remote64(at_rank(&s.odd_mass, r));
-  __syncthreads();
-  return threshold_in_counts(s, bins, s.merged, odd, q, M, scale, S, tau);
-}
-
-// The same from the gathered list[0 .. c)
-__device__ bool threshold_in_list(Shared& s, uint32_t c, const RowSettings& q, float cut, float M, float scale, float S,
-                                  float& tau) {
-  const uint32_t tid = threadIdx.x;
-  KeyBins bins(M, cut);
-  bins.negative0 = M < 0.f;
-  for (uint32_t i = tid; i < bins.n; i += kThreads) s.counts[i] = 0u;
-  if (tid == 0) s.odd_mass = 0ull;
-  __syncthreads();
-  for (uint32_t i = tid; i < c; i += kThreads) {
-    const float x = fkey_inv(uint32_t(s.list[i] >> 32));
-    const uint32_t at = bins.bin(__float_as_uint(x) >> 16);
-    atomicAdd(s.counts + at, 1u);
-    if (bins.is_odd(at)) atomicAdd(&s.odd_mass, mass_q(x, M, scale));
-  }
-  __syncthreads();
-  return threshold_in_counts(s, bins, s.counts, s.odd_mass, q, M, scale, S, tau);
 }
 
 // ---- drawing ------------------------------------------------------------------------
@@ -325,62 +160,215 @@ __device__ Drawn draw_pairs(Shared& s, uint32_t c, const RowSettings& q, float M
   return d;
 }
 
-// Draws from this block's part, tokens >= tau, when they are too many to list:
-// from -log u >= 1 - u, a score is at most z - log(1 - u), which costs one
-// logarithm in the multi-function unit.  Every thread finds its two best bounds
-// and scores the first exactly; a thread whose second bound reaches the block's
-// best exact score scores its whole part.
+// The random numbers of a group's tokens: 16-byte loads where the group is inside
+// the row and the numbers lie on the 16-byte grid with the logits
 template <bool BF16, int NV>
-__device__ unsigned long long draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSettings& q, float tau, float M,
-                                            float c, const float* u) {
-  constexpr uint32_t E = Fmt<BF16>::E;
-  const bool wide = ((reinterpret_cast<uintptr_t>(u) / 4 - h.r.a) & 3u) == 0;
-  float first = -INFINITY, second = -INFINITY, fx = 0.f;
-  uint32_t ft = 0;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
+struct Numbers {
+  static constexpr uint32_t E = Fmt<BF16>::E;
+  const float* u;
+  bool wide;
+  __device__ __forceinline__ Numbers(const Held<BF16, NV>& h, const float* u_) : u(u_) {
+    wide = ((reinterpret_cast<uintptr_t>(u) / 4 - h.r.a) & 3u) == 0;
+  }
+  __device__ __forceinline__ void load(const Held<BF16, NV>& h, uint32_t j, bool wanted, float* out) const {
     const int t0 = h.first_token(j);
-    if (t0 >= int(h.r.V)) continue;
-    float un[E];
-    if (wide && t0 >= 0 && uint32_t(t0) + E <= h.r.V) {
+    if (wanted && wide && t0 >= 0 && uint32_t(t0) + E <= h.r.V) {
 #pragma unroll
       for (uint32_t i = 0; i < E / 4; ++i) {
-        const uint4 w = ld_group(u + t0 + 4 * i);
-        un[4 * i] = __uint_as_float(w.x);
-        un[4 * i + 1] = __uint_as_float(w.y);
-        un[4 * i + 2] = __uint_as_float(w.z);
-        un[4 * i + 3] = __uint_as_float(w.w);
+        const float4 w = __ldcs(reinterpret_cast<const float4*>(u + t0) + i);
+        out[4 * i] = w.x;
+        out[4 * i + 1] = w.y;
+        out[4 * i + 2] = w.z;
+        out[4 * i + 3] = w.w;
       }
-    } else {
+    } else if (wanted) {
 #pragma unroll
-      for (uint32_t e = 0; e < E; ++e) un[e] = t0 + int(e) >= 0 && t0 + int(e) < int(h.r.V) ? u[t0 + int(e)] : 0.5f;
+      for (uint32_t e = 0; e < E; ++e) out[e] = t0 + int(e) >= 0 && t0 + int(e) < int(h.r.V) ? u[t0 + int(e)] : 0.f;
     }
+  }
+};
+
+// Draws from this block's part, tokens >= low, however many.  From -log u >= 1 - u,
+// a score is at most z - log(1 - u), which costs one logarithm in the
+// multi-function unit.  Every thread finds the group with its best bound and the
+// next group's bound; the best token of that group is scored exactly, and a thread
+// with another bound that reaches the block's best score goes over its part again.
+template <bool BF16, int NV>
+__device__ Drawn draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSettings& q, float low, float M, float c,
+                               const float* u) {
+  constexpr uint32_t E = Fmt<BF16>::E;
+  const Numbers<BF16, NV> numbers(h, u);
+  const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c);
+  // upper bounds of a group's scores, in bits
+  auto bounds = [&](const uint4& v, const float* un, float* ub) {
+#pragma unroll
+    for (uint32_t p = 0; p < E / 2; ++p) {
+      const float2 x = pair<BF16>(v, p), z = __fmul2_rn(__fadd2_rn(x, nm), c2);
+      float l0, l1;
+      asm("lg2.approx.f32 %0, %1;" : "=f"(l0) : "f"(__saturatef(1.f - un[2 * p])));
+      asm("lg2.approx.f32 %0, %1;" : "=f"(l1) : "f"(__saturatef(1.f - un[2 * p + 1])));
+      ub[2 * p] = x.x >= low ? z.x - l0 : -INFINITY;
+      ub[2 * p + 1] = x.y >= low ? z.y - l1 : -INFINITY;
+    }
+  };
+  float first = -INFINITY, second = -INFINITY;
+  uint32_t at = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (!(group_max_nan<BF16>(h.v[j]) >= low)) continue;
+    float un[E], ub[E];
+    numbers.load(h, j, true, un);
+    bounds(h.v[j], un, ub);
+    float top = ub[0];
+#pragma unroll
+    for (uint32_t e = 1; e < E; ++e) top = fmaxf(top, ub[e]);
+    second = fmaxf(second, fminf(first, top));
+    if (top > first) {
+      first = top;
+      at = j;
+    }
+  }
+  Drawn d;
+  float score;
+  if (first > -INFINITY) {
+    const uint4 v = h.again(at);
+    float un[E], ub[E], top = -INFINITY;
+    numbers.load(h, at, true, un);
+    bounds(v, un, ub);
+    uint32_t best = 0;
+    float ut = 0.f;
 #pragma unroll
     for (uint32_t e = 0; e < E; ++e) {
-      const float x = elem<BF16>(h.v[j], e);
-      float lg;
-      asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(1.f - clamp_u(un[e])));
-      const float ub = x >= tau ? (x - M) * c - lg : -INFINITY;
-      second = fmaxf(second, fminf(first, ub));
-      if (ub > first) {
-        first = ub;
-        fx = x;
-        ft = uint32_t(t0) + e;
+      second = fmaxf(second, fminf(top, ub[e]));
+      if (ub[e] > top) {
+        top = ub[e];
+        best = e;
+        ut = un[e];
+      }
+    }
+    const float x = elem<BF16>(v, best);
+    if (score_of(q, x - M, ut, score)) d.offer(score, uint32_t(h.first_token(at)) + best, x);
+  }
+  const unsigned long long best = block_max(d.best, s.red64);
+  // 1e-3 nats cover the roundings of the bounds
+  if (second > -INFINITY && (best == 0ull || second >= (fkey_inv(uint32_t(best >> 32)) - 1e-3f) * kLog2e)) {
+#pragma unroll 1
+    for (uint32_t j = 0; j < NV; ++j) {
+      if (!h.r.in_row(h.group(j))) break;
+      const uint4 v = h.again(j);
+#pragma unroll 1
+      for (uint32_t e = 0; e < E; ++e) {
+        const float x = elem<BF16>(v, e);
+        const uint32_t t = uint32_t(h.first_token(j)) + e;
+        if (x >= low && score_of(q, x - M, u[t], score)) d.offer(score, t, x);
       }
     }
   }
-  unsigned long long best = 0ull;
-  float score;
-  if (first > -INFINITY && score_of(q, fx - M, u[ft], score)) best = pack_best(score, ft);
-  best = block_max(best, s.red64);
-  // 1e-3 covers the roundings of the bound (bounds in bits, scores in nats)
-  if (second > -INFINITY && (best == 0ull || second * 0.6931472f + 1e-3f >= fkey_inv(uint32_t(best >> 32)))) {
-    h.each(tau, [&](uint32_t t, float x) {
-      float sc;
-      if (score_of(q, x - M, u[t], sc)) best = max(best, pack_best(sc, t));
-    });
+  return d;
+}
+
+// A top-p row over the whole cluster, by trial as described above.  Returns the
+// drawn token to every block; near: a cut that is likely low enough, low: one that
+// certainly is.
+template <bool BF16, int NV>
+__device__ Drawn draw_by_trial(Shared& s, const Held<BF16, NV>& h, const RowSettings& q, float near, float low, float M,
+                               float c, float S, const float* u, uint32_t* status) {
+  const uint32_t tid = threadIdx.x, lane = tid & 31, n = h.n;
+  const float target = fmaxf(q.p * S, 1e-30f);
+  float cut = fmaxf(near, low);
+  Drawn d;
+  bool listed = false;
+#pragma unroll 1
+  for (uint32_t round = 0;; ++round) {
+    const bool settled = round == kTries;  // the random numbers rank the tokens almost against their logits
+    if (settled) {
+      cut = fkey_inv(threshold_by_levels(
+          s, n, h.rank, [&](auto f) { h.each(low, [&](uint32_t, float y) { f(fkey(y)); }); }, q, low, M, c, S));
+    }
+    __syncthreads();
+    if (!listed) {  // few enough: from a list, else from the registers
+      listed = h.compact(s, cut);
+    }
+    const uint32_t key = fkey(cut);
+    if (listed) {
+      d = Drawn();
+      for (uint32_t i = tid; i < s.n_local; i += kThreads) {
+        const unsigned long long e = s.list[i];
+        const uint32_t k = uint32_t(e >> 32), t = best_id(e);
+        float score;
+        if (k >= key && score_of(q, fkey_inv(k) - M, u[t], score)) d.offer(score, t, fkey_inv(k));
+      }
+    } else {
+      d = draw_screened<BF16, NV>(s, h, q, cut, M, c, u);
+    }
+    const unsigned long long best = block_max(d.best, s.red64b);
+    if (best ? d.best == best : tid == 0) {  // one thread
+      for (uint32_t r = 0; r < n; ++r) {
+        send(at_rank(&s.best[h.rank], r), best, at_rank(&s.bar_best, r));
+        send(at_rank(&s.best_x[h.rank], r), __float_as_uint(d.x), at_rank(&s.bar_best, r));
+      }
+    }
+    if (tid == 0) mbar_expect_tx(&s.bar_best, n * 12u);
+    bool ok = wait_sent(&s.bar_best, round & 1u);
+    d = Drawn();
+    for (uint32_t r = 0; r < n; ++r)
+      if (s.best[r] > d.best) {
+        d.best = s.best[r];
+        d.x = s.best_x[r];
+      }
+    if (ok && (settled || !d.best)) return d;
+    // the mass above the drawn token and, for the first cut, at or above it
+    const bool check = round == 0 && cut > low;
+    float2 w = make_float2(0.f, 0.f);
+    if (listed) {  // in integers: the list's order is arbitrary
+      const uint32_t x = fkey(d.x);
+      unsigned long long above = 0, from = 0;
+      for (uint32_t i = tid; i < s.n_local; i += kThreads) {
+        const uint32_t k = uint32_t(s.list[i] >> 32);
+        const unsigned long long m = mass_q(fkey_inv(k), M, c);
+        above += k > x ? m : 0ull;
+        from += k >= key ? m : 0ull;
+      }
+      __syncthreads();
+      w.x = float(block_sum(above, s.red64)) * (1.f / kMassOne) * (1.f / kWarps);
+      w.y = float(block_sum(from, s.red64b)) * (1.f / kMassOne) * (1.f / kWarps);
+    } else if (__any_sync(0xFFFFFFFFu, h.tm >= cut)) {
+      w = h.masses_from(M, c, d.x, check ? cut : INFINITY);
+      w.x = warp_reduce(w.x, SumOp());
+      w.y = warp_reduce(w.y, SumOp());
+    }
+    if (lane < n)
+      send(at_rank(&s.mass[h.rank * kWarps + (tid >> 5)], lane),
+           (static_cast<unsigned long long>(__float_as_uint(w.y)) << 32) | __float_as_uint(w.x),
+           at_rank(&s.bar_mass, lane));
+    if (tid == 0) mbar_expect_tx(&s.bar_mass, n * kWarps * 8u);
+    ok = wait_sent(&s.bar_mass, round & 1u) && ok;
+    if (!ok) {
+      if (tid == 0) record_error(status, CG_DEV_TIMEOUT);
+      return Drawn();
+    }
+    w = make_float2(0.f, 0.f);
+    for (uint32_t i = lane; i < n * kWarps; i += 32) {
+      w.x += s.mass[i].x;
+      w.y += s.mass[i].y;
+    }
+    w.x = warp_reduce(w.x, SumOp());
+    w.y = warp_reduce(w.y, SumOp());
+    if (check && !(w.y >= target * 1.00001f)) {
+      cut = low;  // kept tokens may lie below
+      listed = false;
+      __syncthreads();
+      if (tid == 0) s.n_local = 0;  // a barrier opens the next round
+      continue;
+    }
+    if (w.x < target) return d;
+    if (!listed) {
+      __syncthreads();
+      if (tid == 0) s.n_local = 0;
+    }
+    // the next value of the type above the refused token's
+    cut = BF16 ? fkey_inv(((fkey(d.x) >> 16) + 1u) << 16) : fkey_inv(fkey(d.x) + 1u);
   }
-  return block_max(best, s.red64b);
 }
 
 template <bool BF16, int NV>
@@ -434,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
       if (q.p < 1.f) {
         const float D = logf(float(a.V) / ((1.f - q.p) * S)) + 1e-3f;
         cut = fmaxf(cut, M - D * q.T);
-        if (mode != kGather && q.p * S < float(kListCap)) {
-          guess = fmaxf(cut, M - fmaxf(D - kGuess, 0.f) * q.T);
-          mode = kGuessFirst;
+        if (mode != kGather) {
+          guess = fmaxf(D, 0.f);
+          mode = S < kFlat ? kGuessFirst : kSample;
         }
       }
     }
@@ -464,24 +452,82 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
   const float* u = a.u + size_t(b) * a.ld_u;
 
   Drawn d;
-  float list_cut = cut;
+  float list_cut = cut, near = cut;
   uint32_t total = 0;
   if (mode == kGather) {
-    h.gather(s, cut, false, [](float) { return 0ull; });
+    h.template gather<false>(s, cut, false, kTooMany - 1u, M, c);
     if (rank != 0) return;  // its entries are with rank 0
-    unsigned long long none;
-    if (!h.tallied(s, total, none)) mode = kNothing;
+    float none;
+    bool whole;
+    if (!h.tallied(s, total, whole, none)) mode = kNothing;
   } else if (mode == kGuessFirst) {
-    list_cut = s.guess;
-    h.gather(s, list_cut, true, [&](float x) { return mass_q(x, M, c); });
-    unsigned long long mass;
-    const bool ok = h.tallied(s, total, mass);
-    mode = !ok ? kNothing : total <= kListCap && mass >= mass_target(q.p, mass_total(S)) ? kGather : kSpread;
-    if (rank != 0 && mode != kSpread) return;
+    list_cut = fmaxf(cut, M - fmaxf(s.guess - kGuess, 0.f) * q.T);
+    h.template gather<true>(s, list_cut, true, kWarpCap, M, c);
+    float mass;
+    bool whole;
+    const bool ok = h.tallied(s, total, whole, mass);
+    mode = !ok ? kNothing : whole && total <= kListCap && mass >= q.p * S * 1.00001f ? kGather : kSpread;
+    if (rank != 0 && (mode == kGather || mode == kNothing)) return;
+    // where the missing mass probably ends: the mass below a cut falls off by
+    // about kFallOff a nat
+    near = list_cut;
+    if (mass < q.p * S * 1.00001f) {
+      const float below = fmaxf(1.f - mass / S, 1e-6f);
+      near -= __fdividef(logf(below / (1.f - q.p)) + 0.05f, kFallOff) * q.T;
+    }
+  }
+  if (mode == kSample) {
+    // the masses below four cuts, estimated from the first group of every thread:
+    // the first cut that leaves little enough below it is the one to try
+    const float depth[4] = {5.f, 3.5f, 2.2f, 1.f};
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto level = [&](int i) { return M - fmaxf(s.guess - depth[i], 0.f) * q.T; };
+#pragma unroll
+    for (uint32_t e = 0; e < Fmt<BF16>::E; ++e) {
+      const float x = elem<BF16>(h.v[0], e), m = ex2((x - M) * c);
+      w.x += x < level(0) ? m : 0.f;
+      w.y += x < level(1) ? m : 0.f;
+      w.z += x < level(2) ? m : 0.f;
+      w.w += x < level(3) ? m : 0.f;
+    }
+    w.x = warp_reduce(w.x, SumOp());
+    w.y = warp_reduce(w.y, SumOp());
+    w.z = warp_reduce(w.z, SumOp());
+    w.w = warp_reduce(w.w, SumOp());
+    const uint32_t lane = tid & 31;
+    if (lane < n)
+      send(at_rank(&s.sample[rank * kWarps + (tid >> 5)], lane),
+           make_uint4(__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w)),
+           at_rank(&s.bar_tally, lane));
+    if (tid == 0) mbar_expect_tx(&s.bar_tally, n * kWarps * 16u);
+    const bool ok = wait_sent(&s.bar_tally);
+    w = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t i = lane; i < n * kWarps; i += 32) {
+      w.x += s.sample[i].x;
+      w.y += s.sample[i].y;
+      w.z += s.sample[i].z;
+      w.w += s.sample[i].w;
+    }
+    const float share = fminf(1.f, float(n * kThreads * Fmt<BF16>::E) / float(a.V));
+    const float most = (1.f - q.p) * S * share * 0.9f;
+    near = level(3);
+    if (warp_reduce(w.w, SumOp()) > most) near = cut;
+    if (warp_reduce(w.z, SumOp()) <= most) near = level(2);
+    if (warp_reduce(w.y, SumOp()) <= most) near = level(1);
+    if (warp_reduce(w.x, SumOp()) <= most) near = level(0);
+    if (!ok) {
+      if (rank == 0 && tid == 0) {
+        record_error(a.status, CG_DEV_TIMEOUT);
+        a.out_tok[b] = CG_NO_TOKEN;
+        if (a.out_lp) a.out_lp[b] = -INFINITY;
+      }
+      return;
+    }
+    mode = kSpread;
   }
   // the entries are on their way to rank 0, which settles them or, after a wrong
   // guess, uses the list's memory again
-  if (s.mode != kSpread && rank == 0 && (mode == kNothing || !h.listed(s, total))) {
+  if ((s.mode == kGather || s.mode == kGuessFirst) && rank == 0 && (mode == kNothing || !h.listed(s, total))) {
     if (tid == 0) {
       record_error(a.status, CG_DEV_TIMEOUT);
       a.out_tok[b] = CG_NO_TOKEN;
@@ -506,11 +552,8 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
       };
       float tau = list_cut;
       if (q.k || q.p < 1.f) {
-        if (!(BF16 && fits && threshold_in_list(s, total, q, list_cut, M, c, S, tau))) {
-          __syncthreads();
-          tau = fkey_inv(threshold_by_levels(
-              s, 1, 0, [&](auto f) { entries([&](uint32_t, float x) { f(fkey(x)); }); }, q, list_cut, M, c, S));
-        }
+        tau = fkey_inv(threshold_by_levels(
+            s, 1, 0, [&](auto f) { entries([&](uint32_t, float x) { f(fkey(x)); }); }, q, list_cut, M, c, S));
       }
       entries([&](uint32_t t, float x) {
         float score;
@@ -526,60 +569,50 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
     return;
   }
 
-  unsigned long long best = 0ull;
-  {
-    float tau = cut;
-    if (!q.greedy && (q.k || q.p < 1.f)) {
-      bool settled = false;
-      if constexpr (BF16) {
-        settled = threshold_by_counts<NV>(s, h, q, cut, M, c, S, tau);
-        if (!settled) cluster_sync(n);  // everybody has read the counts: the histograms take their place
-      }
-      if (!settled)
-        tau = fkey_inv(threshold_by_levels(
-            s, n, rank, [&](auto f) { h.each(cut, [&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S));
-    }
-    bool listed = false;
-    if (q.greedy) {
-      if (h.tm == M) h.each(M, [&](uint32_t t, float) { best = max(best, pack_best(0.f, t)); });
-      best = block_max(best, s.red64);
-    } else {
-      if (tau > -FLT_MAX) {
-        __syncthreads();  // s.merged has been read
-        unsigned long long none;
-        h.collect(s, tau, false, [](float) { return 0ull; }, none);
-        __syncthreads();
-        listed = s.n_local <= kListCap;
-      }
-      if (listed) {
-        for (uint32_t i = tid; i < s.n_local; i += kThreads) {
-          const unsigned long long e = s.local[i];
-          float score;
-          if (score_of(q, fkey_inv(uint32_t(e >> 32)) - M, u[best_id(e)], score)) best = max(best, pack_best(score, best_id(e)));
-        }
-        best = block_max(best, s.red64);
-      } else {
-        best = draw_screened<BF16, NV>(s, h, q, tau, M, c, u);
-      }
-    }
-    if (tid == 0) send(at_rank(&s.best[rank], 0), best, at_rank(&s.bar_best, 0));
-    if (!q.greedy && (q.k || q.p < 1.f)) {  // the others may still be reading this block's counts
-      cluster_arrive_relaxed();
-      cluster_wait();
-    }
+  if (!q.greedy && !q.k && q.p < 1.f) {
+    d = draw_by_trial<BF16, NV>(s, h, q, near, cut, M, c, S, u, a.status);
     if (rank != 0) return;
-    if (tid == 0) mbar_expect_tx(&s.bar_best, n * 8u);
-    if (!wait_sent(&s.bar_best)) {
-      if (tid == 0) record_error(a.status, CG_DEV_TIMEOUT);
-      best = 0ull;
-    } else {
-      for (uint32_t i = 0; i < n; ++i) best = max(best, s.best[i]);
+    if (tid == 0) {
+      a.out_tok[b] = d.best ? best_id(d.best) : CG_NO_TOKEN;
+      if (a.out_lp) a.out_lp[b] = d.best ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
     }
+    return;
   }
+
+  if (q.greedy) {
+    if (h.tm == M)
+      h.each(M, [&](uint32_t t, float x) { d.offer(0.f, t, x); });
+  } else {
+    float tau = cut;
+    if (q.k)
+      tau = fkey_inv(threshold_by_levels(
+          s, n, rank, [&](auto f) { h.each(cut, [&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S));
+    d = draw_screened<BF16, NV>(s, h, q, tau, M, c, u);
+  }
+  unsigned long long best = block_max(d.best, s.red64b);
+  if (best ? d.best == best : tid == 0) {  // one thread
+    send(at_rank(&s.best[rank], 0), best, at_rank(&s.bar_best, 0));
+    send(at_rank(&s.best_x[rank], 0), __float_as_uint(d.x), at_rank(&s.bar_best, 0));
+  }
+  if (q.k) {  // the others may still be reading this block's histograms
+    cluster_arrive_relaxed();
+    cluster_wait();
+  }
+  if (rank != 0) return;
+  if (tid >= 32) return;
+  if (tid == 0) mbar_expect_tx(&s.bar_best, n * 12u);
+  const bool ok = wait_sent(&s.bar_best);
+  d = Drawn();
+  for (uint32_t r = 0; r < n; ++r)
+    if (s.best[r] > d.best) {
+      d.best = s.best[r];
+      d.x = s.best_x[r];
+    }
   if (tid == 0) {
-    const uint32_t tok = best ? best_id(best) : CG_NO_TOKEN;
-    a.out_tok[b] = tok;
-    if (a.out_lp) a.out_lp[b] = best ? __fdiv_rn(h.r.value(tok) - M, q.Ts) - logf(S) : -INFINITY;
+    if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
+    const bool there = ok && d.best;
+    a.out_tok[b] = there ? best_id(d.best) : CG_NO_TOKEN;
+    if (a.out_lp) a.out_lp[b] = there ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
   }
 }
 

@@ -58,10 +58,11 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const To
   uint32_t found = 0;
   bool late = s.late != 0;
   if (M > -INFINITY && !late) {
-    h.gather(s, s.cut, false, [](float) { return 0ull; });
+    h.template gather<false>(s, s.cut, false, kTooMany - 1u, M, kLog2e);
     if (rank != 0) return;  // its entries are with rank 0
-    unsigned long long none;
-    late = !h.tallied(s, found, none) || !h.listed(s, found);
+    float none;
+    bool whole;
+    late = !h.tallied(s, found, whole, none) || !h.listed(s, found);
     if (late) found = 0;
     if (found > kListCap) {
       uint32_t level = 0;

@@ -28,10 +28,11 @@ namespace row {
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kWarps = kThreads / 32;
 constexpr uint32_t kMaxCluster = 16;   // more than 8 is not portable, but the one target has it
-constexpr uint32_t kBins = 1024;       // bins of one selection level
-constexpr uint32_t kListCap = 2048;    // entries of a block's list and of the gathered list
+constexpr uint32_t kBinBits = 9;
+constexpr uint32_t kBins = 1u << kBinBits;  // bins of one selection level
+constexpr uint32_t kListCap = 2048;    // entries of the gathered list
+constexpr uint32_t kWarpCap = 48;      // entries a warp sends for a guess
 constexpr uint32_t kPairCap = kThreads;  // lists ranked by comparing all pairs, an entry a thread
-constexpr uint32_t kCounts = 4096;     // bins of the bf16 key counts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxBf16 = 3.38953138925e38f;  // largest finite bf16
 constexpr uint32_t kKeyInf = 0xFF800000u;      // fkey(+inf); NaN keys lie above
@@ -133,7 +134,7 @@ __device__ __forceinline__ void cluster_sync(uint32_t n) {
 }
 
 constexpr uint32_t kMaxRecords = kMaxCluster * kWarps;  // warps of a cluster
-constexpr uint32_t kMaxBounds = 1024;                    // group maxima a cluster exchanges
+constexpr uint32_t kMaxBounds = 512;                     // group maxima a cluster exchanges
 
 // What a warp tells all blocks about its part of the row: its maximum and its
 // sum of exp2((x - m) c).
@@ -141,19 +142,23 @@ struct __align__(8) Record {
   float m, s;
 };
 // ... about the entries it has listed
-struct __align__(16) Tally {
-  unsigned long long mass;
-  uint32_t count, pad;
+struct __align__(8) Tally {
+  float mass;
+  uint32_t count;   // kTooMany: not sent
 };
+constexpr uint32_t kTooMany = 0xFFFFFFFFu;
 
 // Reductions and exchange
 struct Common {
-  uint64_t bar_rec, bar_tally, bar_list, bar_best;  // one phase each
+  uint64_t bar_rec, bar_tally, bar_list, bar_best, bar_mass;
   float M, S, cut, guess, floor_z;     // what the merging warp found
   uint32_t mode;
   uint32_t late;                       // a bounded wait ran out
   Record rec[kMaxRecords];
-  uint32_t bound[kMaxBounds];          // keys of group maxima
+  union {
+    uint32_t bound[kMaxBounds];                     // keys of group maxima (rows with a count)
+    __align__(16) float4 sample[kMaxRecords];       // sampled masses (rows without)
+  };
   Tally tally[kMaxRecords];
   unsigned long long best[kMaxCluster];
   unsigned long long sums[kMaxCluster];
@@ -162,24 +167,20 @@ struct Common {
   uint32_t red_max[kWarps];
   float red_f[kWarps];
   uint32_t n_list, n_local, bin;
+  float best_x[kMaxCluster];           // the logits of best[]
+  __align__(8) float2 mass[kMaxRecords];            // per warp: mass above the drawn token, mass at or above the cut
 };
-// ... with lists and histograms.  A row is gathered or counted, not both at once.
+// ... with the gathered list and histograms
 struct Shared : Common {
-  union {
-    __align__(16) unsigned long long list[kListCap];   // gathered entries (rank 0) as pack_best packs them
-    __align__(16) unsigned long long local[kListCap];  // this block's entries that stay
-    __align__(16) uint32_t merged[kCounts];            // key counts of the whole row
-  };
+  __align__(16) unsigned long long list[kListCap];   // entries as pack_best packs them: gathered (rank 0) or own
   union {
     __align__(16) unsigned long long hist[2][kBins];   // selection levels, alternating
-    __align__(16) uint32_t counts[kCounts];            // this block's key counts
     struct {
       __align__(16) uint32_t keys[kPairCap];             // of the gathered entries
       uint32_t place[kPairCap];                          // entries above each
       unsigned long long masses[kPairCap];               // by place
     };
   };
-  unsigned long long odd_mass;  // mass of the tokens in the bin of the smallest magnitudes
 };
 
 // ---- block reductions that cost one barrier each --------------------------------------
@@ -224,6 +225,7 @@ __device__ __forceinline__ void begin(Common& s) {
     mbar_init(&s.bar_tally, 1);
     mbar_init(&s.bar_list, 1);
     mbar_init(&s.bar_best, 1);
+    mbar_init(&s.bar_mass, 1);
     s.n_list = s.n_local = s.late = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -416,6 +418,12 @@ struct Held {
       for (int j = 0; j < NV; ++j) v[j] = r.masked(v[j], bits[j]);
     }
   }
+  // group j (any index at run time), from memory again
+  __device__ __forceinline__ uint4 again(uint32_t j) const {
+    uint4 x = clean_group<BF16>(r.load(group(j)));
+    if (r.mask) x = r.masked(x, r.mask_bits(first_token(j)));
+    return x;
+  }
   __device__ __forceinline__ float thread_max() const {
     float t = group_max_nan<BF16>(v[0]);
 #pragma unroll
@@ -479,77 +487,145 @@ struct Held {
       }
     }
   }
-  // Appends (logit, token) of every element >= cut to a list of kListCap
-  // entries: this block's own (to_rank0 false; a block barrier completes it) or
-  // rank 0's gathered one (completing on its bar_list).  The count goes on past
-  // the capacity, the entries do not.  Order is arbitrary.  weigh(x) is added up
-  // over the warp's entries into mass; returns their count.
-  template <typename Weigh>
-  __device__ __forceinline__ uint32_t collect(Shared& s, float cut, bool to_rank0, Weigh weigh,
-                                              unsigned long long& mass) const {
-    mass = 0;
-    if (!__any_sync(0xFFFFFFFFu, tm >= cut)) return 0u;  // most warps, when little is wanted
-    const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u, lane = threadIdx.x & 31;
-    uint32_t hits[(NV + 3) / 4] = {};
-    uint32_t mine = 0;
+  // Sends (logit, token) of every element >= cut to rank 0's list, completing on
+  // its bar_list, and then this warp's count and (MASS) its elements' mass in
+  // units of the maximum's to rank 0 or to every block (all), completing on
+  // bar_tally.  The list's count goes on past its capacity, the entries do not.
+  // Their order is arbitrary.  A warp with more than `most` entries sends none.
+  template <bool MASS>
+  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, uint32_t most, float M, float c) const {
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t found = 0;
+    float mass = 0.f;
+    if (__any_sync(0xFFFFFFFFu, tm >= cut)) {  // few warps, when little is wanted
+      const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
+      uint32_t hits[(NV + 3) / 4] = {};
+      uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) hits[j / 4] |= ge_bits<BF16>(v[j], cut, cut2) << (8 * (j % 4));
+      for (int j = 0; j < NV; ++j) hits[j / 4] |= ge_bits<BF16>(v[j], cut, cut2) << (8 * (j % 4));
 #pragma unroll
-    for (int i = 0; i < (NV + 3) / 4; ++i) mine += __popc(hits[i]);
-    uint32_t inc = mine;
+      for (int i = 0; i < (NV + 3) / 4; ++i) mine += __popc(hits[i]);
+      uint32_t inc = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= uint32_t(o)) inc += y;
-    }
-    uint32_t at = 0;
-    if (lane == 31)
-      at = to_rank0 ? add_remote(at_rank(&s.n_list, 0), inc) : atomicAdd(&s.n_local, inc);
-    at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - mine;
-    const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      uint32_t h = (hits[j / 4] >> (8 * (j % 4))) & 0xFFu;
-      while (h) {
-        const uint32_t e = __ffs(h) - 1;
-        h &= h - 1;
-        const float x = elem<BF16>(v[j], e);
-        const unsigned long long entry = pack_best(x, uint32_t(first_token(j)) + e);
-        if (at < kListCap) {
-          if (to_rank0) send(list + at * 8, entry, bar);
-          else s.local[at] = entry;
-        }
-        mass += weigh(x);
-        ++at;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= uint32_t(o)) inc += y;
       }
+      found = __shfl_sync(0xFFFFFFFFu, inc, 31);
+      if (found <= most) {
+        uint32_t at = 0;
+        if (lane == 31) at = add_remote(at_rank(&s.n_list, 0), inc);
+        at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - mine;
+        const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          uint32_t h = (hits[j / 4] >> (8 * (j % 4))) & 0xFFu;
+          while (h) {
+            const uint32_t e = __ffs(h) - 1;
+            h &= h - 1;
+            const float x = elem<BF16>(v[j], e);
+            if (at < kListCap) send(list + at * 8, pack_best(x, uint32_t(first_token(j)) + e), bar);
+            if (MASS) mass += ex2((x - M) * c);
+            ++at;
+          }
+        }
+      } else {
+        found = kTooMany;
+        if (MASS) mass = mass_where(M, c, [&](float x) { return x >= cut; });
+      }
+      if (MASS) mass = warp_reduce(mass, SumOp());
     }
-    mass = warp_reduce(mass, SumOp());
-    return __shfl_sync(0xFFFFFFFFu, inc, 31);
-  }
-  // collect() to rank 0 followed by this warp's count and mass, to rank 0 or to
-  // every block (all), completing on bar_tally
-  template <typename Weigh>
-  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, Weigh weigh) const {
-    unsigned long long mass;
-    const uint32_t found = collect(s, cut, true, weigh, mass), lane = threadIdx.x & 31;
     if (lane < (all ? n : 1u))
       send(at_rank(&s.tally[rank * kWarps + (threadIdx.x >> 5)], lane),
-           make_uint4(uint32_t(mass), uint32_t(mass >> 32), found, 0u), at_rank(&s.bar_tally, lane));
+           (static_cast<unsigned long long>(found) << 32) | __float_as_uint(mass), at_rank(&s.bar_tally, lane));
   }
-  // The gathered count and mass, to every thread of a block that tallies go to;
-  // false when the wait ran out.  The barrier's expectation is set here: early
-  // tallies wait in its transaction count.
-  __device__ __forceinline__ bool tallied(Shared& s, uint32_t& count, unsigned long long& mass) const {
+  // this thread's sum of exp2((x - M) c) over its elements with which(x)
+  template <typename Which>
+  __device__ __forceinline__ float mass_where(float M, float c, Which which) const {
+    float2 acc[2] = {};
+    const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (uint32_t q = 0; q < F::E / 2; ++q) {
+        const float2 x = pair<BF16>(v[j], q);
+        const float2 e = ex2_pair(__fmul2_rn(__fadd2_rn(x, nm), c2));
+        acc[q & 1u] = __fadd2_rn(acc[q & 1u], make_float2(which(x.x) ? e.x : 0.f, which(x.y) ? e.y : 0.f));
+      }
+    return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+  }
+  // ... over its elements > x, and over those >= y
+  __device__ __forceinline__ float2 masses_from(float M, float c, float x, float y) const {
+    float2 above = {}, from = {};
+    const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (uint32_t q = 0; q < F::E / 2; ++q) {
+        const float2 p = pair<BF16>(v[j], q);
+        const float2 e = ex2_pair(__fmul2_rn(__fadd2_rn(p, nm), c2));
+        above = __fadd2_rn(above, make_float2(p.x > x ? e.x : 0.f, p.y > x ? e.y : 0.f));
+        from = __fadd2_rn(from, make_float2(p.x >= y ? e.x : 0.f, p.y >= y ? e.y : 0.f));
+      }
+    return make_float2(above.x + above.y, from.x + from.y);
+  }
+  // Lists (logit, token) of every element >= cut in this block's own list, where it
+  // holds them all; s.n_local, zero before, receives their number.  Ends with a
+  // barrier.
+  __device__ __forceinline__ bool compact(Shared& s, float cut) const {
+    const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u, lane = threadIdx.x & 31;
+    uint32_t hits[(NV + 3) / 4] = {};
+    uint32_t mine = 0, inc = 0, at = 0;
+    const bool any = __any_sync(0xFFFFFFFFu, tm >= cut);
+    if (any) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) hits[j / 4] |= ge_bits<BF16>(v[j], cut, cut2) << (8 * (j % 4));
+#pragma unroll
+      for (int i = 0; i < (NV + 3) / 4; ++i) mine += __popc(hits[i]);
+      inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= uint32_t(o)) inc += y;
+      }
+      if (lane == 31) at = atomicAdd(&s.n_local, inc);
+      at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - mine;
+    }
+    __syncthreads();
+    const bool fits = s.n_local <= kListCap;
+    if (any && fits) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        uint32_t h = (hits[j / 4] >> (8 * (j % 4))) & 0xFFu;
+        while (h) {
+          const uint32_t e = __ffs(h) - 1;
+          h &= h - 1;
+          s.list[at++] = pack_best(elem<BF16>(v[j], e), uint32_t(first_token(j)) + e);
+        }
+      }
+    }
+    __syncthreads();
+    return fits;
+  }
+  // The gathered entries' count, whether every warp has sent its own, and the
+  // mass, to every thread of a block that tallies go to; false when the wait ran
+  // out.  The barrier's expectation is set here: early tallies wait in its
+  // transaction count.
+  __device__ __forceinline__ bool tallied(Shared& s, uint32_t& count, bool& whole, float& mass) const {
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_tally, n * kWarps * uint32_t(sizeof(Tally)));
     const bool ok = wait_sent(&s.bar_tally);
-    mass = 0;
+    mass = 0.f;
     count = 0;
+    bool over = false;
     for (uint32_t i = threadIdx.x & 31; i < n * kWarps; i += 32) {
       mass += s.tally[i].mass;
-      count += s.tally[i].count;
+      const uint32_t k = s.tally[i].count;
+      over |= k == kTooMany;
+      count += k == kTooMany ? 0u : k;
     }
     mass = warp_reduce(mass, SumOp());
-    count = warp_reduce(count, SumOp());
+    count = __reduce_add_sync(0xFFFFFFFFu, count);
+    whole = !__any_sync(0xFFFFFFFFu, over);
     return ok;
   }
   // Rank 0, after tallied(): the list's entries are there
@@ -594,7 +670,7 @@ __device__ __forceinline__ uint32_t bound_key(const Common& s, uint32_t count, u
   lo = __reduce_min_sync(0xFFFFFFFFu, lo);
   hi = __reduce_max_sync(0xFFFFFFFFu, hi) + 1u;  // fewer than k reach hi, all reach lo
 #pragma unroll 1
-  while (hi - lo > 0x4000u) {
+  while (hi - lo > 0x10000u) {  // 1/128 of an octave
     const uint32_t mid = lo + (hi - lo) / 2;
     uint32_t reach = 0;
     for (uint32_t i = lane; i < count; i += 32) reach += s.bound[i] >= mid;
@@ -606,7 +682,7 @@ __device__ __forceinline__ uint32_t bound_key(const Common& s, uint32_t count, u
 
 // Largest key k in [lo, hi] whose upper set {key >= k}, over the whole row,
 // carries at least `target` of the weights that each(f) reports for this block's
-// part through f(key, weight); lo when none does.  Radix selection: up to 1024
+// part through f(key, weight); lo when none does.  Radix selection: up to kBins
 // equal bins of the key interval per level, the blocks' bins added up by every
 // block, then the bin that the target falls into.  Integer weights: the result
 // does not depend on the order of the atomics.  `above` receives the weight of
@@ -621,7 +697,7 @@ __device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, ui
   above = 0;
   for (;;) {
     const uint32_t range = hi - lo;
-    const uint32_t shift = range < kBins ? 0u : 22u - __clz(range);
+    const uint32_t shift = range < kBins ? 0u : 32u - kBinBits - __clz(range);
     unsigned long long* hist = s.hist[level++ & 1u];
     // the level two before, which used this histogram, was read by every block
     // before the cluster met in the level between
