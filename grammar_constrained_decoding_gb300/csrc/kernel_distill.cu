@@ -18,19 +18,25 @@ namespace {
 
 using namespace row;
 
-constexpr uint32_t kHash = 2 * CG_TOP_MAX;  // slots of the repeated-id check
-
-// The teacher's list in shared memory
+// The teacher's list in shared memory, K entries
 struct List {
-  uint32_t id[CG_TOP_MAX];   // listed ids that count, CG_NO_TOKEN for the others
-  float t[CG_TOP_MAX];       // teacher logits, then weights q
-  float x[CG_TOP_MAX];       // the student's logits there
-  uint32_t hash[kHash];
-  uint32_t repeated;
+  uint32_t* id;     // listed ids that count, CG_NO_TOKEN for the others
+  float* t;         // teacher logits
+  float* x;         // the student's logits there
+  uint32_t* hash;   // slots of the repeated-id check, more than twice K
+  uint32_t slots;
+  __host__ __device__ static uint32_t slots_of(uint32_t K) {
+    uint32_t s = 4;
+    while (s < 2 * K) s <<= 1;
+    return s;
+  }
+  __host__ __device__ static size_t bytes(uint32_t K) { return (size_t(K) * 12 + size_t(slots_of(K)) * 4 + 15) & ~size_t(15); }
+  __device__ List(void* at, uint32_t K)
+      : id(static_cast<uint32_t*>(at)), t(reinterpret_cast<float*>(id + K)), x(t + K),
+        hash(reinterpret_cast<uint32_t*>(x + K)), slots(slots_of(K)) {}
 };
-struct DistillShared {
-  List list;
-  Common s;
+struct DistillShared : Common {
+  uint32_t repeated;
 };
 
 struct DistillArgs {
@@ -80,24 +86,24 @@ __device__ __forceinline__ void store_group(char* row, int t0, uint32_t V, bool 
   }
 }
 
-template <bool BF16, int NV, bool LOSS>
-__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(const DistillArgs a) {
+template <bool BF16, bool LOSS>
+__global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs a, uint32_t nv) {
   extern __shared__ __align__(16) unsigned char smem[];
-  List& l = reinterpret_cast<DistillShared*>(smem)->list;
-  Common& s = reinterpret_cast<DistillShared*>(smem)->s;
+  DistillShared& s = *reinterpret_cast<DistillShared*>(smem);
+  const List l(smem + sizeof(DistillShared), a.K);
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x, K = a.K;
-  if (LOSS) begin(s);
+  begin(s);
+  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, 
+               reinterpret_cast<uint4*>(smem + sizeof(DistillShared) + List::bytes(K)));
+  __syncthreads();
   griddep_wait();
+  h.start(s);
   const float T = a.temp, c = exp_scale(T);
-  Held<BF16, NV> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b));
-  h.load();
-
   // the teacher's list
-  uint32_t slots = 2;
-  while (slots < 2 * K) slots <<= 1;
+  const uint32_t slots = l.slots;
   for (uint32_t i = tid; i < slots; i += kThreads) l.hash[i] = CG_NO_TOKEN;
-  if (tid == 0) l.repeated = 0;
+  if (tid == 0) s.repeated = 0;
   float tm = -INFINITY;
   for (uint32_t k = tid; k < K; k += kThreads) {
     uint32_t id = a.ids[size_t(b) * K + k];
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
       const uint32_t old = atomicCAS(l.hash + at, CG_NO_TOKEN, id);
       if (old == CG_NO_TOKEN) break;
       if (old == id) {
-        l.repeated = 1;
+        s.repeated = 1;
         break;
       }
     }
@@ -136,8 +142,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
 
   float M = 0.f, S = 1.f;  // p = exp2((x - M) c) / S
   if (LOSS) {
-    h.find_max();
-    h.sum_exps(c);
+    if (!h.template take<true>(s, c)) record_error(a.status, CG_DEV_TIMEOUT);
     ready_others();
     h.publish(s, c, 0u);
     if (tid < 32) {
@@ -171,8 +176,9 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
     if (!a.grad) return;
   } else {
     M = a.lse_in[b] * T;  // p = exp((x - lse T) / T)
-    h.find_max();  // for its replacements
-    if (a.grad == a.logits) cluster_sync(n);
+    if (!h.template take<false>(s, c)) record_error(a.status, CG_DEV_TIMEOUT);
+    ready_others();
+    if (a.grad == a.logits) cluster_sync(n);  // every block has read what it needs
   }
 
   const float scale = listed ? T * (a.up ? a.up[b] : 1.f) : 0.f;
@@ -180,20 +186,21 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
   char* row = static_cast<char*>(a.grad) + size_t(b) * a.ld_grad * Fmt<BF16>::kSize;
   const bool wide = ((reinterpret_cast<uintptr_t>(row) / Fmt<BF16>::kSize - h.r.a) & (Fmt<BF16>::E - 1)) == 0;
   const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c), r2 = make_float2(r, r);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (!h.r.in_row(h.group(j))) continue;
+#pragma unroll 2
+  for (uint32_t j = 0; j < nv; ++j) {
+    if (!h.r.in_row(h.group(j))) break;
+    const uint4 v = h.at(j);
     float2 g[Fmt<BF16>::E / 2];
 #pragma unroll
     for (uint32_t q = 0; q < Fmt<BF16>::E / 2; ++q) {
       g[q] = make_float2(0.f, 0.f);
-      if (listed) g[q] = __fmul2_rn(ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(h.v[j], q), nm), c2)), r2);
+      if (listed) g[q] = __fmul2_rn(ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v, q), nm), c2)), r2);
     }
     store_group<BF16>(row, h.first_token(j), a.V, wide, g);
   }
   if (!listed) return;
   __syncthreads();
-  const bool repeated = l.repeated != 0;
+  const bool repeated = s.repeated != 0;
   for (uint32_t k = tid; k < K; k += kThreads) {
     const uint32_t id = l.id[k];
     if (id == CG_NO_TOKEN) continue;
@@ -212,11 +219,9 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) distill_kernel(cons
 template <bool BF16>
 cudaError_t launch_distill(int device, uint32_t B, const DistillArgs& a, bool loss, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld));
-  return with_nv<BF16>(plan.nv, [&](auto nv) {
-    constexpr int NV = decltype(nv)::value;
-    return loss ? launch_clusters<distill_kernel<BF16, NV, true>>(device, B, plan.n, sizeof(DistillShared), stream, a)
-                : launch_clusters<distill_kernel<BF16, NV, false>>(device, B, plan.n, sizeof(DistillShared), stream, a);
-  });
+  const size_t smem = sizeof(DistillShared) + List::bytes(a.K) + size_t(plan.nv) * kThreads * 16;
+  return loss ? launch_clusters<distill_kernel<BF16, true>>(device, B, plan.n, smem, stream, a, plan.nv)
+              : launch_clusters<distill_kernel<BF16, false>>(device, B, plan.n, smem, stream, a, plan.nv);
 }
 
 int distill(cg_ctx* c, const char* call, const DistillArgs& base, int dtype, uint32_t B, bool loss) {

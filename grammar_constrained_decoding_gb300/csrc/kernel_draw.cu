@@ -54,7 +54,7 @@ struct DrawArgs {
 
 // min-p rows whose kept tokens cannot be more than this are gathered: the list
 // then overflows only by ties
-constexpr float kGatherCount = 1536.f;
+constexpr float kGatherCount = 768.f;
 constexpr float kGuess = 3.f;
 constexpr float kFallOff = 0.35f;
 constexpr float kFlat = 3.f;
@@ -162,17 +162,17 @@ __device__ Drawn draw_pairs(Shared& s, uint32_t c, const RowSettings& q, float M
 
 // The random numbers of a group's tokens: 16-byte loads where the group is inside
 // the row and the numbers lie on the 16-byte grid with the logits
-template <bool BF16, int NV>
+template <bool BF16>
 struct Numbers {
   static constexpr uint32_t E = Fmt<BF16>::E;
   const float* u;
   bool wide;
-  __device__ __forceinline__ Numbers(const Held<BF16, NV>& h, const float* u_) : u(u_) {
+  __device__ __forceinline__ Numbers(const Held<BF16>& h, const float* u_) : u(u_) {
     wide = ((reinterpret_cast<uintptr_t>(u) / 4 - h.r.a) & 3u) == 0;
   }
-  __device__ __forceinline__ void load(const Held<BF16, NV>& h, uint32_t j, bool wanted, float* out) const {
+  __device__ __forceinline__ void load(const Held<BF16>& h, uint32_t j, float* out) const {
     const int t0 = h.first_token(j);
-    if (wanted && wide && t0 >= 0 && uint32_t(t0) + E <= h.r.V) {
+    if (wide && t0 >= 0 && uint32_t(t0) + E <= h.r.V) {
 #pragma unroll
       for (uint32_t i = 0; i < E / 4; ++i) {
         const float4 w = __ldcs(reinterpret_cast<const float4*>(u + t0) + i);
@@ -181,7 +181,7 @@ struct Numbers {
         out[4 * i + 2] = w.z;
         out[4 * i + 3] = w.w;
       }
-    } else if (wanted) {
+    } else {
 #pragma unroll
       for (uint32_t e = 0; e < E; ++e) out[e] = t0 + int(e) >= 0 && t0 + int(e) < int(h.r.V) ? u[t0 + int(e)] : 0.f;
     }
@@ -193,11 +193,11 @@ struct Numbers {
 // multi-function unit.  Every thread finds the group with its best bound and the
 // next group's bound; the best token of that group is scored exactly, and a thread
 // with another bound that reaches the block's best score goes over its part again.
-template <bool BF16, int NV>
-__device__ Drawn draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSettings& q, float low, float M, float c,
+template <bool BF16>
+__device__ Drawn draw_screened(Shared& s, const Held<BF16>& h, const RowSettings& q, float low, float M, float c,
                                const float* u) {
   constexpr uint32_t E = Fmt<BF16>::E;
-  const Numbers<BF16, NV> numbers(h, u);
+  const Numbers<BF16> numbers(h, u);
   const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c);
   // upper bounds of a group's scores, in bits
   auto bounds = [&](const uint4& v, const float* un, float* ub) {
@@ -213,12 +213,13 @@ __device__ Drawn draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSett
   };
   float first = -INFINITY, second = -INFINITY;
   uint32_t at = 0;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (!(group_max_nan<BF16>(h.v[j]) >= low)) continue;
+#pragma unroll 2
+  for (uint32_t j = 0; j < h.nv; ++j) {
+    const uint4 v = h.at(j);
+    if (!(group_max_nan<BF16>(v) >= low)) continue;
     float un[E], ub[E];
-    numbers.load(h, j, true, un);
-    bounds(h.v[j], un, ub);
+    numbers.load(h, j, un);
+    bounds(v, un, ub);
     float top = ub[0];
 #pragma unroll
     for (uint32_t e = 1; e < E; ++e) top = fmaxf(top, ub[e]);
@@ -231,9 +232,9 @@ __device__ Drawn draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSett
   Drawn d;
   float score;
   if (first > -INFINITY) {
-    const uint4 v = h.again(at);
+    const uint4 v = h.at(at);
     float un[E], ub[E], top = -INFINITY;
-    numbers.load(h, at, true, un);
+    numbers.load(h, at, un);
     bounds(v, un, ub);
     uint32_t best = 0;
     float ut = 0.f;
@@ -253,9 +254,8 @@ __device__ Drawn draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSett
   // 1e-3 nats cover the roundings of the bounds
   if (second > -INFINITY && (best == 0ull || second >= (fkey_inv(uint32_t(best >> 32)) - 1e-3f) * kLog2e)) {
 #pragma unroll 1
-    for (uint32_t j = 0; j < NV; ++j) {
-      if (!h.r.in_row(h.group(j))) break;
-      const uint4 v = h.again(j);
+    for (uint32_t j = 0; j < h.nv; ++j) {
+      const uint4 v = h.at(j);
 #pragma unroll 1
       for (uint32_t e = 0; e < E; ++e) {
         const float x = elem<BF16>(v, e);
@@ -270,8 +270,8 @@ __device__ Drawn draw_screened(Shared& s, const Held<BF16, NV>& h, const RowSett
 // A top-p row over the whole cluster, by trial as described above.  Returns the
 // drawn token to every block; near: a cut that is likely low enough, low: one that
 // certainly is.
-template <bool BF16, int NV>
-__device__ Drawn draw_by_trial(Shared& s, const Held<BF16, NV>& h, const RowSettings& q, float near, float low, float M,
+template <bool BF16>
+__device__ Drawn draw_by_trial(Shared& s, const Held<BF16>& h, const RowSettings& q, float near, float low, float M,
                                float c, float S, const float* u, uint32_t* status) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, n = h.n;
   const float target = fmaxf(q.p * S, 1e-30f);
@@ -282,11 +282,16 @@ __device__ Drawn draw_by_trial(Shared& s, const Held<BF16, NV>& h, const RowSett
   for (uint32_t round = 0;; ++round) {
     const bool settled = round == kTries;  // the random numbers rank the tokens almost against their logits
     if (settled) {
+      if (listed) {  // the histograms take the list's place
+        listed = false;
+        __syncthreads();
+        if (tid == 0) s.n_local = 0;
+      }
       cut = fkey_inv(threshold_by_levels(
           s, n, h.rank, [&](auto f) { h.each(low, [&](uint32_t, float y) { f(fkey(y)); }); }, q, low, M, c, S));
     }
     __syncthreads();
-    if (!listed) {  // few enough: from a list, else from the registers
+    if (!listed && !settled) {  // few enough: from a list, else from the part itself
       listed = h.compact(s, cut);
     }
     const uint32_t key = fkey(cut);
@@ -299,7 +304,7 @@ __device__ Drawn draw_by_trial(Shared& s, const Held<BF16, NV>& h, const RowSett
         if (k >= key && score_of(q, fkey_inv(k) - M, u[t], score)) d.offer(score, t, fkey_inv(k));
       }
     } else {
-      d = draw_screened<BF16, NV>(s, h, q, cut, M, c, u);
+      d = draw_screened<BF16>(s, h, q, cut, M, c, u);
     }
     const unsigned long long best = block_max(d.best, s.red64b);
     if (best ? d.best == best : tid == 0) {  // one thread
@@ -371,16 +376,17 @@ __device__ Drawn draw_by_trial(Shared& s, const Held<BF16, NV>& h, const RowSett
   }
 }
 
-template <bool BF16, int NV>
-__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const DrawArgs a) {
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uint32_t nv) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
   begin(s);
+  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, reinterpret_cast<uint4*>(smem + sizeof(Shared)));
+  __syncthreads();
   griddep_wait();
-  Held<BF16, NV> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b));
-  h.load();
+  h.start(s);
   RowSettings q;
   q.T = a.temp ? a.temp[b] : 1.f;
   q.k = a.top_k ? a.top_k[b] : 0u;
@@ -391,12 +397,12 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
   if (q.k >= a.V || q.greedy) q.k = 0;
   const float c = exp_scale(q.Ts);
   const uint32_t per_warp = q.k ? bounds_per_warp(q.k, n) : 0u;
-  h.find_max();
-  h.sum_exps(c);
+  const bool taken = h.template take<true>(s, c);
+  if (!taken) s.late = 1;
   ready_others();
   h.publish(s, c, per_warp);
   if (tid < 32) {
-    const bool ok = wait_sent(&s.bar_rec);
+    const bool ok = wait_sent(&s.bar_rec) && s.late == 0;
     float M, S;
     merge(s, n, c, M, S);
     // a lower bound of the threshold, and how to settle it.  Without top-k the
@@ -435,7 +441,6 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
       s.guess = guess;
       s.floor_z = floor_z;
       s.mode = mode;
-      s.late = !ok;
       if (rank == 0 && mode == kNothing) {
         if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
         else if (bad) record_error(a.status, CG_DEV_BAD_PARAM);
@@ -482,9 +487,10 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
     const float depth[4] = {5.f, 3.5f, 2.2f, 1.f};
     float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
     auto level = [&](int i) { return M - fmaxf(s.guess - depth[i], 0.f) * q.T; };
+    const uint4 v0 = h.at(0);
 #pragma unroll
     for (uint32_t e = 0; e < Fmt<BF16>::E; ++e) {
-      const float x = elem<BF16>(h.v[0], e), m = ex2((x - M) * c);
+      const float x = elem<BF16>(v0, e), m = ex2((x - M) * c);
       w.x += x < level(0) ? m : 0.f;
       w.y += x < level(1) ? m : 0.f;
       w.z += x < level(2) ? m : 0.f;
@@ -570,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
   }
 
   if (!q.greedy && !q.k && q.p < 1.f) {
-    d = draw_by_trial<BF16, NV>(s, h, q, near, cut, M, c, S, u, a.status);
+    d = draw_by_trial<BF16>(s, h, q, near, cut, M, c, S, u, a.status);
     if (rank != 0) return;
     if (tid == 0) {
       a.out_tok[b] = d.best ? best_id(d.best) : CG_NO_TOKEN;
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
     if (q.k)
       tau = fkey_inv(threshold_by_levels(
           s, n, rank, [&](auto f) { h.each(cut, [&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S));
-    d = draw_screened<BF16, NV>(s, h, q, tau, M, c, u);
+    d = draw_screened<BF16>(s, h, q, tau, M, c, u);
   }
   unsigned long long best = block_max(d.best, s.red64b);
   if (best ? d.best == best : tid == 0) {  // one thread
@@ -619,9 +625,8 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) draw_kernel(const D
 template <bool BF16>
 cudaError_t launch_draw(int device, uint32_t B, const DrawArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld));
-  return with_nv<BF16>(plan.nv, [&](auto nv) {
-    return launch_clusters<draw_kernel<BF16, decltype(nv)::value>>(device, B, plan.n, sizeof(Shared), stream, a);
-  });
+  return launch_clusters<draw_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + size_t(plan.nv) * kThreads * 16, stream,
+                                            a, plan.nv);
 }
 
 }  // namespace

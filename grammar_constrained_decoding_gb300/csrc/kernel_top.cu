@@ -25,19 +25,19 @@ struct TopArgs {
   uint32_t* status;
 };
 
-template <bool BF16, int NV>
-__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const TopArgs a) {
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint32_t nv) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   using F = Fmt<BF16>;
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
   begin(s);
+  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, reinterpret_cast<uint4*>(smem + sizeof(Shared)));
+  __syncthreads();
   griddep_wait();
-  Held<BF16, NV> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b));
-  h.load();
-  h.find_max();
-  h.sum_exps(kLog2e);
+  h.start(s);
+  if (!h.template take<true>(s, kLog2e)) s.late = 1;
   const uint32_t per_warp = bounds_per_warp(a.n, n);
   ready_others();
   h.publish(s, kLog2e, per_warp);
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const To
       s.M = m;
       s.S = sum;
       s.cut = key >= kKeyLowest ? fkey_inv(key) : -FLT_MAX;
-      s.late = !ok;
+      if (!ok) s.late = 1;
     }
   }
   __syncthreads();
@@ -116,9 +116,8 @@ __global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 2) top_kernel(const To
 template <bool BF16>
 cudaError_t launch_top(int device, uint32_t B, const TopArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld));
-  return with_nv<BF16>(plan.nv, [&](auto nv) {
-    return launch_clusters<top_kernel<BF16, decltype(nv)::value>>(device, B, plan.n, sizeof(Shared), stream, a);
-  });
+  return launch_clusters<top_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + size_t(plan.nv) * kThreads * 16, stream,
+                                           a, plan.nv);
 }
 
 }  // namespace

@@ -1,17 +1,26 @@
 // Rows of logits held on chip, the frame of the per-row operators
 // (sample_rows, top_logprobs, distill).
 //
-// A row belongs to a cluster of n <= 16 blocks of 256 threads.  Every thread
-// loads NV 16-byte groups of it (8 bf16 or 4 floats each) once and keeps them in
-// registers, so the row is read from memory once whatever the operator does
-// with it; the blocks exchange what they must (maxima, sums, bounds, entries,
-// counts) through one another's shared memory.  Short messages go as asynchronous
-// stores that complete on the receiver's mbarrier: the sender neither fences nor
-// waits (a cluster barrier with release semantics made every thread wait for its
-// stores, the longest stall of an earlier form).  Groups lie on the 16-byte
-// grid of the memory, not of the row: a row that starts off the grid has a
-// first group with some elements before the row, loaded one by one, and every
-// other load stays 16 bytes wide.
+// A row belongs to a cluster of n <= 16 blocks of 256 threads.  Each block copies
+// its part once into shared memory (bulk copies completing on mbarriers), and
+// every pass an operator makes over the row reads it there, so the row is read
+// from memory once.  A thread only ever reads the 16-byte groups (8 bf16 or 4
+// floats) that are its own, so the passes need no barriers between them.
+//
+// An earlier form held the parts in registers: 32 of them a thread spilled in the
+// longer passes, whose traffic (118 MB written for 66 MB of logits) cost more
+// than the row, and its unrolled passes missed the instruction cache.
+//
+// Groups lie on the 16-byte grid of the memory, not of the row: a row that starts
+// off the grid has a first group with some elements before the row, which its
+// thread loads one by one, and every other group is copied whatever the row's
+// alignment.
+//
+// The blocks exchange what they must (maxima, sums, bounds, entries) through one
+// another's shared memory.  Short messages go as asynchronous stores that
+// complete on the receiver's mbarrier: the sender neither fences nor waits (a
+// cluster barrier with release semantics made every thread wait for its stores,
+// the longest stall of an earlier form).
 //
 // A logit that is -inf or NaN, or whose bitmask bit is clear, is not allowed
 // and reads as -inf; +inf reads as the largest finite value.
@@ -30,7 +39,7 @@ constexpr uint32_t kWarps = kThreads / 32;
 constexpr uint32_t kMaxCluster = 16;   // more than 8 is not portable, but the one target has it
 constexpr uint32_t kBinBits = 9;
 constexpr uint32_t kBins = 1u << kBinBits;  // bins of one selection level
-constexpr uint32_t kListCap = 2048;    // entries of the gathered list
+constexpr uint32_t kListCap = 1024;    // entries of a list
 constexpr uint32_t kWarpCap = 48;      // entries a warp sends for a guess
 constexpr uint32_t kPairCap = kThreads;  // lists ranked by comparing all pairs, an entry a thread
 constexpr float kLog2e = 1.4426950408889634f;
@@ -147,10 +156,14 @@ struct __align__(8) Tally {
   uint32_t count;   // kTooMany: not sent
 };
 constexpr uint32_t kTooMany = 0xFFFFFFFFu;
+constexpr uint32_t kChunk = 4;       // groups a thread takes at a time
+constexpr uint32_t kMaxChunks = 12;
+constexpr uint32_t kMaxGroups = kChunk * kMaxChunks;  // of a thread
 
 // Reductions and exchange
-struct Common {
+struct __align__(16) Common {
   uint64_t bar_rec, bar_tally, bar_list, bar_best, bar_mass;
+  uint64_t bar_part[kMaxChunks];       // the copies of this block's part
   float M, S, cut, guess, floor_z;     // what the merging warp found
   uint32_t mode;
   uint32_t late;                       // a bounded wait ran out
@@ -170,11 +183,15 @@ struct Common {
   float best_x[kMaxCluster];           // the logits of best[]
   __align__(8) float2 mass[kMaxRecords];            // per warp: mass above the drawn token, mass at or above the cut
 };
-// ... with the gathered list and histograms
+// ... with lists and histograms (the second histogram only where a cluster selects,
+// which then has no use for a list)
 struct Shared : Common {
-  __align__(16) unsigned long long list[kListCap];   // entries as pack_best packs them: gathered (rank 0) or own
   union {
-    __align__(16) unsigned long long hist[2][kBins];   // selection levels, alternating
+    __align__(16) unsigned long long list[kListCap];     // entries as pack_best packs them: gathered (rank 0) or own
+    __align__(16) unsigned long long hist1[kBins];       // odd selection levels of a cluster
+  };
+  union {
+    __align__(16) unsigned long long hist0[kBins];       // the other selection levels
     struct {
       __align__(16) uint32_t keys[kPairCap];             // of the gathered entries
       uint32_t place[kPairCap];                          // entries above each
@@ -226,6 +243,7 @@ __device__ __forceinline__ void begin(Common& s) {
     mbar_init(&s.bar_list, 1);
     mbar_init(&s.bar_best, 1);
     mbar_init(&s.bar_mass, 1);
+    for (uint32_t i = 0; i < kMaxChunks; ++i) mbar_init(s.bar_part + i, 1);
     s.n_list = s.n_local = s.late = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -238,14 +256,6 @@ __device__ __forceinline__ void ready_others() { cluster_wait(); }
 __device__ __forceinline__ float exp_scale(float T) { return fminf(__fdiv_rn(kLog2e, T), FLT_MAX); }
 
 // ---- the row ----------------------------------------------------------------------------
-
-__device__ __forceinline__ uint4 ld_group(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 
 // Where a row's groups lie.  Group g holds tokens g * E - a + (0 .. E-1).
 template <bool BF16>
@@ -274,13 +284,13 @@ struct Row {
     if (sh + F::E > 8u && uint32_t(t0 | 7) + 1u < V) w |= uint32_t(mask[(t0 >> 3) + 1]) << 8;
     return w >> sh;
   }
-  // group g's bits, -inf outside the row (the mask not applied)
-  __device__ __forceinline__ uint4 load(uint32_t g) const {
+  // whole groups, those that a bulk copy may bring: [first, end)
+  __device__ __forceinline__ uint32_t first_whole() const { return a ? 1u : 0u; }
+  __device__ __forceinline__ uint32_t end_whole() const { return (V + a) / F::E; }
+  // a group that is not whole: element by element, -inf outside the row
+  __device__ __forceinline__ uint4 edge(uint32_t g) const {
     const int t0 = int(g * F::E) - int(a);
-    if (t0 >= 0 && uint32_t(t0) + F::E <= V) return ld_group(base + size_t(g) * 16);
-    uint4 v = make_uint4(F::kNegInf, F::kNegInf, F::kNegInf, F::kNegInf);
-    if (t0 >= int(V)) return v;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w[4] = {F::kNegInf, F::kNegInf, F::kNegInf, F::kNegInf};
 #pragma unroll
     for (uint32_t e = 0; e < F::E; ++e) {
       const int t = t0 + int(e);
@@ -391,66 +401,114 @@ __device__ __forceinline__ uint32_t bf16_pair_up(float cut) {
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// The part of a row that a block holds, and what the cluster knows of the row.
-template <bool BF16, int NV>
+// The part of a row that a block holds
+template <bool BF16>
 struct Held {
   using F = Fmt<BF16>;
   Row<BF16> r;
   uint32_t n, rank;   // cluster size, this block
-  uint4 v[NV];
+  uint32_t nv;        // groups of a thread
+  uint4* part;        // group j of thread t at [j * kThreads + t]
   float tm;           // this thread's maximum
   float ts;           // its sum of exp2((x - tm) c)
 
-  __device__ __forceinline__ Held(const Row<BF16>& row) : r(row), n(cluster_size()), rank(cluster_rank()) {}
+  __device__ __forceinline__ Held(const Row<BF16>& row, uint32_t nv_, uint4* part_)
+      : r(row), n(cluster_size()), rank(cluster_rank()), nv(nv_), part(part_) {}
   // group j of this thread: consecutive threads hold consecutive groups, the
   // blocks take turns at runs of kThreads
   __device__ __forceinline__ uint32_t group(uint32_t j) const { return (j * n + rank) * kThreads + threadIdx.x; }
   __device__ __forceinline__ int first_token(uint32_t j) const { return int(group(j) * F::E) - int(r.a); }
+  __device__ __forceinline__ uint4 at(uint32_t j) const { return part[j * kThreads + threadIdx.x]; }
 
-  __device__ __forceinline__ void load() {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = r.load(group(j));
-    if (r.mask) {
-      uint32_t bits[NV];
-#pragma unroll
-      for (int j = 0; j < NV; ++j) bits[j] = r.in_row(group(j)) ? r.mask_bits(first_token(j)) : 0u;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) v[j] = r.masked(v[j], bits[j]);
+  // Starts the copies (after begin() and a block barrier); the groups that they
+  // do not bring are written by their threads.
+  __device__ __forceinline__ void start(Common& s) const {
+    const uint32_t lo = r.first_whole(), hi = r.end_whole();
+    if (threadIdx.x < 32) {
+      // lane i issues run i, i + 32, ... (one lane a chunk's expectation first)
+      for (uint32_t q = threadIdx.x; q * kChunk < nv; q += 32) {
+        uint32_t bytes = 0;
+        for (uint32_t j = q * kChunk; j < min(nv, (q + 1) * kChunk); ++j) {
+          const uint32_t g0 = (j * n + rank) * kThreads, from = max(g0, lo), to = min(g0 + kThreads, hi);
+          bytes += to > from ? (to - from) * 16u : 0u;
+        }
+        mbar_expect_tx(s.bar_part + q, bytes);
+        for (uint32_t j = q * kChunk; j < min(nv, (q + 1) * kChunk); ++j) {
+          const uint32_t g0 = (j * n + rank) * kThreads, from = max(g0, lo), to = min(g0 + kThreads, hi);
+          if (to > from)
+            bulk_g2s(part + j * kThreads + (from - g0), r.base + size_t(from) * 16, (to - from) * 16u, s.bar_part + q);
+        }
+      }
+    }
+    // groups before lo or from hi on: at most one each side in the row
+    const uint32_t run = group(0) - threadIdx.x;
+    if (lo && run == 0 && threadIdx.x == 0) part[0] = r.edge(0);
+    for (uint32_t j = nv; j-- > 0;) {
+      const uint32_t g = group(j);
+      if (g < hi) break;
+      if (g >= lo) part[j * kThreads + threadIdx.x] = r.edge(g);
     }
   }
-  // group j (any index at run time), from memory again
-  __device__ __forceinline__ uint4 again(uint32_t j) const {
-    uint4 x = clean_group<BF16>(r.load(group(j)));
-    if (r.mask) x = r.masked(x, r.mask_bits(first_token(j)));
-    return x;
-  }
-  __device__ __forceinline__ float thread_max() const {
-    float t = group_max_nan<BF16>(v[0]);
+  // First pass, chunk by chunk as the copies land: applies the mask and the
+  // replacements of NaN and +inf (writing back what they change), and finds this
+  // thread's maximum and, with SUM, its sum of exp2((x - tm) c), scaled on as the
+  // maximum rises.  False when a wait ran out.
+  template <bool SUM>
+  __device__ __forceinline__ bool take(Common& s, float c) {
+    bool ok = true;
+    tm = -INFINITY;
+    float2 acc = {};
+    const float2 c2 = make_float2(c, c);
+#pragma unroll 1
+    for (uint32_t j0 = 0; j0 < nv; j0 += kChunk) {
+      uint32_t bits[kChunk];
+      if (r.mask) {
 #pragma unroll
-    for (int j = 1; j < NV; ++j) t = max_nan(t, group_max_nan<BF16>(v[j]));
-    return t;
-  }
-  // this thread's maximum, after NaN and +inf have been replaced
-  __device__ __forceinline__ void find_max() {
-    tm = thread_max();
-    if (fkey(tm) < kKeyInf) return;
+        for (uint32_t i = 0; i < kChunk; ++i)
+          bits[i] = j0 + i < nv && r.in_row(group(j0 + i)) ? r.mask_bits(first_token(j0 + i)) : 0u;
+      }
+      ok = mbar_wait(s.bar_part + j0 / kChunk, 0) && ok;
+      uint4 v[kChunk];
+      float t = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = clean_group<BF16>(v[j]);
-    tm = thread_max();
-  }
-  // its sum of exp2((x - tm) c)
-  __device__ __forceinline__ void sum_exps(float c) {
-    ts = 0.f;
-    if (!(tm > -INFINITY)) return;
-    const float2 nm = make_float2(-tm, -tm), c2 = make_float2(c, c);
-    float2 acc[4] = {};
+      for (uint32_t i = 0; i < kChunk; ++i) {
+        v[i] = make_uint4(F::kNegInf, F::kNegInf, F::kNegInf, F::kNegInf);
+        if (j0 + i < nv) v[i] = at(j0 + i);
+        if (r.mask) {
+          v[i] = r.masked(v[i], bits[i]);
+          if (j0 + i < nv) part[(j0 + i) * kThreads + threadIdx.x] = v[i];
+        }
+        t = max_nan(t, group_max_nan<BF16>(v[i]));
+      }
+      if (fkey(t) >= kKeyInf) {
+        t = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+        for (uint32_t i = 0; i < kChunk; ++i) {
+          v[i] = clean_group<BF16>(v[i]);
+          if (j0 + i < nv) part[(j0 + i) * kThreads + threadIdx.x] = v[i];
+          t = fmaxf(t, group_max_nan<BF16>(v[i]));
+        }
+      }
+      if (t > tm) {
+        if (SUM) {
+          const float f = ex2((tm - t) * c);  // 0 from the first -inf on
+          acc = make_float2(acc.x * f, acc.y * f);
+        }
+        tm = t;
+      }
+      if (SUM && tm > -INFINITY) {
+        const float2 nm = make_float2(-tm, -tm);
+        float2 sum[4] = {};
 #pragma unroll
-      for (uint32_t q = 0; q < F::E / 2; ++q)
-        acc[q] = __fadd2_rn(acc[q], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[j], q), nm), c2)));
+        for (uint32_t i = 0; i < kChunk; ++i)
 #pragma unroll
-    for (uint32_t q = 0; q < 4; ++q) ts += acc[q].x + acc[q].y;
+          for (uint32_t q = 0; q < F::E / 2; ++q)
+            sum[q] = __fadd2_rn(sum[q], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[i], q), nm), c2)));
+        acc = __fadd2_rn(acc, __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3])));
+      }
+    }
+    ts = acc.x + acc.y;
+    return ok;
   }
   // Tells every block of the cluster this warp's maximum and sum, and, for a
   // bound on the k-th largest logit, the maxima of `per_warp` groups of its
@@ -473,19 +531,30 @@ struct Held {
       send(at_rank(&s.bound[w * per_warp + (i & (per_warp - 1))], i / per_warp), key,
            at_rank(&s.bar_rec, i / per_warp));
   }
-  // f(token, logit) for every element of this block's part that is >= cut (finite)
+  // f(token, logit) for every element of this thread's groups that is >= cut (finite)
   template <typename Fn>
   __device__ __forceinline__ void each(float cut, Fn f) const {
+    if (!(tm >= cut)) return;
     const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      uint32_t hits = ge_bits<BF16>(v[j], cut, cut2);
+#pragma unroll 1
+    for (uint32_t j = 0; j < nv; ++j) {
+      const uint4 v = at(j);
+      uint32_t hits = ge_bits<BF16>(v, cut, cut2);
       while (hits) {
         const uint32_t e = __ffs(hits) - 1;
         hits &= hits - 1;
-        f(uint32_t(first_token(j)) + e, elem<BF16>(v[j], e));
+        f(uint32_t(first_token(j)) + e, elem<BF16>(v, e));
       }
     }
+  }
+  // the number of those elements
+  __device__ __forceinline__ uint32_t count(float cut) const {
+    uint32_t c = 0;
+    if (!(tm >= cut)) return c;
+    const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
+#pragma unroll 4
+    for (uint32_t j = 0; j < nv; ++j) c += __popc(ge_bits<BF16>(at(j), cut, cut2));
+    return c;
   }
   // Sends (logit, token) of every element >= cut to rank 0's list, completing on
   // its bar_list, and then this warp's count and (MASS) its elements' mass in
@@ -498,13 +567,7 @@ struct Held {
     uint32_t found = 0;
     float mass = 0.f;
     if (__any_sync(0xFFFFFFFFu, tm >= cut)) {  // few warps, when little is wanted
-      const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
-      uint32_t hits[(NV + 3) / 4] = {};
-      uint32_t mine = 0;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) hits[j / 4] |= ge_bits<BF16>(v[j], cut, cut2) << (8 * (j % 4));
-#pragma unroll
-      for (int i = 0; i < (NV + 3) / 4; ++i) mine += __popc(hits[i]);
+      const uint32_t mine = count(cut);
       uint32_t inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -513,25 +576,18 @@ struct Held {
       }
       found = __shfl_sync(0xFFFFFFFFu, inc, 31);
       if (found <= most) {
-        uint32_t at = 0;
-        if (lane == 31) at = add_remote(at_rank(&s.n_list, 0), inc);
-        at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - mine;
+        uint32_t place = 0;
+        if (lane == 31) place = add_remote(at_rank(&s.n_list, 0), inc);
+        place = __shfl_sync(0xFFFFFFFFu, place, 31) + inc - mine;
         const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          uint32_t h = (hits[j / 4] >> (8 * (j % 4))) & 0xFFu;
-          while (h) {
-            const uint32_t e = __ffs(h) - 1;
-            h &= h - 1;
-            const float x = elem<BF16>(v[j], e);
-            if (at < kListCap) send(list + at * 8, pack_best(x, uint32_t(first_token(j)) + e), bar);
-            if (MASS) mass += ex2((x - M) * c);
-            ++at;
-          }
-        }
+        each(cut, [&](uint32_t t, float x) {
+          if (place < kListCap) send(list + place * 8, pack_best(x, t), bar);
+          if (MASS) mass += ex2((x - M) * c);
+          ++place;
+        });
       } else {
         found = kTooMany;
-        if (MASS) mass = mass_where(M, c, [&](float x) { return x >= cut; });
+        if (MASS) mass = masses_from(M, c, cut, cut).y;
       }
       if (MASS) mass = warp_reduce(mass, SumOp());
     }
@@ -539,71 +595,40 @@ struct Held {
       send(at_rank(&s.tally[rank * kWarps + (threadIdx.x >> 5)], lane),
            (static_cast<unsigned long long>(found) << 32) | __float_as_uint(mass), at_rank(&s.bar_tally, lane));
   }
-  // this thread's sum of exp2((x - M) c) over its elements with which(x)
-  template <typename Which>
-  __device__ __forceinline__ float mass_where(float M, float c, Which which) const {
-    float2 acc[2] = {};
-    const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (uint32_t q = 0; q < F::E / 2; ++q) {
-        const float2 x = pair<BF16>(v[j], q);
-        const float2 e = ex2_pair(__fmul2_rn(__fadd2_rn(x, nm), c2));
-        acc[q & 1u] = __fadd2_rn(acc[q & 1u], make_float2(which(x.x) ? e.x : 0.f, which(x.y) ? e.y : 0.f));
-      }
-    return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-  }
-  // ... over its elements > x, and over those >= y
+  // this thread's sums of exp2((x - M) c) over its elements > x, and over those >= y
   __device__ __forceinline__ float2 masses_from(float M, float c, float x, float y) const {
     float2 above = {}, from = {};
+    if (!(tm >= fminf(x, y))) return above;
     const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
+#pragma unroll 2
+    for (uint32_t j = 0; j < nv; ++j) {
+      const uint4 v = at(j);
 #pragma unroll
       for (uint32_t q = 0; q < F::E / 2; ++q) {
-        const float2 p = pair<BF16>(v[j], q);
+        const float2 p = pair<BF16>(v, q);
         const float2 e = ex2_pair(__fmul2_rn(__fadd2_rn(p, nm), c2));
         above = __fadd2_rn(above, make_float2(p.x > x ? e.x : 0.f, p.y > x ? e.y : 0.f));
         from = __fadd2_rn(from, make_float2(p.x >= y ? e.x : 0.f, p.y >= y ? e.y : 0.f));
       }
+    }
     return make_float2(above.x + above.y, from.x + from.y);
   }
   // Lists (logit, token) of every element >= cut in this block's own list, where it
   // holds them all; s.n_local, zero before, receives their number.  Ends with a
   // barrier.
   __device__ __forceinline__ bool compact(Shared& s, float cut) const {
-    const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u, lane = threadIdx.x & 31;
-    uint32_t hits[(NV + 3) / 4] = {};
-    uint32_t mine = 0, inc = 0, at = 0;
-    const bool any = __any_sync(0xFFFFFFFFu, tm >= cut);
-    if (any) {
+    const uint32_t lane = threadIdx.x & 31, mine = count(cut);
+    uint32_t inc = mine, place = 0;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) hits[j / 4] |= ge_bits<BF16>(v[j], cut, cut2) << (8 * (j % 4));
-#pragma unroll
-      for (int i = 0; i < (NV + 3) / 4; ++i) mine += __popc(hits[i]);
-      inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= uint32_t(o)) inc += y;
-      }
-      if (lane == 31) at = atomicAdd(&s.n_local, inc);
-      at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= uint32_t(o)) inc += y;
     }
+    if (lane == 31 && inc) place = atomicAdd(&s.n_local, inc);
+    place = __shfl_sync(0xFFFFFFFFu, place, 31) + inc - mine;
     __syncthreads();
     const bool fits = s.n_local <= kListCap;
-    if (any && fits) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        uint32_t h = (hits[j / 4] >> (8 * (j % 4))) & 0xFFu;
-        while (h) {
-          const uint32_t e = __ffs(h) - 1;
-          h &= h - 1;
-          s.list[at++] = pack_best(elem<BF16>(v[j], e), uint32_t(first_token(j)) + e);
-        }
-      }
-    }
+    if (fits && mine) each(cut, [&](uint32_t t, float x) { s.list[place++] = pack_best(x, t); });
     __syncthreads();
     return fits;
   }
@@ -698,9 +723,11 @@ __device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, ui
   for (;;) {
     const uint32_t range = hi - lo;
     const uint32_t shift = range < kBins ? 0u : 32u - kBinBits - __clz(range);
-    unsigned long long* hist = s.hist[level++ & 1u];
-    // the level two before, which used this histogram, was read by every block
-    // before the cluster met in the level between
+    // alone, the barriers of the scan separate a level's reads from the next
+    // level's zeros; in a cluster the level two before, which used this histogram,
+    // was read by every block before the cluster met in the level between
+    unsigned long long* hist = n > 1 && (level & 1u) ? s.hist1 : s.hist0;
+    ++level;
     for (uint32_t i = tid; i < kBins; i += kThreads) hist[i] = 0ull;
     if (tid == 0) s.bin = kBins;
     __syncthreads();
@@ -807,34 +834,32 @@ __device__ inline void sort_desc(unsigned long long* list, uint32_t n) {
 
 // ---- launching -----------------------------------------------------------------------
 
-// NV and the cluster size of a launch.  Few rows take the smallest NV (the
-// widest cluster): the row is split over more SMs while all blocks are resident
-// together; many rows take NV = 8, four blocks an SM.
+// The cluster size of a launch and the groups of a thread.  Few rows take the widest
+// cluster whose blocks are all resident together, so that a row is split over more
+// SMs; many rows take parts of kFull groups a thread (32 KB), four blocks an SM.
 struct Plan {
   uint32_t nv, n;
 };
-constexpr uint32_t kSlots = 4 * 152;  // blocks resident at NV = 8
+constexpr uint32_t kSlots = 4 * 152;  // blocks resident together
+constexpr uint32_t kFull = 8;
 inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned) {
   const uint32_t E = bf16 ? 8 : 4;
-  const uint32_t groups = (V + (aligned ? 0 : E - 1) + E - 1) / E;
-  Plan best{0, 0};
-  for (uint32_t nv : {1u, 2u, 4u, 8u, 16u, 24u}) {
-    const uint32_t n = (groups + kThreads * nv - 1) / (kThreads * nv);
-    if (n > kMaxCluster || (best.nv && nv > 8)) continue;
-    best = {nv, n};
-    if (n == 1 || uint64_t(B) * n <= kSlots) break;
-  }
-  return best;
+  const uint32_t runs = ((V + (aligned ? 0 : E - 1) + E - 1) / E + kThreads - 1) / kThreads;  // of kThreads groups
+  uint32_t n = (runs + kFull - 1) / kFull;
+  if (n > kMaxCluster) n = kMaxCluster;
+  while (n < kMaxCluster && n < runs && uint64_t(B) * (n + 1) <= kSlots) ++n;
+  return {(runs + n - 1) / n, n};
 }
 
 // Launches Kernel on clusters of n blocks, `rows` of them.  The kernel's shared
 // memory and cluster size limits are raised on the first launch on a device.
+constexpr int kMaxSmem = 227 * 1024;
 template <auto Kernel, typename... Args>
 cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, size_t smem, cudaStream_t stream, Args&&... args) {
   static std::atomic<uint64_t> raised{0};
   const uint64_t bit = uint64_t(1) << (device & 63);
   if (!(raised.load(std::memory_order_relaxed) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit, std::memory_order_relaxed);
@@ -854,20 +879,6 @@ cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, size_t smem, 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, Kernel, std::forward<Args>(args)...);
-}
-
-// f<NV>() for the plan's NV (24 only for floats, whose rows are the longest)
-template <bool BF16, typename Fn>
-cudaError_t with_nv(uint32_t nv, Fn f) {
-  switch (nv) {
-    case 1: return f(std::integral_constant<int, 1>());
-    case 2: return f(std::integral_constant<int, 2>());
-    case 4: return f(std::integral_constant<int, 4>());
-    case 8: return f(std::integral_constant<int, 8>());
-    case 16: return f(std::integral_constant<int, 16>());
-    case 24: return f(std::integral_constant<int, BF16 ? 16 : 24>());
-    default: return cudaErrorInvalidValue;
-  }
 }
 
 }  // namespace row
