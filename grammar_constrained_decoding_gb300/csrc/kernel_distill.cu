@@ -96,11 +96,17 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
   begin(s);
   Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, 
                reinterpret_cast<uint4*>(smem + sizeof(DistillShared) + List::bytes(K)));
-  __syncthreads();
   griddep_wait();
   h.start(s);
+  may_send();
   const float T = a.temp, c = exp_scale(T);
-  // the teacher's list
+  // the teacher's list (without a gradient only rank 0 has a use for it)
+  if (LOSS && !a.grad && rank != 0) {
+    if (!h.template take<true>(s, c)) record_error(a.status, CG_DEV_TIMEOUT);
+    ready_others();
+    h.template report<false>(s, c);
+    return;
+  }
   const uint32_t slots = l.slots;
   for (uint32_t i = tid; i < slots; i += kThreads) l.hash[i] = CG_NO_TOKEN;
   if (tid == 0) s.repeated = 0;
@@ -144,7 +150,11 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
   if (LOSS) {
     if (!h.template take<true>(s, c)) record_error(a.status, CG_DEV_TIMEOUT);
     ready_others();
-    h.publish(s, c, 0u);
+    if (a.grad) {
+      h.publish(s, c, 0u);
+    } else {
+      h.template report<false>(s, c);
+    }
     if (tid < 32) {
       const bool ok = wait_sent(&s.bar_rec);
       float m, sum;

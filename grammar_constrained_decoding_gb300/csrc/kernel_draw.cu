@@ -133,14 +133,14 @@ struct Drawn {
 // With the number of entries above each (its place) and the masses added up by
 // place, an entry stays when fewer than k are above it and less than the target's
 // mass; the random numbers are on their way meanwhile.
-__device__ Drawn draw_pairs(Shared& s, uint32_t c, const RowSettings& q, float M, float scale, float S, const float* u) {
+__device__ Drawn draw_pairs(Shared& s, const unsigned long long* list, uint32_t c, const RowSettings& q, float M, float scale, float S, const float* u) {
   const uint32_t tid = threadIdx.x;
-  const unsigned long long e = tid < c ? s.list[tid] : 0ull;
+  const unsigned long long e = tid < c ? list[tid] : 0ull;
   const float x = fkey_inv(uint32_t(e >> 32)), ut = tid < c ? u[best_id(e)] : 0.5f;
   bool stays = tid < c;
   if (q.k || q.p < 1.f) {
     s.masses[tid] = 0ull;
-    place_entries<false>(s, c);
+    place_entries<false>(s, list, c);
     const uint32_t place = s.place[tid];
     if (q.k) stays = stays && place < q.k;
     if (q.p < 1.f) {
@@ -384,9 +384,9 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
   begin(s);
   Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, reinterpret_cast<uint4*>(smem + sizeof(Shared)));
-  __syncthreads();
   griddep_wait();
   h.start(s);
+  may_send();
   RowSettings q;
   q.T = a.temp ? a.temp[b] : 1.f;
   q.k = a.top_k ? a.top_k[b] : 0u;
@@ -396,30 +396,65 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   q.Ts = q.greedy ? 1.f : q.T;
   if (q.k >= a.V || q.greedy) q.k = 0;
   const float c = exp_scale(q.Ts);
-  const uint32_t per_warp = q.k ? bounds_per_warp(q.k, n) : 0u;
+  const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || p != p || mp != mp || (!q.greedy && !a.u);
+  // Rows that need nothing of the others' parts before they send what may be drawn:
+  // the maximum; the tokens at or above the block's own bound of the k-th largest,
+  // where the list holds those of all blocks; the best of all tokens.
+  enum { kTogether, kBest, kTopK, kAny } alone = kTogether;
+  if (!bad) {
+    if (q.greedy) alone = kBest;
+    else if (q.k && q.k <= kThreads * 3 / 4 && n * (q.k + q.k / 4 + 16) <= kListCap) alone = kTopK;
+    else if (!q.k && q.p >= 1.f && !(mp > 0.f)) alone = kAny;
+  }
+  const uint32_t per_warp = q.k && !alone ? bounds_per_warp(q.k, n) : 0u;
   const bool taken = h.template take<true>(s, c);
   if (!taken) s.late = 1;
-  ready_others();
-  h.publish(s, c, per_warp);
+  if (alone) {
+    float own_cut = -FLT_MAX;
+    if (alone == kTopK) {
+      const uint32_t key = h.own_bound(s, q.k);
+      if (key >= kKeyLowest) own_cut = fkey_inv(key);
+    }
+    ready_others();
+    if (alone == kBest) {
+      h.template report<true>(s, c);
+    } else {
+      h.template report<false>(s, c);
+      if (alone == kTopK) {
+        h.template gather<false>(s, own_cut, false, kTooMany - 1u, 0.f, 0.f);
+      } else {
+        // the block's best by scores relative to its own maximum: their order is
+        // that of scores relative to the row's
+        q.floor_z = -INFINITY;
+        const float m = fkey_inv(block_max(fkey(h.tm), s.red_max));
+        Drawn d;
+        if (m > -INFINITY) d = draw_screened<BF16>(s, h, q, -FLT_MAX, m, c, a.u + size_t(b) * a.ld_u);
+        const unsigned long long best = block_max(d.best, s.red64b);
+        if (best ? d.best == best : tid == 0)  // one thread
+          send(at_rank(&s.best[rank], 0), best ? pack_best(d.x, best_id(best)) : 0ull, at_rank(&s.bar_best, 0));
+      }
+    }
+    if (rank != 0) return;
+  } else {
+    ready_others();
+    h.publish(s, c, per_warp);
+  }
   if (tid < 32) {
     const bool ok = wait_sent(&s.bar_rec) && s.late == 0;
     float M, S;
     merge(s, n, c, M, S);
     // a lower bound of the threshold, and how to settle it.  Without top-k the
     // mass that top-p refers to is known, so min-p bounds what matters as well.
-    const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || p != p || mp != mp || (!q.greedy && !a.u);
     const float floor_z = logf(fminf(fmaxf(mp, 0.f), 1.f));  // -inf for min_p = 0
     float cut = -FLT_MAX, guess = 0.f;
     Mode mode = kSpread;
     if (bad || !ok || M == -INFINITY) {
       mode = kNothing;
-    } else if (q.greedy) {
-      cut = M;
     } else if (q.k) {
       const uint32_t key = per_warp ? bound_key(s, n * kWarps * per_warp, q.k) : 0u;
       if (key >= kKeyLowest) cut = fkey_inv(key);
-      if (per_warp) mode = kGather;
-    } else {
+      if (per_warp || alone) mode = kGather;
+    } else if (!alone) {
       // a little below M + T log(min_p), for the roundings
       if (floor_z > -INFINITY) {
         cut = fmaxf(M + floor_z * q.T * 1.000001f - 1e-6f * fabsf(M), -FLT_MAX);
@@ -452,16 +487,54 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   __syncthreads();
   const float M = s.M, S = s.S, cut = s.cut;
   uint32_t mode = s.mode;
-  if (mode == kNothing) return;
+  if (mode == kNothing) {  // not before what the others send has arrived
+    uint32_t count;
+    bool whole;
+    float mass;
+    if (alone == kTopK && h.tallied(s, count, whole, mass)) h.listed(s, count);
+    if (alone == kAny) {
+      if (tid == 0) mbar_expect_tx(&s.bar_best, n * 8u);
+      wait_sent(&s.bar_best);
+    }
+    return;
+  }
   q.floor_z = s.floor_z;
   const float* u = a.u + size_t(b) * a.ld_u;
+
+  if (alone == kBest || alone == kAny) {  // rank 0, one warp
+    if (tid >= 32) return;
+    Drawn d;
+    bool ok = true;
+    if (alone == kBest) {
+      for (uint32_t i = tid; i < n * kWarps; i += 32) d.best = max(d.best, s.top[i]);
+      d.x = M;
+    } else {
+      if (tid == 0) mbar_expect_tx(&s.bar_best, n * 8u);
+      ok = wait_sent(&s.bar_best);
+      const unsigned long long e = tid < n ? s.best[tid] : 0ull;
+      float score;
+      if (e) {
+        const float x = fkey_inv(uint32_t(e >> 32));
+        if (score_of(q, x - M, u[best_id(e)], score)) d.offer(score, best_id(e), x);
+      }
+    }
+    const unsigned long long best = warp_reduce(d.best, MaxOp());
+    if (alone == kBest ? tid == 0 : d.best == best) {
+      a.out_tok[b] = ok ? best_id(best) : CG_NO_TOKEN;
+      if (a.out_lp) a.out_lp[b] = ok ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
+      if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
+    }
+    return;
+  }
 
   Drawn d;
   float list_cut = cut, near = cut;
   uint32_t total = 0;
   if (mode == kGather) {
-    h.template gather<false>(s, cut, false, kTooMany - 1u, M, c);
-    if (rank != 0) return;  // its entries are with rank 0
+    if (!alone) {
+      h.template gather<false>(s, cut, false, kTooMany - 1u, M, c);
+      if (rank != 0) return;  // its entries are with rank 0
+    }
     float none;
     bool whole;
     if (!h.tallied(s, total, whole, none)) mode = kNothing;
@@ -543,8 +616,14 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   }
   const bool gather = mode == kGather;
   if (gather) {
-    if (total <= kPairCap) {
-      d = draw_pairs(s, total, q, M, c, S, u);
+    const unsigned long long* list = s.list;
+    uint32_t few = total;
+    if (total > kPairCap && total <= kListCap && q.k) {
+      few = keep_few(s, total, list_bound(s, total, q.k));
+      list = s.few;
+    }
+    if (few <= kPairCap) {
+      d = draw_pairs(s, list, few, q, M, c, S, u);
     } else {
       // from the list, or from the row when ties have made it overflow
       const bool fits = total <= kListCap;
@@ -575,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     return;
   }
 
-  if (!q.greedy && !q.k && q.p < 1.f) {
+  if (!q.k && q.p < 1.f) {
     d = draw_by_trial<BF16>(s, h, q, near, cut, M, c, S, u, a.status);
     if (rank != 0) return;
     if (tid == 0) {
@@ -585,16 +664,11 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     return;
   }
 
-  if (q.greedy) {
-    if (h.tm == M)
-      h.each(M, [&](uint32_t t, float x) { d.offer(0.f, t, x); });
-  } else {
-    float tau = cut;
-    if (q.k)
-      tau = fkey_inv(threshold_by_levels(
-          s, n, rank, [&](auto f) { h.each(cut, [&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S));
-    d = draw_screened<BF16>(s, h, q, tau, M, c, u);
-  }
+  float tau = cut;
+  if (q.k)
+    tau = fkey_inv(threshold_by_levels(
+        s, n, rank, [&](auto f) { h.each(cut, [&](uint32_t, float x) { f(fkey(x)); }); }, q, cut, M, c, S));
+  d = draw_screened<BF16>(s, h, q, tau, M, c, u);
   unsigned long long best = block_max(d.best, s.red64b);
   if (best ? d.best == best : tid == 0) {  // one thread
     send(at_rank(&s.best[rank], 0), best, at_rank(&s.bar_best, 0));

@@ -1,9 +1,10 @@
 // The n best allowed tokens of each row with their log-probabilities
 // (cg_top_logprobs).
 //
-// The row is held on chip by a cluster (logit_row.cuh).  The warps publish maxima
-// of groups of their lanes; at least n tokens lie at or above the n-th largest of
-// them, and little more.  Those are gathered by rank 0 and put in order
+// The row is held on chip by a cluster (logit_row.cuh).  At least n tokens lie at or
+// above the n-th largest of the maxima of any groups of tokens (threads of one
+// block, or groups of lanes of all blocks), and little more for many groups.  Those
+// are gathered by rank 0 and put in order
 // by (logit, lower id).  Where ties make the gathered list overflow, rank 0 reads
 // the row again by itself: the n-th largest logit and the last ids among its
 // ties by radix selection, then exactly n entries.
@@ -34,13 +35,27 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
   begin(s);
   Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, reinterpret_cast<uint4*>(smem + sizeof(Shared)));
-  __syncthreads();
   griddep_wait();
   h.start(s);
+  may_send();
   if (!h.template take<true>(s, kLog2e)) s.late = 1;
-  const uint32_t per_warp = bounds_per_warp(a.n, n);
-  ready_others();
-  h.publish(s, kLog2e, per_warp);
+  // Alone each block can only bound the n-th largest of its own part.  Where the
+  // entries of all parts fit the list they are sent without waiting for the others;
+  // else the bound comes from the whole row's group maxima.
+  const bool alone = a.n <= kThreads * 3 / 4 && n * (a.n + a.n / 4 + 16) <= kListCap;
+  const uint32_t per_warp = alone ? 0u : bounds_per_warp(a.n, n);
+  float cut = -FLT_MAX;
+  if (alone) {
+    const uint32_t key = h.own_bound(s, a.n);
+    if (key >= kKeyLowest) cut = fkey_inv(key);
+    ready_others();
+    h.template report<false>(s, kLog2e);
+    h.template gather<false>(s, cut, false, kTooMany - 1u, 0.f, 0.f);
+    if (rank != 0) return;  // its entries are with rank 0
+  } else {
+    ready_others();
+    h.publish(s, kLog2e, per_warp);
+  }
   if (tid < 32) {
     const bool ok = wait_sent(&s.bar_rec);
     float m, sum;
@@ -57,9 +72,12 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   const float M = s.M, S = s.S;
   uint32_t found = 0;
   bool late = s.late != 0;
-  if (M > -INFINITY && !late) {
-    h.template gather<false>(s, s.cut, false, kTooMany - 1u, M, kLog2e);
-    if (rank != 0) return;  // its entries are with rank 0
+  const unsigned long long* list = s.list;
+  if ((alone || M > -INFINITY) && !late) {
+    if (!alone) {
+      h.template gather<false>(s, s.cut, false, kTooMany - 1u, M, kLog2e);
+      if (rank != 0) return;
+    }
     float none;
     bool whole;
     late = !h.tallied(s, found, whole, none) || !h.listed(s, found);
@@ -87,6 +105,12 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
       });
       __syncthreads();
       found = s.n_list;
+    } else if (found > kPairCap) {
+      const uint32_t few = keep_few(s, found, list_bound(s, found, a.n));
+      if (few <= kPairCap) {
+        found = few;
+        list = s.few;
+      }
     }
   } else if (rank != 0) {
     return;
@@ -100,8 +124,8 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
     lps[i] = (fkey_inv(uint32_t(e >> 32)) - M) - log_s;
   };
   if (found <= kPairCap) {
-    place_entries<true>(s, found);
-    if (tid < found && s.place[tid] < a.n) write(s.place[tid], s.list[tid]);
+    place_entries<true>(s, list, found);
+    if (tid < found && s.place[tid] < a.n) write(s.place[tid], list[tid]);
   } else {
     sort_desc(s.list, found);
     for (uint32_t i = tid; i < min(found, a.n); i += kThreads) write(i, s.list[i]);

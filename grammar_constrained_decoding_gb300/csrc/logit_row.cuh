@@ -158,12 +158,13 @@ struct __align__(8) Tally {
 constexpr uint32_t kTooMany = 0xFFFFFFFFu;
 constexpr uint32_t kChunk = 4;       // groups a thread takes at a time
 constexpr uint32_t kMaxChunks = 12;
+constexpr uint32_t kBars = 5 + kMaxChunks;
 constexpr uint32_t kMaxGroups = kChunk * kMaxChunks;  // of a thread
 
 // Reductions and exchange
 struct __align__(16) Common {
-  uint64_t bar_rec, bar_tally, bar_list, bar_best, bar_mass;
-  uint64_t bar_part[kMaxChunks];       // the copies of this block's part
+  uint64_t bar_rec, bar_tally, bar_list, bar_best, bar_mass;  // kBars barriers in a row ...
+  uint64_t bar_part[kMaxChunks];                              // ... the last for the copies of this block's part
   float M, S, cut, guess, floor_z;     // what the merging warp found
   uint32_t mode;
   uint32_t late;                       // a bounded wait ran out
@@ -171,6 +172,8 @@ struct __align__(16) Common {
   union {
     uint32_t bound[kMaxBounds];                     // keys of group maxima (rows with a count)
     __align__(16) float4 sample[kMaxRecords];       // sampled masses (rows without)
+    unsigned long long few[kPairCap];               // the list's entries that matter (rank 0)
+    unsigned long long top[kMaxRecords];            // the best token of each warp
   };
   Tally tally[kMaxRecords];
   unsigned long long best[kMaxCluster];
@@ -234,22 +237,21 @@ __device__ __forceinline__ T block_scan(T v, T* red) {
   return v;
 }
 
-// The block's barriers and counters, before anything is sent to it.  With
-// ready_others() the blocks of a cluster know that all of them have got here.
+// The block's barriers and counters; ends with a block barrier.
 __device__ __forceinline__ void begin(Common& s) {
-  if (threadIdx.x == 0) {
-    mbar_init(&s.bar_rec, 1);
-    mbar_init(&s.bar_tally, 1);
-    mbar_init(&s.bar_list, 1);
-    mbar_init(&s.bar_best, 1);
-    mbar_init(&s.bar_mass, 1);
-    for (uint32_t i = 0; i < kMaxChunks; ++i) mbar_init(s.bar_part + i, 1);
-    s.n_list = s.n_local = s.late = 0;
+  if (threadIdx.x < kBars) {
+    mbar_init(&s.bar_rec + threadIdx.x, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x == 32) {  // not the warp that issues the copies: the fence would wait for them
+    s.n_list = s.n_local = s.late = 0;
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
   }
-  cluster_arrive_relaxed();
+  __syncthreads();
 }
+// Tells the cluster that this block may be sent to; ready_others() waits until all
+// blocks may.
+__device__ __forceinline__ void may_send() { cluster_arrive_relaxed(); }
 __device__ __forceinline__ void ready_others() { cluster_wait(); }
 
 // scale of the exponent of exp((x - m) / T) as a power of two, finite for every T > 0
@@ -401,6 +403,39 @@ __device__ __forceinline__ uint32_t bf16_pair_up(float cut) {
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 
+// A key that at least k of s.bound[0 .. count) reach, by bisection, count <= 512.  For
+// one warp.
+__device__ __forceinline__ uint32_t bound_key(const Common& s, uint32_t count, uint32_t k) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t v[kMaxBounds / 32], lo = 0xFFFFFFFFu, hi = 0;
+  const uint32_t each = (count + 31) / 32;
+#pragma unroll
+  for (uint32_t i = 0; i < kMaxBounds / 32; ++i) {
+    v[i] = 0;
+    if (i < each && i * 32 + lane < count) {
+      v[i] = s.bound[i * 32 + lane];
+      lo = min(lo, v[i]);
+      hi = max(hi, v[i]);
+    }
+  }
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi) + 1u;  // fewer than k reach hi, all reach lo
+#pragma unroll 1
+  while (hi - lo > 0x10000u) {  // 1/128 of an octave
+    const uint32_t mid = lo + (hi - lo) / 2;
+    uint32_t reach = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kMaxBounds / 32; i += 4)
+      if (i < each) {
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) reach += v[i + q] >= mid;
+      }
+    if (__reduce_add_sync(0xFFFFFFFFu, reach) >= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // The part of a row that a block holds
 template <bool BF16>
 struct Held {
@@ -420,24 +455,27 @@ struct Held {
   __device__ __forceinline__ int first_token(uint32_t j) const { return int(group(j) * F::E) - int(r.a); }
   __device__ __forceinline__ uint4 at(uint32_t j) const { return part[j * kThreads + threadIdx.x]; }
 
-  // Starts the copies (after begin() and a block barrier); the groups that they
-  // do not bring are written by their threads.
+  // Starts the copies, a lane a run of kThreads groups; the groups that they do not
+  // bring are written by their threads.
   __device__ __forceinline__ void start(Common& s) const {
     const uint32_t lo = r.first_whole(), hi = r.end_whole();
     if (threadIdx.x < 32) {
-      // lane i issues run i, i + 32, ... (one lane a chunk's expectation first)
-      for (uint32_t q = threadIdx.x; q * kChunk < nv; q += 32) {
-        uint32_t bytes = 0;
-        for (uint32_t j = q * kChunk; j < min(nv, (q + 1) * kChunk); ++j) {
-          const uint32_t g0 = (j * n + rank) * kThreads, from = max(g0, lo), to = min(g0 + kThreads, hi);
-          bytes += to > from ? (to - from) * 16u : 0u;
-        }
+      auto run = [&](uint32_t j, uint32_t& from) {  // groups to copy of run j
+        const uint32_t g0 = (j * n + rank) * kThreads, to = min(g0 + kThreads, hi);
+        from = max(g0, lo);
+        return to > from ? to - from : 0u;
+      };
+      for (uint32_t j = threadIdx.x; j < nv; j += 32) {
+        uint32_t from;
+        const uint32_t k = run(j, from);
+        if (k)
+          bulk_g2s(part + j * kThreads + (from - (j * n + rank) * kThreads), r.base + size_t(from) * 16, k * 16u,
+                   s.bar_part + j / kChunk);
+      }
+      for (uint32_t q = threadIdx.x; q * kChunk < nv; q += 32) {  // what has arrived by now counts against this
+        uint32_t from, bytes = 0;
+        for (uint32_t j = q * kChunk; j < min(nv, (q + 1) * kChunk); ++j) bytes += run(j, from) * 16u;
         mbar_expect_tx(s.bar_part + q, bytes);
-        for (uint32_t j = q * kChunk; j < min(nv, (q + 1) * kChunk); ++j) {
-          const uint32_t g0 = (j * n + rank) * kThreads, from = max(g0, lo), to = min(g0 + kThreads, hi);
-          if (to > from)
-            bulk_g2s(part + j * kThreads + (from - g0), r.base + size_t(from) * 16, (to - from) * 16u, s.bar_part + q);
-        }
       }
     }
     // groups before lo or from hi on: at most one each side in the row
@@ -517,12 +555,8 @@ struct Held {
   __device__ __forceinline__ void publish(Common& s, float c, uint32_t per_warp) const {
     const uint32_t lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_rec, n * kWarps * (8u + 4u * per_warp));
-    const float m = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, fkey(tm)));
-    const float sum = warp_reduce(tm > -INFINITY ? ts * ex2((tm - m) * c) : 0.f, SumOp());
-    if (lane < n)
-      send(at_rank(&s.rec[w], lane),
-           (static_cast<unsigned long long>(__float_as_uint(sum)) << 32) | __float_as_uint(m),
-           at_rank(&s.bar_rec, lane));
+    const unsigned long long rec = record(c);
+    if (lane < n) send(at_rank(&s.rec[w], lane), rec, at_rank(&s.bar_rec, lane));
     if (per_warp == 0) return;
     uint32_t key = fkey(tm);
     for (uint32_t o = 16; o >= per_warp; o >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
@@ -530,6 +564,47 @@ struct Held {
     for (uint32_t i = lane; i < per_warp * n; i += 32)
       send(at_rank(&s.bound[w * per_warp + (i & (per_warp - 1))], i / per_warp), key,
            at_rank(&s.bar_rec, i / per_warp));
+  }
+  // this warp's maximum and sum
+  __device__ __forceinline__ unsigned long long record(float c) const {
+    const float m = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, fkey(tm)));
+    const float sum = warp_reduce(tm > -INFINITY ? ts * ex2((tm - m) * c) : 0.f, SumOp());
+    return (static_cast<unsigned long long>(__float_as_uint(sum)) << 32) | __float_as_uint(m);
+  }
+  // Tells rank 0 alone, and with BEST this warp's best token too
+  template <bool BEST>
+  __device__ __forceinline__ void report(Common& s, float c) const {
+    const uint32_t lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
+    if (rank == 0 && threadIdx.x == 0) mbar_expect_tx(&s.bar_rec, n * kWarps * (BEST ? 16u : 8u));
+    const unsigned long long rec = record(c);
+    if (BEST) {
+      const float m = __uint_as_float(uint32_t(rec));
+      uint32_t t = 0xFFFFFFFFu;
+      if (tm == m && m > -INFINITY) {
+#pragma unroll 1
+        for (uint32_t j = 0; j < nv && t == 0xFFFFFFFFu; ++j) {  // tokens rise with j
+          const uint32_t hits = ge_bits<BF16>(at(j), m, BF16 ? bf16_pair_up(m) : 0u);
+          if (hits) t = uint32_t(first_token(j)) + __ffs(hits) - 1;
+        }
+      }
+      t = __reduce_min_sync(0xFFFFFFFFu, t);
+      if (lane == 0)
+        send(at_rank(&s.top[w], 0), m > -INFINITY ? pack_best(m, t) : 0ull, at_rank(&s.bar_rec, 0));
+    }
+    if (lane == 0) send(at_rank(&s.rec[w], 0), rec, at_rank(&s.bar_rec, 0));
+  }
+  // A key that at least k <= kThreads threads of this block reach with a token (so
+  // that at least k tokens lie at or above it): for gathering before the blocks
+  // know of one another.
+  __device__ __forceinline__ uint32_t own_bound(Common& s, uint32_t k) const {
+    s.bound[threadIdx.x] = fkey(tm);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const uint32_t key = bound_key(s, kThreads, k);
+      if (threadIdx.x == 0) s.bin = key;
+    }
+    __syncthreads();
+    return s.bin;
   }
   // f(token, logit) for every element of this thread's groups that is >= cut (finite)
   template <typename Fn>
@@ -683,28 +758,6 @@ __device__ __forceinline__ uint32_t bounds_per_warp(uint32_t k, uint32_t n) {
     if (4 * k <= 3 * warps * g) return g;
   return 0;
 }
-// A key that at least k of the published group maxima reach, by bisection (at
-// least k tokens then lie at or above it).  For one warp.
-__device__ __forceinline__ uint32_t bound_key(const Common& s, uint32_t count, uint32_t k) {
-  const uint32_t lane = threadIdx.x & 31;
-  uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  for (uint32_t i = lane; i < count; i += 32) {
-    lo = min(lo, s.bound[i]);
-    hi = max(hi, s.bound[i]);
-  }
-  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-  hi = __reduce_max_sync(0xFFFFFFFFu, hi) + 1u;  // fewer than k reach hi, all reach lo
-#pragma unroll 1
-  while (hi - lo > 0x10000u) {  // 1/128 of an octave
-    const uint32_t mid = lo + (hi - lo) / 2;
-    uint32_t reach = 0;
-    for (uint32_t i = lane; i < count; i += 32) reach += s.bound[i] >= mid;
-    if (__reduce_add_sync(0xFFFFFFFFu, reach) >= k) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // Largest key k in [lo, hi] whose upper set {key >= k}, over the whole row,
 // carries at least `target` of the weights that each(f) reports for this block's
 // part through f(key, weight); lo when none does.  Radix selection: up to kBins
@@ -786,18 +839,18 @@ __device__ uint32_t select_key(Shared& s, uint32_t n, Each each, uint32_t lo, ui
 // by key alone, or by key and id.  The block's threads share the pairs out (parts
 // of it compare with parts of the list).  Ends with a barrier.
 template <bool IDS>
-__device__ __forceinline__ void place_entries(Shared& s, uint32_t c) {
+__device__ __forceinline__ void place_entries(Shared& s, const unsigned long long* list, uint32_t c) {
   uint32_t C = 32;
   while (C < c) C <<= 1;
   const uint32_t tid = threadIdx.x, i = tid & (C - 1), part = tid / C, parts = kThreads / C;
-  if (!IDS) s.keys[tid] = tid < c ? uint32_t(s.list[tid] >> 32) : 0u;  // zeros are above nothing
+  if (!IDS) s.keys[tid] = tid < c ? uint32_t(list[tid] >> 32) : 0u;  // zeros are above nothing
   s.place[tid] = 0;
   __syncthreads();
   if (i < c) {
     uint32_t above = 0;
     if (IDS) {
-      const unsigned long long e = s.list[i];
-      for (uint32_t j = part; j < c; j += parts) above += s.list[j] > e;
+      const unsigned long long e = list[i];
+      for (uint32_t j = part; j < c; j += parts) above += list[j] > e;
     } else {
       const uint32_t key = s.keys[i];
 #pragma unroll 4
@@ -809,6 +862,59 @@ __device__ __forceinline__ void place_entries(Shared& s, uint32_t c) {
     if (above) atomicAdd(s.place + i, above);
   }
   __syncthreads();
+}
+
+// Copies the entries of s.list[0 .. c) whose key is at least `key` to s.few; returns
+// their number (none are copied past kPairCap).  Ends with a barrier.
+__device__ __forceinline__ uint32_t keep_few(Shared& s, uint32_t c, uint32_t key) {
+  __syncthreads();
+  if (threadIdx.x == 0) s.n_local = 0;
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < c; i += kThreads) {
+    const unsigned long long e = s.list[i];
+    if (uint32_t(e >> 32) < key) continue;
+    const uint32_t at = atomicAdd(&s.n_local, 1u);
+    if (at < kPairCap) s.few[at] = e;
+  }
+  __syncthreads();
+  return s.n_local;
+}
+// A key that at least k of s.list[0 .. c), c <= kListCap, reach, and few more: by
+// bisection, the block counting together
+__device__ __forceinline__ uint32_t list_bound(Shared& s, uint32_t c, uint32_t k) {
+  constexpr uint32_t kOwn = kListCap / kThreads;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (c <= k) return 0u;
+  uint32_t v[kOwn], lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < kOwn; ++i) {
+    const uint32_t at = i * kThreads + tid;
+    v[i] = at < c ? uint32_t(s.list[at] >> 32) : 0u;
+    if (at < c) {
+      lo = min(lo, v[i]);
+      hi = max(hi, v[i]);
+    }
+  }
+  lo = ~block_max(~lo, s.red_max);
+  __syncthreads();
+  hi = block_max(hi, s.red_max) + 1u;
+  for (uint32_t round = 0; hi - lo > 0x4000u; ++round) {  // a barrier a round: two sets of counters
+    const uint32_t mid = lo + (hi - lo) / 2;
+    uint32_t reach = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kOwn; ++i) reach += v[i] >= mid;
+    reach = __reduce_add_sync(0xFFFFFFFFu, reach);
+    uint32_t* sum = reinterpret_cast<uint32_t*>(round & 1u ? s.red64 : s.red64b);
+    if (lane == 0) sum[warp] = reach;
+    __syncthreads();
+    reach = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kWarps; ++w) reach += sum[w];
+    if (reach >= k) lo = mid;
+    else hi = mid;
+    if (reach == k) break;
+  }
+  return lo;
 }
 
 // Descending sort of list[0 .. n) (bitonic network over the next power of two,
