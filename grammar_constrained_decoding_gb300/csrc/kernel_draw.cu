@@ -59,7 +59,6 @@ constexpr float kGuess = 3.f;
 constexpr float kFallOff = 0.35f;
 constexpr float kFlat = 3.f;
 constexpr uint32_t kTries = 16;
-constexpr float kMassOne = 1099511627776.f;  // mass_q of the maximum
 
 enum Mode : uint32_t { kNothing, kGather, kGuessFirst, kSample, kSpread };
 
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     } else {
       h.template report<false>(s, c);
       if (alone == kTopK) {
-        h.template gather<false>(s, own_cut, false, kTooMany - 1u, 0.f, 0.f);
+        h.template gather<false>(s, own_cut, false, 0.f, 0.f);
       } else {
         // the block's best by scores relative to its own maximum: their order is
         // that of scores relative to the row's
@@ -530,17 +529,19 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   Drawn d;
   float list_cut = cut, near = cut;
   uint32_t total = 0;
+  bool left_out = false;  // a block had too many entries to send
   if (mode == kGather) {
     if (!alone) {
-      h.template gather<false>(s, cut, false, kTooMany - 1u, M, c);
+      h.template gather<false>(s, cut, false, 0.f, 0.f);
       if (rank != 0) return;  // its entries are with rank 0
     }
     float none;
-    bool whole;
+    bool whole = true;
     if (!h.tallied(s, total, whole, none)) mode = kNothing;
+    else if (!whole) left_out = true;
   } else if (mode == kGuessFirst) {
     list_cut = fmaxf(cut, M - fmaxf(s.guess - kGuess, 0.f) * q.T);
-    h.template gather<true>(s, list_cut, true, kWarpCap, M, c);
+    h.template gather<true>(s, list_cut, true, M, c);
     float mass;
     bool whole;
     const bool ok = h.tallied(s, total, whole, mass);
@@ -618,7 +619,9 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   if (gather) {
     const unsigned long long* list = s.list;
     uint32_t few = total;
-    if (total > kPairCap && total <= kListCap && q.k) {
+    if (left_out) {
+      few = kListCap + 1;
+    } else if (total > kPairCap && total <= kListCap && q.k) {
       few = keep_few(s, total, list_bound(s, total, q.k));
       list = s.few;
     }
@@ -626,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
       d = draw_pairs(s, list, few, q, M, c, S, u);
     } else {
       // from the list, or from the row when ties have made it overflow
-      const bool fits = total <= kListCap;
+      const bool fits = total <= kListCap && !left_out;
       auto entries = [&](auto f) {
         if (fits) {
           for (uint32_t i = tid; i < total; i += kThreads)

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
     if (key >= kKeyLowest) cut = fkey_inv(key);
     ready_others();
     h.template report<false>(s, kLog2e);
-    h.template gather<false>(s, cut, false, kTooMany - 1u, 0.f, 0.f);
+    h.template gather<false>(s, cut, false, 0.f, 0.f);
     if (rank != 0) return;  // its entries are with rank 0
   } else {
     ready_others();
@@ -75,14 +75,14 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   const unsigned long long* list = s.list;
   if ((alone || M > -INFINITY) && !late) {
     if (!alone) {
-      h.template gather<false>(s, s.cut, false, kTooMany - 1u, M, kLog2e);
+      h.template gather<false>(s, s.cut, false, 0.f, 0.f);
       if (rank != 0) return;
     }
     float none;
-    bool whole;
+    bool whole = true;
     late = !h.tallied(s, found, whole, none) || !h.listed(s, found);
     if (late) found = 0;
-    if (found > kListCap) {
+    if (found > kListCap || !whole) {
       uint32_t level = 0;
       unsigned long long above;
       // the n-th largest logit: a key whose upper set holds n tokens

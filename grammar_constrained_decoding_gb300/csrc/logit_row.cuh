@@ -40,7 +40,7 @@ constexpr uint32_t kMaxCluster = 16;   // more than 8 is not portable, but the o
 constexpr uint32_t kBinBits = 9;
 constexpr uint32_t kBins = 1u << kBinBits;  // bins of one selection level
 constexpr uint32_t kListCap = 1024;    // entries of a list
-constexpr uint32_t kWarpCap = 48;      // entries a warp sends for a guess
+constexpr uint32_t kStage = 512;       // entries a block sends
 constexpr uint32_t kPairCap = kThreads;  // lists ranked by comparing all pairs, an entry a thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxBf16 = 3.38953138925e38f;  // largest finite bf16
@@ -145,16 +145,20 @@ __device__ __forceinline__ void cluster_sync(uint32_t n) {
 constexpr uint32_t kMaxRecords = kMaxCluster * kWarps;  // warps of a cluster
 constexpr uint32_t kMaxBounds = 512;                     // group maxima a cluster exchanges
 
+// Exponentials are taken as exp2((x - m) c): the difference to a maximum first, which
+// is exact near it, so that no size of x or c costs precision or overflows.
+
 // What a warp tells all blocks about its part of the row: its maximum and its
 // sum of exp2((x - m) c).
 struct __align__(8) Record {
   float m, s;
 };
-// ... about the entries it has listed
+// What a block tells about the entries it has sent.
 struct __align__(8) Tally {
   float mass;
   uint32_t count;   // kTooMany: not sent
 };
+constexpr float kMassOne = 1099511627776.f;  // mass_q of the maximum
 constexpr uint32_t kTooMany = 0xFFFFFFFFu;
 constexpr uint32_t kChunk = 4;       // groups a thread takes at a time
 constexpr uint32_t kMaxChunks = 12;
@@ -175,14 +179,14 @@ struct __align__(16) Common {
     unsigned long long few[kPairCap];               // the list's entries that matter (rank 0)
     unsigned long long top[kMaxRecords];            // the best token of each warp
   };
-  Tally tally[kMaxRecords];
+  Tally tally[kMaxCluster];
   unsigned long long best[kMaxCluster];
   unsigned long long sums[kMaxCluster];
   unsigned long long red64[kWarps], red64b[kWarps];
   unsigned long long base;
   uint32_t red_max[kWarps];
   float red_f[kWarps];
-  uint32_t n_list, n_local, bin;
+  uint32_t n_list, n_local, n_stage, bin;
   float best_x[kMaxCluster];           // the logits of best[]
   __align__(8) float2 mass[kMaxRecords];            // per warp: mass above the drawn token, mass at or above the cut
 };
@@ -195,6 +199,7 @@ struct Shared : Common {
   };
   union {
     __align__(16) unsigned long long hist0[kBins];       // the other selection levels
+    __align__(16) unsigned long long stage[kStage];      // a block's entries on their way to rank 0
     struct {
       __align__(16) uint32_t keys[kPairCap];             // of the gathered entries
       uint32_t place[kPairCap];                          // entries above each
@@ -244,7 +249,7 @@ __device__ __forceinline__ void begin(Common& s) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (threadIdx.x == 32) {  // not the warp that issues the copies: the fence would wait for them
-    s.n_list = s.n_local = s.late = 0;
+    s.n_list = s.n_local = s.n_stage = s.late = 0;
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -279,6 +284,7 @@ struct Row {
   // Bit e: element e of group g is allowed by the bitmask.  t0 is the group's
   // first token; some token of the group is in the row.
   __device__ __forceinline__ uint32_t mask_bits(int t0) const {
+    if (a == 0) return uint32_t(mask[t0 >> 3]) >> (BF16 ? 0 : t0 & 4);
     if (t0 < 0) return uint32_t(mask[0]) << -t0;
     const uint32_t sh = uint32_t(t0) & 7u;
     uint32_t w = mask[t0 >> 3];
@@ -368,6 +374,25 @@ __device__ __forceinline__ float group_max_nan(const uint4& v) {
   }
   return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
                  max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+// maximum of kN groups, a (positive) NaN when one of them holds one
+template <bool BF16, int kN>
+__device__ __forceinline__ float groups_max_nan(const uint4* v) {
+  if (BF16) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(v);
+    __nv_bfloat162 r[4] = {h[0], h[1], h[2], h[3]};
+#pragma unroll
+    for (int i = 1; i < kN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[q] = __hmax2_nan(r[q], h[4 * i + q]);
+    r[0] = __hmax2_nan(__hmax2_nan(r[0], r[1]), __hmax2_nan(r[2], r[3]));
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&r[0]);
+    return max_nan(lo_f(u), hi_f(u));
+  }
+  float t = group_max_nan<BF16>(v[0]);
+#pragma unroll
+  for (int i = 1; i < kN; ++i) t = max_nan(t, group_max_nan<BF16>(v[i]));
+  return t;
 }
 // NaN -> -inf, +inf -> the largest finite value
 template <bool BF16>
@@ -507,25 +532,26 @@ struct Held {
       }
       ok = mbar_wait(s.bar_part + j0 / kChunk, 0) && ok;
       uint4 v[kChunk];
-      float t = -INFINITY;
 #pragma unroll
       for (uint32_t i = 0; i < kChunk; ++i) {
         v[i] = make_uint4(F::kNegInf, F::kNegInf, F::kNegInf, F::kNegInf);
         if (j0 + i < nv) v[i] = at(j0 + i);
-        if (r.mask) {
+      }
+      if (r.mask) {
+#pragma unroll
+        for (uint32_t i = 0; i < kChunk; ++i) {
           v[i] = r.masked(v[i], bits[i]);
           if (j0 + i < nv) part[(j0 + i) * kThreads + threadIdx.x] = v[i];
         }
-        t = max_nan(t, group_max_nan<BF16>(v[i]));
       }
+      float t = groups_max_nan<BF16, kChunk>(v);
       if (fkey(t) >= kKeyInf) {
-        t = -INFINITY;
 #pragma unroll
         for (uint32_t i = 0; i < kChunk; ++i) {
           v[i] = clean_group<BF16>(v[i]);
           if (j0 + i < nv) part[(j0 + i) * kThreads + threadIdx.x] = v[i];
-          t = fmaxf(t, group_max_nan<BF16>(v[i]));
         }
+        t = groups_max_nan<BF16, kChunk>(v);
       }
       if (t > tm) {
         if (SUM) {
@@ -536,13 +562,13 @@ struct Held {
       }
       if (SUM && tm > -INFINITY) {
         const float2 nm = make_float2(-tm, -tm);
-        float2 sum[4] = {};
+        float2 sum[2] = {};
 #pragma unroll
         for (uint32_t i = 0; i < kChunk; ++i)
 #pragma unroll
           for (uint32_t q = 0; q < F::E / 2; ++q)
-            sum[q] = __fadd2_rn(sum[q], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[i], q), nm), c2)));
-        acc = __fadd2_rn(acc, __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3])));
+            sum[q & 1u] = __fadd2_rn(sum[q & 1u], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[i], q), nm), c2)));
+        acc = __fadd2_rn(acc, __fadd2_rn(sum[0], sum[1]));
       }
     }
     ts = acc.x + acc.y;
@@ -632,43 +658,57 @@ struct Held {
     return c;
   }
   // Sends (logit, token) of every element >= cut to rank 0's list, completing on
-  // its bar_list, and then this warp's count and (MASS) its elements' mass in
-  // units of the maximum's to rank 0 or to every block (all), completing on
-  // bar_tally.  The list's count goes on past its capacity, the entries do not.
-  // Their order is arbitrary.  A warp with more than `most` entries sends none.
+  // its bar_list, and then the block's count and (MASS) its elements' mass in units
+  // of the maximum's to rank 0 or to every block (all), completing on bar_tally.
+  // The list's count goes on past its capacity, the entries do not.  Their order is
+  // arbitrary.  A block with more than kStage entries sends none.  The entries are
+  // staged in the block's own memory: one warp sends them, with one reservation.
   template <bool MASS>
-  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, uint32_t most, float M, float c) const {
+  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, float M, float c) const {
     const uint32_t lane = threadIdx.x & 31;
-    uint32_t found = 0;
+    if (tm >= cut) {
+      const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
+#pragma unroll 1
+      for (uint32_t j = 0; j < nv; ++j) {
+        const uint4 v = at(j);
+        uint32_t hits = ge_bits<BF16>(v, cut, cut2);
+        while (hits) {
+          const uint32_t e = __ffs(hits) - 1;
+          hits &= hits - 1;
+          const uint32_t place = atomicAdd(&s.n_stage, 1u);
+          if (place < kStage) s.stage[place] = pack_best(elem<BF16>(v, e), uint32_t(first_token(j)) + e);
+        }
+      }
+    }
+    __syncthreads();
+    const uint32_t found = s.n_stage;
+    const bool fits = found <= kStage;
+    if (MASS && !fits) {
+      const float mass = warp_reduce(masses_from(M, c, cut, cut).y, SumOp());
+      if (lane == 0) s.red_f[threadIdx.x >> 5] = mass;
+      __syncthreads();
+    }
+    if (threadIdx.x >= 32) return;
     float mass = 0.f;
-    if (__any_sync(0xFFFFFFFFu, tm >= cut)) {  // few warps, when little is wanted
-      const uint32_t mine = count(cut);
-      uint32_t inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= uint32_t(o)) inc += y;
+    if (fits && found) {
+      uint32_t place = 0;
+      if (lane == 0) place = add_remote(at_rank(&s.n_list, 0), found);
+      place = __shfl_sync(0xFFFFFFFFu, place, 0);
+      const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
+      unsigned long long units = 0;  // in integers: the order is arbitrary
+      for (uint32_t i = lane; i < found; i += 32) {
+        const unsigned long long e = s.stage[i];
+        if (place + i < kListCap) send(list + (place + i) * 8, e, bar);
+        if (MASS) units += mass_q(fkey_inv(uint32_t(e >> 32)), M, c);
       }
-      found = __shfl_sync(0xFFFFFFFFu, inc, 31);
-      if (found <= most) {
-        uint32_t place = 0;
-        if (lane == 31) place = add_remote(at_rank(&s.n_list, 0), inc);
-        place = __shfl_sync(0xFFFFFFFFu, place, 31) + inc - mine;
-        const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
-        each(cut, [&](uint32_t t, float x) {
-          if (place < kListCap) send(list + place * 8, pack_best(x, t), bar);
-          if (MASS) mass += ex2((x - M) * c);
-          ++place;
-        });
-      } else {
-        found = kTooMany;
-        if (MASS) mass = masses_from(M, c, cut, cut).y;
-      }
-      if (MASS) mass = warp_reduce(mass, SumOp());
+      if (MASS) mass = float(warp_reduce(units, SumOp())) * (1.f / kMassOne);
+    } else if (MASS && !fits) {
+      for (uint32_t w = 0; w < kWarps; ++w) mass += s.red_f[w];
     }
     if (lane < (all ? n : 1u))
-      send(at_rank(&s.tally[rank * kWarps + (threadIdx.x >> 5)], lane),
-           (static_cast<unsigned long long>(found) << 32) | __float_as_uint(mass), at_rank(&s.bar_tally, lane));
+      send(at_rank(&s.tally[rank], lane),
+           (static_cast<unsigned long long>(fits ? found : kTooMany) << 32) | __float_as_uint(mass),
+           at_rank(&s.bar_tally, lane));
   }
   // this thread's sums of exp2((x - M) c) over its elements > x, and over those >= y
   __device__ __forceinline__ float2 masses_from(float M, float c, float x, float y) const {
@@ -712,20 +752,18 @@ struct Held {
   // out.  The barrier's expectation is set here: early tallies wait in its
   // transaction count.
   __device__ __forceinline__ bool tallied(Shared& s, uint32_t& count, bool& whole, float& mass) const {
-    if (threadIdx.x == 0) mbar_expect_tx(&s.bar_tally, n * kWarps * uint32_t(sizeof(Tally)));
+    if (threadIdx.x == 0) mbar_expect_tx(&s.bar_tally, n * uint32_t(sizeof(Tally)));
     const bool ok = wait_sent(&s.bar_tally);
     mass = 0.f;
     count = 0;
     bool over = false;
-    for (uint32_t i = threadIdx.x & 31; i < n * kWarps; i += 32) {
+    for (uint32_t i = 0; i < n; ++i) {
       mass += s.tally[i].mass;
       const uint32_t k = s.tally[i].count;
       over |= k == kTooMany;
       count += k == kTooMany ? 0u : k;
     }
-    mass = warp_reduce(mass, SumOp());
-    count = __reduce_add_sync(0xFFFFFFFFu, count);
-    whole = !__any_sync(0xFFFFFFFFu, over);
+    whole = !over;
     return ok;
   }
   // Rank 0, after tallied(): the list's entries are there
