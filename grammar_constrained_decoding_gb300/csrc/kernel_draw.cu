@@ -400,9 +400,10 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   // the maximum; the tokens at or above the block's own bound of the k-th largest,
   // where the list holds those of all blocks; the best of all tokens.
   enum { kTogether, kBest, kTopK, kAny } alone = kTogether;
+  const uint32_t most = min(kListCap / n, kStage);
   if (!bad) {
     if (q.greedy) alone = kBest;
-    else if (q.k && q.k <= kThreads * 3 / 4 && n * (q.k + q.k / 4 + 16) <= kListCap) alone = kTopK;
+    else if (q.k && q.k <= kThreads * 3 / 4 && q.k + q.k / 4 + 16 <= most) alone = kTopK;
     else if (!q.k && q.p >= 1.f && !(mp > 0.f)) alone = kAny;
   }
   const uint32_t per_warp = q.k && !alone ? bounds_per_warp(q.k, n) : 0u;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     } else {
       h.template report<false>(s, c);
       if (alone == kTopK) {
-        h.template gather<false>(s, own_cut, false, 0.f, 0.f);
+        h.template gather<false, true>(s, own_cut, false, most, 0.f, 0.f);
       } else {
         // the block's best by scores relative to its own maximum: their order is
         // that of scores relative to the row's
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   bool left_out = false;  // a block had too many entries to send
   if (mode == kGather) {
     if (!alone) {
-      h.template gather<false>(s, cut, false, 0.f, 0.f);
+      h.template gather<false, false>(s, cut, false, kStage, 0.f, 0.f);
       if (rank != 0) return;  // its entries are with rank 0
     }
     float none;
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     else if (!whole) left_out = true;
   } else if (mode == kGuessFirst) {
     list_cut = fmaxf(cut, M - fmaxf(s.guess - kGuess, 0.f) * q.T);
-    h.template gather<true>(s, list_cut, true, M, c);
+    h.template gather<true, false>(s, list_cut, true, kStage, M, c);
     float mass;
     bool whole;
     const bool ok = h.tallied(s, total, whole, mass);
@@ -618,11 +619,15 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   const bool gather = mode == kGather;
   if (gather) {
     const unsigned long long* list = s.list;
-    uint32_t few = total;
+    uint32_t few = total, span = total;
     if (left_out) {
       few = kListCap + 1;
-    } else if (total > kPairCap && total <= kListCap && q.k) {
-      few = keep_few(s, total, list_bound(s, total, q.k));
+    } else if (total <= kListCap && (alone || (total > kPairCap && q.k))) {
+      if (alone) {
+        h.zero_rest(s, most);
+        span = n * most;
+      }
+      few = keep_few(s, span, total > kPairCap ? list_bound(s, span, total, q.k) : 1u);
       list = s.few;
     }
     if (few <= kPairCap) {
@@ -632,8 +637,8 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
       const bool fits = total <= kListCap && !left_out;
       auto entries = [&](auto f) {
         if (fits) {
-          for (uint32_t i = tid; i < total; i += kThreads)
-            f(best_id(s.list[i]), fkey_inv(uint32_t(s.list[i] >> 32)));
+          for (uint32_t i = tid; i < span; i += kThreads)
+            if (s.list[i]) f(best_id(s.list[i]), fkey_inv(uint32_t(s.list[i] >> 32)));
         } else {
           each_of_row(h.r, f);
         }

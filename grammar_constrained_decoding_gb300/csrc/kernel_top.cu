@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   // Alone each block can only bound the n-th largest of its own part.  Where the
   // entries of all parts fit the list they are sent without waiting for the others;
   // else the bound comes from the whole row's group maxima.
-  const bool alone = a.n <= kThreads * 3 / 4 && n * (a.n + a.n / 4 + 16) <= kListCap;
+  const uint32_t most = min(kListCap / n, kStage);
+  const bool alone = a.n <= kThreads * 3 / 4 && a.n + a.n / 4 + 16 <= most;
   const uint32_t per_warp = alone ? 0u : bounds_per_warp(a.n, n);
   float cut = -FLT_MAX;
   if (alone) {
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
     if (key >= kKeyLowest) cut = fkey_inv(key);
     ready_others();
     h.template report<false>(s, kLog2e);
-    h.template gather<false>(s, cut, false, 0.f, 0.f);
+    h.template gather<false, true>(s, cut, false, most, 0.f, 0.f);
     if (rank != 0) return;  // its entries are with rank 0
   } else {
     ready_others();
@@ -73,9 +74,10 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   uint32_t found = 0;
   bool late = s.late != 0;
   const unsigned long long* list = s.list;
+  uint32_t span = 0;  // of the list, zeros included, when it is longer than what was found
   if ((alone || M > -INFINITY) && !late) {
     if (!alone) {
-      h.template gather<false>(s, s.cut, false, 0.f, 0.f);
+      h.template gather<false, false>(s, s.cut, false, kStage, 0.f, 0.f);
       if (rank != 0) return;
     }
     float none;
@@ -105,11 +107,15 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
       });
       __syncthreads();
       found = s.n_list;
-    } else if (found > kPairCap) {
-      const uint32_t few = keep_few(s, found, list_bound(s, found, a.n));
-      if (few <= kPairCap) {
-        found = few;
-        list = s.few;
+    } else {
+      if (alone) h.zero_rest(s, most);
+      if (alone || found > kPairCap) {
+        span = alone ? n * most : found;
+        const uint32_t key = found > kPairCap ? list_bound(s, span, found, a.n) : 1u, few = keep_few(s, span, key);
+        if (few <= kPairCap) {
+          found = few;
+          list = s.few;
+        }
       }
     }
   } else if (rank != 0) {
@@ -127,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
     place_entries<true>(s, list, found);
     if (tid < found && s.place[tid] < a.n) write(s.place[tid], list[tid]);
   } else {
-    sort_desc(s.list, found);
+    sort_desc(s.list, max(found, span));
     for (uint32_t i = tid; i < min(found, a.n); i += kThreads) write(i, s.list[i]);
   }
   for (uint32_t i = found + tid; i < a.n; i += kThreads) {

@@ -161,9 +161,9 @@ struct __align__(8) Tally {
 constexpr float kMassOne = 1099511627776.f;  // mass_q of the maximum
 constexpr uint32_t kTooMany = 0xFFFFFFFFu;
 constexpr uint32_t kChunk = 4;       // groups a thread takes at a time
-constexpr uint32_t kMaxChunks = 12;
+constexpr uint32_t kMaxChunks = 8;
 constexpr uint32_t kBars = 5 + kMaxChunks;
-constexpr uint32_t kMaxGroups = kChunk * kMaxChunks;  // of a thread
+constexpr uint32_t kMaxGroups = kChunk * kMaxChunks;  // of a thread: a lane a copy
 
 // Reductions and exchange
 struct __align__(16) Common {
@@ -446,17 +446,21 @@ __device__ __forceinline__ uint32_t bound_key(const Common& s, uint32_t count, u
   lo = __reduce_min_sync(0xFFFFFFFFu, lo);
   hi = __reduce_max_sync(0xFFFFFFFFu, hi) + 1u;  // fewer than k reach hi, all reach lo
 #pragma unroll 1
-  while (hi - lo > 0x10000u) {  // 1/128 of an octave
-    const uint32_t mid = lo + (hi - lo) / 2;
+  while (hi - lo > 0x10000u) {  // 1/128 of an octave; three pivots a round, counted in 10 bits each
+    const uint32_t q = (hi - lo) / 4, p1 = lo + q, p2 = p1 + q, p3 = p2 + q;
     uint32_t reach = 0;
 #pragma unroll
     for (uint32_t i = 0; i < kMaxBounds / 32; i += 4)
       if (i < each) {
 #pragma unroll
-        for (uint32_t q = 0; q < 4; ++q) reach += v[i + q] >= mid;
+        for (uint32_t w = 0; w < 4; ++w)
+          reach += (v[i + w] >= p1 ? 1u : 0u) + (v[i + w] >= p2 ? 1u << 10 : 0u) + (v[i + w] >= p3 ? 1u << 20 : 0u);
       }
-    if (__reduce_add_sync(0xFFFFFFFFu, reach) >= k) lo = mid;
-    else hi = mid;
+    reach = __reduce_add_sync(0xFFFFFFFFu, reach);
+    if ((reach >> 20) >= k) lo = p3;
+    else if (((reach >> 10) & 1023u) >= k) lo = p2, hi = p3;
+    else if ((reach & 1023u) >= k) lo = p1, hi = p2;
+    else hi = p1;
   }
   return lo;
 }
@@ -480,28 +484,20 @@ struct Held {
   __device__ __forceinline__ int first_token(uint32_t j) const { return int(group(j) * F::E) - int(r.a); }
   __device__ __forceinline__ uint4 at(uint32_t j) const { return part[j * kThreads + threadIdx.x]; }
 
-  // Starts the copies, a lane a run of kThreads groups; the groups that they do not
-  // bring are written by their threads.
+  // Starts the copies, a lane a run of kThreads groups (kMaxGroups lanes, kChunk
+  // neighbours a barrier); the groups that they do not bring are written by their
+  // threads.
   __device__ __forceinline__ void start(Common& s) const {
     const uint32_t lo = r.first_whole(), hi = r.end_whole();
     if (threadIdx.x < 32) {
-      auto run = [&](uint32_t j, uint32_t& from) {  // groups to copy of run j
-        const uint32_t g0 = (j * n + rank) * kThreads, to = min(g0 + kThreads, hi);
-        from = max(g0, lo);
-        return to > from ? to - from : 0u;
-      };
-      for (uint32_t j = threadIdx.x; j < nv; j += 32) {
-        uint32_t from;
-        const uint32_t k = run(j, from);
-        if (k)
-          bulk_g2s(part + j * kThreads + (from - (j * n + rank) * kThreads), r.base + size_t(from) * 16, k * 16u,
-                   s.bar_part + j / kChunk);
-      }
-      for (uint32_t q = threadIdx.x; q * kChunk < nv; q += 32) {  // what has arrived by now counts against this
-        uint32_t from, bytes = 0;
-        for (uint32_t j = q * kChunk; j < min(nv, (q + 1) * kChunk); ++j) bytes += run(j, from) * 16u;
-        mbar_expect_tx(s.bar_part + q, bytes);
-      }
+      const uint32_t j = threadIdx.x, g0 = (j * n + rank) * kThreads, from = max(g0, lo), to = min(g0 + kThreads, hi);
+      uint32_t bytes = j < nv && to > from ? (to - from) * 16u : 0u;
+      if (bytes)
+        bulk_g2s(part + j * kThreads + (from - g0), r.base + size_t(from) * 16, bytes, s.bar_part + j / kChunk);
+      bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, 1);
+      bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, 2);
+      // what has arrived by now counts against this
+      if (j % kChunk == 0 && j < nv) mbar_expect_tx(s.bar_part + j / kChunk, bytes);
     }
     // groups before lo or from hi on: at most one each side in the row
     const uint32_t run = group(0) - threadIdx.x;
@@ -661,28 +657,39 @@ struct Held {
   // its bar_list, and then the block's count and (MASS) its elements' mass in units
   // of the maximum's to rank 0 or to every block (all), completing on bar_tally.
   // The list's count goes on past its capacity, the entries do not.  Their order is
-  // arbitrary.  A block with more than kStage entries sends none.  The entries are
-  // staged in the block's own memory: one warp sends them, with one reservation.
-  template <bool MASS>
-  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, float M, float c) const {
+  // arbitrary.  A block with more than `most` <= kStage entries sends none.  The
+  // entries are staged in the block's own memory: one warp sends them, to a place
+  // reserved at rank 0 (a round trip) or, with REGION, to the block's own share of
+  // the list, `most` entries at rank * most.
+  template <bool MASS, bool REGION>
+  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, uint32_t most, float M, float c) const {
     const uint32_t lane = threadIdx.x & 31;
     if (tm >= cut) {
       const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
 #pragma unroll 1
-      for (uint32_t j = 0; j < nv; ++j) {
-        const uint4 v = at(j);
-        uint32_t hits = ge_bits<BF16>(v, cut, cut2);
-        while (hits) {
-          const uint32_t e = __ffs(hits) - 1;
-          hits &= hits - 1;
-          const uint32_t place = atomicAdd(&s.n_stage, 1u);
-          if (place < kStage) s.stage[place] = pack_best(elem<BF16>(v, e), uint32_t(first_token(j)) + e);
+      for (uint32_t j0 = 0; j0 < nv; j0 += kChunk) {
+        uint32_t with = 0;  // groups of the chunk that hold some
+#pragma unroll
+        for (uint32_t i = 0; i < kChunk; ++i)
+          if (j0 + i < nv && group_max_nan<BF16>(at(j0 + i)) >= cut) with |= 1u << i;
+        while (with) {
+          const uint32_t j = j0 + __ffs(with) - 1;
+          with &= with - 1;
+          const uint4 v = at(j);
+          uint32_t hits = ge_bits<BF16>(v, cut, cut2);
+          uint32_t place = atomicAdd(&s.n_stage, uint32_t(__popc(hits)));
+          while (hits) {
+            const uint32_t e = __ffs(hits) - 1;
+            hits &= hits - 1;
+            if (place < most) s.stage[place] = pack_best(elem<BF16>(v, e), uint32_t(first_token(j)) + e);
+            ++place;
+          }
         }
       }
     }
     __syncthreads();
     const uint32_t found = s.n_stage;
-    const bool fits = found <= kStage;
+    const bool fits = found <= most;
     if (MASS && !fits) {
       const float mass = warp_reduce(masses_from(M, c, cut, cut).y, SumOp());
       if (lane == 0) s.red_f[threadIdx.x >> 5] = mass;
@@ -691,9 +698,11 @@ struct Held {
     if (threadIdx.x >= 32) return;
     float mass = 0.f;
     if (fits && found) {
-      uint32_t place = 0;
-      if (lane == 0) place = add_remote(at_rank(&s.n_list, 0), found);
-      place = __shfl_sync(0xFFFFFFFFu, place, 0);
+      uint32_t place = rank * most;
+      if (!REGION) {
+        if (lane == 0) place = add_remote(at_rank(&s.n_list, 0), found);
+        place = __shfl_sync(0xFFFFFFFFu, place, 0);
+      }
       const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
       unsigned long long units = 0;  // in integers: the order is arbitrary
       for (uint32_t i = lane; i < found; i += 32) {
@@ -770,6 +779,15 @@ struct Held {
   __device__ __forceinline__ bool listed(Shared& s, uint32_t count) const {
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_list, min(count, kListCap) * 8u);
     return wait_sent(&s.bar_list);
+  }
+  // ... of a gather by region: the empty places of the regions read as zeros (after a
+  // barrier), which are below every entry
+  __device__ __forceinline__ void zero_rest(Shared& s, uint32_t most) const {
+    for (uint32_t i = threadIdx.x; i < n * most; i += kThreads) {
+      const uint32_t k = s.tally[i / most].count;
+      if (i % most >= (k == kTooMany ? 0u : k)) s.list[i] = 0ull;
+    }
+    __syncthreads();
   }
 };
 
@@ -902,7 +920,7 @@ __device__ __forceinline__ void place_entries(Shared& s, const unsigned long lon
   __syncthreads();
 }
 
-// Copies the entries of s.list[0 .. c) whose key is at least `key` to s.few; returns
+// Copies the entries of s.list[0 .. c) whose key is at least `key` > 0 to s.few; returns
 // their number (none are copied past kPairCap).  Ends with a barrier.
 __device__ __forceinline__ uint32_t keep_few(Shared& s, uint32_t c, uint32_t key) {
   __syncthreads();
@@ -917,18 +935,19 @@ __device__ __forceinline__ uint32_t keep_few(Shared& s, uint32_t c, uint32_t key
   __syncthreads();
   return s.n_local;
 }
-// A key that at least k of s.list[0 .. c), c <= kListCap, reach, and few more: by
-// bisection, the block counting together
-__device__ __forceinline__ uint32_t list_bound(Shared& s, uint32_t c, uint32_t k) {
+// A key that at least k of the entries of s.list[0 .. c), c <= kListCap, reach, and few
+// more: by bisection, the block counting together.  1 when there are not more than
+// k (of `total`; zeros are no entries).
+__device__ __forceinline__ uint32_t list_bound(Shared& s, uint32_t c, uint32_t total, uint32_t k) {
   constexpr uint32_t kOwn = kListCap / kThreads;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (c <= k) return 0u;
+  if (total <= k) return 1u;
   uint32_t v[kOwn], lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
   for (uint32_t i = 0; i < kOwn; ++i) {
     const uint32_t at = i * kThreads + tid;
     v[i] = at < c ? uint32_t(s.list[at] >> 32) : 0u;
-    if (at < c) {
+    if (v[i]) {
       lo = min(lo, v[i]);
       hi = max(hi, v[i]);
     }
@@ -936,21 +955,30 @@ __device__ __forceinline__ uint32_t list_bound(Shared& s, uint32_t c, uint32_t k
   lo = ~block_max(~lo, s.red_max);
   __syncthreads();
   hi = block_max(hi, s.red_max) + 1u;
-  for (uint32_t round = 0; hi - lo > 0x4000u; ++round) {  // a barrier a round: two sets of counters
-    const uint32_t mid = lo + (hi - lo) / 2;
+  for (uint32_t round = 0; hi - lo > 0x4000u; ++round) {  // three pivots and a barrier a round: two sets of counters
+    const uint32_t q = (hi - lo) / 4, p1 = lo + q, p2 = p1 + q, p3 = p2 + q;
     uint32_t reach = 0;
 #pragma unroll
-    for (uint32_t i = 0; i < kOwn; ++i) reach += v[i] >= mid;
+    for (uint32_t i = 0; i < kOwn; ++i)
+      reach += (v[i] >= p1 ? 1u : 0u) + (v[i] >= p2 ? 1u << 10 : 0u) + (v[i] >= p3 ? 1u << 20 : 0u);
     reach = __reduce_add_sync(0xFFFFFFFFu, reach);
     uint32_t* sum = reinterpret_cast<uint32_t*>(round & 1u ? s.red64 : s.red64b);
     if (lane == 0) sum[warp] = reach;
     __syncthreads();
-    reach = 0;
+    uint32_t r1 = 0, r2 = 0, r3 = 0;
 #pragma unroll
-    for (uint32_t w = 0; w < kWarps; ++w) reach += sum[w];
-    if (reach >= k) lo = mid;
-    else hi = mid;
-    if (reach == k) break;
+    for (uint32_t w = 0; w < kWarps; ++w) {
+      const uint32_t t = sum[w];
+      r1 += t & 1023u;
+      r2 += (t >> 10) & 1023u;
+      r3 += t >> 20;
+    }
+    uint32_t got;
+    if (r3 >= k) lo = p3, got = r3;
+    else if (r2 >= k) lo = p2, hi = p3, got = r2;
+    else if (r1 >= k) lo = p1, hi = p2, got = r1;
+    else hi = p1, got = 0;
+    if (got == k) break;
   }
   return lo;
 }
