@@ -15,6 +15,9 @@ namespace {
 
 using namespace row;
 
+// groups of a thread for many rows (as the sampling kernel)
+constexpr uint32_t kFull = 8;
+
 struct TopArgs {
   const void* logits;
   uint64_t ld;
@@ -42,8 +45,8 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   // Alone each block can only bound the n-th largest of its own part.  Where the
   // entries of all parts fit the list they are sent without waiting for the others;
   // else the bound comes from the whole row's group maxima.
-  const uint32_t most = min(kListCap / n, kStage);
-  const bool alone = a.n <= kThreads * 3 / 4 && a.n + a.n / 4 + 16 <= most;
+  const uint32_t most = share_of(n);
+  const bool alone = fits_share(a.n, n);
   const uint32_t per_warp = alone ? 0u : bounds_per_warp(a.n, n);
   float cut = -FLT_MAX;
   if (alone) {
@@ -77,7 +80,17 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   uint32_t span = 0;  // of the list, zeros included, when it is longer than what was found
   if ((alone || M > -INFINITY) && !late) {
     if (!alone) {
-      h.template gather<false, false>(s, s.cut, false, kStage, 0.f, 0.f);
+      float from = s.cut;
+      if (per_warp == 0 && h.r.V > kStage) {  // no bound: the n-th largest itself, and its ties
+        uint32_t level = 0;
+        unsigned long long above;
+        const uint32_t key = select_key(
+            s, n, [&](auto f) { h.each(-FLT_MAX, [&](uint32_t, float x) { f(fkey(x), 1ull); }); }, kKeyLowest, fkey(M),
+            a.n, level, above);
+        from = fkey_inv(key);
+        cluster_sync(n);  // everybody has read the histograms: the list and the stage take their place
+      }
+      h.template gather<false, false>(s, from, false, kStage, 0.f, 0.f);
       if (rank != 0) return;
     }
     float none;
@@ -145,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
 
 template <bool BF16>
 cudaError_t launch_top(int device, uint32_t B, const TopArgs& a, cudaStream_t stream) {
-  const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld));
+  const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
   return launch_clusters<top_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + size_t(plan.nv) * kThreads * 16, stream,
                                            a, plan.nv);
 }

@@ -148,6 +148,18 @@ constexpr uint32_t kMaxBounds = 512;                     // group maxima a clust
 // Exponentials are taken as exp2((x - m) c): the difference to a maximum first, which
 // is exact near it, so that no size of x or c costs precision or overflows.
 
+// Entries a block may send without knowing of the others' (its share of the list),
+// and whether its k-th bound may be its own: there is room for the tokens at or above
+// it, about k + k^2 / 512, and rank 0 gets entries of four to eight blocks.  With
+// fewer blocks rank 0 is too large a part of the work to be given the longer list
+// (64 best of 2048 x 32000: 97 us instead of 71), with more the list is too long (20
+// best of 8 x 128256: 7.8 us instead of 6.3); between them the saved exchange pays
+// (top-k 50 of 256 x 128256: 39.9 us instead of 42.5).
+__device__ __forceinline__ uint32_t share_of(uint32_t n) { return min(kListCap / n, kStage); }
+__device__ __forceinline__ bool fits_share(uint32_t k, uint32_t n) {
+  return n >= 4 && n <= 8 && k <= kThreads * 3 / 4 && k + k / 4 + 16 <= share_of(n);
+}
+
 // What a warp tells all blocks about its part of the row: its maximum and its
 // sum of exp2((x - m) c).
 struct __align__(8) Record {
@@ -1008,16 +1020,15 @@ __device__ inline void sort_desc(unsigned long long* list, uint32_t n) {
 
 // The cluster size of a launch and the groups of a thread.  Few rows take the widest
 // cluster whose blocks are all resident together, so that a row is split over more
-// SMs; many rows take parts of kFull groups a thread (32 KB), four blocks an SM.
+// SMs; many rows take parts of `full` groups a thread.
 struct Plan {
   uint32_t nv, n;
 };
 constexpr uint32_t kSlots = 4 * 152;  // blocks resident together
-constexpr uint32_t kFull = 8;
-inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned) {
+inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned, uint32_t full) {
   const uint32_t E = bf16 ? 8 : 4;
   const uint32_t runs = ((V + (aligned ? 0 : E - 1) + E - 1) / E + kThreads - 1) / kThreads;  // of kThreads groups
-  uint32_t n = (runs + kFull - 1) / kFull;
+  uint32_t n = (runs + full - 1) / full;
   if (n > kMaxCluster) n = kMaxCluster;
   while (n < kMaxCluster && n < runs && uint64_t(B) * (n + 1) <= kSlots) ++n;
   return {(runs + n - 1) / n, n};
