@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x, K = a.K;
   begin(s);
   Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, 
-               reinterpret_cast<uint4*>(smem + sizeof(DistillShared) + List::bytes(K)));
+               smem + sizeof(DistillShared) + List::bytes(K));
   griddep_wait();
   h.start(s);
   may_send();
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
 template <bool BF16>
 cudaError_t launch_distill(int device, uint32_t B, const DistillArgs& a, bool loss, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
-  const size_t smem = sizeof(DistillShared) + List::bytes(a.K) + size_t(plan.nv) * kThreads * 16;
+  const size_t smem = sizeof(DistillShared) + List::bytes(a.K) + part_bytes(BF16, plan.nv, a.bitmask);
   return loss ? launch_clusters<distill_kernel<BF16, true>>(device, B, plan.n, smem, stream, a, plan.nv)
               : launch_clusters<distill_kernel<BF16, false>>(device, B, plan.n, smem, stream, a, plan.nv);
 }

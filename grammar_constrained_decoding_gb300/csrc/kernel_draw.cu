@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
   begin(s);
-  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, reinterpret_cast<uint4*>(smem + sizeof(Shared)));
+  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, smem + sizeof(Shared));
   griddep_wait();
   h.start(s);
   may_send();
@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     else if (q.k && fits_share(q.k, n)) alone = kTopK;
     else if (!q.k && q.p >= 1.f && !(mp > 0.f)) alone = kAny;
   }
-  const uint32_t per_warp = q.k && !alone ? bounds_per_warp(q.k, n) : 0u;
+  bool tight = true;
+  const uint32_t per_warp = q.k && !alone ? bounds_per_warp(q.k, n, tight) : 0u;
   const bool taken = h.template take<true>(s, c);
   if (!taken) s.late = 1;
   if (alone) {
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     } else if (q.k) {
       const uint32_t key = per_warp ? bound_key(s, n * kWarps * per_warp, q.k) : 0u;
       if (key >= kKeyLowest) cut = fkey_inv(key);
-      if (per_warp || alone) mode = kGather;
+      if (tight) mode = kGather;
     } else if (!alone) {
       // a little below M + T log(min_p), for the roundings
       if (floor_z > -INFINITY) {
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
 template <bool BF16>
 cudaError_t launch_draw(int device, uint32_t B, const DrawArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
-  return launch_clusters<draw_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + size_t(plan.nv) * kThreads * 16, stream,
+  return launch_clusters<draw_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
                                             a, plan.nv);
 }
 

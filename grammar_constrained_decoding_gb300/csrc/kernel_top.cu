@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x;
   begin(s);
-  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, reinterpret_cast<uint4*>(smem + sizeof(Shared)));
+  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, smem + sizeof(Shared));
   griddep_wait();
   h.start(s);
   may_send();
@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   // else the bound comes from the whole row's group maxima.
   const uint32_t most = share_of(n);
   const bool alone = fits_share(a.n, n);
-  const uint32_t per_warp = alone ? 0u : bounds_per_warp(a.n, n);
+  bool tight = true;
+  const uint32_t per_warp = alone ? 0u : bounds_per_warp(a.n, n, tight);
   float cut = -FLT_MAX;
   if (alone) {
     const uint32_t key = h.own_bound(s, a.n);
@@ -81,11 +82,11 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   if ((alone || M > -INFINITY) && !late) {
     if (!alone) {
       float from = s.cut;
-      if (per_warp == 0 && h.r.V > kStage) {  // no bound: the n-th largest itself, and its ties
+      if (!tight && h.r.V > kStage) {  // a bound too low: the n-th largest itself, and its ties
         uint32_t level = 0;
         unsigned long long above;
         const uint32_t key = select_key(
-            s, n, [&](auto f) { h.each(-FLT_MAX, [&](uint32_t, float x) { f(fkey(x), 1ull); }); }, kKeyLowest, fkey(M),
+            s, n, [&](auto f) { h.each(from, [&](uint32_t, float x) { f(fkey(x), 1ull); }); }, fkey(from), fkey(M),
             a.n, level, above);
         from = fkey_inv(key);
         cluster_sync(n);  // everybody has read the histograms: the list and the stage take their place
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
 template <bool BF16>
 cudaError_t launch_top(int device, uint32_t B, const TopArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
-  return launch_clusters<top_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + size_t(plan.nv) * kThreads * 16, stream,
+  return launch_clusters<top_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
                                            a, plan.nv);
 }
 

@@ -282,16 +282,17 @@ struct Row {
   using F = Fmt<BF16>;
   const char* base;      // the row's start rounded down to 16 bytes
   uint32_t a;            // elements between base and the row's start
-  uint32_t V;
+  uint32_t V, W;
   const uint8_t* mask;   // the row's bitmask or null
 
-  __device__ __forceinline__ Row(const void* logits, uint64_t ld, const uint32_t* bitmask, uint32_t W, uint32_t V_,
+  __device__ __forceinline__ Row(const void* logits, uint64_t ld, const uint32_t* bitmask, uint32_t W_, uint32_t V_,
                                  uint32_t b) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(logits) + size_t(b) * ld * F::kSize;
     base = reinterpret_cast<const char*>(p & ~uintptr_t(15));
     a = uint32_t(p & 15u) / F::kSize;
     V = V_;
-    mask = bitmask ? reinterpret_cast<const uint8_t*>(bitmask + size_t(b) * W) : nullptr;
+    W = W_;
+    mask = bitmask ? reinterpret_cast<const uint8_t*>(bitmask + size_t(b) * W_) : nullptr;
   }
   // Bit e: element e of group g is allowed by the bitmask.  t0 is the group's
   // first token; some token of the group is in the row.
@@ -485,11 +486,17 @@ struct Held {
   uint32_t n, rank;   // cluster size, this block
   uint32_t nv;        // groups of a thread
   uint4* part;        // group j of thread t at [j * kThreads + t]
+  const uint8_t* bits;  // the part's mask, kMaskRun bytes a run, where it can be copied; else null
   float tm;           // this thread's maximum
   float ts;           // its sum of exp2((x - tm) c)
 
-  __device__ __forceinline__ Held(const Row<BF16>& row, uint32_t nv_, uint4* part_)
-      : r(row), n(cluster_size()), rank(cluster_rank()), nv(nv_), part(part_) {}
+  static constexpr uint32_t kMaskRun = kThreads * F::E / 8;
+  __device__ __forceinline__ Held(const Row<BF16>& row, uint32_t nv_, void* memory)
+      : r(row), n(cluster_size()), rank(cluster_rank()), nv(nv_), part(static_cast<uint4*>(memory)) {
+    // on the 16-byte grid, whole 16-byte pieces to a row, groups whole bytes or halves
+    const bool copied = r.mask && r.a == 0 && ((reinterpret_cast<uintptr_t>(r.mask) | (r.W * 4u)) & 15u) == 0;
+    bits = copied ? reinterpret_cast<const uint8_t*>(part + nv * kThreads) : nullptr;
+  }
   // group j of this thread: consecutive threads hold consecutive groups, the
   // blocks take turns at runs of kThreads
   __device__ __forceinline__ uint32_t group(uint32_t j) const { return (j * n + rank) * kThreads + threadIdx.x; }
@@ -506,6 +513,12 @@ struct Held {
       uint32_t bytes = j < nv && to > from ? (to - from) * 16u : 0u;
       if (bytes)
         bulk_g2s(part + j * kThreads + (from - g0), r.base + size_t(from) * 16, bytes, s.bar_part + j / kChunk);
+      if (bits && j < nv) {
+        const uint32_t off = (j * n + rank) * kMaskRun, end = r.W * 4u;
+        const uint32_t k = off < end ? min(kMaskRun, end - off) : 0u;
+        if (k) bulk_g2s(const_cast<uint8_t*>(bits) + j * kMaskRun, r.mask + off, k, s.bar_part + j / kChunk);
+        bytes += k;
+      }
       bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, 1);
       bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, 2);
       // what has arrived by now counts against this
@@ -532,11 +545,11 @@ struct Held {
     const float2 c2 = make_float2(c, c);
 #pragma unroll 1
     for (uint32_t j0 = 0; j0 < nv; j0 += kChunk) {
-      uint32_t bits[kChunk];
-      if (r.mask) {
+      uint32_t allowed[kChunk];
+      if (r.mask && !bits) {
 #pragma unroll
         for (uint32_t i = 0; i < kChunk; ++i)
-          bits[i] = j0 + i < nv && r.in_row(group(j0 + i)) ? r.mask_bits(first_token(j0 + i)) : 0u;
+          allowed[i] = j0 + i < nv && r.in_row(group(j0 + i)) ? r.mask_bits(first_token(j0 + i)) : 0u;
       }
       ok = mbar_wait(s.bar_part + j0 / kChunk, 0) && ok;
       uint4 v[kChunk];
@@ -546,9 +559,15 @@ struct Held {
         if (j0 + i < nv) v[i] = at(j0 + i);
       }
       if (r.mask) {
+        if (bits) {  // groups outside the row are -inf whatever their bits
+          const uint8_t* p = bits + j0 * kMaskRun + (BF16 ? threadIdx.x : threadIdx.x / 2);
+#pragma unroll
+          for (uint32_t i = 0; i < kChunk; ++i)
+            allowed[i] = j0 + i < nv ? uint32_t(p[i * kMaskRun]) >> (BF16 ? 0u : (threadIdx.x & 1u) * 4u) : 0u;
+        }
 #pragma unroll
         for (uint32_t i = 0; i < kChunk; ++i) {
-          v[i] = r.masked(v[i], bits[i]);
+          v[i] = r.masked(v[i], allowed[i]);
           if (j0 + i < nv) part[(j0 + i) * kThreads + threadIdx.x] = v[i];
         }
       }
@@ -816,16 +835,22 @@ __device__ __forceinline__ void merge(const Common& s, uint32_t n, float c, floa
   S = warp_reduce(t, SumOp());
 }
 
-// Groups of lanes per warp whose maxima bound the k-th largest logit: somewhat
-// more groups than k over the cluster; 0 when k is too large for that.  More
-// groups make the bound tighter (with P groups of random logits about
-// -P log(1 - k / P) tokens lie at or above it) and the exchange longer.
-__device__ __forceinline__ uint32_t bounds_per_warp(uint32_t k, uint32_t n) {
+// Groups of lanes per warp whose maxima bound the k-th largest logit: the least power
+// of two that gives the cluster a third more groups than k (with P groups of random
+// logits about -P log(1 - k / P) tokens lie at or above the bound), else as many as
+// there are when those are k at least (tight is false then), else 0.
+__device__ __forceinline__ uint32_t bounds_per_warp(uint32_t k, uint32_t n, bool& tight) {
   const uint32_t warps = n * kWarps;
-  for (uint32_t g = 1; g <= 32u && warps * g <= kMaxBounds; g <<= 1)
+  uint32_t most = 0;
+  tight = true;
+  for (uint32_t g = 1; g <= 32u && warps * g <= kMaxBounds; g <<= 1) {
     if (4 * k <= 3 * warps * g) return g;
-  return 0;
+    most = g;
+  }
+  tight = false;
+  return k <= warps * most ? most : 0u;
 }
+
 // Largest key k in [lo, hi] whose upper set {key >= k}, over the whole row,
 // carries at least `target` of the weights that each(f) reports for this block's
 // part through f(key, weight); lo when none does.  Radix selection: up to kBins
@@ -1017,6 +1042,11 @@ __device__ inline void sort_desc(unsigned long long* list, uint32_t n) {
 }
 
 // ---- launching -----------------------------------------------------------------------
+
+// Shared memory of a block's part: its groups and, with a bitmask, their bits
+inline size_t part_bytes(bool bf16, uint32_t nv, bool mask) {
+  return size_t(nv) * kThreads * 16 + (mask ? size_t(nv) * kThreads / (bf16 ? 1 : 2) : 0);
+}
 
 // The cluster size of a launch and the groups of a thread.  Few rows take the widest
 // cluster whose blocks are all resident together, so that a row is split over more
