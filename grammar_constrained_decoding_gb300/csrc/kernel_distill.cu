@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
   Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, 
                smem + sizeof(DistillShared) + List::bytes(K));
   griddep_wait();
-  h.start(s);
+  h.start(s, !a.grad);
   may_send();
   const float T = a.temp, c = exp_scale(T);
   // the teacher's list (without a gradient only rank 0 has a use for it)

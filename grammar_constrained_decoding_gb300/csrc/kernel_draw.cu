@@ -214,6 +214,10 @@ __device__ Drawn draw_screened(Shared& s, const Held<BF16>& h, const RowSettings
       ub[2 * p + 1] = x.y >= low ? z.y - l1 : -INFINITY;
     }
   };
+  if (threadIdx.x < h.nv) {  // the random numbers of a run are one piece: all on their way to L2 at once
+    const int t = int((threadIdx.x * h.n + h.rank) * kThreads * E) - int(h.r.a), V = int(h.r.V);
+    if (t < V) prefetch_l2(u + max(t, 0), u + min(t + int(kThreads * E), V));
+  }
   float first = -INFINITY, second = -INFINITY;
   uint32_t at = 0;
 #pragma unroll 2
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   begin(s);
   Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, smem + sizeof(Shared));
   griddep_wait();
-  h.start(s);
+  h.start(s, true);
   may_send();
   RowSettings q;
   q.T = a.temp ? a.temp[b] : 1.f;

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   begin(s);
   Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, smem + sizeof(Shared));
   griddep_wait();
-  h.start(s);
+  h.start(s, true);
   may_send();
   if (!h.template take<true>(s, kLog2e)) s.late = 1;
   // Alone each block can only bound the n-th largest of its own part.  Where the

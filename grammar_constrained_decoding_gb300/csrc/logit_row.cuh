@@ -97,6 +97,11 @@ __device__ __forceinline__ void send(uint32_t a, uint4 v, uint32_t bar) {
                "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
                : "memory");
 }
+// Asks for [from, to) of global memory to be brought to L2 (whole 16-byte pieces of it)
+__device__ __forceinline__ void prefetch_l2(const void* from, const void* to) {
+  const uintptr_t a = (reinterpret_cast<uintptr_t>(from) + 15) & ~uintptr_t(15), b = reinterpret_cast<uintptr_t>(to) & ~uintptr_t(15);
+  if (b > a) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(uint32_t(b - a)) : "memory");
+}
 // bounded wait for what others have sent
 __device__ __forceinline__ bool wait_sent(uint64_t* bar, uint32_t parity = 0) {
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
@@ -505,14 +510,20 @@ struct Held {
 
   // Starts the copies, a lane a run of kThreads groups (kMaxGroups lanes, kChunk
   // neighbours a barrier); the groups that they do not bring are written by their
-  // threads.
-  __device__ __forceinline__ void start(Common& s) const {
+  // threads.  once: the row is not read or written again soon, so L2 need not keep it
+  // (what else is read, the random numbers, then stays longer: 256 x 128256 rows
+  // without a cut 53.6 -> 51.6 us; a gradient that is written meanwhile loses by it:
+  // 222.5 -> 233.9 us of 2048 x 128256).
+  __device__ __forceinline__ void start(Common& s, bool once) const {
     const uint32_t lo = r.first_whole(), hi = r.end_whole();
     if (threadIdx.x < 32) {
       const uint32_t j = threadIdx.x, g0 = (j * n + rank) * kThreads, from = max(g0, lo), to = min(g0 + kThreads, hi);
       uint32_t bytes = j < nv && to > from ? (to - from) * 16u : 0u;
-      if (bytes)
-        bulk_g2s(part + j * kThreads + (from - g0), r.base + size_t(from) * 16, bytes, s.bar_part + j / kChunk);
+      void* to_part = part + j * kThreads + (from - g0);
+      if (bytes && once)
+        bulk_g2s_hint(to_part, r.base + size_t(from) * 16, bytes, s.bar_part + j / kChunk, evict_first_policy());
+      else if (bytes)
+        bulk_g2s(to_part, r.base + size_t(from) * 16, bytes, s.bar_part + j / kChunk);
       if (bits && j < nv) {
         const uint32_t off = (j * n + rank) * kMaskRun, end = r.W * 4u;
         const uint32_t k = off < end ? min(kMaskRun, end - off) : 0u;
