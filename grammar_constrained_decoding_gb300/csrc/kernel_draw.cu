@@ -405,13 +405,10 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   const float c = exp_scale(q.Ts);
   const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || p != p || mp != mp || (!q.greedy && !a.u);
   // Rows that need nothing of the others' parts before they send what may be drawn:
-  // the maximum; the tokens at or above the block's own bound of the k-th largest,
-  // where the list holds those of all blocks; the best of all tokens.
-  enum { kTogether, kBest, kTopK, kAny } alone = kTogether;
-  const uint32_t most = share_of(n);
+  // the maximum, or the best of all tokens.
+  enum { kTogether, kBest, kAny } alone = kTogether;
   if (!bad) {
     if (q.greedy) alone = kBest;
-    else if (q.k && fits_share(q.k, n)) alone = kTopK;
     else if (!q.k && q.p >= 1.f && !(mp > 0.f)) alone = kAny;
   }
   bool tight = true;
@@ -419,29 +416,20 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   const bool taken = h.template take<true>(s, c);
   if (!taken) s.late = 1;
   if (alone) {
-    float own_cut = -FLT_MAX;
-    if (alone == kTopK) {
-      const uint32_t key = h.own_bound(s, q.k);
-      if (key >= kKeyLowest) own_cut = fkey_inv(key);
-    }
     ready_others();
     if (alone == kBest) {
       h.template report<true>(s, c);
     } else {
       h.template report<false>(s, c);
-      if (alone == kTopK) {
-        h.template gather<false, true>(s, own_cut, false, most, 0.f, 0.f);
-      } else {
-        // the block's best by scores relative to its own maximum: their order is
-        // that of scores relative to the row's
-        q.floor_z = -INFINITY;
-        const float m = fkey_inv(block_max(fkey(h.tm), s.red_max));
-        Drawn d;
-        if (m > -INFINITY) d = draw_screened<BF16>(s, h, q, -FLT_MAX, m, c, a.u + size_t(b) * a.ld_u);
-        const unsigned long long best = block_max(d.best, s.red64b);
-        if (best ? d.best == best : tid == 0)  // one thread
-          send(at_rank(&s.best[rank], 0), best ? pack_best(d.x, best_id(best)) : 0ull, at_rank(&s.bar_best, 0));
-      }
+      // the block's best by scores relative to its own maximum: their order is that
+      // of scores relative to the row's
+      q.floor_z = -INFINITY;
+      const float m = fkey_inv(block_max(fkey(h.tm), s.red_max));
+      Drawn d;
+      if (m > -INFINITY) d = draw_screened<BF16>(s, h, q, -FLT_MAX, m, c, a.u + size_t(b) * a.ld_u);
+      const unsigned long long best = block_max(d.best, s.red64b);
+      if (best ? d.best == best : tid == 0)  // one thread
+        send(at_rank(&s.best[rank], 0), best ? pack_best(d.x, best_id(best)) : 0ull, at_rank(&s.bar_best, 0));
     }
     if (rank != 0) return;
   } else {
@@ -496,12 +484,8 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   __syncthreads();
   const float M = s.M, S = s.S, cut = s.cut;
   uint32_t mode = s.mode;
-  if (mode == kNothing) {  // not before what the others send has arrived
-    uint32_t count;
-    bool whole;
-    float mass;
-    if (alone == kTopK && h.tallied(s, count, whole, mass)) h.listed(s, count);
-    if (alone == kAny) {
+  if (mode == kNothing) {
+    if (alone == kAny) {  // not before what the others send has arrived
       if (tid == 0) mbar_expect_tx(&s.bar_best, n * 8u);
       wait_sent(&s.bar_best);
     }
@@ -541,17 +525,15 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   uint32_t total = 0;
   bool left_out = false;  // a block had too many entries to send
   if (mode == kGather) {
-    if (!alone) {
-      h.template gather<false, false>(s, cut, false, kStage, 0.f, 0.f);
-      if (rank != 0) return;  // its entries are with rank 0
-    }
+    h.template gather<false>(s, cut, false, 0.f, 0.f);
+    if (rank != 0) return;  // its entries are with rank 0
     float none;
     bool whole = true;
     if (!h.tallied(s, total, whole, none)) mode = kNothing;
     else if (!whole) left_out = true;
   } else if (mode == kGuessFirst) {
     list_cut = fmaxf(cut, M - fmaxf(s.guess - kGuess, 0.f) * q.T);
-    h.template gather<true, false>(s, list_cut, true, kStage, M, c);
+    h.template gather<true>(s, list_cut, true, M, c);
     float mass;
     bool whole;
     const bool ok = h.tallied(s, total, whole, mass);
@@ -628,15 +610,11 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   const bool gather = mode == kGather;
   if (gather) {
     const unsigned long long* list = s.list;
-    uint32_t few = total, span = total;
+    uint32_t few = total;
     if (left_out) {
       few = kListCap + 1;
-    } else if (total <= kListCap && (alone || (total > kPairCap && q.k))) {
-      if (alone) {
-        h.zero_rest(s, most);
-        span = n * most;
-      }
-      few = keep_few(s, span, total > kPairCap ? list_bound(s, span, total, q.k) : 1u);
+    } else if (total > kPairCap && total <= kListCap && q.k) {
+      few = keep_few(s, total, list_bound(s, total, q.k));
       list = s.few;
     }
     if (few <= kPairCap) {
@@ -646,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
       const bool fits = total <= kListCap && !left_out;
       auto entries = [&](auto f) {
         if (fits) {
-          for (uint32_t i = tid; i < span; i += kThreads)
-            if (s.list[i]) f(best_id(s.list[i]), fkey_inv(uint32_t(s.list[i] >> 32)));
+          for (uint32_t i = tid; i < total; i += kThreads)
+            f(best_id(s.list[i]), fkey_inv(uint32_t(s.list[i] >> 32)));
         } else {
           each_of_row(h.r, f);
         }

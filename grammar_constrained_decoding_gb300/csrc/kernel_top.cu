@@ -42,25 +42,10 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   h.start(s, true);
   may_send();
   if (!h.template take<true>(s, kLog2e)) s.late = 1;
-  // Alone each block can only bound the n-th largest of its own part.  Where the
-  // entries of all parts fit the list they are sent without waiting for the others;
-  // else the bound comes from the whole row's group maxima.
-  const uint32_t most = share_of(n);
-  const bool alone = fits_share(a.n, n);
-  bool tight = true;
-  const uint32_t per_warp = alone ? 0u : bounds_per_warp(a.n, n, tight);
-  float cut = -FLT_MAX;
-  if (alone) {
-    const uint32_t key = h.own_bound(s, a.n);
-    if (key >= kKeyLowest) cut = fkey_inv(key);
-    ready_others();
-    h.template report<false>(s, kLog2e);
-    h.template gather<false, true>(s, cut, false, most, 0.f, 0.f);
-    if (rank != 0) return;  // its entries are with rank 0
-  } else {
-    ready_others();
-    h.publish(s, kLog2e, per_warp);
-  }
+  bool tight;
+  const uint32_t per_warp = bounds_per_warp(a.n, n, tight);
+  ready_others();
+  h.publish(s, kLog2e, per_warp);
   if (tid < 32) {
     const bool ok = wait_sent(&s.bar_rec);
     float m, sum;
@@ -78,22 +63,19 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   uint32_t found = 0;
   bool late = s.late != 0;
   const unsigned long long* list = s.list;
-  uint32_t span = 0;  // of the list, zeros included, when it is longer than what was found
-  if ((alone || M > -INFINITY) && !late) {
-    if (!alone) {
-      float from = s.cut;
-      if (!tight && h.r.V > kStage) {  // a bound too low: the n-th largest itself, and its ties
-        uint32_t level = 0;
-        unsigned long long above;
-        const uint32_t key = select_key(
-            s, n, [&](auto f) { h.each(from, [&](uint32_t, float x) { f(fkey(x), 1ull); }); }, fkey(from), fkey(M),
-            a.n, level, above);
-        from = fkey_inv(key);
-        cluster_sync(n);  // everybody has read the histograms: the list and the stage take their place
-      }
-      h.template gather<false, false>(s, from, false, kStage, 0.f, 0.f);
-      if (rank != 0) return;
+  if (M > -INFINITY && !late) {
+    float from = s.cut;
+    if (!tight && h.r.V > kStage) {  // a bound too low: the n-th largest itself, and its ties
+      uint32_t level = 0;
+      unsigned long long above;
+      const uint32_t key = select_key(
+          s, n, [&](auto f) { h.each(from, [&](uint32_t, float x) { f(fkey(x), 1ull); }); }, fkey(from), fkey(M), a.n,
+          level, above);
+      from = fkey_inv(key);
+      cluster_sync(n);  // everybody has read the histograms: the list and the stage take their place
     }
+    h.template gather<false>(s, from, false, 0.f, 0.f);
+    if (rank != 0) return;  // its entries are with rank 0
     float none;
     bool whole = true;
     late = !h.tallied(s, found, whole, none) || !h.listed(s, found);
@@ -121,15 +103,11 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
       });
       __syncthreads();
       found = s.n_list;
-    } else {
-      if (alone) h.zero_rest(s, most);
-      if (alone || found > kPairCap) {
-        span = alone ? n * most : found;
-        const uint32_t key = found > kPairCap ? list_bound(s, span, found, a.n) : 1u, few = keep_few(s, span, key);
-        if (few <= kPairCap) {
-          found = few;
-          list = s.few;
-        }
+    } else if (found > kPairCap) {
+      const uint32_t few = keep_few(s, found, list_bound(s, found, a.n));
+      if (few <= kPairCap) {
+        found = few;
+        list = s.few;
       }
     }
   } else if (rank != 0) {
@@ -147,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
     place_entries<true>(s, list, found);
     if (tid < found && s.place[tid] < a.n) write(s.place[tid], list[tid]);
   } else {
-    sort_desc(s.list, max(found, span));
+    sort_desc(s.list, found);
     for (uint32_t i = tid; i < min(found, a.n); i += kThreads) write(i, s.list[i]);
   }
   for (uint32_t i = found + tid; i < a.n; i += kThreads) {

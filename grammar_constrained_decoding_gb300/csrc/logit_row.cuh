@@ -40,7 +40,7 @@ constexpr uint32_t kMaxCluster = 16;   // more than 8 is not portable, but the o
 constexpr uint32_t kBinBits = 9;
 constexpr uint32_t kBins = 1u << kBinBits;  // bins of one selection level
 constexpr uint32_t kListCap = 1024;    // entries of a list
-constexpr uint32_t kStage = 512;       // entries a block sends
+constexpr uint32_t kStage = 512;       // entries a block may send
 constexpr uint32_t kPairCap = kThreads;  // lists ranked by comparing all pairs, an entry a thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxBf16 = 3.38953138925e38f;  // largest finite bf16
@@ -152,18 +152,6 @@ constexpr uint32_t kMaxBounds = 512;                     // group maxima a clust
 
 // Exponentials are taken as exp2((x - m) c): the difference to a maximum first, which
 // is exact near it, so that no size of x or c costs precision or overflows.
-
-// Entries a block may send without knowing of the others' (its share of the list),
-// and whether its k-th bound may be its own: there is room for the tokens at or above
-// it, about k + k^2 / 512, and rank 0 gets entries of four to eight blocks.  With
-// fewer blocks rank 0 is too large a part of the work to be given the longer list
-// (64 best of 2048 x 32000: 97 us instead of 71), with more the list is too long (20
-// best of 8 x 128256: 7.8 us instead of 6.3); between them the saved exchange pays
-// (top-k 50 of 256 x 128256: 39.9 us instead of 42.5).
-__device__ __forceinline__ uint32_t share_of(uint32_t n) { return min(kListCap / n, kStage); }
-__device__ __forceinline__ bool fits_share(uint32_t k, uint32_t n) {
-  return n >= 4 && n <= 8 && k <= kThreads * 3 / 4 && k + k / 4 + 16 <= share_of(n);
-}
 
 // What a warp tells all blocks about its part of the row: its maximum and its
 // sum of exp2((x - m) c).
@@ -657,19 +645,6 @@ struct Held {
     }
     if (lane == 0) send(at_rank(&s.rec[w], 0), rec, at_rank(&s.bar_rec, 0));
   }
-  // A key that at least k <= kThreads threads of this block reach with a token (so
-  // that at least k tokens lie at or above it): for gathering before the blocks
-  // know of one another.
-  __device__ __forceinline__ uint32_t own_bound(Common& s, uint32_t k) const {
-    s.bound[threadIdx.x] = fkey(tm);
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      const uint32_t key = bound_key(s, kThreads, k);
-      if (threadIdx.x == 0) s.bin = key;
-    }
-    __syncthreads();
-    return s.bin;
-  }
   // f(token, logit) for every element of this thread's groups that is >= cut (finite)
   template <typename Fn>
   __device__ __forceinline__ void each(float cut, Fn f) const {
@@ -699,12 +674,10 @@ struct Held {
   // its bar_list, and then the block's count and (MASS) its elements' mass in units
   // of the maximum's to rank 0 or to every block (all), completing on bar_tally.
   // The list's count goes on past its capacity, the entries do not.  Their order is
-  // arbitrary.  A block with more than `most` <= kStage entries sends none.  The
-  // entries are staged in the block's own memory: one warp sends them, to a place
-  // reserved at rank 0 (a round trip) or, with REGION, to the block's own share of
-  // the list, `most` entries at rank * most.
-  template <bool MASS, bool REGION>
-  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, uint32_t most, float M, float c) const {
+  // arbitrary.  A block with more than kStage entries sends none.  The entries are
+  // staged in the block's own memory: one warp sends them, with one reservation.
+  template <bool MASS>
+  __device__ __forceinline__ void gather(Shared& s, float cut, bool all, float M, float c) const {
     const uint32_t lane = threadIdx.x & 31;
     if (tm >= cut) {
       const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
@@ -723,7 +696,7 @@ struct Held {
           while (hits) {
             const uint32_t e = __ffs(hits) - 1;
             hits &= hits - 1;
-            if (place < most) s.stage[place] = pack_best(elem<BF16>(v, e), uint32_t(first_token(j)) + e);
+            if (place < kStage) s.stage[place] = pack_best(elem<BF16>(v, e), uint32_t(first_token(j)) + e);
             ++place;
           }
         }
@@ -731,7 +704,7 @@ struct Held {
     }
     __syncthreads();
     const uint32_t found = s.n_stage;
-    const bool fits = found <= most;
+    const bool fits = found <= kStage;
     if (MASS && !fits) {
       const float mass = warp_reduce(masses_from(M, c, cut, cut).y, SumOp());
       if (lane == 0) s.red_f[threadIdx.x >> 5] = mass;
@@ -740,11 +713,9 @@ struct Held {
     if (threadIdx.x >= 32) return;
     float mass = 0.f;
     if (fits && found) {
-      uint32_t place = rank * most;
-      if (!REGION) {
-        if (lane == 0) place = add_remote(at_rank(&s.n_list, 0), found);
-        place = __shfl_sync(0xFFFFFFFFu, place, 0);
-      }
+      uint32_t place = 0;
+      if (lane == 0) place = add_remote(at_rank(&s.n_list, 0), found);
+      place = __shfl_sync(0xFFFFFFFFu, place, 0);
       const uint32_t list = at_rank(s.list, 0), bar = at_rank(&s.bar_list, 0);
       unsigned long long units = 0;  // in integers: the order is arbitrary
       for (uint32_t i = lane; i < found; i += 32) {
@@ -821,15 +792,6 @@ struct Held {
   __device__ __forceinline__ bool listed(Shared& s, uint32_t count) const {
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_list, min(count, kListCap) * 8u);
     return wait_sent(&s.bar_list);
-  }
-  // ... of a gather by region: the empty places of the regions read as zeros (after a
-  // barrier), which are below every entry
-  __device__ __forceinline__ void zero_rest(Shared& s, uint32_t most) const {
-    for (uint32_t i = threadIdx.x; i < n * most; i += kThreads) {
-      const uint32_t k = s.tally[i / most].count;
-      if (i % most >= (k == kTooMany ? 0u : k)) s.list[i] = 0ull;
-    }
-    __syncthreads();
   }
 };
 
@@ -984,18 +946,17 @@ __device__ __forceinline__ uint32_t keep_few(Shared& s, uint32_t c, uint32_t key
   return s.n_local;
 }
 // A key that at least k of the entries of s.list[0 .. c), c <= kListCap, reach, and few
-// more: by bisection, the block counting together.  1 when there are not more than
-// k (of `total`; zeros are no entries).
-__device__ __forceinline__ uint32_t list_bound(Shared& s, uint32_t c, uint32_t total, uint32_t k) {
+// more: by bisection, the block counting together.  1 when there are not more than k.
+__device__ __forceinline__ uint32_t list_bound(Shared& s, uint32_t c, uint32_t k) {
   constexpr uint32_t kOwn = kListCap / kThreads;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (total <= k) return 1u;
+  if (c <= k) return 1u;
   uint32_t v[kOwn], lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
   for (uint32_t i = 0; i < kOwn; ++i) {
     const uint32_t at = i * kThreads + tid;
     v[i] = at < c ? uint32_t(s.list[at] >> 32) : 0u;
-    if (v[i]) {
+    if (at < c) {
       lo = min(lo, v[i]);
       hi = max(hi, v[i]);
     }
@@ -1065,7 +1026,9 @@ inline size_t part_bytes(bool bf16, uint32_t nv, bool mask) {
 struct Plan {
   uint32_t nv, n;
 };
-constexpr uint32_t kSlots = 4 * 152;  // blocks resident together
+// Blocks up to which a row is split further: two an SM.  64 x 32000, top-k 50 and top-p:
+// 10.5 us at one, 9.5 at two, 14.2 at four; 32 x 128256: 15.2, 11.5, 14.1.
+constexpr uint32_t kSlots = 2 * 152;
 inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned, uint32_t full) {
   const uint32_t E = bf16 ? 8 : 4;
   const uint32_t runs = ((V + (aligned ? 0 : E - 1) + E - 1) / E + kThreads - 1) / kThreads;  // of kThreads groups
