@@ -299,7 +299,9 @@ __device__ Drawn draw_by_trial(Shared& s, const Held<BF16>& h, const RowSettings
     }
     __syncthreads();
     if (!listed && !settled) {  // few enough: from a list, else from the part itself
-      listed = h.compact(s, cut);
+      // the first groups tell about how many there are
+      const uint32_t some = h.tm >= cut ? __popc(ge_bits<BF16>(h.at(0), cut, BF16 ? bf16_pair_up(cut) : 0u)) : 0u;
+      if (block_sum(some, s.red_max) * h.nv <= kListCap) listed = h.compact(s, cut);
     }
     const uint32_t key = fkey(cut);
     if (listed) {
@@ -548,45 +550,51 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     }
   }
   if (mode == kSample) {
-    // the masses below four cuts, estimated from the first group of every thread:
+    // the masses below eight cuts, estimated from the first group of every thread:
     // the first cut that leaves little enough below it is the one to try
-    const float depth[4] = {5.f, 3.5f, 2.2f, 1.f};
-    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto level = [&](int i) { return M - fmaxf(s.guess - depth[i], 0.f) * q.T; };
+    constexpr int kCuts = 8;
+    constexpr float depth[kCuts] = {5.5f, 4.9f, 4.3f, 3.7f, 3.1f, 2.5f, 1.8f, 1.f};
+    float w[kCuts] = {};
+    const float D = s.guess;
+    auto level = [&](int i) { return M - fmaxf(D - depth[i], 0.f) * q.T; };
     const uint4 v0 = h.at(0);
 #pragma unroll
     for (uint32_t e = 0; e < Fmt<BF16>::E; ++e) {
       const float x = elem<BF16>(v0, e), m = ex2((x - M) * c);
-      w.x += x < level(0) ? m : 0.f;
-      w.y += x < level(1) ? m : 0.f;
-      w.z += x < level(2) ? m : 0.f;
-      w.w += x < level(3) ? m : 0.f;
+#pragma unroll
+      for (int i = 0; i < kCuts; ++i) w[i] += x < level(i) ? m : 0.f;
     }
-    w.x = warp_reduce(w.x, SumOp());
-    w.y = warp_reduce(w.y, SumOp());
-    w.z = warp_reduce(w.z, SumOp());
-    w.w = warp_reduce(w.w, SumOp());
+#pragma unroll
+    for (int i = 0; i < kCuts; ++i) w[i] = warp_reduce(w[i], SumOp());
     const uint32_t lane = tid & 31;
-    if (lane < n)
-      send(at_rank(&s.sample[rank * kWarps + (tid >> 5)], lane),
-           make_uint4(__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w)),
-           at_rank(&s.bar_tally, lane));
-    if (tid == 0) mbar_expect_tx(&s.bar_tally, n * kWarps * 16u);
+    if (lane < n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        send(at_rank(&s.sample[rank * kWarps + (tid >> 5)][i], lane),
+             make_uint4(__float_as_uint(w[4 * i]), __float_as_uint(w[4 * i + 1]), __float_as_uint(w[4 * i + 2]),
+                        __float_as_uint(w[4 * i + 3])),
+             at_rank(&s.bar_tally, lane));
+    }
+    if (tid == 0) mbar_expect_tx(&s.bar_tally, n * kWarps * 32u);
     const bool ok = wait_sent(&s.bar_tally);
-    w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kCuts; ++i) w[i] = 0.f;
     for (uint32_t i = lane; i < n * kWarps; i += 32) {
-      w.x += s.sample[i].x;
-      w.y += s.sample[i].y;
-      w.z += s.sample[i].z;
-      w.w += s.sample[i].w;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 t = s.sample[i][k];
+        w[4 * k] += t.x;
+        w[4 * k + 1] += t.y;
+        w[4 * k + 2] += t.z;
+        w[4 * k + 3] += t.w;
+      }
     }
     const float share = fminf(1.f, float(n * kThreads * Fmt<BF16>::E) / float(a.V));
-    const float most = (1.f - q.p) * S * share * 0.9f;
-    near = level(3);
-    if (warp_reduce(w.w, SumOp()) > most) near = cut;
-    if (warp_reduce(w.z, SumOp()) <= most) near = level(2);
-    if (warp_reduce(w.y, SumOp()) <= most) near = level(1);
-    if (warp_reduce(w.x, SumOp()) <= most) near = level(0);
+    const float most = (1.f - q.p) * S * share * 0.93f;
+    near = cut;
+#pragma unroll
+    for (int i = kCuts - 1; i >= 0; --i)
+      if (warp_reduce(w[i], SumOp()) <= most) near = level(i);
     if (!ok) {
       if (rank == 0 && tid == 0) {
         record_error(a.status, CG_DEV_TIMEOUT);

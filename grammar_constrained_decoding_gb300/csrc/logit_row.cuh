@@ -180,7 +180,7 @@ struct __align__(16) Common {
   Record rec[kMaxRecords];
   union {
     uint32_t bound[kMaxBounds];                     // keys of group maxima (rows with a count)
-    __align__(16) float4 sample[kMaxRecords];       // sampled masses (rows without)
+    __align__(16) float4 sample[kMaxRecords][2];    // sampled masses (rows without)
     unsigned long long few[kPairCap];               // the list's entries that matter (rank 0)
     unsigned long long top[kMaxRecords];            // the best token of each warp
   };
@@ -661,14 +661,31 @@ struct Held {
       }
     }
   }
-  // the number of those elements
-  __device__ __forceinline__ uint32_t count(float cut) const {
-    uint32_t c = 0;
-    if (!(tm >= cut)) return c;
+  // Appends (logit, token) of every element >= cut to a list of the block's own, in
+  // any order; *count, zero before, goes on past the capacity, the entries do not.
+  __device__ __forceinline__ void stage(float cut, unsigned long long* list, uint32_t cap, uint32_t* count) const {
+    if (!(tm >= cut)) return;
     const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
-#pragma unroll 4
-    for (uint32_t j = 0; j < nv; ++j) c += __popc(ge_bits<BF16>(at(j), cut, cut2));
-    return c;
+#pragma unroll 1
+    for (uint32_t j0 = 0; j0 < nv; j0 += kChunk) {
+      uint32_t with = 0;  // groups of the chunk that hold some
+#pragma unroll
+      for (uint32_t i = 0; i < kChunk; ++i)
+        if (j0 + i < nv && group_max_nan<BF16>(at(j0 + i)) >= cut) with |= 1u << i;
+      while (with) {
+        const uint32_t j = j0 + __ffs(with) - 1;
+        with &= with - 1;
+        const uint4 v = at(j);
+        uint32_t hits = ge_bits<BF16>(v, cut, cut2);
+        uint32_t place = atomicAdd(count, uint32_t(__popc(hits)));
+        while (hits) {
+          const uint32_t e = __ffs(hits) - 1;
+          hits &= hits - 1;
+          if (place < cap) list[place] = pack_best(elem<BF16>(v, e), uint32_t(first_token(j)) + e);
+          ++place;
+        }
+      }
+    }
   }
   // Sends (logit, token) of every element >= cut to rank 0's list, completing on
   // its bar_list, and then the block's count and (MASS) its elements' mass in units
@@ -679,29 +696,7 @@ struct Held {
   template <bool MASS>
   __device__ __forceinline__ void gather(Shared& s, float cut, bool all, float M, float c) const {
     const uint32_t lane = threadIdx.x & 31;
-    if (tm >= cut) {
-      const uint32_t cut2 = BF16 ? bf16_pair_up(cut) : 0u;
-#pragma unroll 1
-      for (uint32_t j0 = 0; j0 < nv; j0 += kChunk) {
-        uint32_t with = 0;  // groups of the chunk that hold some
-#pragma unroll
-        for (uint32_t i = 0; i < kChunk; ++i)
-          if (j0 + i < nv && group_max_nan<BF16>(at(j0 + i)) >= cut) with |= 1u << i;
-        while (with) {
-          const uint32_t j = j0 + __ffs(with) - 1;
-          with &= with - 1;
-          const uint4 v = at(j);
-          uint32_t hits = ge_bits<BF16>(v, cut, cut2);
-          uint32_t place = atomicAdd(&s.n_stage, uint32_t(__popc(hits)));
-          while (hits) {
-            const uint32_t e = __ffs(hits) - 1;
-            hits &= hits - 1;
-            if (place < kStage) s.stage[place] = pack_best(elem<BF16>(v, e), uint32_t(first_token(j)) + e);
-            ++place;
-          }
-        }
-      }
-    }
+    stage(cut, s.stage, kStage, &s.n_stage);
     __syncthreads();
     const uint32_t found = s.n_stage;
     const bool fits = found <= kStage;
@@ -750,24 +745,11 @@ struct Held {
     }
     return make_float2(above.x + above.y, from.x + from.y);
   }
-  // Lists (logit, token) of every element >= cut in this block's own list, where it
-  // holds them all; s.n_local, zero before, receives their number.  Ends with a
-  // barrier.
+  // stage() to this block's own list, between two barriers; whether it holds them all
   __device__ __forceinline__ bool compact(Shared& s, float cut) const {
-    const uint32_t lane = threadIdx.x & 31, mine = count(cut);
-    uint32_t inc = mine, place = 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= uint32_t(o)) inc += y;
-    }
-    if (lane == 31 && inc) place = atomicAdd(&s.n_local, inc);
-    place = __shfl_sync(0xFFFFFFFFu, place, 31) + inc - mine;
+    stage(cut, s.list, kListCap, &s.n_local);
     __syncthreads();
-    const bool fits = s.n_local <= kListCap;
-    if (fits && mine) each(cut, [&](uint32_t t, float x) { s.list[place++] = pack_best(x, t); });
-    __syncthreads();
-    return fits;
+    return s.n_local <= kListCap;
   }
   // The gathered entries' count, whether every warp has sent its own, and the
   // mass, to every thread of a block that tallies go to; false when the wait ran
