@@ -32,6 +32,12 @@ def ctx_of(V):
     return cg.Ctx([cg.Grammar.compile('root ::= "a"', "gbnf")], cg.Vocab([i.to_bytes(3, "big") for i in range(V)]))
 
 
+@pytest.fixture(scope="module", autouse=True)
+def contexts_end_with_the_module():
+    yield
+    ctx_of.cache_clear()
+
+
 def make_rows(rng, B, V, kind):
     if kind == "flat":
         x = rng.normal(0, 2, (B, V)) + 4.0 * (rng.random((B, V)) < 0.05)
@@ -400,6 +406,84 @@ def test_distill_bad_id_is_recorded():
     assert ctx.status() == 2                                      # CG_DEV_BAD_TOKEN
     want = R.distill_row(v[0], np.array([3, R.NO_TOKEN]), np.zeros(2), 1.0)[0]
     assert abs(float(host(loss)[0]) - want) < 1e-5
+
+
+def test_sample_rows_numbers_against_the_logits():
+    """Random numbers that rank the tokens almost against their logits: the best
+    scored tokens lie outside the nucleus one after another."""
+    def u_of(rng, B, V):
+        x = make_rows(np.random.default_rng([V, 0, 4]), B, V, "flat").astype(np.float64)
+        score = -1.3 * x + 1e-3 * rng.random((B, V))           # wanted Gumbel part
+        score += 6.0 - score.max(axis=1, keepdims=True)
+        return np.exp(-np.exp(-np.maximum(score, -3.0))).astype(np.float32)
+    settings = [(1.0, 0, 0.5, 0.0), (1.0, 0, 0.9, 0.0), (0.7, 0, 0.05, 0.0), (1.0, 0, 0.7, 0.01)]
+    for V, dtype in ((4013, "f32"), (50000, "bf16"), (128256, "bf16")):
+        check_sample(V, dtype, "flat", False, B=8, u_of=u_of, settings=settings)
+
+
+def test_sample_rows_captured_in_a_graph():
+    """The calls allocate nothing and may be captured: replays see new inputs."""
+    import torch
+    from grammar_constrained_decoding_gb300 import Ctx, Grammar, Vocab
+    V, B, n = 5000, 9, 12
+    side = torch.cuda.Stream()
+    ctx = Ctx([Grammar.compile('root ::= "a"', "gbnf")], Vocab([i.to_bytes(3, "big") for i in range(V)]), side)
+    rng = np.random.default_rng(0)
+    x, _ = to_dev(make_rows(rng, B, V, "flat"), "bf16")
+    u, tok, top_p = f32(rng.random((B, V))), empty((B,), torch.int32), f32([0.9] * B)
+    ids, lps = empty((B, n), torch.int32), empty((B, n), torch.float32)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        ctx.sample_rows(x, u, tok, top_p=top_p)
+        ctx.top_logprobs(x, ids, lps)
+    for seed in (1, 2):
+        new, v = to_dev(make_rows(np.random.default_rng(seed), B, V, "flat"), "bf16")
+        x.copy_(new)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            row = R.allowed_logits(v[b], None, "bf16")
+            want = R.sample_rows_row(row, 1.0, 0, float(np.float32(0.9)), 0.0, host(u)[b])
+            assert int(host(tok)[b]) == want.tok or want.gap < TIE or want.margin < TIE
+            assert host(ids).view(np.uint32)[b].tolist() == R.top_logprobs_row(row, n)[0].tolist()
+
+
+def test_rows_beyond_32_bit_offsets():
+    """A row stride that takes the last row past 2^32 elements, logits and random
+    numbers and gradient alike."""
+    import torch
+    V, B, K, ld = 3001, 3, 7, 2 ** 31 + 24
+    rng = np.random.default_rng(1)
+    xs = make_rows(rng, B, V, "peaked")
+    flat = torch.empty((B - 1) * ld + V, dtype=torch.bfloat16, device="cuda")
+    x = flat.as_strided((B, V), (ld, 1))
+    x.copy_(torch.from_numpy(xs))
+    v = x.double().cpu().numpy()
+    ids, t = teacher_list(rng, B, V, K, False)
+    ctx, u = ctx_of(V), rng.random((B, V)).astype(np.float32)
+    tok, best, lps, loss = empty((B,), torch.int32), empty((B, 5), torch.int32), empty((B, 5), torch.float32), empty((B,), torch.float32)
+    ctx.sample_rows(x, f32(u), tok)
+    ctx.top_logprobs(x, best, lps)
+    ctx.distill_loss(x, u32(ids), f32(t), loss, out_grad=x)       # the gradient over the logits
+    assert ctx.status() == 0
+    for b in range(B):
+        row = R.allowed_logits(v[b], None, "bf16")
+        want = R.sample_rows_row(row, 1.0, 0, 1.0, 0.0, u[b])
+        assert int(host(tok)[b]) == want.tok or want.gap < TIE
+        assert host(best).view(np.uint32)[b].tolist() == R.top_logprobs_row(row, 5)[0].tolist()
+        w_loss, _, w_grad = R.distill_row(row, ids[b], t[b], 1.0)
+        assert abs(float(host(loss)[b]) - w_loss) <= 1e-4 * max(1.0, w_loss)
+        assert np.abs(x[b].double().cpu().numpy() - w_grad).max() <= 2.0 ** -8
+
+
+def test_example_runs_them_together():
+    """examples/grammar_distill.py: generation under a grammar, the record, and a
+    student that learns from it."""
+    from examples.grammar_distill import main
+    first, final = main(rows=32, steps=12, n_best=12, epochs=25, verbose=False)
+    assert 0.0 <= final < 0.5 * first
 
 
 def test_repeated_calls_give_the_same_bits():
