@@ -40,7 +40,7 @@ struct List {
       : id(static_cast<uint32_t*>(at)), t(reinterpret_cast<float*>(id + K)), x(t + K),
         hash(reinterpret_cast<uint32_t*>(x + K)), slots(slots_of(K)) {}
 };
-struct DistillShared : Common {
+struct DistillShared : Meet {
   uint32_t repeated;
 };
 
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
     if (!h.template take<true>(s, c)) record_error(a.status, CG_DEV_TIMEOUT);
     ready_others();
     if (a.grad) {
-      h.publish(s, c, 0u);
+      h.publish(s, c);
     } else {
       h.template report<false>(s, c);
     }

@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   if (alone) {
     ready_others();
     if (alone == kBest) {
-      h.template report<true>(s, c);
+      h.template report<true>(s, c, s.top);
     } else {
       h.template report<false>(s, c);
       // the block's best by scores relative to its own maximum: their order is that

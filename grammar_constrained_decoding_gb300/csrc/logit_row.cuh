@@ -170,14 +170,22 @@ constexpr uint32_t kMaxChunks = 8;
 constexpr uint32_t kBars = 5 + kMaxChunks;
 constexpr uint32_t kMaxGroups = kChunk * kMaxChunks;  // of a thread: a lane a copy
 
-// Reductions and exchange
-struct __align__(16) Common {
+// What every operator's cluster meets in: barriers, records, reductions
+struct __align__(16) Meet {
   uint64_t bar_rec, bar_tally, bar_list, bar_best, bar_mass;  // kBars barriers in a row ...
   uint64_t bar_part[kMaxChunks];                              // ... the last for the copies of this block's part
-  float M, S, cut, guess, floor_z;     // what the merging warp found
-  uint32_t mode;
+  float M, S;                          // what the merging warp found
   uint32_t late;                       // a bounded wait ran out
+  uint32_t n_list, n_local, n_stage;
   Record rec[kMaxRecords];
+  unsigned long long red64[kWarps], red64b[kWarps];
+  uint32_t red_max[kWarps];
+  float red_f[kWarps];
+};
+// ... and those in which the tokens above a threshold are sought
+struct __align__(16) Common : Meet {
+  float cut, guess, floor_z;
+  uint32_t mode;
   union {
     uint32_t bound[kMaxBounds];                     // keys of group maxima (rows with a count)
     __align__(16) float4 sample[kMaxRecords][2];    // sampled masses (rows without)
@@ -187,11 +195,8 @@ struct __align__(16) Common {
   Tally tally[kMaxCluster];
   unsigned long long best[kMaxCluster];
   unsigned long long sums[kMaxCluster];
-  unsigned long long red64[kWarps], red64b[kWarps];
   unsigned long long base;
-  uint32_t red_max[kWarps];
-  float red_f[kWarps];
-  uint32_t n_list, n_local, n_stage, bin;
+  uint32_t bin;
   float best_x[kMaxCluster];           // the logits of best[]
   __align__(8) float2 mass[kMaxRecords];            // per warp: mass above the drawn token, mass at or above the cut
 };
@@ -248,7 +253,7 @@ __device__ __forceinline__ T block_scan(T v, T* red) {
 }
 
 // The block's barriers and counters; ends with a block barrier.
-__device__ __forceinline__ void begin(Common& s) {
+__device__ __forceinline__ void begin(Meet& s) {
   if (threadIdx.x < kBars) {
     mbar_init(&s.bar_rec + threadIdx.x, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -502,7 +507,7 @@ struct Held {
   // (what else is read, the random numbers, then stays longer: 256 x 128256 rows
   // without a cut 53.6 -> 51.6 us; a gradient that is written meanwhile loses by it:
   // 222.5 -> 233.9 us of 2048 x 128256).
-  __device__ __forceinline__ void start(Common& s, bool once) const {
+  __device__ __forceinline__ void start(Meet& s, bool once) const {
     const uint32_t lo = r.first_whole(), hi = r.end_whole();
     if (threadIdx.x < 32) {
       const uint32_t j = threadIdx.x, g0 = (j * n + rank) * kThreads, from = max(g0, lo), to = min(g0 + kThreads, hi);
@@ -537,7 +542,7 @@ struct Held {
   // thread's maximum and, with SUM, its sum of exp2((x - tm) c), scaled on as the
   // maximum rises.  False when a wait ran out.
   template <bool SUM>
-  __device__ __forceinline__ bool take(Common& s, float c) {
+  __device__ __forceinline__ bool take(Meet& s, float c) {
     bool ok = true;
     tm = -INFINITY;
     float2 acc = {};
@@ -604,7 +609,11 @@ struct Held {
   // bound on the k-th largest logit, the maxima of `per_warp` groups of its
   // lanes (a power of two, 0 for none), completing on bar_rec.  After
   // ready_others().
+  __device__ __forceinline__ void publish(Meet& s, float c) const { publish_with(s, c, 0u, nullptr); }
   __device__ __forceinline__ void publish(Common& s, float c, uint32_t per_warp) const {
+    publish_with(s, c, per_warp, s.bound);
+  }
+  __device__ __forceinline__ void publish_with(Meet& s, float c, uint32_t per_warp, uint32_t* bound) const {
     const uint32_t lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_rec, n * kWarps * (8u + 4u * per_warp));
     const unsigned long long rec = record(c);
@@ -614,7 +623,7 @@ struct Held {
     for (uint32_t o = 16; o >= per_warp; o >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
     // every lane holds the maximum of the lanes equal to it modulo per_warp
     for (uint32_t i = lane; i < per_warp * n; i += 32)
-      send(at_rank(&s.bound[w * per_warp + (i & (per_warp - 1))], i / per_warp), key,
+      send(at_rank(&bound[w * per_warp + (i & (per_warp - 1))], i / per_warp), key,
            at_rank(&s.bar_rec, i / per_warp));
   }
   // this warp's maximum and sum
@@ -625,7 +634,7 @@ struct Held {
   }
   // Tells rank 0 alone, and with BEST this warp's best token too
   template <bool BEST>
-  __device__ __forceinline__ void report(Common& s, float c) const {
+  __device__ __forceinline__ void report(Meet& s, float c, unsigned long long* top = nullptr) const {
     const uint32_t lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
     if (rank == 0 && threadIdx.x == 0) mbar_expect_tx(&s.bar_rec, n * kWarps * (BEST ? 16u : 8u));
     const unsigned long long rec = record(c);
@@ -641,7 +650,7 @@ struct Held {
       }
       t = __reduce_min_sync(0xFFFFFFFFu, t);
       if (lane == 0)
-        send(at_rank(&s.top[w], 0), m > -INFINITY ? pack_best(m, t) : 0ull, at_rank(&s.bar_rec, 0));
+        send(at_rank(&top[w], 0), m > -INFINITY ? pack_best(m, t) : 0ull, at_rank(&s.bar_rec, 0));
     }
     if (lane == 0) send(at_rank(&s.rec[w], 0), rec, at_rank(&s.bar_rec, 0));
   }
@@ -779,7 +788,7 @@ struct Held {
 
 // The row's maximum and sum of exp2((x - M) c) from the warps' records, the same
 // in every warp of the cluster.  For one warp of a block, after its wait.
-__device__ __forceinline__ void merge(const Common& s, uint32_t n, float c, float& M, float& S) {
+__device__ __forceinline__ void merge(const Meet& s, uint32_t n, float c, float& M, float& S) {
   const uint32_t lane = threadIdx.x & 31, count = n * kWarps;
   uint32_t top = 0;
   for (uint32_t i = lane; i < count; i += 32) top = max(top, fkey(s.rec[i].m));
