@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   if (tid < 32) {
     const bool ok = wait_sent(&s.bar_rec);
     float m, sum;
-    merge(s, n, kLog2e, m, sum);
+    merge(s.rec, n * kWarps, kLog2e, m, sum);
     const uint32_t key = per_warp ? bound_key(s, n * kWarps * per_warp, a.n) : 0u;
     if (tid == 0) {
       s.M = m;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
         }
       });
       __syncthreads();
-      found = s.n_list;
+      found = min(s.n_list, kListCap);  // a.n, unless the row is written meanwhile
     } else if (found > kPairCap) {
       const uint32_t few = keep_few(s, found, list_bound(s, found, a.n));
       if (few <= kPairCap) {
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
 template <bool BF16>
 cudaError_t launch_top(int device, uint32_t B, const TopArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
-  return launch_clusters<top_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
+  return launch_clusters<top_kernel<BF16>>(device, B, plan.n, kThreads, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
                                            a, plan.nv);
 }
 
