@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   if (tid < 32) {
     const bool ok = wait_sent(&s.bar_rec) && s.late == 0;
     float M, S;
-    merge(s, n, c, M, S);
+    merge(s.rec, n * kWarps, c, M, S);
     // a lower bound of the threshold, and how to settle it.  Without top-k the
     // mass that top-p refers to is known, so min-p bounds what matters as well.
     const float floor_z = logf(fminf(fmaxf(mp, 0.f), 1.f));  // -inf for min_p = 0
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
 template <bool BF16>
 cudaError_t launch_draw(int device, uint32_t B, const DrawArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
-  return launch_clusters<draw_kernel<BF16>>(device, B, plan.n, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
+  return launch_clusters<draw_kernel<BF16>>(device, B, plan.n, kThreads, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
                                             a, plan.nv);
 }
 

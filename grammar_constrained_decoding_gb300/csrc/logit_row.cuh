@@ -476,6 +476,33 @@ __device__ __forceinline__ uint32_t bound_key(const Common& s, uint32_t count, u
   return lo;
 }
 
+// Takes kN groups whose maximum is t into a running maximum tm and the running sum
+// acc.x + acc.y of exp2((x - tm) c), which is scaled on as the maximum rises
+template <bool BF16, int kN>
+__device__ __forceinline__ void add_groups(const uint4* v, float t, float c, float& tm, float2& acc) {
+  if (t > tm) {
+    const float f = ex2((tm - t) * c);  // 0 from the first -inf on
+    acc = make_float2(acc.x * f, acc.y * f);
+    tm = t;
+  }
+  if (!(tm > -INFINITY)) return;
+  const float2 nm = make_float2(-tm, -tm), c2 = make_float2(c, c);
+  float2 sum[2] = {};
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (uint32_t q = 0; q < Fmt<BF16>::E / 2; ++q)
+      sum[q & 1u] = __fadd2_rn(sum[q & 1u], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[i], q), nm), c2)));
+  acc = __fadd2_rn(acc, __fadd2_rn(sum[0], sum[1]));
+}
+
+// A warp's maximum and sum from its lanes', as the bits of a Record
+__device__ __forceinline__ unsigned long long warp_record(float tm, float ts, float c) {
+  const float m = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, fkey(tm)));
+  const float sum = warp_reduce(tm > -INFINITY ? ts * ex2((tm - m) * c) : 0.f, SumOp());
+  return (static_cast<unsigned long long>(__float_as_uint(sum)) << 32) | __float_as_uint(m);
+}
+
 // The part of a row that a block holds
 template <bool BF16>
 struct Held {
@@ -546,7 +573,6 @@ struct Held {
     bool ok = true;
     tm = -INFINITY;
     float2 acc = {};
-    const float2 c2 = make_float2(c, c);
 #pragma unroll 1
     for (uint32_t j0 = 0; j0 < nv; j0 += kChunk) {
       uint32_t allowed[kChunk];
@@ -584,23 +610,8 @@ struct Held {
         }
         t = groups_max_nan<BF16, kChunk>(v);
       }
-      if (t > tm) {
-        if (SUM) {
-          const float f = ex2((tm - t) * c);  // 0 from the first -inf on
-          acc = make_float2(acc.x * f, acc.y * f);
-        }
-        tm = t;
-      }
-      if (SUM && tm > -INFINITY) {
-        const float2 nm = make_float2(-tm, -tm);
-        float2 sum[2] = {};
-#pragma unroll
-        for (uint32_t i = 0; i < kChunk; ++i)
-#pragma unroll
-          for (uint32_t q = 0; q < F::E / 2; ++q)
-            sum[q & 1u] = __fadd2_rn(sum[q & 1u], ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[i], q), nm), c2)));
-        acc = __fadd2_rn(acc, __fadd2_rn(sum[0], sum[1]));
-      }
+      if (SUM) add_groups<BF16, kChunk>(v, t, c, tm, acc);
+      else tm = fmaxf(tm, t);
     }
     ts = acc.x + acc.y;
     return ok;
@@ -627,11 +638,7 @@ struct Held {
            at_rank(&s.bar_rec, i / per_warp));
   }
   // this warp's maximum and sum
-  __device__ __forceinline__ unsigned long long record(float c) const {
-    const float m = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, fkey(tm)));
-    const float sum = warp_reduce(tm > -INFINITY ? ts * ex2((tm - m) * c) : 0.f, SumOp());
-    return (static_cast<unsigned long long>(__float_as_uint(sum)) << 32) | __float_as_uint(m);
-  }
+  __device__ __forceinline__ unsigned long long record(float c) const { return warp_record(tm, ts, c); }
   // Tells rank 0 alone, and with BEST this warp's best token too
   template <bool BEST>
   __device__ __forceinline__ void report(Meet& s, float c, unsigned long long* top = nullptr) const {
@@ -788,14 +795,14 @@ struct Held {
 
 // The row's maximum and sum of exp2((x - M) c) from the warps' records, the same
 // in every warp of the cluster.  For one warp of a block, after its wait.
-__device__ __forceinline__ void merge(const Meet& s, uint32_t n, float c, float& M, float& S) {
-  const uint32_t lane = threadIdx.x & 31, count = n * kWarps;
+__device__ __forceinline__ void merge(const Record* rec, uint32_t count, float c, float& M, float& S) {
+  const uint32_t lane = threadIdx.x & 31;
   uint32_t top = 0;
-  for (uint32_t i = lane; i < count; i += 32) top = max(top, fkey(s.rec[i].m));
+  for (uint32_t i = lane; i < count; i += 32) top = max(top, fkey(rec[i].m));
   M = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, top));
   float t = 0.f;
   for (uint32_t i = lane; i < count; i += 32)
-    if (s.rec[i].m > -INFINITY) t += s.rec[i].s * ex2((s.rec[i].m - M) * c);
+    if (rec[i].m > -INFINITY) t += rec[i].s * ex2((rec[i].m - M) * c);
   S = warp_reduce(t, SumOp());
 }
 
@@ -1033,7 +1040,8 @@ inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned, uint32_t f
 // memory and cluster size limits are raised on the first launch on a device.
 constexpr int kMaxSmem = 227 * 1024;
 template <auto Kernel, typename... Args>
-cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, size_t smem, cudaStream_t stream, Args&&... args) {
+cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, uint32_t threads, size_t smem, cudaStream_t stream,
+                            Args&&... args) {
   static std::atomic<uint64_t> raised{0};
   const uint64_t bit = uint64_t(1) << (device & 63);
   if (!(raised.load(std::memory_order_relaxed) & bit)) {
@@ -1044,7 +1052,7 @@ cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, size_t smem, 
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(rows * n);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

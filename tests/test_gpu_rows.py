@@ -286,20 +286,20 @@ def check_distill(V, dtype, kind, masked, K, temp, B=12, pad=0, shift=0, gpad=0,
     both = x if inplace else new()
     ctx.distill_loss(x, d_ids, d_t, loss2, out_grad=both, grad_loss=f32(up), **args)
     assert ctx.status() == 0
-    assert np.array_equal(host(loss).view(np.uint32), host(loss2).view(np.uint32))
-    g_loss, g_lse = host(loss).astype(np.float64), host(lse).astype(np.float64)
+    g_loss, g_lse = np.stack([host(loss), host(loss2)]).astype(np.float64), host(lse).astype(np.float64)
     T = float(np.float32(temp))
     for b in range(B):
         row = R.allowed_logits(v[b], None if mask is None else mask[b], dtype)
         w_loss, w_lse, w_grad = R.distill_row(row, ids[b], t[b], T)
         if w_lse == -np.inf:
-            assert g_lse[b] == -np.inf and g_loss[b] == 0.0
+            assert g_lse[b] == -np.inf and (g_loss[:, b] == 0.0).all()
         elif np.abs(w_lse) < 1e6:
             assert abs(g_lse[b] - w_lse) <= rel_sum(V) + abs(w_lse) * 2.0 ** -22, b
             # the largest term of the sum bounds what its roundings add
             live = [i for i in ids[b] if i < V and row[i] > -np.inf]
             big = max([abs(row[i] / T - w_lse) for i in live], default=0.0) + 8 * abs(np.nan_to_num(t[b], neginf=0)).max() / T
-            assert abs(g_loss[b] - w_loss) <= T * T * (rel_sum(V) + (K + 16) * 2.0 ** -24 + big * 2.0 ** -20), (b, g_loss[b], w_loss)
+            tol = T * T * (rel_sum(V) + (K + 16) * 2.0 ** -24 + big * 2.0 ** -20)
+            assert (np.abs(g_loss[:, b] - w_loss) <= tol).all(), (b, g_loss[:, b], w_loss)
         scale = T * float(up[b])
         half_ulp = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23
         for name, g, rel in (("fused", both, rel_sum(V)),
@@ -337,6 +337,50 @@ def test_distill_few_and_many_rows():
     check_distill(151936, "f32", "flat", True, 8, 1.0, B=5)
     check_distill(262149, "bf16", "flat", True, 32, 1.0, B=5)
     check_distill(515, "bf16", "flat", True, 8, 1.0, B=600)
+
+
+@pytest.mark.parametrize("B,V,dtype,masked,K,pad", [
+    (1500, 1003, "f32", True, 1024, 0),       # rows of a block in turn, a list longer than the row
+    (700, 9001, "bf16", True, 33, 3),         # ... off the 16-byte grid, the mask's bytes one by one
+    (400, 65536, "bf16", True, 64, 64),       # the mask by copies
+    (140, 40000, "f32", False, 5, 0),         # two blocks a row
+    (70, 100003, "bf16", True, 700, 5),       # four
+    (9, 262149, "bf16", False, 64, 0),        # eight
+])
+def test_distill_loss_alone_over_many_rows(B, V, dtype, masked, K, pad):
+    """The loss without a gradient streams rows through each cluster in turn."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(B)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = torch.full((B, V + pad), float("nan"), dtype=dt, device="cuda")[:, :V]
+    x.copy_(torch.randn((B, V), generator=g, device="cuda") * 3)
+    x[::7, ::5] = float("nan")
+    x[::5, 3] = float("-inf")
+    mask, xd = None, torch.where(torch.isnan(x), -np.inf, x.double())
+    if masked:
+        mask = torch.randint(-2 ** 31, 2 ** 31, (B, (V + 31) // 32), generator=g, device="cuda").to(torch.int32)
+        mask[B // 2] = 0
+        at = torch.arange(V, device="cuda")
+        xd = torch.where(((mask[:, at >> 5] >> (at & 31).int()) & 1).bool(), xd, -np.inf)
+    ids = torch.randint(0, V, (B, K), generator=g, device="cuda").int()
+    t = torch.randn((B, K), generator=g, device="cuda") * 2
+    ids[::3, K // 2] = -1
+    loss, lse = torch.empty(B, device="cuda"), torch.empty(B, device="cuda")
+    torch.cuda.synchronize()
+    ctx = ctx_of(V)
+    ctx.distill_loss(x, ids, t, loss, bitmask=mask, out_lse=lse, temp=1.25)
+    assert ctx.status() == 0
+    torch.cuda.synchronize()
+    w_lse = torch.logsumexp(xd / 1.25, 1)
+    xl = torch.where(ids >= 0, xd.gather(1, ids.clamp_min(0).long()), -np.inf)
+    q = torch.softmax(torch.where(xl > -np.inf, t.double(), -np.inf) / 1.25, 1)       # NaN where none is listed
+    log_q = torch.log_softmax(torch.where(xl > -np.inf, t.double(), -np.inf) / 1.25, 1)
+    w_loss = 1.25 ** 2 * torch.where(q > 0, q * (log_q - (xl / 1.25 - w_lse[:, None])), 0.0).sum(1)
+    live = w_lse > -np.inf
+    assert torch.equal(lse == -np.inf, ~live) and (loss[~live] == 0).all()
+    assert (torch.abs(lse - w_lse)[live] <= rel_sum(V) + w_lse[live].abs() * 2.0 ** -22).all()
+    # terms up to 40 nats, each good to 2^-21 of its size
+    assert (torch.abs(loss - w_loss)[live] <= 1.25 ** 2 * (rel_sum(V) + (K + 16) * 2.0 ** -24 + 40 * 2.0 ** -20)).all()
 
 
 def test_distill_gradient_against_differences():
