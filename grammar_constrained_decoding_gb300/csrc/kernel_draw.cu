@@ -26,6 +26,14 @@
 // nothing in it scores better).  If it is not, nothing at or below x_w is kept,
 // and the best of the rest is tried.  The first try succeeds with probability
 // top_p; after kTries the threshold is found by radix selection.
+//
+// What bounds it: instructions and the exchanges between blocks.  256 x 128256 bf16
+// (66 MB, 9.7 us to read) take 23.0 us for greedy rows, which read, sum and report
+// (2.9 TB/s); 37.3 with top-k 50 and top-p 0.9, which gather; 51.1 without a cut, which
+// read 131 MB of random numbers too and take a logarithm a token (3.9 TB/s); 59.6 with
+// top-p 0.9 at T = 0.7 and 82.6 with 0.95 at T = 1, where thousands of tokens a row
+// are scored and their masses added.  A single row of 32000 takes 8.3 us: a launch, a
+// row's copy and two exchanges, one after the other.
 #include "logit_row.cuh"
 
 namespace cgk {
@@ -59,9 +67,20 @@ struct DrawArgs {
 // min-p rows whose kept tokens cannot be more than this are gathered: the list
 // then overflows only by ties
 constexpr float kGatherCount = 768.f;
+// The nats that a peaked top-p row's first gather stays above the certain bound.
+// 256 x 128256 peaked rows, top-p 0.9 at T = 0.7 and 0.95 at T = 1: 2 nats 42.4 and 91.9
+// us, 3 38.8 and 83.6, 4 37.0 and 87.8
 constexpr float kGuess = 3.f;
+// After a guess that fell short: the mass below a cut falls off by about this a nat
 constexpr float kFallOff = 0.35f;
-constexpr float kFlat = 3.f;
+// Rows with less mass than this, in units of the maximum's, are peaked: they gather
+// first, the others sample masses.  256 x 128256, peaked rows at 0.9 and T = 0.7, at 0.95
+// and T = 1, flat rows at 0.9: 1.5 45.0, 80.3 and 59.3 us, 2 40.5, 81.2 and 59.6, 3 38.8,
+// 83.6 and 61.3; none 51.6, 78.4 and 59.0, all 39.3, 87.6 and 76.5
+constexpr float kFlat = 2.f;
+// Tries before the radix selection, which is taken where the random numbers rank the
+// tokens against their logits.  256 x 128256 peaked rows, 0.95 at T = 1: one try 174 us,
+// 16 83.6
 constexpr uint32_t kTries = 16;
 
 enum Mode : uint32_t { kNothing, kGather, kGuessFirst, kSample, kSpread };

@@ -121,19 +121,6 @@ __device__ __forceinline__ uint32_t add_remote(uint32_t a, uint32_t v) {
   asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
   return old;
 }
-__device__ __forceinline__ uint4 ld_remote4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ unsigned long long ld_remote64(uint32_t a) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ void ld_remote2(uint32_t a, unsigned long long& x, unsigned long long& y) {
   asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a) : "memory");
 }
@@ -1027,6 +1014,9 @@ struct Plan {
 // Blocks up to which a row is split further: two an SM.  64 x 32000, top-k 50 and top-p:
 // 10.5 us at one, 9.5 at two, 14.2 at four; 32 x 128256: 15.2, 11.5, 14.1.
 constexpr uint32_t kSlots = 2 * 152;
+// A row always fits kMaxGroups: a context takes vocabularies whose bitmask its mask
+// kernels hold in 48 KB, fewer than 393216 tokens.
+static_assert(kMaxCluster * kMaxGroups * kThreads * 4 >= 393216 + 8, "rows of floats");
 inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned, uint32_t full) {
   const uint32_t E = bf16 ? 8 : 4;
   const uint32_t runs = ((V + (aligned ? 0 : E - 1) + E - 1) / E + kThreads - 1) / kThreads;  // of kThreads groups

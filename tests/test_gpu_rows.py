@@ -522,6 +522,13 @@ def test_rows_beyond_32_bit_offsets():
         assert np.abs(x[b].double().cpu().numpy() - w_grad).max() <= 2.0 ** -8
 
 
+def test_longest_rows():
+    """Float rows as long as a context's vocabulary may be, off the 16-byte grid and masked."""
+    V = 388005
+    check_sample(V, "f32", "flat", True, B=2, settings=[(0.7, 0, 0.9, 0.0), (1.0, 50, 0.9, 0.0)], pad=1, shift=1)
+    check_distill(V, "f32", "flat", True, 8, 1.0, B=3, pad=1, shift=1)
+
+
 def test_example_runs_them_together():
     """examples/grammar_distill.py: generation under a grammar, the record, and a
     student that learns from it."""
