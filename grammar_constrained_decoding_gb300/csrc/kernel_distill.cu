@@ -5,52 +5,19 @@
 //   dloss/dx_v = T (p_v - sum_{k: id_k = v} q_k),
 // q the softmax of the teacher's listed logits / T, S = sum exp((x - m) / T).
 //
-// With a gradient the row is held on chip by a cluster (logit_row.cuh): the logits are
-// read from memory once and the gradient is written once from the registers.  Every
-// gradient is written as T w p_v first; the block that wrote a listed token's
-// writes it over after a block barrier.  All reads of the row's logits, the
-// listed ones by every block included, come before the cluster meets, all
-// writes after it, so the gradient may take the logits' place.  Without a gradient the
-// rows stream (below).
-//
-// What bounds them, of 2048 x 128256 bf16: the loss alone 83.6 us, 6.3 TB/s, the memory;
-// the gradient from the kept normaliser 178.9 us, 5.9 TB/s of reads and writes, nearly
-// so; loss and gradient 221.5 us, 4.7 TB/s: a block waits for its part, then for the
-// cluster's sums, then writes, and three of them on an SM do not always cover one
-// another.
+// A cluster takes rows in turn, its blocks the row's chunks in turn, through a ring of
+// chunks in shared memory that one warp of each block keeps filling across the rows'
+// ends (bulk copies).  Eight warps take the chunks; the rest read the rows' lists
+// meanwhile.  The logits are read from memory once and the gradient is written once.
+// Short rows and small batches with a gradient are held instead (logit_row.cuh).
+#include <algorithm>
+
 #include "logit_row.cuh"
 
 namespace cgk {
 namespace {
 
 using namespace row;
-
-// groups of a thread for many rows: 64 KB parts, three blocks an SM; fewer, longer
-// parts cost fewer exchanges and list look-ups.  Loss and gradient of 2048 x 128256: 8
-// groups 270.6 us, 12 237.9, 16 224.6, 24 274.0
-constexpr uint32_t kFull = 16;
-constexpr size_t kThird = 75 * 1024;  // shared memory of a block of three on an SM
-
-// The teacher's list in shared memory, K entries
-struct List {
-  uint32_t* id;     // listed ids that count, CG_NO_TOKEN for the others
-  float* t;         // teacher logits
-  float* x;         // the student's logits there
-  uint32_t* hash;   // slots of the repeated-id check, more than twice K
-  uint32_t slots;
-  __host__ __device__ static uint32_t slots_of(uint32_t K) {
-    uint32_t s = 4;
-    while (s < 2 * K) s <<= 1;
-    return s;
-  }
-  __host__ __device__ static size_t bytes(uint32_t K) { return (size_t(K) * 12 + size_t(slots_of(K)) * 4 + 15) & ~size_t(15); }
-  __device__ List(void* at, uint32_t K)
-      : id(static_cast<uint32_t*>(at)), t(reinterpret_cast<float*>(id + K)), x(t + K),
-        hash(reinterpret_cast<uint32_t*>(x + K)), slots(slots_of(K)) {}
-};
-struct DistillShared : Meet {
-  uint32_t repeated;
-};
 
 struct DistillArgs {
   const void* logits;
@@ -112,37 +79,577 @@ __device__ __forceinline__ void store_group(char* row, int t0, uint32_t V, bool 
   }
 }
 
-template <bool BF16, bool LOSS>
-__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs a, uint32_t nv) {
+// ---- the teacher's list -------------------------------------------------------------------
+
+// in shared memory, K entries
+struct List {
+  uint32_t* id;     // listed ids that count, CG_NO_TOKEN for the others
+  float* t;         // teacher logits
+  float* x;         // the student's logits there
+  __device__ List(void* at, uint32_t K) : id(static_cast<uint32_t*>(at)), t(reinterpret_cast<float*>(id + K)), x(t + K) {}
+  // reads entry k of row b; the teacher's logit where it counts, else -inf
+  template <bool BF16>
+  __device__ __forceinline__ float read(const DistillArgs& a, const Row<BF16>& r, uint32_t b, uint32_t k, bool report) const {
+    uint32_t i = a.ids[size_t(b) * a.K + k];
+    const float tk = teacher_logit(a.teacher[size_t(b) * a.K + k]);
+    float xk = -INFINITY;
+    if (i < a.V) xk = r.at(i);
+    else if (i != CG_NO_TOKEN && report) record_error(a.status, CG_DEV_BAD_TOKEN);
+    if (!(xk > -INFINITY) || !(tk > -INFINITY)) i = CG_NO_TOKEN;
+    id[k] = i;
+    x[k] = xk;
+    t[k] = tk;
+    return i == CG_NO_TOKEN ? -INFINITY : tk;
+  }
+  // Writes the gradient of entry k's token: tm, ts the list's maximum and sum, M and S
+  // the row's
+  template <bool BF16>
+  __device__ __forceinline__ void write(char* to, uint32_t k, uint32_t K, bool repeated, float tm, float ts, float M,
+                                        float S, float c, float scale) const {
+    float q = ex2((t[k] - tm) * c);
+    if (repeated) {  // every entry of the id writes the same sum
+      q = 0.f;
+      for (uint32_t j = 0; j < K; ++j)
+        if (id[j] == id[k]) q += ex2((t[j] - tm) * c);
+    }
+    store_grad<BF16>(to, id[k], scale * (__fdiv_rn(ex2((x[k] - M) * c), S) - __fdiv_rn(q, ts)));
+  }
+};
+// Repeated ids: every id claims a slot of the hash (more slots than ids, all CG_NO_TOKEN
+// at first); the second of equal ones finds it taken by itself
+__host__ __device__ inline uint32_t hash_slots(uint32_t K) {
+  uint32_t s = 4;
+  while (s < 2 * K) s <<= 1;
+  return s;
+}
+__device__ __forceinline__ bool claimed_before(uint32_t* hash, uint32_t slots, uint32_t id) {
+  for (uint32_t at = (id * 0x9E3779B1u) & (slots - 1);; at = (at + 1) & (slots - 1)) {
+    const uint32_t old = atomicCAS(hash + at, CG_NO_TOKEN, id);
+    if (old == CG_NO_TOKEN) return false;
+    if (old == id) return true;
+  }
+}
+
+// ---- the ring of chunks -------------------------------------------------------------------
+//
+// Chunk g of a row: WARPS * 32 * PER groups from group g on, group k * WARPS * 32 + t of
+// them thread t's.  A block's chunks of all its rows follow one another through the
+// slots; full: the chunk has landed, empty: every warp has taken it.
+
+constexpr uint32_t kTakers = 8;  // warps that take chunks
+template <bool BF16, uint32_t PER>
+struct Ring {
+  using F = Fmt<BF16>;
+  static constexpr uint32_t kGroups = kTakers * 32 * PER, kBytes = kGroups * 16, kBits = kGroups * F::E / 8;
+  uint64_t *full, *empty;
+  unsigned char *data, *bits;  // the chunks, and their part of the bitmask
+  uint32_t slots;
+  uint32_t slot = 0, turn = 0;
+  __device__ __forceinline__ Ring(uint64_t* f, uint64_t* e, unsigned char* memory, uint32_t count)
+      : full(f), empty(e), data(memory), bits(memory + count * kBytes), slots(count) {}
+  static size_t bytes(uint32_t count, bool mask) { return size_t(count) * (kBytes + (mask ? kBits : 0)); }
+  __device__ __forceinline__ void init() const {
+    for (uint32_t i = 0; i < slots; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kTakers);
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == slots) slot = 0, ++turn;
+  }
+  // the chunks' bits come by copies too: on the 16-byte grid, groups whole bytes or halves
+  static __device__ __forceinline__ bool copies_bits(const Row<BF16>& r) {
+    return r.mask && r.a == 0 && ((reinterpret_cast<uintptr_t>(r.mask) | (r.W * 4u)) & 15u) == 0;
+  }
+  static __device__ __forceinline__ uint32_t end(const Row<BF16>& r) { return (r.V + r.a + F::E - 1) / F::E; }
+  // One thread: this block's chunks of row r (of rank's, every n-th).  once: as Held::start.
+  __device__ __forceinline__ bool fill(const Row<BF16>& r, uint32_t n, uint32_t rank, bool once) {
+    const uint32_t lo = r.first_whole(), hi = r.end_whole();
+    const bool with_bits = copies_bits(r);
+    for (uint32_t g = rank * kGroups; g < end(r); g += n * kGroups, next()) {
+      if (turn && !mbar_wait(empty + slot, (turn - 1) & 1u)) return false;
+      const uint32_t from = max(g, lo), to = min(g + kGroups, hi), off = g * F::E / 8;
+      const uint32_t size = to > from ? (to - from) * 16u : 0u, more = with_bits ? min(kBits, r.W * 4u - off) : 0u;
+      mbar_expect_tx(full + slot, size + more);
+      unsigned char* at = data + slot * kBytes + (from - g) * 16;
+      if (size && once) bulk_g2s_hint(at, r.base + size_t(from) * 16, size, full + slot, evict_first_policy());
+      else if (size) bulk_g2s(at, r.base + size_t(from) * 16, size, full + slot);
+      if (more) bulk_g2s(bits + slot * kBits, r.mask + off, more, full + slot);
+    }
+    return true;
+  }
+  // after the last fill: all copies have landed, whatever the block's other warps do
+  __device__ __forceinline__ bool landed() const {
+    bool ok = true;
+    for (uint32_t i = 0; i < slots; ++i)
+      if (turn || i < slot) ok = mbar_wait(full + i, (i < slot ? turn : turn - 1) & 1u) && ok;
+    return ok;
+  }
+  __device__ __forceinline__ uint4* part(uint32_t at) const {
+    return reinterpret_cast<uint4*>(data + at * kBytes) + threadIdx.x;
+  }
+  // A taker: its groups of the chunk in the slot, by the rows' conventions, and their
+  // maximum.  kept: the chunk stays in its slot, as taken (wrote: something of it was
+  // written).  late: a wait ran out; none is begun any more.
+  template <bool KEPT>
+  __device__ __forceinline__ float take(const Row<BF16>& r, uint32_t g, uint4* v, bool& wrote, bool& late) const {
+    const uint32_t lo = r.first_whole(), hi = r.end_whole(), own = g + threadIdx.x;
+    const bool with_bits = copies_bits(r);
+    uint32_t allowed[PER];
+    if (r.mask && !with_bits) {
+#pragma unroll
+      for (uint32_t k = 0; k < PER; ++k) {
+        const uint32_t at = own + k * kTakers * 32;
+        allowed[k] = at < end(r) ? r.mask_bits(int(at * F::E) - int(r.a)) : 0u;
+      }
+    }
+    if (!late) late = !__all_sync(0xFFFFFFFFu, mbar_wait(full + slot, turn & 1u));
+    uint4* held = part(slot);
+#pragma unroll
+    for (uint32_t k = 0; k < PER; ++k) v[k] = held[k * kTakers * 32];
+    if (with_bits) {
+      const unsigned char* p = bits + slot * kBits + (BF16 ? threadIdx.x : threadIdx.x / 2);
+#pragma unroll
+      for (uint32_t k = 0; k < PER; ++k) allowed[k] = uint32_t(p[k * (kBits / PER)]) >> (BF16 ? 0u : (threadIdx.x & 1u) * 4u);
+    }
+    if (!KEPT) release();
+    bool changed = r.mask != nullptr;
+    if (g < lo || g + kGroups > hi) {  // groups that the copies do not bring
+      changed = true;
+#pragma unroll
+      for (uint32_t k = 0; k < PER; ++k) {
+        const uint32_t at = own + k * kTakers * 32;
+        if (at < lo || at >= hi) v[k] = r.edge(at);
+      }
+    }
+    if (r.mask) {
+#pragma unroll
+      for (uint32_t k = 0; k < PER; ++k) v[k] = r.masked(v[k], allowed[k]);
+    }
+    float t = groups_max_nan<BF16, PER>(v);
+    if (fkey(t) >= kKeyInf) {
+      changed = true;
+#pragma unroll
+      for (uint32_t k = 0; k < PER; ++k) v[k] = clean_group<BF16>(v[k]);
+      t = groups_max_nan<BF16, PER>(v);
+    }
+    if (KEPT && changed) {
+#pragma unroll
+      for (uint32_t k = 0; k < PER; ++k) held[k * kTakers * 32] = v[k];
+      wrote = true;
+    }
+    return t;
+  }
+  __device__ __forceinline__ void release() const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty + slot);
+  }
+};
+
+// ---- the loss alone ---------------------------------------------------------------------
+//
+// Nothing of a row is needed twice.  The warps send their maxima and sums of the
+// cluster's i-th row to block i mod n, where one more warp has read the row's list
+// meanwhile and finishes the row.  2048 x 128256 bf16: 83.6 us, 6.3 TB/s, bound by the
+// memory.
+//
+// Few barriers and many loads at once: 8 groups of a thread a chunk.  Of 2048 x 128256
+// bf16, masked too: 16 warps x 2 groups x 6 chunks 93.7 and 108.8 us, 8 x 4 x 6 83.9 and
+// 95.5, 8 x 8 x 3 83.6 and 86.2, three blocks of 8 x 4 x 4 an SM 86.8 and 90.8.
+constexpr uint32_t kLossPer = 8;       // groups of a thread in a chunk
+constexpr uint32_t kLossSlots = 3;     // chunks on their way or being taken, at most
+constexpr uint32_t kLossBlocks = 2 * 152;  // resident
+constexpr size_t kHalfSmem = 113 * 1024;   // of a block of two on an SM
+constexpr uint32_t kLossThreads = (kTakers + 2) * 32;
+// Few rows are split over clusters of 2, 4 or 8 blocks as long as all are resident
+// together (36 clusters of 8, 74 of 4).  Microseconds of B x 128256 bf16 by cluster
+// size, at 16 warps x 2 groups x 6 chunks:
+//   B      1     2     4     8    16
+//   512  30.3  31.4  30.8  37.1  66.5
+//   128  16.0  11.4  12.1  13.6
+//   64   13.1  10.4   8.2   9.1
+//   32          8.1   7.1   6.0
+//   4                 5.4   4.4   4.3
+constexpr uint32_t kLossCluster = 8, kLossSplit = 288;
+
+struct LossShared {
+  uint64_t full[kLossSlots], empty[kLossSlots];
+  uint64_t bar_rec[2];                // by turns of this block's rows
+  uint64_t done[kLossCluster][2];     // ... of each block's: their records have been read
+  __align__(16) Record rec[2][kLossCluster * kTakers];
+};
+// ... then the list's logits, teacher's and student's, and the ring
+__host__ __device__ constexpr size_t loss_fixed(uint32_t K) { return sizeof(LossShared) + ((size_t(K) * 8 + 15) & ~size_t(15)); }
+
+template <bool BF16>
+__global__ void __launch_bounds__(kLossThreads, 2) loss_kernel(const DistillArgs a, uint32_t B, uint32_t slots) {
   extern __shared__ __align__(16) unsigned char smem[];
-  DistillShared& s = *reinterpret_cast<DistillShared*>(smem);
-  const List l(smem + sizeof(DistillShared), a.K);
+  LossShared& s = *reinterpret_cast<LossShared*>(smem);
+  static_assert(sizeof(LossShared) % 16 == 0, "the list and the ring lie behind it");
+  float* list_t = reinterpret_cast<float*>(smem + sizeof(LossShared));  // -inf where an entry does not count
+  float* list_x = list_t + a.K;
+  using R = Ring<BF16, kLossPer>;
+  R ring(s.full, s.empty, smem + loss_fixed(a.K), slots);
+  griddep_launch_dependents();
+  const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t first = blockIdx.x / n, step = gridDim.x / n, rows = (B - first + step - 1) / step;
+  if (tid == 0) {
+    ring.init();
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(s.bar_rec + i, 1);
+      for (uint32_t r = 0; r < kLossCluster; ++r) mbar_init(&s.done[r][i], 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  may_send();
+  griddep_wait();
+  const float T = a.temp, c = exp_scale(T);
+  auto row = [&](uint32_t i) { return Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, first + i * step); };
+  bool late = false;
+  if (warp == kTakers) {  // fills the ring
+    if (lane == 0) {
+      for (uint32_t i = 0; i < rows && !late; ++i) late = !ring.fill(row(i), n, rank, true);
+      late = !ring.landed() || late;
+    }
+    __syncwarp();
+    ready_others();
+  } else if (warp < kTakers) {
+    for (uint32_t i = 0; i < rows; ++i) {
+      const Row<BF16> r = row(i);
+      float tm = -INFINITY;
+      float2 acc = {};
+      bool wrote;
+#pragma unroll 1
+      for (uint32_t g = rank * R::kGroups; g < R::end(r); g += n * R::kGroups, ring.next()) {
+        uint4 v[kLossPer];
+        const float t = ring.template take<false>(r, g, v, wrote, late);
+        add_groups<BF16, kLossPer>(v, t, c, tm, acc);
+      }
+      if (i == 0) ready_others();
+      const unsigned long long rec = warp_record(tm, acc.x + acc.y, c);
+      const uint32_t home = i % n, use = i / n;  // of the home's records, by turns in two buffers
+      if (lane == 0) {
+        if (use >= 2 && !late) late = !wait_sent(&s.done[home][use & 1u], (use / 2 - 1) & 1u);
+        send(at_rank(&s.rec[use & 1u][rank * kTakers + warp], home), rec, at_rank(s.bar_rec + (use & 1u), home));
+      }
+      late = __any_sync(0xFFFFFFFFu, late);
+    }
+  } else {  // finishes the rows that are this block's
+    const uint32_t K = a.K;
+    ready_others();
+    for (uint32_t i = rank; i < rows; i += n) {
+      const uint32_t b = first + i * step, use = i / n;
+      const Row<BF16> r = row(i);
+      if (lane == 0 && !late) mbar_expect_tx(s.bar_rec + (use & 1u), n * kTakers * uint32_t(sizeof(Record)));
+      float tm = -INFINITY;
+#pragma unroll 4
+      for (uint32_t k = lane; k < K; k += 32) {
+        const uint32_t id = a.ids[size_t(b) * K + k];
+        const float t = teacher_logit(a.teacher[size_t(b) * K + k]);
+        const float x = id < a.V ? r.at(id) : -INFINITY;
+        if (id >= a.V && id != CG_NO_TOKEN) record_error(a.status, CG_DEV_BAD_TOKEN);
+        const bool counts = x > -INFINITY && t > -INFINITY;
+        list_x[k] = x;
+        list_t[k] = counts ? t : -INFINITY;
+        if (counts) tm = fmaxf(tm, t);
+      }
+      tm = warp_reduce(tm, MaxOp());
+      const bool listed = tm > -INFINITY;
+      float ts = 0.f;
+      for (uint32_t k = lane; k < K; k += 32)
+        if (list_t[k] > -INFINITY) ts += ex2((list_t[k] - tm) * c);
+      ts = warp_reduce(ts, SumOp());
+      if (!late) late = !__all_sync(0xFFFFFFFFu, wait_sent(s.bar_rec + (use & 1u), (use / 2) & 1u));
+      float M, S;
+      merge(s.rec[use & 1u], n * kTakers, c, M, S);
+      __syncwarp();
+      if (i + 2 * n < rows && lane < n) {  // the buffer is used again
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         at_rank(&s.done[rank][use & 1u], lane))
+                     : "memory");
+      }
+      const float log_ts = logf(ts), log_s = logf(S);
+      float part = 0.f;
+      for (uint32_t k = lane; k < K; k += 32)
+        if (list_t[k] > -INFINITY) part += loss_term(list_t[k] - tm, ts, log_ts, list_x[k] - M, log_s, c, T);
+      part = warp_reduce(part, SumOp());
+      if (lane == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, log_s);
+    }
+  }
+  if (late) record_error(a.status, CG_DEV_TIMEOUT);
+  __syncwarp();
+  cluster_sync(n);  // what others send arrives, and so do their signals
+}
+
+// ---- the gradient, and the loss with it ---------------------------------------------------
+//
+// A block's chunks of a row stay in the ring until their gradient is written.  With the
+// loss the warps take them once for the row's maximum and sum, tell every block
+// of the cluster, and take them again for the gradient; with the kept normaliser the
+// second pass is the only one.  Every gradient is written as T w p_v first; the lists'
+// warps write the listed tokens' over after the row.  They also tell the cluster when
+// they have read the row's listed logits, before which nothing of it is written: the
+// gradient may take the logits' place.  (That keeps a cluster's blocks side by side, too:
+// without it the gradient alone of 512 x 151936 took 63.8 us, with it 57.4.)
+//
+// 2048 x 128256 bf16: loss and gradient 195 us, 5.4 TB/s of reads and writes, the
+// gradient alone 174, 6.0 TB/s: the memory, and with the loss the exchange of a row's
+// sums, which the next row's copies cover only in part (at 96 KB a block two chunks
+// of six are ahead).  Clusters of 6 and 8 blocks with two or three chunks each are not
+// all resident together: 397 and 472 us.
+constexpr uint32_t kGradPer = 4;       // groups of a thread in a chunk
+constexpr uint32_t kGradSlots = 12;    // at most
+constexpr uint32_t kListWarps = 4;
+constexpr uint32_t kListThreads = kListWarps * 32;
+constexpr uint32_t kGradThreads = (kTakers + 1) * 32 + kListThreads;
+
+struct GradShared {
+  uint64_t full[kGradSlots], empty[kGradSlots];
+  uint64_t bar_rec[2], bar_list[2], bar_done[2];   // by turns of the rows: the cluster's records and notes, this
+                                                   // block's list, its takers' stores
+  __align__(16) Record rec[2][kMaxCluster * kTakers];
+  uint32_t note[2][kMaxCluster];
+  float tm[2], ts[2];                              // the list's maximum (-inf: none listed) and sum
+  uint32_t repeated[2];
+  float red[kListWarps];
+};
+// ... then two lists, the hash and the ring
+__host__ __device__ inline size_t grad_fixed(uint32_t K) {
+  return (sizeof(GradShared) + size_t(K) * 24 + size_t(hash_slots(K)) * 4 + 15) & ~size_t(15);
+}
+
+__device__ __forceinline__ void list_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kListThreads) : "memory"); }
+template <typename Op>
+__device__ __forceinline__ float list_fold(float v, Op op, float* red) {
+  v = warp_reduce(v, op);
+  const uint32_t w = (threadIdx.x >> 5) - (kTakers + 1);
+  if ((threadIdx.x & 31) == 0) red[w] = v;
+  list_sync();
+  v = op(op(red[0], red[1]), op(red[2], red[3]));
+  list_sync();
+  return v;
+}
+static_assert(kListWarps == 4, "the fold above");
+
+template <bool BF16, bool LOSS>
+__global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs a, uint32_t B, uint32_t slots) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  GradShared& s = *reinterpret_cast<GradShared*>(smem);
+  const uint32_t K = a.K;
+  unsigned char* lists = smem + sizeof(GradShared);
+  uint32_t* hash = reinterpret_cast<uint32_t*>(lists + size_t(K) * 24);
+  using R = Ring<BF16, kGradPer>;
+  R ring(s.full, s.empty, smem + grad_fixed(K), slots);
+  griddep_launch_dependents();
+  const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t first = blockIdx.x / n, step = gridDim.x / n, rows = (B - first + step - 1) / step;
+  const uint32_t told = n * (LOSS ? kTakers * uint32_t(sizeof(Record)) + 4u : 4u);  // bytes of a row's records and notes
+  if (tid == 0) {
+    ring.init();
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(s.bar_rec + i, 1);
+      mbar_init(s.bar_list + i, 1);
+      mbar_init(s.bar_done + i, kTakers);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // armed once a phase: the first two rows here, the others when the phase before is over
+    mbar_expect_tx(s.bar_rec, told);
+    mbar_expect_tx(s.bar_rec + 1, told);
+  }
+  __syncthreads();
+  may_send();
+  griddep_wait();
+  const float T = a.temp, c = exp_scale(T);
+  auto row = [&](uint32_t i) { return Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, first + i * step); };
+  auto out = [&](uint32_t i) {
+    return static_cast<char*>(a.grad) + size_t(first + i * step) * a.ld_grad * Fmt<BF16>::kSize;
+  };
+  bool late = false;
+  if (warp == kTakers) {  // fills the ring
+    if (lane == 0) {
+      for (uint32_t i = 0; i < rows && !late; ++i) late = !ring.fill(row(i), n, rank, false);
+      late = !ring.landed() || late;
+    }
+    __syncwarp();
+    ready_others();
+  } else if (warp < kTakers) {
+    for (uint32_t i = 0; i < rows; ++i) {
+      const Row<BF16> r = row(i);
+      const uint32_t b = first + i * step, buf = i & 1u, parity = (i / 2) & 1u;
+      const float up = a.up ? a.up[b] : 1.f;
+      float M = LOSS ? 0.f : a.lse_in[b] * T, S = 1.f;  // p = exp2((x - M) c) / S
+      bool wrote = false;
+      if (LOSS) {
+        R ahead = ring;
+        float tm = -INFINITY;
+        float2 acc = {};
+#pragma unroll 1
+        for (uint32_t g = rank * R::kGroups; g < R::end(r); g += n * R::kGroups, ahead.next()) {
+          uint4 v[kGradPer];
+          const float t = ahead.template take<true>(r, g, v, wrote, late);
+          add_groups<BF16, kGradPer>(v, t, c, tm, acc);
+        }
+        if (i == 0) ready_others();
+        const unsigned long long rec = warp_record(tm, acc.x + acc.y, c);
+        if (lane < n) send(at_rank(&s.rec[buf][rank * kTakers + warp], lane), rec, at_rank(s.bar_rec + buf, lane));
+      } else if (i == 0) {
+        ready_others();
+      }
+      if (!late) late = !__all_sync(0xFFFFFFFFu, mbar_wait(s.bar_list + buf, parity) &&
+                                                 wait_sent(s.bar_rec + buf, parity));
+      if (LOSS) merge(s.rec[buf], n * kTakers, c, M, S);
+      const bool listed = s.tm[buf] > -INFINITY;
+      const float w = __fdiv_rn(listed ? T * up : 0.f, S);
+      char* to = out(i);
+      const bool wide = ((reinterpret_cast<uintptr_t>(to) / Fmt<BF16>::kSize - r.a) & (Fmt<BF16>::E - 1)) == 0;
+      const float2 nm = make_float2(-M, -M), c2 = make_float2(c, c), w2 = make_float2(w, w);
+#pragma unroll 1
+      for (uint32_t g = rank * R::kGroups; g < R::end(r); g += n * R::kGroups, ring.next()) {
+        uint4 v[kGradPer];
+        if (LOSS) {
+          const uint4* held = ring.part(ring.slot);
+#pragma unroll
+          for (uint32_t k = 0; k < kGradPer; ++k) v[k] = held[k * kTakers * 32];
+          // what this thread wrote there comes before the next copy
+          if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          ring.release();
+        } else {
+          ring.template take<false>(r, g, v, wrote, late);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kGradPer; ++k) {
+          const uint32_t at = g + k * kTakers * 32 + tid;
+          float2 d[Fmt<BF16>::E / 2];
+#pragma unroll
+          for (uint32_t q = 0; q < Fmt<BF16>::E / 2; ++q) {
+            d[q] = make_float2(0.f, 0.f);
+            if (listed) d[q] = __fmul2_rn(ex2_pair(__fmul2_rn(__fadd2_rn(pair<BF16>(v[k], q), nm), c2)), w2);
+          }
+          if (at < R::end(r)) store_group<BF16>(to, int(at * Fmt<BF16>::E) - int(r.a), a.V, wide, d);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s.bar_done + buf);
+    }
+  } else {  // the lists
+    const uint32_t lt = tid - (kTakers + 1) * 32, size = hash_slots(K);
+    auto read = [&](uint32_t i) {  // row i's, its maximum, sum and repeated ids
+      const Row<BF16> r = row(i);
+      const uint32_t b = first + i * step, buf = i & 1u;
+      const List l(lists + buf * size_t(K) * 12, K);
+      for (uint32_t k = lt; k < size; k += kListThreads) hash[k] = CG_NO_TOKEN;
+      if (lt == 0) s.repeated[buf] = 0;
+      float tm = -INFINITY;
+#pragma unroll 2
+      for (uint32_t k = lt; k < K; k += kListThreads) tm = fmaxf(tm, l.read<BF16>(a, r, b, k, rank == 0));
+      tm = list_fold(tm, MaxOp(), s.red);
+      float ts = 0.f;
+      for (uint32_t k = lt; k < K; k += kListThreads) {
+        const uint32_t id = l.id[k];
+        if (id == CG_NO_TOKEN) continue;
+        ts += ex2((l.t[k] - tm) * c);
+        if (claimed_before(hash, size, id)) s.repeated[buf] = 1;
+      }
+      ts = list_fold(ts, SumOp(), s.red);
+      if (lt == 0) {
+        s.tm[buf] = tm;
+        s.ts[buf] = ts;
+        mbar_arrive(s.bar_list + buf);
+      }
+    };
+    auto tell = [&](uint32_t i) {  // after what of the buffer's former row has been read here
+      if (lt < n) send(at_rank(&s.note[i & 1u][rank], lt), 1u, at_rank(s.bar_rec + (i & 1u), lt));
+    };
+    read(0);
+    ready_others();
+    tell(0);
+    for (uint32_t i = 0; i < rows; ++i) {
+      const uint32_t b = first + i * step, buf = i & 1u, parity = (i / 2) & 1u;
+      if (i + 1 < rows) read(i + 1);
+      if (!late) late = !__all_sync(0xFFFFFFFFu, wait_sent(s.bar_rec + buf, parity));
+      float M = LOSS ? 0.f : a.lse_in[b] * T, S = 1.f;
+      if (LOSS) merge(s.rec[buf], n * kTakers, c, M, S);
+      list_sync();
+      if (!late && lt == 0 && i + 2 < rows) mbar_expect_tx(s.bar_rec + buf, told);
+      if (i + 1 < rows) tell(i + 1);
+      const Row<BF16> r = row(i);
+      const List l(lists + buf * size_t(K) * 12, K);
+      const float tm = s.tm[buf], ts = s.ts[buf];
+      const bool listed = tm > -INFINITY;
+      if (LOSS && rank == 0) {
+        float part = 0.f;
+        const float log_ts = logf(ts), log_s = logf(S);
+        for (uint32_t k = lt; k < K; k += kListThreads)
+          if (l.id[k] != CG_NO_TOKEN) part += loss_term(l.t[k] - tm, ts, log_ts, l.x[k] - M, log_s, c, T);
+        part = list_fold(part, SumOp(), s.red);
+        if (lt == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, log_s);
+      }
+      if (!late) late = !__all_sync(0xFFFFFFFFu, mbar_wait(s.bar_done + buf, parity));
+      if (listed) {
+        const bool repeated = s.repeated[buf] != 0;
+        const float scale = T * (a.up ? a.up[b] : 1.f);
+        char* to = out(i);
+        for (uint32_t k = lt; k < K; k += kListThreads) {
+          const uint32_t id = l.id[k];
+          if (id == CG_NO_TOKEN || ((id + r.a) / Fmt<BF16>::E / R::kGroups) % n != rank) continue;
+          l.write<BF16>(to, k, K, repeated, tm, ts, M, S, c, scale);
+        }
+      }
+      list_sync();  // the next list takes this one's place
+    }
+  }
+  if (late) record_error(a.status, CG_DEV_TIMEOUT);
+  __syncwarp();
+  cluster_sync(n);
+}
+
+// ---- the gradient of short rows and small batches -------------------------------------------
+//
+// Where a cluster has one row, or rows of a chunk or two, there is nothing to stream: the
+// blocks hold the row (logit_row.cuh) and more of them share an SM.
+//
+// Microseconds, held and streamed, loss and gradient, then the gradient alone (bf16):
+//   4096 x 12000    78.3   87.6     51.4   58.3
+//   4096 x 20000    94.7   94.1     64.9   65.3
+//   1024 x 32000    37.5   36.1     31.6   28.3
+//   64 x 64006       9.2    8.0      7.1    7.9
+//   64 x 128256     14.0   10.9     10.9   11.3
+//   128 x 128256    23.7   18.1     19.3   16.3
+//   2048 x 128256  221.2  195.0    177.9  173.9
+constexpr uint64_t kShortRow = 48 << 10, kSmallLoss = 6 << 20, kSmallGrad = 16 << 20;  // bytes
+// Groups of a thread for many rows: 64 KB parts, three blocks an SM.
+constexpr uint32_t kFull = 16;
+constexpr size_t kThird = 75 * 1024;  // shared memory of a block of three on an SM
+
+struct HeldShared : Meet {
+  uint32_t repeated;
+};
+// ... then the list, the hash and the part
+__host__ __device__ inline size_t held_fixed(uint32_t K) {
+  return (sizeof(HeldShared) + size_t(K) * 12 + size_t(hash_slots(K)) * 4 + 15) & ~size_t(15);
+}
+
+template <bool BF16, bool LOSS>
+__global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, uint32_t nv) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  HeldShared& s = *reinterpret_cast<HeldShared*>(smem);
+  const List l(smem + sizeof(HeldShared), a.K);
+  uint32_t* hash = reinterpret_cast<uint32_t*>(smem + sizeof(HeldShared) + size_t(a.K) * 12);
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), b = blockIdx.x / n, tid = threadIdx.x, K = a.K;
   begin(s);
-  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, 
-               smem + sizeof(DistillShared) + List::bytes(K));
+  Held<BF16> h(Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b), nv, smem + held_fixed(K));
   griddep_wait();
   h.start(s, false);
   may_send();
   const float T = a.temp, c = exp_scale(T);
   // the teacher's list
-  const uint32_t slots = l.slots;
-  for (uint32_t i = tid; i < slots; i += kThreads) l.hash[i] = CG_NO_TOKEN;
+  const uint32_t slots = hash_slots(K);
+  for (uint32_t i = tid; i < slots; i += kThreads) hash[i] = CG_NO_TOKEN;
   if (tid == 0) s.repeated = 0;
   float tm = -INFINITY;
-  for (uint32_t k = tid; k < K; k += kThreads) {
-    uint32_t id = a.ids[size_t(b) * K + k];
-    const float t = teacher_logit(a.teacher[size_t(b) * K + k]);
-    float x = -INFINITY;
-    if (id < a.V) x = h.r.at(id);
-    else if (id != CG_NO_TOKEN && rank == 0) record_error(a.status, CG_DEV_BAD_TOKEN);
-    if (!(x > -INFINITY) || !(t > -INFINITY)) id = CG_NO_TOKEN;
-    l.id[k] = id;
-    l.x[k] = x;
-    l.t[k] = t;
-    if (id != CG_NO_TOKEN) tm = fmaxf(tm, t);
-  }
+  for (uint32_t k = tid; k < K; k += kThreads) tm = fmaxf(tm, l.read<BF16>(a, h.r, b, k, rank == 0));
   tm = block_max(tm, s.red_f);
   const bool listed = tm > -INFINITY;
   float ts = 0.f;
@@ -150,16 +657,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
     const uint32_t id = l.id[k];
     if (id == CG_NO_TOKEN) continue;
     ts += ex2((l.t[k] - tm) * c);
-    // repeated ids: every id claims a slot (more slots than ids), the second
-    // of equal ones finds it taken by itself
-    for (uint32_t at = (id * 0x9E3779B1u) & (slots - 1);; at = (at + 1) & (slots - 1)) {
-      const uint32_t old = atomicCAS(l.hash + at, CG_NO_TOKEN, id);
-      if (old == CG_NO_TOKEN) break;
-      if (old == id) {
-        s.repeated = 1;
-        break;
-      }
-    }
+    if (claimed_before(hash, slots, id)) s.repeated = 1;
   }
   __syncthreads();
   ts = block_sum(ts, s.red_f);
@@ -224,248 +722,85 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
     if (id == CG_NO_TOKEN) continue;
     const uint32_t g = (id + h.r.a) / Fmt<BF16>::E;
     if ((g / kThreads) % n != rank) continue;
-    float q = ex2((l.t[k] - tm) * c);
-    if (repeated) {  // every entry of the id writes the same sum
-      q = 0.f;
-      for (uint32_t j = 0; j < K; ++j)
-        if (l.id[j] == id) q += ex2((l.t[j] - tm) * c);
-    }
-    store_grad<BF16>(row, id, scale * (__fdiv_rn(ex2((l.x[k] - M) * c), S) - __fdiv_rn(q, ts)));
+    l.write<BF16>(row, k, K, repeated, tm, ts, M, S, c, scale);
   }
-}
-
-// ---- the loss alone ---------------------------------------------------------------------
-//
-// Nothing of a row is needed twice, so it streams: a cluster takes rows in turn, its
-// blocks the row's chunks in turn, through a ring of chunks that one warp keeps
-// filling across the rows' ends.  The warps send their maxima and sums of row i to
-// block i mod n, where one more warp has read the row's list meanwhile and finishes
-// the row.
-// Few barriers and many loads at once: 8 groups of a thread a chunk.  Of 2048 x 128256
-// bf16, masked too: 16 warps x 2 groups x 6 chunks 93.7 and 108.8 us, 8 x 4 x 6 83.9 and
-// 95.5, 8 x 8 x 3 83.6 and 86.2, three blocks of 8 x 4 x 4 an SM 86.8 and 90.8.
-constexpr uint32_t kStreamWarps = 8;   // that take chunks
-constexpr uint32_t kPer = 8;           // groups of a thread in a chunk
-constexpr uint32_t kRing = 3;          // chunks on their way or being taken, at most
-constexpr uint32_t kStreamBlocks = 2;  // an SM
-constexpr uint32_t kStreamSlots = kStreamBlocks * 152;
-constexpr size_t kStreamSmem = 113 * 1024;  // of a block
-constexpr uint32_t kStreamThreads = (kStreamWarps + 2) * 32;
-constexpr uint32_t kChunkGroups = kStreamWarps * 32 * kPer;
-// Few rows are split over clusters of 2, 4 or 8 blocks as long as all are resident
-// together (36 clusters of 8, 74 of 4).  Microseconds of B x 128256 bf16 by cluster
-// size, at 16 warps x 2 groups x 6 chunks:
-//   B      1     2     4     8    16
-//   512  30.3  31.4  30.8  37.1  66.5
-//   128  16.0  11.4  12.1  13.6
-//   64   13.1  10.4   8.2   9.1
-//   32          8.1   7.1   6.0
-//   4                 5.4   4.4   4.3
-constexpr uint32_t kStreamCluster = 8, kStreamSplit = 288;
-
-struct StreamShared {
-  uint64_t full[kRing], empty[kRing];
-  uint64_t bar_rec[2];                  // by turns of this block's rows
-  uint64_t done[kStreamCluster][2];        // ... of each block's: their records have been read
-  Record rec[2][kStreamCluster * kStreamWarps];
-};
-// ... then the list's logits, teacher's and student's, and the ring: its chunks, their bits
-size_t stream_smem(uint32_t K, uint32_t ring, uint32_t bits) {
-  return sizeof(StreamShared) + ((size_t(K) * 8 + 15) & ~size_t(15)) + size_t(ring) * (kChunkGroups * 16 + bits);
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kStreamThreads, kStreamBlocks) stream_loss_kernel(const DistillArgs a, uint32_t B,
-                                                                                       uint32_t chunks) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  using F = Fmt<BF16>;
-  constexpr uint32_t kBytes = kChunkGroups * 16, kBits = kChunkGroups * F::E / 8;
-  StreamShared& s = *reinterpret_cast<StreamShared*>(smem);
-  static_assert(sizeof(StreamShared) % 16 == 0, "the list and the ring lie behind it");
-  float* list_t = reinterpret_cast<float*>(smem + sizeof(StreamShared));  // -inf where an entry does not count
-  float* list_x = list_t + a.K;
-  unsigned char* ring = smem + sizeof(StreamShared) + ((a.K * 8 + 15) & ~15u);
-  unsigned char* ring_bits = ring + chunks * kBytes;
-  griddep_launch_dependents();
-  const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t first = blockIdx.x / n, step = gridDim.x / n;
-  if (tid == 0) {
-    for (uint32_t i = 0; i < chunks; ++i) {
-      mbar_init(s.full + i, 1);
-      mbar_init(s.empty + i, kStreamWarps);
-    }
-    for (uint32_t i = 0; i < 2; ++i) {
-      mbar_init(s.bar_rec + i, 1);
-      for (uint32_t r = 0; r < kStreamCluster; ++r) mbar_init(&s.done[r][i], 1);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-  may_send();
-  griddep_wait();
-  const float T = a.temp, c = exp_scale(T);
-  auto row = [&](uint32_t b) { return Row<BF16>(a.logits, a.ld, a.bitmask, a.W, a.V, b); };
-  auto groups = [&](const Row<BF16>& r) { return (a.V + r.a + F::E - 1) / F::E; };
-  auto copied = [&](const Row<BF16>& r) {  // the chunks' bits come by copies
-    return r.mask && r.a == 0 && ((reinterpret_cast<uintptr_t>(r.mask) | (a.W * 4u)) & 15u) == 0;
-  };
-  bool ok = true;
-  if (warp == kStreamWarps) {  // fills the ring
-    if (lane == 0) {
-      const uint64_t policy = evict_first_policy();
-      uint32_t slot = 0, turn = 0;
-      for (uint32_t b = first; ok && b < B; b += step) {
-        const Row<BF16> r = row(b);
-        const uint32_t lo = r.first_whole(), hi = r.end_whole(), end = groups(r);
-        const bool bits = copied(r);
-        for (uint32_t g = rank * kChunkGroups; g < end; g += n * kChunkGroups) {
-          if (turn && !(ok = mbar_wait(s.empty + slot, (turn - 1) & 1u))) break;
-          const uint32_t from = max(g, lo), to = min(g + kChunkGroups, hi), off = g * F::E / 8;
-          const uint32_t bytes = to > from ? (to - from) * 16u : 0u, more = bits ? min(kBits, a.W * 4u - off) : 0u;
-          mbar_expect_tx(s.full + slot, bytes + more);
-          if (bytes)
-            bulk_g2s_hint(ring + slot * kBytes + (from - g) * 16, r.base + size_t(from) * 16, bytes, s.full + slot, policy);
-          if (more) bulk_g2s(ring_bits + slot * kBits, r.mask + off, more, s.full + slot);
-          if (++slot == chunks) slot = 0, ++turn;
-        }
-      }
-      for (uint32_t i = 0; i < chunks; ++i)  // all have landed when the block ends, whatever its other warps did
-        if (turn || i < slot) ok = mbar_wait(s.full + i, (i < slot ? turn : turn - 1) & 1u) && ok;
-    }
-    __syncwarp();
-    ready_others();
-  } else if (warp < kStreamWarps) {
-    uint32_t slot = 0, turn = 0, i = 0;
-    for (uint32_t b = first; ok && b < B; b += step, ++i) {
-      const Row<BF16> r = row(b);
-      const uint32_t lo = r.first_whole(), hi = r.end_whole(), end = groups(r);
-      const bool bits = copied(r);
-      float tm = -INFINITY;
-      float2 acc = {};
-#pragma unroll 1
-      for (uint32_t g = rank * kChunkGroups; g < end; g += n * kChunkGroups) {
-        uint32_t allowed[kPer];
-        if (r.mask && !bits) {
-#pragma unroll
-          for (uint32_t k = 0; k < kPer; ++k) {
-            const uint32_t own = g + k * kStreamWarps * 32 + tid;
-            allowed[k] = own < end ? r.mask_bits(int(own * F::E) - int(r.a)) : 0u;
-          }
-        }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(s.full + slot, turn & 1u));
-        if (!ok) break;
-        uint4 v[kPer];
-        const uint4* part = reinterpret_cast<const uint4*>(ring + slot * kBytes) + tid;
-#pragma unroll
-        for (uint32_t k = 0; k < kPer; ++k) v[k] = part[k * kStreamWarps * 32];
-        if (bits) {
-          const unsigned char* p = ring_bits + slot * kBits + (BF16 ? tid : tid / 2);
-#pragma unroll
-          for (uint32_t k = 0; k < kPer; ++k)
-            allowed[k] = uint32_t(p[k * (kBits / kPer)]) >> (BF16 ? 0u : (tid & 1u) * 4u);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s.empty + slot);
-        if (++slot == chunks) slot = 0, ++turn;
-        if (g < lo || g + kChunkGroups > hi) {  // groups that the copies do not bring
-#pragma unroll
-          for (uint32_t k = 0; k < kPer; ++k) {
-            const uint32_t own = g + k * kStreamWarps * 32 + tid;
-            if (own < lo || own >= hi) v[k] = r.edge(own);
-          }
-        }
-        if (r.mask) {
-#pragma unroll
-          for (uint32_t k = 0; k < kPer; ++k) v[k] = r.masked(v[k], allowed[k]);
-        }
-        float t = groups_max_nan<BF16, kPer>(v);
-        if (fkey(t) >= kKeyInf) {
-#pragma unroll
-          for (uint32_t k = 0; k < kPer; ++k) v[k] = clean_group<BF16>(v[k]);
-          t = groups_max_nan<BF16, kPer>(v);
-        }
-        add_groups<BF16, kPer>(v, t, c, tm, acc);
-      }
-      if (i == 0) ready_others();
-      if (!ok) break;
-      const unsigned long long rec = warp_record(tm, acc.x + acc.y, c);
-      const uint32_t home = i % n, use = i / n;  // of the home's records, by turns in two buffers
-      if (lane == 0) {
-        if (use >= 2) ok = wait_sent(&s.done[home][use & 1u], (use / 2 - 1) & 1u);
-        send(at_rank(&s.rec[use & 1u][rank * kStreamWarps + warp], home), rec, at_rank(s.bar_rec + (use & 1u), home));
-      }
-      ok = __all_sync(0xFFFFFFFFu, ok);
-    }
-  } else {  // finishes the rows that are this block's
-    const uint32_t K = a.K, rows = (B - first + step - 1) / step;
-    ready_others();
-    for (uint32_t i = rank; i < rows; i += n) {
-      const uint32_t b = first + i * step, use = i / n;
-      const Row<BF16> r = row(b);
-      if (lane == 0) mbar_expect_tx(s.bar_rec + (use & 1u), n * kStreamWarps * uint32_t(sizeof(Record)));
-      float tm = -INFINITY;
-#pragma unroll 4
-      for (uint32_t k = lane; k < K; k += 32) {
-        const uint32_t id = a.ids[size_t(b) * K + k];
-        const float t = teacher_logit(a.teacher[size_t(b) * K + k]);
-        const float x = id < a.V ? r.at(id) : -INFINITY;
-        if (id >= a.V && id != CG_NO_TOKEN) record_error(a.status, CG_DEV_BAD_TOKEN);
-        const bool counts = x > -INFINITY && t > -INFINITY;
-        list_x[k] = x;
-        list_t[k] = counts ? t : -INFINITY;
-        if (counts) tm = fmaxf(tm, t);
-      }
-      tm = warp_reduce(tm, MaxOp());
-      const bool listed = tm > -INFINITY;
-      float ts = 0.f;
-      for (uint32_t k = lane; k < K; k += 32)
-        if (list_t[k] > -INFINITY) ts += ex2((list_t[k] - tm) * c);
-      ts = warp_reduce(ts, SumOp());
-      ok = __all_sync(0xFFFFFFFFu, wait_sent(s.bar_rec + (use & 1u), (use / 2) & 1u));
-      if (!ok) break;
-      float M, S;
-      merge(s.rec[use & 1u], n * kStreamWarps, c, M, S);
-      __syncwarp();
-      if (i + 2 * n < rows && lane < n) {  // the buffer is used again
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                         at_rank(&s.done[rank][use & 1u], lane))
-                     : "memory");
-      }
-      const float log_ts = logf(ts), log_s = logf(S);
-      float part = 0.f;
-      for (uint32_t k = lane; k < K; k += 32)
-        if (list_t[k] > -INFINITY) part += loss_term(list_t[k] - tm, ts, log_ts, list_x[k] - M, log_s, c, T);
-      part = warp_reduce(part, SumOp());
-      if (lane == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, log_s);
-    }
-  }
-  if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
-  __syncwarp();
-  cluster_sync(n);  // what others send arrives, and so do their signals
-}
-
-template <bool BF16>
-cudaError_t launch_stream(int device, uint32_t B, const DistillArgs& a, cudaStream_t stream) {
-  const uint32_t chunks = (a.V / Fmt<BF16>::E + kChunkGroups) / kChunkGroups;
+cudaError_t launch_loss(int device, uint32_t B, const DistillArgs& a, cudaStream_t stream) {
+  using R = Ring<BF16, kLossPer>;
+  const uint32_t chunks = (a.V / Fmt<BF16>::E + R::kGroups) / R::kGroups;
   uint32_t n = 1;
-  while (n < kStreamCluster && 2 * n <= chunks && uint64_t(B) * 2 * n <= kStreamSplit) n *= 2;
-  const uint32_t bits = a.bitmask ? kChunkGroups * Fmt<BF16>::E / 8 : 0;
-  uint32_t ring = kRing;
-  while (stream_smem(a.K, ring, bits) > kStreamSmem) --ring;
-  return launch_clusters<stream_loss_kernel<BF16>>(device, n == 1 && B > kStreamSlots ? kStreamSlots : B, n, kStreamThreads,
-                                                  stream_smem(a.K, ring, bits), stream, a, B, ring);
+  while (n < kLossCluster && 2 * n <= chunks && uint64_t(B) * 2 * n <= kLossSplit) n *= 2;
+  uint32_t slots = kLossSlots;
+  while (loss_fixed(a.K) + R::bytes(slots, a.bitmask) > kHalfSmem) --slots;
+  return launch_clusters<loss_kernel<BF16>>(device, n == 1 && B > kLossBlocks ? kLossBlocks : B, n, kLossThreads,
+                                            loss_fixed(a.K) + R::bytes(slots, a.bitmask), stream, a, B, slots);
+}
+
+// Clusters of n = 1, 2, 4, 8, 16 blocks that are resident together, asked once per n and
+// blocks an SM (which smem decides); 0 and an error where the device cannot tell
+template <auto Kernel>
+uint32_t resident(int device, uint32_t n, size_t smem, cudaError_t& e) {
+  static std::atomic<int> known[2][5];
+  std::atomic<int>& k = known[smem > kHalfSmem][__builtin_ctz(n)];
+  int clusters = k.load(std::memory_order_relaxed);
+  e = cudaSuccess;
+  if (clusters == 0) {
+    e = raise_limits<Kernel>(device);
+    const ClusterLaunch l(1, n, kGradThreads, smem > kHalfSmem ? kMaxSmem : kHalfSmem, nullptr);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, Kernel, &l.cfg);
+    if (e == cudaSuccess && clusters <= 0) e = cudaErrorInvalidConfiguration;
+    if (e != cudaSuccess) return 0;
+    k.store(clusters, std::memory_order_relaxed);
+  }
+  return uint32_t(clusters);
+}
+
+template <bool BF16, bool LOSS>
+cudaError_t launch_grad(int device, uint32_t B, const DistillArgs& a, cudaStream_t stream) {
+  using R = Ring<BF16, kGradPer>;
+  constexpr uint32_t E = Fmt<BF16>::E;
+  const uint32_t chunks = ((a.V + 2 * E - 2) / E + R::kGroups - 1) / R::kGroups;
+  const size_t fixed = grad_fixed(a.K);
+  uint32_t slots = 0, n = 1;
+  // a row has to fit the cluster's rings (with the loss): the longest take one block an SM
+  for (size_t limit : {kHalfSmem, size_t(kMaxSmem)}) {
+    slots = std::min(kGradSlots, uint32_t((limit - fixed) / R::bytes(1, a.bitmask)));
+    n = 1;
+    while (n < kMaxCluster && n * slots < chunks) n *= 2;
+    if (n * slots >= chunks) break;
+  }
+  while (n < kLossCluster && 2 * n <= chunks && uint64_t(B) * 2 * n <= kLossSplit) n *= 2;
+  const size_t smem = fixed + R::bytes(slots, a.bitmask);
+  cudaError_t e;
+  const uint32_t at_once = resident<grad_kernel<BF16, LOSS>>(device, n, smem, e);
+  if (e != cudaSuccess) return e;
+  return launch_clusters<grad_kernel<BF16, LOSS>>(device, std::min(B, at_once), n, kGradThreads, smem, stream, a, B,
+                                                       slots);
 }
 
 template <bool BF16>
-cudaError_t launch_distill(int device, uint32_t B, const DistillArgs& a, bool loss, cudaStream_t stream) {
-  if (!a.grad) return launch_stream<BF16>(device, B, a, stream);
-  const size_t fixed = sizeof(DistillShared) + List::bytes(a.K);
+cudaError_t launch_held(int device, uint32_t B, const DistillArgs& a, bool loss, cudaStream_t stream) {
+  const size_t fixed = held_fixed(a.K);
   uint32_t full = kFull;
   while (full > 1 && fixed + part_bytes(BF16, full, a.bitmask) > kThird) --full;
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), full);
   const size_t smem = fixed + part_bytes(BF16, plan.nv, a.bitmask);
-  return loss ? launch_clusters<distill_kernel<BF16, true>>(device, B, plan.n, kThreads, smem, stream, a, plan.nv)
-              : launch_clusters<distill_kernel<BF16, false>>(device, B, plan.n, kThreads, smem, stream, a, plan.nv);
+  return loss ? launch_clusters<held_kernel<BF16, true>>(device, B, plan.n, kThreads, smem, stream, a, plan.nv)
+              : launch_clusters<held_kernel<BF16, false>>(device, B, plan.n, kThreads, smem, stream, a, plan.nv);
+}
+// whether rows with a gradient stream
+bool streams(bool bf16, uint32_t V, uint32_t B, bool loss) {
+  const uint64_t row = uint64_t(V) * (bf16 ? 2 : 4);
+  return row > kShortRow && row * B > (loss ? kSmallLoss : kSmallGrad);
+}
+
+template <bool BF16>
+cudaError_t launch_distill(int device, uint32_t B, const DistillArgs& a, bool loss, cudaStream_t stream) {
+  if (!a.grad) return launch_loss<BF16>(device, B, a, stream);
+  if (!streams(BF16, a.V, B, loss)) return launch_held<BF16>(device, B, a, loss, stream);
+  return loss ? launch_grad<BF16, true>(device, B, a, stream) : launch_grad<BF16, false>(device, B, a, stream);
 }
 
 int distill(cg_ctx* c, const char* call, const DistillArgs& base, int dtype, uint32_t B, bool loss) {

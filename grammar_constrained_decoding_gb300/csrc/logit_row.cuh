@@ -1026,12 +1026,30 @@ inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned, uint32_t f
   return {(runs + n - 1) / n, n};
 }
 
-// Launches Kernel on clusters of n blocks, `rows` of them.  The kernel's shared
-// memory and cluster size limits are raised on the first launch on a device.
+// A launch of clusters of n blocks
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2] = {};
+  ClusterLaunch(uint32_t clusters, uint32_t n, uint32_t threads, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(clusters * n);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = n;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+// The kernel's shared memory and cluster size limits are raised on its first launch on
+// a device.
 constexpr int kMaxSmem = 227 * 1024;
-template <auto Kernel, typename... Args>
-cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, uint32_t threads, size_t smem, cudaStream_t stream,
-                            Args&&... args) {
+template <auto Kernel>
+cudaError_t raise_limits(int device) {
   static std::atomic<uint64_t> raised{0};
   const uint64_t bit = uint64_t(1) << (device & 63);
   if (!(raised.load(std::memory_order_relaxed) & bit)) {
@@ -1040,21 +1058,15 @@ cudaError_t launch_clusters(int device, uint32_t rows, uint32_t n, uint32_t thre
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(rows * n);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = n;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, Kernel, std::forward<Args>(args)...);
+  return cudaSuccess;
+}
+template <auto Kernel, typename... Args>
+cudaError_t launch_clusters(int device, uint32_t clusters, uint32_t n, uint32_t threads, size_t smem,
+                            cudaStream_t stream, Args&&... args) {
+  const cudaError_t e = raise_limits<Kernel>(device);
+  if (e != cudaSuccess) return e;
+  ClusterLaunch l(clusters, n, threads, smem, stream);
+  return cudaLaunchKernelEx(&l.cfg, Kernel, std::forward<Args>(args)...);
 }
 
 }  // namespace row

@@ -383,6 +383,64 @@ def test_distill_loss_alone_over_many_rows(B, V, dtype, masked, K, pad):
     assert (torch.abs(loss - w_loss)[live] <= 1.25 ** 2 * (rel_sum(V) + (K + 16) * 2.0 ** -24 + 40 * 2.0 ** -20)).all()
 
 
+@pytest.mark.parametrize("B,V,dtype,masked,K,pad,inplace", [
+    (1500, 1003, "f32", True, 1024, 0, False),
+    (1500, 1003, "bf16", False, 64, 2, True),
+    (700, 40001, "bf16", True, 33, 0, False),
+    (420, 65536, "bf16", True, 64, 64, True),
+    (400, 200000, "bf16", False, 300, 0, False),
+    (300, 70003, "f32", True, 1024, 3, True),
+    (150, 40960, "f32", True, 20, 0, False),
+])
+def test_distill_gradient_over_many_rows(B, V, dtype, masked, K, pad, inplace):
+    """Each cluster takes several rows in turn: the gradient with the loss and alone."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(B)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = torch.full((B, V + pad), float("nan"), dtype=dt, device="cuda")[:, :V]
+    x.copy_(torch.randn((B, V), generator=g, device="cuda") * 2)
+    x[::5, 3] = float("-inf")
+    mask = None
+    if masked:
+        mask = torch.randint(-2 ** 31, 2 ** 31, (B, (V + 31) // 32), generator=g, device="cuda").to(torch.int32)
+        mask[B // 2] = 0
+    ids = torch.randint(0, V, (B, K), generator=g, device="cuda").int()
+    t = torch.randn((B, K), generator=g, device="cuda") * 2
+    ids[::3, K // 2] = -1
+    ids[1] = -1
+    up = torch.randn(B, generator=g, device="cuda")
+    loss, lse = torch.empty(B, device="cuda"), torch.empty(B, device="cuda")
+    ctx, src, grads = ctx_of(V), x.clone(), []
+    for alone in (False, True):
+        here = src.clone() if inplace else x
+        dx = here if inplace else torch.full((B, V + pad), float("nan"), dtype=dt, device="cuda")[:, :V]
+        if alone:
+            ctx.distill_grad(here, ids, t, lse, dx, temp=1.25, bitmask=mask, grad_loss=up)
+        else:
+            ctx.distill_loss(here, ids, t, loss, temp=1.25, bitmask=mask, out_lse=lse, out_grad=dx, grad_loss=up)
+        grads.append(dx)
+    assert ctx.status() == 0
+    half_ulp = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23
+    for lo in range(0, B, 200):
+        rows = slice(lo, min(lo + 200, B))
+        xd = src[rows].double()
+        if masked:
+            at = torch.arange(V, device="cuda")
+            xd = torch.where(((mask[rows][:, at >> 5] >> (at & 31).int()) & 1).bool(), xd, -np.inf)
+        p = torch.nan_to_num(torch.softmax(xd / 1.25, 1))
+        i = ids[rows]
+        xl = torch.where(i >= 0, xd.gather(1, i.clamp_min(0).long()), -np.inf)
+        q = torch.nan_to_num(torch.softmax(torch.where(xl > -np.inf, t[rows].double(), -np.inf) / 1.25, 1))
+        any_listed = (xl > -np.inf).any(1, keepdim=True)
+        q_v = torch.zeros_like(xd).scatter_add_(1, i.clamp_min(0).long(), torch.where(i >= 0, q, 0.0))
+        scale = 1.25 * up[rows].double()[:, None]
+        want = torch.where(any_listed, scale * (p - q_v), 0.0)
+        w_lse = torch.logsumexp(xd / 1.25, 1, keepdim=True).nan_to_num(neginf=0.0)
+        tol = want.abs() * half_ulp + scale.abs() * (p + q_v) * (rel_sum(V) + (w_lse.abs() + 1) * 2.0 ** -20 + 64 * 2.0 ** -24) + 1e-37
+        for dx in grads:
+            assert ((dx[rows].double() - want).abs() <= tol).all(), (lo, (dx[rows].double() - want).abs().max())
+
+
 def test_distill_gradient_against_differences():
     """Autograd through distill() on float logits against central differences of
     the 64-bit loss (step 1e-4: truncation about 1e-8; the kernel's 32 bits give
