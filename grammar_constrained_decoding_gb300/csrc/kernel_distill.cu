@@ -86,10 +86,12 @@ struct List {
   uint32_t* id;     // listed ids that count, CG_NO_TOKEN for the others
   float* t;         // teacher logits
   float* x;         // the student's logits there
-  __device__ List(void* at, uint32_t K) : id(static_cast<uint32_t*>(at)), t(reinterpret_cast<float*>(id + K)), x(t + K) {}
+  __device__ List(void* at, uint32_t K)
+      : id(static_cast<uint32_t*>(at)), t(reinterpret_cast<float*>(id + K)), x(t + K) {}
   // reads entry k of row b; the teacher's logit where it counts, else -inf
   template <bool BF16>
-  __device__ __forceinline__ float read(const DistillArgs& a, const Row<BF16>& r, uint32_t b, uint32_t k, bool report) const {
+  __device__ __forceinline__ float read(const DistillArgs& a, const Row<BF16>& r, uint32_t b, uint32_t k,
+                                        bool report) const {
     uint32_t i = a.ids[size_t(b) * a.K + k];
     const float tk = teacher_logit(a.teacher[size_t(b) * a.K + k]);
     float xk = -INFINITY;
@@ -210,9 +212,9 @@ struct Ring {
     if (with_bits) {
       const unsigned char* p = bits + slot * kBits + (BF16 ? threadIdx.x : threadIdx.x / 2);
 #pragma unroll
-      for (uint32_t k = 0; k < PER; ++k) allowed[k] = uint32_t(p[k * (kBits / PER)]) >> (BF16 ? 0u : (threadIdx.x & 1u) * 4u);
+      for (uint32_t k = 0; k < PER; ++k)
+        allowed[k] = uint32_t(p[k * (kBits / PER)]) >> (BF16 ? 0u : (threadIdx.x & 1u) * 4u);
     }
-    if (!KEPT) release();
     bool changed = r.mask != nullptr;
     if (g < lo || g + kGroups > hi) {  // groups that the copies do not bring
       changed = true;
@@ -240,9 +242,17 @@ struct Ring {
     }
     return t;
   }
-  __device__ __forceinline__ void release() const {
+  // This warp has taken the chunk in the slot.  An arrival may overtake loads that are
+  // still queued behind stores, so it follows an instruction that needs their
+  // results: t, the chunk's maximum by the rows' conventions, which is never +inf.
+  __device__ __forceinline__ void release(float t) const {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(empty + slot);
+    if ((threadIdx.x & 31) == 0)
+      asm volatile(
+          "{\n .reg .pred p;\n setp.neu.f32 p, %1, 0f7F800000;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(
+              smem_addr(empty + slot)),
+          "f"(t)
+          : "memory");
   }
 };
 
@@ -279,7 +289,9 @@ struct LossShared {
   __align__(16) Record rec[2][kLossCluster * kTakers];
 };
 // ... then the list's logits, teacher's and student's, and the ring
-__host__ __device__ constexpr size_t loss_fixed(uint32_t K) { return sizeof(LossShared) + ((size_t(K) * 8 + 15) & ~size_t(15)); }
+__host__ __device__ constexpr size_t loss_fixed(uint32_t K) {
+  return sizeof(LossShared) + ((size_t(K) * 8 + 15) & ~size_t(15));
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kLossThreads, 2) loss_kernel(const DistillArgs a, uint32_t B, uint32_t slots) {
@@ -324,6 +336,7 @@ __global__ void __launch_bounds__(kLossThreads, 2) loss_kernel(const DistillArgs
       for (uint32_t g = rank * R::kGroups; g < R::end(r); g += n * R::kGroups, ring.next()) {
         uint4 v[kLossPer];
         const float t = ring.template take<false>(r, g, v, wrote, late);
+        ring.release(t);
         add_groups<BF16, kLossPer>(v, t, c, tm, acc);
       }
       if (i == 0) ready_others();
@@ -444,7 +457,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t first = blockIdx.x / n, step = gridDim.x / n, rows = (B - first + step - 1) / step;
-  const uint32_t told = n * (LOSS ? kTakers * uint32_t(sizeof(Record)) + 4u : 4u);  // bytes of a row's records and notes
+  // bytes of a row's records and notes
+  const uint32_t told = n * (LOSS ? kTakers * uint32_t(sizeof(Record)) + 4u : 4u);
   if (tid == 0) {
     ring.init();
     for (uint32_t i = 0; i < 2; ++i) {
@@ -513,9 +527,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
           for (uint32_t k = 0; k < kGradPer; ++k) v[k] = held[k * kTakers * 32];
           // what this thread wrote there comes before the next copy
           if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          ring.release();
+          ring.release(groups_max_nan<BF16, kGradPer>(v));
         } else {
-          ring.template take<false>(r, g, v, wrote, late);
+          ring.release(ring.template take<false>(r, g, v, wrote, late));
         }
 #pragma unroll
         for (uint32_t k = 0; k < kGradPer; ++k) {

@@ -116,7 +116,8 @@ __device__ uint32_t threshold_by_levels(Shared& s, uint32_t n, uint32_t rank, Ke
   const uint32_t top = fkey(M);
   uint32_t tau = fkey(cut), level = 0;
   unsigned long long above;
-  if (q.k) tau = select_key(s, n, [&](auto f) { keys([&](uint32_t key) { f(key, 1ull); }); }, tau, top, q.k, level, above);
+  if (q.k)
+    tau = select_key(s, n, [&](auto f) { keys([&](uint32_t key) { f(key, 1ull); }); }, tau, top, q.k, level, above);
   if (q.p >= 1.f) return tau;
   unsigned long long kept = mass_total(S);
   if (q.k) {  // the mass of what top-k keeps
@@ -155,7 +156,8 @@ struct Drawn {
 // With the number of entries above each (its place) and the masses added up by
 // place, an entry stays when fewer than k are above it and less than the target's
 // mass; the random numbers are on their way meanwhile.
-__device__ Drawn draw_pairs(Shared& s, const unsigned long long* list, uint32_t c, const RowSettings& q, float M, float scale, float S, const float* u) {
+__device__ Drawn draw_pairs(Shared& s, const unsigned long long* list, uint32_t c, const RowSettings& q, float M,
+                            float scale, float S, const float* u) {
   const uint32_t tid = threadIdx.x;
   const unsigned long long e = tid < c ? list[tid] : 0ull;
   const float x = fkey_inv(uint32_t(e >> 32)), ut = tid < c ? u[best_id(e)] : 0.5f;
@@ -721,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
 template <bool BF16>
 cudaError_t launch_draw(int device, uint32_t B, const DrawArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
-  return launch_clusters<draw_kernel<BF16>>(device, B, plan.n, kThreads, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
-                                            a, plan.nv);
+  return launch_clusters<draw_kernel<BF16>>(device, B, plan.n, kThreads,
+                                            sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream, a, plan.nv);
 }
 
 }  // namespace

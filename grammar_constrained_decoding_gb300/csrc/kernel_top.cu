@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
 template <bool BF16>
 cudaError_t launch_top(int device, uint32_t B, const TopArgs& a, cudaStream_t stream) {
   const Plan plan = plan_row(BF16, a.V, B, rows_on_grid(a.logits, BF16 ? CG_BF16 : CG_F32, a.ld), kFull);
-  return launch_clusters<top_kernel<BF16>>(device, B, plan.n, kThreads, sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream,
-                                           a, plan.nv);
+  return launch_clusters<top_kernel<BF16>>(device, B, plan.n, kThreads,
+                                           sizeof(Shared) + part_bytes(BF16, plan.nv, a.bitmask), stream, a, plan.nv);
 }
 
 }  // namespace

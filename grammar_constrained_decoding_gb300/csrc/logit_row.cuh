@@ -1,5 +1,5 @@
 // Rows of logits held on chip, the frame of the per-row operators
-// (sample_rows, top_logprobs, distill).
+// (sample_rows, top_logprobs, and distill's gradient of short rows and small batches).
 //
 // A row belongs to a cluster of n <= 16 blocks of 256 threads.  Each block copies
 // its part once into shared memory (bulk copies completing on mbarriers), and
@@ -99,7 +99,8 @@ __device__ __forceinline__ void send(uint32_t a, uint4 v, uint32_t bar) {
 }
 // Asks for [from, to) of global memory to be brought to L2 (whole 16-byte pieces of it)
 __device__ __forceinline__ void prefetch_l2(const void* from, const void* to) {
-  const uintptr_t a = (reinterpret_cast<uintptr_t>(from) + 15) & ~uintptr_t(15), b = reinterpret_cast<uintptr_t>(to) & ~uintptr_t(15);
+  const uintptr_t a = (reinterpret_cast<uintptr_t>(from) + 15) & ~uintptr_t(15);
+  const uintptr_t b = reinterpret_cast<uintptr_t>(to) & ~uintptr_t(15);
   if (b > a) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(uint32_t(b - a)) : "memory");
 }
 // bounded wait for what others have sent

@@ -595,6 +595,29 @@ def test_example_runs_them_together():
     assert 0.0 <= final < 0.5 * first
 
 
+@pytest.mark.parametrize("V,dtype,B", [(200000, "bf16", 400), (70003, "f32", 300)])
+def test_streamed_rows_give_the_same_bits_every_time(V, dtype, B):
+    """Many rows through each ring, under the load of the gradient's stores: no chunk is
+    replaced before it has been read."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn((B, V), generator=g, device="cuda") * 2).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    ids = torch.randint(0, V, (B, 300), generator=g, device="cuda").int()
+    t = torch.randn((B, 300), generator=g, device="cuda")
+    ctx, first = ctx_of(V), None
+    for _ in range(40):
+        loss, loss2, lse = (torch.empty(B, device="cuda") for _ in range(3))
+        both, alone = torch.empty_like(x), torch.empty_like(x)
+        ctx.distill_loss(x, ids, t, loss, out_lse=lse)
+        ctx.distill_loss(x, ids, t, loss2, out_grad=both)
+        ctx.distill_grad(x, ids, t, lse, alone)
+        got = [loss, lse, loss2, both, alone]
+        if first is None:
+            first = got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+    assert ctx.status() == 0
+
+
 def test_repeated_calls_give_the_same_bits():
     import torch
     V, B = 128256, 12
