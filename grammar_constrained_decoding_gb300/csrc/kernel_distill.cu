@@ -260,7 +260,7 @@ struct Ring {
 //
 // Nothing of a row is needed twice.  The warps send their maxima and sums of the
 // cluster's i-th row to block i mod n, where one more warp has read the row's list
-// meanwhile and finishes the row.  2048 x 128256 bf16: 83.6 us, 6.3 TB/s, bound by the
+// meanwhile and finishes the row.  2048 x 128256 bf16: 83.0 us, 6.3 TB/s, bound by the
 // memory.
 //
 // Few barriers and many loads at once: 8 groups of a thread a chunk.  Of 2048 x 128256
@@ -404,13 +404,14 @@ __global__ void __launch_bounds__(kLossThreads, 2) loss_kernel(const DistillArgs
 // warps write the listed tokens' over after the row.  They also tell the cluster when
 // they have read the row's listed logits, before which nothing of it is written: the
 // gradient may take the logits' place.  (That keeps a cluster's blocks side by side, too:
-// without it the gradient alone of 512 x 151936 took 63.8 us, with it 57.4.)
+// without it the gradient alone of 512 x 151936 took 63.8 us, with it 57.2.)
 //
-// 2048 x 128256 bf16: loss and gradient 195 us, 5.4 TB/s of reads and writes, the
-// gradient alone 174, 6.0 TB/s: the memory, and with the loss the exchange of a row's
-// sums, which the next row's copies cover only in part (at 96 KB a block two chunks
-// of six are ahead).  Clusters of 6 and 8 blocks with two or three chunks each are not
-// all resident together: 397 and 472 us.
+// 2048 x 128256 bf16: loss and gradient 201.5 us, 5.2 TB/s of reads and writes; the
+// gradient alone 171.5, 6.1 TB/s.  The memory bounds them, and with the loss the exchange
+// of a row's sums, which the next row's copies cover only in part: of a block's six chunks
+// two are ahead.  Fetching a chunk's values before the stores of the one before: 218 us.
+// Clusters of 6 and 8 blocks with three or two chunks each are not all resident together:
+// 397 and 472 us.
 constexpr uint32_t kGradPer = 4;       // groups of a thread in a chunk
 constexpr uint32_t kGradSlots = 12;    // at most
 constexpr uint32_t kListWarps = 4;
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
 //   64 x 64006       9.2    8.0      7.1    7.9
 //   64 x 128256     14.0   10.9     10.9   11.3
 //   128 x 128256    23.7   18.1     19.3   16.3
-//   2048 x 128256  221.2  195.0    177.9  173.9
+//   2048 x 128256  221.2  201.5    177.9  171.5
 constexpr uint64_t kShortRow = 48 << 10, kSmallLoss = 6 << 20, kSmallGrad = 16 << 20;  // bytes
 // Groups of a thread for many rows: 64 KB parts, three blocks an SM.
 constexpr uint32_t kFull = 16;
