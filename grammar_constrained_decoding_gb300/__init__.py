@@ -161,9 +161,11 @@ class Ctx:
 
     def __init__(self, grammars: list[Grammar], vocab: Vocab, stream=None):
         import torch
+        from . import _rows
         if stream is None:
             stream = torch.cuda.current_stream()
         self.stream = stream
+        self._rows = _rows  # an import in every call would be a twentieth of the smallest
         arr = (C.c_void_p * len(grammars))(*[g._h.value for g in grammars])
         h = C.c_void_p()
         L.check("cg_ctx_create", L.lib().cg_ctx_create(arr, len(grammars), vocab._h, C.c_void_p(stream.cuda_stream),
@@ -272,26 +274,25 @@ class Ctx:
         own ([B] tensors or None), drawn with the given random numbers uniform
         [B, V] (a [1, V] or expanded tensor shares one row; None for an all-greedy
         batch); out_logprob receives log p of the token before any cut."""
-        from . import _rows as R
-        call, B, W = "cg_sample_rows", logits.shape[0], self.W
+        R, call, B, W = self._rows, "cg_sample_rows", logits.shape[0], self.W
         x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
         u, ldu = None, 0
         if uniform is not None:
             shared = uniform.shape[0] == 1
             u, ldu = R.rows_of(call, uniform, "uniform", R.F32, (1 if shared else B, self.V))
             ldu = 0 if shared else ldu
+        each = (B,)
         rc = L.lib().cg_sample_rows(
             self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, W)),
-            R.opt(call, temp, "temp", R.F32, (B,)), R.opt(call, top_k, "top_k", R.U32, (B,)),
-            R.opt(call, top_p, "top_p", R.F32, (B,)), R.opt(call, min_p, "min_p", R.F32, (B,)), u, ldu,
-            R.want(call, out_tok, "out_tok", R.U32, (B,)), R.opt(call, out_logprob, "out_logprob", R.F32, (B,)))
+            R.opt(call, temp, "temp", R.F32, each), R.opt(call, top_k, "top_k", R.U32, each),
+            R.opt(call, top_p, "top_p", R.F32, each), R.opt(call, min_p, "min_p", R.F32, each), u, ldu,
+            R.want(call, out_tok, "out_tok", R.U32, each), R.opt(call, out_logprob, "out_logprob", R.F32, each))
         L.check(call, rc)
 
     def top_logprobs(self, logits, out_ids, out_logprobs, bitmask=None, out_lse=None) -> None:
         """The n best allowed tokens of each row (n = out_ids.shape[1]), best
         first, with their log-probabilities."""
-        from . import _rows as R
-        call, B, n = "cg_top_logprobs", logits.shape[0], out_ids.shape[1]
+        R, call, B, n = self._rows, "cg_top_logprobs", logits.shape[0], out_ids.shape[1]
         x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
         rc = L.lib().cg_top_logprobs(
             self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)), n,
@@ -303,8 +304,7 @@ class Ctx:
                      out_grad=None, grad_loss=None) -> None:
         """Loss of each row against the teacher's listed tokens (ids, teacher
         [B, K]); with out_grad also the gradient by the logits, times grad_loss [B]."""
-        from . import _rows as R
-        call, B, K = "cg_distill_loss", logits.shape[0], ids.shape[1]
+        R, call, B, K = self._rows, "cg_distill_loss", logits.shape[0], ids.shape[1]
         x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
         g, ldg = (None, 0) if out_grad is None else R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
         rc = L.lib().cg_distill_loss(
@@ -317,8 +317,7 @@ class Ctx:
     def distill_grad(self, logits, ids, teacher, lse, out_grad, temp: float = 1.0, bitmask=None,
                      grad_loss=None) -> None:
         """The gradient alone, from the normaliser distill_loss left in out_lse."""
-        from . import _rows as R
-        call, B, K = "cg_distill_grad", logits.shape[0], ids.shape[1]
+        R, call, B, K = self._rows, "cg_distill_grad", logits.shape[0], ids.shape[1]
         x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
         g, ldg = R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
         rc = L.lib().cg_distill_grad(
