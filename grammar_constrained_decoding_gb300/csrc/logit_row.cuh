@@ -1012,8 +1012,14 @@ inline size_t part_bytes(bool bf16, uint32_t nv, bool mask) {
 struct Plan {
   uint32_t nv, n;
 };
-// Blocks up to which a row is split further: two an SM.  64 x 32000, top-k 50 and top-p:
-// 10.5 us at one, 9.5 at two, 14.2 at four; 32 x 128256: 15.2, 11.5, 14.1.
+// Blocks up to which a row is split further, over 2, 4, 8 or 16 blocks (clusters of
+// other sizes take longer to meet): two an SM, for 16 blocks one an SM and three
+// groups a thread at least.  Microseconds, top-k 50 with top-p, then top-p alone:
+//   64 x 32000    by blocks at one, two, four an SM   10.5   9.5  14.2
+//   1 x 32000     8 blocks 7.5 and 8.9, 12 7.7 and 9.3, 16 8.1 and 9.5
+//   1 x 128256    8 blocks 8.4 and 10.1, 12 8.6 and 10.3, 16 7.8 and 9.7
+//   12 x 128256   8 blocks 9.0 and 12.3, 16 9.0 and 13.8
+//   32 x 128256   8 blocks 11.2 and 16.0, 9 11.7 and 17.2
 constexpr uint32_t kSlots = 2 * 152;
 // A row always fits kMaxGroups: a context takes vocabularies whose bitmask its mask
 // kernels hold in 48 KB, fewer than 393216 tokens.
@@ -1023,7 +1029,10 @@ inline Plan plan_row(bool bf16, uint32_t V, uint32_t B, bool aligned, uint32_t f
   const uint32_t runs = ((V + (aligned ? 0 : E - 1) + E - 1) / E + kThreads - 1) / kThreads;  // of kThreads groups
   uint32_t n = (runs + full - 1) / full;
   if (n > kMaxCluster) n = kMaxCluster;
-  while (n < kMaxCluster && n < runs && uint64_t(B) * (n + 1) <= kSlots) ++n;
+  for (uint32_t k = 2; k <= kMaxCluster; k *= 2) {
+    const bool wide = k == kMaxCluster;
+    if (k > n && k <= runs && uint64_t(B) * k <= (wide ? kSlots / 2 : kSlots) && (!wide || runs >= 3 * k)) n = k;
+  }
   return {(runs + n - 1) / n, n};
 }
 
