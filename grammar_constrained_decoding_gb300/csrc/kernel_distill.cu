@@ -88,20 +88,43 @@ struct List {
   float* x;         // the student's logits there
   __device__ List(void* at, uint32_t K)
       : id(static_cast<uint32_t*>(at)), t(reinterpret_cast<float*>(id + K)), x(t + K) {}
-  // reads entry k of row b; the teacher's logit where it counts, else -inf
+  // A thread reads its entries of row b: k, k + step and so on; the largest teacher's
+  // logit that counts, else -inf.  Several at a time where there are more, so that their
+  // loads are under way together.
   template <bool BF16>
-  __device__ __forceinline__ float read(const DistillArgs& a, const Row<BF16>& r, uint32_t b, uint32_t k,
+  __device__ __forceinline__ float read(const DistillArgs& a, const Row<BF16>& r, uint32_t b, uint32_t k, uint32_t step,
                                         bool report) const {
-    uint32_t i = a.ids[size_t(b) * a.K + k];
-    const float tk = teacher_logit(a.teacher[size_t(b) * a.K + k]);
-    float xk = -INFINITY;
-    if (i < a.V) xk = r.at(i);
-    else if (i != CG_NO_TOKEN && report) record_error(a.status, CG_DEV_BAD_TOKEN);
-    if (!(xk > -INFINITY) || !(tk > -INFINITY)) i = CG_NO_TOKEN;
-    id[k] = i;
-    x[k] = xk;
-    t[k] = tk;
-    return i == CG_NO_TOKEN ? -INFINITY : tk;
+    return a.K <= step ? read_by<BF16, 1>(a, r, b, k, step, report) : read_by<BF16, 4>(a, r, b, k, step, report);
+  }
+  template <bool BF16, uint32_t kBatch>
+  __device__ __forceinline__ float read_by(const DistillArgs& a, const Row<BF16>& r, uint32_t b, uint32_t k,
+                                           uint32_t step, bool report) const {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (; k < a.K; k += kBatch * step) {
+      uint32_t i[kBatch];
+      float tk[kBatch], xk[kBatch];
+#pragma unroll
+      for (uint32_t u = 0; u < kBatch; ++u) {
+        const bool in = k + u * step < a.K;
+        i[u] = in ? a.ids[size_t(b) * a.K + k + u * step] : CG_NO_TOKEN;
+        tk[u] = in ? a.teacher[size_t(b) * a.K + k + u * step] : -INFINITY;
+      }
+#pragma unroll
+      for (uint32_t u = 0; u < kBatch; ++u) xk[u] = r.at_any(i[u]);
+#pragma unroll
+      for (uint32_t u = 0; u < kBatch; ++u) {
+        if (k + u * step >= a.K) break;
+        if (i[u] >= a.V && i[u] != CG_NO_TOKEN && report) record_error(a.status, CG_DEV_BAD_TOKEN);
+        tk[u] = teacher_logit(tk[u]);
+        const bool counts = xk[u] > -INFINITY && tk[u] > -INFINITY;
+        id[k + u * step] = counts ? i[u] : CG_NO_TOKEN;
+        x[k + u * step] = xk[u];
+        t[k + u * step] = tk[u];
+        if (counts) top = fmaxf(top, tk[u]);
+      }
+    }
+    return top;
   }
   // Writes the gradient of entry k's token: tm, ts the list's maximum and sum, M and S
   // the row's
@@ -259,8 +282,8 @@ struct Ring {
 // ---- the loss alone ---------------------------------------------------------------------
 //
 // Nothing of a row is needed twice.  The warps send their maxima and sums of the
-// cluster's i-th row to block i mod n, where one more warp has read the row's list
-// meanwhile and finishes the row.  2048 x 128256 bf16: 83.0 us, 6.3 TB/s, bound by the
+// cluster's i-th row to block i mod n, where one more warp (of one or two) has read
+// the row's list meanwhile and finishes the row.  2048 x 128256 bf16: 83.0 us, 6.3 TB/s, bound by the
 // memory.
 //
 // Few barriers and many loads at once: 8 groups of a thread a chunk.  Of 2048 x 128256
@@ -269,8 +292,14 @@ struct Ring {
 constexpr uint32_t kLossPer = 8;       // groups of a thread in a chunk
 constexpr uint32_t kLossSlots = 3;     // chunks on their way or being taken, at most
 constexpr uint32_t kLossBlocks = 2 * 152;  // resident
+constexpr uint32_t kLossBatch = 8;     // list entries of a lane read at a time
+// Longer lists and shorter rows (in bytes) take two warps, a row each, the others one:
+//   2048 x 32000, 64 listed     one 37.5 us, two 29.2
+//   2048 x 32000, 1024 listed   two 108, one reading an entry at a time 316
+//   1024 x 128256, 256 listed   one 54.3, two 47.1; 64 listed 46.0 and 45.9
+//   512 x 128256 masked, 64     one 28.7, two 30.9 (fewer registers for the takers)
+constexpr uint32_t kLongList = 64, kShortLossRow = 128 << 10;
 constexpr size_t kHalfSmem = 113 * 1024;   // of a block of two on an SM
-constexpr uint32_t kLossThreads = (kTakers + 2) * 32;
 // Few rows are split over clusters of 2, 4 or 8 blocks as long as all are resident
 // together (36 clusters of 8, 74 of 4).  Microseconds of B x 128256 bf16 by cluster
 // size, at 16 warps x 2 groups x 6 chunks:
@@ -288,20 +317,18 @@ struct LossShared {
   uint64_t done[kLossCluster][2];     // ... of each block's: their records have been read
   __align__(16) Record rec[2][kLossCluster * kTakers];
 };
-// ... then the list's logits, teacher's and student's, and the ring
-__host__ __device__ constexpr size_t loss_fixed(uint32_t K) {
-  return sizeof(LossShared) + ((size_t(K) * 8 + 15) & ~size_t(15));
+// ... then the lists' logits, teacher's and student's, and the ring
+__host__ __device__ constexpr size_t loss_fixed(uint32_t K, uint32_t lists) {
+  return sizeof(LossShared) + ((size_t(K) * 8 * lists + 15) & ~size_t(15));
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kLossThreads, 2) loss_kernel(const DistillArgs a, uint32_t B, uint32_t slots) {
+template <bool BF16, uint32_t LISTS>
+__global__ void __launch_bounds__((kTakers + 1 + LISTS) * 32, 2) loss_kernel(const DistillArgs a, uint32_t B, uint32_t slots) {
   extern __shared__ __align__(16) unsigned char smem[];
   LossShared& s = *reinterpret_cast<LossShared*>(smem);
   static_assert(sizeof(LossShared) % 16 == 0, "the list and the ring lie behind it");
-  float* list_t = reinterpret_cast<float*>(smem + sizeof(LossShared));  // -inf where an entry does not count
-  float* list_x = list_t + a.K;
   using R = Ring<BF16, kLossPer>;
-  R ring(s.full, s.empty, smem + loss_fixed(a.K), slots);
+  R ring(s.full, s.empty, smem + loss_fixed(a.K, LISTS), slots);
   griddep_launch_dependents();
   const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t first = blockIdx.x / n, step = gridDim.x / n, rows = (B - first + step - 1) / step;
@@ -348,24 +375,38 @@ __global__ void __launch_bounds__(kLossThreads, 2) loss_kernel(const DistillArgs
       }
       late = __any_sync(0xFFFFFFFFu, late);
     }
-  } else {  // finishes the rows that are this block's
-    const uint32_t K = a.K;
+  } else {  // the lists' warps finish the rows that are this block's, in turn
+    const uint32_t K = a.K, turn = warp - (kTakers + 1);
+    float* list_t = reinterpret_cast<float*>(smem + sizeof(LossShared)) + size_t(turn) * 2 * K;  // -inf: does not count
+    float* list_x = list_t + K;
     ready_others();
-    for (uint32_t i = rank; i < rows; i += n) {
+    for (uint32_t i = rank + turn * n; i < rows; i += LISTS * n) {
       const uint32_t b = first + i * step, use = i / n;
       const Row<BF16> r = row(i);
       if (lane == 0 && !late) mbar_expect_tx(s.bar_rec + (use & 1u), n * kTakers * uint32_t(sizeof(Record)));
       float tm = -INFINITY;
-#pragma unroll 4
-      for (uint32_t k = lane; k < K; k += 32) {
-        const uint32_t id = a.ids[size_t(b) * K + k];
-        const float t = teacher_logit(a.teacher[size_t(b) * K + k]);
-        const float x = id < a.V ? r.at(id) : -INFINITY;
-        if (id >= a.V && id != CG_NO_TOKEN) record_error(a.status, CG_DEV_BAD_TOKEN);
-        const bool counts = x > -INFINITY && t > -INFINITY;
-        list_x[k] = x;
-        list_t[k] = counts ? t : -INFINITY;
-        if (counts) tm = fmaxf(tm, t);
+#pragma unroll 1
+      for (uint32_t k0 = lane; k0 < K; k0 += 32 * kLossBatch) {  // the loads of a batch are under way together
+        uint32_t id[kLossBatch];
+        float t[kLossBatch], x[kLossBatch];
+#pragma unroll
+        for (uint32_t u = 0; u < kLossBatch; ++u) {
+          const bool in = k0 + u * 32 < K;
+          id[u] = in ? a.ids[size_t(b) * K + k0 + u * 32] : CG_NO_TOKEN;
+          t[u] = in ? a.teacher[size_t(b) * K + k0 + u * 32] : -INFINITY;
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kLossBatch; ++u) x[u] = r.at_any(id[u]);
+#pragma unroll
+        for (uint32_t u = 0; u < kLossBatch; ++u) {
+          if (k0 + u * 32 >= K) break;
+          if (id[u] >= a.V && id[u] != CG_NO_TOKEN) record_error(a.status, CG_DEV_BAD_TOKEN);
+          const float tk = teacher_logit(t[u]);
+          const bool counts = x[u] > -INFINITY && tk > -INFINITY;
+          list_x[k0 + u * 32] = x[u];
+          list_t[k0 + u * 32] = counts ? tk : -INFINITY;
+          if (counts) tm = fmaxf(tm, tk);
+        }
       }
       tm = warp_reduce(tm, MaxOp());
       const bool listed = tm > -INFINITY;
@@ -406,8 +447,8 @@ __global__ void __launch_bounds__(kLossThreads, 2) loss_kernel(const DistillArgs
 // gradient may take the logits' place.  (That keeps a cluster's blocks side by side, too:
 // without it the gradient alone of 512 x 151936 took 63.8 us, with it 57.2.)
 //
-// 2048 x 128256 bf16: loss and gradient 201.5 us, 5.2 TB/s of reads and writes; the
-// gradient alone 171.5, 6.1 TB/s.  The memory bounds them, and with the loss the exchange
+// 2048 x 128256 bf16: loss and gradient 203.7 us, 5.2 TB/s of reads and writes; the
+// gradient alone 172.1, 6.1 TB/s.  The memory bounds them, and with the loss the exchange
 // of a row's sums, which the next row's copies cover only in part: of a block's six chunks
 // two are ahead.  Fetching a chunk's values before the stores of the one before: 218 us.
 // Clusters of 6 and 8 blocks with three or two chunks each are not all resident together:
@@ -555,10 +596,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
       const List l(lists + buf * size_t(K) * 12, K);
       for (uint32_t k = lt; k < size; k += kListThreads) hash[k] = CG_NO_TOKEN;
       if (lt == 0) s.repeated[buf] = 0;
-      float tm = -INFINITY;
-#pragma unroll 2
-      for (uint32_t k = lt; k < K; k += kListThreads) tm = fmaxf(tm, l.read<BF16>(a, r, b, k, rank == 0));
-      tm = list_fold(tm, MaxOp(), s.red);
+      const float tm = list_fold(l.read<BF16>(a, r, b, lt, kListThreads, rank == 0), MaxOp(), s.red);
       float ts = 0.f;
       for (uint32_t k = lt; k < K; k += kListThreads) {
         const uint32_t id = l.id[k];
@@ -631,7 +669,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
 //   64 x 64006       9.2    8.0      7.1    7.9
 //   64 x 128256     14.0   10.9     10.9   11.3
 //   128 x 128256    23.7   18.1     19.3   16.3
-//   2048 x 128256  221.2  201.5    177.9  171.5
+//   2048 x 128256  221.2  203.7    177.9  172.1
 constexpr uint64_t kShortRow = 48 << 10, kSmallLoss = 6 << 20, kSmallGrad = 16 << 20;  // bytes
 // Groups of a thread for many rows: 64 KB parts, three blocks an SM.
 constexpr uint32_t kFull = 16;
@@ -663,9 +701,7 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
   const uint32_t slots = hash_slots(K);
   for (uint32_t i = tid; i < slots; i += kThreads) hash[i] = CG_NO_TOKEN;
   if (tid == 0) s.repeated = 0;
-  float tm = -INFINITY;
-  for (uint32_t k = tid; k < K; k += kThreads) tm = fmaxf(tm, l.read<BF16>(a, h.r, b, k, rank == 0));
-  tm = block_max(tm, s.red_f);
+  const float tm = block_max(l.read<BF16>(a, h.r, b, tid, kThreads, rank == 0), s.red_f);
   const bool listed = tm > -INFINITY;
   float ts = 0.f;
   for (uint32_t k = tid; k < K; k += kThreads) {
@@ -741,16 +777,18 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
   }
 }
 
-template <bool BF16>
+template <bool BF16, uint32_t LISTS>
 cudaError_t launch_loss(int device, uint32_t B, const DistillArgs& a, cudaStream_t stream) {
   using R = Ring<BF16, kLossPer>;
   const uint32_t chunks = (a.V / Fmt<BF16>::E + R::kGroups) / R::kGroups;
   uint32_t n = 1;
   while (n < kLossCluster && 2 * n <= chunks && uint64_t(B) * 2 * n <= kLossSplit) n *= 2;
+  const size_t fixed = loss_fixed(a.K, LISTS);
   uint32_t slots = kLossSlots;
-  while (loss_fixed(a.K) + R::bytes(slots, a.bitmask) > kHalfSmem) --slots;
-  return launch_clusters<loss_kernel<BF16>>(device, n == 1 && B > kLossBlocks ? kLossBlocks : B, n, kLossThreads,
-                                            loss_fixed(a.K) + R::bytes(slots, a.bitmask), stream, a, B, slots);
+  while (fixed + R::bytes(slots, a.bitmask) > kHalfSmem) --slots;
+  return launch_clusters<loss_kernel<BF16, LISTS>>(device, n == 1 && B > kLossBlocks ? kLossBlocks : B, n,
+                                                   (kTakers + 1 + LISTS) * 32, fixed + R::bytes(slots, a.bitmask), stream,
+                                                   a, B, slots);
 }
 
 // Clusters of n = 1, 2, 4, 8, 16 blocks that are resident together, asked once per n and
@@ -813,7 +851,9 @@ bool streams(bool bf16, uint32_t V, uint32_t B, bool loss) {
 
 template <bool BF16>
 cudaError_t launch_distill(int device, uint32_t B, const DistillArgs& a, bool loss, cudaStream_t stream) {
-  if (!a.grad) return launch_loss<BF16>(device, B, a, stream);
+  if (!a.grad)
+    return a.K > kLongList || a.V * (BF16 ? 2u : 4u) <= kShortLossRow ? launch_loss<BF16, 2>(device, B, a, stream)
+                                                                      : launch_loss<BF16, 1>(device, B, a, stream);
   if (!streams(BF16, a.V, B, loss)) return launch_held<BF16>(device, B, a, loss, stream);
   return loss ? launch_grad<BF16, true>(device, B, a, stream) : launch_grad<BF16, false>(device, B, a, stream);
 }

@@ -326,6 +326,12 @@ struct Row {
     if (mask && !((mask[t >> 3] >> (t & 7u)) & 1u)) return -INFINITY;
     return value(t);
   }
+  // ... of any id, -inf where it is not in the row: the loads wait for no branch
+  __device__ __forceinline__ float at_any(uint32_t t) const {
+    const uint32_t at = t < V ? t : 0u, allowed = mask ? uint32_t(mask[at >> 3]) >> (at & 7u) : 1u;
+    const float x = value(at);
+    return t < V && (allowed & 1u) ? x : -INFINITY;
+  }
   __device__ __forceinline__ float value(uint32_t t) const {
     const char* p = base + (size_t(t) + a) * F::kSize;
     const float x = BF16 ? bf16_bits_to_float(*reinterpret_cast<const volatile uint16_t*>(p))
