@@ -301,29 +301,35 @@ class Ctx:
         L.check(call, rc)
 
     def distill_loss(self, logits, ids, teacher, out_loss, temp: float = 1.0, bitmask=None, out_lse=None,
-                     out_grad=None, grad_loss=None) -> None:
+                     out_grad=None, grad_loss=None, out_norm=None) -> None:
         """Loss of each row against the teacher's listed tokens (ids, teacher
-        [B, K]); with out_grad also the gradient by the logits, times grad_loss [B]."""
+        [B, K]); with out_grad also the gradient by the logits, times grad_loss [B].
+        out_norm [B, 2] receives the normaliser as distill_grad takes it."""
         R, call, B, K = self._rows, "cg_distill_loss", logits.shape[0], ids.shape[1]
         x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
         g, ldg = (None, 0) if out_grad is None else R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
-        rc = L.lib().cg_distill_loss(
+        rc = L.lib().cg_distill_loss_norm(
             self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)),
             R.want(call, ids, "ids", R.U32, (B, K)), R.want(call, teacher, "teacher", R.F32, (B, K)), K, temp,
             R.want(call, out_loss, "out_loss", R.F32, (B,)), R.opt(call, out_lse, "out_lse", R.F32, (B,)),
-            R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
+            R.opt(call, out_norm, "out_norm", R.F32, (B, 2)), R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
         L.check(call, rc)
 
     def distill_grad(self, logits, ids, teacher, lse, out_grad, temp: float = 1.0, bitmask=None,
-                     grad_loss=None) -> None:
-        """The gradient alone, from the normaliser distill_loss left in out_lse."""
+                     grad_loss=None, norm=None) -> None:
+        """The gradient alone, from the normaliser that distill_loss left in out_norm
+        (norm, with lse None) or, to the rounding of one value a row, in out_lse."""
         R, call, B, K = self._rows, "cg_distill_grad", logits.shape[0], ids.shape[1]
         x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
         g, ldg = R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
-        rc = L.lib().cg_distill_grad(
+        if (lse is None) == (norm is None):
+            raise L.CgError(call, L.CG_E_ARG, "lse or norm: one of the two is wanted")
+        entry = L.lib().cg_distill_grad if norm is None else L.lib().cg_distill_grad_norm
+        kept = R.want(call, lse, "lse", R.F32, (B,)) if norm is None else R.want(call, norm, "norm", R.F32, (B, 2))
+        rc = entry(
             self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)),
             R.want(call, ids, "ids", R.U32, (B, K)), R.want(call, teacher, "teacher", R.F32, (B, K)), K, temp,
-            R.want(call, lse, "lse", R.F32, (B,)), R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
+            kept, R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
         L.check(call, rc)
 
     def self_test_wait_timeout(self) -> None:

@@ -1,5 +1,6 @@
 """Autograd form of the distillation loss: cg_distill_loss forward,
-cg_distill_grad backward, nothing kept but the inputs and one normaliser a row."""
+cg_distill_grad backward, nothing kept but the inputs and the normaliser, two
+values a row (one would lose it in rows far from zero)."""
 
 from __future__ import annotations
 
@@ -30,20 +31,20 @@ class DistillLoss(torch.autograd.Function):
     def forward(fn, logits, ctx, ids, teacher, temp, bitmask):
         B = logits.shape[0]
         loss = torch.empty(B, dtype=torch.float32, device=logits.device)
-        lse = torch.empty_like(loss)
-        with on_ctx_stream(ctx, logits, ids, teacher, bitmask, loss, lse):
-            ctx.distill_loss(logits, ids, teacher, loss, temp=temp, bitmask=bitmask, out_lse=lse)
-        fn.save_for_backward(logits, ids, teacher, bitmask, lse)
+        norm = torch.empty((B, 2), dtype=torch.float32, device=logits.device)
+        with on_ctx_stream(ctx, logits, ids, teacher, bitmask, loss, norm):
+            ctx.distill_loss(logits, ids, teacher, loss, temp=temp, bitmask=bitmask, out_norm=norm)
+        fn.save_for_backward(logits, ids, teacher, bitmask, norm)
         fn.ctx, fn.temp = ctx, temp
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(fn, grad_loss):
-        logits, ids, teacher, bitmask, lse = fn.saved_tensors
+        logits, ids, teacher, bitmask, norm = fn.saved_tensors
         grad_loss = grad_loss.contiguous()  # an expanded scalar (loss.sum()) is one value with stride 0
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        with on_ctx_stream(fn.ctx, logits, ids, teacher, bitmask, lse, grad_loss, grad):
-            fn.ctx.distill_grad(logits, ids, teacher, lse, grad, temp=fn.temp, bitmask=bitmask,
-                                grad_loss=grad_loss)
+        with on_ctx_stream(fn.ctx, logits, ids, teacher, bitmask, norm, grad_loss, grad):
+            fn.ctx.distill_grad(logits, ids, teacher, None, grad, temp=fn.temp, bitmask=bitmask,
+                                grad_loss=grad_loss, norm=norm)
         return grad, None, None, None, None, None

@@ -28,9 +28,11 @@ struct DistillArgs {
   const float* teacher;
   uint32_t K;
   float temp;
-  const float* lse_in;   // backward alone: the kept normaliser
+  const float* lse_in;   // backward alone: the kept normaliser, one value a row
+  const float* norm_in;  // ... or two, which is exact for every row; else null
   float* loss;
   float* lse_out;
+  float* norm_out;
   const float* up;
   void* grad;
   uint64_t ld_grad;
@@ -45,9 +47,19 @@ __device__ __forceinline__ float loss_term(float dt, float ts, float log_ts, flo
   const float q = __fdiv_rn(ex2(dt * c), ts);
   return q > 0.f ? q * ((__fdiv_rn(dt, T) - log_ts) - (__fdiv_rn(dx, T) - log_s)) : 0.f;
 }
-__device__ __forceinline__ void store_loss(const DistillArgs& a, uint32_t b, float loss, float M, float log_s) {
+__device__ __forceinline__ void store_loss(const DistillArgs& a, uint32_t b, float loss, float M, float S, float log_s) {
   a.loss[b] = loss;
+  if (a.norm_out) {
+    a.norm_out[2 * size_t(b)] = M;
+    a.norm_out[2 * size_t(b) + 1] = S;
+  }
   if (a.lse_out) a.lse_out[b] = M > -INFINITY ? __fdiv_rn(M, a.temp) + log_s : -INFINITY;
+}
+// The kept normaliser, p = exp2((x - M) c) / S.  From the one value M = lse T and S = 1: its
+// rounding is an error of |lse| 2^-23 in every p, and where it overflows p is lost.
+__device__ __forceinline__ void kept_norm(const DistillArgs& a, uint32_t b, float& M, float& S) {
+  M = a.norm_in ? a.norm_in[2 * size_t(b)] : a.lse_in[b] * a.temp;
+  S = a.norm_in ? a.norm_in[2 * size_t(b) + 1] : 1.f;
 }
 
 template <bool BF16>
@@ -428,7 +440,7 @@ __global__ void __launch_bounds__((kTakers + 1 + LISTS) * 32, 2) loss_kernel(con
       for (uint32_t k = lane; k < K; k += 32)
         if (list_t[k] > -INFINITY) part += loss_term(list_t[k] - tm, ts, log_ts, list_x[k] - M, log_s, c, T);
       part = warp_reduce(part, SumOp());
-      if (lane == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, log_s);
+      if (lane == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, S, log_s);
     }
   }
   if (late) record_error(a.status, CG_DEV_TIMEOUT);
@@ -534,7 +546,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
       const Row<BF16> r = row(i);
       const uint32_t b = first + i * step, buf = i & 1u, parity = (i / 2) & 1u;
       const float up = a.up ? a.up[b] : 1.f;
-      float M = LOSS ? 0.f : a.lse_in[b] * T, S = 1.f;  // p = exp2((x - M) c) / S
+      float M = 0.f, S = 1.f;  // p = exp2((x - M) c) / S
+      if (!LOSS) kept_norm(a, b, M, S);
       bool wrote = false;
       if (LOSS) {
         R ahead = ring;
@@ -621,8 +634,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
       const uint32_t b = first + i * step, buf = i & 1u, parity = (i / 2) & 1u;
       if (i + 1 < rows) read(i + 1);
       if (!late) late = !__all_sync(0xFFFFFFFFu, wait_sent(s.bar_rec + buf, parity));
-      float M = LOSS ? 0.f : a.lse_in[b] * T, S = 1.f;
+      float M = 0.f, S = 1.f;
       if (LOSS) merge(s.rec[buf], n * kTakers, c, M, S);
+      else kept_norm(a, b, M, S);
       list_sync();
       if (!late && lt == 0 && i + 2 < rows) mbar_expect_tx(s.bar_rec + buf, told);
       if (i + 1 < rows) tell(i + 1);
@@ -636,7 +650,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
         for (uint32_t k = lt; k < K; k += kListThreads)
           if (l.id[k] != CG_NO_TOKEN) part += loss_term(l.t[k] - tm, ts, log_ts, l.x[k] - M, log_s, c, T);
         part = list_fold(part, SumOp(), s.red);
-        if (lt == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, log_s);
+        if (lt == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, S, log_s);
       }
       if (!late) late = !__all_sync(0xFFFFFFFFu, mbar_wait(s.bar_done + buf, parity));
       if (listed) {
@@ -739,10 +753,10 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
         if (l.id[k] != CG_NO_TOKEN) part += loss_term(l.t[k] - tm, ts, log_ts, l.x[k] - M, log_s, c, T);
       __syncthreads();
       part = block_sum(part, s.red_f);
-      if (tid == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, log_s);
+      if (tid == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, S, log_s);
     }
   } else {
-    M = a.lse_in[b] * T;  // p = exp((x - lse T) / T)
+    kept_norm(a, b, M, S);
     if (!h.template take<false>(s, c)) record_error(a.status, CG_DEV_TIMEOUT);
     ready_others();
     if (a.grad == a.logits) cluster_sync(n);  // every block has read what it needs
@@ -902,30 +916,55 @@ int list_args(const cg_ctx* c, const void* logits, int dtype, uint32_t B, uint32
 }  // namespace
 }  // namespace cgk
 
-extern "C" int cg_distill_loss(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
-                               const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
-                               float temp, float* d_out_loss, float* d_out_lse, const float* d_grad_loss,
-                               void* d_out_grad, uint64_t ld_grad) {
+extern "C" int cg_distill_loss_norm(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                                    const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher,
+                                    uint32_t K, float temp, float* d_out_loss, float* d_out_lse, float* d_out_norm,
+                                    const float* d_grad_loss, void* d_out_grad, uint64_t ld_grad) {
   using namespace cgk;
   const int rc = list_args(c, d_logits, dtype, B, V, ld, d_bitmask, d_ids, d_teacher, K, temp, d_grad_loss,
                            d_out_grad, ld_grad);
   if (rc != CG_OK) return rc;
-  if ((B && !d_out_loss) || !aligned4(d_out_loss) || !aligned4(d_out_lse)) return CG_E_ARG;
-  const DistillArgs a{d_logits, ld, d_bitmask, V, 0, d_ids, d_teacher, K, temp, nullptr, d_out_loss, d_out_lse,
-                      d_grad_loss, d_out_grad, ld_grad, nullptr};
+  if ((B && !d_out_loss) || !aligned4(d_out_loss) || !aligned4(d_out_lse) || !aligned4(d_out_norm)) return CG_E_ARG;
+  const DistillArgs a{d_logits, ld,      d_bitmask,  V,         0,          d_ids,       d_teacher,  K,       temp,
+                      nullptr,  nullptr, d_out_loss, d_out_lse, d_out_norm, d_grad_loss, d_out_grad, ld_grad, nullptr};
   return distill(c, "cg_distill_loss", a, dtype, B, true);
+}
+
+extern "C" int cg_distill_loss(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                               const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
+                               float temp, float* d_out_loss, float* d_out_lse, const float* d_grad_loss,
+                               void* d_out_grad, uint64_t ld_grad) {
+  return cg_distill_loss_norm(c, d_logits, dtype, B, V, ld, d_bitmask, d_ids, d_teacher, K, temp, d_out_loss,
+                              d_out_lse, nullptr, d_grad_loss, d_out_grad, ld_grad);
+}
+
+// the backward pass from either form of the normaliser
+static int distill_backward(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                            const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
+                            float temp, const float* d_lse, const float* d_norm, const float* d_grad_loss,
+                            void* d_out_grad, uint64_t ld_grad) {
+  using namespace cgk;
+  const int rc = list_args(c, d_logits, dtype, B, V, ld, d_bitmask, d_ids, d_teacher, K, temp, d_grad_loss,
+                           d_out_grad, ld_grad);
+  if (rc != CG_OK) return rc;
+  if ((B && ((!d_lse && !d_norm) || !d_out_grad)) || !aligned4(d_lse) || !aligned4(d_norm)) return CG_E_ARG;
+  const DistillArgs a{d_logits, ld,     d_bitmask, V,       0,       d_ids,       d_teacher,  K,       temp,
+                      d_lse,    d_norm, nullptr,   nullptr, nullptr, d_grad_loss, d_out_grad, ld_grad, nullptr};
+  return distill(c, "cg_distill_grad", a, dtype, B, false);
 }
 
 extern "C" int cg_distill_grad(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
                                const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
                                float temp, const float* d_lse, const float* d_grad_loss, void* d_out_grad,
                                uint64_t ld_grad) {
-  using namespace cgk;
-  const int rc = list_args(c, d_logits, dtype, B, V, ld, d_bitmask, d_ids, d_teacher, K, temp, d_grad_loss,
-                           d_out_grad, ld_grad);
-  if (rc != CG_OK) return rc;
-  if ((B && (!d_lse || !d_out_grad)) || !aligned4(d_lse)) return CG_E_ARG;
-  const DistillArgs a{d_logits, ld, d_bitmask, V, 0, d_ids, d_teacher, K, temp, d_lse, nullptr, nullptr,
-                      d_grad_loss, d_out_grad, ld_grad, nullptr};
-  return distill(c, "cg_distill_grad", a, dtype, B, false);
+  return distill_backward(c, d_logits, dtype, B, V, ld, d_bitmask, d_ids, d_teacher, K, temp, d_lse, nullptr,
+                          d_grad_loss, d_out_grad, ld_grad);
+}
+
+extern "C" int cg_distill_grad_norm(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                                    const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher,
+                                    uint32_t K, float temp, const float* d_norm, const float* d_grad_loss,
+                                    void* d_out_grad, uint64_t ld_grad) {
+  return distill_backward(c, d_logits, dtype, B, V, ld, d_bitmask, d_ids, d_teacher, K, temp, nullptr, d_norm,
+                          d_grad_loss, d_out_grad, ld_grad);
 }

@@ -498,7 +498,17 @@ int cg_top_logprobs(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint
  *              rounded once from 32 bits to the dtype.  May be d_logits itself
  *              (with ld_grad == ld); must not overlap it otherwise.
  * cg_distill_grad is the backward pass alone: d_lse as cg_distill_loss wrote it
- * for the same logits, mask and temperature.
+ * for the same logits, mask and temperature.  One 32-bit value a row holds the
+ * normaliser to its rounding only: every p has a relative error of |lse| * 2^-23
+ * more, and a row whose lse is not finite or is as large as a logit of +inf makes
+ * it has no gradient this way.
+ * cg_distill_loss_norm and cg_distill_grad_norm are the same two calls with the
+ * normaliser kept as two values, which holds for every row:
+ *  d_out_norm, d_norm : f32 [B][2], for row b m = max x over A_b and sum over A_b
+ *              of exp((x - m) / T) (-inf and 0 for an empty row); d_out_norm may
+ *              be NULL
+ * A loss beyond the largest finite float (a listed token that far below a logit of
+ * +inf) is +inf or rounds to the largest finite value.
  * Device errors: CG_DEV_BAD_TOKEN. */
 int cg_distill_loss(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
                     const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
@@ -507,6 +517,14 @@ int cg_distill_loss(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint
 int cg_distill_grad(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
                     const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
                     float temp, const float* d_lse, const float* d_grad_loss, void* d_out_grad, uint64_t ld_grad);
+int cg_distill_loss_norm(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                         const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
+                         float temp, float* d_out_loss, float* d_out_lse, float* d_out_norm,
+                         const float* d_grad_loss, void* d_out_grad, uint64_t ld_grad);
+int cg_distill_grad_norm(cg_ctx* c, const void* d_logits, int dtype, uint32_t B, uint32_t V, uint64_t ld,
+                         const uint32_t* d_bitmask, const uint32_t* d_ids, const float* d_teacher, uint32_t K,
+                         float temp, const float* d_norm, const float* d_grad_loss, void* d_out_grad,
+                         uint64_t ld_grad);
 
 /* ---- pushdown automaton for recursive grammars ---------------------------------- */
 
