@@ -165,6 +165,7 @@ class Ctx:
         if stream is None:
             stream = torch.cuda.current_stream()
         self.stream = stream
+        self._dev = torch.cuda.current_device()  # where the library creates the context
         self._rows = _rows  # an import in every call would be a twentieth of the smallest
         arr = (C.c_void_p * len(grammars))(*[g._h.value for g in grammars])
         h = C.c_void_p()
@@ -274,30 +275,33 @@ class Ctx:
         own ([B] tensors or None), drawn with the given random numbers uniform
         [B, V] (a [1, V] or expanded tensor shares one row; None for an all-greedy
         batch); out_logprob receives log p of the token before any cut."""
-        R, call, B, W = self._rows, "cg_sample_rows", logits.shape[0], self.W
-        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
+        R, call, dev, B, W = self._rows, "cg_sample_rows", self._dev, logits.shape[0], self.W
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V), dev)
         u, ldu = None, 0
         if uniform is not None:
             shared = uniform.shape[0] == 1
-            u, ldu = R.rows_of(call, uniform, "uniform", R.F32, (1 if shared else B, self.V))
+            u, ldu = R.rows_of(call, uniform, "uniform", R.F32, (1 if shared else B, self.V), dev)
             ldu = 0 if shared else ldu
         each = (B,)
         rc = L.lib().cg_sample_rows(
-            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, W)),
-            R.opt(call, temp, "temp", R.F32, each), R.opt(call, top_k, "top_k", R.U32, each),
-            R.opt(call, top_p, "top_p", R.F32, each), R.opt(call, min_p, "min_p", R.F32, each), u, ldu,
-            R.want(call, out_tok, "out_tok", R.U32, each), R.opt(call, out_logprob, "out_logprob", R.F32, each))
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, W), dev),
+            R.opt(call, temp, "temp", R.F32, each, dev), R.opt(call, top_k, "top_k", R.U32, each, dev),
+            R.opt(call, top_p, "top_p", R.F32, each, dev), R.opt(call, min_p, "min_p", R.F32, each, dev), u, ldu,
+            R.want(call, out_tok, "out_tok", R.U32, each, dev),
+            R.opt(call, out_logprob, "out_logprob", R.F32, each, dev))
         L.check(call, rc)
 
     def top_logprobs(self, logits, out_ids, out_logprobs, bitmask=None, out_lse=None) -> None:
         """The n best allowed tokens of each row (n = out_ids.shape[1]), best
         first, with their log-probabilities."""
-        R, call, B, n = self._rows, "cg_top_logprobs", logits.shape[0], out_ids.shape[1]
-        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
+        R, call, dev, B, n = self._rows, "cg_top_logprobs", self._dev, logits.shape[0], out_ids.shape[1]
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V), dev)
         rc = L.lib().cg_top_logprobs(
-            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)), n,
-            R.want(call, out_ids, "out_ids", R.U32, (B, n)), R.want(call, out_logprobs, "out_logprobs", R.F32, (B, n)),
-            R.opt(call, out_lse, "out_lse", R.F32, (B,)))
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld,
+            R.opt(call, bitmask, "bitmask", R.U32, (B, self.W), dev), n,
+            R.want(call, out_ids, "out_ids", R.U32, (B, n), dev),
+            R.want(call, out_logprobs, "out_logprobs", R.F32, (B, n), dev),
+            R.opt(call, out_lse, "out_lse", R.F32, (B,), dev))
         L.check(call, rc)
 
     def distill_loss(self, logits, ids, teacher, out_loss, temp: float = 1.0, bitmask=None, out_lse=None,
@@ -305,31 +309,36 @@ class Ctx:
         """Loss of each row against the teacher's listed tokens (ids, teacher
         [B, K]); with out_grad also the gradient by the logits, times grad_loss [B].
         out_norm [B, 2] receives the normaliser as distill_grad takes it."""
-        R, call, B, K = self._rows, "cg_distill_loss", logits.shape[0], ids.shape[1]
-        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
-        g, ldg = (None, 0) if out_grad is None else R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
+        R, call, dev, B, K = self._rows, "cg_distill_loss", self._dev, logits.shape[0], ids.shape[1]
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V), dev)
+        g, ldg = None, 0
+        if out_grad is not None:
+            g, ldg = R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V), dev)
         rc = L.lib().cg_distill_loss_norm(
-            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)),
-            R.want(call, ids, "ids", R.U32, (B, K)), R.want(call, teacher, "teacher", R.F32, (B, K)), K, temp,
-            R.want(call, out_loss, "out_loss", R.F32, (B,)), R.opt(call, out_lse, "out_lse", R.F32, (B,)),
-            R.opt(call, out_norm, "out_norm", R.F32, (B, 2)), R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W), dev),
+            R.want(call, ids, "ids", R.U32, (B, K), dev), R.want(call, teacher, "teacher", R.F32, (B, K), dev), K, temp,
+            R.want(call, out_loss, "out_loss", R.F32, (B,), dev), R.opt(call, out_lse, "out_lse", R.F32, (B,), dev),
+            R.opt(call, out_norm, "out_norm", R.F32, (B, 2), dev),
+            R.opt(call, grad_loss, "grad_loss", R.F32, (B,), dev), g, ldg)
         L.check(call, rc)
 
     def distill_grad(self, logits, ids, teacher, lse, out_grad, temp: float = 1.0, bitmask=None,
                      grad_loss=None, norm=None) -> None:
         """The gradient alone, from the normaliser that distill_loss left in out_norm
         (norm, with lse None) or, to the rounding of one value a row, in out_lse."""
-        R, call, B, K = self._rows, "cg_distill_grad", logits.shape[0], ids.shape[1]
-        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V))
-        g, ldg = R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V))
+        R, call, dev, B, K = self._rows, "cg_distill_grad", self._dev, logits.shape[0], ids.shape[1]
+        x, ld = R.rows_of(call, logits, "logits", R.LOGITS, (B, self.V), dev)
+        g, ldg = R.rows_of(call, out_grad, "out_grad", (logits.dtype,), (B, self.V), dev)
         if (lse is None) == (norm is None):
             raise L.CgError(call, L.CG_E_ARG, "lse or norm: one of the two is wanted")
-        entry = L.lib().cg_distill_grad if norm is None else L.lib().cg_distill_grad_norm
-        kept = R.want(call, lse, "lse", R.F32, (B,)) if norm is None else R.want(call, norm, "norm", R.F32, (B, 2))
+        if norm is None:
+            entry, kept = L.lib().cg_distill_grad, R.want(call, lse, "lse", R.F32, (B,), dev)
+        else:
+            entry, kept = L.lib().cg_distill_grad_norm, R.want(call, norm, "norm", R.F32, (B, 2), dev)
         rc = entry(
-            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W)),
-            R.want(call, ids, "ids", R.U32, (B, K)), R.want(call, teacher, "teacher", R.F32, (B, K)), K, temp,
-            kept, R.opt(call, grad_loss, "grad_loss", R.F32, (B,)), g, ldg)
+            self._h, x, R.DTYPE[logits.dtype], B, self.V, ld, R.opt(call, bitmask, "bitmask", R.U32, (B, self.W), dev),
+            R.want(call, ids, "ids", R.U32, (B, K), dev), R.want(call, teacher, "teacher", R.F32, (B, K), dev), K, temp,
+            kept, R.opt(call, grad_loss, "grad_loss", R.F32, (B,), dev), g, ldg)
         L.check(call, rc)
 
     def self_test_wait_timeout(self) -> None:

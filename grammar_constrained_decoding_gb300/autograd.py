@@ -19,10 +19,10 @@ def on_ctx_stream(ctx, *tensors):
         yield
         return
     ctx.stream.wait_stream(cur)
+    yield  # a refused tensor raises here
     for t in tensors:
         if t is not None:
             t.record_stream(ctx.stream)
-    yield
     cur.wait_stream(ctx.stream)
 
 

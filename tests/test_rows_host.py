@@ -15,3 +15,74 @@ def test_two_value_normaliser_calls_refuse_a_missing_context():
     f32 = _lib.CG_F32
     assert lib.cg_distill_loss_norm(None, p, f32, 1, 8, 8, None, p, p, 4, 1.0, p, p, p, None, None, 0) == _lib.CG_E_ARG
     assert lib.cg_distill_grad_norm(None, p, f32, 1, 8, 8, None, p, p, 4, 1.0, p, None, p, 8) == _lib.CG_E_ARG
+
+
+class Stub:
+    """What the checks look at of a tensor, on any device."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device = shape, dtype, device
+        self.is_cuda = device >= 0
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self, i):
+        return (self.shape[1], 1)[i]
+
+    def data_ptr(self):
+        return 4096
+
+
+def calls_on(device):
+    """A context on CUDA device 1 whose library accepts every call: name -> (method, tensors on `device`)."""
+    import torch
+    ctx = object.__new__(gcd.Ctx)
+    ctx._h, ctx._dev, ctx.V, ctx.W = None, 1, 64, 2
+    from grammar_constrained_decoding_gb300 import _rows
+    ctx._rows = _rows
+    B, K = 3, 4
+    f = lambda *shape: Stub(shape, torch.float32, device)  # noqa: E731
+    i = lambda *shape: Stub(shape, torch.int32, device)    # noqa: E731
+    lists = dict(logits=f(B, 64), ids=i(B, K), teacher=f(B, K), bitmask=i(B, 2), grad_loss=f(B), out_grad=f(B, 64))
+    return {
+        "sample_rows": (ctx.sample_rows, dict(logits=f(B, 64), uniform=f(B, 64), out_tok=i(B), bitmask=i(B, 2), temp=f(B),
+                                              top_k=i(B), top_p=f(B), min_p=f(B), out_logprob=f(B))),
+        "top_logprobs": (ctx.top_logprobs, dict(logits=f(B, 64), out_ids=i(B, K), out_logprobs=f(B, K), bitmask=i(B, 2),
+                                                out_lse=f(B))),
+        "distill_loss": (ctx.distill_loss, dict(lists, out_loss=f(B), out_lse=f(B), out_norm=f(B, 2))),
+        "distill_grad": (ctx.distill_grad, dict(lists, lse=f(B))),
+        "distill_grad_norm": (lambda **k: ctx.distill_grad(lse=None, **k), dict(lists, norm=f(B, 2))),
+    }
+
+
+class AcceptingLibrary:
+    calls = 0
+
+    def __getattr__(self, name):
+        def entry(*args):
+            AcceptingLibrary.calls += 1
+            return _lib.CG_OK
+        return entry
+
+
+@pytest.mark.parametrize("name", ["sample_rows", "top_logprobs", "distill_loss", "distill_grad", "distill_grad_norm"])
+def test_tensors_of_another_device_are_refused(monkeypatch, name):
+    """Each argument in turn on device 0 (and on the host) where the context is on device 1:
+    refused before the library is called."""
+    library = AcceptingLibrary()
+    monkeypatch.setattr(_lib, "lib", lambda: library)
+    call, there = calls_on(1)[name]
+    AcceptingLibrary.calls = 0
+    call(**there)
+    assert AcceptingLibrary.calls == 1
+    for device in (0, -1):
+        elsewhere = calls_on(device)[name][1]
+        for arg in there:
+            with pytest.raises(gcd.CgError) as e:
+                call(**{**there, arg: elsewhere[arg]})
+            assert e.value.code == _lib.CG_E_ARG and "cuda:1" in str(e.value), arg
+    assert AcceptingLibrary.calls == 1
