@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   q.Ts = q.greedy ? 1.f : q.T;
   if (q.k >= a.V || q.greedy) q.k = 0;
   const float c = exp_scale(q.Ts);
-  const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || p != p || mp != mp || (!q.greedy && !a.u);
+  const bool bad = !(q.T >= 0.f && q.T <= FLT_MAX) || (!q.greedy && (p != p || mp != mp || !a.u));
   // Rows that need nothing of the others' parts before they send what may be drawn:
   // the maximum, or the best of all tokens.
   enum { kTogether, kBest, kAny } alone = kTogether;

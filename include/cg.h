@@ -100,8 +100,9 @@ extern "C" {
 #define CG_DEV_TIMEOUT         8  /* sample: a bounded wait for an asynchronous copy ran out;
                                      the row gets CG_NO_TOKEN */
 #define CG_DEV_BAD_LENGTH      9  /* accept_many: a draft length > K (clamped to K) */
-#define CG_DEV_BAD_PARAM      10  /* sample_rows: a row's temperature is negative, infinite or NaN, or its
-                                     top_p or min_p is NaN; the row gets CG_NO_TOKEN */
+#define CG_DEV_BAD_PARAM      10  /* sample_rows: a row's temperature is negative, infinite or NaN, or it is
+                                     above 0 and the row's top_p or min_p is NaN or no random numbers
+                                     are given; the row gets CG_NO_TOKEN */
 
 /* mask_and_sample flags */
 #define CG_SAMPLE_INPLACE 1u     /* also write -inf into masked logits (the "&mut [f32]" form) */
