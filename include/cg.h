@@ -446,7 +446,8 @@ int cg_self_test_wait_timeout(cg_ctx* c);
  *   top-p  renormalises over those and keeps x_t >= tau, tau the largest value
  *          whose upper set carries at least top_p of their mass (top_p >= 1
  *          keeps all, top_p <= 0 only the maximum);
- *   min-p  keeps p_t >= min_p * max p, i.e. z_t >= log(min_p) (0 keeps all);
+ *   min-p  keeps p_t >= min_p * max p, i.e. z_t >= log(min_p) (min_p <= 0 keeps
+ *          all, min_p >= 1 only the maximum);
  *   token = argmax over the kept set of z_t - log(-log u_t), ties to the lowest
  *          id, u_t = d_uniform[b * ld_uniform + t] clamped into
  *          [2^-32, 1 - 2^-24] (a NaN counts as 2^-32).
