@@ -25,7 +25,7 @@ CXX_SOURCES = ["compiler/gbnf.cpp", "compiler/schema.cpp", "compiler/structtag.c
 CU_SOURCES = ["ctx.cu", "kernel_mask.cu", "kernel_sample.cu", "kernel_seg.cu", "kernel_accept.cu", "pda.cu",
               "kernel_draw.cu", "kernel_top.cu", "kernel_distill.cu"]
 HEADERS = ["compiler/ir.h", "compiler/json.h", "cg_internal.h", "device.cuh", "row_ops.cuh", "pda.cuh", "bf16_ops.cuh",
-           "logit_row.cuh"]
+           "logit_row.cuh", "device_answers.h"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

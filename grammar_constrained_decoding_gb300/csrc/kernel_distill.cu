@@ -805,23 +805,20 @@ cudaError_t launch_loss(int device, uint32_t B, const DistillArgs& a, cudaStream
                                                    a, B, slots);
 }
 
-// Clusters of n = 1, 2, 4, 8, 16 blocks that are resident together, asked once per n and
-// blocks an SM (which smem decides); 0 and an error where the device cannot tell
+// Clusters of n = 1, 2, 4, 8, 16 blocks that are resident together, asked once per device, n
+// and blocks an SM (which smem decides); 0 and an error where the device cannot tell
 template <auto Kernel>
 uint32_t resident(int device, uint32_t n, size_t smem, cudaError_t& e) {
-  static std::atomic<int> known[2][5];
-  std::atomic<int>& k = known[smem > kHalfSmem][__builtin_ctz(n)];
-  int clusters = k.load(std::memory_order_relaxed);
+  static DeviceAnswers known[2][5];
   e = cudaSuccess;
-  if (clusters == 0) {
+  return uint32_t(known[smem > kHalfSmem][__builtin_ctz(n)].get(device, [&] {
+    int clusters = 0;
     e = raise_limits<Kernel>(device);
     const ClusterLaunch l(1, n, kGradThreads, smem > kHalfSmem ? kMaxSmem : kHalfSmem, nullptr);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, Kernel, &l.cfg);
     if (e == cudaSuccess && clusters <= 0) e = cudaErrorInvalidConfiguration;
-    if (e != cudaSuccess) return 0;
-    k.store(clusters, std::memory_order_relaxed);
-  }
-  return uint32_t(clusters);
+    return e == cudaSuccess ? clusters : 0;
+  }));
 }
 
 template <bool BF16, bool LOSS>

@@ -26,10 +26,10 @@
 // and reads as -inf; +inf reads as the largest finite value.
 #pragma once
 
-#include <atomic>
 #include <cfloat>
 
 #include "bf16_ops.cuh"
+#include "device_answers.h"
 
 namespace cgk {
 namespace row {
@@ -1066,15 +1066,14 @@ struct ClusterLaunch {
 constexpr int kMaxSmem = 227 * 1024;
 template <auto Kernel>
 cudaError_t raise_limits(int device) {
-  static std::atomic<uint64_t> raised{0};
-  const uint64_t bit = uint64_t(1) << (device & 63);
-  if (!(raised.load(std::memory_order_relaxed) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  static DeviceAnswers raised;
+  cudaError_t e = cudaSuccess;
+  raised.get(device, [&] {
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    raised.fetch_or(bit, std::memory_order_relaxed);
-  }
-  return cudaSuccess;
+    return e == cudaSuccess ? 1 : 0;
+  });
+  return e;
 }
 template <auto Kernel, typename... Args>
 cudaError_t launch_clusters(int device, uint32_t clusters, uint32_t n, uint32_t threads, size_t smem,

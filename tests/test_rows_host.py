@@ -1,6 +1,8 @@
 """Host-side checks of the per-row operators that need no GPU."""
 
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -86,3 +88,36 @@ def test_tensors_of_another_device_are_refused(monkeypatch, name):
                 call(**{**there, arg: elsewhere[arg]})
             assert e.value.code == _lib.CG_E_ARG and "cuda:1" in str(e.value), arg
     assert AcceptingLibrary.calls == 1
+
+
+DEVICE_ANSWERS = r"""
+#include <cstdio>
+#include "device_answers.h"
+int main() {
+  static cgk::DeviceAnswers known;
+  int asked = 0;
+  auto ask = [&](int v) { return [&asked, v] { ++asked; return v; }; };
+  bool ok = known.get(0, ask(36)) == 36 && known.get(1, ask(18)) == 18;   // each device its own
+  ok = ok && known.get(0, ask(5)) == 36 && known.get(1, ask(5)) == 18 && asked == 2;
+  ok = ok && known.get(2, ask(0)) == 0 && known.get(2, ask(7)) == 7;      // a failed answer is not kept
+  ok = ok && known.get(63, ask(3)) == 3 && known.get(63, ask(4)) == 3;
+  ok = ok && known.get(64, ask(9)) == 9 && known.get(64, ask(11)) == 11;  // past the table: asked
+  ok = ok && known.get(128, ask(13)) == 13 && known.get(0, ask(5)) == 36;
+  std::puts(ok ? "ok" : "wrong");
+}
+"""
+
+
+def test_answers_are_kept_for_each_device(tmp_path):
+    csrc = os.path.join(os.path.dirname(gcd.__file__), "csrc")
+    (tmp_path / "t.cpp").write_text(DEVICE_ANSWERS)
+    subprocess.run(["g++", "-std=c++17", "-Wall", f"-I{csrc}", str(tmp_path / "t.cpp"), "-o", str(tmp_path / "t")], check=True)
+    assert subprocess.run([str(tmp_path / "t")], capture_output=True, text=True).stdout.strip() == "ok"
+
+
+def test_process_wide_answers_of_the_row_operators_are_kept_per_device():
+    """No answer of a device is kept in a variable of its own beside the table."""
+    csrc = os.path.join(os.path.dirname(gcd.__file__), "csrc")
+    for name in ("logit_row.cuh", "kernel_distill.cu", "kernel_draw.cu", "kernel_top.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            assert "static std::atomic" not in f.read(), name
