@@ -204,7 +204,10 @@ struct Ring {
     const uint32_t lo = r.first_whole(), hi = r.end_whole();
     const bool with_bits = copies_bits(r);
     for (uint32_t g = rank * kGroups; g < end(r); g += n * kGroups, next()) {
-      if (turn && !mbar_wait(empty + slot, (turn - 1) & 1u)) return false;
+      if (turn) {
+        if (!mbar_wait(empty + slot, (turn - 1) & 1u)) return false;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the takers' reads come before the copy
+      }
       const uint32_t from = max(g, lo), to = min(g + kGroups, hi), off = g * F::E / 8;
       const uint32_t size = to > from ? (to - from) * 16u : 0u, more = with_bits ? min(kBits, r.W * 4u - off) : 0u;
       mbar_expect_tx(full + slot, size + more);
@@ -278,16 +281,20 @@ struct Ring {
     return t;
   }
   // This warp has taken the chunk in the slot.  An arrival may overtake loads that are
-  // still queued behind stores, so it follows an instruction that needs their
-  // results: t, the chunk's maximum by the rows' conventions, which is never +inf.
-  __device__ __forceinline__ void release(float t) const {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-      asm volatile(
-          "{\n .reg .pred p;\n setp.neu.f32 p, %1, 0f7F800000;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(
-              smem_addr(empty + slot)),
-          "f"(t)
-          : "memory");
+  // still queued behind stores, so it follows a vote on something that needs the values
+  // of all loads of all lanes and is never true: every load has returned by then.  The
+  // thread that fills the slot puts the proxy fence between the loads and the next copy
+  // (of 512 x 128256 with a fence in every taker 29.8 us, in the filler 29.2).
+  __device__ __forceinline__ void release(bool never) const {
+    const bool none = __any_sync(0xFFFFFFFFu, never);
+    if ((threadIdx.x & 31) == 0 && !none) mbar_arrive(empty + slot);
+  }
+  // a word of each of PER groups by the rows' conventions is a NaN
+  static __device__ __forceinline__ bool holds_nan(const uint4* v) {
+    uint32_t word = v[0].x;
+#pragma unroll
+    for (uint32_t k = 1; k < PER; ++k) word = max(word, v[k].x);
+    return word == 0xFFFFFFFFu;
   }
 };
 
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__((kTakers + 1 + LISTS) * 32, 2) loss_kernel(con
       for (uint32_t g = rank * R::kGroups; g < R::end(r); g += n * R::kGroups, ring.next()) {
         uint4 v[kLossPer];
         const float t = ring.template take<false>(r, g, v, wrote, late);
-        ring.release(t);
+        ring.release(t == INFINITY);  // replaced by the largest finite value
         add_groups<BF16, kLossPer>(v, t, c, tm, acc);
       }
       if (i == 0) ready_others();
@@ -582,9 +589,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
           for (uint32_t k = 0; k < kGradPer; ++k) v[k] = held[k * kTakers * 32];
           // what this thread wrote there comes before the next copy
           if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          ring.release(groups_max_nan<BF16, kGradPer>(v));
+          ring.release(R::holds_nan(v));
         } else {
-          ring.release(ring.template take<false>(r, g, v, wrote, late));
+          ring.release(ring.template take<false>(r, g, v, wrote, late) == INFINITY);
         }
 #pragma unroll
         for (uint32_t k = 0; k < kGradPer; ++k) {
