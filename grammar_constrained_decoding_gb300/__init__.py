@@ -341,6 +341,13 @@ class Ctx:
             kept, R.opt(call, grad_loss, "grad_loss", R.F32, (B,), dev), g, ldg)
         L.check(call, rc)
 
+    def self_test_cluster_timeout(self, out) -> None:
+        """Make a block of a cluster give up while others still send to it (the status then
+        reads CG_DEV_TIMEOUT); out [1] receives the number of messages it stayed for (6)."""
+        call = "cg_self_test_cluster_timeout"
+        L.check(call, L.lib().cg_self_test_cluster_timeout(
+            self._h, self._rows.want(call, out, "out", self._rows.U32, (1,), self._dev)))
+
     def self_test_wait_timeout(self) -> None:
         """Make one bounded device wait run out (the status then reads CG_DEV_TIMEOUT)."""
         L.check("cg_self_test_wait_timeout", L.lib().cg_self_test_wait_timeout(self._h))

@@ -747,7 +747,10 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
       if (tid == 0) {
         s.M = m;
         s.S = sum;
-        if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
+        if (!ok) {
+          s.late = 1;
+          record_error(a.status, CG_DEV_TIMEOUT);
+        }
       }
     }
     __syncthreads();
@@ -786,16 +789,16 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
     }
     store_group<BF16>(row, h.first_token(j), a.V, wide, g);
   }
-  if (!listed) return;
   __syncthreads();
   const bool repeated = s.repeated != 0;
-  for (uint32_t k = tid; k < K; k += kThreads) {
+  for (uint32_t k = tid; listed && k < K; k += kThreads) {
     const uint32_t id = l.id[k];
     if (id == CG_NO_TOKEN) continue;
     const uint32_t g = (id + h.r.a) / Fmt<BF16>::E;
     if ((g / kThreads) % n != rank) continue;
     l.write<BF16>(row, k, K, repeated, tm, ts, M, S, c, scale);
   }
+  if (LOSS && s.late) leave_last(n);
 }
 
 template <bool BF16, uint32_t LISTS>

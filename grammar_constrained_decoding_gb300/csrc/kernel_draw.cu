@@ -297,10 +297,10 @@ __device__ Drawn draw_screened(Shared& s, const Held<BF16>& h, const RowSettings
 
 // A top-p row over the whole cluster, by trial as described above.  Returns the
 // drawn token to every block; near: a cut that is likely low enough, low: one that
-// certainly is.
+// certainly is.  late: a wait of the block ran out.
 template <bool BF16>
 __device__ Drawn draw_by_trial(Shared& s, const Held<BF16>& h, const RowSettings& q, float near, float low, float M,
-                               float c, float S, const float* u, uint32_t* status) {
+                               float c, float S, const float* u, bool& late) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, n = h.n;
   const float target = fmaxf(q.p * S, 1e-30f);
   float cut = fmaxf(near, low);
@@ -344,7 +344,7 @@ __device__ Drawn draw_by_trial(Shared& s, const Held<BF16>& h, const RowSettings
       }
     }
     if (tid == 0) mbar_expect_tx(&s.bar_best, n * 12u);
-    bool ok = wait_sent(&s.bar_best, round & 1u);
+    bool ok = __syncthreads_and(wait_sent(&s.bar_best, round & 1u));
     d = Drawn();
     for (uint32_t r = 0; r < n; ++r)
       if (s.best[r] > d.best) {
@@ -377,11 +377,8 @@ __device__ Drawn draw_by_trial(Shared& s, const Held<BF16>& h, const RowSettings
            (static_cast<unsigned long long>(__float_as_uint(w.y)) << 32) | __float_as_uint(w.x),
            at_rank(&s.bar_mass, lane));
     if (tid == 0) mbar_expect_tx(&s.bar_mass, n * kWarps * 8u);
-    ok = wait_sent(&s.bar_mass, round & 1u) && ok;
-    if (!ok) {
-      if (tid == 0) record_error(status, CG_DEV_TIMEOUT);
-      return Drawn();
-    }
+    late = !__syncthreads_and(wait_sent(&s.bar_mass, round & 1u) && ok);
+    if (late) return Drawn();
     w = make_float2(0.f, 0.f);
     for (uint32_t i = lane; i < n * kWarps; i += 32) {
       w.x += s.mass[i].x;
@@ -460,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     h.publish(s, c, per_warp);
   }
   if (tid < 32) {
-    const bool ok = wait_sent(&s.bar_rec) && s.late == 0;
+    const bool ok = wait_sent(&s.bar_rec);
     float M, S;
     merge(s.rec, n * kWarps, c, M, S);
     // a lower bound of the threshold, and how to settle it.  Without top-k the
@@ -496,22 +493,25 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
       s.guess = guess;
       s.floor_z = floor_z;
       s.mode = mode;
-      if (rank == 0 && mode == kNothing) {
-        if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
-        else if (bad) record_error(a.status, CG_DEV_BAD_PARAM);
-        a.out_tok[b] = CG_NO_TOKEN;
-        if (a.out_lp) a.out_lp[b] = -INFINITY;
-      }
+      if (!ok) s.late = 1;
     }
   }
   __syncthreads();
   const float M = s.M, S = s.S, cut = s.cut;
   uint32_t mode = s.mode;
-  if (mode == kNothing) {
+  bool late = s.late != 0;
+  if (mode == kNothing || late) {
+    if (rank == 0 && tid == 0) {
+      if (late) record_error(a.status, CG_DEV_TIMEOUT);
+      else if (bad) record_error(a.status, CG_DEV_BAD_PARAM);
+      a.out_tok[b] = CG_NO_TOKEN;
+      if (a.out_lp) a.out_lp[b] = -INFINITY;
+    }
     if (alone == kAny) {  // not before what the others send has arrived
       if (tid == 0) mbar_expect_tx(&s.bar_best, n * 8u);
-      wait_sent(&s.bar_best);
+      late = !__syncthreads_and(wait_sent(&s.bar_best)) || late;
     }
+    if (late) leave_last(n);
     return;
   }
   q.floor_z = s.floor_z;
@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
       if (a.out_lp) a.out_lp[b] = ok ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
       if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
     }
+    if (__any_sync(0xFFFFFFFFu, !ok)) leave_last(n);
     return;
   }
 
@@ -561,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     bool whole;
     const bool ok = h.tallied(s, total, whole, mass);
     mode = !ok ? kNothing : whole && total <= kListCap && mass >= q.p * S * 1.00001f ? kGather : kSpread;
+    if (rank != 0 && mode == kNothing) leave_last(n);
     if (rank != 0 && (mode == kGather || mode == kNothing)) return;
     // where the missing mass probably ends: the mass below a cut falls off by
     // about kFallOff a nat
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
              at_rank(&s.bar_tally, lane));
     }
     if (tid == 0) mbar_expect_tx(&s.bar_tally, n * kWarps * 32u);
-    const bool ok = wait_sent(&s.bar_tally);
+    const bool ok = __syncthreads_and(wait_sent(&s.bar_tally));
 #pragma unroll
     for (int i = 0; i < kCuts; ++i) w[i] = 0.f;
     for (uint32_t i = lane; i < n * kWarps; i += 32) {
@@ -622,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
         a.out_tok[b] = CG_NO_TOKEN;
         if (a.out_lp) a.out_lp[b] = -INFINITY;
       }
+      leave_last(n);
       return;
     }
     mode = kSpread;
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
       a.out_tok[b] = CG_NO_TOKEN;
       if (a.out_lp) a.out_lp[b] = -INFINITY;
     }
+    leave_last(n);
     return;
   }
   const bool gather = mode == kGather;
@@ -679,12 +683,13 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   }
 
   if (!q.k && q.p < 1.f) {
-    d = draw_by_trial<BF16>(s, h, q, near, cut, M, c, S, u, a.status);
-    if (rank != 0) return;
-    if (tid == 0) {
+    d = draw_by_trial<BF16>(s, h, q, near, cut, M, c, S, u, late);
+    if (late && tid == 0) record_error(a.status, CG_DEV_TIMEOUT);
+    if (rank == 0 && tid == 0) {
       a.out_tok[b] = d.best ? best_id(d.best) : CG_NO_TOKEN;
       if (a.out_lp) a.out_lp[b] = d.best ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
     }
+    if (late) leave_last(n);
     return;
   }
 
@@ -718,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     a.out_tok[b] = there ? best_id(d.best) : CG_NO_TOKEN;
     if (a.out_lp) a.out_lp[b] = there ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
   }
+  if (__any_sync(0xFFFFFFFFu, !ok)) leave_last(n);
 }
 
 template <bool BF16>

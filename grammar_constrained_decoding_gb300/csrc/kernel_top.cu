@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
       }
     }
   } else if (rank != 0) {
+    if (late) leave_last(n);
     return;
   }
   if (late && tid == 0) record_error(a.status, CG_DEV_TIMEOUT);
@@ -142,6 +143,50 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
     lps[i] = -INFINITY;
   }
   if (a.out_lse && tid == 0) a.out_lse[b] = M > -INFINITY ? M + log_s : -INFINITY;
+  if (late) leave_last(n);
+}
+
+// Self-test of leave_last: rank 0's wait runs out at once and it leaves last; the other
+// blocks are kLag waits slower, meet once as a selection does, and send to rank 0's
+// shared memory then.  out: how many of their messages and additions rank 0 saw.
+constexpr uint32_t kTestCluster = 4, kLag = 2;
+struct TestShared {
+  uint64_t never, sent;
+  unsigned long long slot[kTestCluster];
+  uint32_t added;
+};
+__global__ void __launch_bounds__(64) leave_last_self_test_kernel(uint32_t* out, uint32_t* status) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  TestShared& s = *reinterpret_cast<TestShared*>(smem);
+  const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x;
+  griddep_wait();
+  if (tid == 0) {
+    mbar_init(&s.never, 1);
+    mbar_init(&s.sent, 1);
+    s.added = 0;
+    for (uint32_t i = 0; i < kTestCluster; ++i) s.slot[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  cluster_sync(n);
+  bool ok = true;
+  for (uint32_t i = 0; i < (rank == 0 ? 1 : 1 + kLag); ++i) ok = __syncthreads_and(wait_sent(&s.never)) && ok;
+  if (rank != 0) {
+    cluster_sync(n);
+    if (tid == 0) {
+      add_remote(at_rank(&s.added, 0), 1u);
+      send(at_rank(&s.slot[rank], 0), 1ull, at_rank(&s.sent, 0));
+    }
+    return;
+  }
+  if (!ok) leave_last(n);
+  if (tid == 0) {
+    mbar_expect_tx(&s.sent, (n - 1) * 8u);
+    uint32_t seen = wait_sent(&s.sent) ? s.added : 0u;
+    for (uint32_t i = 0; i < n; ++i) seen += uint32_t(s.slot[i]);
+    *out = seen;
+    if (!ok) record_error(status, CG_DEV_TIMEOUT);
+  }
 }
 
 template <bool BF16>
@@ -170,5 +215,16 @@ extern "C" int cg_top_logprobs(cg_ctx* c, const void* d_logits, int dtype, uint3
   const int dev = ctx_device(c);
   const cudaError_t e =
       dtype == CG_BF16 ? launch_top<true>(dev, B, a, v.stream) : launch_top<false>(dev, B, a, v.stream);
+  return e == cudaSuccess ? CG_OK : CG_E_CUDA;
+}
+
+extern "C" int cg_self_test_cluster_timeout(cg_ctx* c, uint32_t* d_out) {
+  using namespace cgk;
+  if (!c || !d_out || !aligned4(d_out)) return CG_E_ARG;
+  DeviceGuard dg(ctx_device(c), "cg_self_test_cluster_timeout");
+  if (!dg.ok) return CG_E_CUDA;
+  const CtxView v = ctx_view(c);
+  const cudaError_t e = launch_clusters<leave_last_self_test_kernel>(ctx_device(c), 1, kTestCluster, 64,
+                                                                     sizeof(TestShared), v.stream, d_out, v.t.status);
   return e == cudaSuccess ? CG_OK : CG_E_CUDA;
 }

@@ -134,6 +134,20 @@ __device__ __forceinline__ void cluster_sync(uint32_t n) {
     cluster_wait();
   }
 }
+// A block whose wait ran out does not leave before the others of its cluster, who may
+// still send to its shared memory or read it.  Threads that have left count as arrived,
+// so a round ends when the others meet once more or are gone; they meet less than kMeets
+// times (a selection has five levels at most, and there are two of them).  The others'
+// waits are bounded, so they come to their end.  For all threads of the block that have
+// not left.
+constexpr uint32_t kMeets = 32;
+__device__ __forceinline__ void leave_last(uint32_t n) {
+#pragma unroll 1
+  for (uint32_t i = 0; n > 1 && i < kMeets; ++i) {
+    cluster_arrive();
+    cluster_wait();
+  }
+}
 
 constexpr uint32_t kMaxRecords = kMaxCluster * kWarps;  // warps of a cluster
 constexpr uint32_t kMaxBounds = 512;                     // group maxima a cluster exchanges
@@ -762,12 +776,12 @@ struct Held {
     return s.n_local <= kListCap;
   }
   // The gathered entries' count, whether every warp has sent its own, and the
-  // mass, to every thread of a block that tallies go to; false when the wait ran
-  // out.  The barrier's expectation is set here: early tallies wait in its
-  // transaction count.
+  // mass, to every thread of a block that tallies go to; false to all of them when
+  // a wait ran out.  The barrier's expectation is set here: early tallies wait in
+  // its transaction count.
   __device__ __forceinline__ bool tallied(Shared& s, uint32_t& count, bool& whole, float& mass) const {
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_tally, n * uint32_t(sizeof(Tally)));
-    const bool ok = wait_sent(&s.bar_tally);
+    const bool ok = __syncthreads_and(wait_sent(&s.bar_tally));
     mass = 0.f;
     count = 0;
     bool over = false;
@@ -780,10 +794,10 @@ struct Held {
     whole = !over;
     return ok;
   }
-  // Rank 0, after tallied(): the list's entries are there
+  // Rank 0, after tallied(): the list's entries are there; the same to every thread
   __device__ __forceinline__ bool listed(Shared& s, uint32_t count) const {
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_list, min(count, kListCap) * 8u);
-    return wait_sent(&s.bar_list);
+    return __syncthreads_and(wait_sent(&s.bar_list));
   }
 };
 

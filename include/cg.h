@@ -413,6 +413,14 @@ int cg_accept_many(cg_ctx* c, const uint32_t* d_states, const uint16_t* d_gid, c
  * Errors: CG_E_ARG, CG_E_CUDA. */
 int cg_self_test_wait_timeout(cg_ctx* c);
 
+/* Self-test of what a block of a cluster does when its bounded wait runs out while
+ * others may still send to its shared memory: it leaves after them.  One cluster of
+ * four blocks; the first gives up (cg_ctx_status then reports CG_DEV_TIMEOUT), the
+ * others send two messages each a second or so later.  d_out: u32, the number of
+ * messages that had arrived when the first block left (6).  Errors: CG_E_ARG,
+ * CG_E_CUDA. */
+int cg_self_test_cluster_timeout(cg_ctx* c, uint32_t* d_out);
+
 /* ---- per-row sampling, best tokens, distillation -------------------------------- */
 
 /* What a server and a trainer do with the masked rows beyond step 2: sampling
