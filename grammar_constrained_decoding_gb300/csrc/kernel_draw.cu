@@ -434,7 +434,10 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
   bool tight = true;
   const uint32_t per_warp = q.k && !alone ? bounds_per_warp(q.k, n, tight) : 0u;
   const bool taken = h.template take<true>(s, c);
-  if (!taken) s.late = 1;
+  if (!taken) {
+    s.late = 1;
+    record_error(a.status, CG_DEV_TIMEOUT);
+  }
   if (alone) {
     ready_others();
     if (alone == kBest) {

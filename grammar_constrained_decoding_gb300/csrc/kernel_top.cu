@@ -50,7 +50,10 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   griddep_wait();
   h.start(s, true);
   may_send();
-  if (!h.template take<true>(s, kLog2e)) s.late = 1;
+  if (!h.template take<true>(s, kLog2e)) {
+    s.late = 1;
+    record_error(a.status, CG_DEV_TIMEOUT);
+  }
   bool tight;
   const uint32_t per_warp = bounds_per_warp(a.n, n, tight);
   ready_others();
