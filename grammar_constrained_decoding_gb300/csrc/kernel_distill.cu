@@ -434,15 +434,15 @@ __global__ void __launch_bounds__((kTakers + 1 + LISTS) * 32, 2) loss_kernel(con
         if (list_t[k] > -INFINITY) ts += ex2((list_t[k] - tm) * c);
       ts = warp_reduce(ts, SumOp());
       if (!late) late = !__all_sync(0xFFFFFFFFu, wait_sent(s.bar_rec + (use & 1u), (use / 2) & 1u));
-      float M, S;
-      merge(s.rec[use & 1u], n * kTakers, c, M, S);
+      float M, S, rest;
+      merge(s.rec[use & 1u], n * kTakers, c, M, S, rest);
       __syncwarp();
       if (i + 2 * n < rows && lane < n) {  // the buffer is used again
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                          at_rank(&s.done[rank][use & 1u], lane))
                      : "memory");
       }
-      const float log_ts = logf(ts), log_s = logf(S);
+      const float log_ts = logf(ts), log_s = log1pf(rest);
       float part = 0.f;
       for (uint32_t k = lane; k < K; k += 32)
         if (list_t[k] > -INFINITY) part += loss_term(list_t[k] - tm, ts, log_ts, list_x[k] - M, log_s, c, T);
@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
       }
       if (!late) late = !__all_sync(0xFFFFFFFFu, mbar_wait(s.bar_list + buf, parity) &&
                                                  wait_sent(s.bar_rec + buf, parity));
-      if (LOSS) merge(s.rec[buf], n * kTakers, c, M, S);
+      float rest = 0.f;
+      if (LOSS) merge(s.rec[buf], n * kTakers, c, M, S, rest);
       const bool listed = s.tm[buf] > -INFINITY;
       const float w = __fdiv_rn(listed ? T * up : 0.f, S);
       char* to = out(i);
@@ -641,8 +642,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
       const uint32_t b = first + i * step, buf = i & 1u, parity = (i / 2) & 1u;
       if (i + 1 < rows) read(i + 1);
       if (!late) late = !__all_sync(0xFFFFFFFFu, wait_sent(s.bar_rec + buf, parity));
-      float M = 0.f, S = 1.f;
-      if (LOSS) merge(s.rec[buf], n * kTakers, c, M, S);
+      float M = 0.f, S = 1.f, rest = 0.f;
+      if (LOSS) merge(s.rec[buf], n * kTakers, c, M, S, rest);
       else kept_norm(a, b, M, S);
       list_sync();
       if (!late && lt == 0 && i + 2 < rows) mbar_expect_tx(s.bar_rec + buf, told);
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
       const bool listed = tm > -INFINITY;
       if (LOSS && rank == 0) {
         float part = 0.f;
-        const float log_ts = logf(ts), log_s = logf(S);
+        const float log_ts = logf(ts), log_s = log1pf(rest);
         for (uint32_t k = lt; k < K; k += kListThreads)
           if (l.id[k] != CG_NO_TOKEN) part += loss_term(l.t[k] - tm, ts, log_ts, l.x[k] - M, log_s, c, T);
         part = list_fold(part, SumOp(), s.red);
@@ -738,15 +739,16 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
   float M = 0.f, S = 1.f;  // p = exp2((x - M) c) / S
   if (LOSS) {
     if (!h.template take<true>(s, c)) record_error(a.status, CG_DEV_TIMEOUT);
+    const unsigned long long rec = h.record(c);
     ready_others();
-    h.publish(s, c);
+    h.publish(s, rec);
     if (tid < 32) {
       const bool ok = wait_sent(&s.bar_rec);
-      float m, sum;
-      merge(s.rec, n * kWarps, c, m, sum);
+      float m, sum, rest;
+      merge(s.rec, n * kWarps, c, m, sum, rest);
       if (tid == 0) {
         s.M = m;
-        s.S = sum;
+        s.rest = rest;
         if (!ok) {
           s.late = 1;
           record_error(a.status, CG_DEV_TIMEOUT);
@@ -755,10 +757,10 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
     }
     __syncthreads();
     M = s.M;
-    S = s.S;
+    S = M > -INFINITY ? 1.f + s.rest : 0.f;
     if (rank == 0) {
       float part = 0.f;
-      const float log_ts = logf(ts), log_s = logf(S);
+      const float log_ts = logf(ts), log_s = log1pf(s.rest);
       for (uint32_t k = tid; k < K; k += kThreads)
         if (l.id[k] != CG_NO_TOKEN) part += loss_term(l.t[k] - tm, ts, log_ts, l.x[k] - M, log_s, c, T);
       __syncthreads();

@@ -438,12 +438,13 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     s.late = 1;
     record_error(a.status, CG_DEV_TIMEOUT);
   }
+  ready_others();
+  const unsigned long long rec = h.record(c);
   if (alone) {
-    ready_others();
     if (alone == kBest) {
-      h.template report<true>(s, c, s.top);
+      h.template report<true>(s, rec, s.top);
     } else {
-      h.template report<false>(s, c);
+      h.template report<false>(s, rec);
       // the block's best by scores relative to its own maximum: their order is that
       // of scores relative to the row's
       q.floor_z = -INFINITY;
@@ -456,13 +457,12 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     }
     if (rank != 0) return;
   } else {
-    ready_others();
-    h.publish(s, c, per_warp);
+    h.publish(s, rec, per_warp);
   }
   if (tid < 32) {
     const bool ok = wait_sent(&s.bar_rec);
-    float M, S;
-    merge(s.rec, n * kWarps, c, M, S);
+    float M, S, rest;  // S = 1 + rest
+    merge(s.rec, n * kWarps, c, M, S, rest);
     // a lower bound of the threshold, and how to settle it.  Without top-k the
     // mass that top-p refers to is known, so min-p bounds what matters as well.
     const float floor_z = logf(fminf(fmaxf(mp, 0.f), 1.f));  // -inf for min_p = 0
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     }
     if (tid == 0) {
       s.M = M;
-      s.S = S;
+      s.rest = rest;
       s.cut = cut;
       s.guess = guess;
       s.floor_z = floor_z;
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     }
   }
   __syncthreads();
-  const float M = s.M, S = s.S, cut = s.cut;
+  const float M = s.M, S = 1.f + s.rest, cut = s.cut;
   uint32_t mode = s.mode;
   bool late = s.late != 0;
   if (mode == kNothing || late) {
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     const unsigned long long best = warp_reduce(d.best, MaxOp());
     if (alone == kBest ? tid == 0 : d.best == best) {
       a.out_tok[b] = ok ? best_id(best) : CG_NO_TOKEN;
-      if (a.out_lp) a.out_lp[b] = ok ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
+      if (a.out_lp) a.out_lp[b] = ok ? __fdiv_rn(d.x - M, q.Ts) - log1pf(s.rest) : -INFINITY;
       if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
     }
     if (__any_sync(0xFFFFFFFFu, !ok)) leave_last(n);
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     const unsigned long long best = block_max(d.best, s.red64);
     if (d.best == best && (best != 0ull || tid == 0)) {
       a.out_tok[b] = best_id(best);
-      if (a.out_lp) a.out_lp[b] = __fdiv_rn(d.x - M, q.Ts) - logf(S);
+      if (a.out_lp) a.out_lp[b] = __fdiv_rn(d.x - M, q.Ts) - log1pf(s.rest);
     }
     return;
   }
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     if (late && tid == 0) record_error(a.status, CG_DEV_TIMEOUT);
     if (rank == 0 && tid == 0) {
       a.out_tok[b] = d.best ? best_id(d.best) : CG_NO_TOKEN;
-      if (a.out_lp) a.out_lp[b] = d.best ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
+      if (a.out_lp) a.out_lp[b] = d.best ? __fdiv_rn(d.x - M, q.Ts) - log1pf(s.rest) : -INFINITY;
     }
     if (late) leave_last(n);
     return;
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 4) draw_kernel(const DrawArgs a, uin
     if (!ok) record_error(a.status, CG_DEV_TIMEOUT);
     const bool there = ok && d.best;
     a.out_tok[b] = there ? best_id(d.best) : CG_NO_TOKEN;
-    if (a.out_lp) a.out_lp[b] = there ? __fdiv_rn(d.x - M, q.Ts) - logf(S) : -INFINITY;
+    if (a.out_lp) a.out_lp[b] = there ? __fdiv_rn(d.x - M, q.Ts) - log1pf(s.rest) : -INFINITY;
   }
   if (__any_sync(0xFFFFFFFFu, !ok)) leave_last(n);
 }

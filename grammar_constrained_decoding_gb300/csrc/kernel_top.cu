@@ -56,22 +56,23 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
   }
   bool tight;
   const uint32_t per_warp = bounds_per_warp(a.n, n, tight);
+  const unsigned long long rec = h.record(kLog2e);
   ready_others();
-  h.publish(s, kLog2e, per_warp);
+  h.publish(s, rec, per_warp);
   if (tid < 32) {
     const bool ok = wait_sent(&s.bar_rec);
-    float m, sum;
-    merge(s.rec, n * kWarps, kLog2e, m, sum);
+    float m, sum, rest;
+    merge(s.rec, n * kWarps, kLog2e, m, sum, rest);
     const uint32_t key = per_warp ? bound_key(s, n * kWarps * per_warp, a.n) : 0u;
     if (tid == 0) {
       s.M = m;
-      s.S = sum;
+      s.rest = rest;
       s.cut = key >= kKeyLowest ? fkey_inv(key) : -FLT_MAX;
       if (!ok) s.late = 1;
     }
   }
   __syncthreads();
-  const float M = s.M, S = s.S;
+  const float M = s.M;
   uint32_t found = 0;
   bool late = s.late != 0;
   const unsigned long long* list = s.list;
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_kernel(const TopArgs a, uint3
     return;
   }
   if (late && tid == 0) record_error(a.status, CG_DEV_TIMEOUT);
-  const float log_s = logf(S);
+  const float log_s = log1pf(s.rest);
   uint32_t* ids = a.out_ids + size_t(b) * a.n;
   float* lps = a.out_lp + size_t(b) * a.n;
   auto write = [&](uint32_t i, unsigned long long e) {

@@ -155,10 +155,12 @@ constexpr uint32_t kMaxBounds = 512;                     // group maxima a clust
 // Exponentials are taken as exp2((x - m) c): the difference to a maximum first, which
 // is exact near it, so that no size of x or c costs precision or overflows.
 
-// What a warp tells all blocks about its part of the row: its maximum and its
-// sum of exp2((x - m) c).
+// What a warp tells all blocks about its part of the row: its maximum and the sum of
+// exp2((x - m) c) over its elements but one that is the maximum.  Without that 1 the sum
+// is as good where the maximum has nearly all the mass: log p = -log(1 + rest) of such a
+// token had errors of 4e-7 with the 1 inside, 1e-4 of a log p of 0.003, all of one of 5e-9.
 struct __align__(8) Record {
-  float m, s;
+  float m, rest;
 };
 // What a block tells about the entries it has sent.
 struct __align__(8) Tally {
@@ -176,7 +178,7 @@ constexpr uint32_t kMaxGroups = kChunk * kMaxChunks;  // of a thread: a lane a c
 struct __align__(16) Meet {
   uint64_t bar_rec, bar_tally, bar_list, bar_best, bar_mass;  // kBars barriers in a row ...
   uint64_t bar_part[kMaxChunks];                              // ... the last for the copies of this block's part
-  float M, S;                          // what the merging warp found
+  float M, rest;                       // what the merging warp found
   uint32_t late;                       // a bounded wait ran out
   uint32_t n_list, n_local, n_stage;
   Record rec[kMaxRecords];
@@ -504,11 +506,26 @@ __device__ __forceinline__ void add_groups(const uint4* v, float t, float c, flo
   acc = __fadd2_rn(acc, __fadd2_rn(sum[0], sum[1]));
 }
 
-// A warp's maximum and sum from its lanes', as the bits of a Record
+__device__ __forceinline__ unsigned long long record_bits(float m, float rest) {
+  return (static_cast<unsigned long long>(__float_as_uint(rest)) << 32) | __float_as_uint(m);
+}
+// A lane's share of its warp's record: m the warp's maximum, who the lanes that have it.
+// The shares of all lanes and the lanes of `who` but one make the rest.
+__device__ __forceinline__ float share_of(float tm, float ts, float c, float& m, uint32_t& who) {
+  m = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, fkey(tm)));
+  who = __ballot_sync(0xFFFFFFFFu, tm == m);
+  if (!(tm > -INFINITY)) return 0.f;
+  return tm == m ? ts - 1.f : ts * ex2((tm - m) * c);
+}
+__device__ __forceinline__ unsigned long long record_of(float share, float m, uint32_t who) {
+  return record_bits(m, warp_reduce(share, SumOp()) + float(__popc(who) - 1));
+}
+// A warp's record from its lanes' maxima and sums
 __device__ __forceinline__ unsigned long long warp_record(float tm, float ts, float c) {
-  const float m = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, fkey(tm)));
-  const float sum = warp_reduce(tm > -INFINITY ? ts * ex2((tm - m) * c) : 0.f, SumOp());
-  return (static_cast<unsigned long long>(__float_as_uint(sum)) << 32) | __float_as_uint(m);
+  float m;
+  uint32_t who;
+  const float share = share_of(tm, ts, c, m, who);
+  return record_of(share, m, who);
 }
 
 // The part of a row that a block holds
@@ -624,18 +641,17 @@ struct Held {
     ts = acc.x + acc.y;
     return ok;
   }
-  // Tells every block of the cluster this warp's maximum and sum, and, for a
+  // Tells every block of the cluster this warp's record, and, for a
   // bound on the k-th largest logit, the maxima of `per_warp` groups of its
   // lanes (a power of two, 0 for none), completing on bar_rec.  After
   // ready_others().
-  __device__ __forceinline__ void publish(Meet& s, float c) const { publish_with(s, c, 0u, nullptr); }
-  __device__ __forceinline__ void publish(Common& s, float c, uint32_t per_warp) const {
-    publish_with(s, c, per_warp, s.bound);
+  __device__ __forceinline__ void publish(Meet& s, unsigned long long rec) const { publish_with(s, rec, 0u, nullptr); }
+  __device__ __forceinline__ void publish(Common& s, unsigned long long rec, uint32_t per_warp) const {
+    publish_with(s, rec, per_warp, s.bound);
   }
-  __device__ __forceinline__ void publish_with(Meet& s, float c, uint32_t per_warp, uint32_t* bound) const {
+  __device__ __forceinline__ void publish_with(Meet& s, unsigned long long rec, uint32_t per_warp, uint32_t* bound) const {
     const uint32_t lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
     if (threadIdx.x == 0) mbar_expect_tx(&s.bar_rec, n * kWarps * (8u + 4u * per_warp));
-    const unsigned long long rec = record(c);
     if (lane < n) send(at_rank(&s.rec[w], lane), rec, at_rank(&s.bar_rec, lane));
     if (per_warp == 0) return;
     uint32_t key = fkey(tm);
@@ -645,14 +661,42 @@ struct Held {
       send(at_rank(&bound[w * per_warp + (i & (per_warp - 1))], i / per_warp), key,
            at_rank(&s.bar_rec, i / per_warp));
   }
-  // this warp's maximum and sum
-  __device__ __forceinline__ unsigned long long record(float c) const { return warp_record(tm, ts, c); }
+  // This warp's record.  Where no share is large (the rest may be lost in the roundings of
+  // 1 + rest) the sum of the lane with the maximum is added up again without it.
+  __device__ __forceinline__ unsigned long long record(float c) const {
+    float m;
+    uint32_t who;
+    float share = share_of(tm, ts, c, m, who);
+    if (!__any_sync(0xFFFFFFFFu, share >= 0.25f) && __popc(who) == 1) share = again(share, __ffs(who) - 1, m, c);
+    return record_of(share, m, who);
+  }
+  // The shares with the elements of lane `from` but one that is the maximum spread over
+  // the warp, a word of the lane's groups each
+  __device__ __forceinline__ float again(float share, uint32_t from, float m, float c) const {
+    const uint32_t lane = threadIdx.x & 31, words = nv * 4;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(part + (threadIdx.x & ~31u) + from);
+    if (lane == from) share = 0.f;
+    bool left_out = false;
+    __syncwarp();  // what the lane has written there
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < words; i0 += 32) {
+      const uint32_t i = i0 + lane, w = i < words ? p[(i >> 2) * (kThreads * 4) + (i & 3u)] : F::kNegInf;
+      float2 x = BF16 ? make_float2(lo_f(w), hi_f(w)) : make_float2(__uint_as_float(w), -INFINITY);
+      const uint32_t hits = __ballot_sync(0xFFFFFFFFu, x.x == m || x.y == m);
+      if (hits && !left_out) {
+        left_out = true;
+        if (lane == __ffs(hits) - 1) (x.x == m ? x.x : x.y) = -INFINITY;
+      }
+      share += ex2((x.x - m) * c);
+      if (BF16) share += ex2((x.y - m) * c);
+    }
+    return share;
+  }
   // Tells rank 0 alone, and with BEST this warp's best token too
   template <bool BEST>
-  __device__ __forceinline__ void report(Meet& s, float c, unsigned long long* top = nullptr) const {
+  __device__ __forceinline__ void report(Meet& s, unsigned long long rec, unsigned long long* top = nullptr) const {
     const uint32_t lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
     if (rank == 0 && threadIdx.x == 0) mbar_expect_tx(&s.bar_rec, n * kWarps * (BEST ? 16u : 8u));
-    const unsigned long long rec = record(c);
     if (BEST) {
       const float m = __uint_as_float(uint32_t(rec));
       uint32_t t = 0xFFFFFFFFu;
@@ -801,17 +845,33 @@ struct Held {
   }
 };
 
-// The row's maximum and sum of exp2((x - M) c) from the warps' records, the same
-// in every warp of the cluster.  For one warp of a block, after its wait.
-__device__ __forceinline__ void merge(const Record* rec, uint32_t count, float c, float& M, float& S) {
-  const uint32_t lane = threadIdx.x & 31;
+// The row's maximum, and the sum S = 1 + rest of exp2((x - M) c), from the warps'
+// records, the same in every warp of the cluster (0 and 0 for an empty row).  For one
+// warp of a block, after its wait.
+__device__ __forceinline__ void merge(const Record* rec, uint32_t count, float c, float& M, float& S, float& rest) {
+  constexpr uint32_t kEach = kMaxRecords / 32;
+  Record r[kEach];
   uint32_t top = 0;
-  for (uint32_t i = lane; i < count; i += 32) top = max(top, fkey(rec[i].m));
+#pragma unroll
+  for (uint32_t k = 0; k < kEach; ++k) {
+    const uint32_t i = k * 32 + (threadIdx.x & 31);
+    r[k].m = -INFINITY;
+    r[k].rest = 0.f;
+    if (i < count) r[k] = rec[i];
+    top = max(top, fkey(r[k].m));
+  }
   M = fkey_inv(__reduce_max_sync(0xFFFFFFFFu, top));
   float t = 0.f;
-  for (uint32_t i = lane; i < count; i += 32)
-    if (rec[i].m > -INFINITY) t += rec[i].s * ex2((rec[i].m - M) * c);
-  S = warp_reduce(t, SumOp());
+  uint32_t have = 0;  // records with the row's maximum: all but one of their 1s belong to the rest
+#pragma unroll
+  for (uint32_t k = 0; k < kEach; ++k) {
+    const bool has = r[k].m == M;
+    have += has ? 1u : 0u;
+    t += has ? r[k].rest : (1.f + r[k].rest) * ex2((r[k].m - M) * c);
+  }
+  have = __reduce_add_sync(0xFFFFFFFFu, have);
+  rest = warp_reduce(t, SumOp()) + float(have - 1);
+  S = M > -INFINITY ? 1.f + rest : 0.f;
 }
 
 // Groups of lanes per warp whose maxima bound the k-th largest logit: the least power

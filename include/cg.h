@@ -439,7 +439,9 @@ int cg_self_test_cluster_timeout(cg_ctx* c, uint32_t* d_out);
  *  A logit that is -inf or NaN counts as not allowed; +inf counts as the
  *  largest finite value of the type.  A_b is the set of row b's allowed tokens.
  *  Sums, maxima and normalisers are held in 32 bits or more, and no result
- *  depends on the order in which the device runs its blocks.
+ *  depends on the order in which the device runs its blocks.  A log-probability
+ *  near 0 (of a token with nearly all the mass) is good to a relative error of
+ *  the others' sum, not only to the rounding of 1.
  *  The calls allocate nothing and may be captured; they run on the context's
  *  stream like the step calls, so inputs made on another stream need an event
  *  between the two.  Errors: CG_E_ARG for a NULL required pointer, an unknown
