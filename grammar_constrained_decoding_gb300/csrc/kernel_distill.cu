@@ -447,7 +447,7 @@ __global__ void __launch_bounds__((kTakers + 1 + LISTS) * 32, 2) loss_kernel(con
       for (uint32_t k = lane; k < K; k += 32)
         if (list_t[k] > -INFINITY) part += loss_term(list_t[k] - tm, ts, log_ts, list_x[k] - M, log_s, c, T);
       part = warp_reduce(part, SumOp());
-      if (lane == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, S, log_s);
+      if (lane == 0) store_loss(a, b, listed ? T * (T * part) : 0.f, M, S, log_s);
     }
   }
   if (late) record_error(a.status, CG_DEV_TIMEOUT);
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
         for (uint32_t k = lt; k < K; k += kListThreads)
           if (l.id[k] != CG_NO_TOKEN) part += loss_term(l.t[k] - tm, ts, log_ts, l.x[k] - M, log_s, c, T);
         part = list_fold(part, SumOp(), s.red);
-        if (lt == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, S, log_s);
+        if (lt == 0) store_loss(a, b, listed ? T * (T * part) : 0.f, M, S, log_s);
       }
       if (!late) late = !__all_sync(0xFFFFFFFFu, mbar_wait(s.bar_done + buf, parity));
       if (listed) {
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 3) held_kernel(const DistillArgs a, 
         if (l.id[k] != CG_NO_TOKEN) part += loss_term(l.t[k] - tm, ts, log_ts, l.x[k] - M, log_s, c, T);
       __syncthreads();
       part = block_sum(part, s.red_f);
-      if (tid == 0) store_loss(a, b, listed ? T * T * part : 0.f, M, S, log_s);
+      if (tid == 0) store_loss(a, b, listed ? T * (T * part) : 0.f, M, S, log_s);
     }
   } else {
     kept_norm(a, b, M, S);
