@@ -144,7 +144,7 @@ struct List {
   __device__ __forceinline__ void write(char* to, uint32_t k, uint32_t K, bool repeated, float tm, float ts, float M,
                                         float S, float c, float scale) const {
     float q = ex2((t[k] - tm) * c);
-    if (repeated) {  // every entry of the id writes the same sum
+    if (repeated) {  // every entry of the id writes the same sum (K^2 steps: 1024 of 1024 x 128256 1611 us, without 245)
       q = 0.f;
       for (uint32_t j = 0; j < K; ++j)
         if (id[j] == id[k]) q += ex2((t[j] - tm) * c);
@@ -302,7 +302,7 @@ struct Ring {
 //
 // Nothing of a row is needed twice.  The warps send their maxima and sums of the
 // cluster's i-th row to block i mod n, where one more warp (of one or two) has read
-// the row's list meanwhile and finishes the row.  2048 x 128256 bf16: 83.0 us, 6.3 TB/s, bound by the
+// the row's list meanwhile and finishes the row.  2048 x 128256 bf16: 81.2 us, 6.5 TB/s, bound by the
 // memory.
 //
 // Few barriers and many loads at once: 8 groups of a thread a chunk.  Of 2048 x 128256
@@ -466,8 +466,8 @@ __global__ void __launch_bounds__((kTakers + 1 + LISTS) * 32, 2) loss_kernel(con
 // gradient may take the logits' place.  (That keeps a cluster's blocks side by side, too:
 // without it the gradient alone of 512 x 151936 took 63.8 us, with it 57.2.)
 //
-// 2048 x 128256 bf16: loss and gradient 203.7 us, 5.2 TB/s of reads and writes; the
-// gradient alone 172.1, 6.1 TB/s.  The memory bounds them, and with the loss the exchange
+// 2048 x 128256 bf16: loss and gradient 197.4 us, 5.3 TB/s of reads and writes; the
+// gradient alone 162 to 171, 6.1 to 6.5 TB/s.  The memory bounds them, and with the loss the exchange
 // of a row's sums, which the next row's copies cover only in part: of a block's six chunks
 // two are ahead.  Fetching a chunk's values before the stores of the one before: 218 us.
 // Clusters of 6 and 8 blocks with three or two chunks each are not all resident together:
@@ -685,13 +685,13 @@ __global__ void __launch_bounds__(kGradThreads, 2) grad_kernel(const DistillArgs
 // blocks hold the row (logit_row.cuh) and more of them share an SM.
 //
 // Microseconds, held and streamed, loss and gradient, then the gradient alone (bf16):
-//   4096 x 12000    78.3   87.6     51.4   58.3
-//   4096 x 20000    94.7   94.1     64.9   65.3
-//   1024 x 32000    37.5   36.1     31.6   28.3
-//   64 x 64006       9.2    8.0      7.1    7.9
-//   64 x 128256     14.0   10.9     10.9   11.3
-//   128 x 128256    23.7   18.1     19.3   16.3
-//   2048 x 128256  221.2  203.7    177.9  172.1
+//   4096 x 12000    78.2   79.5     52.1   60.4
+//   4096 x 20000    94.8   93.2     66.3   68.9
+//   1024 x 32000    37.3   35.5     32.0   29.4
+//   64 x 64006       9.1    7.5      7.2    7.9
+//   64 x 128256     13.4   10.5     10.4   10.8
+//   128 x 128256    23.6   17.7     19.2   16.2
+//   2048 x 128256  223.2  197.5    182.2  161.9
 constexpr uint64_t kShortRow = 48 << 10, kSmallLoss = 6 << 20, kSmallGrad = 16 << 20;  // bytes
 // Groups of a thread for many rows: 64 KB parts, three blocks an SM.
 constexpr uint32_t kFull = 16;

@@ -27,13 +27,15 @@
 // and the best of the rest is tried.  The first try succeeds with probability
 // top_p; after kTries the threshold is found by radix selection.
 //
-// What bounds it: instructions and the exchanges between blocks.  256 x 128256 bf16
-// (66 MB, 9.7 us to read) take 23.0 us for greedy rows, which read, sum and report
-// (2.9 TB/s); 37.3 with top-k 50 and top-p 0.9, which gather; 51.1 without a cut, which
-// read 131 MB of random numbers too and take a logarithm a token (3.9 TB/s); 59.6 with
-// top-p 0.9 at T = 0.7 and 82.6 with 0.95 at T = 1, where thousands of tokens a row
-// are scored and their masses added.  A single row of 32000 takes 8.3 us: a launch, a
-// row's copy and two exchanges, one after the other.
+// What bounds it: a block's chain of copy, passes and exchanges, with no copy of a later
+// row behind it, and the instructions of the passes.  256 x 128256 bf16 (66 MB, 9.7 us to
+// read), back to back: 23.1 us for greedy rows, which read, sum and report (2.8 TB/s);
+// 37.2 with top-k 50 and top-p 0.9, which gather; 51.9 without a cut, which read 131 MB of
+// random numbers too and take a logarithm a token (3.8 TB/s); 36.2 with min-p 0.05 alone;
+// 60.0 with top-p 0.9 at T = 0.7 (peaked rows 40.3) and 84.0 with 0.95 at T = 1 (78.9),
+// where thousands of tokens a row are scored and their masses added.  A single row of
+// 32000 with top-k and top-p takes 7.4 us: a launch, a row's copy and two exchanges, one
+// after the other.
 #include "logit_row.cuh"
 
 namespace cgk {

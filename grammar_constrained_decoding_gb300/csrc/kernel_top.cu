@@ -11,11 +11,12 @@
 // ties by radix selection, then exactly n entries.
 //
 // What bounds it: the chain of a block, not the memory.  2048 x 32000 bf16, n = 64,
-// takes 69.5 us (1.9 TB/s); the same rows read and summed alone take 27.  A block's
+// takes 69.9 us (1.9 TB/s); the same rows read and summed alone take 27.  A block's
 // part arrives, is summed, the bounds cross the cluster, the entries cross it again,
-// and rank 0 ranks them while its three neighbours on the SM do their own: n = 5 52,
-// n = 20 57 us, so the ordering of 64 costs 12.  Past about 200 entries the bound is
-// loose and the network sorts: n = 256 147 us.
+// and rank 0 ranks them while its three neighbours on the SM do their own: n = 5 52.8,
+// n = 20 57.6 us, so the ordering of 64 costs 12.  Past about 200 entries the bound is
+// loose and the network sorts: n = 256 148 us.  Near the list's capacity the ties of
+// bf16 logits overflow it, and rank 0 reads the row again: n = 1024 4651 us.
 #include "logit_row.cuh"
 
 namespace cgk {

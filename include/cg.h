@@ -467,9 +467,10 @@ int cg_self_test_cluster_timeout(cg_ctx* c, uint32_t* d_out);
  *  d_uniform  : f32, row b at element b * ld_uniform; ld_uniform >= V, or 0 for
  *               one row of numbers shared by every row (coupled draws: a draft
  *               and its verification see the same numbers).  The numbers
- *               of tokens that are not kept have no effect.  NULL is allowed when
- *               d_temp is given and every temperature is 0 (a row with T > 0 then
- *               records CG_DEV_BAD_PARAM).
+ *               of tokens that are not kept have no effect.  Making B x V numbers
+ *               is the caller's, and takes longer than reading the logits.  NULL
+ *               is allowed when d_temp is given and every temperature is 0 (a row
+ *               with T > 0 then records CG_DEV_BAD_PARAM).
  *  d_out_tok  : u32 [B]; CG_NO_TOKEN for a row without allowed tokens
  *  d_out_logprob : f32 [B] or NULL: log p of the token in the softmax over A_b at
  *               temperature T (1 where T = 0), before any cut; -inf without a token
