@@ -121,3 +121,10 @@ def test_process_wide_answers_of_the_row_operators_are_kept_per_device():
     for name in ("logit_row.cuh", "kernel_distill.cu", "kernel_draw.cu", "kernel_top.cu"):
         with open(os.path.join(csrc, name)) as f:
             assert "static std::atomic" not in f.read(), name
+
+
+def test_cluster_self_test_refuses_missing_arguments():
+    lib = _lib.lib()
+    p = ctypes.cast((ctypes.c_uint32 * 4)(), ctypes.c_void_p)
+    assert lib.cg_self_test_cluster_timeout(None, p) == _lib.CG_E_ARG
+    assert lib.cg_self_test_cluster_timeout(None, None) == _lib.CG_E_ARG
