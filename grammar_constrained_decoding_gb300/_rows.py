@@ -1,4 +1,4 @@
-"""Argument checks of the per-row operators' Python entry points.  A tensor of
+"""Argument checks of the vocabulary operators' Python entry points.  A tensor of
 another shape, type, device (the context's is wanted) or layout raises CgError
 with CG_E_ARG before the library sees its pointer."""
 
@@ -33,3 +33,25 @@ def rows_of(call: str, t, what: str, dtypes: tuple, shape: tuple, dev: int = 0) 
     if t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or (t.stride(1) != 1 and shape[1] != 1):
         _refuse(call, what, dtypes, shape, dev, "row-contiguous")
     return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
+
+
+def matrix_of(call: str, t, what: str, dtype, rows: int, dev: int = 0) -> tuple[int, int, int]:
+    """(pointer, row stride in elements, columns) of a matrix of `rows` rows and any width (dtype None: of
+    either float type)."""
+    if t.dim() != 2:
+        raise L.CgError(call, L.CG_E_ARG, f"{what}: a matrix is wanted")
+    shape = (rows, t.shape[1])
+    return *rows_of(call, t, what, LOGITS if dtype is None else (dtype,), shape, dev), t.shape[1]
+
+
+def workspace_of(ctx, call: str, given, nbytes: int) -> tuple[int | None, object]:
+    """(pointer, the tensor that holds it) of nbytes of device memory: the caller's tensor, or a new one that
+    belongs to the context's stream."""
+    if not nbytes:
+        return None, None
+    if given is None:
+        with torch.cuda.device(ctx._dev), torch.cuda.stream(ctx.stream):
+            given = torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
+    elif given.numel() < nbytes:
+        raise L.CgError(call, L.CG_E_ARG, f"workspace: {nbytes} bytes are wanted")
+    return want(call, given, "workspace", (torch.uint8,), given.shape, ctx._dev), given

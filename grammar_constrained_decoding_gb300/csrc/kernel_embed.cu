@@ -1,0 +1,559 @@
+// The embedding lookup with a scale, and its gradient over sorted tokens (cg_embed,
+// cg_embed_grad).
+//
+//   out_i = scale * table[t_i],   grad_v = scale * sum over {i : t_i = v} of g_i
+//
+// Both move rows: memory bounds them.  The lookup is one launch of row copies.  The
+// gradient first sorts the positions by token (stable, so that a token's rows are summed
+// in the order of their positions and no result depends on the order of the blocks), then
+// sums runs of equal tokens: chunks of positions side by side, runs that cross a chunk's
+// border joined afterwards in the chunks' order.  Sums are held in 32 bits and rounded once.
+#include <algorithm>
+
+#include "logit_row.cuh"
+#include "matrix_args.h"
+
+namespace cgk {
+namespace {
+
+using namespace row;
+
+constexpr uint32_t kEmbedSms = 152;
+
+// ---- rows in vectors of BYTES bytes: the widest that every row's start and width allow ----
+template <int BYTES> struct VecOf;
+template <> struct VecOf<16> { using type = uint4; };
+template <> struct VecOf<8> { using type = uint2; };
+template <> struct VecOf<4> { using type = uint32_t; };
+template <> struct VecOf<2> { using type = uint16_t; };
+
+// a vector's elements as floats and back
+template <bool BF16, int BYTES>
+struct Elems {
+  static constexpr int kN = BYTES / (BF16 ? 2 : 4);
+  using Vec = typename VecOf<BYTES>::type;
+  static __device__ __forceinline__ void get(const Vec& v, float (&x)[kN]) {
+    if (BF16) {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) x[i] = __uint_as_float(uint32_t(h[i]) << 16);
+    } else {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) x[i] = __uint_as_float(w[i]);
+    }
+  }
+  static __device__ __forceinline__ Vec put(const float (&x)[kN]) {
+    Vec v;
+    if (BF16) {
+      __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(&v);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) h[i] = __float2bfloat16_rn(x[i]);
+    } else {
+      float* w = reinterpret_cast<float*>(&v);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) w[i] = x[i];
+    }
+    return v;
+  }
+};
+
+// ---- the lookup ----------------------------------------------------------------------------
+
+constexpr uint32_t kLookThreads = 256, kLookEach = 4;
+
+// Vectors are numbered through all rows; a block takes 1024 that follow one another
+template <bool BF16, int BYTES>
+__global__ void __launch_bounds__(kLookThreads) look_kernel(const char* table, uint64_t pitch, const uint32_t* tokens,
+                                                            uint32_t N, uint32_t V, uint32_t vecs, float scale, char* out,
+                                                            uint64_t pitch_out, uint32_t* status) {
+  using E = Elems<BF16, BYTES>;
+  using Vec = typename E::Vec;
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint64_t base = uint64_t(blockIdx.x) * (kLookThreads * kLookEach);
+  const uint32_t row0 = uint32_t(base / vecs), off = uint32_t(base - uint64_t(row0) * vecs);
+  Vec v[kLookEach];
+  uint32_t row[kLookEach], col[kLookEach];
+#pragma unroll
+  for (uint32_t k = 0; k < kLookEach; ++k) {
+    const uint32_t at = off + k * kLookThreads + threadIdx.x;
+    row[k] = row0 + at / vecs;
+    col[k] = at % vecs;
+    v[k] = Vec{};
+    if (row[k] >= N) continue;
+    const uint32_t t = tokens[row[k]];
+    if (t < V) v[k] = *reinterpret_cast<const Vec*>(table + t * pitch + uint64_t(col[k]) * BYTES);
+    else if (t != CG_NO_TOKEN && col[k] == 0) record_error(status, CG_DEV_BAD_TOKEN);
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kLookEach; ++k) {
+    if (row[k] >= N) continue;
+    if (scale != 1.f) {
+      float x[E::kN];
+      E::get(v[k], x);
+#pragma unroll
+      for (int i = 0; i < E::kN; ++i) x[i] = tokens[row[k]] < V ? x[i] * scale : 0.f;
+      v[k] = E::put(x);
+    }
+    *reinterpret_cast<Vec*>(out + row[k] * pitch_out + uint64_t(col[k]) * BYTES) = v[k];
+  }
+}
+
+// ---- sorting the positions by token ----------------------------------------------------------
+
+constexpr uint32_t kSortThreads = 1024, kSortWarps = 32, kSortBits = 9, kBins = 1u << kSortBits;
+constexpr uint32_t kSortMost = 8;   // blocks of the cluster
+
+struct SortArgs {
+  const uint32_t* tokens;
+  uint32_t N, V, passes;
+  uint32_t* key[2];        // tokens in the order so far (V for a row without one)
+  uint32_t* pos[2];        // and their positions; the sorted ones are in key[0], pos[0]
+  uint32_t* status;
+};
+struct SortShared {
+  uint32_t count[kBins];                    // this block's digits, read by the others
+  uint32_t base[kBins];                     // where the next position of a digit goes
+  uint32_t tile_base[kBins];                // ... as a tile begins
+  uint32_t warp_sum[kSortWarps];
+  uint16_t mine[kSortWarps][kBins];         // a tile's digits by warp, then where the warp's begin
+};
+
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i, bool report) {
+  const uint32_t t = a.tokens[i];
+  if (t >= a.V && t != CG_NO_TOKEN && report) record_error(a.status, CG_DEV_BAD_TOKEN);
+  return t < a.V ? t : a.V;
+}
+__device__ __forceinline__ uint32_t read_count(const uint32_t* count, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(count)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// A radix sort by one cluster, 9 bits a pass: each block counts the digits of its own
+// stretch of positions, learns from the others where its digits begin, and moves its
+// positions there tile by tile, in their order.
+__device__ void sort_tokens(const SortArgs& a, SortShared& s) {
+  const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t each = (((a.N + n - 1) / n) + kSortThreads - 1) / kSortThreads * kSortThreads;
+  const uint32_t from = min(a.N, rank * each), to = min(a.N, from + each);
+  for (uint32_t pass = 0; pass < a.passes; ++pass) {
+    const uint32_t shift = pass * kSortBits;
+    const bool odd = (a.passes - pass) & 1u;   // the last pass writes key[0]
+    const uint32_t* const key_in = odd ? a.key[1] : a.key[0];
+    const uint32_t* const pos_in = odd ? a.pos[1] : a.pos[0];
+    uint32_t* const key_out = odd ? a.key[0] : a.key[1];
+    uint32_t* const pos_out = odd ? a.pos[0] : a.pos[1];
+    for (uint32_t i = tid; i < kBins; i += kSortThreads) s.count[i] = 0;
+    __syncthreads();
+    for (uint32_t i = from + tid; i < to; i += kSortThreads) {
+      const uint32_t k = pass == 0 ? sort_key(a, i, true) : __ldcg(key_in + i);
+      atomicAdd(&s.count[(k >> shift) & (kBins - 1)], 1u);
+    }
+    cluster_sync(n);
+    // where this block's positions of digit d begin: all smaller digits, and d's in the blocks before
+    uint32_t all = 0, before = 0;
+    if (tid < kBins)
+      for (uint32_t r = 0; r < n; ++r) {
+        const uint32_t x = n == 1 ? s.count[tid] : read_count(&s.count[tid], r);
+        all += x;
+        if (r < rank) before += x;
+      }
+    uint32_t up = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, up, o);
+      if (lane >= uint32_t(o)) up += x;
+    }
+    if (lane == 31) s.warp_sum[warp] = up;
+    __syncthreads();
+    if (tid < kBins) {
+      uint32_t lower = 0;
+      for (uint32_t w = 0; w < warp; ++w) lower += s.warp_sum[w];
+      s.base[tid] = lower + up - all + before;
+    }
+    for (uint32_t tile = from; tile < to; tile += kSortThreads) {
+      uint32_t* zero = reinterpret_cast<uint32_t*>(s.mine);
+      for (uint32_t i = tid; i < kSortWarps * kBins / 2; i += kSortThreads) zero[i] = 0;
+      __syncthreads();
+      const uint32_t i = tile + tid;
+      const bool there = i < to;
+      uint32_t k = 0, p = i;
+      if (there) {
+        k = pass == 0 ? sort_key(a, i, false) : __ldcg(key_in + i);
+        if (pass) p = __ldcg(pos_in + i);
+      }
+      const uint32_t digit = there ? (k >> shift) & (kBins - 1) : kBins + lane;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
+      const uint32_t nth = __popc(same & ((1u << lane) - 1u));
+      if (there && nth == 0) s.mine[warp][digit] = uint16_t(__popc(same));
+      __syncthreads();
+      if (tid < kBins) {
+        uint32_t at = 0;
+        for (uint32_t w = 0; w < kSortWarps; ++w) {
+          const uint32_t x = s.mine[w][tid];
+          s.mine[w][tid] = uint16_t(at);
+          at += x;
+        }
+        s.tile_base[tid] = s.base[tid];
+        s.base[tid] += at;
+      }
+      __syncthreads();
+      if (there) {
+        const uint32_t to_at = s.tile_base[digit] + s.mine[warp][digit] + nth;
+        __stcg(key_out + to_at, k);
+        __stcg(pos_out + to_at, p);
+      }
+      __syncthreads();
+    }
+    __threadfence();
+    cluster_sync(n);
+  }
+}
+
+// The first cluster sorts; the others meanwhile write zeros over the gradient (all of it: rows
+// of tokens that occur are written again afterwards, at most one a position)
+template <int BYTES>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a, char* out, uint64_t pitch, uint32_t vecs) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using Vec = typename VecOf<BYTES>::type;
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t n = cluster_size();
+  if (blockIdx.x < n) {
+    sort_tokens(a, *reinterpret_cast<SortShared*>(smem));
+    return;
+  }
+  if (!out) return;
+  constexpr uint32_t kEach = 8;
+  const uint64_t all = uint64_t(a.V) * vecs, step = uint64_t(gridDim.x - n) * (kSortThreads * kEach);
+  for (uint64_t base = uint64_t(blockIdx.x - n) * (kSortThreads * kEach); base < all; base += step) {
+    const uint32_t row0 = uint32_t(base / vecs), off = uint32_t(base - uint64_t(row0) * vecs);
+#pragma unroll
+    for (uint32_t k = 0; k < kEach; ++k) {
+      const uint32_t at = off + k * kSortThreads + threadIdx.x, row = row0 + at / vecs;
+      if (row < a.V) *reinterpret_cast<Vec*>(out + row * pitch + uint64_t(at % vecs) * BYTES) = Vec{};
+    }
+  }
+}
+
+// ---- summing runs ------------------------------------------------------------------------------
+
+constexpr uint32_t kSumThreads = 128, kMostChunk = 32;
+
+struct SumArgs {
+  const uint32_t* key;     // sorted tokens, V at the end for rows without one
+  const uint32_t* pos;
+  uint32_t N, V, chunk, vecs, slabs;
+  const char* grad;
+  uint64_t pitch;
+  float scale;
+  bool add;
+  char* out;
+  uint64_t pitch_out;
+  float* part;             // [chunks][2][ld_part]: what a chunk has of the run that began before it, and of the one that goes on
+  uint32_t ld_part;
+};
+
+template <bool BF16, int BYTES>
+__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t token, uint32_t col,
+                                          float (&x)[Elems<BF16, BYTES>::kN]) {
+  using E = Elems<BF16, BYTES>;
+  using Vec = typename E::Vec;
+  Vec* at = reinterpret_cast<Vec*>(a.out + token * a.pitch_out + uint64_t(col) * BYTES);
+  float old[E::kN] = {};
+  if (a.add) E::get(*at, old);
+#pragma unroll
+  for (int i = 0; i < E::kN; ++i) x[i] = a.add ? old[i] + a.scale * x[i] : a.scale * x[i];
+  *at = E::put(x);
+}
+
+// A block takes a chunk of the sorted positions and a slab of the columns
+template <bool BF16, int BYTES>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
+  using E = Elems<BF16, BYTES>;
+  using Vec = typename E::Vec;
+  constexpr uint32_t kAhead = 8;
+  __shared__ uint32_t key[kMostChunk + 2], pos[kMostChunk];
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t chunk = blockIdx.x / a.slabs, col = (blockIdx.x - chunk * a.slabs) * kSumThreads + threadIdx.x;
+  const uint32_t from = chunk * a.chunk, n = min(a.chunk, a.N - from);
+  for (uint32_t i = threadIdx.x; i < n + 2; i += kSumThreads) {
+    // key[i]: of position from + i - 1; past either end a value that no token has
+    const uint32_t at = from + i - 1;
+    key[i] = (i == 0 && from == 0) || at >= a.N ? CG_NO_TOKEN : a.key[at];
+  }
+  for (uint32_t i = threadIdx.x; i < n; i += kSumThreads) pos[i] = a.pos[from + i];
+  __syncthreads();
+  if (col >= a.vecs) return;
+  const char* in = a.grad + uint64_t(col) * BYTES;
+  float acc[E::kN] = {};
+  uint32_t began = 0;
+  for (uint32_t i0 = 0; i0 < n; i0 += kAhead) {
+    Vec v[kAhead];
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u)
+      if (i0 + u < n && key[i0 + u + 1] < a.V) v[u] = *reinterpret_cast<const Vec*>(in + pos[i0 + u] * a.pitch);
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u) {
+      const uint32_t i = i0 + u;
+      if (i >= n) break;
+      const uint32_t token = key[i + 1];
+      if (token >= a.V) break;   // rows without a token come last
+      float x[E::kN];
+      E::get(v[u], x);
+#pragma unroll
+      for (int e = 0; e < E::kN; ++e) acc[e] += x[e];
+      const bool goes_on = key[i + 2] == token;
+      if (goes_on && i + 1 < n) continue;
+      const bool before = began == 0 && key[0] == token;
+      if (!before && !goes_on) {
+        write_sum<BF16, BYTES>(a, token, col, acc);
+      } else {
+        float* to = a.part + (size_t(chunk) * 2 + (before ? 0 : 1)) * a.ld_part + col * E::kN;
+#pragma unroll
+        for (int e = 0; e < E::kN; ++e) to[e] = acc[e];
+      }
+#pragma unroll
+      for (int e = 0; e < E::kN; ++e) acc[e] = 0.f;
+      began = i + 1;
+    }
+  }
+}
+
+constexpr uint32_t kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinColumns = 32;
+
+// A block takes a run that begins in its chunk and goes on, and 32 of its columns: the warps
+// take the chunks' sums in turn, and the warps' sums are added in their order
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumArgs a, uint32_t D) {
+  __shared__ float mine[kJoinWarps][kJoinColumns];
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t chunk = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t from = chunk * a.chunk, to = min(a.N, from + a.chunk);
+  if (to >= a.N) return;
+  const uint32_t token = a.key[to - 1];
+  if (token >= a.V || a.key[to] != token || (from > 0 && a.key[from - 1] == token)) return;
+  uint32_t lo = to, hi = a.N;   // the run's end
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (a.key[mid] > token) hi = mid;
+    else lo = mid + 1;
+  }
+  const uint32_t last = (lo - 1) / a.chunk;
+  for (uint32_t col = blockIdx.y * kJoinColumns + lane; col - lane < D; col += gridDim.y * kJoinColumns) {
+    float s = 0.f;
+    if (col < D)
+#pragma unroll 4
+      for (uint32_t j = chunk + warp; j <= last; j += kJoinWarps)
+        s += a.part[(size_t(j) * 2 + (j == chunk ? 1 : 0)) * a.ld_part + col];
+    mine[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && col < D) {
+      float x = 0.f;
+      for (uint32_t w = 0; w < kJoinWarps; ++w) x += mine[w][lane];
+      x *= a.scale;
+      char* at = a.out + token * a.pitch_out + uint64_t(col) * (BF16 ? 2 : 4);
+      if (BF16) {
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(at);
+        *o = __float2bfloat16_rn(a.add ? __bfloat162float(*o) + x : x);
+      } else {
+        float* o = reinterpret_cast<float*>(at);
+        *o = a.add ? *o + x : x;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+
+// the widest vector that two matrices' rows allow
+int vector_bytes(const void* x, uint64_t pitch_x, const void* y, uint64_t pitch_y, uint64_t width) {
+  const uint64_t all = reinterpret_cast<uintptr_t>(x) | pitch_x | reinterpret_cast<uintptr_t>(y) | pitch_y | width;
+  return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
+}
+
+struct GradPlan {
+  uint32_t chunk, chunks, ld_part;
+  size_t at_key[2], at_pos[2], at_part, bytes;
+};
+// Chunks of 32 positions, fewer where that leaves SMs without work.  Every width gets the same
+// chunks whatever its alignment, so that results do not depend on it.
+GradPlan plan_grad(uint32_t N, uint32_t D, int dtype) {
+  GradPlan p = {};
+  const uint32_t slabs = tiles_of(uint64_t(D) * dtype_size(dtype), kSumThreads * 16);
+  p.chunk = kMostChunk;
+  while (p.chunk > 4 && uint64_t(tiles_of(N, p.chunk)) * slabs < 4 * kEmbedSms) p.chunk /= 2;
+  p.chunks = tiles_of(N, p.chunk);
+  p.ld_part = uint32_t(up_to(D, 4));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up_to(bytes, 256);
+    return here;
+  };
+  for (int i = 0; i < 2; ++i) {
+    p.at_key[i] = take(size_t(N) * 4);
+    p.at_pos[i] = take(size_t(N) * 4);
+  }
+  p.at_part = take(size_t(p.chunks) * 2 * p.ld_part * 4);
+  p.bytes = at;
+  return p;
+}
+
+template <bool BF16, int BYTES>
+cudaError_t launch_look(const void* table, uint64_t pitch, const uint32_t* tokens, uint32_t N, uint32_t V, uint32_t D,
+                        float scale, void* out, uint64_t pitch_out, uint32_t* status, cudaStream_t stream) {
+  const uint32_t vecs = uint32_t(uint64_t(D) * (BF16 ? 2 : 4) / BYTES);
+  const uint32_t blocks = tiles_of(uint64_t(N) * vecs, kLookThreads * kLookEach);
+  return launch_dependent(look_kernel<BF16, BYTES>, dim3(blocks), dim3(kLookThreads), 0, stream,
+                          static_cast<const char*>(table), pitch, tokens, N, V, vecs, scale, static_cast<char*>(out),
+                          pitch_out, status);
+}
+
+template <bool BF16, int BYTES>
+cudaError_t launch_grad(int device, const SortArgs& sort, SumArgs sum, uint32_t chunks, uint32_t D, cudaStream_t stream) {
+  sum.vecs = uint32_t(uint64_t(D) * (BF16 ? 2 : 4) / BYTES);
+  sum.slabs = tiles_of(sum.vecs, kSumThreads);
+  uint32_t n = 1;
+  while (n < kSortMost && sort.N > n * 2048) n *= 2;
+  // without zeros to write the sorting cluster is alone
+  const uint32_t clusters = sum.add ? 1 : kEmbedSms / n;
+  cudaError_t e = launch_clusters<sort_kernel<BYTES>>(device, clusters, n, kSortThreads, sizeof(SortShared), stream, sort,
+                                                     sum.add ? static_cast<char*>(nullptr) : sum.out, sum.pitch_out, sum.vecs);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(sum_kernel<BF16, BYTES>, dim3(chunks * sum.slabs), dim3(kSumThreads), 0, stream, sum);
+  if (e != cudaSuccess || chunks < 2) return e;
+  return launch_dependent(join_kernel<BF16>, dim3(chunks, std::min(tiles_of(D, kJoinColumns), 128u)), dim3(kJoinThreads), 0,
+                          stream, sum, D);
+}
+
+template <typename F>
+cudaError_t by_vector(int dtype, int bytes, const F& f) {
+  if (dtype == CG_BF16)
+    switch (bytes) {
+      case 16: return f.template operator()<true, 16>();
+      case 8: return f.template operator()<true, 8>();
+      case 4: return f.template operator()<true, 4>();
+      default: return f.template operator()<true, 2>();
+    }
+  switch (bytes) {
+    case 16: return f.template operator()<false, 16>();
+    case 8: return f.template operator()<false, 8>();
+    default: return f.template operator()<false, 4>();
+  }
+}
+struct Look {
+  const void* table;
+  uint64_t pitch;
+  const uint32_t* tokens;
+  uint32_t N, V, D;
+  float scale;
+  void* out;
+  uint64_t pitch_out;
+  uint32_t* status;
+  cudaStream_t stream;
+  template <bool BF16, int BYTES>
+  cudaError_t operator()() const {
+    return launch_look<BF16, BYTES>(table, pitch, tokens, N, V, D, scale, out, pitch_out, status, stream);
+  }
+};
+struct Grad {
+  int device;
+  SortArgs sort;
+  SumArgs sum;
+  uint32_t chunks, D;
+  cudaStream_t stream;
+  template <bool BF16, int BYTES>
+  cudaError_t operator()() const {
+    return launch_grad<BF16, BYTES>(device, sort, sum, chunks, D, stream);
+  }
+};
+
+int embed_args(const cg_ctx* c, int dtype, uint32_t N, uint32_t V, uint32_t D, const uint32_t* tokens, float scale) {
+  if (!c || (dtype != CG_F32 && dtype != CG_BF16) || V != ctx_view(c).t.V || D == 0) return CG_E_ARG;
+  if ((N && !tokens) || !aligned4(tokens) || !(fabsf(scale) <= FLT_MAX)) return CG_E_ARG;
+  return N > kMaxMatrixRows || D > kMaxMatrixWidth ? CG_E_LIMIT : CG_OK;
+}
+
+}  // namespace
+}  // namespace cgk
+
+extern "C" int cg_embed(cg_ctx* c, const void* d_table, int dtype, uint32_t V, uint32_t D, uint64_t ld_table,
+                        const uint32_t* d_tokens, uint32_t N, float scale, void* d_out, uint64_t ld_out) {
+  using namespace cgk;
+  const int rc = embed_args(c, dtype, N, V, D, d_tokens, scale);
+  if (rc != CG_OK) return rc;
+  if (!matrix_ok(d_table, dtype, V, D, ld_table) || !matrix_ok(d_out, dtype, N, D, ld_out)) return CG_E_ARG;
+  const uint64_t size = dtype_size(dtype);
+  if (matrices_meet(d_out, N, ld_out, d_table, V, ld_table, D, size)) return CG_E_ARG;
+  if (N == 0) return CG_OK;
+  DeviceGuard dg(ctx_device(c), "cg_embed");
+  if (!dg.ok) return CG_E_CUDA;
+  const CtxView v = ctx_view(c);
+  const Look f{d_table, ld_table * size, d_tokens, N, V, D, scale, d_out, ld_out * size, v.t.status, v.stream};
+  return by_vector(dtype, vector_bytes(d_table, ld_table * size, d_out, ld_out * size, D * size), f) == cudaSuccess
+             ? CG_OK
+             : CG_E_CUDA;
+}
+
+extern "C" int cg_embed_workspace(const cg_ctx* c, int dtype, uint32_t N, uint32_t D, size_t* bytes) {
+  using namespace cgk;
+  if (!c || !bytes || (dtype != CG_F32 && dtype != CG_BF16) || D == 0) return CG_E_ARG;
+  if (N > kMaxMatrixRows || D > kMaxMatrixWidth) return CG_E_LIMIT;
+  *bytes = N == 0 ? 0 : plan_grad(N, D, dtype).bytes;
+  return CG_OK;
+}
+
+extern "C" int cg_embed_grad(cg_ctx* c, const void* d_grad, int dtype, uint32_t N, uint32_t V, uint32_t D, uint64_t ld_grad,
+                             const uint32_t* d_tokens, float scale, int accumulate, void* d_out_grad, uint64_t ld_out,
+                             void* d_workspace, size_t workspace_bytes) {
+  using namespace cgk;
+  const int rc = embed_args(c, dtype, N, V, D, d_tokens, scale);
+  if (rc != CG_OK) return rc;
+  if (!matrix_ok(d_grad, dtype, N, D, ld_grad) || !matrix_ok(d_out_grad, dtype, V, D, ld_out)) return CG_E_ARG;
+  const uint64_t size = dtype_size(dtype);
+  if (matrices_meet(d_out_grad, V, ld_out, d_grad, N, ld_grad, D, size)) return CG_E_ARG;
+  const GradPlan p = plan_grad(std::max(N, 1u), D, dtype);
+  if (N && (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256 || workspace_bytes < p.bytes)) return CG_E_ARG;
+  DeviceGuard dg(ctx_device(c), "cg_embed_grad");
+  if (!dg.ok) return CG_E_CUDA;
+  const CtxView v = ctx_view(c);
+  if (N == 0)  // no rows: zeros, or what is there
+    return accumulate || cudaMemset2DAsync(d_out_grad, ld_out * size, 0, D * size, V, v.stream) == cudaSuccess ? CG_OK
+                                                                                                                : CG_E_CUDA;
+  unsigned char* ws = static_cast<unsigned char*>(d_workspace);
+  SortArgs sort = {};
+  sort.tokens = d_tokens;
+  sort.N = N;
+  sort.V = V;
+  sort.passes = (32 - uint32_t(__builtin_clz(V)) + kSortBits - 1) / kSortBits;
+  for (int i = 0; i < 2; ++i) {
+    sort.key[i] = reinterpret_cast<uint32_t*>(ws + p.at_key[i]);
+    sort.pos[i] = reinterpret_cast<uint32_t*>(ws + p.at_pos[i]);
+  }
+  sort.status = v.t.status;
+  SumArgs sum = {};
+  sum.key = sort.key[0];
+  sum.pos = sort.pos[0];
+  sum.N = N;
+  sum.V = V;
+  sum.chunk = p.chunk;
+  sum.grad = static_cast<const char*>(d_grad);
+  sum.pitch = ld_grad * size;
+  sum.scale = scale;
+  sum.add = accumulate != 0;
+  sum.out = static_cast<char*>(d_out_grad);
+  sum.pitch_out = ld_out * size;
+  sum.part = reinterpret_cast<float*>(ws + p.at_part);
+  sum.ld_part = p.ld_part;
+  const Grad f{ctx_device(c), sort, sum, p.chunks, D, v.stream};
+  return by_vector(dtype, vector_bytes(d_grad, ld_grad * size, d_out_grad, ld_out * size, D * size), f) == cudaSuccess
+             ? CG_OK
+             : CG_E_CUDA;
+}

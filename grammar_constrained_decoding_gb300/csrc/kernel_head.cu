@@ -1,0 +1,865 @@
+// The output layer's cross entropy over the allowed tokens, and its gradients, with no
+// logits kept (cg_head_loss, cg_head_grad).
+//
+//   x_bv = h_b . w_v,  m = max x,  S = sum exp((x - m) / T)  over the allowed tokens,
+//   loss = log S - (x_t - m) / T = log1p(sum_{v != t} exp((x_v - x_t) / T)),
+//   d_bv = g / T * exp((x_bv - m) / T) / S,  d_bt = g / T * expm1(-loss),
+//   dH = d W,  dW = d^T H.
+//
+// All four are matrix products, and one persistent kernel runs them: tiles of 128 (or, a
+// pair of blocks, 256) x 256 on the tensor cores, operands by tensor copies through a ring
+// of stages, two accumulators in tensor memory so that a tile is read out while the next
+// is multiplied.  What is done to a tile as it is read out makes the difference:
+//   kLoss  each row's maximum and sum of exponentials over 128 columns (target apart);
+//   kTerms d, rounded to bf16, for a piece of the vocabulary: it bounds the memory;
+//   kOut   a gradient's elements.
+// d is rounded to bf16 because the tensor cores multiply bf16: its relative error of at most 2^-8
+// is the size of the gradients' own rounding.  Float inputs, and d then, are split into
+// three bf16 parts of 8 bits each, and the six products of parts that are not below 2^-24
+// are summed, the smallest first.
+#include <algorithm>
+
+#include "logit_row.cuh"
+#include "matrix_args.h"
+#include "tensor_core.cuh"
+
+namespace cgk {
+namespace {
+
+using namespace row;
+
+constexpr uint32_t kTileN = 256;          // columns of a tile
+constexpr uint32_t kBlockM = 128;         // a block's rows of it
+constexpr uint32_t kBlockK = 64;          // k of a stage: 128 bytes of bf16
+constexpr uint32_t kReaders = 8;          // warps that read tiles out: four row quarters x two column halves
+constexpr uint32_t kFirstReader = 4;      // after the copying, the multiplying and the allocating warp, and a spare
+constexpr uint32_t kHeadThreads = (kFirstReader + kReaders) * 32;
+constexpr uint32_t kBand = 16;            // row tiles that are taken together over all columns
+constexpr uint32_t kHeadSms = 152;
+
+// one of a product's operands in shared memory: a block's share of a stage
+template <int CTAS>
+struct Stage {
+  static constexpr uint32_t kA = kBlockM * kBlockK * 2;
+  static constexpr uint32_t kB = kTileN / CTAS * kBlockK * 2;
+  static constexpr uint32_t kBytes = kA + kB;
+  static constexpr uint32_t kCount = CTAS == 2 ? 6 : 4;
+};
+
+enum Readout { kLoss, kTerms, kOut };
+
+// What is read out of the tiles
+struct LossOut {
+  float2* part;              // [2 * tiles over all pieces][B]: maximum and sum of 128 columns without the target
+  float* target_logit;       // [B], written by the tile that holds the row's target
+};
+struct TermsOut {
+  __nv_bfloat16* terms;      // [parts][B][ld]
+  uint64_t ld, part_stride;
+  const float* loss;
+  const float* norm;
+  const float* up;
+};
+struct GradOut {
+  float* sums;               // [splits][m][ld_sums] or null
+  uint64_t ld_sums;
+  bool add, keep, wide;      // sums are added to what is there; kept there; out's rows lie on the 16-byte grid
+  void* out;                 // [m][ld] or null
+  uint64_t ld;
+  bool bf16;
+};
+
+struct Product {
+  CUtensorMap a, b;
+  uint32_t m, n, n_m, n_n;   // extent, and in tiles
+  uint32_t blocks, splits;   // stages of one product; splits of them
+  uint32_t products;         // 1, or 6 products of the parts
+  int a_mn, a_k, b_mn, b_k;  // where the product begins in the maps
+  // the rows' vocabulary side (kLoss, kTerms)
+  const uint32_t* bitmask;
+  uint32_t W, v0;            // words a row; the piece's first token
+  const uint32_t* target;
+  float temp;
+  LossOut loss;
+  TermsOut terms;
+  GradOut grad;
+  uint32_t* status;
+};
+
+struct Ends {
+  uint64_t full[6], empty[6], tile_full[2], tile_empty[2], drain;
+  uint32_t tmem;
+};
+
+struct Work {
+  uint32_t m0, n0, split, k0, k1;
+};
+// Bands of row tiles over all columns: what runs at one time shares both operands in L2
+template <int CTAS>
+__device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {
+  Work w;
+  const uint32_t tiles = p.n_m * p.n_n;
+  w.split = t / tiles;
+  t -= w.split * tiles;
+  const uint32_t band = t / (kBand * p.n_n), in = t - band * kBand * p.n_n;
+  const uint32_t rows = min(kBand, p.n_m - band * kBand);
+  w.m0 = (band * kBand + in % rows) * kBlockM * CTAS;
+  w.n0 = in / rows * kTileN;
+  w.k0 = uint32_t(uint64_t(p.blocks) * w.split / p.splits);
+  w.k1 = uint32_t(uint64_t(p.blocks) * (w.split + 1) / p.splits);
+  return w;
+}
+// the parts of the i-th of the six products, the smallest products first
+__device__ __forceinline__ uint32_t part_a(uint32_t products, uint32_t i) { return products == 1 ? 0u : (0x001012u >> (4 * i)) & 15u; }
+__device__ __forceinline__ uint32_t part_b(uint32_t products, uint32_t i) { return products == 1 ? 0u : (0x010210u >> (4 * i)) & 15u; }
+
+// ---- reading a tile out ----------------------------------------------------------------------
+
+__device__ __forceinline__ void store32(void* at, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the rows' conventions: NaN is not allowed, +inf is the largest finite value
+__device__ __forceinline__ float logit(float x, bool allowed) {
+  return allowed ? fminf(fmaxf(x, -INFINITY), FLT_MAX) : -INFINITY;
+}
+
+// The allowed tokens of 128 columns from `col` on of row r of the piece, a word each 32
+__device__ __forceinline__ void mask_words(const Product& p, uint32_t r, uint32_t col, uint32_t (&words)[4]) {
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j) {
+    const uint32_t c = col + 32 * j;
+    uint32_t w = c + 32 <= p.n ? 0xFFFFFFFFu : c < p.n ? (1u << (p.n - c)) - 1u : 0u;
+    if (r >= p.m) w = 0;
+    if (w && p.bitmask) w &= p.bitmask[size_t(r) * p.W + ((p.v0 + c) >> 5)];
+    words[j] = w;
+  }
+}
+
+struct RowSum {
+  float m = -INFINITY, s = 0.f;
+  __device__ __forceinline__ void add(const float (&v)[32], float c) {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+    if (!(top > -INFINITY)) return;
+    if (top > m) {
+      s *= ex2((m - top) * c);
+      m = top;
+    }
+    const float2 nm = make_float2(-m, -m), c2 = make_float2(c, c);
+    float2 sum[2] = {};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], ex2_pair(__fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), nm), c2)));
+    const float2 both = __fadd2_rn(sum[0], sum[1]);
+    s += both.x + both.y;
+  }
+};
+
+__device__ __forceinline__ void read_loss(const Product& p, uint32_t tmem, uint32_t r, uint32_t col, uint32_t target,
+                                          const uint32_t (&words)[4]) {
+  const float c = exp_scale(p.temp);
+  RowSum sum;
+#pragma unroll 1
+  for (uint32_t j = 0; j < 4; ++j) {
+    float v[32];
+    tc::tmem_load32(tmem + 32 * j, v);
+    const uint32_t word = j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = logit(v[i], (word >> i) & 1u);
+    const uint32_t at = target - (p.v0 + col + 32 * j);
+    if (at < 32 && r < p.m) {
+      float x = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (uint32_t(i) == at) {
+          x = v[i];
+          v[i] = -INFINITY;
+        }
+      p.loss.target_logit[r] = x;
+    }
+    sum.add(v, c);
+  }
+  if (r < p.m && col < p.n) p.loss.part[size_t((p.v0 + col) >> 7) * p.m + r] = make_float2(sum.m, sum.s);
+}
+
+struct RowTerms {
+  float m, k, at_target;     // d = k * exp((x - m) / T), at the target as it stands
+  bool counts;
+};
+__device__ __forceinline__ RowTerms row_terms(const Product& p, uint32_t r, uint32_t target) {
+  RowTerms t{0.f, 0.f, 0.f, false};
+  if (r >= p.m) return t;
+  const float loss = p.terms.loss[r], m = p.terms.norm[2 * size_t(r)], s = p.terms.norm[2 * size_t(r) + 1];
+  const float scale = __fdiv_rn(p.terms.up ? p.terms.up[r] : 1.f, p.temp);
+  t.counts = loss > 0.f && target < 0xFFFFFFFFu;   // a loss of 0: no target that counts, or nothing beside it
+  if (t.counts) {
+    t.m = m;
+    t.k = __fdiv_rn(scale, s);
+    t.at_target = scale * expm1f(-loss);
+  }
+  return t;
+}
+__device__ __forceinline__ void read_terms(const Product& p, uint32_t tmem, uint32_t r, uint32_t col, uint32_t target,
+                                           const uint32_t (&words)[4], const RowTerms& t) {
+  const float c = exp_scale(p.temp);
+  const uint32_t parts = p.products == 1 ? 1 : 3;
+#pragma unroll 1
+  for (uint32_t j = 0; j < 4; ++j) {
+    float v[32];
+    tc::tmem_load32(tmem + 32 * j, v);
+    const uint32_t c0 = col + 32 * j;
+    if (r >= p.m || c0 >= p.terms.ld) continue;
+    const uint32_t word = j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3];
+    const float2 nm = make_float2(-t.m, -t.m), c2 = make_float2(c, c), k2 = make_float2(t.k, t.k);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 x = make_float2(logit(v[i], (word >> i) & 1u), logit(v[i + 1], (word >> (i + 1)) & 1u));
+      const float2 d = __fmul2_rn(ex2_pair(__fmul2_rn(__fadd2_rn(x, nm), c2)), k2);
+      v[i] = t.counts ? d.x : 0.f;
+      v[i + 1] = t.counts ? d.y : 0.f;
+    }
+    const uint32_t at = target - (p.v0 + c0);
+    if (at < 32 && t.counts) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (uint32_t(i) == at) v[i] = t.at_target;
+    }
+    __nv_bfloat16* to = p.terms.terms + size_t(r) * p.terms.ld + c0;
+    for (uint32_t part = 0; part < parts; ++part) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        w[i] = pack2(v[2 * i], v[2 * i + 1]);
+        if (parts > 1) {
+          v[2 * i] -= __uint_as_float(w[i] << 16);
+          v[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
+      const uint32_t lo[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+      const uint32_t hi[8] = {w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]};
+      store32(to + part * p.terms.part_stride, lo);
+      store32(to + part * p.terms.part_stride + 16, hi);
+    }
+  }
+}
+
+// A gradient's tile.  Rows on the 16-byte grid are written by the thread that holds them;
+// the others through shared memory, so that a warp writes along a row.
+__device__ __forceinline__ void read_grad(const Product& p, uint32_t tmem, const Work& w, uint32_t row0, uint32_t col,
+                                          float* turn) {
+  const uint32_t lane = threadIdx.x & 31, r = row0 + lane, split = w.split;
+  const GradOut& g = p.grad;
+#pragma unroll 1
+  for (uint32_t j = 0; j < 4; ++j) {
+    const uint32_t c0 = col + 32 * j;
+    if (c0 >= p.n) break;
+    float v[32];
+    tc::tmem_load32(tmem + 32 * j, v);
+    if (w.k0 == w.k1) {   // a split of no stages (more splits than stages): nothing was multiplied
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    }
+    if (g.sums && r < p.m) {
+      // ld_sums is a multiple of 32: the chunk lies in the buffer
+      float4* at = reinterpret_cast<float4*>(g.sums + (size_t(split) * p.m + r) * g.ld_sums + c0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (g.add) {
+          const float4 s = at[i];
+          v[4 * i] += s.x;
+          v[4 * i + 1] += s.y;
+          v[4 * i + 2] += s.z;
+          v[4 * i + 3] += s.w;
+        }
+        if (g.keep) at[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
+    if (!g.out) continue;
+    if (g.wide && c0 + 32 <= p.n) {
+      if (r >= p.m) continue;
+      if (g.bf16) {
+        uint4* at = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) + size_t(r) * g.ld + c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          at[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
+                             pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
+      } else {
+        float4* at = reinterpret_cast<float4*>(static_cast<float*>(g.out) + size_t(r) * g.ld + c0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) at[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+      continue;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
+    __syncwarp();
+    const uint32_t rows = row0 < p.m ? min(32u, p.m - row0) : 0u;
+    if (c0 + lane < p.n)
+      for (uint32_t i = 0; i < rows; ++i) {
+        const float x = turn[i * 33 + lane];
+        const size_t at = size_t(row0 + i) * g.ld + c0 + lane;
+        if (g.bf16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(x);
+        else static_cast<float*>(g.out)[at] = x;
+      }
+  }
+}
+
+// ---- the product kernel ----------------------------------------------------------------------
+
+template <int CTAS, Readout READ, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_constant__ Product p) {
+  using S = Stage<CTAS>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;   // the swizzle's pattern repeats every 1024 bytes
+  float* const turned = reinterpret_cast<float*>(smem + (ring - smem_addr(smem)) + S::kCount * S::kBytes);
+  Ends& ends = *reinterpret_cast<Ends*>(turned + kReaders * 32 * 33);
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 ? tc::cta_rank() : 0u;
+  const uint32_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS, items = p.n_m * p.n_n * p.splits;
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < S::kCount; ++s) {
+      mbar_init(&ends.full[s], 1);
+      mbar_init(&ends.empty[s], 1);
+    }
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(&ends.tile_full[i], 1);
+      mbar_init(&ends.tile_empty[i], CTAS * kReaders);
+    }
+    mbar_init(&ends.drain, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == 2) tc::tmem_alloc<CTAS>(&ends.tmem);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (CTAS == 2) tc::cluster_barrier();
+  tc::fence_after_sync();
+  const uint32_t tmem = ends.tmem;
+  griddep_wait();
+
+  if (warp == 0) {
+    // the copies: a block brings its 128 rows of A and its share of B's 256.  With a pair
+    // the leader's barrier counts the bytes of both.
+    if (lane == 0) {
+      // what the kernel before wrote, as the copies see it
+      asm volatile("fence.proxy.async;" ::: "memory");
+      tc::prefetch_map(&p.a);
+      tc::prefetch_map(&p.b);
+      uint32_t s = 0, phase = 0, issued = 0;
+      bool ok = true;
+      for (uint32_t t = first; ok && t < items; t += step) {
+        const Work w = work_of<CTAS>(p, t);
+        const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * (kTileN / CTAS));
+        for (uint32_t i = 0; ok && i < p.products; ++i) {
+          const int pa = int(part_a(p.products, i)), pb = int(part_b(p.products, i));
+          for (uint32_t k = w.k0; k < w.k1; ++k) {
+            if (!(ok = mbar_wait(&ends.empty[s], phase ^ 1))) break;
+            const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[s]), 0) : smem_addr(&ends.full[s]);
+            if (rank == 0) mbar_expect_tx(&ends.full[s], S::kBytes * CTAS);
+            const uint32_t a = ring + s * S::kBytes, b = a + S::kA;
+            const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
+            if (A_MN)
+              for (uint32_t q = 0; q < kBlockM / 64; ++q) tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, pa, full);
+            else tc::copy_box<CTAS>(a, &p.a, ak, am, pa, full);
+            if (B_MN)
+              for (uint32_t q = 0; q < kTileN / CTAS / 64; ++q)
+                tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, pb, full);
+            else
+              for (uint32_t q = 0; q < kTileN / CTAS / 128; ++q)
+                tc::copy_box<CTAS>(b + q * 16384, &p.b, bk, bn + int(128 * q), pb, full);
+            ++issued;
+            if (++s == S::kCount) s = 0, phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        record_error(p.status, CG_DEV_TIMEOUT);
+        // what is still in flight lands before the block leaves
+        for (uint32_t i = 0; rank == 0 && i < min(issued, S::kCount); ++i) {
+          if (s-- == 0) s = S::kCount - 1, phase ^= 1;
+          if (!mbar_wait(&ends.full[s], phase)) break;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, kTileN);
+      uint32_t s = 0, phase = 0, n = 0;
+      bool ok = true;
+      for (uint32_t t = first; ok && t < items; t += step, ++n) {
+        const Work w = work_of<CTAS>(p, t);
+        const uint32_t acc = n & 1u;
+        if (!(ok = mbar_wait(&ends.tile_empty[acc], ((n >> 1) & 1u) ^ 1u))) break;
+        tc::fence_after_sync();
+        const uint32_t blocks = p.products * (w.k1 - w.k0);
+        for (uint32_t k = 0; k < blocks; ++k) {
+          if (!(ok = mbar_wait(&ends.full[s], phase))) break;
+          tc::fence_after_sync();
+          const uint64_t a = tc::operand<A_MN>(ring + s * S::kBytes), b = tc::operand<B_MN>(ring + s * S::kBytes + S::kA);
+#pragma unroll
+          for (uint32_t q = 0; q < kBlockK / 16; ++q)
+            tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, (k | q) != 0);
+          tc::commit<CTAS>(&ends.empty[s]);
+          if (++s == S::kCount) s = 0, phase ^= 1;
+        }
+        if (ok) tc::commit<CTAS>(&ends.tile_full[acc]);
+      }
+      if (!ok) {
+        record_error(p.status, CG_DEV_TIMEOUT);
+        tc::commit<CTAS>(&ends.drain);   // the instructions in flight end before tensor memory is given back
+        mbar_wait(&ends.drain, 0);
+      }
+    }
+  } else if (warp >= kFirstReader) {
+    const uint32_t quarter = warp & 3u, half = (warp - kFirstReader) >> 2;
+    float* turn = turned + (warp - kFirstReader) * 32 * 33;
+    uint32_t n = 0;
+    for (uint32_t t = first; t < items; t += step, ++n) {
+      const Work w = work_of<CTAS>(p, t);
+      const uint32_t acc = n & 1u, row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane;
+      const uint32_t col = w.n0 + half * 128;
+      uint32_t words[4], target = 0xFFFFFFFFu;
+      RowTerms terms;
+      if (READ != kOut) {
+        mask_words(p, r, col, words);
+        if (r < p.m) target = p.target[r];
+        if (READ == kTerms) terms = row_terms(p, r, target);
+      }
+      if (!mbar_wait(&ends.tile_full[acc], (n >> 1) & 1u)) {
+        record_error(p.status, CG_DEV_TIMEOUT);
+        break;
+      }
+      tc::fence_after_sync();
+      const uint32_t at = tmem + acc * kTileN + half * 128 + ((quarter * 32) << 16);
+      if (READ == kLoss) read_loss(p, at, r, col, target, words);
+      else if (READ == kTerms) read_terms(p, at, r, col, target, words, terms);
+      else read_grad(p, at, w, row0, col, turn);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (CTAS == 2) tc::arrive_at(tc::in_block(smem_addr(&ends.tile_empty[acc]), 0));
+        else mbar_arrive(&ends.tile_empty[acc]);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (CTAS == 2) tc::cluster_barrier();   // the other block's instructions read this one's shared memory
+  tc::fence_after_sync();
+  if (warp == 2) tc::tmem_free<CTAS>(tmem);
+}
+
+template <int CTAS>
+constexpr size_t product_smem() {
+  return 1024 + size_t(Stage<CTAS>::kCount) * Stage<CTAS>::kBytes + size_t(kReaders) * 32 * 33 * 4 + sizeof(Ends);
+}
+static_assert(product_smem<1>() <= size_t(kMaxSmem) && product_smem<2>() <= size_t(kMaxSmem),
+              "the ring, the turned blocks and the barriers fit a block's shared memory");
+
+// ---- joining the parts of a row --------------------------------------------------------------
+
+// 32 rows a block; its 32 warps take the column groups in turn
+__global__ void __launch_bounds__(1024) join_loss_kernel(const float2* part, const float* target_logit,
+                                                         const uint32_t* target, uint32_t groups, uint32_t B, uint32_t V,
+                                                         float T, float* loss, float* lse, float* norm,
+                                                         uint32_t* status) {
+  __shared__ float2 mine[32][33];
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x * 32 + lane;
+  const float c = exp_scale(T);
+  float m = -INFINITY, s = 0.f;
+  if (b < B)
+    for (uint32_t g = warp; g < groups; g += 32) {
+      const float2 x = part[size_t(g) * B + b];
+      if (!(x.x > -INFINITY)) continue;
+      const float top = fmaxf(m, x.x);
+      s = s * ex2((m - top) * c) + x.y * ex2((x.x - top) * c);
+      m = top;
+    }
+  mine[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp != 0 || b >= B) return;
+  for (uint32_t w = 1; w < 32; ++w) {
+    const float2 x = mine[w][lane];
+    if (!(x.x > -INFINITY)) continue;
+    const float top = fmaxf(m, x.x);
+    s = s * ex2((m - top) * c) + x.y * ex2((x.x - top) * c);
+    m = top;
+  }
+  // m, s: the others' maximum and sum; x: the target's logit
+  const uint32_t t = target[b];
+  if (t >= V && t != CG_NO_TOKEN) record_error(status, CG_DEV_BAD_TOKEN);
+  const float x = t < V ? target_logit[b] : -INFINITY;
+  float l = 0.f, M = m, rest = s;   // S = 1 + rest where the target is the maximum
+  bool first = false;
+  if (x > -INFINITY) {
+    if (!(m > -INFINITY)) {
+      M = x;
+      rest = 0.f;
+      first = true;
+    } else if (x >= m) {
+      M = x;
+      rest = s * ex2((m - x) * c);
+      first = true;
+      l = log1pf(rest);
+    } else {
+      rest = s + ex2((x - m) * c);
+      l = __fdiv_rn(m - x, T) + logf(rest);
+    }
+  }
+  loss[b] = l;
+  if (norm) {
+    norm[2 * size_t(b)] = M;
+    norm[2 * size_t(b) + 1] = first ? 1.f + rest : rest;
+  }
+  if (lse) lse[b] = M > -INFINITY ? __fdiv_rn(M, T) + (first ? log1pf(rest) : logf(rest)) : -INFINITY;
+}
+
+// The splits' sums of a gradient, in their order
+__global__ void __launch_bounds__(256) join_grad_kernel(const float* sums, uint64_t ld_sums, uint32_t splits, uint32_t m,
+                                                        uint32_t n, void* out, uint64_t ld, bool bf16) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t r = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = 0.f;
+  for (uint32_t k = 0; k < splits; ++k) s += sums[(size_t(k) * m + r) * ld_sums + i];
+  if (bf16) static_cast<__nv_bfloat16*>(out)[size_t(r) * ld + i] = __float2bfloat16_rn(s);
+  else static_cast<float*>(out)[size_t(r) * ld + i] = s;
+}
+
+// ---- operands that the copies cannot take as they lie ----------------------------------------
+
+// bf16 rows off the 16-byte grid are copied onto it; float rows are split into three parts
+// that add up to the value (8 bits each; a value that is not finite is its first part)
+template <bool F32>
+__global__ void __launch_bounds__(256) lay_out_kernel(const void* from, uint64_t ld, uint32_t rows, uint32_t D, uint32_t Dp,
+                                                      __nv_bfloat16* to) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint64_t n = uint64_t(rows) * Dp, step = uint64_t(gridDim.x) * 256;
+  for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
+    const uint64_t r = i / Dp;
+    const uint32_t d = uint32_t(i - r * Dp);
+    if (!F32) {
+      to[i] = d < D ? static_cast<const __nv_bfloat16*>(from)[r * ld + d] : __float2bfloat16_rn(0.f);
+      continue;
+    }
+    float x = d < D ? static_cast<const float*>(from)[r * ld + d] : 0.f;
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(x);
+      to[uint64_t(part) * n + i] = h;
+      x = fabsf(x) <= FLT_MAX && fabsf(__bfloat162float(h)) <= FLT_MAX ? x - __bfloat162float(h) : 0.f;
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------------------------
+
+constexpr size_t kPieceBytes = size_t(256) << 20;  // of a piece's weight laid out, and of its terms
+
+// What a call works on, and where its workspace's parts lie
+struct HeadPlan {
+  uint32_t B, V, D, Dp, parts, products;
+  bool lay_h, lay_w;
+  uint32_t piece;            // tokens of a piece: a multiple of 256 unless it is all of them
+  uint64_t ld_terms, ld_sums;
+  uint32_t splits;           // of the product that sums over tokens
+  bool pair;                 // rows in pairs of blocks
+  size_t at_h, at_w, at_part, at_target, at_terms, at_sums, bytes;
+};
+
+HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64_t ld_w, int dtype, uint32_t B, uint32_t V,
+                   uint32_t D, bool grad) {
+  HeadPlan p = {};
+  p.B = B;
+  p.V = V;
+  p.D = D;
+  p.Dp = uint32_t(up_to(D, 8));
+  const bool f32 = dtype == CG_F32;
+  p.parts = f32 ? 3 : 1;
+  p.products = f32 ? 6 : 1;
+  p.lay_h = f32 || !rows_on_grid(hidden, dtype, ld_h);
+  p.lay_w = f32 || !rows_on_grid(weight, dtype, ld_w);
+  p.pair = B > kBlockM;
+  uint64_t most = V;
+  if (p.lay_w) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * p.Dp * 2));
+  if (grad) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * std::max(B, 1u) * 2));
+  most = std::max<uint64_t>(most / 256 * 256, 256);
+  const uint64_t pieces = (V + most - 1) / most;
+  p.piece = uint32_t(std::min<uint64_t>(up_to((V + pieces - 1) / pieces, 256), V));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up_to(bytes, 256);
+    return here;
+  };
+  if (p.lay_h) p.at_h = take(size_t(p.parts) * B * p.Dp * 2);
+  if (p.lay_w) p.at_w = take(size_t(p.parts) * p.piece * p.Dp * 2);
+  if (!grad) {
+    p.at_part = take(size_t(tiles_of(V, 128)) * B * 8);
+    p.at_target = take(size_t(B) * 4);
+  } else {
+    p.ld_terms = up_to(p.piece, 32);
+    p.at_terms = take(size_t(p.parts) * B * p.ld_terms * 2);
+    p.ld_sums = up_to(D, 32);
+    const uint32_t tiles = tiles_of(B, kBlockM * (p.pair ? 2 : 1)) * tiles_of(D, kTileN);
+    const uint32_t slots = kHeadSms / (p.pair ? 2 : 1), blocks = tiles_of(p.piece, kBlockK);
+    p.splits = std::max(1u, std::min(slots / std::max(tiles, 1u), blocks / 8));
+    if (p.splits > 1 || p.piece < V) p.at_sums = take(size_t(p.splits) * B * p.ld_sums * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+template <Readout READ, bool A_MN, bool B_MN>
+cudaError_t launch_product(int device, bool pair, Product& p, cudaStream_t stream) {
+  const uint32_t ctas = pair ? 2 : 1;
+  p.n_m = tiles_of(p.m, kBlockM * ctas);
+  p.n_n = tiles_of(p.n, kTileN);
+  const uint32_t at_once = std::min(p.n_m * p.n_n * p.splits, kHeadSms / ctas);
+  return pair ? launch_clusters<product_kernel<2, READ, A_MN, B_MN>>(device, at_once, 2, kHeadThreads, product_smem<2>(),
+                                                                      stream, p)
+              : launch_clusters<product_kernel<1, READ, A_MN, B_MN>>(device, at_once, 1, kHeadThreads, product_smem<1>(),
+                                                                      stream, p);
+}
+
+cudaError_t lay_out(bool f32, const void* from, uint64_t ld, uint32_t rows, uint32_t D, uint32_t Dp, void* to,
+                    cudaStream_t stream) {
+  const uint64_t n = uint64_t(rows) * Dp;
+  const dim3 grid(uint32_t(std::min<uint64_t>((n + 255) / 256, kHeadSms * 16)));
+  return launch_dependent(f32 ? lay_out_kernel<true> : lay_out_kernel<false>, grid, dim3(256), 0, stream, from, ld, rows, D,
+                          Dp, static_cast<__nv_bfloat16*>(to));
+}
+
+struct HeadArgs {
+  const void* hidden;
+  const void* weight;
+  int dtype;
+  uint32_t B, V, D;
+  uint64_t ld_h, ld_w;
+  const uint32_t* bitmask;
+  const uint32_t* target;
+  float temp;
+};
+
+// the operands as the tensor copies read them: the caller's, or laid out in the workspace
+struct Operands {
+  const void* h;
+  const void* w;
+  uint64_t ld_h, ld_w;
+};
+bool map_h(CUtensorMap* map, const HeadPlan& p, const Operands& o, uint32_t box) {
+  return tc::make_map(map, o.h, p.D, p.B, p.parts, o.ld_h, p.lay_h ? uint64_t(p.B) * p.Dp : o.ld_h, box);
+}
+bool map_w(CUtensorMap* map, const HeadPlan& p, const Operands& o, uint32_t rows, uint32_t box) {
+  return tc::make_map(map, o.w, p.D, rows, p.parts, o.ld_w, p.lay_w ? uint64_t(rows) * p.Dp : o.ld_w, box);
+}
+
+// x = H W^T of a piece, read out one way or the other
+Product logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v0, uint32_t n) {
+  Product q = {};
+  q.m = p.B;
+  q.n = n;
+  q.blocks = tiles_of(p.D, kBlockK);
+  q.splits = 1;
+  q.products = p.products;
+  q.b_mn = p.lay_w ? 0 : int(v0);
+  q.bitmask = a.bitmask;
+  q.W = v.t.W;
+  q.v0 = v0;
+  q.target = a.target;
+  q.temp = a.temp;
+  q.status = v.t.status;
+  return q;
+}
+
+int head_loss(cg_ctx* c, const HeadArgs& a, float* loss, float* lse, float* norm, unsigned char* ws) {
+  DeviceGuard dg(ctx_device(c), "cg_head_loss");
+  if (!dg.ok) return CG_E_CUDA;
+  const CtxView v = ctx_view(c);
+  const int dev = ctx_device(c);
+  const HeadPlan p = plan_head(a.hidden, a.ld_h, a.weight, a.ld_w, a.dtype, a.B, a.V, a.D, false);
+  const bool f32 = a.dtype == CG_F32;
+  Operands o{a.hidden, a.weight, a.ld_h, a.ld_w};
+  if (p.lay_h) {
+    if (lay_out(f32, a.hidden, a.ld_h, p.B, p.D, p.Dp, ws + p.at_h, v.stream) != cudaSuccess) return CG_E_CUDA;
+    o.h = ws + p.at_h;
+    o.ld_h = p.Dp;
+  }
+  for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
+    const uint32_t n = std::min(p.piece, p.V - v0);
+    if (p.lay_w) {
+      const char* from = static_cast<const char*>(a.weight) + uint64_t(v0) * a.ld_w * (f32 ? 4 : 2);
+      if (lay_out(f32, from, a.ld_w, n, p.D, p.Dp, ws + p.at_w, v.stream) != cudaSuccess) return CG_E_CUDA;
+      o.w = ws + p.at_w;
+      o.ld_w = p.Dp;
+    }
+    Product q = logits_of(a, p, v, v0, n);
+    q.loss.part = reinterpret_cast<float2*>(ws + p.at_part);
+    q.loss.target_logit = reinterpret_cast<float*>(ws + p.at_target);
+    if (!map_h(&q.a, p, o, 128) || !map_w(&q.b, p, o, p.lay_w ? n : p.V, 128)) return CG_E_CUDA;
+    if (launch_product<kLoss, false, false>(dev, p.pair, q, v.stream) != cudaSuccess) return CG_E_CUDA;
+  }
+  return launch_dependent(join_loss_kernel, dim3(tiles_of(p.B, 32)), dim3(1024), 0, v.stream,
+                          reinterpret_cast<const float2*>(ws + p.at_part),
+                          reinterpret_cast<const float*>(ws + p.at_target), a.target, tiles_of(p.V, 128), p.B, p.V, a.temp,
+                          loss, lse, norm, v.t.status) == cudaSuccess
+             ? CG_OK
+             : CG_E_CUDA;
+}
+
+int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm, const float* up, void* dh, uint64_t ld_dh,
+              void* dw, uint64_t ld_dw, unsigned char* ws) {
+  DeviceGuard dg(ctx_device(c), "cg_head_grad");
+  if (!dg.ok) return CG_E_CUDA;
+  const CtxView v = ctx_view(c);
+  const int dev = ctx_device(c);
+  const bool f32 = a.dtype == CG_F32;
+  const size_t size = f32 ? 4 : 2;
+  if (a.B == 0)  // no rows: the weight's gradient is zero
+    return !dw || cudaMemset2DAsync(dw, ld_dw * size, 0, size_t(a.D) * size, a.V, v.stream) == cudaSuccess ? CG_OK
+                                                                                                            : CG_E_CUDA;
+  const HeadPlan p = plan_head(a.hidden, a.ld_h, a.weight, a.ld_w, a.dtype, a.B, a.V, a.D, true);
+  Operands o{a.hidden, a.weight, a.ld_h, a.ld_w};
+  if (p.lay_h) {
+    if (lay_out(f32, a.hidden, a.ld_h, p.B, p.D, p.Dp, ws + p.at_h, v.stream) != cudaSuccess) return CG_E_CUDA;
+    o.h = ws + p.at_h;
+    o.ld_h = p.Dp;
+  }
+  __nv_bfloat16* terms = reinterpret_cast<__nv_bfloat16*>(ws + p.at_terms);
+  const uint64_t part_stride = uint64_t(p.B) * p.ld_terms;
+  for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
+    const uint32_t n = std::min(p.piece, p.V - v0);
+    if (p.lay_w) {
+      const char* from = static_cast<const char*>(a.weight) + uint64_t(v0) * a.ld_w * size;
+      if (lay_out(f32, from, a.ld_w, n, p.D, p.Dp, ws + p.at_w, v.stream) != cudaSuccess) return CG_E_CUDA;
+      o.w = ws + p.at_w;
+      o.ld_w = p.Dp;
+    }
+    const uint32_t w_rows = p.lay_w ? n : p.V;
+    Product q = logits_of(a, p, v, v0, n);
+    q.terms = TermsOut{terms, p.ld_terms, part_stride, loss, norm, up};
+    if (!map_h(&q.a, p, o, 128) || !map_w(&q.b, p, o, w_rows, 128)) return CG_E_CUDA;
+    if (launch_product<kTerms, false, false>(dev, p.pair, q, v.stream) != cudaSuccess) return CG_E_CUDA;
+    if (dh) {  // terms [B][n] x W [n][D], summed over the pieces
+      Product g = {};
+      g.m = p.B;
+      g.n = p.D;
+      g.blocks = tiles_of(n, kBlockK);
+      g.splits = p.splits;
+      g.products = p.products;
+      g.b_k = p.lay_w ? 0 : int(v0);
+      g.status = v.t.status;
+      const bool last = v0 + n == p.V, alone = p.splits == 1 && p.piece == p.V;
+      g.grad.sums = alone ? nullptr : reinterpret_cast<float*>(ws + p.at_sums);
+      g.grad.ld_sums = p.ld_sums;
+      g.grad.add = v0 != 0;
+      g.grad.keep = !last || p.splits > 1;
+      g.grad.out = last && p.splits == 1 ? dh : nullptr;
+      g.grad.ld = ld_dh;
+      g.grad.bf16 = !f32;
+      g.grad.wide = rows_on_grid(dh, a.dtype, ld_dh);
+      if (!tc::make_map(&g.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 128) || !map_w(&g.b, p, o, w_rows, 64))
+        return CG_E_CUDA;
+      if (launch_product<kOut, false, true>(dev, p.pair, g, v.stream) != cudaSuccess) return CG_E_CUDA;
+    }
+    if (dw) {  // terms^T [n][B] x H [B][D]
+      Product g = {};
+      g.m = n;
+      g.n = p.D;
+      g.blocks = tiles_of(p.B, kBlockK);
+      g.splits = 1;
+      g.products = p.products;
+      g.status = v.t.status;
+      g.grad.out = static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size;
+      g.grad.ld = ld_dw;
+      g.grad.bf16 = !f32;
+      g.grad.wide = rows_on_grid(dw, a.dtype, ld_dw);
+      if (!tc::make_map(&g.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&g.b, p, o, 64)) return CG_E_CUDA;
+      if (launch_product<kOut, true, true>(dev, n > kBlockM, g, v.stream) != cudaSuccess) return CG_E_CUDA;
+    }
+  }
+  if (dh && p.splits > 1 &&
+      launch_dependent(join_grad_kernel, dim3(tiles_of(p.D, 256), p.B), dim3(256), 0, v.stream,
+                       reinterpret_cast<const float*>(ws + p.at_sums), p.ld_sums, p.splits, p.B, p.D, dh, ld_dh,
+                       !f32) != cudaSuccess)
+    return CG_E_CUDA;
+  return CG_OK;
+}
+
+int head_args(const cg_ctx* c, const HeadArgs& a) {
+  if (!c || (a.dtype != CG_F32 && a.dtype != CG_BF16) || a.V != ctx_view(c).t.V || a.D == 0) return CG_E_ARG;
+  if (!matrix_ok(a.hidden, a.dtype, a.B, a.D, a.ld_h) || !matrix_ok(a.weight, a.dtype, a.V, a.D, a.ld_w)) return CG_E_ARG;
+  if ((a.B && !a.target) || !aligned4(a.target) || !aligned4(a.bitmask)) return CG_E_ARG;
+  if (!(a.temp > 0.f) || a.temp > FLT_MAX) return CG_E_ARG;
+  return a.B > kMaxMatrixRows || a.D > kMaxMatrixWidth ? CG_E_LIMIT : CG_OK;
+}
+}  // namespace
+}  // namespace cgk
+
+extern "C" int cg_head_workspace(const cg_ctx* c, const void* d_hidden, const void* d_weight, int dtype, uint32_t B,
+                                 uint32_t V, uint32_t D, uint64_t ld_hidden, uint64_t ld_weight, int grad, size_t* bytes) {
+  using namespace cgk;
+  if (!c || !bytes || (dtype != CG_F32 && dtype != CG_BF16) || V != ctx_view(c).t.V || D == 0) return CG_E_ARG;
+  if (!matrix_ok(d_hidden, dtype, B, D, ld_hidden) || !matrix_ok(d_weight, dtype, V, D, ld_weight)) return CG_E_ARG;
+  if (B > kMaxMatrixRows || D > kMaxMatrixWidth) return CG_E_LIMIT;
+  *bytes = B == 0 ? 0 : plan_head(d_hidden, ld_hidden, d_weight, ld_weight, dtype, B, V, D, grad != 0).bytes;
+  return CG_OK;
+}
+
+extern "C" int cg_head_loss(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtype, uint32_t B, uint32_t V,
+                            uint32_t D, uint64_t ld_hidden, uint64_t ld_weight, const uint32_t* d_bitmask,
+                            const uint32_t* d_target, float temp, float* d_out_loss, float* d_out_lse, float* d_out_norm,
+                            void* d_workspace, size_t workspace_bytes) {
+  using namespace cgk;
+  const HeadArgs a{d_hidden, d_weight, dtype, B, V, D, ld_hidden, ld_weight, d_bitmask, d_target, temp};
+  const int rc = head_args(c, a);
+  if (rc != CG_OK) return rc;
+  if (B == 0) return CG_OK;
+  if (!d_out_loss || !aligned4(d_out_loss) || !aligned4(d_out_lse) || !aligned4(d_out_norm)) return CG_E_ARG;
+  if (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256 ||
+      workspace_bytes < plan_head(d_hidden, ld_hidden, d_weight, ld_weight, dtype, B, V, D, false).bytes)
+    return CG_E_ARG;
+  return head_loss(c, a, d_out_loss, d_out_lse, d_out_norm, static_cast<unsigned char*>(d_workspace));
+}
+
+extern "C" int cg_head_grad(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtype, uint32_t B, uint32_t V,
+                            uint32_t D, uint64_t ld_hidden, uint64_t ld_weight, const uint32_t* d_bitmask,
+                            const uint32_t* d_target, float temp, const float* d_loss, const float* d_norm,
+                            const float* d_grad_loss, void* d_out_grad_hidden, uint64_t ld_grad_hidden,
+                            void* d_out_grad_weight, uint64_t ld_grad_weight, void* d_workspace, size_t workspace_bytes) {
+  using namespace cgk;
+  const HeadArgs a{d_hidden, d_weight, dtype, B, V, D, ld_hidden, ld_weight, d_bitmask, d_target, temp};
+  const int rc = head_args(c, a);
+  if (rc != CG_OK) return rc;
+  if (!d_out_grad_hidden && !d_out_grad_weight) return CG_E_ARG;
+  if (B && (!d_loss || !d_norm)) return CG_E_ARG;
+  if (!aligned4(d_loss) || !aligned4(d_norm) || !aligned4(d_grad_loss)) return CG_E_ARG;
+  const uint64_t size = dtype == CG_BF16 ? 2 : 4;
+  const void* out[2] = {d_out_grad_hidden, d_out_grad_weight};
+  const uint64_t rows[2] = {B, V}, ld[2] = {ld_grad_hidden, ld_grad_weight};
+  for (int i = 0; i < 2; ++i) {
+    if (!out[i]) continue;
+    if (!matrix_ok(out[i], dtype, rows[i], D, ld[i]) || matrices_meet(out[i], rows[i], ld[i], d_hidden, B, ld_hidden, D, size) ||
+        matrices_meet(out[i], rows[i], ld[i], d_weight, V, ld_weight, D, size))
+      return CG_E_ARG;
+  }
+  if (out[0] && out[1] && matrices_meet(out[0], rows[0], ld[0], out[1], rows[1], ld[1], D, size)) return CG_E_ARG;
+  if (B && (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256 ||
+            workspace_bytes < plan_head(d_hidden, ld_hidden, d_weight, ld_weight, dtype, B, V, D, true).bytes))
+    return CG_E_ARG;
+  return head_grad(c, a, d_loss, d_norm, d_grad_loss, d_out_grad_hidden, ld_grad_hidden, d_out_grad_weight,
+                   ld_grad_weight, static_cast<unsigned char*>(d_workspace));
+}

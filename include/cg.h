@@ -539,6 +539,94 @@ int cg_distill_grad_norm(cg_ctx* c, const void* d_logits, int dtype, uint32_t B,
                          float temp, const float* d_norm, const float* d_grad_loss, void* d_out_grad,
                          uint64_t ld_grad);
 
+/* ---- the model's two ends: embedding and output layer ------------------------------ */
+
+/* Where a model's rows meet the vocabulary: tokens become rows of a table, and rows
+ * become logits over the allowed tokens, with the gradients that training needs.  The
+ * tokens are those that the step calls write, the masks those that cg_fill_bitmask
+ * writes; one table may be both ends.  The pages give no form for these; the
+ * definitions are here.
+ *
+ * Common to the four calls
+ *  matrices  : CG_F32 or CG_BF16, row-major, row r at element r * ld, D <= ld <= 2^32
+ *              (rows of a wider or padded buffer); any alignment that the element
+ *              type has (16-byte aligned rows are fastest).  All matrices of a call
+ *              have the one dtype.  Outputs share no memory with inputs or with
+ *              each other, but may be other columns of the same buffer
+ *  V         : the vocabulary's; D <= 2^16 columns, at most 2^22 rows (CG_E_LIMIT)
+ *  tokens    : u32; CG_NO_TOKEN for a row without one.  An id >= V other than that
+ *              records CG_DEV_BAD_TOKEN and counts as none
+ *  workspace : device memory, 256-byte aligned, as many bytes as the query call of the
+ *              same arguments says; what is in it before and after is of no meaning,
+ *              and one may serve calls that follow one another on a stream.  The
+ *              queries launch nothing
+ *  Sums are held in 32 bits or more, results are rounded once to the dtype, and none
+ *  depends on the order in which the device runs its blocks.  The calls allocate
+ *  nothing, may be captured, and run on the context's stream.  Errors: CG_E_ARG (a
+ *  NULL required pointer, an unknown dtype, a size, pitch, alignment or workspace out
+ *  of range, matrices that share memory), CG_E_LIMIT, CG_E_CUDA. */
+
+/* out[i] = scale * table[d_tokens[i]] for i < N, rounded to the dtype; zeros for a row
+ * without a token.
+ *  d_table : [V][ld_table]; d_out : [N][ld_out]; scale finite
+ * Device errors: CG_DEV_BAD_TOKEN. */
+int cg_embed(cg_ctx* c, const void* d_table, int dtype, uint32_t V, uint32_t D, uint64_t ld_table,
+             const uint32_t* d_tokens, uint32_t N, float scale, void* d_out, uint64_t ld_out);
+
+/* The gradient by the table: out[v] = scale * sum of grad[i] over the i with token v,
+ * zeros for a token that does not occur; with accumulate != 0, added to what out holds
+ * (tokens that do not occur are then left alone).  The positions are sorted by token
+ * and a token's rows summed in the order of their positions.
+ *  d_grad : [N][ld_grad]; d_out_grad : [V][ld_out]
+ * Device errors: CG_DEV_BAD_TOKEN. */
+int cg_embed_workspace(const cg_ctx* c, int dtype, uint32_t N, uint32_t D, size_t* bytes);
+int cg_embed_grad(cg_ctx* c, const void* d_grad, int dtype, uint32_t N, uint32_t V, uint32_t D, uint64_t ld_grad,
+                  const uint32_t* d_tokens, float scale, int accumulate, void* d_out_grad, uint64_t ld_out,
+                  void* d_workspace, size_t workspace_bytes);
+
+/* Cross entropy of the output layer over the allowed tokens, with no logits kept: for
+ * row b with x_v = hidden[b] . weight[v], T = temp, target t and A_b the tokens that the
+ * bitmask allows and whose x is neither NaN nor -inf (+inf counts as the largest finite
+ * value):
+ *   loss[b] = log sum over A_b of exp(x_v / T) - x_t / T,  0 for a row whose target is
+ *             CG_NO_TOKEN or not in A_b (it does not count);
+ *   lse[b]  = log sum over A_b of exp(x_v / T), -inf for an empty A_b;
+ *   norm[b] = max x over A_b and sum over A_b of exp((x_v - max) / T), -inf and 0 for
+ *             an empty A_b: what cg_head_grad takes.
+ * A loss near 0 keeps its relative precision.  The products of bf16 matrices are summed
+ * in 32 bits; float matrices are multiplied as three bf16 parts each, to about the
+ * precision of 32-bit products.
+ *  d_hidden : [B][ld_hidden], d_weight : [V][ld_weight], of D columns
+ *  d_bitmask: u32 [B][W] or NULL: every token is allowed
+ *  d_target : u32 [B]; temp : T > 0, finite
+ *  d_out_loss: f32 [B]; d_out_lse: f32 [B] or NULL; d_out_norm: f32 [B][2] or NULL
+ * Device errors: CG_DEV_BAD_TOKEN, CG_DEV_TIMEOUT. */
+int cg_head_workspace(const cg_ctx* c, const void* d_hidden, const void* d_weight, int dtype, uint32_t B, uint32_t V,
+                      uint32_t D, uint64_t ld_hidden, uint64_t ld_weight, int grad, size_t* bytes);
+int cg_head_loss(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtype, uint32_t B, uint32_t V, uint32_t D,
+                 uint64_t ld_hidden, uint64_t ld_weight, const uint32_t* d_bitmask, const uint32_t* d_target, float temp,
+                 float* d_out_loss, float* d_out_lse, float* d_out_norm, void* d_workspace, size_t workspace_bytes);
+
+/* The gradients of sum over b of g_b loss[b] (g = d_grad_loss, f32 [B], NULL for 1) by
+ * hidden and by weight, the logits computed again, a piece of the vocabulary at a time
+ * (the workspace holds one piece's terms, 256 MB or 256 tokens of them):
+ *   d_bv = g_b / T * (p_v - [v = t]) over A_b, 0 elsewhere and in a row whose loss is 0;
+ *   grad_hidden = d weight,  grad_weight = d^T hidden.
+ * p_t - 1 is taken from the loss, as expm1(-loss).  Terms d of bf16 matrices are rounded
+ * to bf16 for the products (a relative error of 2^-8 at most, as the gradients'
+ * own rounding has).  hidden and weight have to be finite: 0 * inf is NaN, also for a token
+ * that no row allows.
+ *  d_loss, d_norm : as cg_head_loss wrote them for the same arguments
+ *  d_out_grad_hidden : [B][ld_grad_hidden] or NULL; d_out_grad_weight :
+ *              [V][ld_grad_weight] or NULL (not both)
+ *  workspace : of cg_head_workspace with grad != 0
+ * Device errors: CG_DEV_TIMEOUT. */
+int cg_head_grad(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtype, uint32_t B, uint32_t V, uint32_t D,
+                 uint64_t ld_hidden, uint64_t ld_weight, const uint32_t* d_bitmask, const uint32_t* d_target, float temp,
+                 const float* d_loss, const float* d_norm, const float* d_grad_loss, void* d_out_grad_hidden,
+                 uint64_t ld_grad_hidden, void* d_out_grad_weight, uint64_t ld_grad_weight, void* d_workspace,
+                 size_t workspace_bytes);
+
 /* ---- pushdown automaton for recursive grammars ---------------------------------- */
 
 /* usetacet.com/docs/grammar, "The guarantee": the automaton that masks the
