@@ -165,6 +165,7 @@ class Ctx:
         if stream is None:
             stream = torch.cuda.current_stream()
         self.stream = stream
+        self._stream = stream.cuda_stream
         self._dev = torch.cuda.current_device()  # where the library creates the context
         self._rows = _rows  # an import in every call would be a twentieth of the smallest
         arr = (C.c_void_p * len(grammars))(*[g._h.value for g in grammars])
@@ -363,58 +364,58 @@ class Ctx:
         g, ld, D = R.matrix_of(call, grad, "grad", None, N, dev)
         o, ldo = R.rows_of(call, out_grad, "out_grad", (grad.dtype,), (self.V, D), dev)
         tok = R.want(call, tokens, "tokens", R.U32, (N,), dev)
-        need = self.embed_workspace(grad, tokens)
-        ws, _keep = R.workspace_of(self, call, workspace, need)
+        work = R.workspace_of(self, call, workspace, self.embed_workspace(grad, tokens))
         L.check(call, L.lib().cg_embed_grad(self._h, g, R.DTYPE[grad.dtype], N, self.V, D, ld, tok, scale,
-                                            int(accumulate), o, ldo, ws, need if _keep is None else _keep.numel()))
+                                            int(accumulate), o, ldo, _ptr(work), 0 if work is None else work.numel()))
+
+    def _head_operands(self, call, hidden, weight):
+        """(what the calls take of the two matrices, B, D)."""
+        R, dev, B = self._rows, self._dev, hidden.shape[0]
+        h, ldh, D = R.matrix_of(call, hidden, "hidden", None, B, dev)
+        w, ldw = R.rows_of(call, weight, "weight", (hidden.dtype,), (self.V, D), dev)
+        return (self._h, h, w, R.DTYPE[hidden.dtype], B, self.V, D, ldh, ldw), B, D
+
+    def _head_bytes(self, operands, grad) -> int:
+        n = C.c_size_t()
+        L.check("cg_head_workspace", L.lib().cg_head_workspace(*operands, grad, C.byref(n)))
+        return n.value
 
     def head_workspace(self, hidden, weight, grad: bool = False) -> int:
         """Bytes that head_loss (or head_grad) works in."""
-        R, call, dev = self._rows, "cg_head_workspace", self._dev
-        h, ldh, D = R.matrix_of(call, hidden, "hidden", None, hidden.shape[0], dev)
-        w, ldw = R.rows_of(call, weight, "weight", (hidden.dtype,), (self.V, D), dev)
-        n = C.c_size_t()
-        L.check(call, L.lib().cg_head_workspace(self._h, h, w, R.DTYPE[hidden.dtype], hidden.shape[0], self.V, D, ldh,
-                                                ldw, int(grad), C.byref(n)))
-        return n.value
+        return self._head_bytes(self._head_operands("cg_head_workspace", hidden, weight)[0], int(grad))
 
     def head_loss(self, hidden, weight, target, out_loss, temp: float = 1.0, bitmask=None, out_lse=None,
                   out_norm=None, workspace=None) -> None:
         """Cross entropy of each row of hidden [B, D] against its target token [B] over the allowed tokens, the
         logits hidden @ weight.T (weight [V, D]) never stored; out_norm [B, 2] receives the normaliser as
         head_grad takes it.  workspace: u8 tensor of head_workspace() bytes, else one is allocated."""
-        R, call, dev, B = self._rows, "cg_head_loss", self._dev, hidden.shape[0]
-        h, ldh, D = R.matrix_of(call, hidden, "hidden", None, B, dev)
-        w, ldw = R.rows_of(call, weight, "weight", (hidden.dtype,), (self.V, D), dev)
-        t = R.want(call, target, "target", R.U32, (B,), dev)
+        R, call, dev = self._rows, "cg_head_loss", self._dev
+        operands, B, _ = self._head_operands(call, hidden, weight)
         mask = R.opt(call, bitmask, "bitmask", R.U32, (B, self.W), dev)
-        loss, lse = R.want(call, out_loss, "out_loss", R.F32, (B,), dev), R.opt(call, out_lse, "out_lse", R.F32, (B,), dev)
-        norm = R.opt(call, out_norm, "out_norm", R.F32, (B, 2), dev)
-        need = self.head_workspace(hidden, weight)
-        ws, _keep = R.workspace_of(self, call, workspace, need)
-        L.check(call, L.lib().cg_head_loss(self._h, h, w, R.DTYPE[hidden.dtype], B, self.V, D, ldh, ldw, mask, t, temp,
-                                           loss, lse, norm, ws, need if _keep is None else _keep.numel()))
+        t, loss = R.want(call, target, "target", R.U32, (B,), dev), R.want(call, out_loss, "out_loss", R.F32, (B,), dev)
+        lse, norm = R.opt(call, out_lse, "out_lse", R.F32, (B,), dev), R.opt(call, out_norm, "out_norm", R.F32, (B, 2), dev)
+        work = R.workspace_of(self, call, workspace, self._head_bytes(operands, 0))
+        L.check(call, L.lib().cg_head_loss(*operands, mask, t, temp, loss, lse, norm, _ptr(work),
+                                           0 if work is None else work.numel()))
 
     def head_grad(self, hidden, weight, target, loss, norm, out_grad_hidden=None, out_grad_weight=None,
                   temp: float = 1.0, bitmask=None, grad_loss=None, workspace=None) -> None:
         """The gradients of the sum of grad_loss [B] * loss by hidden and by weight (one of them may be None), from
         the loss and the normaliser that head_loss left.  workspace: of head_workspace(..., grad=True) bytes."""
-        R, call, dev, B = self._rows, "cg_head_grad", self._dev, hidden.shape[0]
-        h, ldh, D = R.matrix_of(call, hidden, "hidden", None, B, dev)
-        w, ldw = R.rows_of(call, weight, "weight", (hidden.dtype,), (self.V, D), dev)
+        R, call, dev = self._rows, "cg_head_grad", self._dev
+        operands, B, D = self._head_operands(call, hidden, weight)
         dh, lddh, dw, lddw = None, 0, None, 0
         if out_grad_hidden is not None:
             dh, lddh = R.rows_of(call, out_grad_hidden, "out_grad_hidden", (hidden.dtype,), (B, D), dev)
         if out_grad_weight is not None:
             dw, lddw = R.rows_of(call, out_grad_weight, "out_grad_weight", (hidden.dtype,), (self.V, D), dev)
-        t = R.want(call, target, "target", R.U32, (B,), dev)
         mask = R.opt(call, bitmask, "bitmask", R.U32, (B, self.W), dev)
-        kept = R.want(call, loss, "loss", R.F32, (B,), dev), R.want(call, norm, "norm", R.F32, (B, 2), dev)
+        t, kept = R.want(call, target, "target", R.U32, (B,), dev), R.want(call, loss, "loss", R.F32, (B,), dev)
+        norm = R.want(call, norm, "norm", R.F32, (B, 2), dev)
         up = R.opt(call, grad_loss, "grad_loss", R.F32, (B,), dev)
-        need = self.head_workspace(hidden, weight, grad=True)
-        ws, _keep = R.workspace_of(self, call, workspace, need)
-        L.check(call, L.lib().cg_head_grad(self._h, h, w, R.DTYPE[hidden.dtype], B, self.V, D, ldh, ldw, mask, t, temp,
-                                           *kept, up, dh, lddh, dw, lddw, ws, need if _keep is None else _keep.numel()))
+        work = R.workspace_of(self, call, workspace, self._head_bytes(operands, 1))
+        L.check(call, L.lib().cg_head_grad(*operands, mask, t, temp, kept, norm, up, dh, lddh, dw, lddw, _ptr(work),
+                                           0 if work is None else work.numel()))
 
     def self_test_cluster_timeout(self, out) -> None:
         """Make a block of a cluster give up while others still send to it (the status then

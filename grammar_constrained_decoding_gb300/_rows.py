@@ -44,14 +44,17 @@ def matrix_of(call: str, t, what: str, dtype, rows: int, dev: int = 0) -> tuple[
     return *rows_of(call, t, what, LOGITS if dtype is None else (dtype,), shape, dev), t.shape[1]
 
 
-def workspace_of(ctx, call: str, given, nbytes: int) -> tuple[int | None, object]:
-    """(pointer, the tensor that holds it) of nbytes of device memory: the caller's tensor, or a new one that
-    belongs to the context's stream."""
+def workspace_of(ctx, call: str, given, nbytes: int):
+    """A u8 tensor of at least nbytes of device memory: the caller's, or a new one that belongs to the context's
+    stream; None where nothing is needed."""
     if not nbytes:
-        return None, None
-    if given is None:
-        with torch.cuda.device(ctx._dev), torch.cuda.stream(ctx.stream):
-            given = torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
-    elif given.numel() < nbytes:
-        raise L.CgError(call, L.CG_E_ARG, f"workspace: {nbytes} bytes are wanted")
-    return want(call, given, "workspace", (torch.uint8,), given.shape, ctx._dev), given
+        return None
+    if given is not None:
+        want(call, given, "workspace", (torch.uint8,), given.shape, ctx._dev)
+        if given.numel() < nbytes:
+            raise L.CgError(call, L.CG_E_ARG, f"workspace: {nbytes} bytes are wanted")
+        return given
+    if torch.cuda.current_stream(ctx._dev).cuda_stream == ctx._stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
+    with torch.cuda.stream(ctx.stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)

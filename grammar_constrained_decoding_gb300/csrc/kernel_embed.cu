@@ -60,15 +60,18 @@ struct Elems {
 
 // ---- the lookup ----------------------------------------------------------------------------
 
-constexpr uint32_t kLookThreads = 256, kLookEach = 4;
+constexpr uint32_t kLookThreads = 256;
+constexpr uint32_t look_each(int bytes) { return bytes == 16 ? 4 : 8; }
 
-// Vectors are numbered through all rows; a block takes 1024 that follow one another
+// Vectors are numbered through all rows; a block takes 1024 (2048 narrow ones) that follow
+// one another, all of a thread's loads under way together
 template <bool BF16, int BYTES>
 __global__ void __launch_bounds__(kLookThreads) look_kernel(const char* table, uint64_t pitch, const uint32_t* tokens,
                                                             uint32_t N, uint32_t V, uint32_t vecs, float scale, char* out,
                                                             uint64_t pitch_out, uint32_t* status) {
   using E = Elems<BF16, BYTES>;
   using Vec = typename E::Vec;
+  constexpr uint32_t kLookEach = look_each(BYTES);
   griddep_launch_dependents();
   griddep_wait();
   const uint64_t base = uint64_t(blockIdx.x) * (kLookThreads * kLookEach);
@@ -155,12 +158,15 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
     cluster_sync(n);
     // where this block's positions of digit d begin: all smaller digits, and d's in the blocks before
     uint32_t all = 0, before = 0;
-    if (tid < kBins)
-      for (uint32_t r = 0; r < n; ++r) {
+    if (tid < kBins) {
+#pragma unroll
+      for (uint32_t r = 0; r < kSortMost; ++r) {
+        if (r >= n) break;
         const uint32_t x = n == 1 ? s.count[tid] : read_count(&s.count[tid], r);
         all += x;
         if (r < rank) before += x;
       }
+    }
     uint32_t up = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -191,11 +197,13 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
       if (there && nth == 0) s.mine[warp][digit] = uint16_t(__popc(same));
       __syncthreads();
       if (tid < kBins) {
-        uint32_t at = 0;
+        uint32_t at = 0, x[kSortWarps];
+#pragma unroll
+        for (uint32_t w = 0; w < kSortWarps; ++w) x[w] = s.mine[w][tid];
+#pragma unroll
         for (uint32_t w = 0; w < kSortWarps; ++w) {
-          const uint32_t x = s.mine[w][tid];
           s.mine[w][tid] = uint16_t(at);
-          at += x;
+          at += x[w];
         }
         s.tile_base[tid] = s.base[tid];
         s.base[tid] += at;
@@ -213,31 +221,55 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
   }
 }
 
-// The first cluster sorts; the others meanwhile write zeros over the gradient (all of it: rows
-// of tokens that occur are written again afterwards, at most one a position)
+constexpr uint32_t kZeroBytes = 32768;   // of zeros in shared memory, copied out again and again
+
+__device__ __forceinline__ void bulk_s2g(void* to, const void* from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_addr(from)), "r"(bytes)
+               : "memory");
+}
+
+// Zeros over the gradient by `blocks` blocks: rows without gaps on the 16-byte grid by bulk
+// copies of 32 KB from shared memory, other rows by vectors.
 template <int BYTES>
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a, char* out, uint64_t pitch, uint32_t vecs) {
-  extern __shared__ __align__(16) unsigned char smem[];
+__device__ void write_zeros(char* out, uint64_t pitch, uint32_t rows, uint32_t vecs, uint32_t block, uint32_t blocks,
+                            unsigned char* smem) {
   using Vec = typename VecOf<BYTES>::type;
-  griddep_launch_dependents();
-  griddep_wait();
-  const uint32_t n = cluster_size();
-  if (blockIdx.x < n) {
-    sort_tokens(a, *reinterpret_cast<SortShared*>(smem));
+  if (BYTES == 16 && pitch == uint64_t(vecs) * BYTES) {
+    for (uint32_t i = threadIdx.x; i < kZeroBytes / 16; i += kSortThreads) reinterpret_cast<uint4*>(smem)[i] = uint4{};
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const uint64_t all = uint64_t(rows) * pitch;
+      for (uint64_t at = uint64_t(block) * kZeroBytes; at < all; at += uint64_t(blocks) * kZeroBytes)
+        bulk_s2g(out + at, smem, uint32_t(min(uint64_t(kZeroBytes), all - at)));
+      asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group 0;" ::: "memory");
+    }
     return;
   }
-  if (!out) return;
   constexpr uint32_t kEach = 8;
-  const uint64_t all = uint64_t(a.V) * vecs, step = uint64_t(gridDim.x - n) * (kSortThreads * kEach);
-  for (uint64_t base = uint64_t(blockIdx.x - n) * (kSortThreads * kEach); base < all; base += step) {
+  const uint64_t all = uint64_t(rows) * vecs, step = uint64_t(blocks) * (kSortThreads * kEach);
+  for (uint64_t base = uint64_t(block) * (kSortThreads * kEach); base < all; base += step) {
     const uint32_t row0 = uint32_t(base / vecs), off = uint32_t(base - uint64_t(row0) * vecs);
 #pragma unroll
     for (uint32_t k = 0; k < kEach; ++k) {
       const uint32_t at = off + k * kSortThreads + threadIdx.x, row = row0 + at / vecs;
-      if (row < a.V) *reinterpret_cast<Vec*>(out + row * pitch + uint64_t(at % vecs) * BYTES) = Vec{};
+      if (row < rows) *reinterpret_cast<Vec*>(out + row * pitch + uint64_t(at % vecs) * BYTES) = Vec{};
     }
   }
 }
+
+// The first cluster sorts; the others meanwhile write zeros over the gradient (all of it: rows
+// of tokens that occur are written again afterwards, at most one a position)
+template <int BYTES>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a, char* out, uint64_t pitch, uint32_t vecs) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t n = cluster_size();
+  if (blockIdx.x < n) sort_tokens(a, *reinterpret_cast<SortShared*>(smem));
+  else if (out) write_zeros<BYTES>(out, pitch, a.V, vecs, blockIdx.x - n, gridDim.x - n, smem);
+}
+constexpr size_t kSortSmem = sizeof(SortShared) > kZeroBytes ? sizeof(SortShared) : kZeroBytes;
 
 // ---- summing runs ------------------------------------------------------------------------------
 
@@ -270,16 +302,18 @@ __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t token, uint
   *at = E::put(x);
 }
 
-// A block takes a chunk of the sorted positions and a slab of the columns
+// A block takes a chunk of the sorted positions and a slab of the columns, 16 bytes of a row
+// to a thread (several narrow vectors, a slab's width apart in threads)
 template <bool BF16, int BYTES>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   using E = Elems<BF16, BYTES>;
   using Vec = typename E::Vec;
-  constexpr uint32_t kAhead = 8;
+  constexpr uint32_t kAhead = 8, kCols = 16 / BYTES;
   __shared__ uint32_t key[kMostChunk + 2], pos[kMostChunk];
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t chunk = blockIdx.x / a.slabs, col = (blockIdx.x - chunk * a.slabs) * kSumThreads + threadIdx.x;
+  const uint32_t chunk = blockIdx.x / a.slabs;
+  const uint32_t col0 = (blockIdx.x - chunk * a.slabs) * kSumThreads * kCols + threadIdx.x;
   const uint32_t from = chunk * a.chunk, n = min(a.chunk, a.N - from);
   for (uint32_t i = threadIdx.x; i < n + 2; i += kSumThreads) {
     // key[i]: of position from + i - 1; past either end a value that no token has
@@ -288,49 +322,61 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   }
   for (uint32_t i = threadIdx.x; i < n; i += kSumThreads) pos[i] = a.pos[from + i];
   __syncthreads();
-  if (col >= a.vecs) return;
-  const char* in = a.grad + uint64_t(col) * BYTES;
-  float acc[E::kN] = {};
+  if (col0 >= a.vecs) return;
+  const char* in = a.grad + uint64_t(col0) * BYTES;
+  float acc[kCols][E::kN] = {};
   uint32_t began = 0;
   for (uint32_t i0 = 0; i0 < n; i0 += kAhead) {
-    Vec v[kAhead];
+    Vec v[kAhead][kCols];
 #pragma unroll
     for (uint32_t u = 0; u < kAhead; ++u)
-      if (i0 + u < n && key[i0 + u + 1] < a.V) v[u] = *reinterpret_cast<const Vec*>(in + pos[i0 + u] * a.pitch);
+#pragma unroll
+      for (uint32_t q = 0; q < kCols; ++q)
+        if (i0 + u < n && key[i0 + u + 1] < a.V && col0 + q * kSumThreads < a.vecs)
+          v[u][q] = *reinterpret_cast<const Vec*>(in + pos[i0 + u] * a.pitch + q * (kSumThreads * BYTES));
 #pragma unroll
     for (uint32_t u = 0; u < kAhead; ++u) {
       const uint32_t i = i0 + u;
       if (i >= n) break;
       const uint32_t token = key[i + 1];
       if (token >= a.V) break;   // rows without a token come last
-      float x[E::kN];
-      E::get(v[u], x);
 #pragma unroll
-      for (int e = 0; e < E::kN; ++e) acc[e] += x[e];
+      for (uint32_t q = 0; q < kCols; ++q) {
+        float x[E::kN];
+        E::get(v[u][q], x);
+#pragma unroll
+        for (int e = 0; e < E::kN; ++e) acc[q][e] += x[e];
+      }
       const bool goes_on = key[i + 2] == token;
       if (goes_on && i + 1 < n) continue;
       const bool before = began == 0 && key[0] == token;
-      if (!before && !goes_on) {
-        write_sum<BF16, BYTES>(a, token, col, acc);
-      } else {
-        float* to = a.part + (size_t(chunk) * 2 + (before ? 0 : 1)) * a.ld_part + col * E::kN;
 #pragma unroll
-        for (int e = 0; e < E::kN; ++e) to[e] = acc[e];
+      for (uint32_t q = 0; q < kCols; ++q) {
+        const uint32_t col = col0 + q * kSumThreads;
+        if (col < a.vecs) {
+          if (!before && !goes_on) {
+            write_sum<BF16, BYTES>(a, token, col, acc[q]);
+          } else {
+            float* to = a.part + (size_t(chunk) * 2 + (before ? 0 : 1)) * a.ld_part + col * E::kN;
+#pragma unroll
+            for (int e = 0; e < E::kN; ++e) to[e] = acc[q][e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < E::kN; ++e) acc[q][e] = 0.f;
       }
-#pragma unroll
-      for (int e = 0; e < E::kN; ++e) acc[e] = 0.f;
       began = i + 1;
     }
   }
 }
 
-constexpr uint32_t kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinColumns = 32;
+constexpr uint32_t kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinColumns = 128, kJoinBlocks = 2048;
 
-// A block takes a run that begins in its chunk and goes on, and 32 of its columns: the warps
+// A block takes a run that begins in its chunk and goes on, 128 columns at a time: the warps
 // take the chunks' sums in turn, and the warps' sums are added in their order
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumArgs a, uint32_t D) {
-  __shared__ float mine[kJoinWarps][kJoinColumns];
+  __shared__ float4 mine[kJoinWarps][32];
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t chunk = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -338,26 +384,34 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumArgs a, uin
   if (to >= a.N) return;
   const uint32_t token = a.key[to - 1];
   if (token >= a.V || a.key[to] != token || (from > 0 && a.key[from - 1] == token)) return;
-  uint32_t lo = to, hi = a.N;   // the run's end
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (a.key[mid] > token) hi = mid;
-    else lo = mid + 1;
+  // the run's last chunk: the one after which the next does not begin with the token
+  uint32_t last = chunk + 1;
+  for (;;) {
+    const uint64_t at = (uint64_t(last) + 1 + lane) * a.chunk;
+    const uint32_t same = __ballot_sync(0xFFFFFFFFu, at < a.N && a.key[min(at, uint64_t(a.N - 1))] == token);
+    last += __ffs(~same) ? __ffs(~same) - 1 : 32;
+    if (same != 0xFFFFFFFFu) break;
   }
-  const uint32_t last = (lo - 1) / a.chunk;
-  for (uint32_t col = blockIdx.y * kJoinColumns + lane; col - lane < D; col += gridDim.y * kJoinColumns) {
-    float s = 0.f;
+  for (uint32_t base = blockIdx.y * kJoinColumns; base < D; base += gridDim.y * kJoinColumns) {
+    const uint32_t col = base + 4 * lane;   // a part's rows are padded to whole groups of 4
+    float4 s = {};
     if (col < D)
 #pragma unroll 4
-      for (uint32_t j = chunk + warp; j <= last; j += kJoinWarps)
-        s += a.part[(size_t(j) * 2 + (j == chunk ? 1 : 0)) * a.ld_part + col];
+      for (uint32_t j = chunk + warp; j <= last; j += kJoinWarps) {
+        const float4 x = *reinterpret_cast<const float4*>(a.part + (size_t(j) * 2 + (j == chunk ? 1 : 0)) * a.ld_part + col);
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+      }
     mine[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && col < D) {
+    if (threadIdx.x < kJoinColumns && base + threadIdx.x < D) {
       float x = 0.f;
-      for (uint32_t w = 0; w < kJoinWarps; ++w) x += mine[w][lane];
+#pragma unroll
+      for (uint32_t w = 0; w < kJoinWarps; ++w) x += reinterpret_cast<const float*>(mine[w])[threadIdx.x];
       x *= a.scale;
-      char* at = a.out + token * a.pitch_out + uint64_t(col) * (BF16 ? 2 : 4);
+      char* at = a.out + token * a.pitch_out + uint64_t(base + threadIdx.x) * (BF16 ? 2 : 4);
       if (BF16) {
         __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(at);
         *o = __float2bfloat16_rn(a.add ? __bfloat162float(*o) + x : x);
@@ -410,7 +464,7 @@ template <bool BF16, int BYTES>
 cudaError_t launch_look(const void* table, uint64_t pitch, const uint32_t* tokens, uint32_t N, uint32_t V, uint32_t D,
                         float scale, void* out, uint64_t pitch_out, uint32_t* status, cudaStream_t stream) {
   const uint32_t vecs = uint32_t(uint64_t(D) * (BF16 ? 2 : 4) / BYTES);
-  const uint32_t blocks = tiles_of(uint64_t(N) * vecs, kLookThreads * kLookEach);
+  const uint32_t blocks = tiles_of(uint64_t(N) * vecs, kLookThreads * look_each(BYTES));
   return launch_dependent(look_kernel<BF16, BYTES>, dim3(blocks), dim3(kLookThreads), 0, stream,
                           static_cast<const char*>(table), pitch, tokens, N, V, vecs, scale, static_cast<char*>(out),
                           pitch_out, status);
@@ -419,18 +473,18 @@ cudaError_t launch_look(const void* table, uint64_t pitch, const uint32_t* token
 template <bool BF16, int BYTES>
 cudaError_t launch_grad(int device, const SortArgs& sort, SumArgs sum, uint32_t chunks, uint32_t D, cudaStream_t stream) {
   sum.vecs = uint32_t(uint64_t(D) * (BF16 ? 2 : 4) / BYTES);
-  sum.slabs = tiles_of(sum.vecs, kSumThreads);
+  sum.slabs = tiles_of(sum.vecs, kSumThreads * (16 / BYTES));
   uint32_t n = 1;
-  while (n < kSortMost && sort.N > n * 2048) n *= 2;
+  while (n < kSortMost && sort.N > n * kSortThreads) n *= 2;
   // without zeros to write the sorting cluster is alone
   const uint32_t clusters = sum.add ? 1 : kEmbedSms / n;
-  cudaError_t e = launch_clusters<sort_kernel<BYTES>>(device, clusters, n, kSortThreads, sizeof(SortShared), stream, sort,
+  cudaError_t e = launch_clusters<sort_kernel<BYTES>>(device, clusters, n, kSortThreads, kSortSmem, stream, sort,
                                                      sum.add ? static_cast<char*>(nullptr) : sum.out, sum.pitch_out, sum.vecs);
   if (e != cudaSuccess) return e;
   e = launch_dependent(sum_kernel<BF16, BYTES>, dim3(chunks * sum.slabs), dim3(kSumThreads), 0, stream, sum);
   if (e != cudaSuccess || chunks < 2) return e;
-  return launch_dependent(join_kernel<BF16>, dim3(chunks, std::min(tiles_of(D, kJoinColumns), 128u)), dim3(kJoinThreads), 0,
-                          stream, sum, D);
+  const uint32_t across = std::max(1u, std::min(tiles_of(D, kJoinColumns), kJoinBlocks / chunks));
+  return launch_dependent(join_kernel<BF16>, dim3(chunks, across), dim3(kJoinThreads), 0, stream, sum, D);
 }
 
 template <typename F>

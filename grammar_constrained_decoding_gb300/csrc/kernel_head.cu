@@ -596,7 +596,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   uint64_t most = V;
   if (p.lay_w) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * p.Dp * 2));
   if (grad) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * std::max(B, 1u) * 2));
-  most = std::max<uint64_t>(most / 256 * 256, 256);
+  if (most < V) most = std::max<uint64_t>(most / 256 * 256, 256);
   const uint64_t pieces = (V + most - 1) / most;
   p.piece = uint32_t(std::min<uint64_t>(up_to((V + pieces - 1) / pieces, 256), V));
   size_t at = 0;
