@@ -34,19 +34,23 @@ constexpr uint32_t kBlockK = 64;          // k of a stage: 128 bytes of bf16
 constexpr uint32_t kReaders = 8;          // warps that read tiles out: four row quarters x two column halves
 constexpr uint32_t kFirstReader = 4;      // after the copying, the multiplying and the allocating warp, and a spare
 constexpr uint32_t kHeadThreads = (kFirstReader + kReaders) * 32;
+constexpr uint32_t kChain = 16;           // stages whose products are summed in tensor memory: 1024 k
+constexpr uint32_t kStore = 4096;         // bytes of a box that a reader writes out: 32 rows of 128 bytes
 constexpr uint32_t kBand = 16;            // row tiles that are taken together over all columns
+constexpr uint32_t kBoxesEach = 1;
 constexpr uint32_t kHeadSms = 152;
 
-// one of a product's operands in shared memory: a block's share of a stage
-template <int CTAS>
+enum Readout { kLoss, kTerms, kOut };
+
+// a block's share of a stage, and how many fit beside the readers' boxes
+template <int CTAS, Readout READ>
 struct Stage {
   static constexpr uint32_t kA = kBlockM * kBlockK * 2;
   static constexpr uint32_t kB = kTileN / CTAS * kBlockK * 2;
   static constexpr uint32_t kBytes = kA + kB;
-  static constexpr uint32_t kCount = CTAS == 2 ? 6 : 4;
+  static constexpr uint32_t kBoxes = READ == kLoss ? 0 : kBoxesEach;   // a reader's boxes under way
+  static constexpr uint32_t kCount = (kMaxSmem - 2048 - kReaders * kBoxes * kStore) / kBytes;
 };
-
-enum Readout { kLoss, kTerms, kOut };
 
 // What is read out of the tiles
 struct LossOut {
@@ -54,23 +58,19 @@ struct LossOut {
   float* target_logit;       // [B], written by the tile that holds the row's target
 };
 struct TermsOut {
-  __nv_bfloat16* terms;      // [parts][B][ld]
-  uint64_t ld, part_stride;
   const float* loss;
   const float* norm;
   const float* up;
 };
 struct GradOut {
-  float* sums;               // [splits][m][ld_sums] or null
-  uint64_t ld_sums;
-  bool add, keep, wide;      // sums are added to what is there; kept there; out's rows lie on the 16-byte grid
-  void* out;                 // [m][ld] or null
+  bool boxes;                // written (added, with `add`) as boxes of `out`; else element by element to `at`
+  bool add, f32;
+  void* at;                  // [m][ld]
   uint64_t ld;
-  bool bf16;
 };
 
 struct Product {
-  CUtensorMap a, b;
+  CUtensorMap a, b, out;     // operands; the terms or the gradient as they are written
   uint32_t m, n, n_m, n_n;   // extent, and in tiles
   uint32_t blocks, splits;   // stages of one product; splits of them
   uint32_t products;         // 1, or 6 products of the parts
@@ -87,26 +87,36 @@ struct Product {
 };
 
 struct Ends {
-  uint64_t full[6], empty[6], tile_full[2], tile_empty[2], drain;
+  uint64_t full[7], empty[7], tile_full[2], tile_empty[2], drain;
   uint32_t tmem;
 };
 
 struct Work {
   uint32_t m0, n0, split, k0, k1;
 };
+// A work item's stages: all of them, or its split's.  (blocks * splits fits 32 bits: the
+// multiplying thread takes this between two tiles, while the tensor cores have nothing.)
+__device__ __forceinline__ void stages_of(const Product& p, uint32_t t, Work& w) {
+  w.split = 0;
+  w.k0 = 0;
+  w.k1 = p.blocks;
+  if (p.splits > 1) {
+    w.split = t / (p.n_m * p.n_n);
+    w.k0 = p.blocks * w.split / p.splits;
+    w.k1 = p.blocks * (w.split + 1) / p.splits;
+  }
+}
 // Bands of row tiles over all columns: what runs at one time shares both operands in L2
 template <int CTAS>
 __device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {
   Work w;
-  const uint32_t tiles = p.n_m * p.n_n;
-  w.split = t / tiles;
-  t -= w.split * tiles;
+  stages_of(p, t, w);
+  t -= w.split * p.n_m * p.n_n;
   const uint32_t band = t / (kBand * p.n_n), in = t - band * kBand * p.n_n;
   const uint32_t rows = min(kBand, p.n_m - band * kBand);
-  w.m0 = (band * kBand + in % rows) * kBlockM * CTAS;
-  w.n0 = in / rows * kTileN;
-  w.k0 = uint32_t(uint64_t(p.blocks) * w.split / p.splits);
-  w.k1 = uint32_t(uint64_t(p.blocks) * (w.split + 1) / p.splits);
+  w.n0 = in / rows;
+  w.m0 = (band * kBand + in - w.n0 * rows) * kBlockM * CTAS;
+  w.n0 *= kTileN;
   return w;
 }
 // the parts of the i-th of the six products, the smallest products first
@@ -115,11 +125,6 @@ __device__ __forceinline__ uint32_t part_b(uint32_t products, uint32_t i) { retu
 
 // ---- reading a tile out ----------------------------------------------------------------------
 
-__device__ __forceinline__ void store32(void* at, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -141,186 +146,246 @@ __device__ __forceinline__ void mask_words(const Product& p, uint32_t r, uint32_
   }
 }
 
-struct RowSum {
-  float m = -INFINITY, s = 0.f;
-  __device__ __forceinline__ void add(const float (&v)[32], float c) {
-    float top = v[0];
-#pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-    if (!(top > -INFINITY)) return;
-    if (top > m) {
-      s *= ex2((m - top) * c);
-      m = top;
-    }
-    const float2 nm = make_float2(-m, -m), c2 = make_float2(c, c);
-    float2 sum[2] = {};
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-      sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], ex2_pair(__fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), nm), c2)));
-    const float2 both = __fadd2_rn(sum[0], sum[1]);
-    s += both.x + both.y;
+// exp((x - m) / T) of a row as 2^(x c - r) 2^(r - m c), r the integer next to m c: one
+// instruction an element in place of two, and no rounding that m shares among them.  Where
+// m c is too large for that (+inf among the logits, a temperature near 0) as (x - m) c.
+struct Scale {
+  float c, m, r, rest;       // rest = 2^(r - m c)
+  bool fast;
+  __device__ __forceinline__ Scale(float c_, float m_) : c(c_), m(m_), r(rintf(m_ * c_)), rest(1.f) {
+    fast = fabsf(m * c) < 1048576.f;
+    if (fast) rest = ex2(-fmaf(m, c, -r));
+  }
+  __device__ __forceinline__ float2 at(float x, float y) const {
+    return ex2_pair(__ffma2_rn(make_float2(x, y), make_float2(c, c), make_float2(-r, -r)));
+  }
+  __device__ __forceinline__ float2 far(float x, float y) const {
+    return ex2_pair(__fmul2_rn(__fadd2_rn(make_float2(x, y), make_float2(-m, -m)), make_float2(c, c)));
   }
 };
 
-__device__ __forceinline__ void read_loss(const Product& p, uint32_t tmem, uint32_t r, uint32_t col, uint32_t target,
-                                          const uint32_t (&words)[4]) {
-  const float c = exp_scale(p.temp);
-  RowSum sum;
-#pragma unroll 1
-  for (uint32_t j = 0; j < 4; ++j) {
-    float v[32];
-    tc::tmem_load32(tmem + 32 * j, v);
-    const uint32_t word = j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3];
+// the convention for values that are not finite, and what the mask forbids, over 32 columns
+__device__ __forceinline__ void set_allowed(float* x, uint32_t word) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = logit(v[i], (word >> i) & 1u);
-    const uint32_t at = target - (p.v0 + col + 32 * j);
-    if (at < 32 && r < p.m) {
-      float x = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (uint32_t(i) == at) {
-          x = v[i];
-          v[i] = -INFINITY;
-        }
-      p.loss.target_logit[r] = x;
-    }
-    sum.add(v, c);
-  }
-  if (r < p.m && col < p.n) p.loss.part[size_t((p.v0 + col) >> 7) * p.m + r] = make_float2(sum.m, sum.s);
+  for (int i = 0; i < 32; ++i) x[i] = logit(x[i], (word >> i) & 1u);
 }
 
+struct RowSum {
+  float m = -INFINITY, s = 0.f;   // maximum, sum of exp((x - m) / T)
+  // 32 columns; first as they are where the whole warp's are allowed, again where that met an
+  // infinity or a NaN
+  __device__ __forceinline__ void add(float* x, uint32_t word, float c) {
+    bool plain = __all_sync(0xFFFFFFFFu, word == 0xFFFFFFFFu);
+#pragma unroll 1
+    for (;; plain = false) {
+      if (!plain) set_allowed(x, word);
+      float top = x[0], top2 = x[1];
+#pragma unroll
+      for (int i = 2; i < 32; i += 2) {
+        top = fmaxf(top, x[i]);
+        top2 = fmaxf(top2, x[i + 1]);
+      }
+      top = fmaxf(fmaxf(top, top2), m);
+      const Scale t(c, top);
+      float2 sum[2] = {};
+      const bool fast = __all_sync(0xFFFFFFFFu, t.fast);
+      if (fast) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], t.at(x[i], x[i + 1]));
+      } else if (top > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], t.far(x[i], x[i + 1]));
+      }
+      const float2 all = __fadd2_rn(sum[0], sum[1]);
+      const float add = (all.x + all.y) * (fast ? t.rest : 1.f);
+      if (plain && __any_sync(0xFFFFFFFFu, !(add <= FLT_MAX) || !(top <= FLT_MAX))) continue;
+      if (top > -INFINITY) {
+        s = s * (m > -INFINITY ? ex2((m - top) * c) : 0.f) + add;
+        m = top;
+      }
+      return;
+    }
+  }
+};
+
+// 32 columns of a row's logits, from column `col` of the piece on
+__device__ __forceinline__ void read_loss(const Product& p, float* x, uint32_t r, uint32_t col, uint32_t target, uint32_t word,
+                                          float c, RowSum& sum) {
+  const uint32_t at = target - (p.v0 + col);
+  if (at < 32) {   // the target is apart from the others
+    float xt = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (uint32_t(i) == at) {
+        xt = x[i];
+        x[i] = -INFINITY;
+      }
+    if (r < p.m) p.loss.target_logit[r] = logit(xt, (word >> at) & 1u);
+  }
+  __syncwarp();
+  sum.add(x, word, c);
+}
+
+// A reader's box in shared memory as the copies store it: 32 rows of 128 bytes, the 16-byte
+// pieces of row i exchanged by i mod 8
+__device__ __forceinline__ uint32_t box_piece(uint32_t box, uint32_t row, uint32_t piece) {
+  return box + row * 128 + ((piece ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void box_write(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// The boxes of a reader, taken in turn: a box is written again once its last copy has read it
+template <uint32_t BOXES>
+struct Boxes {
+  uint32_t at, turn = 0;
+  __device__ __forceinline__ explicit Boxes(uint32_t first) : at(first) {}
+  __device__ __forceinline__ void next() {
+    if ((threadIdx.x & 31) == 0) tc::stores_read<BOXES - 1>();
+    __syncwarp();
+    turn = turn + 1 == BOXES ? 0 : turn + 1;
+  }
+  __device__ __forceinline__ uint32_t now() const { return at + turn * kStore; }
+  template <bool ADD>
+  __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t x, uint32_t y, uint32_t z) const {
+    tc::fence_shared();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      if (ADD) tc::add_box(map, now(), int(x), int(y), int(z));
+      else tc::store_box(map, now(), int(x), int(y), int(z));
+      tc::stores_commit();
+    }
+  }
+};
+
+// d = k * exp((x - m) / T), at the target as it stands
 struct RowTerms {
-  float m, k, at_target;     // d = k * exp((x - m) / T), at the target as it stands
-  bool counts;
+  Scale scale;
+  float k, at_target;
+  uint32_t target;           // CG_NO_TOKEN in a row that does not count
 };
 __device__ __forceinline__ RowTerms row_terms(const Product& p, uint32_t r, uint32_t target) {
-  RowTerms t{0.f, 0.f, 0.f, false};
-  if (r >= p.m) return t;
-  const float loss = p.terms.loss[r], m = p.terms.norm[2 * size_t(r)], s = p.terms.norm[2 * size_t(r) + 1];
-  const float scale = __fdiv_rn(p.terms.up ? p.terms.up[r] : 1.f, p.temp);
-  t.counts = loss > 0.f && target < 0xFFFFFFFFu;   // a loss of 0: no target that counts, or nothing beside it
-  if (t.counts) {
-    t.m = m;
-    t.k = __fdiv_rn(scale, s);
-    t.at_target = scale * expm1f(-loss);
-  }
-  return t;
-}
-__device__ __forceinline__ void read_terms(const Product& p, uint32_t tmem, uint32_t r, uint32_t col, uint32_t target,
-                                           const uint32_t (&words)[4], const RowTerms& t) {
   const float c = exp_scale(p.temp);
-  const uint32_t parts = p.products == 1 ? 1 : 3;
-#pragma unroll 1
-  for (uint32_t j = 0; j < 4; ++j) {
-    float v[32];
-    tc::tmem_load32(tmem + 32 * j, v);
-    const uint32_t c0 = col + 32 * j;
-    if (r >= p.m || c0 >= p.terms.ld) continue;
-    const uint32_t word = j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3];
-    const float2 nm = make_float2(-t.m, -t.m), c2 = make_float2(c, c), k2 = make_float2(t.k, t.k);
+  if (r < p.m && target != CG_NO_TOKEN) {
+    const float loss = p.terms.loss[r], m = p.terms.norm[2 * size_t(r)], s = p.terms.norm[2 * size_t(r) + 1];
+    if (loss > 0.f) {   // a loss of 0: no target that counts, or nothing beside it
+      const Scale t(c, m);
+      const float g = __fdiv_rn(p.terms.up ? p.terms.up[r] : 1.f, p.temp);
+      return {t, __fdiv_rn(g, s) * t.rest, g * expm1f(-loss), target};
+    }
+  }
+  return {Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};   // c = 0, k = 0: every term is 0
+}
+// turns 32 columns of a row's logits into its terms
+__device__ __forceinline__ void set_terms(const Product& p, float* x, uint32_t col, uint32_t word, const RowTerms& t) {
+  const float2 k2 = make_float2(t.k, t.k);
+  const bool none = t.target == CG_NO_TOKEN;
+  // as they are: all allowed, no row with a maximum out of the ordinary
+  if (__all_sync(0xFFFFFFFFu, (word == 0xFFFFFFFFu || none) && t.scale.fast)) {
+    float2 check = {};
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const float2 x = make_float2(logit(v[i], (word >> i) & 1u), logit(v[i + 1], (word >> (i + 1)) & 1u));
-      const float2 d = __fmul2_rn(ex2_pair(__fmul2_rn(__fadd2_rn(x, nm), c2)), k2);
-      v[i] = t.counts ? d.x : 0.f;
-      v[i + 1] = t.counts ? d.y : 0.f;
+      const float2 d = __fmul2_rn(t.scale.at(x[i], x[i + 1]), k2);
+      check = __fadd2_rn(check, d);
+      x[i] = d.x;
+      x[i + 1] = d.y;
     }
-    const uint32_t at = target - (p.v0 + c0);
-    if (at < 32 && t.counts) {
+    if (!(fabsf(check.x + check.y) <= FLT_MAX)) {   // NaN among them (no +inf: the maximum would be it)
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (uint32_t(i) == at) v[i] = t.at_target;
+      for (int i = 0; i < 32; ++i) x[i] = fabsf(x[i]) <= FLT_MAX ? x[i] : 0.f;
     }
-    __nv_bfloat16* to = p.terms.terms + size_t(r) * p.terms.ld + c0;
-    for (uint32_t part = 0; part < parts; ++part) {
-      uint32_t w[16];
+  } else {
+    set_allowed(x, word);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        w[i] = pack2(v[2 * i], v[2 * i + 1]);
-        if (parts > 1) {
-          v[2 * i] -= __uint_as_float(w[i] << 16);
-          v[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-      }
-      const uint32_t lo[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
-      const uint32_t hi[8] = {w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]};
-      store32(to + part * p.terms.part_stride, lo);
-      store32(to + part * p.terms.part_stride + 16, hi);
+    for (int i = 0; i < 32; i += 2) {
+      const float2 d = __fmul2_rn(t.scale.fast ? t.scale.at(x[i], x[i + 1]) : t.scale.far(x[i], x[i + 1]), k2);
+      x[i] = none ? 0.f : d.x;
+      x[i + 1] = none ? 0.f : d.y;
     }
+  }
+  const uint32_t at = t.target - (p.v0 + col);
+  if (at < 32 && !none) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (uint32_t(i) == at) x[i] = t.at_target;
+  }
+  __syncwarp();
+}
+// 32 columns as bf16: the first or the second half of a box
+__device__ __forceinline__ void write_bf16(uint32_t box, uint32_t half, const float* x) {
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i)
+    box_write(box_piece(box, threadIdx.x & 31, 4 * half + i), pack2(x[8 * i], x[8 * i + 1]), pack2(x[8 * i + 2], x[8 * i + 3]),
+              pack2(x[8 * i + 4], x[8 * i + 5]), pack2(x[8 * i + 6], x[8 * i + 7]));
+}
+// 32 rows of 32 columns (chunk j of the reader's 128) on their way: bf16 boxes hold two chunks
+template <uint32_t BOXES>
+__device__ __forceinline__ void send_bf16(const Product& p, const float* x, uint32_t z, uint32_t row0, uint32_t col, uint32_t j,
+                                          Boxes<BOXES>& boxes) {
+  if (row0 >= p.m || (col & ~63u) >= p.n) return;
+  if (!(j & 1u)) boxes.next();
+  write_bf16(boxes.now(), j & 1u, x);
+  if (j & 1u) boxes.template send<false>(&p.out, col & ~63u, row0, z);
+}
+// 64 columns of float matrices' terms: the three parts one after the other
+template <uint32_t BOXES>
+__device__ __forceinline__ void send_parts(const Product& p, float* x, uint32_t row0, uint32_t col, Boxes<BOXES>& boxes) {
+  if (row0 >= p.m || col >= p.n) return;
+#pragma unroll 1
+  for (uint32_t part = 0; part < 3; ++part) {
+    boxes.next();
+    write_bf16(boxes.now(), 0, x);
+    write_bf16(boxes.now(), 1, x + 32);
+#pragma unroll
+    for (int i = 0; i < 64; ++i) x[i] -= __bfloat162float(__float2bfloat16_rn(x[i]));
+    boxes.template send<false>(&p.out, col, row0, part);
   }
 }
 
-// A gradient's tile.  Rows on the 16-byte grid are written by the thread that holds them;
-// the others through shared memory, so that a warp writes along a row.
-__device__ __forceinline__ void read_grad(const Product& p, uint32_t tmem, const Work& w, uint32_t row0, uint32_t col,
-                                          float* turn) {
-  const uint32_t lane = threadIdx.x & 31, r = row0 + lane, split = w.split;
+// 32 x 32 elements of a gradient, as boxes; rows off the 16-byte grid element by element, a
+// warp along a row
+template <uint32_t BOXES>
+__device__ __forceinline__ void send_grad(const Product& p, const float* x, uint32_t split, uint32_t row0, uint32_t col, uint32_t j,
+                                          Boxes<BOXES>& boxes) {
+  const uint32_t lane = threadIdx.x & 31;
   const GradOut& g = p.grad;
-#pragma unroll 1
-  for (uint32_t j = 0; j < 4; ++j) {
-    const uint32_t c0 = col + 32 * j;
-    if (c0 >= p.n) break;
-    float v[32];
-    tc::tmem_load32(tmem + 32 * j, v);
-    if (w.k0 == w.k1) {   // a split of no stages (more splits than stages): nothing was multiplied
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    }
-    if (g.sums && r < p.m) {
-      // ld_sums is a multiple of 32: the chunk lies in the buffer
-      float4* at = reinterpret_cast<float4*>(g.sums + (size_t(split) * p.m + r) * g.ld_sums + c0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (g.add) {
-          const float4 s = at[i];
-          v[4 * i] += s.x;
-          v[4 * i + 1] += s.y;
-          v[4 * i + 2] += s.z;
-          v[4 * i + 3] += s.w;
-        }
-        if (g.keep) at[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      }
-    }
-    if (!g.out) continue;
-    if (g.wide && c0 + 32 <= p.n) {
-      if (r >= p.m) continue;
-      if (g.bf16) {
-        uint4* at = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) + size_t(r) * g.ld + c0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          at[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
-                             pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
-      } else {
-        float4* at = reinterpret_cast<float4*>(static_cast<float*>(g.out) + size_t(r) * g.ld + c0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) at[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      }
-      continue;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
-    __syncwarp();
-    const uint32_t rows = row0 < p.m ? min(32u, p.m - row0) : 0u;
-    if (c0 + lane < p.n)
-      for (uint32_t i = 0; i < rows; ++i) {
-        const float x = turn[i * 33 + lane];
-        const size_t at = size_t(row0 + i) * g.ld + c0 + lane;
-        if (g.bf16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(x);
-        else static_cast<float*>(g.out)[at] = x;
-      }
+  if (g.boxes && !g.f32) {
+    send_bf16(p, x, split, row0, col, j, boxes);
+    return;
   }
+  if (row0 >= p.m || col >= p.n) return;
+  boxes.next();
+  const uint32_t box = boxes.now();
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i)
+    box_write(box_piece(box, lane, i), __float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+              __float_as_uint(x[4 * i + 3]));
+  if (g.boxes) {
+    if (g.add) boxes.template send<true>(&p.out, col, row0, split);
+    else boxes.template send<false>(&p.out, col, row0, split);
+    return;
+  }
+  __syncwarp();
+  const uint32_t rows = min(32u, p.m - row0);
+  if (col + lane < p.n)
+    for (uint32_t i = 0; i < rows; ++i) {
+      float e;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e) : "r"(box_piece(box, i, lane >> 2) + 4 * (lane & 3)) : "memory");
+      const size_t at = size_t(row0 + i) * g.ld + col + lane;
+      if (g.f32) static_cast<float*>(g.at)[at] = e;
+      else static_cast<__nv_bfloat16*>(g.at)[at] = __float2bfloat16_rn(e);
+    }
+  __syncwarp();
 }
 
 // ---- the product kernel ----------------------------------------------------------------------
 
-template <int CTAS, Readout READ, bool A_MN, bool B_MN>
+template <int CTAS, Readout READ, bool CHAINS, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_constant__ Product p) {
-  using S = Stage<CTAS>;
+  using S = Stage<CTAS, READ>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;   // the swizzle's pattern repeats every 1024 bytes
-  float* const turned = reinterpret_cast<float*>(smem + (ring - smem_addr(smem)) + S::kCount * S::kBytes);
-  Ends& ends = *reinterpret_cast<Ends*>(turned + kReaders * 32 * 33);
+  const uint32_t boxes_at = ring + S::kCount * S::kBytes;
+  Ends& ends = *reinterpret_cast<Ends*>(smem + (boxes_at - smem_addr(smem)) + kReaders * S::kBoxes * kStore);
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? tc::cta_rank() : 0u;
   const uint32_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS, items = p.n_m * p.n_n * p.splits;
@@ -394,23 +459,28 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       constexpr uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, kTileN);
       uint32_t s = 0, phase = 0, n = 0;
       bool ok = true;
-      for (uint32_t t = first; ok && t < items; t += step, ++n) {
-        const Work w = work_of<CTAS>(p, t);
-        const uint32_t acc = n & 1u;
-        if (!(ok = mbar_wait(&ends.tile_empty[acc], ((n >> 1) & 1u) ^ 1u))) break;
-        tc::fence_after_sync();
+      bool ready = false;   // the next stage is known to have arrived
+      for (uint32_t t = first; ok && t < items; t += step) {
+        Work w;
+        stages_of(p, t, w);
         const uint32_t blocks = p.products * (w.k1 - w.k0);
-        for (uint32_t k = 0; k < blocks; ++k) {
-          if (!(ok = mbar_wait(&ends.full[s], phase))) break;
+        for (uint32_t k = 0; ok && k < blocks; ++n) {
+          const uint32_t acc = n & 1u, end = CHAINS ? min(blocks, k + kChain) : blocks;
+          if (!(ok = mbar_wait(&ends.tile_empty[acc], ((n >> 1) & 1u) ^ 1u))) break;
           tc::fence_after_sync();
-          const uint64_t a = tc::operand<A_MN>(ring + s * S::kBytes), b = tc::operand<B_MN>(ring + s * S::kBytes + S::kA);
+          for (bool add = false; k < end; ++k, add = true) {
+            if (!ready && !(ok = mbar_wait(&ends.full[s], phase))) break;
+            tc::fence_after_sync();
+            const uint64_t a = tc::operand<A_MN>(ring + s * S::kBytes), b = tc::operand<B_MN>(ring + s * S::kBytes + S::kA);
 #pragma unroll
-          for (uint32_t q = 0; q < kBlockK / 16; ++q)
-            tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, (k | q) != 0);
-          tc::commit<CTAS>(&ends.empty[s]);
-          if (++s == S::kCount) s = 0, phase ^= 1;
+            for (uint32_t q = 0; q < kBlockK / 16; ++q)
+              tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
+            tc::commit<CTAS>(&ends.empty[s]);
+            if (++s == S::kCount) s = 0, phase ^= 1;
+            ready = tc::mbar_test(&ends.full[s], phase);
+          }
+          if (ok) tc::commit<CTAS>(&ends.tile_full[acc]);
         }
-        if (ok) tc::commit<CTAS>(&ends.tile_full[acc]);
       }
       if (!ok) {
         record_error(p.status, CG_DEV_TIMEOUT);
@@ -420,35 +490,94 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
     }
   } else if (warp >= kFirstReader) {
     const uint32_t quarter = warp & 3u, half = (warp - kFirstReader) >> 2;
-    float* turn = turned + (warp - kFirstReader) * 32 * 33;
+    Boxes<S::kBoxes ? S::kBoxes : 1> boxes(boxes_at + (warp - kFirstReader) * S::kBoxes * kStore);
     uint32_t n = 0;
-    for (uint32_t t = first; t < items; t += step, ++n) {
-      const Work w = work_of<CTAS>(p, t);
-      const uint32_t acc = n & 1u, row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane;
-      const uint32_t col = w.n0 + half * 128;
-      uint32_t words[4], target = 0xFFFFFFFFu;
-      RowTerms terms;
-      if (READ != kOut) {
-        mask_words(p, r, col, words);
-        if (r < p.m) target = p.target[r];
-        if (READ == kTerms) terms = row_terms(p, r, target);
-      }
-      if (!mbar_wait(&ends.tile_full[acc], (n >> 1) & 1u)) {
-        record_error(p.status, CG_DEV_TIMEOUT);
-        break;
-      }
-      tc::fence_after_sync();
-      const uint32_t at = tmem + acc * kTileN + half * 128 + ((quarter * 32) << 16);
-      if (READ == kLoss) read_loss(p, at, r, col, target, words);
-      else if (READ == kTerms) read_terms(p, at, r, col, target, words, terms);
-      else read_grad(p, at, w, row0, col, turn);
+    const float c = exp_scale(p.temp);
+    // frees the accumulator that has been read
+    auto done = [&](uint32_t acc) {
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         if (CTAS == 2) tc::arrive_at(tc::in_block(smem_addr(&ends.tile_empty[acc]), 0));
         else mbar_arrive(&ends.tile_empty[acc]);
       }
+    };
+    auto full = [&](uint32_t i) {
+      if (!mbar_wait(&ends.tile_full[i & 1u], (i >> 1) & 1u)) {
+        record_error(p.status, CG_DEV_TIMEOUT);
+        return false;
+      }
+      tc::fence_after_sync();
+      __syncwarp();
+      return true;
+    };
+    for (uint32_t t = first; t < items; t += step) {
+      const Work w = work_of<CTAS>(p, t);
+      const uint32_t row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane, col = w.n0 + half * 128;
+      const uint32_t blocks = p.products * (w.k1 - w.k0);
+      uint32_t words[4], target = CG_NO_TOKEN;
+      if (READ != kOut) {
+        mask_words(p, r, col, words);
+        if (r < p.m) target = p.target[r];
+      }
+      RowSum sum;
+      const RowTerms terms = READ == kTerms ? row_terms(p, r, target) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
+      auto read = [&](float* x, uint32_t j, uint32_t word) {
+        if (READ == kLoss) {
+          read_loss(p, x, r, col + 32 * j, target, word, c, sum);
+        } else if (READ == kTerms) {
+          set_terms(p, x, col + 32 * j, word, terms);
+          if (!CHAINS) send_bf16(p, x, 0, row0, col + 32 * j, j, boxes);
+          else if (j & 1u) send_parts(p, x - 32, row0, col + 32 * j - 32, boxes);   // with the 32 before
+        } else {
+          send_grad(p, x, w.split, row0, col + 32 * j, j, boxes);
+        }
+      };
+      const uint32_t at = tmem + half * 128 + ((quarter * 32) << 16);
+      if (CHAINS) {
+        // the chains' sums, added up in registers; none in a split without stages
+        float v[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i] = 0.f;
+        bool ok = true;
+        for (uint32_t k = 0; k < blocks; k += kChain, ++n) {
+          if (!(ok = full(n))) break;
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q) {
+            uint32_t x[32];
+            tc::tmem_load(at + (n & 1u) * kTileN + 32 * q, x);
+            tc::tmem_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[32 * q + i] += __uint_as_float(x[i]);
+          }
+          done(n & 1u);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) read(v + 32 * j, j, words[j]);
+      } else {
+        if (blocks && !full(n)) break;
+        const uint32_t acc = n & 1u;
+        n += blocks != 0;
+#pragma unroll 1
+        for (uint32_t j = 0; j < 4; ++j) {
+          uint32_t x[32];
+          float v[32];
+          tc::tmem_load(at + acc * kTileN + 32 * j, x);
+          tc::tmem_wait();
+          if (j == 3 && blocks) done(acc);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]);
+          if (!blocks) {   // a split without stages: nothing was multiplied
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+          read(v, j, j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3]);
+        }
+      }
+      if (READ == kLoss && r < p.m && col < p.n) p.loss.part[size_t((p.v0 + col) >> 7) * p.m + r] = make_float2(sum.m, sum.s);
     }
+    if (READ != kLoss && lane == 0) tc::stores_done();
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -458,12 +587,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
   if (warp == 2) tc::tmem_free<CTAS>(tmem);
 }
 
-template <int CTAS>
+template <int CTAS, Readout READ>
 constexpr size_t product_smem() {
-  return 1024 + size_t(Stage<CTAS>::kCount) * Stage<CTAS>::kBytes + size_t(kReaders) * 32 * 33 * 4 + sizeof(Ends);
+  using S = Stage<CTAS, READ>;
+  static_assert(S::kCount <= 7 && S::kCount >= 3, "barriers for the stages");
+  return 1024 + size_t(S::kCount) * S::kBytes + size_t(kReaders) * S::kBoxes * kStore + sizeof(Ends);
 }
-static_assert(product_smem<1>() <= size_t(kMaxSmem) && product_smem<2>() <= size_t(kMaxSmem),
-              "the ring, the turned blocks and the barriers fit a block's shared memory");
+static_assert(sizeof(Ends) <= 1024, "the ring, the boxes and the barriers fit a block's shared memory");
 
 // ---- joining the parts of a row --------------------------------------------------------------
 
@@ -611,9 +741,9 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
     p.at_part = take(size_t(tiles_of(V, 128)) * B * 8);
     p.at_target = take(size_t(B) * 4);
   } else {
-    p.ld_terms = up_to(p.piece, 32);
+    p.ld_terms = up_to(p.piece, 8);
     p.at_terms = take(size_t(p.parts) * B * p.ld_terms * 2);
-    p.ld_sums = up_to(D, 32);
+    p.ld_sums = up_to(D, 4);
     const uint32_t tiles = tiles_of(B, kBlockM * (p.pair ? 2 : 1)) * tiles_of(D, kTileN);
     const uint32_t slots = kHeadSms / (p.pair ? 2 : 1), blocks = tiles_of(p.piece, kBlockK);
     p.splits = std::max(1u, std::min(slots / std::max(tiles, 1u), blocks / 8));
@@ -623,16 +753,24 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   return p;
 }
 
+template <int CTAS, Readout READ, bool CHAINS, bool A_MN, bool B_MN>
+cudaError_t launch_product(int device, Product& p, cudaStream_t stream) {
+  p.n_m = tiles_of(p.m, kBlockM * CTAS);
+  p.n_n = tiles_of(p.n, kTileN);
+  return launch_clusters<product_kernel<CTAS, READ, CHAINS, A_MN, B_MN>>(
+      device, std::min(p.n_m * p.n_n * p.splits, kHeadSms / CTAS), CTAS, kHeadThreads, product_smem<CTAS, READ>(), stream, p);
+}
+// Rows in pairs of blocks above 128.  Results in 32 bits are summed in chains (losses, and all
+// that float matrices give): a long chain of sums in tensor memory drifts, as its steps are not
+// rounded to nearest.
 template <Readout READ, bool A_MN, bool B_MN>
 cudaError_t launch_product(int device, bool pair, Product& p, cudaStream_t stream) {
-  const uint32_t ctas = pair ? 2 : 1;
-  p.n_m = tiles_of(p.m, kBlockM * ctas);
-  p.n_n = tiles_of(p.n, kTileN);
-  const uint32_t at_once = std::min(p.n_m * p.n_n * p.splits, kHeadSms / ctas);
-  return pair ? launch_clusters<product_kernel<2, READ, A_MN, B_MN>>(device, at_once, 2, kHeadThreads, product_smem<2>(),
-                                                                      stream, p)
-              : launch_clusters<product_kernel<1, READ, A_MN, B_MN>>(device, at_once, 1, kHeadThreads, product_smem<1>(),
-                                                                      stream, p);
+  const bool chains = p.products > 1 || (READ == kLoss && p.blocks > kChain);
+  if (pair)
+    return chains ? launch_product<2, READ, true, A_MN, B_MN>(device, p, stream)
+                  : launch_product<2, READ, false, A_MN, B_MN>(device, p, stream);
+  return chains ? launch_product<1, READ, true, A_MN, B_MN>(device, p, stream)
+                : launch_product<1, READ, false, A_MN, B_MN>(device, p, stream);
 }
 
 cudaError_t lay_out(bool f32, const void* from, uint64_t ld, uint32_t rows, uint32_t D, uint32_t Dp, void* to,
@@ -720,6 +858,15 @@ int head_loss(cg_ctx* c, const HeadArgs& a, float* loss, float* lse, float* norm
              : CG_E_CUDA;
 }
 
+// where a product's elements go: [rows][ld] at `to`
+bool grad_out(Product& g, void* to, uint32_t rows, uint64_t ld, int dtype) {
+  g.grad.f32 = dtype == CG_F32;
+  g.grad.boxes = rows_on_grid(to, dtype, ld);
+  g.grad.at = to;
+  g.grad.ld = ld;
+  return !g.grad.boxes || tc::make_map(&g.out, to, g.n, rows, 1, ld, ld, 32, g.grad.f32);
+}
+
 int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm, const float* up, void* dh, uint64_t ld_dh,
               void* dw, uint64_t ld_dw, unsigned char* ws) {
   DeviceGuard dg(ctx_device(c), "cg_head_grad");
@@ -740,6 +887,9 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
   }
   __nv_bfloat16* terms = reinterpret_cast<__nv_bfloat16*>(ws + p.at_terms);
   const uint64_t part_stride = uint64_t(p.B) * p.ld_terms;
+  // the hidden rows' gradient is summed over pieces and splits in 32 bits where there are several
+  const bool summed = p.splits > 1 || p.piece < p.V;
+  float* sums = reinterpret_cast<float*>(ws + p.at_sums);
   for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, p.V - v0);
     if (p.lay_w) {
@@ -750,8 +900,10 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
     }
     const uint32_t w_rows = p.lay_w ? n : p.V;
     Product q = logits_of(a, p, v, v0, n);
-    q.terms = TermsOut{terms, p.ld_terms, part_stride, loss, norm, up};
-    if (!map_h(&q.a, p, o, 128) || !map_w(&q.b, p, o, w_rows, 128)) return CG_E_CUDA;
+    q.terms = TermsOut{loss, norm, up};
+    if (!map_h(&q.a, p, o, 128) || !map_w(&q.b, p, o, w_rows, 128) ||
+        !tc::make_map(&q.out, terms, n, p.B, p.parts, p.ld_terms, part_stride, 32))
+      return CG_E_CUDA;
     if (launch_product<kTerms, false, false>(dev, p.pair, q, v.stream) != cudaSuccess) return CG_E_CUDA;
     if (dh) {  // terms [B][n] x W [n][D], summed over the pieces
       Product g = {};
@@ -762,15 +914,13 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
       g.products = p.products;
       g.b_k = p.lay_w ? 0 : int(v0);
       g.status = v.t.status;
-      const bool last = v0 + n == p.V, alone = p.splits == 1 && p.piece == p.V;
-      g.grad.sums = alone ? nullptr : reinterpret_cast<float*>(ws + p.at_sums);
-      g.grad.ld_sums = p.ld_sums;
-      g.grad.add = v0 != 0;
-      g.grad.keep = !last || p.splits > 1;
-      g.grad.out = last && p.splits == 1 ? dh : nullptr;
-      g.grad.ld = ld_dh;
-      g.grad.bf16 = !f32;
-      g.grad.wide = rows_on_grid(dh, a.dtype, ld_dh);
+      if (summed) {
+        g.grad.boxes = g.grad.f32 = true;
+        g.grad.add = v0 != 0;
+        if (!tc::make_map(&g.out, sums, p.D, p.B, p.splits, p.ld_sums, uint64_t(p.B) * p.ld_sums, 32, true)) return CG_E_CUDA;
+      } else if (!grad_out(g, dh, p.B, ld_dh, a.dtype)) {
+        return CG_E_CUDA;
+      }
       if (!tc::make_map(&g.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 128) || !map_w(&g.b, p, o, w_rows, 64))
         return CG_E_CUDA;
       if (launch_product<kOut, false, true>(dev, p.pair, g, v.stream) != cudaSuccess) return CG_E_CUDA;
@@ -783,18 +933,14 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
       g.splits = 1;
       g.products = p.products;
       g.status = v.t.status;
-      g.grad.out = static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size;
-      g.grad.ld = ld_dw;
-      g.grad.bf16 = !f32;
-      g.grad.wide = rows_on_grid(dw, a.dtype, ld_dw);
+      if (!grad_out(g, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
       if (!tc::make_map(&g.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&g.b, p, o, 64)) return CG_E_CUDA;
       if (launch_product<kOut, true, true>(dev, n > kBlockM, g, v.stream) != cudaSuccess) return CG_E_CUDA;
     }
   }
-  if (dh && p.splits > 1 &&
+  if (dh && summed &&
       launch_dependent(join_grad_kernel, dim3(tiles_of(p.D, 256), p.B), dim3(256), 0, v.stream,
-                       reinterpret_cast<const float*>(ws + p.at_sums), p.ld_sums, p.splits, p.B, p.D, dh, ld_dh,
-                       !f32) != cudaSuccess)
+                       static_cast<const float*>(sums), p.ld_sums, p.splits, p.B, p.D, dh, ld_dh, !f32) != cudaSuccess)
     return CG_E_CUDA;
   return CG_OK;
 }
