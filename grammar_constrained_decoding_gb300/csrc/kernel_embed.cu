@@ -106,13 +106,15 @@ __global__ void __launch_bounds__(kLookThreads) look_kernel(const char* table, u
 // ---- sorting the positions by token ----------------------------------------------------------
 
 constexpr uint32_t kSortThreads = 1024, kSortWarps = 32, kSortBits = 9, kBins = 1u << kSortBits;
-constexpr uint32_t kSortMost = 8;   // blocks of the cluster
+constexpr uint32_t kSortMost = 16;  // blocks of the cluster
+constexpr uint32_t kSortKeep = 4;   // tiles whose keys a thread keeps between counting and moving
 
 struct SortArgs {
   const uint32_t* tokens;
   uint32_t N, V, passes;
   uint32_t* key[2];        // tokens in the order so far (V for a row without one)
   uint32_t* pos[2];        // and their positions; the sorted ones are in key[0], pos[0]
+  uint32_t* runs;          // the count of the runs to be joined, set to none
   uint32_t* status;
 };
 struct SortShared {
@@ -120,7 +122,7 @@ struct SortShared {
   uint32_t base[kBins];                     // where the next position of a digit goes
   uint32_t tile_base[kBins];                // ... as a tile begins
   uint32_t warp_sum[kSortWarps];
-  uint16_t mine[kSortWarps][kBins];         // a tile's digits by warp, then where the warp's begin
+  alignas(16) uint16_t mine[kSortWarps][kBins];         // a tile's digits by warp, then where the warp's begin
 };
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i, bool report) {
@@ -135,11 +137,18 @@ __device__ __forceinline__ uint32_t read_count(const uint32_t* count, uint32_t r
   return v;
 }
 
+__device__ __forceinline__ void clear_tile(SortShared& s) {
+  uint4* zero = reinterpret_cast<uint4*>(s.mine);
+#pragma unroll
+  for (uint32_t i = 0; i < sizeof(s.mine) / 16 / kSortThreads; ++i) zero[i * kSortThreads + threadIdx.x] = uint4{};
+}
+
 // A radix sort by one cluster, 9 bits a pass: each block counts the digits of its own
 // stretch of positions, learns from the others where its digits begin, and moves its
 // positions there tile by tile, in their order.
 __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
   const uint32_t n = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (rank == 0 && tid == 0) *a.runs = 0;
   const uint32_t each = (((a.N + n - 1) / n) + kSortThreads - 1) / kSortThreads * kSortThreads;
   const uint32_t from = min(a.N, rank * each), to = min(a.N, from + each);
   for (uint32_t pass = 0; pass < a.passes; ++pass) {
@@ -149,9 +158,24 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
     const uint32_t* const pos_in = odd ? a.pos[1] : a.pos[0];
     uint32_t* const key_out = odd ? a.key[0] : a.key[1];
     uint32_t* const pos_out = odd ? a.pos[0] : a.pos[1];
-    for (uint32_t i = tid; i < kBins; i += kSortThreads) s.count[i] = 0;
+    uint32_t kept[kSortKeep], kept_pos[kSortKeep];
+#pragma unroll
+    for (uint32_t q = 0; q < kSortKeep; ++q) {
+      const uint32_t i = from + q * kSortThreads + tid;
+      kept[q] = 0;
+      kept_pos[q] = i;
+      if (i < to) {
+        kept[q] = pass == 0 ? sort_key(a, i, true) : __ldcg(key_in + i);
+        if (pass) kept_pos[q] = __ldcg(pos_in + i);
+      }
+    }
+    if (tid < kBins) s.count[tid] = 0;
+    clear_tile(s);
     __syncthreads();
-    for (uint32_t i = from + tid; i < to; i += kSortThreads) {
+#pragma unroll
+    for (uint32_t q = 0; q < kSortKeep; ++q)
+      if (from + q * kSortThreads + tid < to) atomicAdd(&s.count[(kept[q] >> shift) & (kBins - 1)], 1u);
+    for (uint32_t i = from + kSortKeep * kSortThreads + tid; i < to; i += kSortThreads) {
       const uint32_t k = pass == 0 ? sort_key(a, i, true) : __ldcg(key_in + i);
       atomicAdd(&s.count[(k >> shift) & (kBins - 1)], 1u);
     }
@@ -161,8 +185,7 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
     if (tid < kBins) {
 #pragma unroll
       for (uint32_t r = 0; r < kSortMost; ++r) {
-        if (r >= n) break;
-        const uint32_t x = n == 1 ? s.count[tid] : read_count(&s.count[tid], r);
+        const uint32_t x = r >= n ? 0u : n == 1 ? s.count[tid] : read_count(&s.count[tid], r);
         all += x;
         if (r < rank) before += x;
       }
@@ -176,24 +199,28 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
     if (lane == 31) s.warp_sum[warp] = up;
     __syncthreads();
     if (tid < kBins) {
-      uint32_t lower = 0;
-      for (uint32_t w = 0; w < warp; ++w) lower += s.warp_sum[w];
-      s.base[tid] = lower + up - all + before;
+      const uint32_t w = lane < warp ? s.warp_sum[lane] : 0u;   // at most 16 warps of bins
+      s.base[tid] = __reduce_add_sync(0xFFFFFFFFu, w) + up - all + before;
     }
-    for (uint32_t tile = from; tile < to; tile += kSortThreads) {
-      uint32_t* zero = reinterpret_cast<uint32_t*>(s.mine);
-      for (uint32_t i = tid; i < kSortWarps * kBins / 2; i += kSortThreads) zero[i] = 0;
-      __syncthreads();
+#pragma unroll 1
+    for (uint32_t tile = from, q = 0; tile < to; tile += kSortThreads, ++q) {
       const uint32_t i = tile + tid;
       const bool there = i < to;
-      uint32_t k = 0, p = i;
-      if (there) {
+      uint32_t k = kept[0], p = kept_pos[0];
+#pragma unroll
+      for (uint32_t u = 1; u < kSortKeep; ++u)
+        if (q == u) k = kept[u], p = kept_pos[u];
+      if (q >= kSortKeep && there) {
         k = pass == 0 ? sort_key(a, i, false) : __ldcg(key_in + i);
-        if (pass) p = __ldcg(pos_in + i);
+        p = pass ? __ldcg(pos_in + i) : i;
       }
       const uint32_t digit = there ? (k >> shift) & (kBins - 1) : kBins + lane;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
       const uint32_t nth = __popc(same & ((1u << lane) - 1u));
+      if (q) {
+        clear_tile(s);
+        __syncthreads();
+      }
       if (there && nth == 0) s.mine[warp][digit] = uint16_t(__popc(same));
       __syncthreads();
       if (tid < kBins) {
@@ -273,7 +300,7 @@ constexpr size_t kSortSmem = sizeof(SortShared) > kZeroBytes ? sizeof(SortShared
 
 // ---- summing runs ------------------------------------------------------------------------------
 
-constexpr uint32_t kSumThreads = 128, kMostChunk = 32;
+constexpr uint32_t kSumThreads = 128, kMostChunk = 32, kMostShort = 2 * kMostChunk;
 
 struct SumArgs {
   const uint32_t* key;     // sorted tokens, V at the end for rows without one
@@ -287,6 +314,7 @@ struct SumArgs {
   uint64_t pitch_out;
   float* part;             // [chunks][2][ld_part]: what a chunk has of the run that began before it, and of the one that goes on
   uint32_t ld_part;
+  uint32_t* runs;          // how many runs are to be joined, and the chunks they begin in (in any order)
 };
 
 template <bool BF16, int BYTES>
@@ -302,43 +330,80 @@ __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t token, uint
   *at = E::put(x);
 }
 
+// How many keys right before, or from, `at` on equal the token: up to 64
+__device__ __forceinline__ uint32_t equal_before(const uint32_t* at, uint32_t token, uint32_t lane) {
+  const uint32_t a = __ballot_sync(0xFFFFFFFFu, *(at - 1 - int(lane)) == token);
+  if (a != 0xFFFFFFFFu) return __ffs(~a) - 1;
+  const uint32_t b = __ballot_sync(0xFFFFFFFFu, *(at - 33 - int(lane)) == token);
+  return 32 + (b != 0xFFFFFFFFu ? __ffs(~b) - 1 : 32);
+}
+__device__ __forceinline__ uint32_t equal_after(const uint32_t* at, uint32_t token, uint32_t lane) {
+  const uint32_t a = __ballot_sync(0xFFFFFFFFu, at[lane] == token);
+  if (a != 0xFFFFFFFFu) return __ffs(~a) - 1;
+  const uint32_t b = __ballot_sync(0xFFFFFFFFu, at[32 + lane] == token);
+  return 32 + (b != 0xFFFFFFFFu ? __ffs(~b) - 1 : 32);
+}
+
 // A block takes a chunk of the sorted positions and a slab of the columns, 16 bytes of a row
 // to a thread (several narrow vectors, a slab's width apart in threads)
 template <bool BF16, int BYTES>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   using E = Elems<BF16, BYTES>;
   using Vec = typename E::Vec;
-  constexpr uint32_t kAhead = 8, kCols = 16 / BYTES;
-  __shared__ uint32_t key[kMostChunk + 2], pos[kMostChunk];
+  constexpr uint32_t kAhead = 8, kCols = 16 / BYTES, kWindow = kMostChunk + 2 * kMostShort;
+  __shared__ uint32_t key[kWindow], pos[kMostChunk + kMostShort];
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t chunk = blockIdx.x / a.slabs;
+  const uint32_t chunk = blockIdx.x / a.slabs, lane = threadIdx.x & 31;
   const uint32_t col0 = (blockIdx.x - chunk * a.slabs) * kSumThreads * kCols + threadIdx.x;
   const uint32_t from = chunk * a.chunk, n = min(a.chunk, a.N - from);
-  for (uint32_t i = threadIdx.x; i < n + 2; i += kSumThreads) {
-    // key[i]: of position from + i - 1; past either end a value that no token has
-    const uint32_t at = from + i - 1;
-    key[i] = (i == 0 && from == 0) || at >= a.N ? CG_NO_TOKEN : a.key[at];
+  // key[i]: of position from + i - kMostShort; past either end a value that no token has
+  for (uint32_t i = threadIdx.x; i < n + 2 * kMostShort; i += kSumThreads) {
+    const uint32_t at = from + i - kMostShort;
+    key[i] = from + i < kMostShort || at >= a.N ? CG_NO_TOKEN : a.key[at];
   }
-  for (uint32_t i = threadIdx.x; i < n; i += kSumThreads) pos[i] = a.pos[from + i];
+  for (uint32_t i = threadIdx.x; i < n + kMostShort; i += kSumThreads) pos[i] = from + i < a.N ? a.pos[from + i] : 0u;
   __syncthreads();
+  // a run of up to two chunks is summed by the chunk it begins in: [begin, end) of the positions
+  // from `from` on
+  const uint32_t* const k0 = key + kMostShort;
+  const uint32_t most = 2 * a.chunk;
+  const uint32_t head = k0[0], tail = k0[n - 1];
+  const uint32_t before = equal_before(k0, head, lane), after = equal_after(k0 + n, tail, lane);
+  uint32_t begin = 0, end = n;
+  bool head_part = false, tail_part = false;   // longer ones in parts
+  if (before) {
+    const uint32_t here = equal_after(k0, head, lane);   // up to 64: enough to tell
+    head_part = before + here > most;
+    if (!head_part) begin = min(here, n);
+  }
+  if (after && begin < n) {
+    const uint32_t here = min(equal_before(k0 + n, tail, lane), n);
+    const bool whole = here == n && head == tail;           // the chunk is one run
+    if (!(whole && before)) {
+      tail_part = here + after > most;
+      if (!tail_part) end = n + after;
+    }
+  }
+  // a longer run is for the join: it begins here
+  if (tail_part && tail < a.V && threadIdx.x == 0 && blockIdx.x == chunk * a.slabs) a.runs[1 + atomicAdd(a.runs, 1u)] = chunk;
   if (col0 >= a.vecs) return;
   const char* in = a.grad + uint64_t(col0) * BYTES;
   float acc[kCols][E::kN] = {};
-  uint32_t began = 0;
-  for (uint32_t i0 = 0; i0 < n; i0 += kAhead) {
+  bool first = head_part;   // the run at hand began before the chunk
+  for (uint32_t i0 = begin; i0 < end; i0 += kAhead) {
     Vec v[kAhead][kCols];
 #pragma unroll
     for (uint32_t u = 0; u < kAhead; ++u)
 #pragma unroll
       for (uint32_t q = 0; q < kCols; ++q)
-        if (i0 + u < n && key[i0 + u + 1] < a.V && col0 + q * kSumThreads < a.vecs)
+        if (i0 + u < end && k0[i0 + u] < a.V && col0 + q * kSumThreads < a.vecs)
           v[u][q] = *reinterpret_cast<const Vec*>(in + pos[i0 + u] * a.pitch + q * (kSumThreads * BYTES));
 #pragma unroll
     for (uint32_t u = 0; u < kAhead; ++u) {
       const uint32_t i = i0 + u;
-      if (i >= n) break;
-      const uint32_t token = key[i + 1];
+      if (i >= end) break;
+      const uint32_t token = k0[i];
       if (token >= a.V) break;   // rows without a token come last
 #pragma unroll
       for (uint32_t q = 0; q < kCols; ++q) {
@@ -347,17 +412,16 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
 #pragma unroll
         for (int e = 0; e < E::kN; ++e) acc[q][e] += x[e];
       }
-      const bool goes_on = key[i + 2] == token;
-      if (goes_on && i + 1 < n) continue;
-      const bool before = began == 0 && key[0] == token;
+      if (i + 1 < end && k0[i + 1] == token) continue;
+      const bool part = first || (tail_part && i + 1 == n);
 #pragma unroll
       for (uint32_t q = 0; q < kCols; ++q) {
         const uint32_t col = col0 + q * kSumThreads;
         if (col < a.vecs) {
-          if (!before && !goes_on) {
+          if (!part) {
             write_sum<BF16, BYTES>(a, token, col, acc[q]);
           } else {
-            float* to = a.part + (size_t(chunk) * 2 + (before ? 0 : 1)) * a.ld_part + col * E::kN;
+            float* to = a.part + (size_t(chunk) * 2 + (first ? 0 : 1)) * a.ld_part + col * E::kN;
 #pragma unroll
             for (int e = 0; e < E::kN; ++e) to[e] = acc[q][e];
           }
@@ -365,38 +429,37 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
 #pragma unroll
         for (int e = 0; e < E::kN; ++e) acc[q][e] = 0.f;
       }
-      began = i + 1;
+      first = false;
     }
   }
 }
 
-constexpr uint32_t kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinColumns = 128, kJoinBlocks = 2048;
+constexpr uint32_t kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinColumns = 128;
 
-// A block takes a run that begins in its chunk and goes on, 128 columns at a time: the warps
-// take the chunks' sums in turn, and the warps' sums are added in their order
+// A block takes 128 columns of a run in turn: the warps take the chunks' sums in turn, and the
+// warps' sums are added in their order
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumArgs a, uint32_t D) {
   __shared__ float4 mine[kJoinWarps][32];
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t chunk = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t from = chunk * a.chunk, to = min(a.N, from + a.chunk);
-  if (to >= a.N) return;
-  const uint32_t token = a.key[to - 1];
-  if (token >= a.V || a.key[to] != token || (from > 0 && a.key[from - 1] == token)) return;
-  // the run's last chunk: the one after which the next does not begin with the token
-  uint32_t last = chunk + 1;
-  for (;;) {
-    const uint64_t at = (uint64_t(last) + 1 + lane) * a.chunk;
-    const uint32_t same = __ballot_sync(0xFFFFFFFFu, at < a.N && a.key[min(at, uint64_t(a.N - 1))] == token);
-    last += __ffs(~same) ? __ffs(~same) - 1 : 32;
-    if (same != 0xFFFFFFFFu) break;
-  }
-  for (uint32_t base = blockIdx.y * kJoinColumns; base < D; base += gridDim.y * kJoinColumns) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, across = (D + kJoinColumns - 1) / kJoinColumns;
+  const uint32_t items = a.runs[0] * across;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t run = item / across, base = (item - run * across) * kJoinColumns, chunk = a.runs[1 + run];
+    const uint32_t token = a.key[(chunk + 1) * a.chunk];   // it goes on into the next chunk
+    // the run's last chunk: the one after which the next does not begin with the token
+    uint32_t last = chunk + 1;
+    for (;;) {
+      const uint64_t at = (uint64_t(last) + 1 + lane) * a.chunk;
+      const uint32_t same = __ballot_sync(0xFFFFFFFFu, at < a.N && a.key[min(at, uint64_t(a.N - 1))] == token);
+      last += __ffs(~same) ? __ffs(~same) - 1 : 32;
+      if (same != 0xFFFFFFFFu) break;
+    }
     const uint32_t col = base + 4 * lane;   // a part's rows are padded to whole groups of 4
     float4 s = {};
     if (col < D)
-#pragma unroll 4
+#pragma unroll 8
       for (uint32_t j = chunk + warp; j <= last; j += kJoinWarps) {
         const float4 x = *reinterpret_cast<const float4*>(a.part + (size_t(j) * 2 + (j == chunk ? 1 : 0)) * a.ld_part + col);
         s.x += x.x;
@@ -434,7 +497,7 @@ int vector_bytes(const void* x, uint64_t pitch_x, const void* y, uint64_t pitch_
 
 struct GradPlan {
   uint32_t chunk, chunks, ld_part;
-  size_t at_key[2], at_pos[2], at_part, bytes;
+  size_t at_key[2], at_pos[2], at_part, at_runs, bytes;
 };
 // Chunks of 32 positions, fewer where that leaves SMs without work.  Every width gets the same
 // chunks whatever its alignment, so that results do not depend on it.
@@ -456,6 +519,7 @@ GradPlan plan_grad(uint32_t N, uint32_t D, int dtype) {
     p.at_pos[i] = take(size_t(N) * 4);
   }
   p.at_part = take(size_t(p.chunks) * 2 * p.ld_part * 4);
+  p.at_runs = take((size_t(p.chunks) + 1) * 4);
   p.bytes = at;
   return p;
 }
@@ -483,8 +547,8 @@ cudaError_t launch_grad(int device, const SortArgs& sort, SumArgs sum, uint32_t 
   if (e != cudaSuccess) return e;
   e = launch_dependent(sum_kernel<BF16, BYTES>, dim3(chunks * sum.slabs), dim3(kSumThreads), 0, stream, sum);
   if (e != cudaSuccess || chunks < 2) return e;
-  const uint32_t across = std::max(1u, std::min(tiles_of(D, kJoinColumns), kJoinBlocks / chunks));
-  return launch_dependent(join_kernel<BF16>, dim3(chunks, across), dim3(kJoinThreads), 0, stream, sum, D);
+  return launch_dependent(join_kernel<BF16>, dim3(std::min(chunks * tiles_of(D, kJoinColumns), 4 * kEmbedSms)),
+                          dim3(kJoinThreads), 0, stream, sum, D);
 }
 
 template <typename F>
@@ -606,6 +670,7 @@ extern "C" int cg_embed_grad(cg_ctx* c, const void* d_grad, int dtype, uint32_t 
   sum.pitch_out = ld_out * size;
   sum.part = reinterpret_cast<float*>(ws + p.at_part);
   sum.ld_part = p.ld_part;
+  sum.runs = sort.runs = reinterpret_cast<uint32_t*>(ws + p.at_runs);
   const Grad f{ctx_device(c), sort, sum, p.chunks, D, v.stream};
   return by_vector(dtype, vector_bytes(d_grad, ld_grad * size, d_out_grad, ld_out * size, D * size), f) == cudaSuccess
              ? CG_OK

@@ -38,6 +38,7 @@ constexpr uint32_t kChain = 16;           // stages whose products are summed in
 constexpr uint32_t kStore = 4096;         // bytes of a box that a reader writes out: 32 rows of 128 bytes
 constexpr uint32_t kBand = 16;            // row tiles that are taken together over all columns
 constexpr uint32_t kBoxesEach = 1;
+constexpr uint32_t kReadBoxes = 13, kReadElements = 32;   // stages multiplied while a gradient's tile is read out
 constexpr uint32_t kHeadSms = 152;
 
 enum Readout { kLoss, kTerms, kOut };
@@ -73,8 +74,15 @@ struct Product {
   CUtensorMap a, b, out;     // operands; the terms or the gradient as they are written
   uint32_t m, n, n_m, n_n;   // extent, and in tiles
   uint32_t blocks, splits;   // stages of one product; splits of them
-  uint32_t products;         // 1, or 6 products of the parts
   int a_mn, a_k, b_mn, b_k;  // where the product begins in the maps
+  GradOut grad;
+};
+// What a launch computes: one product, or (kOut) the gradient by the hidden rows and the one
+// by the weight
+struct Job {
+  Product p[2];
+  uint32_t products;         // 1, or 6 products of the parts
+  uint32_t early;            // items of the second product that a pair without a last item of the first takes meanwhile
   // the rows' vocabulary side (kLoss, kTerms)
   const uint32_t* bitmask;
   uint32_t W, v0;            // words a row; the piece's first token
@@ -82,7 +90,6 @@ struct Product {
   float temp;
   LossOut loss;
   TermsOut terms;
-  GradOut grad;
   uint32_t* status;
 };
 
@@ -91,11 +98,40 @@ struct Ends {
   uint32_t tmem;
 };
 
+// The items of a launch, dealt out to `pairs` takers (blocks, or pairs of them) beforehand.  The
+// first product's (a tile, or a split of one) go round in turn; a taker without one in the last
+// round takes items of the second in that time, and from then on they go round.
+template <bool TWO>
+struct Turns {
+  uint32_t pair, pairs, extra, mine, items, early, nth = 0;
+  __device__ __forceinline__ Turns(const Job& j, uint32_t pair_, uint32_t pairs_) : pair(pair_), pairs(pairs_) {
+    const uint32_t first = j.p[0].n_m * j.p[0].n_n * j.p[0].splits;
+    mine = first / pairs;
+    extra = first - mine * pairs;
+    items = TWO ? j.p[1].n_m * j.p[1].n_n * j.p[1].splits : 0;
+    early = pair < extra ? 0 : j.early;
+    mine += pair < extra;
+    if (TWO) head = j.early * (pairs - extra);
+  }
+  uint32_t head = 0;
+  __device__ __forceinline__ bool next(bool& second, uint32_t& t) {
+    const uint32_t i = nth++;
+    second = i >= mine;
+    if (!second) {
+      t = pair + i * pairs;
+      return true;
+    }
+    if (!TWO) return false;
+    const uint32_t k = i - mine;
+    t = k < early ? k * (pairs - extra) + pair - extra : head + (k - early) * pairs + pair;
+    return t < items;
+  }
+};
+
 struct Work {
   uint32_t m0, n0, split, k0, k1;
 };
-// A work item's stages: all of them, or its split's.  (blocks * splits fits 32 bits: the
-// multiplying thread takes this between two tiles, while the tensor cores have nothing.)
+// An item's stages: all of them, or its split's (blocks * splits fits 32 bits)
 __device__ __forceinline__ void stages_of(const Product& p, uint32_t t, Work& w) {
   w.split = 0;
   w.k0 = 0;
@@ -135,13 +171,13 @@ __device__ __forceinline__ float logit(float x, bool allowed) {
 }
 
 // The allowed tokens of 128 columns from `col` on of row r of the piece, a word each 32
-__device__ __forceinline__ void mask_words(const Product& p, uint32_t r, uint32_t col, uint32_t (&words)[4]) {
+__device__ __forceinline__ void mask_words(const Job& job, uint32_t r, uint32_t col, uint32_t (&words)[4]) {
 #pragma unroll
   for (uint32_t j = 0; j < 4; ++j) {
     const uint32_t c = col + 32 * j;
-    uint32_t w = c + 32 <= p.n ? 0xFFFFFFFFu : c < p.n ? (1u << (p.n - c)) - 1u : 0u;
-    if (r >= p.m) w = 0;
-    if (w && p.bitmask) w &= p.bitmask[size_t(r) * p.W + ((p.v0 + c) >> 5)];
+    uint32_t w = c + 32 <= job.p[0].n ? 0xFFFFFFFFu : c < job.p[0].n ? (1u << (job.p[0].n - c)) - 1u : 0u;
+    if (r >= job.p[0].m) w = 0;
+    if (w && job.bitmask) w &= job.bitmask[size_t(r) * job.W + ((job.v0 + c) >> 5)];
     words[j] = w;
   }
 }
@@ -209,9 +245,9 @@ struct RowSum {
 };
 
 // 32 columns of a row's logits, from column `col` of the piece on
-__device__ __forceinline__ void read_loss(const Product& p, float* x, uint32_t r, uint32_t col, uint32_t target, uint32_t word,
+__device__ __forceinline__ void read_loss(const Job& job, float* x, uint32_t r, uint32_t col, uint32_t target, uint32_t word,
                                           float c, RowSum& sum) {
-  const uint32_t at = target - (p.v0 + col);
+  const uint32_t at = target - (job.v0 + col);
   if (at < 32) {   // the target is apart from the others
     float xt = 0.f;
 #pragma unroll
@@ -220,7 +256,7 @@ __device__ __forceinline__ void read_loss(const Product& p, float* x, uint32_t r
         xt = x[i];
         x[i] = -INFINITY;
       }
-    if (r < p.m) p.loss.target_logit[r] = logit(xt, (word >> at) & 1u);
+    if (r < job.p[0].m) job.loss.target_logit[r] = logit(xt, (word >> at) & 1u);
   }
   __syncwarp();
   sum.add(x, word, c);
@@ -263,20 +299,20 @@ struct RowTerms {
   float k, at_target;
   uint32_t target;           // CG_NO_TOKEN in a row that does not count
 };
-__device__ __forceinline__ RowTerms row_terms(const Product& p, uint32_t r, uint32_t target) {
-  const float c = exp_scale(p.temp);
-  if (r < p.m && target != CG_NO_TOKEN) {
-    const float loss = p.terms.loss[r], m = p.terms.norm[2 * size_t(r)], s = p.terms.norm[2 * size_t(r) + 1];
+__device__ __forceinline__ RowTerms row_terms(const Job& job, uint32_t r, uint32_t target) {
+  const float c = exp_scale(job.temp);
+  if (r < job.p[0].m && target != CG_NO_TOKEN) {
+    const float loss = job.terms.loss[r], m = job.terms.norm[2 * size_t(r)], s = job.terms.norm[2 * size_t(r) + 1];
     if (loss > 0.f) {   // a loss of 0: no target that counts, or nothing beside it
       const Scale t(c, m);
-      const float g = __fdiv_rn(p.terms.up ? p.terms.up[r] : 1.f, p.temp);
+      const float g = __fdiv_rn(job.terms.up ? job.terms.up[r] : 1.f, job.temp);
       return {t, __fdiv_rn(g, s) * t.rest, g * expm1f(-loss), target};
     }
   }
   return {Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};   // c = 0, k = 0: every term is 0
 }
 // turns 32 columns of a row's logits into its terms
-__device__ __forceinline__ void set_terms(const Product& p, float* x, uint32_t col, uint32_t word, const RowTerms& t) {
+__device__ __forceinline__ void set_terms(const Job& job, float* x, uint32_t col, uint32_t word, const RowTerms& t) {
   const float2 k2 = make_float2(t.k, t.k);
   const bool none = t.target == CG_NO_TOKEN;
   // as they are: all allowed, no row with a maximum out of the ordinary
@@ -302,7 +338,7 @@ __device__ __forceinline__ void set_terms(const Product& p, float* x, uint32_t c
       x[i + 1] = none ? 0.f : d.y;
     }
   }
-  const uint32_t at = t.target - (p.v0 + col);
+  const uint32_t at = t.target - (job.v0 + col);
   if (at < 32 && !none) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
@@ -379,8 +415,71 @@ __device__ __forceinline__ void send_grad(const Product& p, const float* x, uint
 
 // ---- the product kernel ----------------------------------------------------------------------
 
-template <int CTAS, Readout READ, bool CHAINS, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_constant__ Product p) {
+// where the copying or the multiplying thread is in the ring
+struct Place {
+  uint32_t s = 0, phase = 0;
+  template <uint32_t COUNT>
+  __device__ __forceinline__ void step() {
+    if (++s == COUNT) s = 0, phase ^= 1;
+  }
+};
+
+// An item's stages into the ring: a block brings its 128 rows of A and its share of B's 256.
+// With a pair the leader's barrier counts the bytes of both.
+template <int CTAS, typename S, bool A_MN, bool B_MN>
+__device__ __forceinline__ bool copy_item(const Job& job, const Product& p, const Work& w, uint32_t rank, uint32_t ring, Ends& ends,
+                                          Place& at, uint32_t& issued) {
+  const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * (kTileN / CTAS));
+  for (uint32_t i = 0; i < job.products; ++i) {
+    const int pa = int(part_a(job.products, i)), pb = int(part_b(job.products, i));
+    for (uint32_t k = w.k0; k < w.k1; ++k) {
+      if (!mbar_wait(&ends.empty[at.s], at.phase ^ 1)) return false;
+      const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[at.s]), 0) : smem_addr(&ends.full[at.s]);
+      if (rank == 0) mbar_expect_tx(&ends.full[at.s], S::kBytes * CTAS);
+      const uint32_t a = ring + at.s * S::kBytes, b = a + S::kA;
+      const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
+      if (A_MN)
+        for (uint32_t q = 0; q < kBlockM / 64; ++q) tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, pa, full);
+      else tc::copy_box<CTAS>(a, &p.a, ak, am, pa, full);
+      if (B_MN)
+        for (uint32_t q = 0; q < kTileN / CTAS / 64; ++q) tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, pb, full);
+      else
+        for (uint32_t q = 0; q < kTileN / CTAS / 128; ++q)
+          tc::copy_box<CTAS>(b + q * 16384, &p.b, bk, bn + int(128 * q), pb, full);
+      ++issued;
+      at.template step<S::kCount>();
+    }
+  }
+  return true;
+}
+
+// An item's products, chain after chain; n counts accumulators used
+template <int CTAS, typename S, bool CHAINS, bool A_MN, bool B_MN>
+__device__ __forceinline__ bool multiply_item(uint32_t blocks, uint32_t ring, uint32_t tmem, Ends& ends, Place& at, bool& ready,
+                                              uint32_t& n) {
+  constexpr uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, kTileN);
+  for (uint32_t k = 0; k < blocks; ++n) {
+    const uint32_t acc = n & 1u, end = CHAINS ? min(blocks, k + kChain) : blocks;
+    if (!mbar_wait(&ends.tile_empty[acc], ((n >> 1) & 1u) ^ 1u)) return false;
+    tc::fence_after_sync();
+    for (bool add = false; k < end; ++k, add = true) {
+      if (!ready && !mbar_wait(&ends.full[at.s], at.phase)) return false;
+      tc::fence_after_sync();
+      const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kA);
+#pragma unroll
+      for (uint32_t q = 0; q < kBlockK / 16; ++q)
+        tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
+      tc::commit<CTAS>(&ends.empty[at.s]);
+      at.template step<S::kCount>();
+      ready = tc::mbar_test(&ends.full[at.s], at.phase);
+    }
+    tc::commit<CTAS>(&ends.tile_full[acc]);
+  }
+  return true;
+}
+
+template <int CTAS, Readout READ, bool CHAINS>
+__global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_constant__ Job job) {
   using S = Stage<CTAS, READ>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;   // the swizzle's pattern repeats every 1024 bytes
@@ -388,7 +487,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
   Ends& ends = *reinterpret_cast<Ends*>(smem + (boxes_at - smem_addr(smem)) + kReaders * S::kBoxes * kStore);
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? tc::cta_rank() : 0u;
-  const uint32_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS, items = p.n_m * p.n_n * p.splits;
+  Turns<READ == kOut> turns(job, blockIdx.x / CTAS, gridDim.x / CTAS);
+  bool second;
+  uint32_t t;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S::kCount; ++s) {
@@ -411,79 +512,45 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
   griddep_wait();
 
   if (warp == 0) {
-    // the copies: a block brings its 128 rows of A and its share of B's 256.  With a pair
-    // the leader's barrier counts the bytes of both.
     if (lane == 0) {
       // what the kernel before wrote, as the copies see it
       asm volatile("fence.proxy.async;" ::: "memory");
-      tc::prefetch_map(&p.a);
-      tc::prefetch_map(&p.b);
-      uint32_t s = 0, phase = 0, issued = 0;
+      Place at;
+      uint32_t issued = 0;
       bool ok = true;
-      for (uint32_t t = first; ok && t < items; t += step) {
-        const Work w = work_of<CTAS>(p, t);
-        const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * (kTileN / CTAS));
-        for (uint32_t i = 0; ok && i < p.products; ++i) {
-          const int pa = int(part_a(p.products, i)), pb = int(part_b(p.products, i));
-          for (uint32_t k = w.k0; k < w.k1; ++k) {
-            if (!(ok = mbar_wait(&ends.empty[s], phase ^ 1))) break;
-            const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[s]), 0) : smem_addr(&ends.full[s]);
-            if (rank == 0) mbar_expect_tx(&ends.full[s], S::kBytes * CTAS);
-            const uint32_t a = ring + s * S::kBytes, b = a + S::kA;
-            const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
-            if (A_MN)
-              for (uint32_t q = 0; q < kBlockM / 64; ++q) tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, pa, full);
-            else tc::copy_box<CTAS>(a, &p.a, ak, am, pa, full);
-            if (B_MN)
-              for (uint32_t q = 0; q < kTileN / CTAS / 64; ++q)
-                tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, pb, full);
-            else
-              for (uint32_t q = 0; q < kTileN / CTAS / 128; ++q)
-                tc::copy_box<CTAS>(b + q * 16384, &p.b, bk, bn + int(128 * q), pb, full);
-            ++issued;
-            if (++s == S::kCount) s = 0, phase ^= 1;
-          }
+      while (ok && turns.next(second, t)) {
+        if (READ == kOut && second) {
+          ok = copy_item<CTAS, S, true, true>(job, job.p[1], work_of<CTAS>(job.p[1], t), rank, ring, ends, at, issued);
+        } else {
+          ok = copy_item<CTAS, S, false, READ == kOut>(job, job.p[0], work_of<CTAS>(job.p[0], t), rank, ring, ends, at, issued);
         }
       }
       if (!ok) {
-        record_error(p.status, CG_DEV_TIMEOUT);
+        record_error(job.status, CG_DEV_TIMEOUT);
         // what is still in flight lands before the block leaves
         for (uint32_t i = 0; rank == 0 && i < min(issued, S::kCount); ++i) {
-          if (s-- == 0) s = S::kCount - 1, phase ^= 1;
-          if (!mbar_wait(&ends.full[s], phase)) break;
+          if (at.s-- == 0) at.s = S::kCount - 1, at.phase ^= 1;
+          if (!mbar_wait(&ends.full[at.s], at.phase)) break;
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, kTileN);
-      uint32_t s = 0, phase = 0, n = 0;
-      bool ok = true;
-      bool ready = false;   // the next stage is known to have arrived
-      for (uint32_t t = first; ok && t < items; t += step) {
+      Place at;
+      uint32_t n = 0;
+      bool ok = true, ready = false;   // ready: the next stage is known to have arrived
+      while (ok && turns.next(second, t)) {
         Work w;
-        stages_of(p, t, w);
-        const uint32_t blocks = p.products * (w.k1 - w.k0);
-        for (uint32_t k = 0; ok && k < blocks; ++n) {
-          const uint32_t acc = n & 1u, end = CHAINS ? min(blocks, k + kChain) : blocks;
-          if (!(ok = mbar_wait(&ends.tile_empty[acc], ((n >> 1) & 1u) ^ 1u))) break;
-          tc::fence_after_sync();
-          for (bool add = false; k < end; ++k, add = true) {
-            if (!ready && !(ok = mbar_wait(&ends.full[s], phase))) break;
-            tc::fence_after_sync();
-            const uint64_t a = tc::operand<A_MN>(ring + s * S::kBytes), b = tc::operand<B_MN>(ring + s * S::kBytes + S::kA);
-#pragma unroll
-            for (uint32_t q = 0; q < kBlockK / 16; ++q)
-              tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
-            tc::commit<CTAS>(&ends.empty[s]);
-            if (++s == S::kCount) s = 0, phase ^= 1;
-            ready = tc::mbar_test(&ends.full[s], phase);
-          }
-          if (ok) tc::commit<CTAS>(&ends.tile_full[acc]);
+        if (READ == kOut && second) {
+          stages_of(job.p[1], t, w);
+          ok = multiply_item<CTAS, S, CHAINS, true, true>(job.products * (w.k1 - w.k0), ring, tmem, ends, at, ready, n);
+        } else {
+          stages_of(job.p[0], t, w);
+          ok = multiply_item<CTAS, S, CHAINS, false, READ == kOut>(job.products * (w.k1 - w.k0), ring, tmem, ends, at, ready, n);
         }
       }
       if (!ok) {
-        record_error(p.status, CG_DEV_TIMEOUT);
+        record_error(job.status, CG_DEV_TIMEOUT);
         tc::commit<CTAS>(&ends.drain);   // the instructions in flight end before tensor memory is given back
         mbar_wait(&ends.drain, 0);
       }
@@ -492,7 +559,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
     const uint32_t quarter = warp & 3u, half = (warp - kFirstReader) >> 2;
     Boxes<S::kBoxes ? S::kBoxes : 1> boxes(boxes_at + (warp - kFirstReader) * S::kBoxes * kStore);
     uint32_t n = 0;
-    const float c = exp_scale(p.temp);
+    const float c = exp_scale(job.temp);
     // frees the accumulator that has been read
     auto done = [&](uint32_t acc) {
       tc::fence_before_sync();
@@ -504,29 +571,29 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
     };
     auto full = [&](uint32_t i) {
       if (!mbar_wait(&ends.tile_full[i & 1u], (i >> 1) & 1u)) {
-        record_error(p.status, CG_DEV_TIMEOUT);
+        record_error(job.status, CG_DEV_TIMEOUT);
         return false;
       }
       tc::fence_after_sync();
       __syncwarp();
       return true;
     };
-    for (uint32_t t = first; t < items; t += step) {
+    auto read_item = [&](const Product& p) {
       const Work w = work_of<CTAS>(p, t);
       const uint32_t row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane, col = w.n0 + half * 128;
-      const uint32_t blocks = p.products * (w.k1 - w.k0);
+      const uint32_t blocks = job.products * (w.k1 - w.k0);
       uint32_t words[4], target = CG_NO_TOKEN;
       if (READ != kOut) {
-        mask_words(p, r, col, words);
-        if (r < p.m) target = p.target[r];
+        mask_words(job, r, col, words);
+        if (r < p.m) target = job.target[r];
       }
       RowSum sum;
-      const RowTerms terms = READ == kTerms ? row_terms(p, r, target) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
+      const RowTerms terms = READ == kTerms ? row_terms(job, r, target) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
       auto read = [&](float* x, uint32_t j, uint32_t word) {
         if (READ == kLoss) {
-          read_loss(p, x, r, col + 32 * j, target, word, c, sum);
+          read_loss(job, x, r, col + 32 * j, target, word, c, sum);
         } else if (READ == kTerms) {
-          set_terms(p, x, col + 32 * j, word, terms);
+          set_terms(job, x, col + 32 * j, word, terms);
           if (!CHAINS) send_bf16(p, x, 0, row0, col + 32 * j, j, boxes);
           else if (j & 1u) send_parts(p, x - 32, row0, col + 32 * j - 32, boxes);   // with the 32 before
         } else {
@@ -552,11 +619,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           }
           done(n & 1u);
         }
-        if (!ok) break;
+        if (!ok) return false;
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) read(v + 32 * j, j, words[j]);
       } else {
-        if (blocks && !full(n)) break;
+        if (blocks && !full(n)) return false;
         const uint32_t acc = n & 1u;
         n += blocks != 0;
 #pragma unroll 1
@@ -575,8 +642,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           read(v, j, j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3]);
         }
       }
-      if (READ == kLoss && r < p.m && col < p.n) p.loss.part[size_t((p.v0 + col) >> 7) * p.m + r] = make_float2(sum.m, sum.s);
-    }
+      if (READ == kLoss && r < p.m && col < p.n) job.loss.part[size_t((job.v0 + col) >> 7) * p.m + r] = make_float2(sum.m, sum.s);
+      return true;
+    };
+    // (each product read where it lies: through a pointer to either the gradients' tiles took a fifth longer)
+    bool ok = true;
+    while (ok && turns.next(second, t)) ok = READ == kOut && second ? read_item(job.p[1]) : read_item(job.p[0]);
     if (READ != kLoss && lane == 0) tc::stores_done();
   }
   __syncwarp();
@@ -608,28 +679,38 @@ __global__ void __launch_bounds__(1024) join_loss_kernel(const float2* part, con
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x * 32 + lane;
   const float c = exp_scale(T);
   float m = -INFINITY, s = 0.f;
-  if (b < B)
-    for (uint32_t g = warp; g < groups; g += 32) {
-      const float2 x = part[size_t(g) * B + b];
-      if (!(x.x > -INFINITY)) continue;
-      const float top = fmaxf(m, x.x);
-      s = s * ex2((m - top) * c) + x.y * ex2((x.x - top) * c);
+  if (b < B) {
+    constexpr uint32_t kAhead = 8;
+    for (uint32_t g0 = warp; g0 < groups; g0 += 32 * kAhead) {
+      float2 x[kAhead];
+      float top = m;
+#pragma unroll
+      for (uint32_t u = 0; u < kAhead; ++u) {
+        const uint32_t g = g0 + 32 * u;
+        x[u] = g < groups ? part[size_t(g) * B + b] : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (uint32_t u = 0; u < kAhead; ++u) top = fmaxf(top, x[u].x);
+      if (!(top > -INFINITY)) continue;
+      float add = 0.f;
+#pragma unroll
+      for (uint32_t u = 0; u < kAhead; ++u) add += x[u].y * ex2((x[u].x - top) * c);   // 0 times 0 for an empty group
+      s = s * (m > -INFINITY ? ex2((m - top) * c) : 0.f) + add;
       m = top;
     }
+  }
   mine[warp][lane] = make_float2(m, s);
   __syncthreads();
-  if (warp != 0 || b >= B) return;
-  for (uint32_t w = 1; w < 32; ++w) {
-    const float2 x = mine[w][lane];
-    if (!(x.x > -INFINITY)) continue;
-    const float top = fmaxf(m, x.x);
-    s = s * ex2((m - top) * c) + x.y * ex2((x.x - top) * c);
-    m = top;
-  }
+  // each warp joins a row's 32 entries, then the first thread of each finishes its row
+  const uint32_t row = blockIdx.x * 32 + warp;
+  const float2 part_of_row = mine[lane][warp];
+  m = warp_reduce(part_of_row.x, MaxOp());
+  s = warp_reduce(m > -INFINITY ? part_of_row.y * ex2((part_of_row.x - m) * c) : 0.f, SumOp());
+  if (lane != 0 || row >= B) return;
   // m, s: the others' maximum and sum; x: the target's logit
-  const uint32_t t = target[b];
+  const uint32_t t = target[row];
   if (t >= V && t != CG_NO_TOKEN) record_error(status, CG_DEV_BAD_TOKEN);
-  const float x = t < V ? target_logit[b] : -INFINITY;
+  const float x = t < V ? target_logit[row] : -INFINITY;
   float l = 0.f, M = m, rest = s;   // S = 1 + rest where the target is the maximum
   bool first = false;
   if (x > -INFINITY) {
@@ -647,50 +728,92 @@ __global__ void __launch_bounds__(1024) join_loss_kernel(const float2* part, con
       l = __fdiv_rn(m - x, T) + logf(rest);
     }
   }
-  loss[b] = l;
+  loss[row] = l;
   if (norm) {
-    norm[2 * size_t(b)] = M;
-    norm[2 * size_t(b) + 1] = first ? 1.f + rest : rest;
+    norm[2 * size_t(row)] = M;
+    norm[2 * size_t(row) + 1] = first ? 1.f + rest : rest;
   }
-  if (lse) lse[b] = M > -INFINITY ? __fdiv_rn(M, T) + (first ? log1pf(rest) : logf(rest)) : -INFINITY;
+  if (lse) lse[row] = M > -INFINITY ? __fdiv_rn(M, T) + (first ? log1pf(rest) : logf(rest)) : -INFINITY;
 }
 
-// The splits' sums of a gradient, in their order
-__global__ void __launch_bounds__(256) join_grad_kernel(const float* sums, uint64_t ld_sums, uint32_t splits, uint32_t m,
-                                                        uint32_t n, void* out, uint64_t ld, bool bf16) {
+// The splits' sums of a gradient, in their order: 4 columns to a thread
+__global__ void __launch_bounds__(256) join_grad_kernel(const float* sums, uint32_t ld_sums, uint32_t splits, uint32_t m,
+                                                        uint32_t n, void* out, uint64_t ld, bool bf16, bool wide) {
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t r = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.f;
-  for (uint32_t k = 0; k < splits; ++k) s += sums[(size_t(k) * m + r) * ld_sums + i];
-  if (bf16) static_cast<__nv_bfloat16*>(out)[size_t(r) * ld + i] = __float2bfloat16_rn(s);
-  else static_cast<float*>(out)[size_t(r) * ld + i] = s;
+  const uint32_t groups = ld_sums / 4;
+  const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+  const uint32_t r = uint32_t(i / groups), col = 4 * uint32_t(i - uint64_t(r) * groups);
+  if (r >= m || col >= n) return;
+  float4 s = {};
+#pragma unroll 4
+  for (uint32_t k = 0; k < splits; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(sums + (size_t(k) * m + r) * ld_sums + col);
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  const size_t at = size_t(r) * ld + col;
+  if (wide && col + 4 <= n) {
+    if (bf16) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
+    else *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
+    return;
+  }
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) {
+    if (col + e >= n) break;
+    if (bf16) static_cast<__nv_bfloat16*>(out)[at + e] = __float2bfloat16_rn(v[e]);
+    else static_cast<float*>(out)[at + e] = v[e];
+  }
 }
 
 // ---- operands that the copies cannot take as they lie ----------------------------------------
 
 // bf16 rows off the 16-byte grid are copied onto it; float rows are split into three parts
-// that add up to the value (8 bits each; a value that is not finite is its first part)
+// that add up to the value (8 bits each; a value that is not finite is its first part).  A
+// thread writes 8 columns at once; it reads them one by one where the rows' start or pitch
+// does not allow more.
 template <bool F32>
 __global__ void __launch_bounds__(256) lay_out_kernel(const void* from, uint64_t ld, uint32_t rows, uint32_t D, uint32_t Dp,
-                                                      __nv_bfloat16* to) {
+                                                      bool wide, __nv_bfloat16* to) {
   griddep_launch_dependents();
   griddep_wait();
-  const uint64_t n = uint64_t(rows) * Dp, step = uint64_t(gridDim.x) * 256;
-  for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
-    const uint64_t r = i / Dp;
-    const uint32_t d = uint32_t(i - r * Dp);
+  const uint32_t groups = Dp / 8;
+  const uint64_t all = uint64_t(rows) * groups, step = uint64_t(gridDim.x) * 256, n = uint64_t(rows) * Dp;
+  for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += step) {
+    const uint64_t r = all >> 32 ? i / groups : uint32_t(i) / groups;
+    const uint32_t d = uint32_t(i - r * groups) * 8;
     if (!F32) {
-      to[i] = d < D ? static_cast<const __nv_bfloat16*>(from)[r * ld + d] : __float2bfloat16_rn(0.f);
+      const uint16_t* x = static_cast<const uint16_t*>(from) + r * ld + d;
+      uint32_t w[4];
+#pragma unroll
+      for (uint32_t q = 0; q < 4; ++q)
+        w[q] = (d + 2 * q < D ? x[2 * q] : 0u) | (d + 2 * q + 1 < D ? uint32_t(x[2 * q + 1]) << 16 : 0u);
+      *reinterpret_cast<uint4*>(to + r * Dp + d) = make_uint4(w[0], w[1], w[2], w[3]);
       continue;
     }
-    float x = d < D ? static_cast<const float*>(from)[r * ld + d] : 0.f;
+    const float* x = static_cast<const float*>(from) + r * ld + d;
+    float v[8];
+    if (wide && d + 8 <= D) {
+      const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q) v[q] = d + q < D ? x[q] : 0.f;
+    }
 #pragma unroll
     for (int part = 0; part < 3; ++part) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(x);
-      to[uint64_t(part) * n + i] = h;
-      x = fabsf(x) <= FLT_MAX && fabsf(__bfloat162float(h)) <= FLT_MAX ? x - __bfloat162float(h) : 0.f;
+      uint32_t w[4];
+#pragma unroll
+      for (uint32_t q = 0; q < 4; ++q) w[q] = pack2(v[2 * q], v[2 * q + 1]);
+      *reinterpret_cast<uint4*>(to + uint64_t(part) * n + r * Dp + d) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q) {
+        const float h = __uint_as_float(q & 1u ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16);
+        v[q] = fabsf(v[q]) <= FLT_MAX && fabsf(h) <= FLT_MAX ? v[q] - h : 0.f;
+      }
     }
   }
 }
@@ -753,32 +876,38 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   return p;
 }
 
-template <int CTAS, Readout READ, bool CHAINS, bool A_MN, bool B_MN>
-cudaError_t launch_product(int device, Product& p, cudaStream_t stream) {
-  p.n_m = tiles_of(p.m, kBlockM * CTAS);
-  p.n_n = tiles_of(p.n, kTileN);
-  return launch_clusters<product_kernel<CTAS, READ, CHAINS, A_MN, B_MN>>(
-      device, std::min(p.n_m * p.n_n * p.splits, kHeadSms / CTAS), CTAS, kHeadThreads, product_smem<CTAS, READ>(), stream, p);
+template <int CTAS, Readout READ, bool CHAINS>
+cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
+  uint32_t items[2] = {0, 0}, longest[2] = {0, 0};
+  for (int i = 0; i < (READ == kOut ? 2 : 1); ++i) {
+    Product& p = j.p[i];
+    p.n_m = tiles_of(p.m, kBlockM * CTAS);
+    p.n_n = tiles_of(p.n, kTileN);
+    items[i] = p.n_m * p.n_n * p.splits;
+    // in stages; a tile of few is as long as it takes to read out and write
+    if (items[i]) longest[i] = std::max(tiles_of(p.blocks, p.splits) * j.products, p.grad.boxes ? kReadBoxes : kReadElements);
+  }
+  // what one item of the first product is worth in items of the second
+  j.early = longest[1] ? (longest[0] + longest[1] / 2) / longest[1] : 0;
+  return launch_clusters<product_kernel<CTAS, READ, CHAINS>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
+                                                             kHeadThreads, product_smem<CTAS, READ>(), stream, j);
 }
 // Rows in pairs of blocks above 128.  Results in 32 bits are summed in chains (losses, and all
 // that float matrices give): a long chain of sums in tensor memory drifts, as its steps are not
 // rounded to nearest.
-template <Readout READ, bool A_MN, bool B_MN>
-cudaError_t launch_product(int device, bool pair, Product& p, cudaStream_t stream) {
-  const bool chains = p.products > 1 || (READ == kLoss && p.blocks > kChain);
-  if (pair)
-    return chains ? launch_product<2, READ, true, A_MN, B_MN>(device, p, stream)
-                  : launch_product<2, READ, false, A_MN, B_MN>(device, p, stream);
-  return chains ? launch_product<1, READ, true, A_MN, B_MN>(device, p, stream)
-                : launch_product<1, READ, false, A_MN, B_MN>(device, p, stream);
+template <Readout READ>
+cudaError_t launch_job(int device, bool pair, Job& j, cudaStream_t stream) {
+  const bool chains = j.products > 1 || (READ == kLoss && j.p[0].blocks > kChain);
+  if (pair) return chains ? launch_job<2, READ, true>(device, j, stream) : launch_job<2, READ, false>(device, j, stream);
+  return chains ? launch_job<1, READ, true>(device, j, stream) : launch_job<1, READ, false>(device, j, stream);
 }
 
 cudaError_t lay_out(bool f32, const void* from, uint64_t ld, uint32_t rows, uint32_t D, uint32_t Dp, void* to,
                     cudaStream_t stream) {
-  const uint64_t n = uint64_t(rows) * Dp;
-  const dim3 grid(uint32_t(std::min<uint64_t>((n + 255) / 256, kHeadSms * 16)));
+  const uint64_t groups = uint64_t(rows) * (Dp / 8);
+  const dim3 grid(uint32_t(std::min<uint64_t>((groups + 255) / 256, kHeadSms * 16)));
   return launch_dependent(f32 ? lay_out_kernel<true> : lay_out_kernel<false>, grid, dim3(256), 0, stream, from, ld, rows, D,
-                          Dp, static_cast<__nv_bfloat16*>(to));
+                          Dp, rows_on_grid(from, f32 ? CG_F32 : CG_BF16, ld), static_cast<__nv_bfloat16*>(to));
 }
 
 struct HeadArgs {
@@ -806,21 +935,22 @@ bool map_w(CUtensorMap* map, const HeadPlan& p, const Operands& o, uint32_t rows
 }
 
 // x = H W^T of a piece, read out one way or the other
-Product logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v0, uint32_t n) {
-  Product q = {};
+Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v0, uint32_t n) {
+  Job j = {};
+  Product& q = j.p[0];
   q.m = p.B;
   q.n = n;
   q.blocks = tiles_of(p.D, kBlockK);
   q.splits = 1;
-  q.products = p.products;
   q.b_mn = p.lay_w ? 0 : int(v0);
-  q.bitmask = a.bitmask;
-  q.W = v.t.W;
-  q.v0 = v0;
-  q.target = a.target;
-  q.temp = a.temp;
-  q.status = v.t.status;
-  return q;
+  j.products = p.products;
+  j.bitmask = a.bitmask;
+  j.W = v.t.W;
+  j.v0 = v0;
+  j.target = a.target;
+  j.temp = a.temp;
+  j.status = v.t.status;
+  return j;
 }
 
 int head_loss(cg_ctx* c, const HeadArgs& a, float* loss, float* lse, float* norm, unsigned char* ws) {
@@ -844,11 +974,11 @@ int head_loss(cg_ctx* c, const HeadArgs& a, float* loss, float* lse, float* norm
       o.w = ws + p.at_w;
       o.ld_w = p.Dp;
     }
-    Product q = logits_of(a, p, v, v0, n);
-    q.loss.part = reinterpret_cast<float2*>(ws + p.at_part);
-    q.loss.target_logit = reinterpret_cast<float*>(ws + p.at_target);
-    if (!map_h(&q.a, p, o, 128) || !map_w(&q.b, p, o, p.lay_w ? n : p.V, 128)) return CG_E_CUDA;
-    if (launch_product<kLoss, false, false>(dev, p.pair, q, v.stream) != cudaSuccess) return CG_E_CUDA;
+    Job j = logits_of(a, p, v, v0, n);
+    j.loss.part = reinterpret_cast<float2*>(ws + p.at_part);
+    j.loss.target_logit = reinterpret_cast<float*>(ws + p.at_target);
+    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, p.lay_w ? n : p.V, 128)) return CG_E_CUDA;
+    if (launch_job<kLoss>(dev, p.pair, j, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
   return launch_dependent(join_loss_kernel, dim3(tiles_of(p.B, 32)), dim3(1024), 0, v.stream,
                           reinterpret_cast<const float2*>(ws + p.at_part),
@@ -899,48 +1029,49 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
       o.ld_w = p.Dp;
     }
     const uint32_t w_rows = p.lay_w ? n : p.V;
-    Product q = logits_of(a, p, v, v0, n);
-    q.terms = TermsOut{loss, norm, up};
-    if (!map_h(&q.a, p, o, 128) || !map_w(&q.b, p, o, w_rows, 128) ||
-        !tc::make_map(&q.out, terms, n, p.B, p.parts, p.ld_terms, part_stride, 32))
+    Job j = logits_of(a, p, v, v0, n);
+    j.terms = TermsOut{loss, norm, up};
+    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, w_rows, 128) ||
+        !tc::make_map(&j.p[0].out, terms, n, p.B, p.parts, p.ld_terms, part_stride, 32))
       return CG_E_CUDA;
-    if (launch_product<kTerms, false, false>(dev, p.pair, q, v.stream) != cudaSuccess) return CG_E_CUDA;
+    if (launch_job<kTerms>(dev, p.pair, j, v.stream) != cudaSuccess) return CG_E_CUDA;
+
+    Job g = {};
+    g.products = p.products;
+    g.temp = 1.f;
+    g.status = v.t.status;
     if (dh) {  // terms [B][n] x W [n][D], summed over the pieces
-      Product g = {};
-      g.m = p.B;
-      g.n = p.D;
-      g.blocks = tiles_of(n, kBlockK);
-      g.splits = p.splits;
-      g.products = p.products;
-      g.b_k = p.lay_w ? 0 : int(v0);
-      g.status = v.t.status;
+      Product& q = g.p[0];
+      q.m = p.B;
+      q.n = p.D;
+      q.blocks = tiles_of(n, kBlockK);
+      q.splits = p.splits;
+      q.b_k = p.lay_w ? 0 : int(v0);
       if (summed) {
-        g.grad.boxes = g.grad.f32 = true;
-        g.grad.add = v0 != 0;
-        if (!tc::make_map(&g.out, sums, p.D, p.B, p.splits, p.ld_sums, uint64_t(p.B) * p.ld_sums, 32, true)) return CG_E_CUDA;
-      } else if (!grad_out(g, dh, p.B, ld_dh, a.dtype)) {
+        q.grad.boxes = q.grad.f32 = true;
+        q.grad.add = v0 != 0;
+        if (!tc::make_map(&q.out, sums, p.D, p.B, p.splits, p.ld_sums, uint64_t(p.B) * p.ld_sums, 32, true)) return CG_E_CUDA;
+      } else if (!grad_out(q, dh, p.B, ld_dh, a.dtype)) {
         return CG_E_CUDA;
       }
-      if (!tc::make_map(&g.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 128) || !map_w(&g.b, p, o, w_rows, 64))
+      if (!tc::make_map(&q.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 128) || !map_w(&q.b, p, o, w_rows, 64))
         return CG_E_CUDA;
-      if (launch_product<kOut, false, true>(dev, p.pair, g, v.stream) != cudaSuccess) return CG_E_CUDA;
     }
     if (dw) {  // terms^T [n][B] x H [B][D]
-      Product g = {};
-      g.m = n;
-      g.n = p.D;
-      g.blocks = tiles_of(p.B, kBlockK);
-      g.splits = 1;
-      g.products = p.products;
-      g.status = v.t.status;
-      if (!grad_out(g, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
-      if (!tc::make_map(&g.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&g.b, p, o, 64)) return CG_E_CUDA;
-      if (launch_product<kOut, true, true>(dev, n > kBlockM, g, v.stream) != cudaSuccess) return CG_E_CUDA;
+      Product& q = g.p[1];
+      q.m = n;
+      q.n = p.D;
+      q.blocks = tiles_of(p.B, kBlockK);
+      q.splits = 1;
+      if (!grad_out(q, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
+      if (!tc::make_map(&q.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&q.b, p, o, 64)) return CG_E_CUDA;
     }
+    if (launch_job<kOut>(dev, p.pair, g, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
   if (dh && summed &&
-      launch_dependent(join_grad_kernel, dim3(tiles_of(p.D, 256), p.B), dim3(256), 0, v.stream,
-                       static_cast<const float*>(sums), p.ld_sums, p.splits, p.B, p.D, dh, ld_dh, !f32) != cudaSuccess)
+      launch_dependent(join_grad_kernel, dim3(tiles_of(p.B * (p.ld_sums / 4), 256)), dim3(256), 0, v.stream,
+                       static_cast<const float*>(sums), uint32_t(p.ld_sums), p.splits, p.B, p.D, dh, ld_dh, !f32,
+                       rows_on_grid(dh, a.dtype, ld_dh)) != cudaSuccess)
     return CG_E_CUDA;
   return CG_OK;
 }
