@@ -22,6 +22,7 @@ tokens, and a student's distillation loss (see distill() for autograd):
 from __future__ import annotations
 
 import ctypes as C
+import threading
 from dataclasses import dataclass
 
 import numpy as np
@@ -166,6 +167,7 @@ class Ctx:
             stream = torch.cuda.current_stream()
         self.stream = stream
         self._stream = stream.cuda_stream
+        self._kept = threading.local()  # a workspace for each thread's calls
         self._dev = torch.cuda.current_device()  # where the library creates the context
         self._rows = _rows  # an import in every call would be a twentieth of the smallest
         arr = (C.c_void_p * len(grammars))(*[g._h.value for g in grammars])

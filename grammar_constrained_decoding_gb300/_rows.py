@@ -44,9 +44,14 @@ def matrix_of(call: str, t, what: str, dtype, rows: int, dev: int = 0) -> tuple[
     return *rows_of(call, t, what, LOGITS if dtype is None else (dtype,), shape, dev), t.shape[1]
 
 
+KEPT_WORKSPACE = 64 << 20   # bytes: what a thread keeps between its calls; larger ones are allocated for each
+
+
 def workspace_of(ctx, call: str, given, nbytes: int):
-    """A u8 tensor of at least nbytes of device memory: the caller's, or a new one that belongs to the context's
-    stream; None where nothing is needed."""
+    """A u8 tensor of at least nbytes of device memory: the caller's; or the one that this thread's calls on the
+    context's stream have kept (allocating in every call costs as much host time as a small call itself); or a
+    new one, which belongs to the context's stream: in a graph capture, which has to own what its replays use,
+    for a stream that is not torch's current one, and for large calls.  None where nothing is needed."""
     if not nbytes:
         return None
     if given is not None:
@@ -54,7 +59,12 @@ def workspace_of(ctx, call: str, given, nbytes: int):
         if given.numel() < nbytes:
             raise L.CgError(call, L.CG_E_ARG, f"workspace: {nbytes} bytes are wanted")
         return given
-    if torch.cuda.current_stream(ctx._dev).cuda_stream == ctx._stream:
+    if torch.cuda.current_stream(ctx._dev).cuda_stream != ctx._stream:
+        with torch.cuda.stream(ctx.stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
+    if nbytes > KEPT_WORKSPACE or torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
-    with torch.cuda.stream(ctx.stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
+    kept = getattr(ctx._kept, "workspace", None)
+    if kept is None or kept.numel() < nbytes:
+        kept = ctx._kept.workspace = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=ctx._dev)
+    return kept

@@ -344,13 +344,13 @@ __device__ __forceinline__ uint32_t equal_after(const uint32_t* at, uint32_t tok
   return 32 + (b != 0xFFFFFFFFu ? __ffs(~b) - 1 : 32);
 }
 
-// A block takes a chunk of the sorted positions and a slab of the columns, 16 bytes of a row
-// to a thread (several narrow vectors, a slab's width apart in threads)
-template <bool BF16, int BYTES>
+// A block takes a chunk of the sorted positions and a slab of the columns: kCols vectors of a
+// row to a thread, 128 vectors apart (rows of more than 128 narrow vectors: 16 bytes in all)
+template <bool BF16, int BYTES, uint32_t kCols>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   using E = Elems<BF16, BYTES>;
   using Vec = typename E::Vec;
-  constexpr uint32_t kAhead = 8, kCols = 16 / BYTES, kWindow = kMostChunk + 2 * kMostShort;
+  constexpr uint32_t kAhead = 8, kWindow = kMostChunk + 2 * kMostShort;
   __shared__ uint32_t key[kWindow], pos[kMostChunk + kMostShort];
   griddep_launch_dependents();
   griddep_wait();
@@ -537,7 +537,8 @@ cudaError_t launch_look(const void* table, uint64_t pitch, const uint32_t* token
 template <bool BF16, int BYTES>
 cudaError_t launch_grad(int device, const SortArgs& sort, SumArgs sum, uint32_t chunks, uint32_t D, cudaStream_t stream) {
   sum.vecs = uint32_t(uint64_t(D) * (BF16 ? 2 : 4) / BYTES);
-  sum.slabs = tiles_of(sum.vecs, kSumThreads * (16 / BYTES));
+  const uint32_t cols = sum.vecs > kSumThreads ? 16 / BYTES : 1;
+  sum.slabs = tiles_of(sum.vecs, kSumThreads * cols);
   uint32_t n = 1;
   while (n < kSortMost && sort.N > n * kSortThreads) n *= 2;
   // without zeros to write the sorting cluster is alone
@@ -545,7 +546,7 @@ cudaError_t launch_grad(int device, const SortArgs& sort, SumArgs sum, uint32_t 
   cudaError_t e = launch_clusters<sort_kernel<BYTES>>(device, clusters, n, kSortThreads, kSortSmem, stream, sort,
                                                      sum.add ? static_cast<char*>(nullptr) : sum.out, sum.pitch_out, sum.vecs);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(sum_kernel<BF16, BYTES>, dim3(chunks * sum.slabs), dim3(kSumThreads), 0, stream, sum);
+  e = launch_dependent(cols == 1 ? sum_kernel<BF16, BYTES, 1> : sum_kernel<BF16, BYTES, 16 / BYTES>, dim3(chunks * sum.slabs), dim3(kSumThreads), 0, stream, sum);
   if (e != cudaSuccess || chunks < 2) return e;
   return launch_dependent(join_kernel<BF16>, dim3(std::min(chunks * tiles_of(D, kJoinColumns), 4 * kEmbedSms)),
                           dim3(kJoinThreads), 0, stream, sum, D);

@@ -42,6 +42,12 @@ constexpr uint32_t kReadBoxes = 13, kReadElements = 32;   // stages multiplied w
 constexpr uint32_t kHeadSms = 152;
 
 enum Readout { kLoss, kTerms, kOut };
+// How a tile's stages are summed: bf16 products in one accumulator (and the next tile's in
+// the other); in chains of 16 stages, added up in registers; or float matrices' six products a
+// stage, in chains, the five small ones in an accumulator of their own (in the large one's they
+// would each cost a step that is not rounded to nearest).
+enum Sums { kOne, kChains, kParts };
+constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : 1; }
 
 // a block's share of a stage, and how many fit beside the readers' boxes
 template <int CTAS, Readout READ>
@@ -81,7 +87,6 @@ struct Product {
 // by the weight
 struct Job {
   Product p[2];
-  uint32_t products;         // 1, or 6 products of the parts
   uint32_t early;            // items of the second product that a pair without a last item of the first takes meanwhile
   // the rows' vocabulary side (kLoss, kTerms)
   const uint32_t* bitmask;
@@ -155,9 +160,9 @@ __device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {
   w.n0 *= kTileN;
   return w;
 }
-// the parts of the i-th of the six products, the smallest products first
-__device__ __forceinline__ uint32_t part_a(uint32_t products, uint32_t i) { return products == 1 ? 0u : (0x001012u >> (4 * i)) & 15u; }
-__device__ __forceinline__ uint32_t part_b(uint32_t products, uint32_t i) { return products == 1 ? 0u : (0x010210u >> (4 * i)) & 15u; }
+// the parts of the i-th of the six products of a stage; the last is the largest
+__device__ __forceinline__ uint32_t part_a(uint32_t i) { return (0x001012u >> (4 * i)) & 15u; }
+__device__ __forceinline__ uint32_t part_b(uint32_t i) { return (0x010210u >> (4 * i)) & 15u; }
 
 // ---- reading a tile out ----------------------------------------------------------------------
 
@@ -402,14 +407,23 @@ __device__ __forceinline__ void send_grad(const Product& p, const float* x, uint
   }
   __syncwarp();
   const uint32_t rows = min(32u, p.m - row0);
-  if (col + lane < p.n)
-    for (uint32_t i = 0; i < rows; ++i) {
-      float e;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e) : "r"(box_piece(box, i, lane >> 2) + 4 * (lane & 3)) : "memory");
-      const size_t at = size_t(row0 + i) * g.ld + col + lane;
-      if (g.f32) static_cast<float*>(g.at)[at] = e;
-      else static_cast<__nv_bfloat16*>(g.at)[at] = __float2bfloat16_rn(e);
+  if (col + lane < p.n) {
+    const uint32_t from = 4 * (lane & 3);
+    size_t at = size_t(row0) * g.ld + col + lane;
+#pragma unroll 1
+    for (uint32_t i = 0; i < rows; i += 8) {   // eight rows' elements on their way together
+      float e[8];
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u)
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[u]) : "r"(box_piece(box, i + u, lane >> 2) + from) : "memory");
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u, at += g.ld) {
+        if (i + u >= rows) break;
+        if (g.f32) static_cast<float*>(g.at)[at] = e[u];
+        else static_cast<__nv_bfloat16*>(g.at)[at] = __float2bfloat16_rn(e[u]);
+      }
     }
+  }
   __syncwarp();
 }
 
@@ -425,19 +439,20 @@ struct Place {
 };
 
 // An item's stages into the ring: a block brings its 128 rows of A and its share of B's 256.
-// With a pair the leader's barrier counts the bytes of both.
-template <int CTAS, typename S, bool A_MN, bool B_MN>
-__device__ __forceinline__ bool copy_item(const Job& job, const Product& p, const Work& w, uint32_t rank, uint32_t ring, Ends& ends,
-                                          Place& at, uint32_t& issued) {
+// With a pair the leader's barrier counts the bytes of both.  Six products of a stage follow
+// one another: the parts that they share come from L2.
+template <int CTAS, typename S, Sums SUMS, bool A_MN, bool B_MN>
+__device__ __forceinline__ bool copy_item(const Product& p, const Work& w, uint32_t rank, uint32_t ring, Ends& ends, Place& at,
+                                          uint32_t& issued) {
   const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * (kTileN / CTAS));
-  for (uint32_t i = 0; i < job.products; ++i) {
-    const int pa = int(part_a(job.products, i)), pb = int(part_b(job.products, i));
-    for (uint32_t k = w.k0; k < w.k1; ++k) {
+  for (uint32_t k = w.k0; k < w.k1; ++k) {
+    const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
+    for (uint32_t i = 0; i < products_of(SUMS); ++i) {
+      const int pa = SUMS == kParts ? int(part_a(i)) : 0, pb = SUMS == kParts ? int(part_b(i)) : 0;
       if (!mbar_wait(&ends.empty[at.s], at.phase ^ 1)) return false;
       const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[at.s]), 0) : smem_addr(&ends.full[at.s]);
       if (rank == 0) mbar_expect_tx(&ends.full[at.s], S::kBytes * CTAS);
       const uint32_t a = ring + at.s * S::kBytes, b = a + S::kA;
-      const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
       if (A_MN)
         for (uint32_t q = 0; q < kBlockM / 64; ++q) tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, pa, full);
       else tc::copy_box<CTAS>(a, &p.a, ak, am, pa, full);
@@ -453,32 +468,40 @@ __device__ __forceinline__ bool copy_item(const Job& job, const Product& p, cons
   return true;
 }
 
-// An item's products, chain after chain; n counts accumulators used
-template <int CTAS, typename S, bool CHAINS, bool A_MN, bool B_MN>
+// An item's products, chain after chain; n counts the chains.  Chains take the two accumulators
+// in turn; the six products of a float matrices' stage take both.
+template <int CTAS, typename S, Sums SUMS, bool A_MN, bool B_MN>
 __device__ __forceinline__ bool multiply_item(uint32_t blocks, uint32_t ring, uint32_t tmem, Ends& ends, Place& at, bool& ready,
                                               uint32_t& n) {
   constexpr uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, kTileN);
   for (uint32_t k = 0; k < blocks; ++n) {
-    const uint32_t acc = n & 1u, end = CHAINS ? min(blocks, k + kChain) : blocks;
-    if (!mbar_wait(&ends.tile_empty[acc], ((n >> 1) & 1u) ^ 1u)) return false;
+    const uint32_t end = SUMS == kOne ? blocks : min(blocks, k + kChain);
+    const uint32_t acc = SUMS == kParts ? 0u : n & 1u, round = SUMS == kParts ? n : n >> 1;
+    if (!mbar_wait(&ends.tile_empty[acc], (round & 1u) ^ 1u)) return false;
     tc::fence_after_sync();
-    for (bool add = false; k < end; ++k, add = true) {
-      if (!ready && !mbar_wait(&ends.full[at.s], at.phase)) return false;
-      tc::fence_after_sync();
-      const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kA);
+    for (uint32_t begin = k; k < end; ++k) {
+#pragma unroll 1
+      for (uint32_t i = 0; i < products_of(SUMS); ++i) {
+        if (!ready && !mbar_wait(&ends.full[at.s], at.phase)) return false;
+        tc::fence_after_sync();
+        const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kA);
+        const bool large = SUMS != kParts || i + 1 == products_of(SUMS);
+        const bool add = k != begin || (SUMS == kParts && i != 0 && !large);
+        const uint32_t to = tmem + (SUMS == kParts && !large ? kTileN : acc * kTileN);
 #pragma unroll
-      for (uint32_t q = 0; q < kBlockK / 16; ++q)
-        tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
-      tc::commit<CTAS>(&ends.empty[at.s]);
-      at.template step<S::kCount>();
-      ready = tc::mbar_test(&ends.full[at.s], at.phase);
+        for (uint32_t q = 0; q < kBlockK / 16; ++q)
+          tc::mma<CTAS>(to, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
+        tc::commit<CTAS>(&ends.empty[at.s]);
+        at.template step<S::kCount>();
+        ready = tc::mbar_test(&ends.full[at.s], at.phase);
+      }
     }
     tc::commit<CTAS>(&ends.tile_full[acc]);
   }
   return true;
 }
 
-template <int CTAS, Readout READ, bool CHAINS>
+template <int CTAS, Readout READ, Sums SUMS>
 __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_constant__ Job job) {
   using S = Stage<CTAS, READ>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -520,9 +543,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       bool ok = true;
       while (ok && turns.next(second, t)) {
         if (READ == kOut && second) {
-          ok = copy_item<CTAS, S, true, true>(job, job.p[1], work_of<CTAS>(job.p[1], t), rank, ring, ends, at, issued);
+          ok = copy_item<CTAS, S, SUMS, true, true>(job.p[1], work_of<CTAS>(job.p[1], t), rank, ring, ends, at, issued);
         } else {
-          ok = copy_item<CTAS, S, false, READ == kOut>(job, job.p[0], work_of<CTAS>(job.p[0], t), rank, ring, ends, at, issued);
+          ok = copy_item<CTAS, S, SUMS, false, READ == kOut>(job.p[0], work_of<CTAS>(job.p[0], t), rank, ring, ends, at, issued);
         }
       }
       if (!ok) {
@@ -543,10 +566,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         Work w;
         if (READ == kOut && second) {
           stages_of(job.p[1], t, w);
-          ok = multiply_item<CTAS, S, CHAINS, true, true>(job.products * (w.k1 - w.k0), ring, tmem, ends, at, ready, n);
+          ok = multiply_item<CTAS, S, SUMS, true, true>(w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         } else {
           stages_of(job.p[0], t, w);
-          ok = multiply_item<CTAS, S, CHAINS, false, READ == kOut>(job.products * (w.k1 - w.k0), ring, tmem, ends, at, ready, n);
+          ok = multiply_item<CTAS, S, SUMS, false, READ == kOut>(w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         }
       }
       if (!ok) {
@@ -570,7 +593,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       }
     };
     auto full = [&](uint32_t i) {
-      if (!mbar_wait(&ends.tile_full[i & 1u], (i >> 1) & 1u)) {
+      if (!mbar_wait(&ends.tile_full[SUMS == kParts ? 0 : i & 1u], (SUMS == kParts ? i : i >> 1) & 1u)) {
         record_error(job.status, CG_DEV_TIMEOUT);
         return false;
       }
@@ -581,7 +604,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
     auto read_item = [&](const Product& p) {
       const Work w = work_of<CTAS>(p, t);
       const uint32_t row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane, col = w.n0 + half * 128;
-      const uint32_t blocks = job.products * (w.k1 - w.k0);
+      const uint32_t blocks = w.k1 - w.k0;
       uint32_t words[4], target = CG_NO_TOKEN;
       if (READ != kOut) {
         mask_words(job, r, col, words);
@@ -594,14 +617,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           read_loss(job, x, r, col + 32 * j, target, word, c, sum);
         } else if (READ == kTerms) {
           set_terms(job, x, col + 32 * j, word, terms);
-          if (!CHAINS) send_bf16(p, x, 0, row0, col + 32 * j, j, boxes);
+          if (SUMS != kParts) send_bf16(p, x, 0, row0, col + 32 * j, j, boxes);
           else if (j & 1u) send_parts(p, x - 32, row0, col + 32 * j - 32, boxes);   // with the 32 before
         } else {
           send_grad(p, x, w.split, row0, col + 32 * j, j, boxes);
         }
       };
       const uint32_t at = tmem + half * 128 + ((quarter * 32) << 16);
-      if (CHAINS) {
+      if (SUMS != kOne) {
         // the chains' sums, added up in registers; none in a split without stages
         float v[128];
 #pragma unroll
@@ -609,15 +632,22 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         bool ok = true;
         for (uint32_t k = 0; k < blocks; k += kChain, ++n) {
           if (!(ok = full(n))) break;
+          const uint32_t acc = SUMS == kParts ? 0u : n & 1u;
 #pragma unroll
           for (uint32_t q = 0; q < 4; ++q) {
             uint32_t x[32];
-            tc::tmem_load(at + (n & 1u) * kTileN + 32 * q, x);
+            if (SUMS == kParts) {   // the small ones first
+              tc::tmem_load(at + kTileN + 32 * q, x);
+              tc::tmem_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[32 * q + i] += __uint_as_float(x[i]);
+            }
+            tc::tmem_load(at + acc * kTileN + 32 * q, x);
             tc::tmem_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[32 * q + i] += __uint_as_float(x[i]);
           }
-          done(n & 1u);
+          done(acc);
         }
         if (!ok) return false;
 #pragma unroll
@@ -773,32 +803,54 @@ __global__ void __launch_bounds__(256) join_grad_kernel(const float* sums, uint3
 
 // bf16 rows off the 16-byte grid are copied onto it; float rows are split into three parts
 // that add up to the value (8 bits each; a value that is not finite is its first part).  A
-// thread writes 8 columns at once; it reads them one by one where the rows' start or pitch
-// does not allow more.
+// thread writes 8 columns at once.
+struct Layout {
+  const void* from;          // null: not this one
+  uint64_t ld;
+  uint32_t rows;
+  bool wide;                 // the rows lie on the 16-byte grid
+  __nv_bfloat16* to;         // [parts][rows][Dp]
+};
+struct Layouts {
+  Layout m[2];               // hidden, weight: blockIdx.y
+};
 template <bool F32>
-__global__ void __launch_bounds__(256) lay_out_kernel(const void* from, uint64_t ld, uint32_t rows, uint32_t D, uint32_t Dp,
-                                                      bool wide, __nv_bfloat16* to) {
+__global__ void __launch_bounds__(256) lay_out_kernel(const Layouts both, uint32_t D, uint32_t Dp) {
   griddep_launch_dependents();
   griddep_wait();
+  const Layout a = both.m[blockIdx.y];
   const uint32_t groups = Dp / 8;
-  const uint64_t all = uint64_t(rows) * groups, step = uint64_t(gridDim.x) * 256, n = uint64_t(rows) * Dp;
+  const uint64_t all = a.from ? uint64_t(a.rows) * groups : 0, step = uint64_t(gridDim.x) * 256, n = uint64_t(a.rows) * Dp;
   for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += step) {
     const uint64_t r = all >> 32 ? i / groups : uint32_t(i) / groups;
     const uint32_t d = uint32_t(i - r * groups) * 8;
     if (!F32) {
-      const uint16_t* x = static_cast<const uint16_t*>(from) + r * ld + d;
+      const uint16_t* x = static_cast<const uint16_t*>(a.from) + r * a.ld + d;
       uint32_t w[4];
+      if (d + 8 <= D) {
+        // whole words, shifted where the row begins in the middle of one (the halves beside it
+        // share a word with the row's own first or last element)
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(x) & ~uintptr_t(3));
+        const uint32_t shift = (reinterpret_cast<uintptr_t>(x) & 2u) * 8;
+        uint32_t word[5];
 #pragma unroll
-      for (uint32_t q = 0; q < 4; ++q)
-        w[q] = (d + 2 * q < D ? x[2 * q] : 0u) | (d + 2 * q + 1 < D ? uint32_t(x[2 * q + 1]) << 16 : 0u);
-      *reinterpret_cast<uint4*>(to + r * Dp + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (uint32_t q = 0; q < 4; ++q) word[q] = at[q];
+        word[4] = shift ? at[4] : 0u;
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) w[q] = __funnelshift_r(word[q], word[q + 1], shift);
+      } else {
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q)
+          w[q] = (d + 2 * q < D ? x[2 * q] : 0u) | (d + 2 * q + 1 < D ? uint32_t(x[2 * q + 1]) << 16 : 0u);
+      }
+      *reinterpret_cast<uint4*>(a.to + r * Dp + d) = make_uint4(w[0], w[1], w[2], w[3]);
       continue;
     }
-    const float* x = static_cast<const float*>(from) + r * ld + d;
+    const float* x = static_cast<const float*>(a.from) + r * a.ld + d;
     float v[8];
-    if (wide && d + 8 <= D) {
-      const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    if (a.wide && d + 8 <= D) {
+      const float4 lo = *reinterpret_cast<const float4*>(x), hi = *reinterpret_cast<const float4*>(x + 4);
+      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
     } else {
 #pragma unroll
       for (uint32_t q = 0; q < 8; ++q) v[q] = d + q < D ? x[q] : 0.f;
@@ -808,7 +860,7 @@ __global__ void __launch_bounds__(256) lay_out_kernel(const void* from, uint64_t
       uint32_t w[4];
 #pragma unroll
       for (uint32_t q = 0; q < 4; ++q) w[q] = pack2(v[2 * q], v[2 * q + 1]);
-      *reinterpret_cast<uint4*>(to + uint64_t(part) * n + r * Dp + d) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(a.to + uint64_t(part) * n + r * Dp + d) = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
       for (uint32_t q = 0; q < 8; ++q) {
         const float h = __uint_as_float(q & 1u ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16);
@@ -824,7 +876,7 @@ constexpr size_t kPieceBytes = size_t(256) << 20;  // of a piece's weight laid o
 
 // What a call works on, and where its workspace's parts lie
 struct HeadPlan {
-  uint32_t B, V, D, Dp, parts, products;
+  uint32_t B, V, D, Dp, parts;
   bool lay_h, lay_w;
   uint32_t piece;            // tokens of a piece: a multiple of 256 unless it is all of them
   uint64_t ld_terms, ld_sums;
@@ -842,7 +894,6 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   p.Dp = uint32_t(up_to(D, 8));
   const bool f32 = dtype == CG_F32;
   p.parts = f32 ? 3 : 1;
-  p.products = f32 ? 6 : 1;
   p.lay_h = f32 || !rows_on_grid(hidden, dtype, ld_h);
   p.lay_w = f32 || !rows_on_grid(weight, dtype, ld_w);
   p.pair = B > kBlockM;
@@ -876,7 +927,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   return p;
 }
 
-template <int CTAS, Readout READ, bool CHAINS>
+template <int CTAS, Readout READ, Sums SUMS>
 cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
   uint32_t items[2] = {0, 0}, longest[2] = {0, 0};
   for (int i = 0; i < (READ == kOut ? 2 : 1); ++i) {
@@ -885,29 +936,25 @@ cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
     p.n_n = tiles_of(p.n, kTileN);
     items[i] = p.n_m * p.n_n * p.splits;
     // in stages; a tile of few is as long as it takes to read out and write
-    if (items[i]) longest[i] = std::max(tiles_of(p.blocks, p.splits) * j.products, p.grad.boxes ? kReadBoxes : kReadElements);
+    if (items[i]) longest[i] = std::max(tiles_of(p.blocks, p.splits) * products_of(SUMS), p.grad.boxes ? kReadBoxes : kReadElements);
   }
   // what one item of the first product is worth in items of the second
   j.early = longest[1] ? (longest[0] + longest[1] / 2) / longest[1] : 0;
-  return launch_clusters<product_kernel<CTAS, READ, CHAINS>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
+  return launch_clusters<product_kernel<CTAS, READ, SUMS>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
                                                              kHeadThreads, product_smem<CTAS, READ>(), stream, j);
 }
 // Rows in pairs of blocks above 128.  Results in 32 bits are summed in chains (losses, and all
 // that float matrices give): a long chain of sums in tensor memory drifts, as its steps are not
-// rounded to nearest.
-template <Readout READ>
-cudaError_t launch_job(int device, bool pair, Job& j, cudaStream_t stream) {
-  const bool chains = j.products > 1 || (READ == kLoss && j.p[0].blocks > kChain);
-  if (pair) return chains ? launch_job<2, READ, true>(device, j, stream) : launch_job<2, READ, false>(device, j, stream);
-  return chains ? launch_job<1, READ, true>(device, j, stream) : launch_job<1, READ, false>(device, j, stream);
+// rounded to nearest (the loss of 256 x 128256 x 4096 in one chain 2.2e-6 off, in chains 4.6e-7).
+template <int CTAS, Readout READ>
+cudaError_t launch_job(int device, bool f32, Job& j, cudaStream_t stream) {
+  if (f32) return launch_job<CTAS, READ, kParts>(device, j, stream);
+  if (READ == kLoss && j.p[0].blocks > kChain) return launch_job<CTAS, READ, READ == kLoss ? kChains : kOne>(device, j, stream);
+  return launch_job<CTAS, READ, kOne>(device, j, stream);
 }
-
-cudaError_t lay_out(bool f32, const void* from, uint64_t ld, uint32_t rows, uint32_t D, uint32_t Dp, void* to,
-                    cudaStream_t stream) {
-  const uint64_t groups = uint64_t(rows) * (Dp / 8);
-  const dim3 grid(uint32_t(std::min<uint64_t>((groups + 255) / 256, kHeadSms * 16)));
-  return launch_dependent(f32 ? lay_out_kernel<true> : lay_out_kernel<false>, grid, dim3(256), 0, stream, from, ld, rows, D,
-                          Dp, rows_on_grid(from, f32 ? CG_F32 : CG_BF16, ld), static_cast<__nv_bfloat16*>(to));
+template <Readout READ>
+cudaError_t launch_job(int device, const HeadPlan& p, Job& j, cudaStream_t stream) {
+  return p.pair ? launch_job<2, READ>(device, p.parts > 1, j, stream) : launch_job<1, READ>(device, p.parts > 1, j, stream);
 }
 
 struct HeadArgs {
@@ -927,6 +974,31 @@ struct Operands {
   const void* w;
   uint64_t ld_h, ld_w;
 };
+// The hidden rows (with the first piece) and a piece's n rows of the weight from v0 on, laid out
+// where that is needed
+cudaError_t lay_out(const HeadArgs& a, const HeadPlan& p, uint32_t v0, uint32_t n, unsigned char* ws, Operands& o,
+                    cudaStream_t stream) {
+  const bool f32 = a.dtype == CG_F32;
+  Layouts both = {};
+  uint32_t rows = 0;
+  if (p.lay_h && v0 == 0) {
+    both.m[0] = Layout{a.hidden, a.ld_h, p.B, rows_on_grid(a.hidden, a.dtype, a.ld_h),
+                       reinterpret_cast<__nv_bfloat16*>(ws + p.at_h)};
+    o.h = ws + p.at_h;
+    o.ld_h = p.Dp;
+    rows = p.B;
+  }
+  if (p.lay_w) {
+    both.m[1] = Layout{static_cast<const char*>(a.weight) + uint64_t(v0) * a.ld_w * dtype_size(a.dtype), a.ld_w, n,
+                       rows_on_grid(a.weight, a.dtype, a.ld_w), reinterpret_cast<__nv_bfloat16*>(ws + p.at_w)};
+    o.w = ws + p.at_w;
+    o.ld_w = p.Dp;
+    rows = std::max(rows, n);
+  }
+  if (!rows) return cudaSuccess;
+  const dim3 grid(uint32_t(std::min<uint64_t>((uint64_t(rows) * (p.Dp / 8) + 255) / 256, kHeadSms * 16)), 2);
+  return launch_dependent(f32 ? lay_out_kernel<true> : lay_out_kernel<false>, grid, dim3(256), 0, stream, both, p.D, p.Dp);
+}
 bool map_h(CUtensorMap* map, const HeadPlan& p, const Operands& o, uint32_t box) {
   return tc::make_map(map, o.h, p.D, p.B, p.parts, o.ld_h, p.lay_h ? uint64_t(p.B) * p.Dp : o.ld_h, box);
 }
@@ -943,7 +1015,6 @@ Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v
   q.blocks = tiles_of(p.D, kBlockK);
   q.splits = 1;
   q.b_mn = p.lay_w ? 0 : int(v0);
-  j.products = p.products;
   j.bitmask = a.bitmask;
   j.W = v.t.W;
   j.v0 = v0;
@@ -959,26 +1030,15 @@ int head_loss(cg_ctx* c, const HeadArgs& a, float* loss, float* lse, float* norm
   const CtxView v = ctx_view(c);
   const int dev = ctx_device(c);
   const HeadPlan p = plan_head(a.hidden, a.ld_h, a.weight, a.ld_w, a.dtype, a.B, a.V, a.D, false);
-  const bool f32 = a.dtype == CG_F32;
   Operands o{a.hidden, a.weight, a.ld_h, a.ld_w};
-  if (p.lay_h) {
-    if (lay_out(f32, a.hidden, a.ld_h, p.B, p.D, p.Dp, ws + p.at_h, v.stream) != cudaSuccess) return CG_E_CUDA;
-    o.h = ws + p.at_h;
-    o.ld_h = p.Dp;
-  }
   for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, p.V - v0);
-    if (p.lay_w) {
-      const char* from = static_cast<const char*>(a.weight) + uint64_t(v0) * a.ld_w * (f32 ? 4 : 2);
-      if (lay_out(f32, from, a.ld_w, n, p.D, p.Dp, ws + p.at_w, v.stream) != cudaSuccess) return CG_E_CUDA;
-      o.w = ws + p.at_w;
-      o.ld_w = p.Dp;
-    }
+    if (lay_out(a, p, v0, n, ws, o, v.stream) != cudaSuccess) return CG_E_CUDA;
     Job j = logits_of(a, p, v, v0, n);
     j.loss.part = reinterpret_cast<float2*>(ws + p.at_part);
     j.loss.target_logit = reinterpret_cast<float*>(ws + p.at_target);
     if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, p.lay_w ? n : p.V, 128)) return CG_E_CUDA;
-    if (launch_job<kLoss>(dev, p.pair, j, v.stream) != cudaSuccess) return CG_E_CUDA;
+    if (launch_job<kLoss>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
   return launch_dependent(join_loss_kernel, dim3(tiles_of(p.B, 32)), dim3(1024), 0, v.stream,
                           reinterpret_cast<const float2*>(ws + p.at_part),
@@ -1010,11 +1070,6 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
                                                                                                             : CG_E_CUDA;
   const HeadPlan p = plan_head(a.hidden, a.ld_h, a.weight, a.ld_w, a.dtype, a.B, a.V, a.D, true);
   Operands o{a.hidden, a.weight, a.ld_h, a.ld_w};
-  if (p.lay_h) {
-    if (lay_out(f32, a.hidden, a.ld_h, p.B, p.D, p.Dp, ws + p.at_h, v.stream) != cudaSuccess) return CG_E_CUDA;
-    o.h = ws + p.at_h;
-    o.ld_h = p.Dp;
-  }
   __nv_bfloat16* terms = reinterpret_cast<__nv_bfloat16*>(ws + p.at_terms);
   const uint64_t part_stride = uint64_t(p.B) * p.ld_terms;
   // the hidden rows' gradient is summed over pieces and splits in 32 bits where there are several
@@ -1022,22 +1077,16 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
   float* sums = reinterpret_cast<float*>(ws + p.at_sums);
   for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, p.V - v0);
-    if (p.lay_w) {
-      const char* from = static_cast<const char*>(a.weight) + uint64_t(v0) * a.ld_w * size;
-      if (lay_out(f32, from, a.ld_w, n, p.D, p.Dp, ws + p.at_w, v.stream) != cudaSuccess) return CG_E_CUDA;
-      o.w = ws + p.at_w;
-      o.ld_w = p.Dp;
-    }
+    if (lay_out(a, p, v0, n, ws, o, v.stream) != cudaSuccess) return CG_E_CUDA;
     const uint32_t w_rows = p.lay_w ? n : p.V;
     Job j = logits_of(a, p, v, v0, n);
     j.terms = TermsOut{loss, norm, up};
     if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, w_rows, 128) ||
         !tc::make_map(&j.p[0].out, terms, n, p.B, p.parts, p.ld_terms, part_stride, 32))
       return CG_E_CUDA;
-    if (launch_job<kTerms>(dev, p.pair, j, v.stream) != cudaSuccess) return CG_E_CUDA;
+    if (launch_job<kTerms>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
 
     Job g = {};
-    g.products = p.products;
     g.temp = 1.f;
     g.status = v.t.status;
     if (dh) {  // terms [B][n] x W [n][D], summed over the pieces
@@ -1066,7 +1115,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
       if (!grad_out(q, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
       if (!tc::make_map(&q.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&q.b, p, o, 64)) return CG_E_CUDA;
     }
-    if (launch_job<kOut>(dev, p.pair, g, v.stream) != cudaSuccess) return CG_E_CUDA;
+    if (launch_job<kOut>(dev, p, g, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
   if (dh && summed &&
       launch_dependent(join_grad_kernel, dim3(tiles_of(p.B * (p.ld_sums / 4), 256)), dim3(256), 0, v.stream,
