@@ -28,7 +28,7 @@ namespace {
 
 using namespace row;
 
-constexpr uint32_t kTileN = 256;          // columns of a tile
+constexpr uint32_t kTileN = 256;          // most columns of a tile
 constexpr uint32_t kBlockM = 128;         // a block's rows of it
 constexpr uint32_t kBlockK = 64;          // k of a stage: 128 bytes of bf16
 constexpr uint32_t kReaders = 8;          // warps that read tiles out: four row quarters x two column halves
@@ -61,7 +61,7 @@ struct Stage {
 
 // What is read out of the tiles
 struct LossOut {
-  float2* part;              // [2 * tiles over all pieces][B]: maximum and sum of 128 columns without the target
+  float2* part;              // [readers' column groups over all pieces][B]: maximum and sum without the target
   float* target_logit;       // [B], written by the tile that holds the row's target
 };
 struct TermsOut {
@@ -79,6 +79,7 @@ struct GradOut {
 struct Product {
   CUtensorMap a, b, out;     // operands; the terms or the gradient as they are written
   uint32_t m, n, n_m, n_n;   // extent, and in tiles
+  uint32_t tile_n;           // columns of a tile: 256, or 128 or 64 where tiles are few
   uint32_t blocks, splits;   // stages of one product; splits of them
   int a_mn, a_k, b_mn, b_k;  // where the product begins in the maps
   GradOut grad;
@@ -136,6 +137,8 @@ struct Turns {
 struct Work {
   uint32_t m0, n0, split, k0, k1;
 };
+template <bool NARROW>
+__device__ __forceinline__ uint32_t width(const Product& p) { return NARROW ? p.tile_n : kTileN; }
 // An item's stages: all of them, or its split's (blocks * splits fits 32 bits)
 __device__ __forceinline__ void stages_of(const Product& p, uint32_t t, Work& w) {
   w.split = 0;
@@ -148,7 +151,7 @@ __device__ __forceinline__ void stages_of(const Product& p, uint32_t t, Work& w)
   }
 }
 // Bands of row tiles over all columns: what runs at one time shares both operands in L2
-template <int CTAS>
+template <int CTAS, bool NARROW>
 __device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {
   Work w;
   stages_of(p, t, w);
@@ -157,7 +160,7 @@ __device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {
   const uint32_t rows = min(kBand, p.n_m - band * kBand);
   w.n0 = in / rows;
   w.m0 = (band * kBand + in - w.n0 * rows) * kBlockM * CTAS;
-  w.n0 *= kTileN;
+  w.n0 *= width<NARROW>(p);
   return w;
 }
 // the parts of the i-th of the six products of a stage; the last is the largest
@@ -441,25 +444,26 @@ struct Place {
 // An item's stages into the ring: a block brings its 128 rows of A and its share of B's 256.
 // With a pair the leader's barrier counts the bytes of both.  Six products of a stage follow
 // one another: the parts that they share come from L2.
-template <int CTAS, typename S, Sums SUMS, bool A_MN, bool B_MN>
+template <int CTAS, typename S, Sums SUMS, bool NARROW, bool A_MN, bool B_MN>
 __device__ __forceinline__ bool copy_item(const Product& p, const Work& w, uint32_t rank, uint32_t ring, Ends& ends, Place& at,
                                           uint32_t& issued) {
-  const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * (kTileN / CTAS));
+  const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * (width<NARROW>(p) / CTAS));
+  const uint32_t share = width<NARROW>(p) / CTAS, bytes = (S::kA + share * (kBlockK * 2)) * CTAS;
   for (uint32_t k = w.k0; k < w.k1; ++k) {
     const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
     for (uint32_t i = 0; i < products_of(SUMS); ++i) {
       const int pa = SUMS == kParts ? int(part_a(i)) : 0, pb = SUMS == kParts ? int(part_b(i)) : 0;
       if (!mbar_wait(&ends.empty[at.s], at.phase ^ 1)) return false;
       const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[at.s]), 0) : smem_addr(&ends.full[at.s]);
-      if (rank == 0) mbar_expect_tx(&ends.full[at.s], S::kBytes * CTAS);
+      if (rank == 0) mbar_expect_tx(&ends.full[at.s], bytes);
       const uint32_t a = ring + at.s * S::kBytes, b = a + S::kA;
       if (A_MN)
         for (uint32_t q = 0; q < kBlockM / 64; ++q) tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, pa, full);
       else tc::copy_box<CTAS>(a, &p.a, ak, am, pa, full);
       if (B_MN)
-        for (uint32_t q = 0; q < kTileN / CTAS / 64; ++q) tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, pb, full);
+        for (uint32_t q = 0; q < share / 64; ++q) tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, pb, full);
       else
-        for (uint32_t q = 0; q < kTileN / CTAS / 128; ++q)
+        for (uint32_t q = 0; q < (share + 127) / 128; ++q)   // boxes of 128 rows, or of all where they are fewer
           tc::copy_box<CTAS>(b + q * 16384, &p.b, bk, bn + int(128 * q), pb, full);
       ++issued;
       at.template step<S::kCount>();
@@ -471,9 +475,9 @@ __device__ __forceinline__ bool copy_item(const Product& p, const Work& w, uint3
 // An item's products, chain after chain; n counts the chains.  Chains take the two accumulators
 // in turn; the six products of a float matrices' stage take both.
 template <int CTAS, typename S, Sums SUMS, bool A_MN, bool B_MN>
-__device__ __forceinline__ bool multiply_item(uint32_t blocks, uint32_t ring, uint32_t tmem, Ends& ends, Place& at, bool& ready,
+__device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, uint32_t ring, uint32_t tmem, Ends& ends, Place& at, bool& ready,
                                               uint32_t& n) {
-  constexpr uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, kTileN);
+  const uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, tile_n);
   for (uint32_t k = 0; k < blocks; ++n) {
     const uint32_t end = SUMS == kOne ? blocks : min(blocks, k + kChain);
     const uint32_t acc = SUMS == kParts ? 0u : n & 1u, round = SUMS == kParts ? n : n >> 1;
@@ -501,7 +505,7 @@ __device__ __forceinline__ bool multiply_item(uint32_t blocks, uint32_t ring, ui
   return true;
 }
 
-template <int CTAS, Readout READ, Sums SUMS>
+template <int CTAS, Readout READ, Sums SUMS, bool NARROW>
 __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_constant__ Job job) {
   using S = Stage<CTAS, READ>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -543,9 +547,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       bool ok = true;
       while (ok && turns.next(second, t)) {
         if (READ == kOut && second) {
-          ok = copy_item<CTAS, S, SUMS, true, true>(job.p[1], work_of<CTAS>(job.p[1], t), rank, ring, ends, at, issued);
+          ok = copy_item<CTAS, S, SUMS, false, true, true>(job.p[1], work_of<CTAS, false>(job.p[1], t), rank, ring, ends, at, issued);
         } else {
-          ok = copy_item<CTAS, S, SUMS, false, READ == kOut>(job.p[0], work_of<CTAS>(job.p[0], t), rank, ring, ends, at, issued);
+          ok = copy_item<CTAS, S, SUMS, NARROW, false, READ == kOut>(job.p[0], work_of<CTAS, NARROW>(job.p[0], t), rank, ring, ends, at, issued);
         }
       }
       if (!ok) {
@@ -566,10 +570,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         Work w;
         if (READ == kOut && second) {
           stages_of(job.p[1], t, w);
-          ok = multiply_item<CTAS, S, SUMS, true, true>(w.k1 - w.k0, ring, tmem, ends, at, ready, n);
+          ok = multiply_item<CTAS, S, SUMS, true, true>(kTileN, w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         } else {
           stages_of(job.p[0], t, w);
-          ok = multiply_item<CTAS, S, SUMS, false, READ == kOut>(w.k1 - w.k0, ring, tmem, ends, at, ready, n);
+          ok = multiply_item<CTAS, S, SUMS, false, READ == kOut>(width<NARROW>(job.p[0]), w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         }
       }
       if (!ok) {
@@ -602,8 +606,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       return true;
     };
     auto read_item = [&](const Product& p) {
-      const Work w = work_of<CTAS>(p, t);
-      const uint32_t row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane, col = w.n0 + half * 128;
+      const Work w = work_of<CTAS, NARROW>(p, t);
+      // the reader's columns: half of the tile's, at least 64 (the second half's readers then have none)
+      const uint32_t wide = NARROW ? max(64u, p.tile_n / 2) : 128u, chunks = !NARROW ? 4u : half * wide < width<NARROW>(p) ? wide / 32 : 0;
+      const uint32_t row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane, col = w.n0 + half * wide;
       const uint32_t blocks = w.k1 - w.k0;
       uint32_t words[4], target = CG_NO_TOKEN;
       if (READ != kOut) {
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           send_grad(p, x, w.split, row0, col + 32 * j, j, boxes);
         }
       };
-      const uint32_t at = tmem + half * 128 + ((quarter * 32) << 16);
+      const uint32_t at = tmem + half * wide + ((quarter * 32) << 16);
       if (SUMS != kOne) {
         // the chains' sums, added up in registers; none in a split without stages
         float v[128];
@@ -635,6 +641,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           const uint32_t acc = SUMS == kParts ? 0u : n & 1u;
 #pragma unroll
           for (uint32_t q = 0; q < 4; ++q) {
+            if (q >= chunks) break;
             uint32_t x[32];
             if (SUMS == kParts) {   // the small ones first
               tc::tmem_load(at + kTileN + 32 * q, x);
@@ -651,18 +658,20 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         }
         if (!ok) return false;
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) read(v + 32 * j, j, words[j]);
+        for (uint32_t j = 0; j < 4; ++j)
+          if (j < chunks) read(v + 32 * j, j, words[j]);
       } else {
         if (blocks && !full(n)) return false;
         const uint32_t acc = n & 1u;
         n += blocks != 0;
+        if (chunks == 0 && blocks) done(acc);
 #pragma unroll 1
-        for (uint32_t j = 0; j < 4; ++j) {
+        for (uint32_t j = 0; j < chunks; ++j) {
           uint32_t x[32];
           float v[32];
           tc::tmem_load(at + acc * kTileN + 32 * j, x);
           tc::tmem_wait();
-          if (j == 3 && blocks) done(acc);
+          if (j + 1 == chunks && blocks) done(acc);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]);
           if (!blocks) {   // a split without stages: nothing was multiplied
@@ -672,7 +681,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           read(v, j, j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3]);
         }
       }
-      if (READ == kLoss && r < p.m && col < p.n) job.loss.part[size_t((job.v0 + col) >> 7) * p.m + r] = make_float2(sum.m, sum.s);
+      if (READ == kLoss && chunks && r < p.m && col < p.n)
+        job.loss.part[size_t((job.v0 + col) / wide) * p.m + r] = make_float2(sum.m, sum.s);
       return true;
     };
     // (each product read where it lies: through a pointer to either the gradients' tiles took a fifth longer)
@@ -766,40 +776,78 @@ __global__ void __launch_bounds__(1024) join_loss_kernel(const float2* part, con
   if (lse) lse[row] = M > -INFINITY ? __fdiv_rn(M, T) + (first ? log1pf(rest) : logf(rest)) : -INFINITY;
 }
 
-// The splits' sums of a gradient, in their order: 4 columns to a thread
-__global__ void __launch_bounds__(256) join_grad_kernel(const float* sums, uint32_t ld_sums, uint32_t splits, uint32_t m,
-                                                        uint32_t n, void* out, uint64_t ld, bool bf16, bool wide) {
+// 4 columns of a gradient's row, `left` of them in the row
+__device__ __forceinline__ void put4(void* out, size_t at, uint32_t left, bool bf16, bool wide, float4 s) {
+  if (wide && left >= 4) {
+    if (bf16) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
+    else *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
+    return;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) {
+    if (e >= left) break;
+    if (bf16) static_cast<__nv_bfloat16*>(out)[at + e] = __float2bfloat16_rn(v[e]);
+    else static_cast<float*>(out)[at + e] = v[e];
+  }
+}
+// The splits' sums of a gradient, added in their order.  A few splits: a thread takes 4 columns
+// of all of them.
+constexpr uint32_t kFewSplits = 8;
+__global__ void __launch_bounds__(256) join_few_kernel(const float* sums, uint32_t ld_sums, uint32_t splits, uint32_t m,
+                                                       uint32_t n, void* out, uint64_t ld, bool bf16, bool wide) {
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t groups = ld_sums / 4;
   const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
   const uint32_t r = uint32_t(i / groups), col = 4 * uint32_t(i - uint64_t(r) * groups);
   if (r >= m || col >= n) return;
-  float4 s = {};
+  float4 s = *reinterpret_cast<const float4*>(sums + size_t(r) * ld_sums + col);
 #pragma unroll 4
-  for (uint32_t k = 0; k < splits; ++k) {
+  for (uint32_t k = 1; k < splits; ++k) {
     const float4 x = *reinterpret_cast<const float4*>(sums + (size_t(k) * m + r) * ld_sums + col);
     s.x += x.x;
     s.y += x.y;
     s.z += x.z;
     s.w += x.w;
   }
-  const float v[4] = {s.x, s.y, s.z, s.w};
-  const size_t at = size_t(r) * ld + col;
-  if (wide && col + 4 <= n) {
-    if (bf16) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
-    else *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
-    return;
-  }
-#pragma unroll
-  for (uint32_t e = 0; e < 4; ++e) {
-    if (col + e >= n) break;
-    if (bf16) static_cast<__nv_bfloat16*>(out)[at + e] = __float2bfloat16_rn(v[e]);
-    else static_cast<float*>(out)[at + e] = v[e];
-  }
+  put4(out, size_t(r) * ld + col, n - col, bf16, wide, s);
 }
-
-// ---- operands that the copies cannot take as they lie ----------------------------------------
+// Many (few rows, which leave few threads): 32 groups of 4 columns to a block, whose warps take
+// the splits in turn; the warps' sums are added in their order (152 splits of 127 x 192: 26 us
+// the way above).
+__global__ void __launch_bounds__(256) join_many_kernel(const float* sums, uint32_t ld_sums, uint32_t splits, uint32_t m,
+                                                        uint32_t n, void* out, uint64_t ld, bool bf16, bool wide) {
+  __shared__ float4 mine[8][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t groups = ld_sums / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t i = uint64_t(blockIdx.x) * 32 + lane;
+  const uint32_t r = uint32_t(i / groups), col = 4 * uint32_t(i - uint64_t(r) * groups);
+  const bool there = r < m && col < n;
+  float4 s = {};
+  if (there)
+#pragma unroll 4
+    for (uint32_t k = warp; k < splits; k += 8) {
+      const float4 x = *reinterpret_cast<const float4*>(sums + (size_t(k) * m + r) * ld_sums + col);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+  mine[warp][lane] = s;
+  __syncthreads();
+  if (warp || !there) return;
+#pragma unroll
+  for (uint32_t w = 1; w < 8; ++w) {
+    const float4 x = mine[w][lane];
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+  put4(out, size_t(r) * ld + col, n - col, bf16, wide, s);
+}
 
 // bf16 rows off the 16-byte grid are copied onto it; float rows are split into three parts
 // that add up to the value (8 bits each; a value that is not finite is its first part).  A
@@ -879,11 +927,21 @@ struct HeadPlan {
   uint32_t B, V, D, Dp, parts;
   bool lay_h, lay_w;
   uint32_t piece;            // tokens of a piece: a multiple of 256 unless it is all of them
+  uint32_t tile_n, groups;   // columns of the logits' tiles; column groups of their readers
   uint64_t ld_terms, ld_sums;
   uint32_t splits;           // of the product that sums over tokens
   bool pair;                 // rows in pairs of blocks
   size_t at_h, at_w, at_part, at_target, at_terms, at_sums, bytes;
 };
+
+// Columns of the logits' tiles: few rows' are halved, and halved again, while the blocks are twice
+// as many as the tiles.  (Where every block has a tile, narrow ones read the rows' operand more
+// often for nothing: 4 x 48675 x 3520 in 191 tiles of 256 80 us, in 381 of 128 121.)
+uint32_t tile_width(uint32_t B, uint32_t columns) {
+  uint32_t w = kTileN;
+  while (B <= kBlockM && w > 64 && 2 * tiles_of(columns, w) <= kHeadSms) w /= 2;
+  return w;
+}
 
 HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64_t ld_w, int dtype, uint32_t B, uint32_t V,
                    uint32_t D, bool grad) {
@@ -903,6 +961,9 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   if (most < V) most = std::max<uint64_t>(most / 256 * 256, 256);
   const uint64_t pieces = (V + most - 1) / most;
   p.piece = uint32_t(std::min<uint64_t>(up_to((V + pieces - 1) / pieces, 256), V));
+  const uint32_t slots = kHeadSms / (p.pair ? 2 : 1);
+  p.tile_n = tile_width(B, p.piece);
+  p.groups = tiles_of(V, std::max(64u, p.tile_n / 2));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -912,14 +973,14 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   if (p.lay_h) p.at_h = take(size_t(p.parts) * B * p.Dp * 2);
   if (p.lay_w) p.at_w = take(size_t(p.parts) * p.piece * p.Dp * 2);
   if (!grad) {
-    p.at_part = take(size_t(tiles_of(V, 128)) * B * 8);
+    p.at_part = take(size_t(p.groups) * B * 8);
     p.at_target = take(size_t(B) * 4);
   } else {
     p.ld_terms = up_to(p.piece, 8);
     p.at_terms = take(size_t(p.parts) * B * p.ld_terms * 2);
     p.ld_sums = up_to(D, 4);
     const uint32_t tiles = tiles_of(B, kBlockM * (p.pair ? 2 : 1)) * tiles_of(D, kTileN);
-    const uint32_t slots = kHeadSms / (p.pair ? 2 : 1), blocks = tiles_of(p.piece, kBlockK);
+    const uint32_t blocks = tiles_of(p.piece, kBlockK);
     p.splits = std::max(1u, std::min(slots / std::max(tiles, 1u), blocks / 8));
     if (p.splits > 1 || p.piece < V) p.at_sums = take(size_t(p.splits) * B * p.ld_sums * 4);
   }
@@ -927,34 +988,39 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   return p;
 }
 
-template <int CTAS, Readout READ, Sums SUMS>
+template <int CTAS, Readout READ, Sums SUMS, bool NARROW>
 cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
   uint32_t items[2] = {0, 0}, longest[2] = {0, 0};
   for (int i = 0; i < (READ == kOut ? 2 : 1); ++i) {
     Product& p = j.p[i];
+    if (!p.splits) continue;   // not wanted
     p.n_m = tiles_of(p.m, kBlockM * CTAS);
-    p.n_n = tiles_of(p.n, kTileN);
+    p.n_n = tiles_of(p.n, p.tile_n);
     items[i] = p.n_m * p.n_n * p.splits;
     // in stages; a tile of few is as long as it takes to read out and write
     if (items[i]) longest[i] = std::max(tiles_of(p.blocks, p.splits) * products_of(SUMS), p.grad.boxes ? kReadBoxes : kReadElements);
   }
   // what one item of the first product is worth in items of the second
   j.early = longest[1] ? (longest[0] + longest[1] / 2) / longest[1] : 0;
-  return launch_clusters<product_kernel<CTAS, READ, SUMS>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
+  return launch_clusters<product_kernel<CTAS, READ, SUMS, NARROW>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
                                                              kHeadThreads, product_smem<CTAS, READ>(), stream, j);
 }
 // Rows in pairs of blocks above 128.  Results in 32 bits are summed in chains (losses, and all
 // that float matrices give): a long chain of sums in tensor memory drifts, as its steps are not
 // rounded to nearest (the loss of 256 x 128256 x 4096 in one chain 2.2e-6 off, in chains 4.6e-7).
-template <int CTAS, Readout READ>
+template <int CTAS, Readout READ, bool NARROW>
 cudaError_t launch_job(int device, bool f32, Job& j, cudaStream_t stream) {
-  if (f32) return launch_job<CTAS, READ, kParts>(device, j, stream);
-  if (READ == kLoss && j.p[0].blocks > kChain) return launch_job<CTAS, READ, READ == kLoss ? kChains : kOne>(device, j, stream);
-  return launch_job<CTAS, READ, kOne>(device, j, stream);
+  if (f32) return launch_job<CTAS, READ, kParts, NARROW>(device, j, stream);
+  if (READ == kLoss && j.p[0].blocks > kChain)
+    return launch_job<CTAS, READ, READ == kLoss ? kChains : kOne, NARROW>(device, j, stream);
+  return launch_job<CTAS, READ, kOne, NARROW>(device, j, stream);
 }
 template <Readout READ>
 cudaError_t launch_job(int device, const HeadPlan& p, Job& j, cudaStream_t stream) {
-  return p.pair ? launch_job<2, READ>(device, p.parts > 1, j, stream) : launch_job<1, READ>(device, p.parts > 1, j, stream);
+  const bool f32 = p.parts > 1;
+  if (p.pair) return launch_job<2, READ, false>(device, f32, j, stream);
+  if (READ != kOut && p.tile_n < kTileN) return launch_job<1, READ, READ != kOut>(device, f32, j, stream);
+  return launch_job<1, READ, false>(device, f32, j, stream);
 }
 
 struct HeadArgs {
@@ -1006,6 +1072,8 @@ bool map_w(CUtensorMap* map, const HeadPlan& p, const Operands& o, uint32_t rows
   return tc::make_map(map, o.w, p.D, rows, p.parts, o.ld_w, p.lay_w ? uint64_t(rows) * p.Dp : o.ld_w, box);
 }
 
+// rows of the weight's boxes: a block's share of a tile's, at most 128
+uint32_t b_rows(const HeadPlan& p) { return std::min(128u, p.tile_n / (p.pair ? 2 : 1)); }
 // x = H W^T of a piece, read out one way or the other
 Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v0, uint32_t n) {
   Job j = {};
@@ -1014,6 +1082,7 @@ Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v
   q.n = n;
   q.blocks = tiles_of(p.D, kBlockK);
   q.splits = 1;
+  q.tile_n = p.tile_n;
   q.b_mn = p.lay_w ? 0 : int(v0);
   j.bitmask = a.bitmask;
   j.W = v.t.W;
@@ -1037,12 +1106,12 @@ int head_loss(cg_ctx* c, const HeadArgs& a, float* loss, float* lse, float* norm
     Job j = logits_of(a, p, v, v0, n);
     j.loss.part = reinterpret_cast<float2*>(ws + p.at_part);
     j.loss.target_logit = reinterpret_cast<float*>(ws + p.at_target);
-    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, p.lay_w ? n : p.V, 128)) return CG_E_CUDA;
+    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, p.lay_w ? n : p.V, b_rows(p))) return CG_E_CUDA;
     if (launch_job<kLoss>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
   return launch_dependent(join_loss_kernel, dim3(tiles_of(p.B, 32)), dim3(1024), 0, v.stream,
                           reinterpret_cast<const float2*>(ws + p.at_part),
-                          reinterpret_cast<const float*>(ws + p.at_target), a.target, tiles_of(p.V, 128), p.B, p.V, a.temp,
+                          reinterpret_cast<const float*>(ws + p.at_target), a.target, p.groups, p.B, p.V, a.temp,
                           loss, lse, norm, v.t.status) == cudaSuccess
              ? CG_OK
              : CG_E_CUDA;
@@ -1081,7 +1150,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
     const uint32_t w_rows = p.lay_w ? n : p.V;
     Job j = logits_of(a, p, v, v0, n);
     j.terms = TermsOut{loss, norm, up};
-    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, w_rows, 128) ||
+    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, w_rows, b_rows(p)) ||
         !tc::make_map(&j.p[0].out, terms, n, p.B, p.parts, p.ld_terms, part_stride, 32))
       return CG_E_CUDA;
     if (launch_job<kTerms>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
@@ -1095,6 +1164,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
       q.n = p.D;
       q.blocks = tiles_of(n, kBlockK);
       q.splits = p.splits;
+      q.tile_n = kTileN;
       q.b_k = p.lay_w ? 0 : int(v0);
       if (summed) {
         q.grad.boxes = q.grad.f32 = true;
@@ -1112,17 +1182,20 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
       q.n = p.D;
       q.blocks = tiles_of(p.B, kBlockK);
       q.splits = 1;
+      q.tile_n = kTileN;
       if (!grad_out(q, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
       if (!tc::make_map(&q.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&q.b, p, o, 64)) return CG_E_CUDA;
     }
     if (launch_job<kOut>(dev, p, g, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
-  if (dh && summed &&
-      launch_dependent(join_grad_kernel, dim3(tiles_of(p.B * (p.ld_sums / 4), 256)), dim3(256), 0, v.stream,
-                       static_cast<const float*>(sums), uint32_t(p.ld_sums), p.splits, p.B, p.D, dh, ld_dh, !f32,
-                       rows_on_grid(dh, a.dtype, ld_dh)) != cudaSuccess)
-    return CG_E_CUDA;
-  return CG_OK;
+  if (!dh || !summed) return CG_OK;
+  const uint64_t groups = p.B * (p.ld_sums / 4);
+  const bool wide = rows_on_grid(dh, a.dtype, ld_dh);
+  const bool few = p.splits <= kFewSplits;
+  const cudaError_t e = launch_dependent(few ? join_few_kernel : join_many_kernel, dim3(tiles_of(groups, few ? 256 : 32)),
+                                         dim3(256), 0, v.stream, static_cast<const float*>(sums), uint32_t(p.ld_sums), p.splits,
+                                         p.B, p.D, dh, ld_dh, !f32, wide);
+  return e == cudaSuccess ? CG_OK : CG_E_CUDA;
 }
 
 int head_args(const cg_ctx* c, const HeadArgs& a) {
