@@ -17,6 +17,12 @@ tokens, and a student's distillation loss (see distill() for autograd):
     ctx.sample_rows(logits, uniform, out_tok, bitmask, temp, top_k, top_p, min_p)
     ctx.top_logprobs(logits, out_ids, out_logprobs, bitmask)
     ctx.distill_loss(logits, ids, teacher, out_loss, temp, bitmask)
+
+And the model's two ends, where tokens become rows and rows become logits (see
+embed() and head_loss() for autograd):
+
+    ctx.embed(table, tokens, out, scale)
+    ctx.head_loss(hidden, weight, target, out_loss, temp, bitmask)
 """
 
 from __future__ import annotations
@@ -562,3 +568,18 @@ def distill(ctx: Ctx, logits, ids, teacher, temp: float = 1.0, bitmask=None):
     the context's stream, ordered after and before torch's current one."""
     from .autograd import DistillLoss
     return DistillLoss.apply(logits, ctx, ids, teacher, float(temp), bitmask)
+
+
+def embed(ctx: Ctx, table, tokens, scale: float = 1.0):
+    """scale * table[tokens], [N, D] of the table's dtype (zeros where a token is CG_NO_TOKEN), differentiable by
+    table [V, D]: Ctx.embed forward, Ctx.embed_grad backward.  Ordered with torch's current stream as distill()."""
+    from .autograd import Embed
+    return Embed.apply(table, ctx, tokens, float(scale))
+
+
+def head_loss(ctx: Ctx, hidden, weight, target, temp: float = 1.0, bitmask=None):
+    """Cross entropy of each row, f32 [B], of the output layer hidden [B, D] @ weight [V, D].T over the allowed
+    tokens, differentiable by hidden and weight, no logits kept: Ctx.head_loss forward, Ctx.head_grad backward.
+    Rows whose target is CG_NO_TOKEN or forbidden have loss 0.  Ordered with torch's current stream as distill()."""
+    from .autograd import HeadLoss
+    return HeadLoss.apply(hidden, weight, ctx, target, float(temp), bitmask)
