@@ -372,9 +372,8 @@ class Ctx:
         g, ld, D = R.matrix_of(call, grad, "grad", None, N, dev)
         o, ldo = R.rows_of(call, out_grad, "out_grad", (grad.dtype,), (self.V, D), dev)
         tok = R.want(call, tokens, "tokens", R.U32, (N,), dev)
-        work = R.workspace_of(self, call, workspace, self.embed_workspace(grad, tokens))
-        L.check(call, L.lib().cg_embed_grad(self._h, g, R.DTYPE[grad.dtype], N, self.V, D, ld, tok, scale,
-                                            int(accumulate), o, ldo, _ptr(work), 0 if work is None else work.numel()))
+        R.with_workspace(self, call, workspace, lambda: self.embed_workspace(grad, tokens), L.lib().cg_embed_grad,
+                         (self._h, g, R.DTYPE[grad.dtype], N, self.V, D, ld, tok, scale, int(accumulate), o, ldo))
 
     def _head_operands(self, call, hidden, weight):
         """(what the calls take of the two matrices, B, D)."""
@@ -402,9 +401,8 @@ class Ctx:
         mask = R.opt(call, bitmask, "bitmask", R.U32, (B, self.W), dev)
         t, loss = R.want(call, target, "target", R.U32, (B,), dev), R.want(call, out_loss, "out_loss", R.F32, (B,), dev)
         lse, norm = R.opt(call, out_lse, "out_lse", R.F32, (B,), dev), R.opt(call, out_norm, "out_norm", R.F32, (B, 2), dev)
-        work = R.workspace_of(self, call, workspace, self._head_bytes(operands, 0))
-        L.check(call, L.lib().cg_head_loss(*operands, mask, t, temp, loss, lse, norm, _ptr(work),
-                                           0 if work is None else work.numel()))
+        R.with_workspace(self, call, workspace, lambda: self._head_bytes(operands, 0), L.lib().cg_head_loss,
+                         (*operands, mask, t, temp, loss, lse, norm))
 
     def head_grad(self, hidden, weight, target, loss, norm, out_grad_hidden=None, out_grad_weight=None,
                   temp: float = 1.0, bitmask=None, grad_loss=None, workspace=None) -> None:
@@ -421,9 +419,8 @@ class Ctx:
         t, kept = R.want(call, target, "target", R.U32, (B,), dev), R.want(call, loss, "loss", R.F32, (B,), dev)
         norm = R.want(call, norm, "norm", R.F32, (B, 2), dev)
         up = R.opt(call, grad_loss, "grad_loss", R.F32, (B,), dev)
-        work = R.workspace_of(self, call, workspace, self._head_bytes(operands, 1))
-        L.check(call, L.lib().cg_head_grad(*operands, mask, t, temp, kept, norm, up, dh, lddh, dw, lddw, _ptr(work),
-                                           0 if work is None else work.numel()))
+        R.with_workspace(self, call, workspace, lambda: self._head_bytes(operands, 1), L.lib().cg_head_grad,
+                         (*operands, mask, t, temp, kept, norm, up, dh, lddh, dw, lddw))
 
     def self_test_cluster_timeout(self, out) -> None:
         """Make a block of a cluster give up while others still send to it (the status then

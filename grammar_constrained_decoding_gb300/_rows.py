@@ -47,24 +47,31 @@ def matrix_of(call: str, t, what: str, dtype, rows: int, dev: int = 0) -> tuple[
 KEPT_WORKSPACE = 64 << 20   # bytes: what a thread keeps between its calls; larger ones are allocated for each
 
 
-def workspace_of(ctx, call: str, given, nbytes: int):
-    """A u8 tensor of at least nbytes of device memory: the caller's; or the one that this thread's calls on the
-    context's stream have kept (allocating in every call costs as much host time as a small call itself); or a
-    new one, which belongs to the context's stream: in a graph capture, which has to own what its replays use,
-    for a stream that is not torch's current one, and for large calls.  None where nothing is needed."""
-    if not nbytes:
-        return None
+def with_workspace(ctx, call: str, given, need, entry, args) -> None:
+    """entry(*args, workspace, its bytes) in the caller's workspace (a u8 tensor), or in one that the library's own
+    need() says the size of:
+      - the one that this thread's calls on the context's stream have kept (allocating in every call costs as
+        much host time as a small call itself), tried before need() is asked;
+      - a new one, which belongs to the context's stream: in a graph capture, which has to own what its replays
+        use, for a stream that is not torch's current one, and for large calls."""
     if given is not None:
         want(call, given, "workspace", (torch.uint8,), given.shape, ctx._dev)
-        if given.numel() < nbytes:
-            raise L.CgError(call, L.CG_E_ARG, f"workspace: {nbytes} bytes are wanted")
-        return given
-    if torch.cuda.current_stream(ctx._dev).cuda_stream != ctx._stream:
+        L.check(call, entry(*args, given.data_ptr(), given.numel()))
+        return
+    here = torch.cuda.current_stream(ctx._dev).cuda_stream == ctx._stream
+    may_keep = here and not torch.cuda.is_current_stream_capturing()
+    kept = getattr(ctx._kept, "workspace", None) if may_keep else None
+    if kept is not None:
+        rc = entry(*args, kept.data_ptr(), kept.numel())
+        if rc != L.CG_E_NOMEM:
+            L.check(call, rc)
+            return
+    nbytes = max(need(), 256)
+    if here:
+        new = torch.empty(max(nbytes, 1 << 20) if may_keep else nbytes, dtype=torch.uint8, device=ctx._dev)
+        if may_keep and nbytes <= KEPT_WORKSPACE:
+            ctx._kept.workspace = new
+    else:
         with torch.cuda.stream(ctx.stream):
-            return torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
-    if nbytes > KEPT_WORKSPACE or torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
-    kept = getattr(ctx._kept, "workspace", None)
-    if kept is None or kept.numel() < nbytes:
-        kept = ctx._kept.workspace = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=ctx._dev)
-    return kept
+            new = torch.empty(nbytes, dtype=torch.uint8, device=ctx._dev)
+    L.check(call, entry(*args, new.data_ptr(), new.numel()))

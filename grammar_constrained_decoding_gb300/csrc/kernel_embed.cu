@@ -255,46 +255,54 @@ __device__ __forceinline__ void bulk_s2g(void* to, const void* from, uint32_t by
                : "memory");
 }
 
-// Zeros over the gradient by `blocks` blocks: rows without gaps on the 16-byte grid by bulk
-// copies of 32 KB from shared memory, other rows by vectors.
-template <int BYTES>
-__device__ void write_zeros(char* out, uint64_t pitch, uint32_t rows, uint32_t vecs, uint32_t block, uint32_t blocks,
+// Zeros over the gradient by `blocks` blocks: rows without gaps by bulk copies of 32 KB from
+// shared memory, other rows a warp each in 16-byte stores; what lies off the 16-byte grid at
+// either end element by element.
+template <uint32_t SIZE>
+__device__ __forceinline__ void zero_edge(char* from, uint32_t bytes, uint32_t lane) {   // fewer than 16
+  if (lane * SIZE < bytes) *reinterpret_cast<typename VecOf<SIZE>::type*>(from + lane * SIZE) = 0;
+}
+template <uint32_t SIZE>
+__device__ void write_zeros(char* out, uint64_t pitch, uint32_t rows, uint64_t width, uint32_t block, uint32_t blocks,
                             unsigned char* smem) {
-  using Vec = typename VecOf<BYTES>::type;
-  if (BYTES == 16 && pitch == uint64_t(vecs) * BYTES) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (pitch == width) {
     for (uint32_t i = threadIdx.x; i < kZeroBytes / 16; i += kSortThreads) reinterpret_cast<uint4*>(smem)[i] = uint4{};
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
+    const uint64_t all = uint64_t(rows) * pitch, lead = min(all, uint64_t(-reinterpret_cast<uintptr_t>(out) & 15u));
+    const uint64_t body = (all - lead) & ~uint64_t(15);
     if (threadIdx.x == 0) {
-      const uint64_t all = uint64_t(rows) * pitch;
-      for (uint64_t at = uint64_t(block) * kZeroBytes; at < all; at += uint64_t(blocks) * kZeroBytes)
-        bulk_s2g(out + at, smem, uint32_t(min(uint64_t(kZeroBytes), all - at)));
+      for (uint64_t at = uint64_t(block) * kZeroBytes; at < body; at += uint64_t(blocks) * kZeroBytes)
+        bulk_s2g(out + lead + at, smem, uint32_t(min(uint64_t(kZeroBytes), body - at)));
       asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    if (block == 0 && warp == 1) {
+      zero_edge<SIZE>(out, uint32_t(lead), lane);
+      zero_edge<SIZE>(out + lead + body, uint32_t(all - lead - body), lane);
     }
     return;
   }
-  constexpr uint32_t kEach = 8;
-  const uint64_t all = uint64_t(rows) * vecs, step = uint64_t(blocks) * (kSortThreads * kEach);
-  for (uint64_t base = uint64_t(block) * (kSortThreads * kEach); base < all; base += step) {
-    const uint32_t row0 = uint32_t(base / vecs), off = uint32_t(base - uint64_t(row0) * vecs);
-#pragma unroll
-    for (uint32_t k = 0; k < kEach; ++k) {
-      const uint32_t at = off + k * kSortThreads + threadIdx.x, row = row0 + at / vecs;
-      if (row < rows) *reinterpret_cast<Vec*>(out + row * pitch + uint64_t(at % vecs) * BYTES) = Vec{};
-    }
+  for (uint64_t row = uint64_t(block) * kSortWarps + warp; row < rows; row += uint64_t(blocks) * kSortWarps) {
+    char* at = out + row * pitch;
+    const uint64_t lead = min(width, uint64_t(-reinterpret_cast<uintptr_t>(at) & 15u)), body = (width - lead) & ~uint64_t(15);
+    zero_edge<SIZE>(at, uint32_t(lead), lane);
+#pragma unroll 4
+    for (uint64_t i = lane * 16; i < body; i += 512) *reinterpret_cast<uint4*>(at + lead + i) = uint4{};
+    zero_edge<SIZE>(at + lead + body, uint32_t(width - lead - body), lane);
   }
 }
 
 // The first cluster sorts; the others meanwhile write zeros over the gradient (all of it: rows
 // of tokens that occur are written again afterwards, at most one a position)
-template <int BYTES>
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a, char* out, uint64_t pitch, uint32_t vecs) {
+template <uint32_t SIZE>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a, char* out, uint64_t pitch, uint64_t width) {
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t n = cluster_size();
   if (blockIdx.x < n) sort_tokens(a, *reinterpret_cast<SortShared*>(smem));
-  else if (out) write_zeros<BYTES>(out, pitch, a.V, vecs, blockIdx.x - n, gridDim.x - n, smem);
+  else if (out) write_zeros<SIZE>(out, pitch, a.V, width, blockIdx.x - n, gridDim.x - n, smem);
 }
 constexpr size_t kSortSmem = sizeof(SortShared) > kZeroBytes ? sizeof(SortShared) : kZeroBytes;
 
@@ -345,7 +353,7 @@ __device__ __forceinline__ uint32_t equal_after(const uint32_t* at, uint32_t tok
 }
 
 // A block takes a chunk of the sorted positions and a slab of the columns: kCols vectors of a
-// row to a thread, 128 vectors apart (rows of more than 128 narrow vectors: 16 bytes in all)
+// row to a thread, 128 vectors apart (two in rows of more than 128 narrow vectors)
 template <bool BF16, int BYTES, uint32_t kCols>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   using E = Elems<BF16, BYTES>;
@@ -537,16 +545,19 @@ cudaError_t launch_look(const void* table, uint64_t pitch, const uint32_t* token
 template <bool BF16, int BYTES>
 cudaError_t launch_grad(int device, const SortArgs& sort, SumArgs sum, uint32_t chunks, uint32_t D, cudaStream_t stream) {
   sum.vecs = uint32_t(uint64_t(D) * (BF16 ? 2 : 4) / BYTES);
-  const uint32_t cols = sum.vecs > kSumThreads ? 16 / BYTES : 1;
+  // (4-byte vectors of 20000 x 1001 floats: one a thread 55.1 us, two 49.7, four 53.3)
+  constexpr uint32_t kMany = BYTES == 16 ? 1 : 2;
+  const uint32_t cols = sum.vecs > kSumThreads ? kMany : 1;
   sum.slabs = tiles_of(sum.vecs, kSumThreads * cols);
   uint32_t n = 1;
   while (n < kSortMost && sort.N > n * kSortThreads) n *= 2;
   // without zeros to write the sorting cluster is alone
   const uint32_t clusters = sum.add ? 1 : kEmbedSms / n;
-  cudaError_t e = launch_clusters<sort_kernel<BYTES>>(device, clusters, n, kSortThreads, kSortSmem, stream, sort,
-                                                     sum.add ? static_cast<char*>(nullptr) : sum.out, sum.pitch_out, sum.vecs);
+  cudaError_t e = launch_clusters<sort_kernel<BF16 ? 2 : 4>>(device, clusters, n, kSortThreads, kSortSmem, stream, sort,
+                                                            sum.add ? static_cast<char*>(nullptr) : sum.out, sum.pitch_out,
+                                                            uint64_t(D) * (BF16 ? 2 : 4));
   if (e != cudaSuccess) return e;
-  e = launch_dependent(cols == 1 ? sum_kernel<BF16, BYTES, 1> : sum_kernel<BF16, BYTES, 16 / BYTES>, dim3(chunks * sum.slabs), dim3(kSumThreads), 0, stream, sum);
+  e = launch_dependent(cols == 1 ? sum_kernel<BF16, BYTES, 1> : sum_kernel<BF16, BYTES, kMany>, dim3(chunks * sum.slabs), dim3(kSumThreads), 0, stream, sum);
   if (e != cudaSuccess || chunks < 2) return e;
   return launch_dependent(join_kernel<BF16>, dim3(std::min(chunks * tiles_of(D, kJoinColumns), 4 * kEmbedSms)),
                           dim3(kJoinThreads), 0, stream, sum, D);
@@ -639,7 +650,8 @@ extern "C" int cg_embed_grad(cg_ctx* c, const void* d_grad, int dtype, uint32_t 
   const uint64_t size = dtype_size(dtype);
   if (matrices_meet(d_out_grad, V, ld_out, d_grad, N, ld_grad, D, size)) return CG_E_ARG;
   const GradPlan p = plan_grad(std::max(N, 1u), D, dtype);
-  if (N && (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256 || workspace_bytes < p.bytes)) return CG_E_ARG;
+  if (N && (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256)) return CG_E_ARG;
+  if (N && workspace_bytes < p.bytes) return CG_E_NOMEM;
   DeviceGuard dg(ctx_device(c), "cg_embed_grad");
   if (!dg.ok) return CG_E_CUDA;
   const CtxView v = ctx_view(c);

@@ -954,7 +954,9 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   p.parts = f32 ? 3 : 1;
   p.lay_h = f32 || !rows_on_grid(hidden, dtype, ld_h);
   p.lay_w = f32 || !rows_on_grid(weight, dtype, ld_w);
-  p.pair = B > kBlockM;
+  // rows in pairs of blocks, but not 257 to 384: three blocks pad them to 384, two pairs to 512
+  // (333 x 32000 x 1024 step: 107.9 us in blocks, 110.5 in pairs)
+  p.pair = B > kBlockM && !(B > 2 * kBlockM && B <= 3 * kBlockM);
   uint64_t most = V;
   if (p.lay_w) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * p.Dp * 2));
   if (grad) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * std::max(B, 1u) * 2));
@@ -1005,7 +1007,7 @@ cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
   return launch_clusters<product_kernel<CTAS, READ, SUMS, NARROW>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
                                                              kHeadThreads, product_smem<CTAS, READ>(), stream, j);
 }
-// Rows in pairs of blocks above 128.  Results in 32 bits are summed in chains (losses, and all
+// Results in 32 bits are summed in chains (losses, and all
 // that float matrices give): a long chain of sums in tensor memory drifts, as its steps are not
 // rounded to nearest (the loss of 256 x 128256 x 4096 in one chain 2.2e-6 off, in chains 4.6e-7).
 template <int CTAS, Readout READ, bool NARROW>
@@ -1093,12 +1095,11 @@ Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v
   return j;
 }
 
-int head_loss(cg_ctx* c, const HeadArgs& a, float* loss, float* lse, float* norm, unsigned char* ws) {
+int head_loss(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, float* loss, float* lse, float* norm, unsigned char* ws) {
   DeviceGuard dg(ctx_device(c), "cg_head_loss");
   if (!dg.ok) return CG_E_CUDA;
   const CtxView v = ctx_view(c);
   const int dev = ctx_device(c);
-  const HeadPlan p = plan_head(a.hidden, a.ld_h, a.weight, a.ld_w, a.dtype, a.B, a.V, a.D, false);
   Operands o{a.hidden, a.weight, a.ld_h, a.ld_w};
   for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, p.V - v0);
@@ -1126,7 +1127,7 @@ bool grad_out(Product& g, void* to, uint32_t rows, uint64_t ld, int dtype) {
   return !g.grad.boxes || tc::make_map(&g.out, to, g.n, rows, 1, ld, ld, 32, g.grad.f32);
 }
 
-int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm, const float* up, void* dh, uint64_t ld_dh,
+int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss, const float* norm, const float* up, void* dh, uint64_t ld_dh,
               void* dw, uint64_t ld_dw, unsigned char* ws) {
   DeviceGuard dg(ctx_device(c), "cg_head_grad");
   if (!dg.ok) return CG_E_CUDA;
@@ -1137,7 +1138,6 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const float* loss, const float* norm
   if (a.B == 0)  // no rows: the weight's gradient is zero
     return !dw || cudaMemset2DAsync(dw, ld_dw * size, 0, size_t(a.D) * size, a.V, v.stream) == cudaSuccess ? CG_OK
                                                                                                             : CG_E_CUDA;
-  const HeadPlan p = plan_head(a.hidden, a.ld_h, a.weight, a.ld_w, a.dtype, a.B, a.V, a.D, true);
   Operands o{a.hidden, a.weight, a.ld_h, a.ld_w};
   __nv_bfloat16* terms = reinterpret_cast<__nv_bfloat16*>(ws + p.at_terms);
   const uint64_t part_stride = uint64_t(p.B) * p.ld_terms;
@@ -1228,10 +1228,10 @@ extern "C" int cg_head_loss(cg_ctx* c, const void* d_hidden, const void* d_weigh
   if (rc != CG_OK) return rc;
   if (B == 0) return CG_OK;
   if (!d_out_loss || !aligned4(d_out_loss) || !aligned4(d_out_lse) || !aligned4(d_out_norm)) return CG_E_ARG;
-  if (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256 ||
-      workspace_bytes < plan_head(d_hidden, ld_hidden, d_weight, ld_weight, dtype, B, V, D, false).bytes)
-    return CG_E_ARG;
-  return head_loss(c, a, d_out_loss, d_out_lse, d_out_norm, static_cast<unsigned char*>(d_workspace));
+  const HeadPlan p = plan_head(d_hidden, ld_hidden, d_weight, ld_weight, dtype, B, V, D, false);
+  if (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256) return CG_E_ARG;
+  if (workspace_bytes < p.bytes) return CG_E_NOMEM;
+  return head_loss(c, a, p, d_out_loss, d_out_lse, d_out_norm, static_cast<unsigned char*>(d_workspace));
 }
 
 extern "C" int cg_head_grad(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtype, uint32_t B, uint32_t V,
@@ -1256,9 +1256,9 @@ extern "C" int cg_head_grad(cg_ctx* c, const void* d_hidden, const void* d_weigh
       return CG_E_ARG;
   }
   if (out[0] && out[1] && matrices_meet(out[0], rows[0], ld[0], out[1], rows[1], ld[1], D, size)) return CG_E_ARG;
-  if (B && (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256 ||
-            workspace_bytes < plan_head(d_hidden, ld_hidden, d_weight, ld_weight, dtype, B, V, D, true).bytes))
-    return CG_E_ARG;
-  return head_grad(c, a, d_loss, d_norm, d_grad_loss, d_out_grad_hidden, ld_grad_hidden, d_out_grad_weight,
+  const HeadPlan p = plan_head(d_hidden, ld_hidden, d_weight, ld_weight, dtype, B, V, D, true);
+  if (B && (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256)) return CG_E_ARG;
+  if (B && workspace_bytes < p.bytes) return CG_E_NOMEM;
+  return head_grad(c, a, p, d_loss, d_norm, d_grad_loss, d_out_grad_hidden, ld_grad_hidden, d_out_grad_weight,
                    ld_grad_weight, static_cast<unsigned char*>(d_workspace));
 }

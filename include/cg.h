@@ -60,7 +60,7 @@ extern "C" {
 #define CG_E_LIMIT          -6  /* automaton, table or token length beyond a library limit */
 #define CG_E_CUDA           -7  /* a CUDA runtime call failed */
 #define CG_E_DEVICE         -8  /* cg_ctx_status: the device recorded an error */
-#define CG_E_NOMEM          -9  /* host allocation failed */
+#define CG_E_NOMEM          -9  /* host allocation failed; a workspace smaller than the call wants */
 
 /* ---- enumerations ---------------------------------------------------------- */
 #define CG_GBNF        0        /* GBNF-style rule text, start rule "root" */
@@ -563,8 +563,9 @@ int cg_distill_grad_norm(cg_ctx* c, const void* d_logits, int dtype, uint32_t B,
  *  Sums are held in 32 bits or more, results are rounded once to the dtype, and none
  *  depends on the order in which the device runs its blocks.  The calls allocate
  *  nothing, may be captured, and run on the context's stream.  Errors: CG_E_ARG (a
- *  NULL required pointer, an unknown dtype, a size, pitch, alignment or workspace out
- *  of range, matrices that share memory), CG_E_LIMIT, CG_E_CUDA. */
+ *  NULL required pointer, an unknown dtype, a size, pitch or alignment out of range,
+ *  matrices that share memory), CG_E_LIMIT, CG_E_NOMEM (a workspace too small),
+ *  CG_E_CUDA. */
 
 /* out[i] = scale * table[d_tokens[i]] for i < N, rounded to the dtype; zeros for a row
  * without a token.

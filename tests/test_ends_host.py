@@ -57,7 +57,7 @@ def calls_on(device):
 
 
 class AcceptingLibrary:
-    """Says that every call wants 1024 bytes of workspace, and counts the others."""
+    """Every call that takes a workspace (its last two arguments) wants 1024 bytes; the calls that were accepted."""
 
     def __init__(self):
         self.calls = []
@@ -66,8 +66,10 @@ class AcceptingLibrary:
         def entry(*args):
             if name.endswith("_workspace"):
                 args[-1]._obj.value = 1024
-            else:
-                self.calls.append(name)
+                return _lib.CG_OK
+            if name != "cg_embed" and args[-1] < 1024:
+                return _lib.CG_E_NOMEM
+            self.calls.append(name)
             return _lib.CG_OK
         return entry
 
@@ -96,8 +98,9 @@ def test_a_small_workspace_is_refused(monkeypatch, name):
     library = AcceptingLibrary()
     monkeypatch.setattr(_lib, "lib", lambda: library)
     call, there = calls_on(1)[name]
-    with pytest.raises(gcd.CgError):
+    with pytest.raises(gcd.CgError) as e:
         call(**{**there, "workspace": Stub((1023,), torch.uint8, 1)})
+    assert e.value.code == _lib.CG_E_NOMEM
     with pytest.raises(gcd.CgError):
         call(**{**there, "workspace": Stub((4096,), torch.int32, 1)})
     assert not library.calls
