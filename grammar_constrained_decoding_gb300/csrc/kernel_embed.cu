@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   using E = Elems<BF16, BYTES>;
   using Vec = typename E::Vec;
   constexpr uint32_t kAhead = 8, kWindow = kMostChunk + 2 * kMostShort;
-  __shared__ uint32_t key[kWindow], pos[kMostChunk + kMostShort];
+  __shared__ uint32_t key[kWindow];
+  __shared__ uint64_t row[kMostChunk + kMostShort];   // where the positions' rows begin
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t chunk = blockIdx.x / a.slabs, lane = threadIdx.x & 31;
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
     const uint32_t at = from + i - kMostShort;
     key[i] = from + i < kMostShort || at >= a.N ? CG_NO_TOKEN : a.key[at];
   }
-  for (uint32_t i = threadIdx.x; i < n + kMostShort; i += kSumThreads) pos[i] = from + i < a.N ? a.pos[from + i] : 0u;
+  for (uint32_t i = threadIdx.x; i < n + kMostShort; i += kSumThreads) row[i] = from + i < a.N ? a.pos[from + i] * a.pitch : 0u;
   __syncthreads();
   // a run of up to two chunks is summed by the chunk it begins in: [begin, end) of the positions
   // from `from` on
@@ -396,6 +397,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   // a longer run is for the join: it begins here
   if (tail_part && tail < a.V && threadIdx.x == 0 && blockIdx.x == chunk * a.slabs) a.runs[1 + atomicAdd(a.runs, 1u)] = chunk;
   if (col0 >= a.vecs) return;
+  // rows without a token come last
+  while (end > begin && k0[end - 1] >= a.V) --end;
   const char* in = a.grad + uint64_t(col0) * BYTES;
   float acc[kCols][E::kN] = {};
   bool first = head_part;   // the run at hand began before the chunk
@@ -405,14 +408,13 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
     for (uint32_t u = 0; u < kAhead; ++u)
 #pragma unroll
       for (uint32_t q = 0; q < kCols; ++q)
-        if (i0 + u < end && k0[i0 + u] < a.V && col0 + q * kSumThreads < a.vecs)
-          v[u][q] = *reinterpret_cast<const Vec*>(in + pos[i0 + u] * a.pitch + q * (kSumThreads * BYTES));
+        if (i0 + u < end && (q == 0 || col0 + q * kSumThreads < a.vecs))
+          v[u][q] = *reinterpret_cast<const Vec*>(in + row[i0 + u] + q * (kSumThreads * BYTES));
 #pragma unroll
     for (uint32_t u = 0; u < kAhead; ++u) {
       const uint32_t i = i0 + u;
       if (i >= end) break;
       const uint32_t token = k0[i];
-      if (token >= a.V) break;   // rows without a token come last
 #pragma unroll
       for (uint32_t q = 0; q < kCols; ++q) {
         float x[E::kN];

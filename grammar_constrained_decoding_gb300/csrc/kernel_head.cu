@@ -47,14 +47,17 @@ enum Readout { kLoss, kTerms, kOut };
 // stage, in chains, the five small ones in an accumulator of their own (in the large one's they
 // would each cost a step that is not rounded to nearest).
 enum Sums { kOne, kChains, kParts };
-constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : 1; }
+constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : 1; }  // of a stage
 
-// a block's share of a stage, and how many fit beside the readers' boxes
-template <int CTAS, Readout READ>
+// A block's share of a stage, and how many fit beside the readers' boxes.  Float matrices' stages
+// hold all three parts of both operands, and a single block's tile then has 128 columns.
+template <int CTAS, Readout READ, Sums SUMS>
 struct Stage {
-  static constexpr uint32_t kA = kBlockM * kBlockK * 2;
-  static constexpr uint32_t kB = kTileN / CTAS * kBlockK * 2;
-  static constexpr uint32_t kBytes = kA + kB;
+  static constexpr uint32_t kParts = SUMS == Sums::kParts ? 3 : 1;
+  static constexpr uint32_t kWidth = SUMS == Sums::kParts && CTAS == 1 ? 128 : kTileN;   // most columns of a tile
+  static constexpr uint32_t kA = kBlockM * kBlockK * 2;                                   // one part's
+  static constexpr uint32_t kB = kWidth / CTAS * kBlockK * 2;
+  static constexpr uint32_t kBytes = kParts * (kA + kB);
   static constexpr uint32_t kBoxes = READ == kLoss ? 0 : kBoxesEach;   // a reader's boxes under way
   static constexpr uint32_t kCount = (kMaxSmem - 2048 - kReaders * kBoxes * kStore) / kBytes;
 };
@@ -137,8 +140,8 @@ struct Turns {
 struct Work {
   uint32_t m0, n0, split, k0, k1;
 };
-template <bool NARROW>
-__device__ __forceinline__ uint32_t width(const Product& p) { return NARROW ? p.tile_n : kTileN; }
+template <typename S, bool NARROW>
+__device__ __forceinline__ uint32_t width(const Product& p) { return NARROW ? p.tile_n : S::kWidth; }
 // An item's stages: all of them, or its split's (blocks * splits fits 32 bits)
 __device__ __forceinline__ void stages_of(const Product& p, uint32_t t, Work& w) {
   w.split = 0;
@@ -151,7 +154,7 @@ __device__ __forceinline__ void stages_of(const Product& p, uint32_t t, Work& w)
   }
 }
 // Bands of row tiles over all columns: what runs at one time shares both operands in L2
-template <int CTAS, bool NARROW>
+template <int CTAS, typename S, bool NARROW>
 __device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {
   Work w;
   stages_of(p, t, w);
@@ -160,10 +163,10 @@ __device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {
   const uint32_t rows = min(kBand, p.n_m - band * kBand);
   w.n0 = in / rows;
   w.m0 = (band * kBand + in - w.n0 * rows) * kBlockM * CTAS;
-  w.n0 *= width<NARROW>(p);
+  w.n0 *= width<S, NARROW>(p);
   return w;
 }
-// the parts of the i-th of the six products of a stage; the last is the largest
+// the parts of the i-th of the six products of a stage; the last is the large one
 __device__ __forceinline__ uint32_t part_a(uint32_t i) { return (0x001012u >> (4 * i)) & 15u; }
 __device__ __forceinline__ uint32_t part_b(uint32_t i) { return (0x010210u >> (4 * i)) & 15u; }
 
@@ -441,33 +444,33 @@ struct Place {
   }
 };
 
-// An item's stages into the ring: a block brings its 128 rows of A and its share of B's 256.
-// With a pair the leader's barrier counts the bytes of both.  Six products of a stage follow
-// one another: the parts that they share come from L2.
-template <int CTAS, typename S, Sums SUMS, bool NARROW, bool A_MN, bool B_MN>
+// An item's stages into the ring: a block brings its 128 rows of A and its share of B's, all
+// their parts.  With a pair the leader's barrier counts the bytes of both.
+template <int CTAS, typename S, bool NARROW, bool A_MN, bool B_MN>
 __device__ __forceinline__ bool copy_item(const Product& p, const Work& w, uint32_t rank, uint32_t ring, Ends& ends, Place& at,
                                           uint32_t& issued) {
-  const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * (width<NARROW>(p) / CTAS));
-  const uint32_t share = width<NARROW>(p) / CTAS, bytes = (S::kA + share * (kBlockK * 2)) * CTAS;
+  const uint32_t share = width<S, NARROW>(p) / CTAS, bytes = S::kParts * (S::kA + share * (kBlockK * 2)) * CTAS;
+  const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * share);
   for (uint32_t k = w.k0; k < w.k1; ++k) {
     const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
-    for (uint32_t i = 0; i < products_of(SUMS); ++i) {
-      const int pa = SUMS == kParts ? int(part_a(i)) : 0, pb = SUMS == kParts ? int(part_b(i)) : 0;
-      if (!mbar_wait(&ends.empty[at.s], at.phase ^ 1)) return false;
-      const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[at.s]), 0) : smem_addr(&ends.full[at.s]);
-      if (rank == 0) mbar_expect_tx(&ends.full[at.s], bytes);
-      const uint32_t a = ring + at.s * S::kBytes, b = a + S::kA;
+    if (!mbar_wait(&ends.empty[at.s], at.phase ^ 1)) return false;
+    const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[at.s]), 0) : smem_addr(&ends.full[at.s]);
+    if (rank == 0) mbar_expect_tx(&ends.full[at.s], bytes);
+#pragma unroll
+    for (uint32_t part = 0; part < S::kParts; ++part) {
+      const uint32_t a = ring + at.s * S::kBytes + part * S::kA, b = ring + at.s * S::kBytes + S::kParts * S::kA + part * S::kB;
       if (A_MN)
-        for (uint32_t q = 0; q < kBlockM / 64; ++q) tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, pa, full);
-      else tc::copy_box<CTAS>(a, &p.a, ak, am, pa, full);
+        for (uint32_t q = 0; q < kBlockM / 64; ++q)
+          tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, int(part), full);
+      else tc::copy_box<CTAS>(a, &p.a, ak, am, int(part), full);
       if (B_MN)
-        for (uint32_t q = 0; q < share / 64; ++q) tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, pb, full);
+        for (uint32_t q = 0; q < share / 64; ++q) tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, int(part), full);
       else
         for (uint32_t q = 0; q < (share + 127) / 128; ++q)   // boxes of 128 rows, or of all where they are fewer
-          tc::copy_box<CTAS>(b + q * 16384, &p.b, bk, bn + int(128 * q), pb, full);
-      ++issued;
-      at.template step<S::kCount>();
+          tc::copy_box<CTAS>(b + q * 16384, &p.b, bk, bn + int(128 * q), int(part), full);
     }
+    ++issued;
+    at.template step<S::kCount>();
   }
   return true;
 }
@@ -483,22 +486,28 @@ __device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, 
     const uint32_t acc = SUMS == kParts ? 0u : n & 1u, round = SUMS == kParts ? n : n >> 1;
     if (!mbar_wait(&ends.tile_empty[acc], (round & 1u) ^ 1u)) return false;
     tc::fence_after_sync();
-    for (uint32_t begin = k; k < end; ++k) {
+    for (bool add = false; k < end; ++k, add = true) {
+      if (!ready && !mbar_wait(&ends.full[at.s], at.phase)) return false;
+      tc::fence_after_sync();
+      const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kParts * S::kA);
+      if (SUMS == kParts) {
 #pragma unroll 1
-      for (uint32_t i = 0; i < products_of(SUMS); ++i) {
-        if (!ready && !mbar_wait(&ends.full[at.s], at.phase)) return false;
-        tc::fence_after_sync();
-        const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kA);
-        const bool large = SUMS != kParts || i + 1 == products_of(SUMS);
-        const bool add = k != begin || (SUMS == kParts && i != 0 && !large);
-        const uint32_t to = tmem + (SUMS == kParts && !large ? kTileN : acc * kTileN);
+        for (uint32_t i = 0; i < 6; ++i) {   // the large product last, in an accumulator of its own
+          const uint64_t pa = a + part_a(i) * (S::kA >> 4), pb = b + part_b(i) * (S::kB >> 4);
+          const uint32_t to = tmem + (i < 5 ? kTileN : 0u);
+          const bool more = add || (i != 0 && i != 5);
+#pragma unroll
+          for (uint32_t q = 0; q < kBlockK / 16; ++q)
+            tc::mma<CTAS>(to, pa + q * tc::kStep16<A_MN>, pb + q * tc::kStep16<B_MN>, instr, more || q != 0);
+        }
+      } else {
 #pragma unroll
         for (uint32_t q = 0; q < kBlockK / 16; ++q)
-          tc::mma<CTAS>(to, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
-        tc::commit<CTAS>(&ends.empty[at.s]);
-        at.template step<S::kCount>();
-        ready = tc::mbar_test(&ends.full[at.s], at.phase);
+          tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
       }
+      tc::commit<CTAS>(&ends.empty[at.s]);
+      at.template step<S::kCount>();
+      ready = tc::mbar_test(&ends.full[at.s], at.phase);
     }
     tc::commit<CTAS>(&ends.tile_full[acc]);
   }
@@ -507,7 +516,7 @@ __device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, 
 
 template <int CTAS, Readout READ, Sums SUMS, bool NARROW>
 __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_constant__ Job job) {
-  using S = Stage<CTAS, READ>;
+  using S = Stage<CTAS, READ, SUMS>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;   // the swizzle's pattern repeats every 1024 bytes
   const uint32_t boxes_at = ring + S::kCount * S::kBytes;
@@ -547,9 +556,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       bool ok = true;
       while (ok && turns.next(second, t)) {
         if (READ == kOut && second) {
-          ok = copy_item<CTAS, S, SUMS, false, true, true>(job.p[1], work_of<CTAS, false>(job.p[1], t), rank, ring, ends, at, issued);
+          ok = copy_item<CTAS, S, false, true, true>(job.p[1], work_of<CTAS, S, false>(job.p[1], t), rank, ring, ends, at, issued);
         } else {
-          ok = copy_item<CTAS, S, SUMS, NARROW, false, READ == kOut>(job.p[0], work_of<CTAS, NARROW>(job.p[0], t), rank, ring, ends, at, issued);
+          ok = copy_item<CTAS, S, NARROW, false, READ == kOut>(job.p[0], work_of<CTAS, S, NARROW>(job.p[0], t), rank, ring, ends, at, issued);
         }
       }
       if (!ok) {
@@ -570,10 +579,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         Work w;
         if (READ == kOut && second) {
           stages_of(job.p[1], t, w);
-          ok = multiply_item<CTAS, S, SUMS, true, true>(kTileN, w.k1 - w.k0, ring, tmem, ends, at, ready, n);
+          ok = multiply_item<CTAS, S, SUMS, true, true>(S::kWidth, w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         } else {
           stages_of(job.p[0], t, w);
-          ok = multiply_item<CTAS, S, SUMS, false, READ == kOut>(width<NARROW>(job.p[0]), w.k1 - w.k0, ring, tmem, ends, at, ready, n);
+          ok = multiply_item<CTAS, S, SUMS, false, READ == kOut>(width<S, NARROW>(job.p[0]), w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         }
       }
       if (!ok) {
@@ -606,9 +615,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       return true;
     };
     auto read_item = [&](const Product& p) {
-      const Work w = work_of<CTAS, NARROW>(p, t);
+      const Work w = work_of<CTAS, S, NARROW>(p, t);
       // the reader's columns: half of the tile's, at least 64 (the second half's readers then have none)
-      const uint32_t wide = NARROW ? max(64u, p.tile_n / 2) : 128u, chunks = !NARROW ? 4u : half * wide < width<NARROW>(p) ? wide / 32 : 0;
+      const uint32_t wide = NARROW ? max(64u, p.tile_n / 2) : S::kWidth / 2;
+      const uint32_t chunks = !NARROW ? S::kWidth / 64 : half * wide < p.tile_n ? wide / 32 : 0;
       const uint32_t row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane, col = w.n0 + half * wide;
       const uint32_t blocks = w.k1 - w.k0;
       uint32_t words[4], target = CG_NO_TOKEN;
@@ -698,10 +708,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
   if (warp == 2) tc::tmem_free<CTAS>(tmem);
 }
 
-template <int CTAS, Readout READ>
+template <int CTAS, Readout READ, Sums SUMS>
 constexpr size_t product_smem() {
-  using S = Stage<CTAS, READ>;
-  static_assert(S::kCount <= 7 && S::kCount >= 3, "barriers for the stages");
+  using S = Stage<CTAS, READ, SUMS>;
+  static_assert(S::kCount <= 7 && S::kCount >= 2, "barriers for the stages");
   return 1024 + size_t(S::kCount) * S::kBytes + size_t(kReaders) * S::kBoxes * kStore + sizeof(Ends);
 }
 static_assert(sizeof(Ends) <= 1024, "the ring, the boxes and the barriers fit a block's shared memory");
@@ -853,25 +863,28 @@ __global__ void __launch_bounds__(256) join_many_kernel(const float* sums, uint3
 // that add up to the value (8 bits each; a value that is not finite is its first part).  A
 // thread writes 8 columns at once.
 struct Layout {
-  const void* from;          // null: not this one
+  const void* from;
   uint64_t ld;
-  uint32_t rows;
+  uint32_t rows;             // 0: not this one
   bool wide;                 // the rows lie on the 16-byte grid
   __nv_bfloat16* to;         // [parts][rows][Dp]
 };
 struct Layouts {
-  Layout m[2];               // hidden, weight: blockIdx.y
+  Layout hidden, weight;
 };
 template <bool F32>
 __global__ void __launch_bounds__(256) lay_out_kernel(const Layouts both, uint32_t D, uint32_t Dp) {
   griddep_launch_dependents();
   griddep_wait();
-  const Layout a = both.m[blockIdx.y];
   const uint32_t groups = Dp / 8;
-  const uint64_t all = a.from ? uint64_t(a.rows) * groups : 0, step = uint64_t(gridDim.x) * 256, n = uint64_t(a.rows) * Dp;
+  const uint64_t all = uint64_t(both.hidden.rows + both.weight.rows) * groups, step = uint64_t(gridDim.x) * 256;
   for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += step) {
-    const uint64_t r = all >> 32 ? i / groups : uint32_t(i) / groups;
+    uint64_t r = all >> 32 ? i / groups : uint32_t(i) / groups;
     const uint32_t d = uint32_t(i - r * groups) * 8;
+    const bool first = r < both.hidden.rows;
+    const Layout& a = first ? both.hidden : both.weight;
+    if (!first) r -= both.hidden.rows;
+    const uint64_t n = uint64_t(a.rows) * Dp;
     if (!F32) {
       const uint16_t* x = static_cast<const uint16_t*>(a.from) + r * a.ld + d;
       uint32_t w[4];
@@ -927,6 +940,7 @@ struct HeadPlan {
   uint32_t B, V, D, Dp, parts;
   bool lay_h, lay_w;
   uint32_t piece;            // tokens of a piece: a multiple of 256 unless it is all of them
+  uint32_t out_n;            // columns of the gradients' tiles
   uint32_t tile_n, groups;   // columns of the logits' tiles; column groups of their readers
   uint64_t ld_terms, ld_sums;
   uint32_t splits;           // of the product that sums over tokens
@@ -937,8 +951,7 @@ struct HeadPlan {
 // Columns of the logits' tiles: few rows' are halved, and halved again, while the blocks are twice
 // as many as the tiles.  (Where every block has a tile, narrow ones read the rows' operand more
 // often for nothing: 4 x 48675 x 3520 in 191 tiles of 256 80 us, in 381 of 128 121.)
-uint32_t tile_width(uint32_t B, uint32_t columns) {
-  uint32_t w = kTileN;
+uint32_t tile_width(uint32_t B, uint32_t columns, uint32_t w) {
   while (B <= kBlockM && w > 64 && 2 * tiles_of(columns, w) <= kHeadSms) w /= 2;
   return w;
 }
@@ -964,7 +977,8 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   const uint64_t pieces = (V + most - 1) / most;
   p.piece = uint32_t(std::min<uint64_t>(up_to((V + pieces - 1) / pieces, 256), V));
   const uint32_t slots = kHeadSms / (p.pair ? 2 : 1);
-  p.tile_n = tile_width(B, p.piece);
+  p.out_n = p.parts > 1 && !p.pair ? 128 : kTileN;
+  p.tile_n = tile_width(B, p.piece, p.out_n);
   p.groups = tiles_of(V, std::max(64u, p.tile_n / 2));
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -981,7 +995,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
     p.ld_terms = up_to(p.piece, 8);
     p.at_terms = take(size_t(p.parts) * B * p.ld_terms * 2);
     p.ld_sums = up_to(D, 4);
-    const uint32_t tiles = tiles_of(B, kBlockM * (p.pair ? 2 : 1)) * tiles_of(D, kTileN);
+    const uint32_t tiles = tiles_of(B, kBlockM * (p.pair ? 2 : 1)) * tiles_of(D, p.out_n);
     const uint32_t blocks = tiles_of(p.piece, kBlockK);
     p.splits = std::max(1u, std::min(slots / std::max(tiles, 1u), blocks / 8));
     if (p.splits > 1 || p.piece < V) p.at_sums = take(size_t(p.splits) * B * p.ld_sums * 4);
@@ -1005,7 +1019,7 @@ cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
   // what one item of the first product is worth in items of the second
   j.early = longest[1] ? (longest[0] + longest[1] / 2) / longest[1] : 0;
   return launch_clusters<product_kernel<CTAS, READ, SUMS, NARROW>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
-                                                             kHeadThreads, product_smem<CTAS, READ>(), stream, j);
+                                                             kHeadThreads, product_smem<CTAS, READ, SUMS>(), stream, j);
 }
 // Results in 32 bits are summed in chains (losses, and all
 // that float matrices give): a long chain of sums in tensor memory drifts, as its steps are not
@@ -1021,7 +1035,7 @@ template <Readout READ>
 cudaError_t launch_job(int device, const HeadPlan& p, Job& j, cudaStream_t stream) {
   const bool f32 = p.parts > 1;
   if (p.pair) return launch_job<2, READ, false>(device, f32, j, stream);
-  if (READ != kOut && p.tile_n < kTileN) return launch_job<1, READ, READ != kOut>(device, f32, j, stream);
+  if (READ != kOut && p.tile_n < p.out_n) return launch_job<1, READ, READ != kOut>(device, f32, j, stream);
   return launch_job<1, READ, false>(device, f32, j, stream);
 }
 
@@ -1050,21 +1064,21 @@ cudaError_t lay_out(const HeadArgs& a, const HeadPlan& p, uint32_t v0, uint32_t 
   Layouts both = {};
   uint32_t rows = 0;
   if (p.lay_h && v0 == 0) {
-    both.m[0] = Layout{a.hidden, a.ld_h, p.B, rows_on_grid(a.hidden, a.dtype, a.ld_h),
+    both.hidden = Layout{a.hidden, a.ld_h, p.B, rows_on_grid(a.hidden, a.dtype, a.ld_h),
                        reinterpret_cast<__nv_bfloat16*>(ws + p.at_h)};
     o.h = ws + p.at_h;
     o.ld_h = p.Dp;
-    rows = p.B;
+    rows += p.B;
   }
   if (p.lay_w) {
-    both.m[1] = Layout{static_cast<const char*>(a.weight) + uint64_t(v0) * a.ld_w * dtype_size(a.dtype), a.ld_w, n,
+    both.weight = Layout{static_cast<const char*>(a.weight) + uint64_t(v0) * a.ld_w * dtype_size(a.dtype), a.ld_w, n,
                        rows_on_grid(a.weight, a.dtype, a.ld_w), reinterpret_cast<__nv_bfloat16*>(ws + p.at_w)};
     o.w = ws + p.at_w;
     o.ld_w = p.Dp;
-    rows = std::max(rows, n);
+    rows += n;
   }
   if (!rows) return cudaSuccess;
-  const dim3 grid(uint32_t(std::min<uint64_t>((uint64_t(rows) * (p.Dp / 8) + 255) / 256, kHeadSms * 16)), 2);
+  const dim3 grid(uint32_t(std::min<uint64_t>((uint64_t(rows) * (p.Dp / 8) + 255) / 256, 1u << 30)));
   return launch_dependent(f32 ? lay_out_kernel<true> : lay_out_kernel<false>, grid, dim3(256), 0, stream, both, p.D, p.Dp);
 }
 bool map_h(CUtensorMap* map, const HeadPlan& p, const Operands& o, uint32_t box) {
@@ -1164,7 +1178,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       q.n = p.D;
       q.blocks = tiles_of(n, kBlockK);
       q.splits = p.splits;
-      q.tile_n = kTileN;
+      q.tile_n = p.out_n;
       q.b_k = p.lay_w ? 0 : int(v0);
       if (summed) {
         q.grad.boxes = q.grad.f32 = true;
@@ -1182,7 +1196,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       q.n = p.D;
       q.blocks = tiles_of(p.B, kBlockK);
       q.splits = 1;
-      q.tile_n = kTileN;
+      q.tile_n = p.out_n;
       if (!grad_out(q, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
       if (!tc::make_map(&q.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&q.b, p, o, 64)) return CG_E_CUDA;
     }
