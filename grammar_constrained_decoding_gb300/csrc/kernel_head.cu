@@ -948,11 +948,13 @@ struct HeadPlan {
   size_t at_h, at_w, at_part, at_target, at_terms, at_sums, bytes;
 };
 
-// Columns of the logits' tiles: few rows' are halved, and halved again, while the blocks are twice
-// as many as the tiles.  (Where every block has a tile, narrow ones read the rows' operand more
-// often for nothing: 4 x 48675 x 3520 in 191 tiles of 256 80 us, in 381 of 128 121.)
-uint32_t tile_width(uint32_t B, uint32_t columns, uint32_t w) {
-  while (B <= kBlockM && w > 64 && 2 * tiles_of(columns, w) <= kHeadSms) w /= 2;
+// Columns of the logits' tiles: halved, and halved again, where that takes a third of the time
+// off what the tiles' rounds over all blocks take (few tiles: 95 rows of 18944 tokens in 74 tiles
+// of 256 on 152 blocks).  Narrow tiles read the rows' operand more often: 4 x 48675 x 3520 in two
+// rounds of 256 80 us, in three of 128 121.
+uint32_t tile_width(uint32_t row_tiles, uint32_t columns, uint32_t slots, uint32_t w) {
+  auto rounds = [&](uint32_t width) { return (uint64_t(row_tiles) * tiles_of(columns, width) + slots - 1) / slots; };
+  while (w > 64 && 3 * rounds(w / 2) < 4 * rounds(w)) w /= 2;
   return w;
 }
 
@@ -978,7 +980,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   p.piece = uint32_t(std::min<uint64_t>(up_to((V + pieces - 1) / pieces, 256), V));
   const uint32_t slots = kHeadSms / (p.pair ? 2 : 1);
   p.out_n = p.parts > 1 && !p.pair ? 128 : kTileN;
-  p.tile_n = tile_width(B, p.piece, p.out_n);
+  p.tile_n = tile_width(tiles_of(B, kBlockM * (p.pair ? 2 : 1)), p.piece, slots, p.out_n);
   p.groups = tiles_of(V, std::max(64u, p.tile_n / 2));
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1034,9 +1036,10 @@ cudaError_t launch_job(int device, bool f32, Job& j, cudaStream_t stream) {
 template <Readout READ>
 cudaError_t launch_job(int device, const HeadPlan& p, Job& j, cudaStream_t stream) {
   const bool f32 = p.parts > 1;
-  if (p.pair) return launch_job<2, READ, false>(device, f32, j, stream);
-  if (READ != kOut && p.tile_n < p.out_n) return launch_job<1, READ, READ != kOut>(device, f32, j, stream);
-  return launch_job<1, READ, false>(device, f32, j, stream);
+  if (READ != kOut && p.tile_n < p.out_n)
+    return p.pair ? launch_job<2, READ, READ != kOut>(device, f32, j, stream)
+                  : launch_job<1, READ, READ != kOut>(device, f32, j, stream);
+  return p.pair ? launch_job<2, READ, false>(device, f32, j, stream) : launch_job<1, READ, false>(device, f32, j, stream);
 }
 
 struct HeadArgs {
