@@ -10,13 +10,20 @@
 // pair of blocks, 256) x 256 on the tensor cores, operands by tensor copies through a ring
 // of stages, two accumulators in tensor memory so that a tile is read out while the next
 // is multiplied.  What is done to a tile as it is read out makes the difference:
-//   kLoss  each row's maximum and sum of exponentials over 128 columns (target apart);
+//   kLoss  each row's maximum and sum of exponentials over a reader's columns (target apart);
 //   kTerms d, rounded to bf16, for a piece of the vocabulary: it bounds the memory;
 //   kOut   a gradient's elements.
 // d is rounded to bf16 because the tensor cores multiply bf16: its relative error of at most 2^-8
 // is the size of the gradients' own rounding.  Float inputs, and d then, are split into
 // three bf16 parts of 8 bits each, and the six products of parts that are not below 2^-24
-// are summed, the smallest first.
+// are summed, the five small ones apart from the large one.
+//
+// Bound by the tensor cores where rows are many: 4096 x 128256 x 2048, loss and gradients, 8.6
+// TFLOP with the logits twice in 5.0 ms, 1.72 PFLOP/s, what a plain library product sustains at
+// the card's power limit (1.73); the gradients' launch keeps the tensor pipe 92 % busy (2048 rows,
+// K = 2048).  Few rows are bound by reading the weight: 256 x 128256 x 4096 masked 200 us, 5.3 TB/s.
+// Between those, what stands in the way: an accumulator's 256 x 256 tile takes as many bytes a
+// cycle from L2 as an SM can get (64), and a stage 560 to 600 cycles instead of 512.
 #include <algorithm>
 
 #include "logit_row.cuh"
@@ -34,11 +41,10 @@ constexpr uint32_t kBlockK = 64;          // k of a stage: 128 bytes of bf16
 constexpr uint32_t kReaders = 8;          // warps that read tiles out: four row quarters x two column halves
 constexpr uint32_t kFirstReader = 4;      // after the copying, the multiplying and the allocating warp, and a spare
 constexpr uint32_t kHeadThreads = (kFirstReader + kReaders) * 32;
-constexpr uint32_t kChain = 16;           // stages whose products are summed in tensor memory: 1024 k
 constexpr uint32_t kStore = 4096;         // bytes of a box that a reader writes out: 32 rows of 128 bytes
-constexpr uint32_t kBand = 16;            // row tiles that are taken together over all columns
-constexpr uint32_t kBoxesEach = 1;
-constexpr uint32_t kReadBoxes = 13, kReadElements = 32;   // stages multiplied while a gradient's tile is read out
+constexpr uint32_t kBand = 16;            // row tiles that are taken together over all columns (4096 x 151936 x 1024: 713 us; 4: 755, 32: 713)
+constexpr uint32_t kBoxesEach = 1;        // a reader's boxes under way (two, with a stage less: 106.6 -> 108.5 us, 364 -> 368)
+constexpr uint32_t kReadBoxes = 13, kReadElements = 32;   // stages' time that reading a gradient's tile out takes, at least
 constexpr uint32_t kHeadSms = 152;
 
 enum Readout { kLoss, kTerms, kOut };
@@ -48,6 +54,11 @@ enum Readout { kLoss, kTerms, kOut };
 // would each cost a step that is not rounded to nearest).
 enum Sums { kOne, kChains, kParts };
 constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : 1; }  // of a stage
+// Stages of a chain.  A chain of sums in tensor memory drifts, as its steps are not rounded to
+// nearest: over 16 stages (1024 k) losses are 2e-7 to 7e-7 off (in one chain of 4096 k 2.2e-6),
+// over 4 a quarter of that.  4 for float matrices (their gradients 4e-7 off against 1.1e-6, for 3 %
+// of the time) and for few rows, which wait for memory; 16 for many (4: 968 us where 16 take 714).
+constexpr uint32_t chain_of(Sums sums, int ctas) { return sums == kParts || ctas == 1 ? 4 : 16; }
 
 // A block's share of a stage, and how many fit beside the readers' boxes.  Float matrices' stages
 // hold all three parts of both operands, and a single block's tile then has 128 columns.
@@ -58,7 +69,7 @@ struct Stage {
   static constexpr uint32_t kA = kBlockM * kBlockK * 2;                                   // one part's
   static constexpr uint32_t kB = kWidth / CTAS * kBlockK * 2;
   static constexpr uint32_t kBytes = kParts * (kA + kB);
-  static constexpr uint32_t kBoxes = READ == kLoss ? 0 : kBoxesEach;   // a reader's boxes under way
+  static constexpr uint32_t kBoxes = READ == kLoss ? 0 : kBoxesEach;
   static constexpr uint32_t kCount = (kMaxSmem - 2048 - kReaders * kBoxes * kStore) / kBytes;
 };
 
@@ -482,7 +493,7 @@ __device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, 
                                               uint32_t& n) {
   const uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, tile_n);
   for (uint32_t k = 0; k < blocks; ++n) {
-    const uint32_t end = SUMS == kOne ? blocks : min(blocks, k + kChain);
+    const uint32_t end = SUMS == kOne ? blocks : min(blocks, k + chain_of(SUMS, CTAS));
     const uint32_t acc = SUMS == kParts ? 0u : n & 1u, round = SUMS == kParts ? n : n >> 1;
     if (!mbar_wait(&ends.tile_empty[acc], (round & 1u) ^ 1u)) return false;
     tc::fence_after_sync();
@@ -622,6 +633,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       const uint32_t row0 = w.m0 + rank * kBlockM + quarter * 32, r = row0 + lane, col = w.n0 + half * wide;
       const uint32_t blocks = w.k1 - w.k0;
       uint32_t words[4], target = CG_NO_TOKEN;
+      const bool rows = row0 < p.m;   // the warp has rows at all
       if (READ != kOut) {
         mask_words(job, r, col, words);
         if (r < p.m) target = job.target[r];
@@ -646,12 +658,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < 128; ++i) v[i] = 0.f;
         bool ok = true;
-        for (uint32_t k = 0; k < blocks; k += kChain, ++n) {
+        for (uint32_t k = 0; k < blocks; k += chain_of(SUMS, CTAS), ++n) {
           if (!(ok = full(n))) break;
           const uint32_t acc = SUMS == kParts ? 0u : n & 1u;
 #pragma unroll
           for (uint32_t q = 0; q < 4; ++q) {
-            if (q >= chunks) break;
+            if (q >= chunks || !rows) break;
             uint32_t x[32];
             if (SUMS == kParts) {   // the small ones first
               tc::tmem_load(at + kTileN + 32 * q, x);
@@ -669,14 +681,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         if (!ok) return false;
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j)
-          if (j < chunks) read(v + 32 * j, j, words[j]);
+          if (j < chunks && rows) read(v + 32 * j, j, words[j]);
       } else {
         if (blocks && !full(n)) return false;
         const uint32_t acc = n & 1u;
         n += blocks != 0;
-        if (chunks == 0 && blocks) done(acc);
+        if ((chunks == 0 || !rows) && blocks) done(acc);
 #pragma unroll 1
-        for (uint32_t j = 0; j < chunks; ++j) {
+        for (uint32_t j = 0; rows && j < chunks; ++j) {
           uint32_t x[32];
           float v[32];
           tc::tmem_load(at + acc * kTileN + 32 * j, x);
@@ -933,7 +945,9 @@ __global__ void __launch_bounds__(256) lay_out_kernel(const Layouts both, uint32
 
 // ---- host ------------------------------------------------------------------------------------
 
-constexpr size_t kPieceBytes = size_t(256) << 20;  // of a piece's weight laid out, and of its terms
+// of a piece's weight laid out, and of its terms: 4096 x 128256 x 2048 in pieces of 64 MB 5.45 ms, of
+// 128 5.25, of 256 5.17, of 512 0.3 % less
+constexpr size_t kPieceBytes = size_t(256) << 20;
 
 // What a call works on, and where its workspace's parts lie
 struct HeadPlan {
@@ -1023,13 +1037,11 @@ cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
   return launch_clusters<product_kernel<CTAS, READ, SUMS, NARROW>>(device, std::min(items[0] + items[1], kHeadSms / CTAS), CTAS,
                                                              kHeadThreads, product_smem<CTAS, READ, SUMS>(), stream, j);
 }
-// Results in 32 bits are summed in chains (losses, and all
-// that float matrices give): a long chain of sums in tensor memory drifts, as its steps are not
-// rounded to nearest (the loss of 256 x 128256 x 4096 in one chain 2.2e-6 off, in chains 4.6e-7).
+// Results in 32 bits are summed in chains: losses, and all that float matrices give.
 template <int CTAS, Readout READ, bool NARROW>
 cudaError_t launch_job(int device, bool f32, Job& j, cudaStream_t stream) {
   if (f32) return launch_job<CTAS, READ, kParts, NARROW>(device, j, stream);
-  if (READ == kLoss && j.p[0].blocks > kChain)
+  if (READ == kLoss && j.p[0].blocks > chain_of(kChains, CTAS))
     return launch_job<CTAS, READ, READ == kLoss ? kChains : kOne, NARROW>(device, j, stream);
   return launch_job<CTAS, READ, kOne, NARROW>(device, j, stream);
 }
