@@ -44,6 +44,12 @@ def matrix_of(call: str, t, what: str, dtype, rows: int, dev: int = 0) -> tuple[
     return *rows_of(call, t, what, LOGITS if dtype is None else (dtype,), shape, dev), t.shape[1]
 
 
+try:  # the handle alone: a microsecond less than the stream object
+    from torch._C import _cuda_getCurrentRawStream as raw_stream
+except ImportError:  # a build of torch without CUDA, or one that names it otherwise
+    def raw_stream(dev: int) -> int:
+        return torch.cuda.current_stream(dev).cuda_stream
+
 KEPT_WORKSPACE = 64 << 20   # bytes: what a thread keeps between its calls; larger ones are allocated for each
 
 
@@ -58,7 +64,7 @@ def with_workspace(ctx, call: str, given, need, entry, args) -> None:
         want(call, given, "workspace", (torch.uint8,), given.shape, ctx._dev)
         L.check(call, entry(*args, given.data_ptr(), given.numel()))
         return
-    here = torch.cuda.current_stream(ctx._dev).cuda_stream == ctx._stream
+    here = raw_stream(ctx._dev) == ctx._stream
     may_keep = here and not torch.cuda.is_current_stream_capturing()
     kept = getattr(ctx._kept, "workspace", None) if may_keep else None
     if kept is not None:

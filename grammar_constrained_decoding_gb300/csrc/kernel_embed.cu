@@ -238,8 +238,10 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& s) {
       __syncthreads();
       if (there) {
         const uint32_t to_at = s.tile_base[digit] + s.mine[warp][digit] + nth;
-        __stcg(key_out + to_at, k);
-        __stcg(pos_out + to_at, p);
+        if (to_at < a.N) {   // always, unless the tokens were written meanwhile
+          __stcg(key_out + to_at, k);
+          __stcg(pos_out + to_at, p);
+        }
       }
       __syncthreads();
     }
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
     const uint32_t at = from + i - kMostShort;
     key[i] = from + i < kMostShort || at >= a.N ? CG_NO_TOKEN : a.key[at];
   }
-  for (uint32_t i = threadIdx.x; i < n + kMostShort; i += kSumThreads) row[i] = from + i < a.N ? a.pos[from + i] * a.pitch : 0u;
+  for (uint32_t i = threadIdx.x; i < n + kMostShort; i += kSumThreads) row[i] = from + i < a.N ? min(a.pos[from + i], a.N - 1) * a.pitch : 0u;
   __syncthreads();
   // a run of up to two chunks is summed by the chunk it begins in: [begin, end) of the positions
   // from `from` on
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
 #pragma unroll
       for (uint32_t q = 0; q < kCols; ++q) {
         const uint32_t col = col0 + q * kSumThreads;
-        if (col < a.vecs) {
+        if (col < a.vecs && token < a.V) {   // the token is, unless the tokens were written meanwhile
           if (!part) {
             write_sum<BF16, BYTES>(a, token, col, acc[q]);
           } else {
