@@ -51,9 +51,11 @@ enum Readout { kLoss, kTerms, kOut };
 // How a tile's stages are summed: bf16 products in one accumulator (and the next tile's in
 // the other); in chains of 16 stages, added up in registers; or float matrices' six products a
 // stage, in chains, the five small ones in an accumulator of their own (in the large one's they
-// would each cost a step that is not rounded to nearest).
-enum Sums { kOne, kChains, kParts };
-constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : 1; }  // of a stage
+// would each cost a step that is not rounded to nearest).  kTwo is kOne with terms of two parts:
+// up to 128 rows, whose products wait for the weight, the terms keep 16 bits (rounded to 8, the one
+// term that makes up a row's gradient would double its error).
+enum Sums { kOne, kChains, kParts, kTwo };
+constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : sums == kTwo ? 2 : 1; }  // of a stage
 // Stages of a chain.  A chain of sums in tensor memory drifts, as its steps are not rounded to
 // nearest: over 16 stages (1024 k) losses are 2e-7 to 7e-7 off (in one chain of 4096 k 2.2e-6),
 // over 4 a quarter of that.  4 for float matrices (their gradients 4e-7 off against 1.1e-6, for 3 %
@@ -64,12 +66,13 @@ constexpr uint32_t chain_of(Sums sums, int ctas) { return sums == kParts || ctas
 // hold all three parts of both operands, and a single block's tile then has 128 columns.
 template <int CTAS, Readout READ, Sums SUMS>
 struct Stage {
-  static constexpr uint32_t kParts = SUMS == Sums::kParts ? 3 : 1;
-  static constexpr uint32_t kWidth = SUMS == Sums::kParts && CTAS == 1 ? 128 : kTileN;   // most columns of a tile
-  static constexpr uint32_t kA = kBlockM * kBlockK * 2;                                   // one part's
+  static constexpr uint32_t kPartsA = SUMS == kParts ? 3 : SUMS == kTwo && READ == kOut ? 2 : 1;   // the terms are A
+  static constexpr uint32_t kPartsB = SUMS == kParts ? 3 : 1;
+  static constexpr uint32_t kWidth = SUMS == kParts && CTAS == 1 ? 128 : kTileN;   // most columns of a tile
+  static constexpr uint32_t kA = kBlockM * kBlockK * 2;                             // one part's
   static constexpr uint32_t kB = kWidth / CTAS * kBlockK * 2;
-  static constexpr uint32_t kBytes = kParts * (kA + kB);
-  static constexpr uint32_t kBoxes = READ == kLoss ? 0 : kBoxesEach;
+  static constexpr uint32_t kBytes = kPartsA * kA + kPartsB * kB;
+  static constexpr uint32_t kBoxes = READ == kLoss ? 0 : SUMS == kTwo && READ == kTerms ? 2 : kBoxesEach;
   static constexpr uint32_t kCount = (kMaxSmem - 2048 - kReaders * kBoxes * kStore) / kBytes;
 };
 
@@ -302,6 +305,10 @@ struct Boxes {
     __syncwarp();
     turn = turn + 1 == BOXES ? 0 : turn + 1;
   }
+  __device__ __forceinline__ void all_free() const {
+    if ((threadIdx.x & 31) == 0) tc::stores_read<0>();
+    __syncwarp();
+  }
   __device__ __forceinline__ uint32_t now() const { return at + turn * kStore; }
   template <bool ADD>
   __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t x, uint32_t y, uint32_t z) const {
@@ -384,6 +391,24 @@ __device__ __forceinline__ void send_bf16(const Product& p, const float* x, uint
   write_bf16(boxes.now(), j & 1u, x);
   if (j & 1u) boxes.template send<false>(&p.out, col & ~63u, row0, z);
 }
+// ... of terms in two parts: two boxes hold two chunks
+template <uint32_t BOXES>
+__device__ __forceinline__ void send_two(const Product& p, float* x, uint32_t row0, uint32_t col, uint32_t j,
+                                         Boxes<BOXES>& boxes) {
+  if (BOXES != 2 || row0 >= p.m || (col & ~63u) >= p.n) return;
+  if (!(j & 1u)) boxes.all_free();
+  write_bf16(boxes.at, j & 1u, x);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] -= __bfloat162float(__float2bfloat16_rn(x[i]));
+  write_bf16(boxes.at + kStore, j & 1u, x);
+  if (j & 1u) {
+#pragma unroll
+    for (uint32_t part = 0; part < 2; ++part) {
+      boxes.turn = part;
+      boxes.template send<false>(&p.out, col & ~63u, row0, part);
+    }
+  }
+}
 // 64 columns of float matrices' terms: the three parts one after the other
 template <uint32_t BOXES>
 __device__ __forceinline__ void send_parts(const Product& p, float* x, uint32_t row0, uint32_t col, Boxes<BOXES>& boxes) {
@@ -460,25 +485,30 @@ struct Place {
 template <int CTAS, typename S, bool NARROW, bool A_MN, bool B_MN>
 __device__ __forceinline__ bool copy_item(const Product& p, const Work& w, uint32_t rank, uint32_t ring, Ends& ends, Place& at,
                                           uint32_t& issued) {
-  const uint32_t share = width<S, NARROW>(p) / CTAS, bytes = S::kParts * (S::kA + share * (kBlockK * 2)) * CTAS;
+  const uint32_t share = width<S, NARROW>(p) / CTAS;
+  const uint32_t bytes = (S::kPartsA * S::kA + S::kPartsB * share * (kBlockK * 2)) * CTAS;
   const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * share);
   for (uint32_t k = w.k0; k < w.k1; ++k) {
     const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
     if (!mbar_wait(&ends.empty[at.s], at.phase ^ 1)) return false;
     const uint32_t full = CTAS == 2 ? tc::in_block(smem_addr(&ends.full[at.s]), 0) : smem_addr(&ends.full[at.s]);
     if (rank == 0) mbar_expect_tx(&ends.full[at.s], bytes);
+    const uint32_t a = ring + at.s * S::kBytes, b = a + S::kPartsA * S::kA;
 #pragma unroll
-    for (uint32_t part = 0; part < S::kParts; ++part) {
-      const uint32_t a = ring + at.s * S::kBytes + part * S::kA, b = ring + at.s * S::kBytes + S::kParts * S::kA + part * S::kB;
+    for (uint32_t part = 0; part < S::kPartsA; ++part) {
       if (A_MN)
         for (uint32_t q = 0; q < kBlockM / 64; ++q)
-          tc::copy_box<CTAS>(a + q * 8192, &p.a, am + int(64 * q), ak, int(part), full);
-      else tc::copy_box<CTAS>(a, &p.a, ak, am, int(part), full);
+          tc::copy_box<CTAS>(a + part * S::kA + q * 8192, &p.a, am + int(64 * q), ak, int(part), full);
+      else tc::copy_box<CTAS>(a + part * S::kA, &p.a, ak, am, int(part), full);
+    }
+#pragma unroll
+    for (uint32_t part = 0; part < S::kPartsB; ++part) {
       if (B_MN)
-        for (uint32_t q = 0; q < share / 64; ++q) tc::copy_box<CTAS>(b + q * 8192, &p.b, bn + int(64 * q), bk, int(part), full);
+        for (uint32_t q = 0; q < share / 64; ++q)
+          tc::copy_box<CTAS>(b + part * S::kB + q * 8192, &p.b, bn + int(64 * q), bk, int(part), full);
       else
         for (uint32_t q = 0; q < (share + 127) / 128; ++q)   // boxes of 128 rows, or of all where they are fewer
-          tc::copy_box<CTAS>(b + q * 16384, &p.b, bk, bn + int(128 * q), int(part), full);
+          tc::copy_box<CTAS>(b + part * S::kB + q * 16384, &p.b, bk, bn + int(128 * q), int(part), full);
     }
     ++issued;
     at.template step<S::kCount>();
@@ -493,14 +523,14 @@ __device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, 
                                               uint32_t& n) {
   const uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, tile_n);
   for (uint32_t k = 0; k < blocks; ++n) {
-    const uint32_t end = SUMS == kOne ? blocks : min(blocks, k + chain_of(SUMS, CTAS));
+    const uint32_t end = SUMS == kOne || SUMS == kTwo ? blocks : min(blocks, k + chain_of(SUMS, CTAS));
     const uint32_t acc = SUMS == kParts ? 0u : n & 1u, round = SUMS == kParts ? n : n >> 1;
     if (!mbar_wait(&ends.tile_empty[acc], (round & 1u) ^ 1u)) return false;
     tc::fence_after_sync();
     for (bool add = false; k < end; ++k, add = true) {
       if (!ready && !mbar_wait(&ends.full[at.s], at.phase)) return false;
       tc::fence_after_sync();
-      const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kParts * S::kA);
+      const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kPartsA * S::kA);
       if (SUMS == kParts) {
 #pragma unroll 1
         for (uint32_t i = 0; i < 6; ++i) {   // the large product last, in an accumulator of its own
@@ -512,6 +542,12 @@ __device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, 
             tc::mma<CTAS>(to, pa + q * tc::kStep16<A_MN>, pb + q * tc::kStep16<B_MN>, instr, more || q != 0);
         }
       } else {
+        if (S::kPartsA == 2) {   // the terms' second parts
+#pragma unroll
+          for (uint32_t q = 0; q < kBlockK / 16; ++q)
+            tc::mma<CTAS>(tmem + acc * kTileN, a + (S::kA >> 4) + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
+          add = true;
+        }
 #pragma unroll
         for (uint32_t q = 0; q < kBlockK / 16; ++q)
           tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
@@ -645,14 +681,15 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           read_loss(job, x, r, col + 32 * j, target, word, c, sum);
         } else if (READ == kTerms) {
           set_terms(job, x, col + 32 * j, word, terms);
-          if (SUMS != kParts) send_bf16(p, x, 0, row0, col + 32 * j, j, boxes);
+          if (SUMS == kTwo) send_two(p, x, row0, col + 32 * j, j, boxes);
+          else if (SUMS != kParts) send_bf16(p, x, 0, row0, col + 32 * j, j, boxes);
           else if (j & 1u) send_parts(p, x - 32, row0, col + 32 * j - 32, boxes);   // with the 32 before
         } else {
           send_grad(p, x, w.split, row0, col + 32 * j, j, boxes);
         }
       };
       const uint32_t at = tmem + half * wide + ((quarter * 32) << 16);
-      if (SUMS != kOne) {
+      if (SUMS == kChains || SUMS == kParts) {
         // the chains' sums, added up in registers; none in a split without stages
         float v[128];
 #pragma unroll
@@ -951,7 +988,7 @@ constexpr size_t kPieceBytes = size_t(256) << 20;
 
 // What a call works on, and where its workspace's parts lie
 struct HeadPlan {
-  uint32_t B, V, D, Dp, parts;
+  uint32_t B, V, D, Dp, parts, term_parts;
   bool lay_h, lay_w;
   uint32_t piece;            // tokens of a piece: a multiple of 256 unless it is all of them
   uint32_t out_n;            // columns of the gradients' tiles
@@ -981,6 +1018,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   p.Dp = uint32_t(up_to(D, 8));
   const bool f32 = dtype == CG_F32;
   p.parts = f32 ? 3 : 1;
+  p.term_parts = f32 ? 3 : B <= kBlockM ? 2 : 1;
   p.lay_h = f32 || !rows_on_grid(hidden, dtype, ld_h);
   p.lay_w = f32 || !rows_on_grid(weight, dtype, ld_w);
   // rows in pairs of blocks, but not 257 to 384: three blocks pad them to 384, two pairs to 512
@@ -988,7 +1026,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   p.pair = B > kBlockM && !(B > 2 * kBlockM && B <= 3 * kBlockM);
   uint64_t most = V;
   if (p.lay_w) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * p.Dp * 2));
-  if (grad) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * std::max(B, 1u) * 2));
+  if (grad) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.term_parts) * std::max(B, 1u) * 2));
   if (most < V) most = std::max<uint64_t>(most / 256 * 256, 256);
   const uint64_t pieces = (V + most - 1) / most;
   p.piece = uint32_t(std::min<uint64_t>(up_to((V + pieces - 1) / pieces, 256), V));
@@ -1009,7 +1047,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
     p.at_target = take(size_t(B) * 4);
   } else {
     p.ld_terms = up_to(p.piece, 8);
-    p.at_terms = take(size_t(p.parts) * B * p.ld_terms * 2);
+    p.at_terms = take(size_t(p.term_parts) * B * p.ld_terms * 2);
     p.ld_sums = up_to(D, 4);
     const uint32_t tiles = tiles_of(B, kBlockM * (p.pair ? 2 : 1)) * tiles_of(D, p.out_n);
     const uint32_t blocks = tiles_of(p.piece, kBlockK);
@@ -1039,19 +1077,20 @@ cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
 }
 // Results in 32 bits are summed in chains: losses, and all that float matrices give.
 template <int CTAS, Readout READ, bool NARROW>
-cudaError_t launch_job(int device, bool f32, Job& j, cudaStream_t stream) {
-  if (f32) return launch_job<CTAS, READ, kParts, NARROW>(device, j, stream);
-  if (READ == kLoss && j.p[0].blocks > chain_of(kChains, CTAS))
-    return launch_job<CTAS, READ, READ == kLoss ? kChains : kOne, NARROW>(device, j, stream);
+cudaError_t launch_job(int device, const HeadPlan& p, Job& j, cudaStream_t stream) {
+  if (p.parts > 1) return launch_job<CTAS, READ, kParts, NARROW>(device, j, stream);
+  if (READ == kLoss)
+    return j.p[0].blocks > chain_of(kChains, CTAS) ? launch_job<CTAS, READ, READ == kLoss ? kChains : kOne, NARROW>(device, j, stream)
+                                                   : launch_job<CTAS, READ, kOne, NARROW>(device, j, stream);
+  if (CTAS == 1 && p.term_parts == 2)
+    return launch_job<CTAS, READ, CTAS == 1 && READ != kLoss ? kTwo : kOne, NARROW>(device, j, stream);
   return launch_job<CTAS, READ, kOne, NARROW>(device, j, stream);
 }
 template <Readout READ>
 cudaError_t launch_job(int device, const HeadPlan& p, Job& j, cudaStream_t stream) {
-  const bool f32 = p.parts > 1;
   if (READ != kOut && p.tile_n < p.out_n)
-    return p.pair ? launch_job<2, READ, READ != kOut>(device, f32, j, stream)
-                  : launch_job<1, READ, READ != kOut>(device, f32, j, stream);
-  return p.pair ? launch_job<2, READ, false>(device, f32, j, stream) : launch_job<1, READ, false>(device, f32, j, stream);
+    return p.pair ? launch_job<2, READ, READ != kOut>(device, p, j, stream) : launch_job<1, READ, READ != kOut>(device, p, j, stream);
+  return p.pair ? launch_job<2, READ, false>(device, p, j, stream) : launch_job<1, READ, false>(device, p, j, stream);
 }
 
 struct HeadArgs {
@@ -1180,7 +1219,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
     Job j = logits_of(a, p, v, v0, n);
     j.terms = TermsOut{loss, norm, up};
     if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, w_rows, b_rows(p)) ||
-        !tc::make_map(&j.p[0].out, terms, n, p.B, p.parts, p.ld_terms, part_stride, 32))
+        !tc::make_map(&j.p[0].out, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, 32))
       return CG_E_CUDA;
     if (launch_job<kTerms>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
 
@@ -1202,7 +1241,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       } else if (!grad_out(q, dh, p.B, ld_dh, a.dtype)) {
         return CG_E_CUDA;
       }
-      if (!tc::make_map(&q.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 128) || !map_w(&q.b, p, o, w_rows, 64))
+      if (!tc::make_map(&q.a, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, 128) || !map_w(&q.b, p, o, w_rows, 64))
         return CG_E_CUDA;
     }
     if (dw) {  // terms^T [n][B] x H [B][D]
@@ -1213,7 +1252,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       q.splits = 1;
       q.tile_n = p.out_n;
       if (!grad_out(q, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
-      if (!tc::make_map(&q.a, terms, n, p.B, p.parts, p.ld_terms, part_stride, 64) || !map_h(&q.b, p, o, 64)) return CG_E_CUDA;
+      if (!tc::make_map(&q.a, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, 64) || !map_h(&q.b, p, o, 64)) return CG_E_CUDA;
     }
     if (launch_job<kOut>(dev, p, g, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
