@@ -333,9 +333,17 @@ __device__ __forceinline__ RowTerms row_terms(const Job& job, uint32_t r, uint32
   if (r < job.p[0].m && target != CG_NO_TOKEN) {
     const float loss = job.terms.loss[r], m = job.terms.norm[2 * size_t(r)], s = job.terms.norm[2 * size_t(r) + 1];
     if (loss > 0.f) {   // a loss of 0: no target that counts, or nothing beside it
-      const Scale t(c, m);
+      Scale t(c, m);
       const float g = __fdiv_rn(job.terms.up ? job.terms.up[r] : 1.f, job.temp);
-      return {t, __fdiv_rn(g, s) * t.rest, g * expm1f(-loss), target};
+      float k = __fdiv_rn(g, s) * t.rest;
+      if (!(fabsf(k) <= FLT_MAX)) {
+        // an infinite or NaN g, whose terms are not finite, but 0 for the tokens that are not allowed: as
+        // exponentials that overflow, as 0 times g is NaN
+        t.fast = false;
+        t.m -= fmaxf(fminf(__fdiv_rn(300.f, c), 1e38f), fabsf(m) * 1e-3f);
+        k = copysignf(1.f, k);
+      }
+      return {t, k, g * expm1f(-loss), target};
     }
   }
   return {Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};   // c = 0, k = 0: every term is 0

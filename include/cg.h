@@ -577,8 +577,7 @@ int cg_embed(cg_ctx* c, const void* d_table, int dtype, uint32_t V, uint32_t D, 
 /* The gradient by the table: out[v] = scale * sum of grad[i] over the i with token v,
  * zeros for a token that does not occur; with accumulate != 0, added to what out holds
  * (tokens that do not occur are then left alone).  The positions are sorted by token;
- * a token's rows are summed in the order of their positions, in groups that N and D
- * alone decide.
+ * a token's rows are summed in an order that only the tokens, N, D and the dtype decide.
  *  d_grad : [N][ld_grad]; d_out_grad : [V][ld_out]
  * Device errors: CG_DEV_BAD_TOKEN. */
 int cg_embed_workspace(const cg_ctx* c, int dtype, uint32_t N, uint32_t D, size_t* bytes);
@@ -615,7 +614,8 @@ int cg_head_loss(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtyp
  * (the workspace holds one piece's terms, 256 MB or those of 256 tokens):
  *   d_bv = g_b / T * (p_v - [v = t]) over A_b, 0 elsewhere and in a row whose loss is 0;
  *   grad_hidden = d weight,  grad_weight = d^T hidden.
- * p_t - 1 is taken from the loss, as expm1(-loss).  Terms d of bf16 matrices are rounded
+ * p_t - 1 is taken from the loss, as expm1(-loss).  An infinite or NaN g_b gives terms that
+ * are not finite over A_b, and 0 elsewhere as any other.  Terms d of bf16 matrices are rounded
  * to bf16 for the products (a relative error of 2^-8 at most, as the gradients' own
  * rounding has), with up to 128 rows to two bf16 parts (2^-16).  hidden and weight have
  * to be finite: 0 * inf is NaN, also for a token that no row allows.

@@ -320,6 +320,46 @@ def test_values_that_are_not_finite():
     assert open_[0][7] == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("B", [40, 200])
+def test_a_gradient_that_is_not_finite_stays_visible(B, masked, dtype):
+    """Rows whose g is infinite or NaN: their gradients, and those of the tokens that they allow, are not finite
+    either; other rows, and tokens that they forbid, are as without them."""
+    import torch
+    V, D = 900, 40
+    ctx, g = ctx_of(V), generator(B + masked)
+    h, w = matrix(B, D, dtype, 0, 0, g, 1.0), matrix(V, D, dtype, 0, 0, g, 0.3)
+    bad, half = torch.tensor([3, 17, 33], device="cuda"), V // 2
+    bits = None
+    if masked:
+        bits = torch.rand((B, V), generator=g, device="cuda") < 0.8
+        bits[bad, :half] = True
+        bits[bad, half:] = False
+    target = torch.randint(0, half, (B,), generator=g, device="cuda").int()
+    if masked:
+        bits.scatter_(1, target.long()[:, None], True)
+    up = torch.rand(B, generator=g, device="cuda") - 0.3
+    up[bad] = torch.tensor([torch.inf, torch.nan, -torch.inf], device="cuda")
+    loss, lse, norm = (torch.empty(s, device="cuda") for s in ((B,), (B,), (B, 2)))
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    mask = pack(bits) if masked else None
+    ctx.head_loss(h, w, target, loss, bitmask=mask, out_lse=lse, out_norm=norm)
+    ctx.head_grad(h, w, target, loss, norm, dh, dw, bitmask=mask, grad_loss=up)
+    assert ctx.status() == 0
+    good = torch.ones(B, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    assert not dh[bad].isfinite().any() and not dw[:half].isfinite().any()
+    assert masked or not dw.isfinite().any()
+    # the others against the definition without those rows (a row of g = 0 gives terms of 0)
+    e = Exact(h, w, target, 1.0, bits, torch.where(good, up, 0.0).double(), dtype)
+    dh[bad] = 0
+    e.check_grad(dh, None)
+    if masked:
+        e.d, e.w = e.d[:, half:].contiguous(), e.w[half:]
+        e.check_grad(None, dw[half:])
+
+
 def test_rows_that_do_not_count():
     import torch
     from grammar_constrained_decoding_gb300._lib import CG_DEV_BAD_TOKEN
