@@ -360,9 +360,9 @@ class Ctx:
 
     def embed_workspace(self, grad, tokens) -> int:
         """Bytes that embed_grad works in."""
-        n = C.c_size_t()
-        L.check("cg_embed_workspace", L.lib().cg_embed_workspace(self._h, self._rows.DTYPE[grad.dtype], tokens.shape[0],
-                                                                  grad.shape[1], C.byref(n)))
+        n, call, N = C.c_size_t(), "cg_embed_workspace", tokens.shape[0]
+        D = self._rows.matrix_of(call, grad, "grad", None, N, self._dev)[2]
+        L.check(call, L.lib().cg_embed_workspace(self._h, self._rows.DTYPE[grad.dtype], N, D, C.byref(n)))
         return n.value
 
     def embed_grad(self, grad, tokens, out_grad, scale: float = 1.0, accumulate: bool = False, workspace=None) -> None:

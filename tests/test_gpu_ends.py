@@ -414,6 +414,9 @@ def test_refusals():
                      ((h, w, t, loss), dict(out_norm=loss)), ((h.t(), w, t, loss), {}), ((h[:, :0], w[:, :0], t, loss), {})]:
         with pytest.raises((cg.CgError, IndexError)):
             ctx.head_loss(*args, **kw)
+    for bad in (dh.half(), dh[0], dh.long(), dh.cpu()):
+        with pytest.raises(cg.CgError):
+            ctx.embed_workspace(bad, t)
     both = torch.ones((V, 2 * D), device="cuda")
     for args, kw in [((h, w, t, loss, norm), {}), ((h, w, t, loss, norm, h, dw), {}), ((h, w, t, loss, norm, dh, w), {}),
                      ((h, w, t, loss, norm, dh, dw[1:]), {}), ((h, w, t, loss, norm, dw[:B], dw), {}), ((h, w, t, loss, loss, dh, dw), {}),
