@@ -97,6 +97,7 @@ struct Product {
   CUtensorMap a, b, out;     // operands; the terms or the gradient as they are written
   uint32_t m, n, n_m, n_n;   // extent, and in tiles
   uint32_t tile_n;           // columns of a tile: 256, or 128 or 64 where tiles are few
+  uint32_t a_rows, k_rows;   // rows of a box of A where k is its width, of A and B where k is their rows
   uint32_t blocks, splits;   // stages of one product; splits of them
   int a_mn, a_k, b_mn, b_k;  // where the product begins in the maps
   GradOut grad;
@@ -494,7 +495,8 @@ template <int CTAS, typename S, bool NARROW, bool A_MN, bool B_MN>
 __device__ __forceinline__ bool copy_item(const Product& p, const Work& w, uint32_t rank, uint32_t ring, Ends& ends, Place& at,
                                           uint32_t& issued) {
   const uint32_t share = width<S, NARROW>(p) / CTAS;
-  const uint32_t bytes = (S::kPartsA * S::kA + S::kPartsB * share * (kBlockK * 2)) * CTAS;
+  const uint32_t bytes = (S::kPartsA * (A_MN ? kBlockM * p.k_rows : p.a_rows * kBlockK) +
+                          S::kPartsB * share * (B_MN ? p.k_rows : kBlockK)) * (2 * CTAS);
   const int am = p.a_mn + int(w.m0 + rank * kBlockM), bn = p.b_mn + int(w.n0 + rank * share);
   for (uint32_t k = w.k0; k < w.k1; ++k) {
     const int ak = p.a_k + int(k * kBlockK), bk = p.b_k + int(k * kBlockK);
@@ -525,11 +527,17 @@ __device__ __forceinline__ bool copy_item(const Product& p, const Work& w, uint3
 }
 
 // An item's products, chain after chain; n counts the chains.  Chains take the two accumulators
-// in turn; the six products of a float matrices' stage take both.
-template <int CTAS, typename S, Sums SUMS, bool A_MN, bool B_MN>
-__device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, uint32_t ring, uint32_t tmem, Ends& ends, Place& at, bool& ready,
+// in turn; the six products of a float matrices' stage take both.  FEW: where k runs over few rows,
+// fewer than a stage's 64.
+template <int CTAS, typename S, Sums SUMS, bool A_MN, bool B_MN, bool FEW = false>
+__device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t k_rows, uint32_t blocks, uint32_t ring, uint32_t tmem, Ends& ends, Place& at, bool& ready,
                                               uint32_t& n) {
   const uint32_t instr = tc::instruction<A_MN, B_MN>(kBlockM * CTAS, tile_n);
+  auto multiply = [&](uint32_t to, uint64_t a, uint64_t b, bool more) {
+#pragma unroll
+    for (uint32_t q = 0; q < kBlockK / 16; ++q)
+      if (!FEW || q < k_rows / 16) tc::mma<CTAS>(to, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, more || q != 0);
+  };
   for (uint32_t k = 0; k < blocks; ++n) {
     const uint32_t end = SUMS == kOne || SUMS == kTwo ? blocks : min(blocks, k + chain_of(SUMS, CTAS));
     const uint32_t acc = SUMS == kParts ? 0u : n & 1u, round = SUMS == kParts ? n : n >> 1;
@@ -541,24 +549,11 @@ __device__ __forceinline__ bool multiply_item(uint32_t tile_n, uint32_t blocks, 
       const uint64_t a = tc::operand<A_MN>(ring + at.s * S::kBytes), b = tc::operand<B_MN>(ring + at.s * S::kBytes + S::kPartsA * S::kA);
       if (SUMS == kParts) {
 #pragma unroll 1
-        for (uint32_t i = 0; i < 6; ++i) {   // the large product last, in an accumulator of its own
-          const uint64_t pa = a + part_a(i) * (S::kA >> 4), pb = b + part_b(i) * (S::kB >> 4);
-          const uint32_t to = tmem + (i < 5 ? kTileN : 0u);
-          const bool more = add || (i != 0 && i != 5);
-#pragma unroll
-          for (uint32_t q = 0; q < kBlockK / 16; ++q)
-            tc::mma<CTAS>(to, pa + q * tc::kStep16<A_MN>, pb + q * tc::kStep16<B_MN>, instr, more || q != 0);
-        }
+        for (uint32_t i = 0; i < 6; ++i)   // the large product last, in an accumulator of its own
+          multiply(tmem + (i < 5 ? kTileN : 0u), a + part_a(i) * (S::kA >> 4), b + part_b(i) * (S::kB >> 4), add || (i != 0 && i != 5));
       } else {
-        if (S::kPartsA == 2) {   // the terms' second parts
-#pragma unroll
-          for (uint32_t q = 0; q < kBlockK / 16; ++q)
-            tc::mma<CTAS>(tmem + acc * kTileN, a + (S::kA >> 4) + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
-          add = true;
-        }
-#pragma unroll
-        for (uint32_t q = 0; q < kBlockK / 16; ++q)
-          tc::mma<CTAS>(tmem + acc * kTileN, a + q * tc::kStep16<A_MN>, b + q * tc::kStep16<B_MN>, instr, add || q != 0);
+        if (S::kPartsA == 2) multiply(tmem + acc * kTileN, a + (S::kA >> 4), b, add);   // the terms' second parts
+        multiply(tmem + acc * kTileN, a, b, add || S::kPartsA == 2);
       }
       tc::commit<CTAS>(&ends.empty[at.s]);
       at.template step<S::kCount>();
@@ -634,10 +629,15 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         Work w;
         if (READ == kOut && second) {
           stages_of(job.p[1], t, w);
-          ok = multiply_item<CTAS, S, SUMS, true, true>(S::kWidth, w.k1 - w.k0, ring, tmem, ends, at, ready, n);
+          const uint32_t k_rows = job.p[1].k_rows;
+          // (one loop for both: 333 x 32003 x 509 f32 296 us in place of 292)
+          if (CTAS == 1 && k_rows < kBlockK)
+            ok = multiply_item<CTAS, S, SUMS, true, true, CTAS == 1>(S::kWidth, k_rows, w.k1 - w.k0, ring, tmem, ends, at, ready, n);
+          else
+            ok = multiply_item<CTAS, S, SUMS, true, true>(S::kWidth, kBlockK, w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         } else {
           stages_of(job.p[0], t, w);
-          ok = multiply_item<CTAS, S, SUMS, false, READ == kOut>(width<S, NARROW>(job.p[0]), w.k1 - w.k0, ring, tmem, ends, at, ready, n);
+          ok = multiply_item<CTAS, S, SUMS, false, READ == kOut>(width<S, NARROW>(job.p[0]), kBlockK, w.k1 - w.k0, ring, tmem, ends, at, ready, n);
         }
       }
       if (!ok) {
@@ -1152,6 +1152,10 @@ bool map_w(CUtensorMap* map, const HeadPlan& p, const Operands& o, uint32_t rows
 
 // rows of the weight's boxes: a block's share of a tile's, at most 128
 uint32_t b_rows(const HeadPlan& p) { return std::min(128u, p.tile_n / (p.pair ? 2 : 1)); }
+// and of the hidden rows', or the terms': where they are few, what lies past them in the tile stays
+// as it is (it reaches only rows that are not there).  Copies that fill whole boxes with zeros held
+// up 152 blocks that all read the same few rows: 1 x 128256 x 4096 221 -> 178 us, 16 rows alike
+uint32_t h_rows(const HeadPlan& p) { return std::min<uint32_t>(kBlockM, uint32_t(up_to(p.B, 8))); }
 // x = H W^T of a piece, read out one way or the other
 Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v0, uint32_t n) {
   Job j = {};
@@ -1161,6 +1165,7 @@ Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v
   q.blocks = tiles_of(p.D, kBlockK);
   q.splits = 1;
   q.tile_n = p.tile_n;
+  q.a_rows = h_rows(p);
   q.b_mn = p.lay_w ? 0 : int(v0);
   j.bitmask = a.bitmask;
   j.W = v.t.W;
@@ -1183,7 +1188,7 @@ int head_loss(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, float* loss, floa
     Job j = logits_of(a, p, v, v0, n);
     j.loss.part = reinterpret_cast<float2*>(ws + p.at_part);
     j.loss.target_logit = reinterpret_cast<float*>(ws + p.at_target);
-    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, p.lay_w ? n : p.V, b_rows(p))) return CG_E_CUDA;
+    if (!map_h(&j.p[0].a, p, o, h_rows(p)) || !map_w(&j.p[0].b, p, o, p.lay_w ? n : p.V, b_rows(p))) return CG_E_CUDA;
     if (launch_job<kLoss>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
   return launch_dependent(join_loss_kernel, dim3(tiles_of(p.B, 32)), dim3(1024), 0, v.stream,
@@ -1226,7 +1231,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
     const uint32_t w_rows = p.lay_w ? n : p.V;
     Job j = logits_of(a, p, v, v0, n);
     j.terms = TermsOut{loss, norm, up};
-    if (!map_h(&j.p[0].a, p, o, 128) || !map_w(&j.p[0].b, p, o, w_rows, b_rows(p)) ||
+    if (!map_h(&j.p[0].a, p, o, h_rows(p)) || !map_w(&j.p[0].b, p, o, w_rows, b_rows(p)) ||
         !tc::make_map(&j.p[0].out, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, 32))
       return CG_E_CUDA;
     if (launch_job<kTerms>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
@@ -1241,6 +1246,8 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       q.blocks = tiles_of(n, kBlockK);
       q.splits = p.splits;
       q.tile_n = p.out_n;
+      q.a_rows = h_rows(p);
+      q.k_rows = kBlockK;
       q.b_k = p.lay_w ? 0 : int(v0);
       if (summed) {
         q.grad.boxes = q.grad.f32 = true;
@@ -1249,7 +1256,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       } else if (!grad_out(q, dh, p.B, ld_dh, a.dtype)) {
         return CG_E_CUDA;
       }
-      if (!tc::make_map(&q.a, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, 128) || !map_w(&q.b, p, o, w_rows, 64))
+      if (!tc::make_map(&q.a, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, h_rows(p)) || !map_w(&q.b, p, o, w_rows, 64))
         return CG_E_CUDA;
     }
     if (dw) {  // terms^T [n][B] x H [B][D]
@@ -1259,8 +1266,9 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       q.blocks = tiles_of(p.B, kBlockK);
       q.splits = 1;
       q.tile_n = p.out_n;
+      q.k_rows = std::min<uint32_t>(kBlockK, uint32_t(up_to(p.B, 16)));   // zeros past the rows, to a whole step of k
       if (!grad_out(q, static_cast<char*>(dw) + uint64_t(v0) * ld_dw * size, n, ld_dw, a.dtype)) return CG_E_CUDA;
-      if (!tc::make_map(&q.a, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, 64) || !map_h(&q.b, p, o, 64)) return CG_E_CUDA;
+      if (!tc::make_map(&q.a, terms, n, p.B, p.term_parts, p.ld_terms, part_stride, q.k_rows) || !map_h(&q.b, p, o, q.k_rows)) return CG_E_CUDA;
     }
     if (launch_job<kOut>(dev, p, g, v.stream) != cudaSuccess) return CG_E_CUDA;
   }

@@ -256,6 +256,24 @@ def test_extremes(B, V, D, dtype):
     run(B, V, D, dtype, masked=B < 100)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [1, 7, 9, 17, 40, 63])
+def test_few_rows_after_a_call_full_of_nan(B, dtype):
+    """Tiles that few rows fill in part: what an earlier launch left in shared memory reaches nothing."""
+    import torch
+    V, D = 40000, 136
+    ctx, dt = ctx_of(V), torch.bfloat16 if dtype == "bf16" else torch.float32
+    h, w = (torch.full((n, D), float("nan"), dtype=dt, device="cuda") for n in (128, V))
+    target = torch.zeros(128, dtype=torch.int32, device="cuda")
+    loss, norm = torch.empty(128, device="cuda"), torch.empty((128, 2), device="cuda")
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    for masked in (True, False):
+        ctx.head_loss(h, w, target, loss, out_norm=norm)
+        ctx.head_grad(h, w, target, loss, norm, dh, dw)
+        assert not loss.any() and ctx.status() == 0
+        run(B, V, D, dtype, masked=masked)
+
+
 @pytest.mark.parametrize("pad", [2 ** 23, 2 ** 23 + 1])
 def test_rows_beyond_32_bit_offsets(pad):
     """Pitches that take the last rows of the weight and of its gradient past 2^32 elements, on the 16-byte grid
