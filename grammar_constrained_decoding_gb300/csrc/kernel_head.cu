@@ -89,6 +89,7 @@ struct TermsOut {
 struct GradOut {
   bool boxes;                // written (added, with `add`) as boxes of `out`; else element by element to `at`
   bool add, f32;
+  uint32_t whole;            // columns that boxes write: a box ends on the 16-byte grid, whatever lies there
   void* at;                  // [m][ld]
   uint64_t ld;
 };
@@ -393,12 +394,12 @@ __device__ __forceinline__ void write_bf16(uint32_t box, uint32_t half, const fl
 }
 // 32 rows of 32 columns (chunk j of the reader's 128) on their way: bf16 boxes hold two chunks
 template <uint32_t BOXES>
-__device__ __forceinline__ void send_bf16(const Product& p, const float* x, uint32_t z, uint32_t row0, uint32_t col, uint32_t j,
-                                          Boxes<BOXES>& boxes) {
+__device__ __forceinline__ void send_bf16(const Product& p, uint32_t whole, const float* x, uint32_t z, uint32_t row0, uint32_t col,
+                                          uint32_t j, Boxes<BOXES>& boxes) {
   if (row0 >= p.m || (col & ~63u) >= p.n) return;
   if (!(j & 1u)) boxes.next();
   write_bf16(boxes.now(), j & 1u, x);
-  if (j & 1u) boxes.template send<false>(&p.out, col & ~63u, row0, z);
+  if ((j & 1u) && (col & ~63u) < whole) boxes.template send<false>(&p.out, col & ~63u, row0, z);
 }
 // ... of terms in two parts: two boxes hold two chunks
 template <uint32_t BOXES>
@@ -441,7 +442,7 @@ __device__ __forceinline__ void send_grad(const Product& p, const float* x, uint
   const uint32_t lane = threadIdx.x & 31;
   const GradOut& g = p.grad;
   if (g.boxes && !g.f32) {
-    send_bf16(p, x, split, row0, col, j, boxes);
+    send_bf16(p, g.whole, x, split, row0, col, j, boxes);
     return;
   }
   if (row0 >= p.m || col >= p.n) return;
@@ -453,7 +454,7 @@ __device__ __forceinline__ void send_grad(const Product& p, const float* x, uint
               __float_as_uint(x[4 * i + 3]));
   if (g.boxes) {
     if (g.add) boxes.template send<true>(&p.out, col, row0, split);
-    else boxes.template send<false>(&p.out, col, row0, split);
+    else if (col < g.whole) boxes.template send<false>(&p.out, col, row0, split);
     return;
   }
   __syncwarp();
@@ -476,6 +477,27 @@ __device__ __forceinline__ void send_grad(const Product& p, const float* x, uint
     }
   }
   __syncwarp();
+}
+
+// What boxes leave of a gradient's rows, at most 15 bytes of each: a lane's row as it lies in the
+// box that a reader of `columns` from `col` on wrote last, if that is the rows' last
+__device__ __forceinline__ void send_rest(const Product& p, uint32_t box, uint32_t row0, uint32_t col, uint32_t columns) {
+  const GradOut& g = p.grad;
+  const uint32_t lane = threadIdx.x & 31, first = (p.n - 1) & ~(g.f32 ? 31u : 63u);
+  if (first < col || first >= col + columns || row0 + lane >= p.m) return;
+#pragma unroll 1
+  for (uint32_t c = g.whole; c < p.n; ++c) {
+    const uint32_t off = (c - first) * (g.f32 ? 4 : 2), from = box_piece(box, lane, off >> 4) + (off & 15);
+    const size_t at = size_t(row0 + lane) * g.ld + c;
+    uint32_t x = 0;
+    if (g.f32) {
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
+      static_cast<uint32_t*>(g.at)[at] = x;
+    } else {
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
+      static_cast<uint16_t*>(g.at)[at] = uint16_t(x);
+    }
+  }
 }
 
 // ---- the product kernel ----------------------------------------------------------------------
@@ -690,7 +712,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         } else if (READ == kTerms) {
           set_terms(job, x, col + 32 * j, word, terms);
           if (SUMS == kTwo) send_two(p, x, row0, col + 32 * j, j, boxes);
-          else if (SUMS != kParts) send_bf16(p, x, 0, row0, col + 32 * j, j, boxes);
+          else if (SUMS != kParts) send_bf16(p, p.n, x, 0, row0, col + 32 * j, j, boxes);
           else if (j & 1u) send_parts(p, x - 32, row0, col + 32 * j - 32, boxes);   // with the 32 before
         } else {
           send_grad(p, x, w.split, row0, col + 32 * j, j, boxes);
@@ -748,6 +770,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           read(v, j, j == 0 ? words[0] : j == 1 ? words[1] : j == 2 ? words[2] : words[3]);
         }
       }
+      if (READ == kOut && p.grad.boxes && p.grad.whole < p.n) send_rest(p, boxes.now(), row0, col, 32 * chunks);
       if (READ == kLoss && chunks && r < p.m && col < p.n)
         job.loss.part[size_t((job.v0 + col) / wide) * p.m + r] = make_float2(sum.m, sum.s);
       return true;
@@ -1202,10 +1225,11 @@ int head_loss(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, float* loss, floa
 // where a product's elements go: [rows][ld] at `to`
 bool grad_out(Product& g, void* to, uint32_t rows, uint64_t ld, int dtype) {
   g.grad.f32 = dtype == CG_F32;
-  g.grad.boxes = rows_on_grid(to, dtype, ld);
+  g.grad.whole = g.n & ~(g.grad.f32 ? 3u : 7u);
+  g.grad.boxes = rows_on_grid(to, dtype, ld) && g.grad.whole;
   g.grad.at = to;
   g.grad.ld = ld;
-  return !g.grad.boxes || tc::make_map(&g.out, to, g.n, rows, 1, ld, ld, 32, g.grad.f32);
+  return !g.grad.boxes || tc::make_map(&g.out, to, g.grad.whole, rows, 1, ld, ld, 32, g.grad.f32);
 }
 
 int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss, const float* norm, const float* up, void* dh, uint64_t ld_dh,
@@ -1252,6 +1276,7 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       if (summed) {
         q.grad.boxes = q.grad.f32 = true;
         q.grad.add = v0 != 0;
+        q.grad.whole = p.D;   // the workspace's rows end on the grid
         if (!tc::make_map(&q.out, sums, p.D, p.B, p.splits, p.ld_sums, uint64_t(p.B) * p.ld_sums, 32, true)) return CG_E_CUDA;
       } else if (!grad_out(q, dh, p.B, ld_dh, a.dtype)) {
         return CG_E_CUDA;

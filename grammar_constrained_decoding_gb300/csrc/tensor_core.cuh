@@ -190,7 +190,8 @@ inline EncodeTiled encode_tiled() {
 }
 
 // [parts][rows][width] of bf16 (or float), rows `ld` elements apart, boxes of 128 bytes x
-// box_rows with a 128-byte swizzle; what lies outside reads as zero and is not written.  The
+// box_rows with a 128-byte swizzle; what lies outside reads as zero and is not written, but for
+// the rest of the 16 bytes that a row's last element lies in: a store writes those too.  The
 // address and the row pitch are multiples of 16 bytes.
 inline bool make_map(CUtensorMap* map, const void* at, uint64_t width, uint64_t rows, uint64_t parts, uint64_t ld,
                      uint64_t part_stride, uint32_t box_rows, bool f32 = false) {

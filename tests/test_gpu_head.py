@@ -196,6 +196,15 @@ def test_head_layouts(pad, shift, dtype):
     run(60, 1500, 130, dtype, pad, shift, masked=False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 3, 7, 65, 129, 130, 135, 191, 193, 257, 261])
+def test_head_leaves_what_lies_beside_its_rows(D, dtype):
+    """Rows on the 16-byte grid whose last elements do not end there: what follows them stays."""
+    pad = -D % (8 if dtype == "bf16" else 4)
+    for B in (20, 150):
+        run(B, 800, D, dtype, pad, 0)
+
+
 @pytest.mark.parametrize("which", ["dh", "dw"])
 def test_head_one_gradient(which):
     run(200, 3000, 96, "bf16", which=which)
