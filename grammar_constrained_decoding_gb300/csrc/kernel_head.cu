@@ -16,7 +16,8 @@
 // d is rounded to bf16 because the tensor cores multiply bf16: its relative error of at most 2^-8
 // is the size of the gradients' own rounding.  Float inputs, and d then, are split into
 // three bf16 parts of 8 bits each, and the six products of parts that are not below 2^-24
-// are summed, the five small ones apart from the large one.
+// are summed, the five small ones apart from the large one.  Up to 8 rows of them, which wait
+// for the weight alone, are multiplied without the tensor cores.
 //
 // Bound by the tensor cores where rows are many: 4096 x 128256 x 2048, loss and gradients, 8.6
 // TFLOP with the logits twice in 5.0 ms, 1.72 PFLOP/s, what a plain library product sustains at
@@ -330,13 +331,13 @@ struct RowTerms {
   float k, at_target;
   uint32_t target;           // CG_NO_TOKEN in a row that does not count
 };
-__device__ __forceinline__ RowTerms row_terms(const Job& job, uint32_t r, uint32_t target) {
-  const float c = exp_scale(job.temp);
-  if (r < job.p[0].m && target != CG_NO_TOKEN) {
-    const float loss = job.terms.loss[r], m = job.terms.norm[2 * size_t(r)], s = job.terms.norm[2 * size_t(r) + 1];
+__device__ __forceinline__ RowTerms row_terms(const TermsOut& terms, float temp, uint32_t rows, uint32_t r, uint32_t target) {
+  const float c = exp_scale(temp);
+  if (r < rows && target != CG_NO_TOKEN) {
+    const float loss = terms.loss[r], m = terms.norm[2 * size_t(r)], s = terms.norm[2 * size_t(r) + 1];
     if (loss > 0.f) {   // a loss of 0: no target that counts, or nothing beside it
       Scale t(c, m);
-      const float g = __fdiv_rn(job.terms.up ? job.terms.up[r] : 1.f, job.temp);
+      const float g = __fdiv_rn(terms.up ? terms.up[r] : 1.f, temp);
       float k = __fdiv_rn(g, s) * t.rest;
       if (!(fabsf(k) <= FLT_MAX)) {
         // an infinite or NaN g, whose terms are not finite, but 0 for the tokens that are not allowed: as
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         if (r < p.m) target = job.target[r];
       }
       RowSum sum;
-      const RowTerms terms = READ == kTerms ? row_terms(job, r, target) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
+      const RowTerms terms = READ == kTerms ? row_terms(job.terms, job.temp, job.p[0].m, r, target) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
       auto read = [&](float* x, uint32_t j, uint32_t word) {
         if (READ == kLoss) {
           read_loss(job, x, r, col + 32 * j, target, word, c, sum);
@@ -939,6 +940,260 @@ __global__ void __launch_bounds__(256) join_many_kernel(const float* sums, uint3
   put4(out, size_t(r) * ld + col, n - col, bf16, wide, s);
 }
 
+// ---- float matrices of few rows ----------------------------------------------------------------
+
+// Up to 8 rows of float matrices are multiplied on the ordinary pipes as they are: reading the
+// weight bounds that, and laying it out as three bf16 parts takes 16 bytes an element where this
+// takes 4.  60000 x 2003, this way and by the tensor cores: loss of 1 row 92 and 442 us, of 8 127
+// and 442, of 16 390 and 442 (the hidden rows no longer fit); gradients of 1 row 366 and 819, of
+// 8 352 and 819, of 16 872 and 821.  128256 x 2048, 1 row: 153 us, 6.9 TB/s.
+constexpr uint32_t kFewRows = 8, kFewThreads = 256, kFewBytes = 96 << 10;   // of the hidden rows at once
+constexpr uint32_t few_tokens(uint32_t rows) { return rows <= 2 ? 8 : 4; }  // of a warp at once
+
+struct FewArgs {
+  const float* hidden;
+  const float* weight;
+  uint64_t ld_h, ld_w;
+  uint32_t B, V, D, chunk;   // columns at once: a multiple of 128 unless it is all of them
+  const uint32_t* bitmask;
+  uint32_t W;
+  const uint32_t* target;
+  float temp;
+  LossOut loss;              // parts by block
+  TermsOut terms;
+  float* d;                  // [V][ROWS]
+};
+
+// Sums N values of every lane over the lanes; lane i ends with those from i * N / 32 on (several
+// lanes with the same one where N < 32)
+template <uint32_t N>
+__device__ __forceinline__ void sum_lanes(float (&v)[N]) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t n = N;
+#pragma unroll
+  for (uint32_t o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n /= 2;
+      const bool upper = lane & o;
+#pragma unroll
+      for (uint32_t i = 0; i < N / 2; ++i)
+        if (i < n) {
+          const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+        }
+    } else {
+      v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    }
+  }
+}
+
+// A warp takes a few tokens at a time, its lanes the columns; the hidden rows lie in shared
+// memory.  WIDE: the weight's rows lie on the 16-byte grid.
+template <uint32_t ROWS, bool WIDE, Readout READ>
+__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const FewArgs a) {
+  constexpr uint32_t T = few_tokens(ROWS), N = T * ROWS, kWarps = kFewThreads / 32;
+  static_assert(N >= 8 && N <= 32, "a value for each lane");
+  extern __shared__ __align__(16) float hidden[];   // [ROWS][chunk]
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_launch_dependents();
+  griddep_wait();
+  // the value that a lane ends with
+  const uint32_t slot = lane / (32 / N), token = slot / ROWS, r = slot % ROWS;
+  const uint32_t target = r < a.B ? a.target[r] : CG_NO_TOKEN;
+  const float c = exp_scale(a.temp);
+  const RowTerms terms = READ == kTerms ? row_terms(a.terms, a.temp, a.B, r, target) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
+  float m = -INFINITY, s = 0.f;
+  const uint32_t tiles = (a.V + kWarps * T - 1) / (kWarps * T);
+  bool loaded = false;
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const uint32_t v0 = (tile * kWarps + warp) * T;
+    const float* w[T];   // past the vocabulary its last row, whose values nobody takes
+#pragma unroll
+    for (uint32_t t = 0; t < T; ++t) w[t] = a.weight + min(v0 + t, a.V - 1) * a.ld_w;
+    float2 acc[N];
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) acc[i] = float2{};
+    for (uint32_t k0 = 0; k0 < a.D; k0 += a.chunk) {
+      const uint32_t n = min(a.chunk, a.D - k0);
+      if (!loaded || a.chunk < a.D) {
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < ROWS * n; i += kFewThreads) {
+          const uint32_t row = i / n, k = i - row * n;
+          hidden[row * a.chunk + k] = row < a.B ? a.hidden[row * a.ld_h + k0 + k] : 0.f;
+        }
+        loaded = true;
+        __syncthreads();
+      }
+      const uint32_t whole = WIDE ? n & ~3u : 0u;
+      if constexpr (WIDE) {
+#pragma unroll 2
+        for (uint32_t k = 4 * lane; k < whole; k += 128) {
+          float4 x[T];
+#pragma unroll
+          for (uint32_t t = 0; t < T; ++t) x[t] = __ldg(reinterpret_cast<const float4*>(w[t] + k0 + k));
+#pragma unroll
+          for (uint32_t b = 0; b < ROWS; ++b) {
+            const float4 h = *reinterpret_cast<const float4*>(hidden + b * a.chunk + k);
+#pragma unroll
+            for (uint32_t t = 0; t < T; ++t) {
+              float2& y = acc[t * ROWS + b];
+              y = __ffma2_rn(make_float2(x[t].x, x[t].y), make_float2(h.x, h.y), y);
+              y = __ffma2_rn(make_float2(x[t].z, x[t].w), make_float2(h.z, h.w), y);
+            }
+          }
+        }
+      }
+#pragma unroll 4
+      for (uint32_t k = whole + lane; k < n; k += 32) {
+        float x[T];
+#pragma unroll
+        for (uint32_t t = 0; t < T; ++t) x[t] = __ldg(w[t] + k0 + k);
+#pragma unroll
+        for (uint32_t b = 0; b < ROWS; ++b) {
+          const float h = hidden[b * a.chunk + k];
+#pragma unroll
+          for (uint32_t t = 0; t < T; ++t) acc[t * ROWS + b].x = fmaf(x[t], h, acc[t * ROWS + b].x);
+        }
+      }
+    }
+    float x[N];
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) x[i] = acc[i].x + acc[i].y;
+    sum_lanes<N>(x);
+    const uint32_t v = v0 + token;
+    bool allowed = v < a.V && r < a.B;
+    if (allowed && a.bitmask) allowed = (a.bitmask[size_t(r) * a.W + (v >> 5)] >> (v & 31)) & 1u;
+    float y = logit(x[0], allowed);
+    if (READ == kLoss) {
+      if (v == target && v < a.V) {   // the target is apart from the others
+        a.loss.target_logit[r] = y;   // (from all lanes that hold it)
+        y = -INFINITY;
+      }
+      if (y > -INFINITY) {
+        const float top = fmaxf(m, y);
+        s = s * (m > -INFINITY ? ex2((m - top) * c) : 0.f) + ex2((y - top) * c);
+        m = top;
+      }
+    } else if (v < a.V && lane % (32 / N) == 0) {
+      const float2 e = terms.scale.fast ? terms.scale.at(y, y) : terms.scale.far(y, y);
+      float d = terms.target == CG_NO_TOKEN ? 0.f : e.x * terms.k;
+      if (v == terms.target) d = terms.at_target;
+      a.d[size_t(v) * ROWS + r] = d;
+    }
+  }
+  if constexpr (READ == kLoss) {
+    // the tokens' lanes of a row, then the warps
+#pragma unroll
+    for (uint32_t o = 32 / T; o < 32; o <<= 1) {
+      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o), top = fmaxf(m, m2);
+      if (top > -INFINITY) s = s * ex2((m - top) * c) + s2 * ex2((m2 - top) * c);   // 0 times 0 for an empty one
+      m = top;
+    }
+    float2(*mine)[ROWS] = reinterpret_cast<float2(*)[ROWS]>(hidden);   // the rows are done with
+    __syncthreads();
+    if (lane < 32 / T && lane % (32 / N) == 0) mine[warp][r] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x < a.B) {
+      float top = -INFINITY, sum = 0.f;
+      for (uint32_t i = 0; i < kWarps; ++i) top = fmaxf(top, mine[i][threadIdx.x].x);
+      if (top > -INFINITY)
+        for (uint32_t i = 0; i < kWarps; ++i) sum += mine[i][threadIdx.x].y * ex2((mine[i][threadIdx.x].x - top) * c);
+      a.loss.part[size_t(blockIdx.x) * a.B + threadIdx.x] = make_float2(top, sum);
+    }
+  }
+}
+
+constexpr uint32_t kFewGradThreads = 128, kFewAhead = 4;
+struct FewGradArgs {
+  const float* hidden;
+  const float* weight;
+  const float* d;            // [V][ROWS]
+  uint64_t ld_h, ld_w;
+  uint32_t B, V, D, slabs, each;   // tokens of a block
+  float* dw;                 // or none
+  uint64_t ld_dw;
+  float* sums;               // [blocks of tokens][B][ld_sums], or none
+  uint32_t ld_sums;
+};
+// A thread takes 4 columns (WIDE: side by side, in one vector) over a block's tokens: grad_weight's
+// elements, and its part of grad_hidden's sums
+template <uint32_t ROWS, bool WIDE>
+__global__ void __launch_bounds__(kFewGradThreads) few_grad_kernel(const FewGradArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t split = blockIdx.x / a.slabs, base = (blockIdx.x - split * a.slabs) * (4 * kFewGradThreads);
+  const uint32_t from = split * a.each, to = min(a.V, from + a.each);
+  uint32_t col[4];
+  bool there[4];
+#pragma unroll
+  for (uint32_t q = 0; q < 4; ++q) {
+    col[q] = base + (WIDE ? 4 * threadIdx.x + q : threadIdx.x + q * kFewGradThreads);
+    there[q] = col[q] < a.D;
+  }
+  if (!there[0]) return;
+  const bool wide = WIDE && there[3];
+  float2 h[ROWS][2], acc[ROWS][2];
+#pragma unroll
+  for (uint32_t b = 0; b < ROWS; ++b)
+#pragma unroll
+    for (uint32_t q = 0; q < 2; ++q) {
+      const float* x = a.hidden + b * a.ld_h;
+      h[b][q] = make_float2(b < a.B && there[2 * q] ? x[col[2 * q]] : 0.f, b < a.B && there[2 * q + 1] ? x[col[2 * q + 1]] : 0.f);
+      acc[b][q] = float2{};
+    }
+  for (uint32_t v0 = from; v0 < to; v0 += kFewAhead) {
+    float4 w[kFewAhead];
+    if (a.sums)
+#pragma unroll
+      for (uint32_t u = 0; u < kFewAhead; ++u) {
+        if (v0 + u >= to) break;
+        const float* x = a.weight + (v0 + u) * a.ld_w;
+        if (wide) w[u] = __ldg(reinterpret_cast<const float4*>(x + col[0]));
+        else w[u] = make_float4(x[col[0]], there[1] ? x[col[1]] : 0.f, there[2] ? x[col[2]] : 0.f, there[3] ? x[col[3]] : 0.f);
+      }
+#pragma unroll
+    for (uint32_t u = 0; u < kFewAhead; ++u) {
+      if (v0 + u >= to) break;
+      float2 y[2] = {};
+      const float* at = a.d + size_t(v0 + u) * ROWS;
+#pragma unroll
+      for (uint32_t b = 0; b < ROWS; ++b) {
+        const float d = at[b];
+        const float2 d2 = make_float2(d, d);
+        if (a.dw) {
+          y[0] = __ffma2_rn(d2, h[b][0], y[0]);
+          y[1] = __ffma2_rn(d2, h[b][1], y[1]);
+        }
+        if (a.sums) {
+          acc[b][0] = __ffma2_rn(d2, make_float2(w[u].x, w[u].y), acc[b][0]);
+          acc[b][1] = __ffma2_rn(d2, make_float2(w[u].z, w[u].w), acc[b][1]);
+        }
+      }
+      if (a.dw) {
+        float* out = a.dw + (v0 + u) * a.ld_dw;
+        if (wide) {
+          *reinterpret_cast<float4*>(out + col[0]) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+        } else {
+          out[col[0]] = y[0].x;
+          if (there[1]) out[col[1]] = y[0].y;
+          if (there[2]) out[col[2]] = y[1].x;
+          if (there[3]) out[col[3]] = y[1].y;
+        }
+      }
+    }
+  }
+  if (a.sums)
+#pragma unroll
+    for (uint32_t b = 0; b < ROWS; ++b)
+      if (b < a.B) {
+        float* out = a.sums + (size_t(split) * a.B + b) * a.ld_sums;
+        out[col[0]] = acc[b][0].x;
+        if (there[1]) out[col[1]] = acc[b][0].y;
+        if (there[2]) out[col[2]] = acc[b][1].x;
+        if (there[3]) out[col[3]] = acc[b][1].y;
+      }
+}
+
 // bf16 rows off the 16-byte grid are copied onto it; float rows are split into three parts
 // that add up to the value (8 bits each; a value that is not finite is its first part).  A
 // thread writes 8 columns at once.
@@ -1027,6 +1282,7 @@ struct HeadPlan {
   uint64_t ld_terms, ld_sums;
   uint32_t splits;           // of the product that sums over tokens
   bool pair;                 // rows in pairs of blocks
+  uint32_t few;              // or none of all this: few rows of float matrices, as many as this at most
   size_t at_h, at_w, at_part, at_target, at_terms, at_sums, bytes;
 };
 
@@ -1048,6 +1304,29 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   p.D = D;
   p.Dp = uint32_t(up_to(D, 8));
   const bool f32 = dtype == CG_F32;
+  p.few = f32 && B <= kFewRows ? B <= 2 ? std::max(B, 1u) : B <= 4 ? 4 : 8 : 0;
+  if (p.few) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+      const size_t here = at;
+      at += up_to(bytes, 256);
+      return here;
+    };
+    p.groups = std::min(tiles_of(V, kFewThreads / 32 * few_tokens(p.few)), 2 * kHeadSms);
+    p.ld_sums = up_to(D, 4);
+    // four blocks an SM
+    p.splits = std::min(std::max(1u, 4 * kHeadSms / tiles_of(D, 4 * kFewGradThreads)), tiles_of(V, 16));
+    p.splits = tiles_of(V, tiles_of(V, p.splits));
+    if (!grad) {
+      p.at_part = take(size_t(p.groups) * B * 8);
+      p.at_target = take(size_t(B) * 4);
+    } else {
+      p.at_terms = take(size_t(V) * p.few * 4);
+      p.at_sums = take(size_t(p.splits) * B * p.ld_sums * 4);
+    }
+    p.bytes = at;
+    return p;
+  }
   p.parts = f32 ? 3 : 1;
   p.term_parts = f32 ? 3 : B <= kBlockM ? 2 : 1;
   p.lay_h = f32 || !rows_on_grid(hidden, dtype, ld_h);
@@ -1199,25 +1478,76 @@ Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v
   return j;
 }
 
+template <uint32_t ROWS, Readout READ>
+cudaError_t launch_few(int device, const HeadPlan& p, FewArgs& f, cudaStream_t stream) {
+  f.chunk = uint32_t(std::min<uint64_t>(up_to(f.D, 4), kFewBytes / (ROWS * 4) / 128 * 128));
+  const size_t smem = size_t(ROWS) * std::max(f.chunk * 4, kFewThreads / 32 * 8);
+  return rows_on_grid(f.weight, CG_F32, f.ld_w)
+             ? launch_clusters<few_kernel<ROWS, true, READ>>(device, p.groups, 1, kFewThreads, smem, stream, f)
+             : launch_clusters<few_kernel<ROWS, false, READ>>(device, p.groups, 1, kFewThreads, smem, stream, f);
+}
+template <uint32_t ROWS>
+cudaError_t launch_few_grad(const HeadPlan& p, const FewGradArgs& f, cudaStream_t stream) {
+  const bool wide = (!f.sums || rows_on_grid(f.weight, CG_F32, f.ld_w)) && (!f.dw || rows_on_grid(f.dw, CG_F32, f.ld_dw));
+  return launch_dependent(wide ? few_grad_kernel<ROWS, true> : few_grad_kernel<ROWS, false>, dim3(f.slabs * p.splits),
+                          dim3(kFewGradThreads), 0, stream, f);
+}
+template <Readout READ>
+cudaError_t launch_few(int device, const HeadPlan& p, FewArgs& f, cudaStream_t stream) {
+  switch (p.few) {
+    case 1: return launch_few<1, READ>(device, p, f, stream);
+    case 2: return launch_few<2, READ>(device, p, f, stream);
+    case 4: return launch_few<4, READ>(device, p, f, stream);
+    default: return launch_few<8, READ>(device, p, f, stream);
+  }
+}
+cudaError_t launch_few_grad(const HeadPlan& p, const FewGradArgs& f, cudaStream_t stream) {
+  switch (p.few) {
+    case 1: return launch_few_grad<1>(p, f, stream);
+    case 2: return launch_few_grad<2>(p, f, stream);
+    case 4: return launch_few_grad<4>(p, f, stream);
+    default: return launch_few_grad<8>(p, f, stream);
+  }
+}
+FewArgs few_args(const HeadArgs& a, const CtxView& v) {
+  FewArgs f = {};
+  f.hidden = static_cast<const float*>(a.hidden);
+  f.weight = static_cast<const float*>(a.weight);
+  f.ld_h = a.ld_h;
+  f.ld_w = a.ld_w;
+  f.B = a.B;
+  f.V = a.V;
+  f.D = a.D;
+  f.bitmask = a.bitmask;
+  f.W = v.t.W;
+  f.target = a.target;
+  f.temp = a.temp;
+  return f;
+}
+
 int head_loss(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, float* loss, float* lse, float* norm, unsigned char* ws) {
   DeviceGuard dg(ctx_device(c), "cg_head_loss");
   if (!dg.ok) return CG_E_CUDA;
   const CtxView v = ctx_view(c);
   const int dev = ctx_device(c);
+  const LossOut out{reinterpret_cast<float2*>(ws + p.at_part), reinterpret_cast<float*>(ws + p.at_target)};
   Operands o{a.hidden, a.weight, a.ld_h, a.ld_w};
-  for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
+  if (p.few) {
+    FewArgs f = few_args(a, v);
+    f.loss = out;
+    if (launch_few<kLoss>(dev, p, f, v.stream) != cudaSuccess) return CG_E_CUDA;
+  }
+  for (uint32_t v0 = 0; !p.few && v0 < p.V; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, p.V - v0);
     if (lay_out(a, p, v0, n, ws, o, v.stream) != cudaSuccess) return CG_E_CUDA;
     Job j = logits_of(a, p, v, v0, n);
-    j.loss.part = reinterpret_cast<float2*>(ws + p.at_part);
-    j.loss.target_logit = reinterpret_cast<float*>(ws + p.at_target);
+    j.loss = out;
     if (!map_h(&j.p[0].a, p, o, h_rows(p)) || !map_w(&j.p[0].b, p, o, p.lay_w ? n : p.V, b_rows(p))) return CG_E_CUDA;
     if (launch_job<kLoss>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
   }
   return launch_dependent(join_loss_kernel, dim3(tiles_of(p.B, 32)), dim3(1024), 0, v.stream,
-                          reinterpret_cast<const float2*>(ws + p.at_part),
-                          reinterpret_cast<const float*>(ws + p.at_target), a.target, p.groups, p.B, p.V, a.temp,
-                          loss, lse, norm, v.t.status) == cudaSuccess
+                          static_cast<const float2*>(out.part), static_cast<const float*>(out.target_logit), a.target,
+                          p.groups, p.B, p.V, a.temp, loss, lse, norm, v.t.status) == cudaSuccess
              ? CG_OK
              : CG_E_CUDA;
 }
@@ -1247,9 +1577,31 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
   __nv_bfloat16* terms = reinterpret_cast<__nv_bfloat16*>(ws + p.at_terms);
   const uint64_t part_stride = uint64_t(p.B) * p.ld_terms;
   // the hidden rows' gradient is summed over pieces and splits in 32 bits where there are several
-  const bool summed = p.splits > 1 || p.piece < p.V;
+  const bool summed = p.few || p.splits > 1 || p.piece < p.V;
   float* sums = reinterpret_cast<float*>(ws + p.at_sums);
-  for (uint32_t v0 = 0; v0 < p.V; v0 += p.piece) {
+  if (p.few) {
+    FewArgs f = few_args(a, v);
+    f.terms = TermsOut{loss, norm, up};
+    f.d = reinterpret_cast<float*>(ws + p.at_terms);
+    if (launch_few<kTerms>(dev, p, f, v.stream) != cudaSuccess) return CG_E_CUDA;
+    FewGradArgs g = {};
+    g.hidden = f.hidden;
+    g.weight = f.weight;
+    g.d = f.d;
+    g.ld_h = a.ld_h;
+    g.ld_w = a.ld_w;
+    g.B = a.B;
+    g.V = a.V;
+    g.D = a.D;
+    g.slabs = tiles_of(a.D, 4 * kFewGradThreads);
+    g.each = tiles_of(a.V, p.splits);
+    g.dw = static_cast<float*>(dw);
+    g.ld_dw = ld_dw;
+    g.sums = dh ? sums : nullptr;
+    g.ld_sums = uint32_t(p.ld_sums);
+    if (launch_few_grad(p, g, v.stream) != cudaSuccess) return CG_E_CUDA;
+  }
+  for (uint32_t v0 = 0; !p.few && v0 < p.V; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, p.V - v0);
     if (lay_out(a, p, v0, n, ws, o, v.stream) != cudaSuccess) return CG_E_CUDA;
     const uint32_t w_rows = p.lay_w ? n : p.V;

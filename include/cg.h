@@ -595,9 +595,10 @@ int cg_embed_grad(cg_ctx* c, const void* d_grad, int dtype, uint32_t N, uint32_t
  *   norm[b] = max x over A_b and sum over A_b of exp((x_v - max) / T), -inf and 0 for
  *             an empty A_b: what cg_head_grad takes.
  * A loss near 0 keeps its relative precision.  The products of bf16 matrices are summed
- * in 32 bits; float matrices are multiplied as three bf16 parts each, to about the
- * precision of 32-bit products, and have to be finite and below 2^127 (in bf16 ones a
- * row of the weight that is not finite reaches only the rows that allow its token).
+ * in 32 bits; float matrices are multiplied in 32 bits up to 8 rows, from then on as three
+ * bf16 parts each, to about the precision of 32-bit products, and have to be finite and
+ * below 2^127 (in bf16 ones a row of the weight that is not finite reaches only the rows
+ * that allow its token).
  *  d_hidden : [B][ld_hidden], d_weight : [V][ld_weight], of D columns
  *  d_bitmask: u32 [B][W] or NULL: every token is allowed
  *  d_target : u32 [B]; temp : T > 0, finite

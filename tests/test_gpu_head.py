@@ -220,3 +220,13 @@ def test_head_in_several_pieces(B, V, D, dtype):
 @pytest.mark.parametrize("T", [1e-3, 0.05, 50.0])
 def test_head_temperatures(T):
     run(70, 1000, 64, "bf16", T=T, std=0.01 if T < 0.01 else 2.0)
+
+
+@pytest.mark.parametrize("B", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("V,D,pad,shift", [(500, 1, 0, 0), (777, 131, 1, 0), (4013, 516, 0, 3), (4013, 516, 4, 4), (513, 9001, 3, 0), (600, 24580, 0, 0)])
+def test_head_few_float_rows(B, V, D, pad, shift):
+    """Multiplied without the tensor cores (products in 32 bits, in shorter chains: the bounds above hold), on and
+    off the 16-byte grid, in one stretch of the columns and in several."""
+    run(B, V, D, "f32", pad, shift, masked=B != 3, T=0.8)
+    if B < 3:
+        run(B, V, D, "f32", pad, shift, which="dh" if B == 1 else "dw")
