@@ -54,7 +54,8 @@ enum Readout { kLoss, kTerms, kOut };
 // stage, in chains, the five small ones in an accumulator of their own (in the large one's they
 // would each cost a step that is not rounded to nearest).  kTwo is kOne with terms of two parts:
 // up to 128 rows, whose products wait for the weight, the terms keep 16 bits (rounded to 8, the one
-// term that makes up a row's gradient would double its error).
+// term that makes up a row's gradient would double its error).  Pairs of blocks would take it
+// worse: 192 x 32000 x 2048 108 -> 127 us.
 enum Sums { kOne, kChains, kParts, kTwo };
 constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : sums == kTwo ? 2 : 1; }  // of a stage
 // Stages of a chain.  A chain of sums in tensor memory drifts, as its steps are not rounded to
@@ -116,6 +117,7 @@ struct Job {
   float temp;
   LossOut loss;
   TermsOut terms;
+  uint32_t rows;             // of the batch
   uint32_t* status;
 };
 
@@ -325,19 +327,32 @@ struct Boxes {
   }
 };
 
+// The significand of the first g / T among 32 rows that is a normal number.  Terms rounded to bf16 are
+// rounded in units of it, and the gradients multiplied by it: where all rows have one g, as under a
+// mean, a target's term -g / T (1 - p) is then near a power of two and all but exact, where
+// g / T itself may be rounded by up to 2^-8, the same way in every row.
+__device__ __forceinline__ float common_scale(const Job& job) {
+  const uint32_t lane = threadIdx.x & 31;
+  const float g = __fdiv_rn(!job.terms.up ? 1.f : lane < job.rows ? job.terms.up[lane] : 0.f, job.temp);
+  const uint32_t who = __ballot_sync(0xFFFFFFFFu, fabsf(g) >= FLT_MIN && fabsf(g) <= FLT_MAX);
+  const uint32_t bits = __shfl_sync(0xFFFFFFFFu, __float_as_uint(g), who ? __ffs(who) - 1 : 0);
+  return who ? __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u) : 1.f;
+}
+
 // d = k * exp((x - m) / T), at the target as it stands
 struct RowTerms {
   Scale scale;
   float k, at_target;
   uint32_t target;           // CG_NO_TOKEN in a row that does not count
 };
-__device__ __forceinline__ RowTerms row_terms(const TermsOut& terms, float temp, uint32_t rows, uint32_t r, uint32_t target) {
+__device__ __forceinline__ RowTerms row_terms(const TermsOut& terms, float temp, uint32_t rows, uint32_t r, uint32_t target,
+                                              float scale = 1.f) {
   const float c = exp_scale(temp);
   if (r < rows && target != CG_NO_TOKEN) {
     const float loss = terms.loss[r], m = terms.norm[2 * size_t(r)], s = terms.norm[2 * size_t(r) + 1];
     if (loss > 0.f) {   // a loss of 0: no target that counts, or nothing beside it
       Scale t(c, m);
-      const float g = __fdiv_rn(terms.up ? terms.up[r] : 1.f, temp);
+      const float g = __fdiv_rn(__fdiv_rn(terms.up ? terms.up[r] : 1.f, temp), scale);
       float k = __fdiv_rn(g, s) * t.rest;
       if (!(fabsf(k) <= FLT_MAX)) {
         // an infinite or NaN g, whose terms are not finite, but 0 for the tokens that are not allowed: as
@@ -674,6 +689,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
     Boxes<S::kBoxes ? S::kBoxes : 1> boxes(boxes_at + (warp - kFirstReader) * S::kBoxes * kStore);
     uint32_t n = 0;
     const float c = exp_scale(job.temp);
+    const float scale = READ != kLoss && SUMS == kOne ? common_scale(job) : 1.f;
     // frees the accumulator that has been read
     auto done = [&](uint32_t acc) {
       tc::fence_before_sync();
@@ -706,7 +722,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         if (r < p.m) target = job.target[r];
       }
       RowSum sum;
-      const RowTerms terms = READ == kTerms ? row_terms(job.terms, job.temp, job.p[0].m, r, target) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
+      const RowTerms terms = READ == kTerms ? row_terms(job.terms, job.temp, job.p[0].m, r, target, scale) : RowTerms{Scale(0.f, 0.f), 0.f, 0.f, CG_NO_TOKEN};
       auto read = [&](float* x, uint32_t j, uint32_t word) {
         if (READ == kLoss) {
           read_loss(job, x, r, col + 32 * j, target, word, c, sum);
@@ -763,7 +779,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           tc::tmem_wait();
           if (j + 1 == chunks && blocks) done(acc);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]);
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]) * (READ == kOut ? scale : 1.f);
           if (!blocks) {   // a split without stages: nothing was multiplied
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -1474,6 +1490,7 @@ Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v
   j.v0 = v0;
   j.target = a.target;
   j.temp = a.temp;
+  j.rows = p.B;
   j.status = v.t.status;
   return j;
 }
@@ -1613,7 +1630,9 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
     if (launch_job<kTerms>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
 
     Job g = {};
-    g.temp = 1.f;
+    g.temp = a.temp;
+    g.terms.up = up;
+    g.rows = p.B;
     g.status = v.t.status;
     if (dh) {  // terms [B][n] x W [n][D], summed over the pieces
       Product& q = g.p[0];

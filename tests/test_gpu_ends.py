@@ -338,6 +338,28 @@ def test_values_that_are_not_finite():
     assert open_[0][7] == 0
 
 
+@pytest.mark.parametrize("up", [1.0, 1 / 85, -1 / 4095])
+def test_one_gradient_for_all_rows_is_rounded_once(up):
+    """bf16 terms under one g: the targets' terms are g / T (1 - p), p at most 0.1 here, rounded in units of g / T's
+    significand to 2^-9 relative of a value next to a power of two, evenly spread: 2^-9 / sqrt 3.  The other terms
+    are spread over many tokens, so their roundings count less than a third of that.  With the result's own
+    rounding of 2^-8 / sqrt 3 or less on average over significands (sqrt(1/2) of it): 1.3 of what it gives alone."""
+    import torch
+    V, B, D, T = 4000, 300, 64, 0.85
+    ctx, g = ctx_of(V), generator(3)
+    h, w = matrix(B, D, "bf16", 0, 0, g, 1.0), matrix(V, D, "bf16", 0, 0, g, D ** -0.5)
+    target = torch.randint(0, V, (B,), generator=g, device="cuda").int()
+    loss, lse, norm = (torch.empty(s, device="cuda") for s in ((B,), (B,), (B, 2)))
+    dh, dw, ups = torch.empty_like(h), torch.empty_like(w), torch.full((B,), up, device="cuda")
+    ctx.head_loss(h, w, target, loss, temp=T, out_lse=lse, out_norm=norm)
+    ctx.head_grad(h, w, target, loss, norm, dh, dw, temp=T, grad_loss=ups)
+    e = Exact(h, w, target, T, None, ups.double(), "bf16")
+    assert float(e.loss.min()) > 2.4   # p at most 0.1
+    for got, want in ((dh, e.d @ e.w), (dw, e.d.T @ e.h)):
+        once = float((want.bfloat16().double() - want).norm())
+        assert float((got.double() - want).norm()) <= 1.3 * once
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("masked", [False, True])
 @pytest.mark.parametrize("B", [40, 200])
