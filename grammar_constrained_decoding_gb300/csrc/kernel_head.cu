@@ -119,6 +119,10 @@ struct Job {
   TermsOut terms;
   uint32_t rows;             // of the batch
   uint32_t* status;
+  // kOut: the weight from the piece's first token on, and the piece's tokens
+  const __nv_bfloat16* w;
+  uint64_t ld_w;
+  uint32_t tokens;
 };
 
 struct Ends {
@@ -495,6 +499,37 @@ __device__ __forceinline__ void send_grad(const Product& p, const float* x, uint
   __syncwarp();
 }
 
+// What rounding to bf16 left of row r's term at its target, or 0 where that is not in the piece.  It is
+// the row's largest term, and added times the target's row of the weight as the row's gradient is read
+// out: with a g for each row 1.0 times one rounding's error in place of 1.4 to 1.5, for a read of B
+// rows.  (In the gradient by the weight each reader would have to look for its tokens' rows: 192 x
+// 32000 x 2048 108 -> 166 us.)
+__device__ __forceinline__ float target_rest(const Job& job, uint32_t r, uint32_t target, float scale) {
+  if (target - job.v0 >= job.tokens) return 0.f;
+  const float loss = job.terms.loss[r];
+  if (!(loss > 0.f)) return 0.f;
+  const float d = __fdiv_rn(__fdiv_rn(job.terms.up ? job.terms.up[r] : 1.f, job.temp), scale) * expm1f(-loss);
+  return d - __bfloat162float(__float2bfloat16_rn(d));
+}
+// x += e * 32 columns of a row from `col` on
+__device__ __forceinline__ void add_row(float* x, float e, const __nv_bfloat16* row, uint32_t col, uint32_t columns) {
+#pragma unroll
+  for (uint32_t q = 0; q < 4; ++q) {
+    if (col + 8 * q + 8 <= columns) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + col + 8 * q);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        x[8 * q + 2 * i] = fmaf(e, __uint_as_float(w[i] << 16), x[8 * q + 2 * i]);
+        x[8 * q + 2 * i + 1] = fmaf(e, __uint_as_float(w[i] & 0xFFFF0000u), x[8 * q + 2 * i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 8; ++i)
+        if (col + 8 * q + i < columns) x[8 * q + i] = fmaf(e, __bfloat162float(row[col + 8 * q + i]), x[8 * q + i]);
+    }
+  }
+}
 // What boxes leave of a gradient's rows, at most 15 bytes of each: a lane's row as it lies in the
 // box that a reader of `columns` from `col` on wrote last, if that is the rows' last
 __device__ __forceinline__ void send_rest(const Product& p, uint32_t box, uint32_t row0, uint32_t col, uint32_t columns) {
@@ -708,7 +743,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
       __syncwarp();
       return true;
     };
-    auto read_item = [&](const Product& p) {
+    auto read_item = [&](const Product& p, bool second) {
       const Work w = work_of<CTAS, S, NARROW>(p, t);
       // the reader's columns: half of the tile's, at least 64 (the second half's readers then have none)
       const uint32_t wide = NARROW ? max(64u, p.tile_n / 2) : S::kWidth / 2;
@@ -767,6 +802,16 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         for (uint32_t j = 0; j < 4; ++j)
           if (j < chunks && rows) read(v + 32 * j, j, words[j]);
       } else {
+        float rest = 0.f;
+        const __nv_bfloat16* target_row = nullptr;
+        if (READ == kOut && SUMS == kOne && !second) {
+          if (w.split == 0 && r < p.m) {
+            const uint32_t t = job.target[r];
+            rest = target_rest(job, r, t, scale);
+            target_row = job.w + uint64_t(t - job.v0) * job.ld_w;
+          }
+          __syncwarp();
+        }
         if (blocks && !full(n)) return false;
         const uint32_t acc = n & 1u;
         n += blocks != 0;
@@ -779,7 +824,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           tc::tmem_wait();
           if (j + 1 == chunks && blocks) done(acc);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]) * (READ == kOut ? scale : 1.f);
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]);
+          if (READ == kOut && SUMS == kOne && !second) {
+            if (rest != 0.f) add_row(v, rest, target_row, col + 32 * j, p.n);
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= READ == kOut ? scale : 1.f;
           if (!blocks) {   // a split without stages: nothing was multiplied
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -794,7 +845,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
     };
     // (each product read where it lies: through a pointer to either the gradients' tiles took a fifth longer)
     bool ok = true;
-    while (ok && turns.next(second, t)) ok = READ == kOut && second ? read_item(job.p[1]) : read_item(job.p[0]);
+    while (ok && turns.next(second, t)) ok = READ == kOut && second ? read_item(job.p[1], true) : read_item(job.p[0], false);
     if (READ != kLoss && lane == 0) tc::stores_done();
   }
   __syncwarp();
@@ -1633,7 +1684,12 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
     g.temp = a.temp;
     g.terms.up = up;
     g.rows = p.B;
-    g.status = v.t.status;
+    g.terms.loss = loss;
+    g.target = a.target;
+    g.v0 = v0;
+    g.tokens = n;
+    g.w = static_cast<const __nv_bfloat16*>(o.w) + (p.lay_w ? 0 : uint64_t(v0) * o.ld_w);   // (float matrices' is not read)
+    g.ld_w = o.ld_w;
     if (dh) {  // terms [B][n] x W [n][D], summed over the pieces
       Product& q = g.p[0];
       q.m = p.B;

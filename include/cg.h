@@ -618,8 +618,8 @@ int cg_head_loss(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtyp
  * p_t - 1 is taken from the loss, as expm1(-loss).  An infinite or NaN g_b gives terms that
  * are not finite over A_b, and 0 elsewhere as any other.  Terms d of bf16 matrices are rounded
  * to bf16 for the products (a relative error of 2^-8 at most, as the gradients' own
- * rounding has), in units that keep one g_b / T for all rows exact; with up to 128 rows
- * to two bf16 parts (2^-16). hidden and weight have
+ * rounding has), in units that keep one g_b / T for all rows exact; by hidden the targets'
+ * terms count whole.  Up to 128 rows d keeps two bf16 parts (2^-16).  hidden and weight have
  * to be finite: 0 * inf is NaN, also for a token that no row allows.
  *  d_loss, d_norm : as cg_head_loss wrote them for the same arguments
  *  d_out_grad_hidden : [B][ld_grad_hidden] or NULL; d_out_grad_weight :

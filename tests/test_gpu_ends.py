@@ -360,6 +360,28 @@ def test_one_gradient_for_all_rows_is_rounded_once(up):
         assert float((got.double() - want).norm()) <= 1.3 * once
 
 
+@pytest.mark.parametrize("B,D,pad", [(130, 136, 0), (200, 70, 1), (300, 72, 8), (700, 33, 7)])
+def test_gradient_by_rows_is_rounded_once(B, D, pad):
+    """bf16 terms under a g for each row: the targets' terms count whole, the others (p at most 0.1) are spread over
+    many tokens, so their roundings of 2^-9 / sqrt 3 shrink with the number of them: below a third of the result's
+    own.  1.3 of that alone, as above; one rounding more would make it 1.41."""
+    import torch
+    V, T = 4000, 0.85
+    ctx, g = ctx_of(V), generator(B)
+    h, w = matrix(B, D, "bf16", pad, 0, g, 1.0), matrix(V, D, "bf16", pad, 0, g, D ** -0.5)
+    target = torch.randint(0, V, (B,), generator=g, device="cuda").int()
+    target[5], target[9] = -1, V - 1
+    loss, lse, norm = (torch.empty(s, device="cuda") for s in ((B,), (B,), (B, 2)))
+    dh, up = torch.empty(B, D, dtype=h.dtype, device="cuda"), torch.rand(B, generator=g, device="cuda") - 0.3
+    ctx.head_loss(h, w, target, loss, temp=T, out_lse=lse, out_norm=norm)
+    ctx.head_grad(h, w, target, loss, norm, dh, temp=T, grad_loss=up)
+    e = Exact(h, w, target, T, None, up.double(), "bf16")
+    e.check_grad(dh, None)
+    assert float(e.loss[target >= 0].min()) > 2.4
+    want = e.d @ e.w
+    assert float((dh.double() - want).norm()) <= 1.3 * float((want.bfloat16().double() - want).norm())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("masked", [False, True])
 @pytest.mark.parametrize("B", [40, 200])
