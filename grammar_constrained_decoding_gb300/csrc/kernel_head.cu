@@ -27,6 +27,7 @@
 // cycle from L2 as an SM can get (64), and a stage 560 to 600 cycles instead of 512.
 #include <algorithm>
 
+#include "head_jobs.h"
 #include "logit_row.cuh"
 #include "matrix_args.h"
 #include "tensor_core.cuh"
@@ -76,53 +77,6 @@ struct Stage {
   static constexpr uint32_t kBytes = kPartsA * kA + kPartsB * kB;
   static constexpr uint32_t kBoxes = READ == kLoss ? 0 : SUMS == kTwo && READ == kTerms ? 2 : kBoxesEach;
   static constexpr uint32_t kCount = (kMaxSmem - 2048 - kReaders * kBoxes * kStore) / kBytes;
-};
-
-// What is read out of the tiles
-struct LossOut {
-  float2* part;              // [readers' column groups over all pieces][B]: maximum and sum without the target
-  float* target_logit;       // [B], written by the tile that holds the row's target
-};
-struct TermsOut {
-  const float* loss;
-  const float* norm;
-  const float* up;
-};
-struct GradOut {
-  bool boxes;                // written (added, with `add`) as boxes of `out`; else element by element to `at`
-  bool add, f32;
-  uint32_t whole;            // columns that boxes write: a box ends on the 16-byte grid, whatever lies there
-  void* at;                  // [m][ld]
-  uint64_t ld;
-};
-
-struct Product {
-  CUtensorMap a, b, out;     // operands; the terms or the gradient as they are written
-  uint32_t m, n, n_m, n_n;   // extent, and in tiles
-  uint32_t tile_n;           // columns of a tile: 256, or 128 or 64 where tiles are few
-  uint32_t a_rows, k_rows;   // rows of a box of A where k is its width, of A and B where k is their rows
-  uint32_t blocks, splits;   // stages of one product; splits of them
-  int a_mn, a_k, b_mn, b_k;  // where the product begins in the maps
-  GradOut grad;
-};
-// What a launch computes: one product, or (kOut) the gradient by the hidden rows and the one
-// by the weight
-struct Job {
-  Product p[2];
-  uint32_t early;            // items of the second product that a pair without a last item of the first takes meanwhile
-  // the rows' vocabulary side (kLoss, kTerms)
-  const uint32_t* bitmask;
-  uint32_t W, v0;            // words a row; the piece's first token
-  const uint32_t* target;
-  float temp;
-  LossOut loss;
-  TermsOut terms;
-  uint32_t rows;             // of the batch
-  uint32_t* status;
-  // kOut: the weight from the piece's first token on, and the piece's tokens
-  const __nv_bfloat16* w;
-  uint64_t ld_w;
-  uint32_t tokens;
 };
 
 struct Ends {
@@ -808,7 +762,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
           if (w.split == 0 && r < p.m) {
             const uint32_t t = job.target[r];
             rest = target_rest(job, r, t, scale);
-            target_row = job.w + uint64_t(t - job.v0) * job.ld_w;
+            target_row = static_cast<const __nv_bfloat16*>(job.w) + uint64_t(t - job.v0) * job.ld_w;
           }
           __syncwarp();
         }
@@ -1437,6 +1391,7 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
 
 template <int CTAS, Readout READ, Sums SUMS, bool NARROW>
 cudaError_t launch_job(int device, Job& j, cudaStream_t stream) {
+  if (!j.status) return cudaErrorInvalidValue;   // where a wait that runs out writes
   uint32_t items[2] = {0, 0}, longest[2] = {0, 0};
   for (int i = 0; i < (READ == kOut ? 2 : 1); ++i) {
     Product& p = j.p[i];
@@ -1469,17 +1424,6 @@ cudaError_t launch_job(int device, const HeadPlan& p, Job& j, cudaStream_t strea
     return p.pair ? launch_job<2, READ, READ != kOut>(device, p, j, stream) : launch_job<1, READ, READ != kOut>(device, p, j, stream);
   return p.pair ? launch_job<2, READ, false>(device, p, j, stream) : launch_job<1, READ, false>(device, p, j, stream);
 }
-
-struct HeadArgs {
-  const void* hidden;
-  const void* weight;
-  int dtype;
-  uint32_t B, V, D;
-  uint64_t ld_h, ld_w;
-  const uint32_t* bitmask;
-  const uint32_t* target;
-  float temp;
-};
 
 // the operands as the tensor copies read them: the caller's, or laid out in the workspace
 struct Operands {
@@ -1527,7 +1471,7 @@ uint32_t b_rows(const HeadPlan& p) { return std::min(128u, p.tile_n / (p.pair ? 
 uint32_t h_rows(const HeadPlan& p) { return std::min<uint32_t>(kBlockM, uint32_t(up_to(p.B, 8))); }
 // x = H W^T of a piece, read out one way or the other
 Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v0, uint32_t n) {
-  Job j = {};
+  Job j(a, v.t.W, v.t.status, v0, n);
   Product& q = j.p[0];
   q.m = p.B;
   q.n = n;
@@ -1536,13 +1480,6 @@ Job logits_of(const HeadArgs& a, const HeadPlan& p, const CtxView& v, uint32_t v
   q.tile_n = p.tile_n;
   q.a_rows = h_rows(p);
   q.b_mn = p.lay_w ? 0 : int(v0);
-  j.bitmask = a.bitmask;
-  j.W = v.t.W;
-  j.v0 = v0;
-  j.target = a.target;
-  j.temp = a.temp;
-  j.rows = p.B;
-  j.status = v.t.status;
   return j;
 }
 
@@ -1680,14 +1617,8 @@ int head_grad(cg_ctx* c, const HeadArgs& a, const HeadPlan& p, const float* loss
       return CG_E_CUDA;
     if (launch_job<kTerms>(dev, p, j, v.stream) != cudaSuccess) return CG_E_CUDA;
 
-    Job g = {};
-    g.temp = a.temp;
-    g.terms.up = up;
-    g.rows = p.B;
-    g.terms.loss = loss;
-    g.target = a.target;
-    g.v0 = v0;
-    g.tokens = n;
+    Job g(a, v.t.W, v.t.status, v0, n);
+    g.terms = j.terms;
     g.w = static_cast<const __nv_bfloat16*>(o.w) + (p.lay_w ? 0 : uint64_t(v0) * o.ld_w);   // (float matrices' is not read)
     g.ld_w = o.ld_w;
     if (dh) {  // terms [B][n] x W [n][D], summed over the pieces

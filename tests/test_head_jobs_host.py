@@ -1,0 +1,48 @@
+"""Host-side checks of what the output layer's launches are made of (csrc/head_jobs.h), compiled without a GPU."""
+
+import os
+import re
+import subprocess
+
+import pytest
+
+gcd = pytest.importorskip("grammar_constrained_decoding_gb300")
+from grammar_constrained_decoding_gb300 import build  # noqa: E402
+
+CSRC = os.path.join(os.path.dirname(gcd.__file__), "csrc")
+
+
+def compile_and_run(tmp_path, program, *args):
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc()))), "include")
+    source, binary = str(tmp_path / "t.cpp"), str(tmp_path / "t")
+    with open(source, "w") as f:
+        f.write(program)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", f"-I{CSRC}", f"-isystem{include}", source, "-o", binary], check=True)
+    return subprocess.run([binary, *args], capture_output=True, text=True, check=True).stdout
+
+
+JOB = r"""
+#include <cstdio>
+#include <type_traits>
+#include "head_jobs.h"
+using namespace cgk;
+static_assert(!std::is_default_constructible_v<Job>, "a launch cannot be made without what all of them read");
+static_assert(std::is_trivially_copyable_v<Job>, "a kernel's argument");
+int main() {
+  uint32_t status, mask, target;
+  const HeadArgs a{nullptr, nullptr, 0, 300, 5000, 64, 64, 64, &mask, &target, 0.5f};
+  const Job j(a, 157, &status, 512, 256);
+  const bool ok = j.status == &status && j.bitmask == &mask && j.target == &target && j.temp == 0.5f && j.rows == 300 &&
+                  j.W == 157 && j.v0 == 512 && j.tokens == 256 && j.p[0].splits == 0 && j.p[1].splits == 0 && !j.w && !j.terms.up;
+  std::puts(ok ? "ok" : "wrong");
+}
+"""
+
+
+def test_every_launch_has_what_all_of_them_read(tmp_path):
+    """The status among it, which a wait that runs out writes to: no launch is made but by the constructor."""
+    assert compile_and_run(tmp_path, JOB).strip() == "ok"
+    with open(os.path.join(CSRC, "kernel_head.cu")) as f:
+        source = f.read()
+    made = re.findall(r"^\s*Job \w+\s*[({=].*$", source, re.M)
+    assert len(made) == 2 and all("(a, v.t.W, v.t.status, v0, n);" in line for line in made), made
