@@ -285,16 +285,30 @@ struct Boxes {
   }
 };
 
-// The significand of the first g / T among 32 rows that is a normal number.  Terms rounded to bf16 are
-// rounded in units of it, and the gradients multiplied by it: where all rows have one g, as under a
-// mean, a target's term -g / T (1 - p) is then near a power of two and all but exact, where
-// g / T itself may be rounded by up to 2^-8, the same way in every row.
+// The significand of g / T of the first row that counts (its loss is above 0) and whose g / T is a
+// normal number.  Terms rounded to bf16 are rounded in units of it, and the gradients multiplied by it:
+// where all rows that count have one g, as under a mean, whether or not others are weighted with 0, a
+// target's term -g / T (1 - p) is then near a power of two and all but exact, where g / T itself may be
+// rounded by up to 2^-8, the same way in every row.  256 rows at a time; mostly the first has it.
 __device__ __forceinline__ float common_scale(const Job& job) {
+  constexpr uint32_t kAhead = 8;
   const uint32_t lane = threadIdx.x & 31;
-  const float g = __fdiv_rn(!job.terms.up ? 1.f : lane < job.rows ? job.terms.up[lane] : 0.f, job.temp);
-  const uint32_t who = __ballot_sync(0xFFFFFFFFu, fabsf(g) >= FLT_MIN && fabsf(g) <= FLT_MAX);
-  const uint32_t bits = __shfl_sync(0xFFFFFFFFu, __float_as_uint(g), who ? __ffs(who) - 1 : 0);
-  return who ? __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u) : 1.f;
+#pragma unroll 1
+  for (uint32_t r0 = 0; r0 < job.rows; r0 += 32 * kAhead) {
+    float g[kAhead];
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u) {
+      const uint32_t r = r0 + 32 * u + lane;
+      g[u] = r < job.rows && job.terms.loss[r] > 0.f ? job.terms.up ? job.terms.up[r] : 1.f : 0.f;
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u) {
+      const float x = __fdiv_rn(g[u], job.temp);
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, fabsf(x) >= FLT_MIN && fabsf(x) <= FLT_MAX);
+      if (who) return __uint_as_float((__shfl_sync(0xFFFFFFFFu, __float_as_uint(x), __ffs(who) - 1) & 0x007FFFFFu) | 0x3F800000u);
+    }
+  }
+  return 1.f;
 }
 
 // d = k * exp((x - m) / T), at the target as it stands
