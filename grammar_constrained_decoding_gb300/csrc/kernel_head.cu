@@ -702,13 +702,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1) product_kernel(const __grid_c
         else mbar_arrive(&ends.tile_empty[acc]);
       }
     };
+    // (whether a wait ran out is the warp's to say: lanes that went on alone would read tensor memory without the others)
     auto full = [&](uint32_t i) {
-      if (!mbar_wait(&ends.tile_full[SUMS == kParts ? 0 : i & 1u], (SUMS == kParts ? i : i >> 1) & 1u)) {
-        record_error(job.status, CG_DEV_TIMEOUT);
+      const bool there = mbar_wait(&ends.tile_full[SUMS == kParts ? 0 : i & 1u], (SUMS == kParts ? i : i >> 1) & 1u);
+      if (!__all_sync(0xFFFFFFFFu, there)) {
+        if (lane == 0) record_error(job.status, CG_DEV_TIMEOUT);
         return false;
       }
       tc::fence_after_sync();
-      __syncwarp();
       return true;
     };
     auto read_item = [&](const Product& p, bool second) {

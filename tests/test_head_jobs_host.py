@@ -46,3 +46,13 @@ def test_every_launch_has_what_all_of_them_read(tmp_path):
         source = f.read()
     made = [line for line in re.findall(r"^ +Job \w+.*;$", source, re.M) if "= logits_of(a, p, v, v0, n);" not in line]
     assert len(made) == 2 and all(line.endswith("(a, v.t.W, v.t.status, v0, n);") for line in made), made
+
+
+def test_a_warp_gives_up_a_wait_as_one():
+    """A wait by all lanes of a warp may run out for some of them alone: what follows is for whole warps (tensor
+    memory, __syncwarp), so the warp votes.  Shown by reading: waits are by one lane, or under a vote."""
+    with open(os.path.join(CSRC, "kernel_head.cu")) as f:
+        source = f.read()
+    readers = source[source.index("} else if (warp >= kFirstReader) {"):source.index("constexpr size_t product_smem()")]
+    waits = re.findall(r"const bool (\w+) = mbar_wait\([^;]*;\s*if \(!__all_sync\(0xFFFFFFFFu, (\w+)\)\)", readers)
+    assert waits == [("there", "there")] and readers.count("mbar_wait(") == 1
