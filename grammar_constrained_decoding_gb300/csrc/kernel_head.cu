@@ -324,6 +324,10 @@ __device__ __forceinline__ RowTerms row_terms(const TermsOut& terms, float temp,
     const float loss = terms.loss[r], m = terms.norm[2 * size_t(r)], s = terms.norm[2 * size_t(r) + 1];
     if (loss > 0.f) {   // a loss of 0: no target that counts, or nothing beside it
       Scale t(c, m);
+      if (m == FLT_MAX) {   // a logit of +inf, which counts as this: not as it is, however high T
+        t.fast = false;
+        t.rest = 1.f;
+      }
       const float g = __fdiv_rn(__fdiv_rn(terms.up ? terms.up[r] : 1.f, temp), scale);
       float k = __fdiv_rn(g, s) * t.rest;
       if (!(fabsf(k) <= FLT_MAX)) {
@@ -352,7 +356,7 @@ __device__ __forceinline__ void set_terms(const Job& job, float* x, uint32_t col
       x[i] = d.x;
       x[i + 1] = d.y;
     }
-    if (!(fabsf(check.x + check.y) <= FLT_MAX)) {   // NaN among them (no +inf: the maximum would be it)
+    if (!(fabsf(check.x + check.y) <= FLT_MAX)) {   // NaN among them (a row with +inf is not here: its maximum is out of the ordinary)
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] = fabsf(x[i]) <= FLT_MAX ? x[i] : 0.f;
     }
