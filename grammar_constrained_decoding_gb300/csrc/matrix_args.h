@@ -22,6 +22,8 @@ inline bool matrix_ok(const void* at, int dtype, uint64_t rows, uint32_t D, uint
 inline bool matrices_meet(const void* x, uint64_t nx, uint64_t ldx, const void* y, uint64_t ny, uint64_t ldy, uint32_t D,
                           uint64_t size) {
   if (!nx || !ny) return false;
+  if (nx == 1) ldx = ldy;   // the pitch of one row is nobody's
+  if (ny == 1) ldy = ldx;
   const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
   const uint64_t width = D * size;
   if (a + (nx - 1) * ldx * size + width <= b || b + (ny - 1) * ldy * size + width <= a) return false;

@@ -56,3 +56,29 @@ def test_a_warp_gives_up_a_wait_as_one():
     readers = source[source.index("} else if (warp >= kFirstReader) {"):source.index("constexpr size_t product_smem()")]
     waits = re.findall(r"const bool (\w+) = mbar_wait\([^;]*;\s*if \(!__all_sync\(0xFFFFFFFFu, (\w+)\)\)", readers)
     assert waits == [("there", "there")] and readers.count("mbar_wait(") == 1
+
+
+ONE_ROW = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "matrix_args.h"
+using namespace cgk;
+int main() {
+  char* b = reinterpret_cast<char*>(1 << 20);
+  bool ok = true;
+  // one row of 8 columns of 4 bytes in a buffer of pitch 16, whatever its own pitch is said to be, beside 4 rows and over them
+  for (uint64_t ld : {8, 9, 16, 100}) {
+    ok = ok && !matrices_meet(b + 8 * 4, 1, ld, b, 4, 16, 8, 4) && !matrices_meet(b, 4, 16, b + 8 * 4, 1, ld, 8, 4);
+    ok = ok && !matrices_meet(b + (32 + 8) * 4, 1, ld, b, 4, 16, 8, 4) && !matrices_meet(b, 4, 16, b + (32 + 8) * 4, 1, ld, 8, 4);
+    for (int at : {0, 1, 7, 9, 15, 16, 32, 48}) ok = ok && matrices_meet(b + at * 4, 1, ld, b, 4, 16, 8, 4) && matrices_meet(b, 4, 16, b + at * 4, 1, ld, 8, 4);
+    ok = ok && !matrices_meet(b + 64 * 4, 1, ld, b, 4, 16, 8, 4) && !matrices_meet(b, 4, 16, b - 8 * 4, 1, ld, 8, 4);
+    ok = ok && matrices_meet(b, 1, ld, b + 7 * 4, 1, 8, 8, 4) && !matrices_meet(b, 1, ld, b + 8 * 4, 1, 8, 8, 4);
+  }
+  std::puts(ok ? "ok" : "wrong");
+}
+"""
+
+
+def test_one_row_beside_a_matrix(tmp_path):
+    """One row's pitch says nothing: a row in other columns of a matrix's buffer shares no memory with it."""
+    assert compile_and_run(tmp_path, ONE_ROW).strip() == "ok"
