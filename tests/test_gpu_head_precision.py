@@ -59,3 +59,26 @@ def test_the_rows_that_count_set_the_unit(B, first):
     assert float(e.loss[target >= 0].min()) > 2.4
     assert off_in_roundings(dh, e.d @ e.w) <= 1.3
     assert off_in_roundings(dw, e.d.T @ e.h) <= 1.3
+
+
+@pytest.mark.parametrize("kind", ["halfway", "random"])
+@pytest.mark.parametrize("B,D,pad", [(1, 64, 0), (2, 72, 8), (17, 64, 0), (40, 70, 1), (128, 64, 0)])
+def test_few_rows_terms_keep_two_parts(B, D, pad, kind):
+    """Up to 128 rows, under a g for each: both gradients as close as one rounding of the result.  `halfway`: each g
+    so that its target's term lies halfway between two bf16 values; a term of one part alone would be off by 2^-8
+    (1.6 to 2.9 of one rounding for these sizes, worked out in 64 bits; with both parts 1.00)."""
+    import torch
+    V, T = 4000, 0.85
+    g = generator(B)
+    target = torch.randint(0, V, (B,), generator=g, device="cuda").int()
+    state = g.get_state()
+    e, _, _ = gradients(B, V, D, T, torch.ones(B, device="cuda"), target, g, pad)
+    if kind == "halfway":
+        up = (T * (1 + 2.0 ** -8) / -torch.expm1(-e.loss)).float() * 2.0 ** (torch.arange(B, device="cuda") % 5 - 2)
+    else:
+        up = torch.rand(B, generator=g, device="cuda") - 0.3
+    g.set_state(state)     # the same rows and weight
+    e, dh, dw = gradients(B, V, D, T, up, target, g, pad)
+    assert float(e.loss.min()) > 1e-2
+    assert off_in_roundings(dh, e.d @ e.w) <= 1.3
+    assert off_in_roundings(dw, e.d.T @ e.h) <= 1.3
