@@ -1,11 +1,17 @@
-// What a launch of the output layer's product kernel computes (kernel_head.cu).  No device
-// code: compiles on the host alone.
+// What a launch of the output layer's product kernel computes, and how its items are dealt out
+// (kernel_head.cu).  Compiles on the host alone, where it is tested.
 #pragma once
 
 #include <cstdint>
 
 #include <cuda.h>
 #include <vector_types.h>
+
+#ifdef __CUDACC__
+#define CG_BOTH __host__ __device__ __forceinline__
+#else
+#define CG_BOTH inline
+#endif
 
 namespace cgk {
 
@@ -70,5 +76,50 @@ struct Job {
   Job(const HeadArgs& a, uint32_t words, uint32_t* status_, uint32_t first, uint32_t count)
       : bitmask(a.bitmask), W(words), v0(first), tokens(count), target(a.target), temp(a.temp), rows(a.B), status(status_) {}
 };
+
+// The items of a launch, dealt out to `pairs` takers (blocks, or pairs of them) beforehand.  The
+// first product's (a tile, or a split of one) go round in turn; a taker without one in the last
+// round takes items of the second in that time, and from then on they go round.
+template <bool TWO>
+struct Turns {
+  uint32_t pair, pairs, extra, mine, items, early, nth = 0;
+  CG_BOTH Turns(const Job& j, uint32_t pair_, uint32_t pairs_) : pair(pair_), pairs(pairs_) {
+    const uint32_t first = j.p[0].n_m * j.p[0].n_n * j.p[0].splits;
+    mine = first / pairs;
+    extra = first - mine * pairs;
+    items = TWO ? j.p[1].n_m * j.p[1].n_n * j.p[1].splits : 0;
+    early = pair < extra ? 0 : j.early;
+    mine += pair < extra;
+    if (TWO) head = j.early * (pairs - extra);
+  }
+  uint32_t head = 0;
+  CG_BOTH bool next(bool& second, uint32_t& t) {
+    const uint32_t i = nth++;
+    second = i >= mine;
+    if (!second) {
+      t = pair + i * pairs;
+      return true;
+    }
+    if (!TWO) return false;
+    const uint32_t k = i - mine;
+    t = k < early ? k * (pairs - extra) + pair - extra : head + (k - early) * pairs + pair;
+    return t < items;
+  }
+};
+
+struct Work {
+  uint32_t m0, n0, split, k0, k1;
+};
+// An item's stages: all of them, or its split's (blocks * splits fits 32 bits)
+CG_BOTH void stages_of(const Product& p, uint32_t t, Work& w) {
+  w.split = 0;
+  w.k0 = 0;
+  w.k1 = p.blocks;
+  if (p.splits > 1) {
+    w.split = t / (p.n_m * p.n_n);
+    w.k0 = p.blocks * w.split / p.splits;
+    w.k1 = p.blocks * (w.split + 1) / p.splits;
+  }
+}
 
 }  // namespace cgk

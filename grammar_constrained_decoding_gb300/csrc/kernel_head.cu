@@ -84,52 +84,8 @@ struct Ends {
   uint32_t tmem;
 };
 
-// The items of a launch, dealt out to `pairs` takers (blocks, or pairs of them) beforehand.  The
-// first product's (a tile, or a split of one) go round in turn; a taker without one in the last
-// round takes items of the second in that time, and from then on they go round.
-template <bool TWO>
-struct Turns {
-  uint32_t pair, pairs, extra, mine, items, early, nth = 0;
-  __device__ __forceinline__ Turns(const Job& j, uint32_t pair_, uint32_t pairs_) : pair(pair_), pairs(pairs_) {
-    const uint32_t first = j.p[0].n_m * j.p[0].n_n * j.p[0].splits;
-    mine = first / pairs;
-    extra = first - mine * pairs;
-    items = TWO ? j.p[1].n_m * j.p[1].n_n * j.p[1].splits : 0;
-    early = pair < extra ? 0 : j.early;
-    mine += pair < extra;
-    if (TWO) head = j.early * (pairs - extra);
-  }
-  uint32_t head = 0;
-  __device__ __forceinline__ bool next(bool& second, uint32_t& t) {
-    const uint32_t i = nth++;
-    second = i >= mine;
-    if (!second) {
-      t = pair + i * pairs;
-      return true;
-    }
-    if (!TWO) return false;
-    const uint32_t k = i - mine;
-    t = k < early ? k * (pairs - extra) + pair - extra : head + (k - early) * pairs + pair;
-    return t < items;
-  }
-};
-
-struct Work {
-  uint32_t m0, n0, split, k0, k1;
-};
 template <typename S, bool NARROW>
 __device__ __forceinline__ uint32_t width(const Product& p) { return NARROW ? p.tile_n : S::kWidth; }
-// An item's stages: all of them, or its split's (blocks * splits fits 32 bits)
-__device__ __forceinline__ void stages_of(const Product& p, uint32_t t, Work& w) {
-  w.split = 0;
-  w.k0 = 0;
-  w.k1 = p.blocks;
-  if (p.splits > 1) {
-    w.split = t / (p.n_m * p.n_n);
-    w.k0 = p.blocks * w.split / p.splits;
-    w.k1 = p.blocks * (w.split + 1) / p.splits;
-  }
-}
 // Bands of row tiles over all columns: what runs at one time shares both operands in L2
 template <int CTAS, typename S, bool NARROW>
 __device__ __forceinline__ Work work_of(const Product& p, uint32_t t) {

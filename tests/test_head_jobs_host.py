@@ -82,3 +82,76 @@ int main() {
 def test_one_row_beside_a_matrix(tmp_path):
     """One row's pitch says nothing: a row in other columns of a matrix's buffer shares no memory with it."""
     assert compile_and_run(tmp_path, ONE_ROW).strip() == "ok"
+
+
+DEALT = r"""
+#include <cstdio>
+#include <vector>
+#include "head_jobs.h"
+using namespace cgk;
+template <bool TWO>
+bool dealt_once(uint32_t pairs, uint32_t tiles, uint32_t splits, uint32_t second_items, uint32_t early) {
+  const HeadArgs a{};
+  uint32_t status;
+  Job j(a, 0, &status, 0, 0);
+  j.p[0].n_m = tiles ? 1 : 0;
+  j.p[0].n_n = tiles;
+  j.p[0].splits = splits;
+  j.p[1].n_m = second_items ? 1 : 0;
+  j.p[1].n_n = second_items;
+  j.p[1].splits = 1;
+  j.early = early;
+  const uint32_t items[2] = {tiles * splits, TWO ? second_items : 0};
+  std::vector<int> seen[2] = {std::vector<int>(items[0]), std::vector<int>(items[1])};
+  for (uint32_t pair = 0; pair < pairs; ++pair) {
+    Turns<TWO> turns(j, pair, pairs);
+    bool second, before = false;
+    uint32_t t, most = items[0] + items[1];
+    while (turns.next(second, t)) {
+      if (t >= items[second] || seen[second][t]++ || (before && !second) || most-- == 0) return false;
+      before = second;
+    }
+  }
+  for (auto& s : seen)
+    for (int n : s)
+      if (n != 1) return false;
+  return true;
+}
+bool stages_once(uint32_t tiles, uint32_t splits, uint32_t blocks) {
+  Product p = {};
+  p.n_m = 1;
+  p.n_n = tiles;
+  p.splits = splits;
+  p.blocks = blocks;
+  std::vector<uint32_t> to(tiles), many(tiles);
+  for (uint32_t t = 0; t < tiles * splits; ++t) {   // a tile's splits follow one another in k
+    Work w;
+    stages_of(p, t, w);
+    const uint32_t tile = t - w.split * tiles;
+    if (tile >= tiles || w.k0 != to[tile] || w.k1 < w.k0 || w.split != many[tile]++) return false;
+    to[tile] = w.k1;
+  }
+  for (uint32_t t = 0; t < tiles; ++t)
+    if (to[t] != blocks || many[t] != splits) return false;
+  return true;
+}
+int main() {
+  for (uint32_t pairs : {1u, 2u, 5u, 76u, 152u})
+    for (uint32_t tiles : {0u, 1u, 4u, 75u, 76u, 77u, 128u, 300u})
+      for (uint32_t splits : {1u, 2u, 9u})
+        for (uint32_t second : {0u, 1u, 3u, 100u, 1000u})
+          for (uint32_t early : {0u, 1u, 8u, 40u})
+            if (!dealt_once<true>(pairs, tiles, splits, second, early) || !dealt_once<false>(pairs, tiles, splits, second, 0))
+              return std::printf("dealt: %u takers, %u x %u, %u, %u\n", pairs, tiles, splits, second, early), 0;
+  for (uint32_t splits : {1u, 2u, 7u, 152u})
+    for (uint32_t blocks : {1u, 6u, 8u, 500u, 6145u})
+      if (!stages_once(3, splits, blocks)) return std::printf("stages: %u of %u\n", splits, blocks), 0;
+  std::puts("ok");
+}
+"""
+
+
+def test_the_kernels_rule_deals_every_item_out_once(tmp_path):
+    """Turns and stages_of, as the kernel includes them: every item of either product to one taker, the first
+    product's before the second's; every stage to one split, in order."""
+    assert compile_and_run(tmp_path, DEALT).strip() == "ok"
