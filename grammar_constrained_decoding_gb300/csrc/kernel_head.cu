@@ -20,11 +20,14 @@
 // for the weight alone, are multiplied without the tensor cores.
 //
 // Bound by the tensor cores where rows are many: 4096 x 128256 x 2048, loss and gradients, 8.6
-// TFLOP with the logits twice in 5.0 ms, 1.72 PFLOP/s, what a plain library product sustains at
-// the card's power limit (1.73); the gradients' launch keeps the tensor pipe 92 % busy (2048 rows,
-// K = 2048).  Few rows are bound by reading the weight: 256 x 128256 x 4096 masked 200 us, 5.3 TB/s.
-// Between those, what stands in the way: an accumulator's 256 x 256 tile takes as many bytes a
-// cycle from L2 as an SM can get (64), and a stage 560 to 600 cycles instead of 512.
+// TFLOP with the logits twice in 5.2 ms, 1.65 PFLOP/s (a plain library product sustains 1.73 at the
+// card's power limit; runs of a few hundred ms, before that is reached, take 5.1); the gradients'
+// launch keeps the tensor pipe 92 % busy (2048 rows, K = 2048).  Few rows wait for the weight: 256 x
+// 128256 x 4096 masked 215 us, 4.9 TB/s, the loads alone 186.  That is not the memory's limit
+// (few_kernel below reads as many bytes in 153) but how they are asked for: boxes of 128 bytes out of
+// each of 128 rows.  Between those, what stands in the way: an accumulator's 256 x 256 tile takes as
+// many bytes a cycle from L2 as an SM can get (64), and a stage 560 to 600 cycles instead of 512.
+// Figures beside the choices below are of short runs, both sides in turn.
 #include <algorithm>
 
 #include "head_jobs.h"
@@ -44,8 +47,8 @@ constexpr uint32_t kReaders = 8;          // warps that read tiles out: four row
 constexpr uint32_t kFirstReader = 4;      // after the copying, the multiplying and the allocating warp, and a spare
 constexpr uint32_t kHeadThreads = (kFirstReader + kReaders) * 32;
 constexpr uint32_t kStore = 4096;         // bytes of a box that a reader writes out: 32 rows of 128 bytes
-constexpr uint32_t kBand = 16;            // row tiles that are taken together over all columns (4096 x 151936 x 1024: 713 us; 4: 755, 32: 713)
-constexpr uint32_t kBoxesEach = 1;        // a reader's boxes under way (two, with a stage less: 106.6 -> 108.5 us, 364 -> 368)
+constexpr uint32_t kBand = 16;            // row tiles that are taken together over all columns (4096 x 151936 x 1024: 714 us; 4: 758, 32: 713)
+constexpr uint32_t kBoxesEach = 1;        // a reader's boxes under way (two, with a stage less, of bf16: 192 x 32000 x 2048 gradients 110.9 -> 112.5 us, the tied step 367 -> 372)
 constexpr uint32_t kReadBoxes = 13, kReadElements = 32;   // stages' time that reading a gradient's tile out takes, at least
 constexpr uint32_t kHeadSms = 152;
 
@@ -60,9 +63,12 @@ enum Readout { kLoss, kTerms, kOut };
 enum Sums { kOne, kChains, kParts, kTwo };
 constexpr uint32_t products_of(Sums sums) { return sums == kParts ? 6 : sums == kTwo ? 2 : 1; }  // of a stage
 // Stages of a chain.  A chain of sums in tensor memory drifts, as its steps are not rounded to
-// nearest: over 16 stages (1024 k) losses are 2e-7 to 7e-7 off (in one chain of 4096 k 2.2e-6),
-// over 4 a quarter of that.  4 for float matrices (their gradients 4e-7 off against 1.1e-6, for 3 %
-// of the time) and for few rows, which wait for memory; 16 for many (4: 968 us where 16 take 714).
+// nearest: over 16 stages (1024 k) losses are 2e-7 to 7e-7 off (in one chain of 4096 k 2.2e-6).
+// 4 for float matrices (their gradients 4e-7 off against 1.1e-6, for 3 % of the time) and for few
+// rows, which wait for memory: 1.0e-7 to 1.5e-7 off there on the whole (of 2, 0.7e-7 to 1.2e-7 for 1
+// to 3 % of the time up to 128 rows and 14 to 17 % of 300's; of 1 no better), a lone small loss up to
+// 3e-6 of itself with any of them.  16 for many (4096 x 151936 x 1024 in chains of 4: 1000 us where
+// 16 take 714).
 constexpr uint32_t chain_of(Sums sums, int ctas) { return sums == kParts || ctas == 1 ? 4 : 16; }
 
 // A block's share of a stage, and how many fit beside the readers' boxes.  Float matrices' stages
@@ -1328,7 +1334,9 @@ HeadPlan plan_head(const void* hidden, uint64_t ld_h, const void* weight, uint64
   p.lay_h = f32 || !rows_on_grid(hidden, dtype, ld_h);
   p.lay_w = f32 || !rows_on_grid(weight, dtype, ld_w);
   // rows in pairs of blocks, but not 257 to 384: three blocks pad them to 384, two pairs to 512
-  // (333 x 32000 x 1024 step: 107.9 us in blocks, 110.5 in pairs)
+  // (steps in blocks and in pairs, us: 333 x 32000 x 1024 bf16 112 and 114, 300 x 32003 x 509 bf16 114 and
+  // 126, 300 x 128256 x 2048 bf16 645 and 667; float matrices, 333 x 32003 x 509 301 and 370, 257 x
+  // 128256 x 2048 4140 and 4970)
   p.pair = B > kBlockM && !(B > 2 * kBlockM && B <= 3 * kBlockM);
   uint64_t most = V;
   if (p.lay_w) most = std::min<uint64_t>(most, kPieceBytes / (uint64_t(p.parts) * p.Dp * 2));

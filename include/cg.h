@@ -597,8 +597,8 @@ int cg_embed_grad(cg_ctx* c, const void* d_grad, int dtype, uint32_t N, uint32_t
  * A loss near 0 keeps its relative precision.  The products of bf16 matrices are summed
  * in 32 bits; float matrices are multiplied in 32 bits up to 8 rows, from then on as three
  * bf16 parts each, to about the precision of 32-bit products, and have to be finite and
- * below 2^127 (in bf16 ones a row of the weight that is not finite reaches only the rows
- * that allow its token).
+ * below 2^127, the sums of their products too (in bf16 ones a row of the weight that is not
+ * finite reaches only the rows that allow its token).
  *  d_hidden : [B][ld_hidden], d_weight : [V][ld_weight], of D columns
  *  d_bitmask: u32 [B][W] or NULL: every token is allowed
  *  d_target : u32 [B]; temp : T > 0, finite
@@ -618,8 +618,8 @@ int cg_head_loss(cg_ctx* c, const void* d_hidden, const void* d_weight, int dtyp
  * p_t - 1 is taken from the loss, as expm1(-loss).  An infinite or NaN g_b gives terms that
  * are not finite over A_b, and 0 elsewhere as any other.  Terms d of bf16 matrices are rounded
  * to bf16 for the products (a relative error of 2^-8 at most, as the gradients' own
- * rounding has), in units that keep one g_b / T for all rows exact; by hidden the targets'
- * terms count whole.  Up to 128 rows d keeps two bf16 parts (2^-16).  hidden and weight have
+ * rounding has), in units that keep one g_b / T for all rows that count (whose loss is above
+ * 0 and g_b not 0) exact; by hidden the targets' terms count whole.  Up to 128 rows d keeps two bf16 parts (2^-16).  hidden and weight have
  * to be finite: 0 * inf is NaN, also for a token that no row allows.
  *  d_loss, d_norm : as cg_head_loss wrote them for the same arguments
  *  d_out_grad_hidden : [B][ld_grad_hidden] or NULL; d_out_grad_weight :
